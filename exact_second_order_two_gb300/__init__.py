@@ -30,6 +30,8 @@ from ._binding import (  # noqa: F401
     workspace_size,
 )
 from .autograd import attention  # noqa: F401
+from .diff_attention import diff_attention, diff_backward, diff_forward  # noqa: F401
+from .rotary import rotary, rotary_frequencies  # noqa: F401
 from . import meta  # noqa: F401
 from .build import build_library  # noqa: F401
 

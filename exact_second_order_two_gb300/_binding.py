@@ -42,10 +42,29 @@ class Shape(ctypes.Structure):
                 ("causal", ctypes.c_int), ("scale", ctypes.c_float)]
 
 
+class Rotary(ctypes.Structure):
+    _fields_ = [("B", ctypes.c_int), ("H", ctypes.c_int), ("N", ctypes.c_int),
+                ("d", ctypes.c_int), ("rotary_dim", ctypes.c_int),
+                ("interleaved", ctypes.c_int), ("inverse", ctypes.c_int),
+                ("in_dtype", ctypes.c_int), ("out_dtype", ctypes.c_int),
+                ("magnitude", ctypes.c_float),
+                ("x_strides", ctypes.c_longlong * 3), ("y_strides", ctypes.c_longlong * 3),
+                ("pos_stride", ctypes.c_longlong), ("offset", ctypes.c_longlong)]
+
+
+class DiffShape(ctypes.Structure):
+    _fields_ = [("B", ctypes.c_int), ("H", ctypes.c_int), ("Hk", ctypes.c_int),
+                ("N", ctypes.c_int), ("d", ctypes.c_int), ("dv", ctypes.c_int),
+                ("dtype", ctypes.c_int), ("causal", ctypes.c_int),
+                ("lam_kind", ctypes.c_int), ("lam_dtype", ctypes.c_int),
+                ("scale", ctypes.c_float)]
+
+
 _LIB = None
 _P = ctypes.c_void_p
 _SZ = ctypes.c_size_t
 _SHP = ctypes.POINTER(Shape)
+_DSHP = ctypes.POINTER(DiffShape)
 
 _SIGNATURES = {
     "fbob_version": (ctypes.c_int, []),
@@ -64,6 +83,11 @@ _SIGNATURES = {
     "fbob_bob_noalloc": (ctypes.c_int, [_SHP] + [_P] * 13 + [_P]),
     "fbob_noalloc_status": (ctypes.c_int, [_P]),
     "fbob_set_wait_limit": (ctypes.c_longlong, [ctypes.c_longlong]),
+    "fbob_diff_workspace_size": (_SZ, [ctypes.c_int, _DSHP]),
+    "fbob_diff_path": (ctypes.c_int, [ctypes.c_int, _DSHP]),
+    "fbob_diff_forward": (ctypes.c_int, [_DSHP] + [_P] * 8 + [_SZ, _P]),
+    "fbob_diff_backward": (ctypes.c_int, [_DSHP] + [_P] * 13 + [_SZ, _P]),
+    "fbob_rotary": (ctypes.c_int, [ctypes.POINTER(Rotary), _P, _P, _P, _P, _P]),
 }
 
 
@@ -133,6 +157,22 @@ def _check_tensors(ref: torch.Tensor, named: dict, scalar_names=()):
 
 def _stream(device) -> ctypes.c_void_p:
     return ctypes.c_void_p(torch.cuda.current_stream(device).cuda_stream)
+
+
+class on_device:
+    """Makes ``device`` current for a block; costs nothing where it already is."""
+
+    def __init__(self, device):
+        self.guard = (None if torch.cuda.current_device() == device.index
+                      else torch.cuda.device(device))
+
+    def __enter__(self):
+        if self.guard is not None:
+            self.guard.__enter__()
+
+    def __exit__(self, *exc):
+        if self.guard is not None:
+            self.guard.__exit__(*exc)
 
 
 def workspace_size(op: int, shape: Shape) -> int:

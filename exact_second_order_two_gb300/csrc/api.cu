@@ -7,6 +7,7 @@
 #include "common.cuh"
 #include "fbob.h"
 #include "internal.h"
+#include "ops.h"
 
 namespace fbob {
 namespace {
@@ -117,6 +118,14 @@ void LaunchLog::mark() {
   ++launches;
   if (launches < g_event_count) cudaEventRecord(g_events[launches], stream);
 }
+
+void begin_call(LaunchLog& log) {
+  if (g_event_count > 0) cudaEventRecord(g_events[0], log.stream);
+}
+
+void end_call(const LaunchLog& log) { g_last_launches = log.launches; }
+
+int forced_path() { return g_force_path; }
 
 }  // namespace fbob
 

@@ -1,0 +1,470 @@
+// CUDA-core kernels of differential attention: fp32 tensors, and bf16 with
+// head sizes the tensor-core kernels do not serve.  Per head, with m = 1, 2,
+//   S^m = c Q^m K^mT, P^m = softmax(S^m), O = P^1 V - lam P^2 V;
+//   dP = dO V^T, D^m = dO . O^m, dS^1 = P^1*(dP - D^1),
+//   dS^2 = -lam P^2*(dP - D^2), dQ^m = c dS^m K^m, dK^m = c dS^mT Q^m,
+//   dV = (P^1 - lam P^2)^T dO.
+//
+// Arithmetic is fp32 throughout.  A block of 16 x 16 threads holds a 64-row
+// tile (queries, or keys for dK and dV) and streams 64-row tiles of the other
+// side through shared memory; thread (ty, tx) computes the 4 x 4 scores of
+// rows 4 ty.. and columns tx + 16 j.  A row of scores lives in 16 lanes of one
+// warp, so row maxima and sums are shuffles, and the probabilities pass to
+// their product through shared memory inside the warp.  Bound: FFMA issue,
+// at 8 FFMA per 16-byte shared-memory read.  Everything a row or key
+// accumulates is summed by one block in a fixed order.
+#include <cuda_bf16.h>
+#include <math.h>
+
+#include "common.cuh"
+#include "internal.h"
+#include "ops.h"
+
+namespace fbob {
+namespace {
+
+constexpr int kT = 64;       // rows of a tile
+constexpr int kThreads = 256;
+constexpr int kLdp = kT + 4;  // row stride of the score tile
+
+// Row stride of a [64][width] tile in floats: whole 16-byte steps, and rows
+// shifted by four banks against one another.
+__host__ __device__ inline int ld_of(int width) {
+  const int w = (width + 3) / 4 * 4;
+  return (w % 32 == 0 || w % 8 == 0) ? w + 4 : w;
+}
+
+struct Args {
+  const void *q, *k, *v, *dO;
+  void *o, *o2, *dq, *dk, *dv;
+  float* lse;
+  const float* D;
+  LamArg lam;
+  int H, G, N, d, dv_, causal;
+  float scale;
+};
+
+__device__ __forceinline__ float lam_at(const LamArg& l, int H, int N, int b, int h, int n) {
+  const size_t i = l.kind == 0 ? 0 : l.kind == 1 ? (size_t)h : ((size_t)b * H + h) * N + n;
+  return l.bf16 ? __bfloat162float(static_cast<const __nv_bfloat16*>(l.p)[i])
+                : static_cast<const float*>(l.p)[i];
+}
+
+// Rows row0.. of src [rows][width] into dst [64][ld]; rows past N and the
+// columns up to the next multiple of four read as zero.
+template <typename T>
+__device__ __forceinline__ void load_rows(float* dst, int ld, const T* src, int row0, int N,
+                                          int width) {
+  const int w4 = (width + 3) / 4;
+  for (int e = threadIdx.x; e < kT * w4; e += kThreads) {
+    const int r = e / w4, c = (e - r * w4) * 4;
+    float4 f = make_float4(0.f, 0.f, 0.f, 0.f);
+    if (row0 + r < N) {
+      const T* p = src + (size_t)(row0 + r) * width + c;
+      f.x = to_f32<T>(p[0]);
+      if (c + 1 < width) f.y = to_f32<T>(p[1]);
+      if (c + 2 < width) f.z = to_f32<T>(p[2]);
+      if (c + 3 < width) f.w = to_f32<T>(p[3]);
+    }
+    *reinterpret_cast<float4*>(dst + r * ld + c) = f;
+  }
+}
+
+// s[i][j] = sum_c A[4 ty + i][c] B[tx + 16 j][c]
+__device__ __forceinline__ void tile_dot(float (&s)[4][4], const float* A, const float* B, int ld,
+                                         int width, int ty, int tx) {
+#pragma unroll
+  for (int i = 0; i < 4; ++i)
+#pragma unroll
+    for (int j = 0; j < 4; ++j) s[i][j] = 0.f;
+  const float* a0 = A + 4 * ty * ld;
+  const float* b0 = B + tx * ld;
+#pragma unroll 2
+  for (int c = 0; c < width; c += 4) {
+    float4 a[4], b[4];
+#pragma unroll
+    for (int i = 0; i < 4; ++i) a[i] = *reinterpret_cast<const float4*>(a0 + i * ld + c);
+#pragma unroll
+    for (int j = 0; j < 4; ++j) b[j] = *reinterpret_cast<const float4*>(b0 + 16 * j * ld + c);
+#pragma unroll
+    for (int i = 0; i < 4; ++i)
+#pragma unroll
+      for (int j = 0; j < 4; ++j) {
+        s[i][j] = fmaf(a[i].x, b[j].x, s[i][j]);
+        s[i][j] = fmaf(a[i].y, b[j].y, s[i][j]);
+        s[i][j] = fmaf(a[i].z, b[j].z, s[i][j]);
+        s[i][j] = fmaf(a[i].w, b[j].w, s[i][j]);
+      }
+  }
+}
+
+// acc[i][4 g + e] += sum_k P[4 ty + i][k] X[k][4 tx + 64 g + e], over the
+// column groups g that hold some of the width's columns.
+template <int NG>
+__device__ __forceinline__ void tile_add(float (&acc)[4][4 * NG], const float* P, const float* X,
+                                         int ld, int width, int ty, int tx) {
+  const float* p0 = P + 4 * ty * kLdp;
+#pragma unroll 2
+  for (int k = 0; k < kT; k += 4) {
+    float4 p[4];
+#pragma unroll
+    for (int i = 0; i < 4; ++i) p[i] = *reinterpret_cast<const float4*>(p0 + i * kLdp + k);
+#pragma unroll
+    for (int g = 0; g < NG; ++g) {
+      const int col = 4 * tx + 64 * g;
+      if (col < width) {
+#pragma unroll
+        for (int u = 0; u < 4; ++u) {
+          const float4 x = *reinterpret_cast<const float4*>(X + (k + u) * ld + col);
+#pragma unroll
+          for (int i = 0; i < 4; ++i) {
+            const float w = u == 0 ? p[i].x : u == 1 ? p[i].y : u == 2 ? p[i].z : p[i].w;
+            acc[i][4 * g + 0] = fmaf(w, x.x, acc[i][4 * g + 0]);
+            acc[i][4 * g + 1] = fmaf(w, x.y, acc[i][4 * g + 1]);
+            acc[i][4 * g + 2] = fmaf(w, x.z, acc[i][4 * g + 2]);
+            acc[i][4 * g + 3] = fmaf(w, x.w, acc[i][4 * g + 3]);
+          }
+        }
+      }
+    }
+  }
+}
+
+// The warp's own rows of the score tile: written, and visible to its product.
+__device__ __forceinline__ void put_tile(float* P, const float (&s)[4][4], int ty, int tx) {
+  __syncwarp();
+#pragma unroll
+  for (int i = 0; i < 4; ++i)
+#pragma unroll
+    for (int j = 0; j < 4; ++j) P[(4 * ty + i) * kLdp + tx + 16 * j] = s[i][j];
+  __syncwarp();
+}
+
+template <typename T, int NG>
+__device__ __forceinline__ void store_rows(T* dst, const float (&acc)[4][4 * NG], float mul, int row0,
+                                           int N, int width, int ty, int tx) {
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    const int r = row0 + 4 * ty + i;
+    if (r >= N) continue;
+#pragma unroll
+    for (int g = 0; g < NG; ++g)
+#pragma unroll
+      for (int e = 0; e < 4; ++e) {
+        const int c = 4 * tx + 64 * g + e;
+        if (c < width) dst[(size_t)r * width + c] = from_f32<T>(mul * acc[i][4 * g + e]);
+      }
+  }
+}
+
+__device__ __forceinline__ float row16_max(float v) {
+#pragma unroll
+  for (int o = 8; o > 0; o >>= 1) v = fmaxf(v, __shfl_xor_sync(0xffffffffu, v, o));
+  return v;
+}
+__device__ __forceinline__ float row16_sum(float v) {
+#pragma unroll
+  for (int o = 8; o > 0; o >>= 1) v += __shfl_xor_sync(0xffffffffu, v, o);
+  return v;
+}
+
+// ---- forward: one block per 64 query rows of a head -----------------------
+template <typename T, int NGV>
+__global__ void __launch_bounds__(kThreads) diff_fwd(Args a) {
+  extern __shared__ __align__(16) float sm[];
+  const int ld = ld_of(a.d), ldv = ld_of(a.dv_), N = a.N;
+  float* qs = sm;                      // [2][64][ld]
+  float* ks = qs + 2 * kT * ld;        // [2][64][ld]
+  float* vs = ks + 2 * kT * ld;        // [64][ldv]
+  float* ps = vs + kT * ldv;           // [64][kLdp]
+  const int ty = threadIdx.x >> 4, tx = threadIdx.x & 15;
+  const int bh = blockIdx.y, b = bh / a.H, h = bh % a.H;
+  const int kvh = b * (a.H / a.G) + h / a.G;
+  const int row0 = (a.causal ? (int)(gridDim.x - 1 - blockIdx.x) : (int)blockIdx.x) * kT;
+  const size_t qsz = (size_t)N * a.d;
+  const T* q = static_cast<const T*>(a.q) + (size_t)bh * 2 * qsz;
+  const T* k = static_cast<const T*>(a.k) + (size_t)kvh * 2 * qsz;
+  const T* v = static_cast<const T*>(a.v) + (size_t)kvh * N * a.dv_;
+  load_rows(qs, ld, q, row0, N, a.d);
+  load_rows(qs + kT * ld, ld, q + qsz, row0, N, a.d);
+
+  float acc[2][4][4 * NGV], mx[2][4], l[2][4];
+#pragma unroll
+  for (int m = 0; m < 2; ++m)
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      mx[m][i] = -INFINITY;
+      l[m][i] = 0.f;
+#pragma unroll
+      for (int e = 0; e < 4 * NGV; ++e) acc[m][i][e] = 0.f;
+    }
+  const int kend = a.causal ? min(N, row0 + kT) : N;
+  for (int j0 = 0; j0 < kend; j0 += kT) {
+    __syncthreads();
+    load_rows(ks, ld, k, j0, N, a.d);
+    load_rows(ks + kT * ld, ld, k + qsz, j0, N, a.d);
+    load_rows(vs, ldv, v, j0, N, a.dv_);
+    __syncthreads();
+#pragma unroll
+    for (int m = 0; m < 2; ++m) {
+      float s[4][4];
+      tile_dot(s, qs + m * kT * ld, ks + m * kT * ld, ld, a.d, ty, tx);
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        const int r = row0 + 4 * ty + i;
+        float t = -INFINITY;
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+          const int col = j0 + tx + 16 * j;
+          s[i][j] = (col < N && (!a.causal || col <= r)) ? s[i][j] * a.scale : -INFINITY;
+          t = fmaxf(t, s[i][j]);
+        }
+        // every row sees a key of its first tile, so the maximum is finite
+        // from there on (rows past N see them too; they are not stored)
+        t = fmaxf(mx[m][i], row16_max(t));
+        const float alpha = expf(mx[m][i] - t);
+        mx[m][i] = t;
+        float sum = 0.f;
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+          s[i][j] = expf(s[i][j] - t);
+          sum += s[i][j];
+        }
+        l[m][i] = l[m][i] * alpha + row16_sum(sum);
+#pragma unroll
+        for (int e = 0; e < 4 * NGV; ++e) acc[m][i][e] *= alpha;
+      }
+      put_tile(ps, s, ty, tx);
+      tile_add<NGV>(acc[m], ps, vs, ldv, a.dv_, ty, tx);
+    }
+  }
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    const int r = row0 + 4 * ty + i;
+    const float w = r < N ? lam_at(a.lam, a.H, N, b, h, r) : 0.f;
+    const float i1 = 1.f / l[0][i], i2 = 1.f / l[1][i];
+#pragma unroll
+    for (int e = 0; e < 4 * NGV; ++e) {
+      acc[1][i][e] *= i2;
+      acc[0][i][e] = acc[0][i][e] * i1 - w * acc[1][i][e];
+    }
+    if (r < N && tx == 0 && a.lse) {
+      a.lse[((size_t)bh * 2 + 0) * N + r] = mx[0][i] + logf(l[0][i]);
+      a.lse[((size_t)bh * 2 + 1) * N + r] = mx[1][i] + logf(l[1][i]);
+    }
+  }
+  const size_t ob = (size_t)bh * N * a.dv_;
+  store_rows<T, NGV>(static_cast<T*>(a.o) + ob, acc[0], 1.f, row0, N, a.dv_, ty, tx);
+  if (a.o2) store_rows<T, NGV>(static_cast<T*>(a.o2) + ob, acc[1], 1.f, row0, N, a.dv_, ty, tx);
+}
+
+// ---- dQ: one block per 64 query rows of a head -----------------------------
+template <typename T, int NGD>
+__global__ void __launch_bounds__(kThreads) diff_bwd_row(Args a) {
+  extern __shared__ __align__(16) float sm[];
+  const int ld = ld_of(a.d), ldv = ld_of(a.dv_), N = a.N;
+  float* qs = sm;                      // [2][64][ld]
+  float* dos = qs + 2 * kT * ld;       // [64][ldv]
+  float* ks = dos + kT * ldv;          // [2][64][ld]
+  float* vs = ks + 2 * kT * ld;        // [64][ldv]
+  float* ps = vs + kT * ldv;           // [64][kLdp]
+  const int ty = threadIdx.x >> 4, tx = threadIdx.x & 15;
+  const int bh = blockIdx.y, b = bh / a.H, h = bh % a.H;
+  const int kvh = b * (a.H / a.G) + h / a.G;
+  const int row0 = (a.causal ? (int)(gridDim.x - 1 - blockIdx.x) : (int)blockIdx.x) * kT;
+  const size_t qsz = (size_t)N * a.d;
+  const T* q = static_cast<const T*>(a.q) + (size_t)bh * 2 * qsz;
+  const T* k = static_cast<const T*>(a.k) + (size_t)kvh * 2 * qsz;
+  const T* v = static_cast<const T*>(a.v) + (size_t)kvh * N * a.dv_;
+  load_rows(qs, ld, q, row0, N, a.d);
+  load_rows(qs + kT * ld, ld, q + qsz, row0, N, a.d);
+  load_rows(dos, ldv, static_cast<const T*>(a.dO) + (size_t)bh * N * a.dv_, row0, N, a.dv_);
+  float lse[2][4], D[2][4], w[4], acc[2][4][4 * NGD];
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    const int r = row0 + 4 * ty + i;
+#pragma unroll
+    for (int m = 0; m < 2; ++m) {
+      const size_t at = ((size_t)bh * 2 + m) * N + (r < N ? r : 0);
+      lse[m][i] = a.lse[at];
+      D[m][i] = a.D[at];
+#pragma unroll
+      for (int e = 0; e < 4 * NGD; ++e) acc[m][i][e] = 0.f;
+    }
+    w[i] = lam_at(a.lam, a.H, N, b, h, r < N ? r : 0);
+  }
+  const int kend = a.causal ? min(N, row0 + kT) : N;
+  for (int j0 = 0; j0 < kend; j0 += kT) {
+    __syncthreads();
+    load_rows(ks, ld, k, j0, N, a.d);
+    load_rows(ks + kT * ld, ld, k + qsz, j0, N, a.d);
+    load_rows(vs, ldv, v, j0, N, a.dv_);
+    __syncthreads();
+    float dp[4][4];
+    tile_dot(dp, dos, vs, ldv, a.dv_, ty, tx);
+#pragma unroll
+    for (int m = 0; m < 2; ++m) {
+      float s[4][4];
+      tile_dot(s, qs + m * kT * ld, ks + m * kT * ld, ld, a.d, ty, tx);
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        const int r = row0 + 4 * ty + i;
+        const float f = m == 0 ? 1.f : -w[i];
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+          const int col = j0 + tx + 16 * j;
+          const bool in = r < N && col < N && (!a.causal || col <= r);
+          s[i][j] = in ? f * expf(s[i][j] * a.scale - lse[m][i]) * (dp[i][j] - D[m][i]) : 0.f;
+        }
+      }
+      put_tile(ps, s, ty, tx);
+      tile_add<NGD>(acc[m], ps, ks + m * kT * ld, ld, a.d, ty, tx);
+    }
+  }
+#pragma unroll
+  for (int m = 0; m < 2; ++m)
+    store_rows<T, NGD>(static_cast<T*>(a.dq) + ((size_t)bh * 2 + m) * qsz, acc[m], a.scale, row0, N,
+                       a.d, ty, tx);
+}
+
+// ---- dK, dV: one block per 64 keys of a key head, over its query heads ------
+template <typename T, int NGD, int NGV>
+__global__ void __launch_bounds__(kThreads) diff_bwd_col(Args a) {
+  extern __shared__ __align__(16) float sm[];
+  const int ld = ld_of(a.d), ldv = ld_of(a.dv_), N = a.N;
+  float* ks = sm;                      // [2][64][ld]
+  float* vs = ks + 2 * kT * ld;        // [64][ldv]
+  float* qs = vs + kT * ldv;           // [2][64][ld]
+  float* dos = qs + 2 * kT * ld;       // [64][ldv]
+  float* ps = dos + kT * ldv;          // [64][kLdp]
+  float* sc = ps + kT * kLdp;          // [5][64]: LSE^1, LSE^2, D^1, D^2, lam
+  const int ty = threadIdx.x >> 4, tx = threadIdx.x & 15;
+  const int kvh = blockIdx.y, Hk = a.H / a.G;
+  const int b = kvh / Hk;
+  const int col0 = blockIdx.x * kT;
+  const size_t qsz = (size_t)N * a.d;
+  const T* k = static_cast<const T*>(a.k) + (size_t)kvh * 2 * qsz;
+  load_rows(ks, ld, k, col0, N, a.d);
+  load_rows(ks + kT * ld, ld, k + qsz, col0, N, a.d);
+  load_rows(vs, ldv, static_cast<const T*>(a.v) + (size_t)kvh * N * a.dv_, col0, N, a.dv_);
+  float ak[2][4][4 * NGD], av[4][4 * NGV];
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+#pragma unroll
+    for (int e = 0; e < 4 * NGD; ++e) ak[0][i][e] = ak[1][i][e] = 0.f;
+#pragma unroll
+    for (int e = 0; e < 4 * NGV; ++e) av[i][e] = 0.f;
+  }
+  for (int g = 0; g < a.G; ++g) {
+    const int h = (kvh % Hk) * a.G + g;
+    const size_t bh = (size_t)b * a.H + h;
+    const T* q = static_cast<const T*>(a.q) + bh * 2 * qsz;
+    const T* dO = static_cast<const T*>(a.dO) + bh * N * a.dv_;
+    for (int i0 = a.causal ? col0 : 0; i0 < N; i0 += kT) {
+      __syncthreads();
+      load_rows(qs, ld, q, i0, N, a.d);
+      load_rows(qs + kT * ld, ld, q + qsz, i0, N, a.d);
+      load_rows(dos, ldv, dO, i0, N, a.dv_);
+      if (threadIdx.x < kT) {
+        const int r = min(i0 + (int)threadIdx.x, N - 1);
+        sc[0 * kT + threadIdx.x] = a.lse[(bh * 2 + 0) * N + r];
+        sc[1 * kT + threadIdx.x] = a.lse[(bh * 2 + 1) * N + r];
+        sc[2 * kT + threadIdx.x] = a.D[(bh * 2 + 0) * N + r];
+        sc[3 * kT + threadIdx.x] = a.D[(bh * 2 + 1) * N + r];
+        sc[4 * kT + threadIdx.x] = lam_at(a.lam, a.H, N, b, h, r);
+      }
+      __syncthreads();
+      float dp[4][4], wt[4][4];
+      tile_dot(dp, vs, dos, ldv, a.dv_, ty, tx);
+#pragma unroll
+      for (int m = 0; m < 2; ++m) {
+        float s[4][4];
+        tile_dot(s, ks + m * kT * ld, qs + m * kT * ld, ld, a.d, ty, tx);
+#pragma unroll
+        for (int i = 0; i < 4; ++i)
+#pragma unroll
+          for (int j = 0; j < 4; ++j) {
+            const int key = col0 + 4 * ty + i, c = tx + 16 * j, r = i0 + c;
+            const bool in = r < N && key < N && (!a.causal || key <= r);
+            const float p = in ? expf(s[i][j] * a.scale - sc[m * kT + c]) : 0.f;
+            const float f = m == 0 ? p : -sc[4 * kT + c] * p;
+            wt[i][j] = m == 0 ? f : wt[i][j] + f;
+            s[i][j] = in ? f * (dp[i][j] - sc[(2 + m) * kT + c]) : 0.f;
+          }
+        put_tile(ps, s, ty, tx);
+        tile_add<NGD>(ak[m], ps, qs + m * kT * ld, ld, a.d, ty, tx);
+      }
+      put_tile(ps, wt, ty, tx);
+      tile_add<NGV>(av, ps, dos, ldv, a.dv_, ty, tx);
+    }
+  }
+#pragma unroll
+  for (int m = 0; m < 2; ++m)
+    store_rows<T, NGD>(static_cast<T*>(a.dk) + ((size_t)kvh * 2 + m) * qsz, ak[m], a.scale, col0, N,
+                       a.d, ty, tx);
+  store_rows<T, NGV>(static_cast<T*>(a.dv) + (size_t)kvh * N * a.dv_, av, 1.f, col0, N, a.dv_, ty,
+                     tx);
+}
+
+Args make_args(const DiffProblem& p, const DiffTensors& t) {
+  Args a{};
+  a.q = t.q; a.k = t.k; a.v = t.v; a.dO = t.dO;
+  a.o = t.o; a.o2 = t.o2; a.dq = t.dq; a.dk = t.dk; a.dv = t.dv;
+  a.lse = t.lse;
+  a.lam = t.lam;
+  a.H = p.H; a.G = p.G(); a.N = p.N; a.d = p.d; a.dv_ = p.dv; a.causal = p.causal;
+  a.scale = p.scale;
+  return a;
+}
+
+template <typename K>
+cudaError_t run(K kernel, dim3 grid, size_t floats, const Args& a, LaunchLog& log) {
+  const size_t bytes = floats * sizeof(float);
+  cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)bytes);
+  if (e != cudaSuccess) return e;
+  kernel<<<grid, kThreads, bytes, log.stream>>>(a);
+  e = cudaGetLastError();
+  log.mark();
+  return e;
+}
+
+template <typename T>
+cudaError_t forward_t(const DiffProblem& p, const DiffTensors& t, LaunchLog& log) {
+  const dim3 grid((p.N + kT - 1) / kT, p.B * p.H);
+  const size_t floats = (size_t)kT * (4 * ld_of(p.d) + ld_of(p.dv) + kLdp);
+  const Args a = make_args(p, t);
+  return p.dv <= 64 ? run(diff_fwd<T, 1>, grid, floats, a, log)
+                    : run(diff_fwd<T, 2>, grid, floats, a, log);
+}
+
+template <typename T>
+cudaError_t backward_t(const DiffProblem& p, const DiffTensors& t, const DiffWorkspace& ws,
+                       LaunchLog& log) {
+  Args a = make_args(p, t);
+  a.D = ws.D;
+  const int blocks = (p.N + kT - 1) / kT;
+  const size_t floats = (size_t)kT * (4 * ld_of(p.d) + 2 * ld_of(p.dv) + kLdp);
+  const dim3 rows(blocks, p.B * p.H), cols(blocks, p.B * p.Hk);
+  cudaError_t e = p.d <= 64 ? run(diff_bwd_row<T, 1>, rows, floats, a, log)
+                            : run(diff_bwd_row<T, 2>, rows, floats, a, log);
+  if (e != cudaSuccess) return e;
+  const size_t cf = floats + 5 * kT;
+  if (p.d <= 64)
+    return p.dv <= 64 ? run(diff_bwd_col<T, 1, 1>, cols, cf, a, log)
+                      : run(diff_bwd_col<T, 1, 2>, cols, cf, a, log);
+  return p.dv <= 64 ? run(diff_bwd_col<T, 2, 1>, cols, cf, a, log)
+                    : run(diff_bwd_col<T, 2, 2>, cols, cf, a, log);
+}
+
+}  // namespace
+
+cudaError_t diff_simt_forward(const DiffProblem& p, const DiffTensors& t, LaunchLog& log) {
+  return p.bf16 ? forward_t<__nv_bfloat16>(p, t, log) : forward_t<float>(p, t, log);
+}
+
+cudaError_t diff_simt_backward(const DiffProblem& p, const DiffTensors& t, const DiffWorkspace& ws,
+                               LaunchLog& log) {
+  return p.bf16 ? backward_t<__nv_bfloat16>(p, t, ws, log) : backward_t<float>(p, t, ws, log);
+}
+
+}  // namespace fbob

@@ -1,0 +1,56 @@
+// Internal declarations of the attention-layer operators (rotary positions,
+// differential attention), next to those of internal.h.
+#pragma once
+
+#include <cuda_runtime.h>
+#include <stddef.h>
+#include <initializer_list>
+
+#include "fbob.h"
+#include "internal.h"
+
+namespace fbob {
+
+// Profiling-event and launch-count bookkeeping around one entry point's work.
+void begin_call(LaunchLog& log);
+void end_call(const LaunchLog& log);
+// Kernel family forced by fbob_force_path, or -1.
+int forced_path();
+
+// Differential attention after validation (see fbob_diff_shape_t).
+struct DiffProblem {
+  int B, H, Hk, N, d, dv;
+  int bf16, causal;
+  int lam_kind, lam_bf16;
+  float scale;
+  int G() const { return H / Hk; }
+  size_t rows() const { return (size_t)B * H * N; }
+};
+
+// lam of row n of head bh = b H + h, in fp32.
+struct LamArg {
+  const void* p;
+  int kind, bf16;
+};
+
+struct DiffWorkspace {
+  int* status = nullptr;
+  float* D = nullptr;        // [B, 2H, N]: D^1 and D^2 of each row
+  float* partial = nullptr;  // [B, H]: sums of D^2, for lam's gradient
+};
+
+struct DiffTensors {
+  const void *q, *k, *v;
+  LamArg lam;
+  void *o, *o2;  // o2 may be null in the forward
+  float* lse;    // [B, 2H, N]
+  const void* dO;
+  void *dq, *dk, *dv;
+};
+
+// ---- CUDA-core kernels: fp32 or bf16, any d and dv up to 128 -------------
+cudaError_t diff_simt_forward(const DiffProblem& p, const DiffTensors& t, LaunchLog& log);
+cudaError_t diff_simt_backward(const DiffProblem& p, const DiffTensors& t, const DiffWorkspace& ws,
+                               LaunchLog& log);
+
+}  // namespace fbob

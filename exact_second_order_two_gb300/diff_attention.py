@@ -1,0 +1,256 @@
+"""Differential attention: the weighted difference of two softmax maps over
+the same values, O = softmax(c Q1 K1^T) V - lam softmax(c Q2 K2^T) V, with a
+learned lam.
+
+``diff_forward`` and ``diff_backward`` are the library's two calls
+(``fbob_diff_forward``, ``fbob_diff_backward``); ``diff_attention`` is the
+twice-differentiable function on top of them, next to ``attention``.
+
+The second derivative needs no kernel of its own.  The first backward is that
+of plain attention for each map, with upstream gradient dO for the first and
+-lam dO for the second, and dlam_i = -dO_i . O2_i.  So its backward is the
+library's backward-over-backward (``fbob_bob``) of each map, with the chain
+rule through -lam dO, plus, for the cotangent g of dlam, a first backward of
+the second map with upstream -g dO.  The maps' queries and keys are padded
+with zero features (or the values with zero columns) where their widths
+differ, which changes no score and no product.
+"""
+from __future__ import annotations
+
+import ctypes
+import math
+
+import torch
+
+from . import _binding as _b
+
+LAM_ONE, LAM_HEAD, LAM_ROW = 0, 1, 2
+
+
+def _shape(q, k, v, lam, causal, scale) -> _b.DiffShape:
+    """Checks the inputs against one another and describes the problem."""
+    if not q.is_cuda:
+        raise _b.FbobError(1, "diff_attention: tensors must be CUDA tensors")
+    for name, t in (("q", q), ("k", k), ("v", v)):
+        if t.dim() != 4:
+            raise ValueError(f"{name} must have four dimensions")
+        if t.device != q.device:
+            raise ValueError(f"{name} is on {t.device}, expected {q.device}")
+        if t.dtype != q.dtype:
+            raise ValueError(f"{name} must match q: {q.dtype}")
+        if not t.is_contiguous():
+            raise ValueError(f"{name} must be contiguous")
+    if q.dtype not in _b.DTYPES:
+        raise TypeError(f"unsupported dtype {q.dtype}; use bfloat16 or float32")
+    B, H2, N, d = q.shape
+    Hk, dv = v.shape[1], v.shape[3]
+    if H2 % 2:
+        raise ValueError("q must hold two query heads per head: [B, 2H, N, d]")
+    H = H2 // 2
+    if tuple(k.shape) != (B, 2 * Hk, N, d):
+        raise ValueError(f"k must be [{B}, 2 * {Hk}, {N}, {d}] to go with q and v")
+    if v.shape[0] != B or v.shape[2] != N:
+        raise ValueError(f"v must be [{B}, heads, {N}, width] to go with q")
+    if Hk == 0 or H % Hk:
+        raise ValueError(f"{H} query heads cannot share {Hk} key heads evenly")
+    if lam.device != q.device:
+        raise ValueError(f"lam is on {lam.device}, expected {q.device}")
+    if lam.dtype not in _b.DTYPES:
+        raise TypeError(f"unsupported lam dtype {lam.dtype}; use bfloat16 or float32")
+    if lam.dim() == 0:
+        kind = LAM_ONE
+    elif tuple(lam.shape) == (H,):
+        kind = LAM_HEAD
+    elif tuple(lam.shape) == (B, H, N):
+        kind = LAM_ROW
+    else:
+        raise ValueError(f"lam must have no dimensions, [{H}] or [{B}, {H}, {N}]")
+    if not lam.is_contiguous():
+        raise ValueError("lam must be contiguous")
+    if scale is None:
+        scale = 1.0 / math.sqrt(d)
+    return _b.DiffShape(B, H, Hk, N, d, dv, _b.DTYPES[q.dtype], int(bool(causal)), kind,
+                        _b.DTYPES[lam.dtype], float(scale))
+
+
+def _match(name, t, shape, dtype, device):
+    if tuple(t.shape) != tuple(shape) or t.dtype != dtype or t.device != device or \
+            not t.is_contiguous():
+        raise ValueError(f"{name} must be contiguous {dtype} {tuple(shape)} on {device}")
+
+
+def _workspace(op, shp, device):
+    n = _b.lib().fbob_diff_workspace_size(op, ctypes.byref(shp))
+    if n == 0:
+        raise _b.FbobError(2, "fbob_diff_workspace_size")
+    return torch.empty(n, dtype=torch.uint8, device=device)
+
+
+def diff_forward(q, k, v, lam, causal: bool = False, scale: float | None = None,
+                 need_o2: bool = True, workspace=None):
+    """Differential attention forward: returns (O, O2, LSE), with
+    O2 = softmax(c Q2 K2^T) V, or None where ``need_o2`` is false, and LSE
+    [B, 2H, N] the rows' log-sum-exp of both maps.
+
+    q: [B, 2H, N, d], the two queries of head h as heads 2h and 2h + 1;
+    k: [B, 2Hk, N, d] likewise; v: [B, Hk, N, dv], with H a multiple of Hk
+    (query head h reads key head h // (H / Hk)); bf16 or fp32, contiguous.
+    lam: no dimensions, [H] or [B, H, N], bf16 or fp32.  scale > 0 defaults to
+    1/sqrt(d); with ``causal`` key j is visible to query i iff j <= i.
+    """
+    shp = _shape(q, k, v, lam, causal, scale)
+    o = torch.empty((shp.B, shp.H, shp.N, shp.dv), dtype=q.dtype, device=q.device)
+    o2 = torch.empty_like(o) if need_o2 else None
+    lse = torch.empty((shp.B, 2 * shp.H, shp.N), dtype=torch.float32, device=q.device)
+    with _b.on_device(q.device):
+        ws = _workspace(_b.OP_FORWARD, shp, q.device) if workspace is None else workspace
+        _b._check(_b.lib().fbob_diff_forward(
+            ctypes.byref(shp), q.data_ptr(), k.data_ptr(), v.data_ptr(), lam.data_ptr(),
+            o.data_ptr(), None if o2 is None else o2.data_ptr(), lse.data_ptr(), ws.data_ptr(),
+            ws.numel(), _b._stream(q.device)), "fbob_diff_forward")
+    return o, o2, lse
+
+
+def diff_backward(q, k, v, lam, o, o2, lse, do, causal: bool = False,
+                  scale: float | None = None, workspace=None):
+    """First backward for upstream gradient ``do`` and the forward's results:
+    returns (dQ, dK, dV, dlam), of the inputs' shapes and dtypes."""
+    shp = _shape(q, k, v, lam, causal, scale)
+    rows = (shp.B, shp.H, shp.N, shp.dv)
+    for name, t in (("o", o), ("o2", o2), ("do", do)):
+        _match(name, t, rows, q.dtype, q.device)
+    _match("lse", lse, (shp.B, 2 * shp.H, shp.N), torch.float32, q.device)
+    dq, dk, dv, dlam = (torch.empty_like(t) for t in (q, k, v, lam))
+    with _b.on_device(q.device):
+        ws = _workspace(_b.OP_BACKWARD, shp, q.device) if workspace is None else workspace
+        _b._check(_b.lib().fbob_diff_backward(
+            ctypes.byref(shp), *(t.data_ptr() for t in (q, k, v, lam, o, o2, lse, do, dq, dk, dv,
+                                                        dlam, ws)),
+            ws.numel(), _b._stream(q.device)), "fbob_diff_backward")
+    return dq, dk, dv, dlam
+
+
+def _contig(t: torch.Tensor) -> torch.Tensor:
+    return t if t.is_contiguous() else t.contiguous()
+
+
+def _rows(lam, B, H, N):
+    """lam, or its cotangent, as fp32 [B, H, N, 1]."""
+    f = lam.float()
+    f = f[:, None] if f.dim() == 1 else f
+    return f.expand(B, H, N).unsqueeze(-1)
+
+
+class _DiffBackward(torch.autograd.Function):
+    """(q, k, v, lam, dO) -> (dQ, dK, dV, dlam); its backward runs fbob_bob
+    on each map."""
+
+    @staticmethod
+    def forward(ctx, q, k, v, lam, do, o, o2, lse, causal, scale):
+        do = _contig(do)
+        grads = diff_backward(q, k, v, lam, o, o2, lse, do, causal, scale)
+        ctx.save_for_backward(q, k, v, lam, do, o, o2, lse)
+        ctx.causal, ctx.scale = causal, scale
+        ctx.set_materialize_grads(False)
+        return grads
+
+    @staticmethod
+    @torch.autograd.function.once_differentiable
+    def backward(ctx, gq, gk, gv, glam):
+        q, k, v, lam, do, o, o2, lse = ctx.saved_tensors
+        none = (None,) * 5
+        if gq is None and gk is None and gv is None and glam is None:
+            return (None,) * 5 + none
+        B, H2, N, d = q.shape
+        H, Hk, dv = H2 // 2, v.shape[1], v.shape[3]
+        G, wide = H // Hk, max(d, dv)
+        dtype = q.dtype
+
+        def fit(t, per_head):
+            """[B, heads, N, w] with every query head its own, zero-padded."""
+            if t is None:
+                return None
+            if per_head != H:
+                t = t.repeat_interleave(G, 1)
+            if t.shape[-1] < wide:
+                t = torch.nn.functional.pad(t, (0, wide - t.shape[-1]))
+            return _contig(t)
+
+        w = _rows(lam, B, H, N)
+        vv, gvv = fit(v, Hk), fit(gv, Hk)
+        o1 = (o.float() + w * o2.float()).to(dtype)
+        gdo = torch.zeros(do.shape, dtype=torch.float32, device=do.device)
+        grad_lam = torch.zeros((B, H, N), dtype=torch.float32, device=do.device)
+        gradq, gradk, gradv = [], [], torch.zeros((B, H, N, wide), dtype=torch.float32,
+                                                  device=do.device)
+        for m in (0, 1):
+            qm, km = fit(q[:, m::2], H), fit(k[:, m::2], Hk)
+            om = fit(o2 if m else o1, H)
+            lm = lse[:, m::2].contiguous()
+            up = (-w * do.float()).to(dtype) if m else do
+            gqm = None if gq is None else fit(gq[:, m::2], H)
+            gkm = None if gk is None else fit(gk[:, m::2], Hk)
+            a = _b.bob(qm, km, vv, om, lm, fit(up, H), gqm, gkm, gvv, ctx.causal, ctx.scale)
+            rq, rk = a[0].float(), a[1].float()
+            gradv += a[2].float()
+            gup = a[3][..., :dv].float()
+            if m == 0:
+                gdo += gup
+            else:
+                gdo -= w * gup
+                grad_lam -= (do.float() * gup).sum(-1)
+                if glam is not None:
+                    g = _rows(glam, B, H, N)
+                    b = _b.backward(qm, km, vv, om, lm, fit((-g * do.float()).to(dtype), H),
+                                    ctx.causal, ctx.scale)
+                    rq += b[0].float()
+                    rk += b[1].float()
+                    gradv += b[2].float()
+                    gdo -= g * o2.float()
+            gradq.append(rq[..., :d])
+            gradk.append(rk[..., :d].unflatten(1, (Hk, G)).sum(2))
+        gradv = gradv[..., :dv].unflatten(1, (Hk, G)).sum(2).to(dtype)
+        gradq = torch.stack(gradq, 2).flatten(1, 2).to(dtype)
+        gradk = torch.stack(gradk, 2).flatten(1, 2).to(dtype)
+        if lam.dim() == 0:
+            grad_lam = grad_lam.sum()
+        elif lam.dim() == 1:
+            grad_lam = grad_lam.sum((0, 2))
+        return (gradq, gradk, gradv, grad_lam.to(lam.dtype), gdo.to(dtype)) + none
+
+
+class _DiffAttention(torch.autograd.Function):
+    @staticmethod
+    def forward(ctx, q, k, v, lam, causal, scale, need):
+        o, o2, lse = diff_forward(q, k, v, lam, causal, scale, need_o2=need)
+        if need:
+            ctx.save_for_backward(q, k, v, lam, o, o2, lse)
+            ctx.causal, ctx.scale = causal, scale
+        return o
+
+    @staticmethod
+    def backward(ctx, do):
+        q, k, v, lam, o, o2, lse = ctx.saved_tensors
+        # o, o2 and lse enter as values: the second derivative's paths through
+        # them are part of what fbob_bob returns
+        grads = _DiffBackward.apply(q, k, v, lam, do, o.detach(), o2, lse, ctx.causal, ctx.scale)
+        return tuple(grads) + (None, None, None)
+
+
+def diff_attention(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, lam: torch.Tensor,
+                   causal: bool = False, scale: float | None = None) -> torch.Tensor:
+    """Differential attention whose first and second derivatives run in the
+    library: per head, softmax(scale Q1 K1^T) V - lam softmax(scale Q2 K2^T) V,
+    masked to j <= i when causal.
+
+    q [B, 2H, N, d], k [B, 2Hk, N, d], v [B, Hk, N, dv] and lam as for
+    ``diff_forward`` (non-contiguous inputs are copied first).  Returns
+    [B, H, N, dv].  Differentiable twice in q, k, v and lam; scale is not
+    differentiated.
+    """
+    q, k, v, lam = _contig(q), _contig(k), _contig(v), _contig(lam)
+    if scale is None:
+        scale = 1.0 / math.sqrt(q.shape[-1])
+    # O2 is only kept (and written) where a backward can follow
+    need = torch.is_grad_enabled() and any(t.requires_grad for t in (q, k, v, lam))
+    return _DiffAttention.apply(q, k, v, lam, bool(causal), float(scale), need)

@@ -211,6 +211,87 @@ int fbob_last_launch_count(void);
 int fbob_selftest_wait_timeout(void* ws, size_t ws_bytes, int limit_us,
                                void* stream);
 
+/* ------------------------------------------------------------------------
+ * Rotary positions
+ * ------------------------------------------------------------------------
+ * The first rotary_dim features of each row are pairs; the pair (a, b) with
+ * frequency inv_freq[i] of the row at position p becomes
+ *   magnitude * (a cos t - b sin t, a sin t + b cos t),  t = p inv_freq[i],
+ * and the remaining features are copied.  Pair i holds features 2i, 2i + 1
+ * when interleaved, i and i + rotary_dim / 2 otherwise.  inverse != 0 negates
+ * t: the backward of the call (the map is linear), with the same magnitude.
+ * Whole turns drop out exactly, so far positions keep their angles: the
+ * error is p 2^-63 turns.
+ *
+ * x and y are [B,H,N,d] with feature stride 1 and strides over batch, head
+ * and position in elements (so a projection's [B,N,H,d] output can be read in
+ * place), each FBOB_BF16 or FBOB_FP32; y must not overlap x.  Arithmetic is
+ * fp32, rounded once.  d <= 1024, H <= 65535, B*H*N*d <= 2^38. */
+typedef struct {
+  int B, H, N, d;
+  int rotary_dim;          /* even, 0 <= rotary_dim <= d                     */
+  int interleaved;         /* 0 or 1                                         */
+  int inverse;             /* 0 or 1                                         */
+  int in_dtype, out_dtype; /* fbob_dtype_t of x and y                        */
+  float magnitude;
+  long long x_strides[3], y_strides[3]; /* batch, head, position             */
+  long long pos_stride;    /* elements between the batches of `positions`    */
+  long long offset;        /* position of row 0 where `positions` is NULL    */
+} fbob_rotary_t;
+
+/* y = rotary(x).  inv_freq: rotary_dim / 2 fp64 frequencies in radians per
+ * position, on the device.  positions: int64 on the device, row n of batch b
+ * at [b * pos_stride + n], or NULL for positions offset + n. */
+int fbob_rotary(const fbob_rotary_t* r, const void* x, const double* inv_freq,
+                const long long* positions, void* y, void* stream);
+
+/* ------------------------------------------------------------------------
+ * Differential attention
+ * ------------------------------------------------------------------------
+ * Per head h of H, two softmax maps over the same values and their weighted
+ * difference:
+ *   P^m = softmax(c Q^m K^mT),  m = 1, 2,   O = P^1 V - lam P^2 V.
+ * Layouts, all dense and row-major: q [B,2H,N,d] with Q^1, Q^2 of head h as
+ * heads 2h, 2h + 1; k [B,2Hk,N,d] likewise; v [B,Hk,N,dv]; o, o2, dO
+ * [B,H,N,dv]; lse [B,2H,N] fp32.  H is a multiple of Hk: query head h reads
+ * key head h / (H / Hk).  lam is one value, [H], or [B,H,N], bf16 or fp32.
+ * Masking, ownership, asynchrony and alignment as above (lam to its own
+ * size); scale > 0.  1 <= d, dv <= 128, B*H <= 32767.  fp32, and bf16 at head
+ * sizes without a tensor-core kernel (fbob_diff_path), run on CUDA cores.
+ * Every output is summed in a fixed order: equal inputs give equal bits. */
+typedef enum { FBOB_LAM_ONE = 0, FBOB_LAM_HEAD = 1, FBOB_LAM_ROW = 2 } fbob_lam_t;
+
+typedef struct {
+  int B, H, Hk, N, d, dv;
+  int dtype;               /* fbob_dtype_t of q, k, v and every [..,dv]      */
+  int causal;              /* 0 or 1                                         */
+  int lam_kind, lam_dtype; /* fbob_lam_t, fbob_dtype_t                       */
+  float scale;
+} fbob_diff_shape_t;
+
+/* Bytes of workspace that `op` (FBOB_OP_FORWARD or FBOB_OP_BACKWARD) needs
+ * for `shape`, 0 if it is invalid; and the kernel family that serves it, or
+ * -1.  The workspace's status word is read with fbob_status(). */
+size_t fbob_diff_workspace_size(int op, const fbob_diff_shape_t* shape);
+int fbob_diff_path(int op, const fbob_diff_shape_t* shape);
+
+/* o = O and lse = the log-sum-exp of both maps' rows.  o2 = P^2 V, which the
+ * backward reads, or NULL where no backward follows. */
+int fbob_diff_forward(const fbob_diff_shape_t* shape, const void* q, const void* k, const void* v,
+                      const void* lam, void* o, void* o2, float* lse, void* ws, size_t ws_bytes,
+                      void* stream);
+
+/* Gradients of <dO, O>: with dP = dO V^T, D^m = rowsum(dO * P^m V),
+ *   dS^1 = P^1 * (dP - D^1),  dS^2 = -lam P^2 * (dP - D^2),
+ *   dQ^m = c dS^m K^m,  dK^m = c dS^mT Q^m,  dV = (P^1 - lam P^2)^T dO,
+ *   dlam = -D^2 summed over the rows that share a value.
+ * dk and dv sum over the query heads that share a key head.  dlam has lam's
+ * shape and dtype. */
+int fbob_diff_backward(const fbob_diff_shape_t* shape, const void* q, const void* k,
+                       const void* v, const void* lam, const void* o, const void* o2,
+                       const float* lse, const void* dO, void* dq, void* dk, void* dv, void* dlam,
+                       void* ws, size_t ws_bytes, void* stream);
+
 /* Library ABI version (major*100 + minor). */
 int fbob_version(void);
 
