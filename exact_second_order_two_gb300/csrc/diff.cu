@@ -2,9 +2,12 @@
 // kernel family), the row scalars of its backward and the gradient of lam.
 //
 // D^m_i = dO_i . O^m_i comes from the saved O = O^1 - lam O^2 and O^2:
-// D^2 = dO . O^2 and D^1 = dO . O + lam D^2.  lam's gradient needs no product
-// of its own: dlam_i = -dO_i . O^2_i = -D^2_i, summed over what shares a
-// value of lam (per head, or over everything) in a fixed order.
+// D^2 = dO . O^2 and D^1 = dO . O + lam D^2.  lam's gradient, dlam_i =
+// -dO_i . O^2_i, is summed over what shares a value of lam (per head, or over
+// everything).  Those sums cancel, so a rounded O^2 is not good enough for
+// them: the pass that computes dQ also sums P^2_ij dP_ij over j in fp32, the
+// same number from unrounded factors, and the sums here add them up in a
+// fixed order.
 #include <cuda_bf16.h>
 #include <cuda_runtime.h>
 #include <stdint.h>
@@ -45,18 +48,22 @@ int check_shape(const fbob_diff_shape_t* s, DiffProblem* out) {
 }
 
 int choose_path(const DiffProblem& p) {
-  (void)p;
-  if (forced_path() == FBOB_PATH_TCGEN05) return -1;
-  return FBOB_PATH_SIMT;
+  const bool tc = diff_tc_supported(p);
+  if (forced_path() == FBOB_PATH_SIMT) return FBOB_PATH_SIMT;
+  if (forced_path() == FBOB_PATH_TCGEN05) return tc ? FBOB_PATH_TCGEN05 : -1;
+  return tc ? FBOB_PATH_TCGEN05 : FBOB_PATH_SIMT;
 }
 
-// [status 256 B][D: B*2H*N fp32][partial: B*H fp32], each region aligned
+// [status 256 B][D: B*2H*N fp32][d2: B*H*N fp32][partial: B*H fp32], each
+// region aligned
 size_t carve(int op, const DiffProblem& p, char* base, DiffWorkspace* ws) {
   size_t off = kAlign;
   if (ws) ws->status = reinterpret_cast<int*>(base);
   if (op == FBOB_OP_BACKWARD) {
     if (ws) ws->D = reinterpret_cast<float*>(base + off);
     off += align_up(2 * p.rows() * sizeof(float));
+    if (ws) ws->d2 = reinterpret_cast<float*>(base + off);
+    off += align_up(p.rows() * sizeof(float));
     if (ws) ws->partial = reinterpret_cast<float*>(base + off);
     off += align_up((size_t)p.B * p.H * sizeof(float));
   }
@@ -72,12 +79,11 @@ __device__ __forceinline__ void lam_store(void* p, int bf16, size_t i, float x) 
   else static_cast<float*>(p)[i] = x;
 }
 
-// D^1 and D^2 of every row, one warp per row; where lam is per row its
-// gradient too.
+// D^1 and D^2 of every row, one warp per row.
 template <typename T>
 __global__ void __launch_bounds__(256)
     diff_row_scalars(const T* __restrict__ o, const T* __restrict__ o2, const T* __restrict__ dO,
-                     LamArg lam, float* __restrict__ D, void* dlam, size_t rows, int H, int N, int dv) {
+                     LamArg lam, float* __restrict__ D, size_t rows, int H, int N, int dv) {
   const size_t row = (size_t)blockIdx.x * 8 + (threadIdx.x >> 5);
   const int lane = threadIdx.x & 31;
   if (row >= rows) return;
@@ -94,7 +100,6 @@ __global__ void __launch_bounds__(256)
   const size_t at = lam.kind == FBOB_LAM_ONE ? 0 : lam.kind == FBOB_LAM_HEAD ? bh % H : row;
   D[(bh * 2 + 0) * N + n] = fmaf(lam_load(lam, at), s2, s1);
   D[(bh * 2 + 1) * N + n] = s2;
-  if (lam.kind == FBOB_LAM_ROW) lam_store(dlam, lam.bf16, row, -s2);
 }
 
 __device__ __forceinline__ float block_sum(float v, float* sm) {
@@ -105,11 +110,18 @@ __device__ __forceinline__ float block_sum(float v, float* sm) {
   return threadIdx.x < 32 ? warp_sum(v) : 0.f;
 }
 
-// partial[b, h] = sum over rows of D^2: one block per (batch, head)
+// dlam per row
 __global__ void __launch_bounds__(256)
-    diff_head_sums(const float* __restrict__ D, float* __restrict__ partial, int N) {
+    diff_lam_rows(const float* __restrict__ d2, void* dlam, int bf16, size_t rows) {
+  const size_t i = (size_t)blockIdx.x * 256 + threadIdx.x;
+  if (i < rows) lam_store(dlam, bf16, i, -d2[i]);
+}
+
+// partial[b, h] = sum over rows of d2: one block per (batch, head)
+__global__ void __launch_bounds__(256)
+    diff_head_sums(const float* __restrict__ d2, float* __restrict__ partial, int N) {
   __shared__ float sm[8];
-  const float* d2 = D + ((size_t)blockIdx.x * 2 + 1) * N;
+  d2 += (size_t)blockIdx.x * N;
   float s = 0.f;
   for (int i = threadIdx.x; i < N; i += 256) s += d2[i];
   s = block_sum(s, sm);
@@ -136,20 +148,27 @@ __global__ void __launch_bounds__(256)
 
 template <typename T>
 cudaError_t row_scalars(const DiffProblem& p, const DiffTensors& t, const DiffWorkspace& ws,
-                        void* dlam, LaunchLog& log) {
+                        LaunchLog& log) {
   const size_t rows = p.rows();
   diff_row_scalars<T><<<(unsigned)((rows + 7) / 8), 256, 0, log.stream>>>(
       static_cast<const T*>(t.o), static_cast<const T*>(t.o2), static_cast<const T*>(t.dO), t.lam,
-      ws.D, dlam, rows, p.H, p.N, p.dv);
+      ws.D, rows, p.H, p.N, p.dv);
   const cudaError_t e = cudaGetLastError();
   log.mark();
   return e;
 }
 
 cudaError_t lam_gradient(const DiffProblem& p, const DiffWorkspace& ws, void* dlam, LaunchLog& log) {
-  if (p.lam_kind == FBOB_LAM_ROW) return cudaSuccess;  // written with the row scalars
-  diff_head_sums<<<p.B * p.H, 256, 0, log.stream>>>(ws.D, ws.partial, p.N);
-  cudaError_t e = cudaGetLastError();
+  cudaError_t e;
+  if (p.lam_kind == FBOB_LAM_ROW) {
+    diff_lam_rows<<<(unsigned)((p.rows() + 255) / 256), 256, 0, log.stream>>>(ws.d2, dlam, p.lam_bf16,
+                                                                              p.rows());
+    e = cudaGetLastError();
+    log.mark();
+    return e;
+  }
+  diff_head_sums<<<p.B * p.H, 256, 0, log.stream>>>(ws.d2, ws.partial, p.N);
+  e = cudaGetLastError();
   log.mark();
   if (e != cudaSuccess) return e;
   diff_lam_grad<<<1, 256, 0, log.stream>>>(ws.partial, dlam, p.lam_bf16, p.lam_kind, p.B, p.H);
@@ -207,7 +226,8 @@ int fbob_diff_forward(const fbob_diff_shape_t* shape, const void* q, const void*
   t.q = q; t.k = k; t.v = v; t.o = o; t.o2 = o2; t.lse = lse;
   t.lam = LamArg{lam, p.lam_kind, p.lam_bf16};
   begin_call(log);
-  const cudaError_t e = diff_simt_forward(p, t, log);
+  const cudaError_t e = path == FBOB_PATH_TCGEN05 ? diff_tc_forward(p, t, ws, log)
+                                                  : diff_simt_forward(p, t, log);
   end_call(log);
   return e == cudaSuccess ? FBOB_OK : FBOB_ERR_CUDA;
 }
@@ -233,10 +253,11 @@ int fbob_diff_backward(const fbob_diff_shape_t* shape, const void* q, const void
   t.dq = dq; t.dk = dk; t.dv = dv;
   t.lam = LamArg{lam, p.lam_kind, p.lam_bf16};
   begin_call(log);
-  cudaError_t e = p.bf16 ? row_scalars<__nv_bfloat16>(p, t, ws, dlam, log)
-                         : row_scalars<float>(p, t, ws, dlam, log);
+  cudaError_t e = p.bf16 ? row_scalars<__nv_bfloat16>(p, t, ws, log)
+                         : row_scalars<float>(p, t, ws, log);
+  if (e == cudaSuccess)
+    e = path == FBOB_PATH_TCGEN05 ? diff_tc_backward(p, t, ws, log) : diff_simt_backward(p, t, ws, log);
   if (e == cudaSuccess) e = lam_gradient(p, ws, dlam, log);
-  if (e == cudaSuccess) e = diff_simt_backward(p, t, ws, log);
   end_call(log);
   return e == cudaSuccess ? FBOB_OK : FBOB_ERR_CUDA;
 }

@@ -3,7 +3,7 @@
 //   S^m = c Q^m K^mT, P^m = softmax(S^m), O = P^1 V - lam P^2 V;
 //   dP = dO V^T, D^m = dO . O^m, dS^1 = P^1*(dP - D^1),
 //   dS^2 = -lam P^2*(dP - D^2), dQ^m = c dS^m K^m, dK^m = c dS^mT Q^m,
-//   dV = (P^1 - lam P^2)^T dO.
+//   dV = (P^1 - lam P^2)^T dO, dlam_i = -sum_j P^2_ij dP_ij.
 //
 // Arithmetic is fp32 throughout.  A block of 16 x 16 threads holds a 64-row
 // tile (queries, or keys for dK and dV) and streams 64-row tiles of the other
@@ -39,6 +39,7 @@ struct Args {
   void *o, *o2, *dq, *dk, *dv;
   float* lse;
   const float* D;
+  float* d2;
   LamArg lam;
   int H, G, N, d, dv_, causal;
   float scale;
@@ -279,10 +280,11 @@ __global__ void __launch_bounds__(kThreads) diff_bwd_row(Args a) {
   load_rows(qs, ld, q, row0, N, a.d);
   load_rows(qs + kT * ld, ld, q + qsz, row0, N, a.d);
   load_rows(dos, ldv, static_cast<const T*>(a.dO) + (size_t)bh * N * a.dv_, row0, N, a.dv_);
-  float lse[2][4], D[2][4], w[4], acc[2][4][4 * NGD];
+  float lse[2][4], D[2][4], w[4], d2[4], acc[2][4][4 * NGD];
 #pragma unroll
   for (int i = 0; i < 4; ++i) {
     const int r = row0 + 4 * ty + i;
+    d2[i] = 0.f;
 #pragma unroll
     for (int m = 0; m < 2; ++m) {
       const size_t at = ((size_t)bh * 2 + m) * N + (r < N ? r : 0);
@@ -314,12 +316,20 @@ __global__ void __launch_bounds__(kThreads) diff_bwd_row(Args a) {
         for (int j = 0; j < 4; ++j) {
           const int col = j0 + tx + 16 * j;
           const bool in = r < N && col < N && (!a.causal || col <= r);
-          s[i][j] = in ? f * expf(s[i][j] * a.scale - lse[m][i]) * (dp[i][j] - D[m][i]) : 0.f;
+          const float pr = in ? expf(s[i][j] * a.scale - lse[m][i]) : 0.f;
+          if (m == 1) d2[i] = fmaf(pr, dp[i][j], d2[i]);
+          s[i][j] = in ? f * pr * (dp[i][j] - D[m][i]) : 0.f;
         }
       }
       put_tile(ps, s, ty, tx);
       tile_add<NGD>(acc[m], ps, ks + m * kT * ld, ld, a.d, ty, tx);
     }
+  }
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    const int r = row0 + 4 * ty + i;
+    const float s = row16_sum(d2[i]);
+    if (tx == 0 && r < N) a.d2[(size_t)bh * N + r] = s;
   }
 #pragma unroll
   for (int m = 0; m < 2; ++m)
@@ -442,6 +452,7 @@ cudaError_t backward_t(const DiffProblem& p, const DiffTensors& t, const DiffWor
                        LaunchLog& log) {
   Args a = make_args(p, t);
   a.D = ws.D;
+  a.d2 = ws.d2;
   const int blocks = (p.N + kT - 1) / kT;
   const size_t floats = (size_t)kT * (4 * ld_of(p.d) + 2 * ld_of(p.dv) + kLdp);
   const dim3 rows(blocks, p.B * p.H), cols(blocks, p.B * p.Hk);

@@ -1,0 +1,1120 @@
+// Differential attention on the tensor cores (tcgen05 / TMEM / TMA), bf16,
+// d = 64, dv = 64 or 128.  Per head, with m = 1, 2 (code: 0, 1) and c the scale,
+//   S^m = c Q^m K^mT, P^m = softmax(S^m), O = P^1 V - lam P^2 V;
+//   dP = dO V^T, D^m = dO . O^m, dS^1 = P^1*(dP - D^1),
+//   dS^2 = -lam P^2*(dP - D^2), dQ^m = c dS^m K^m, dK^m = c dS^mT Q^m,
+//   dV = (P^1 - lam P^2)^T dO, dlam_i = -sum_j P^2_ij dP_ij.
+//
+// The two maps are two score streams over one stream of values: the kernels
+// walk "subtiles" u = 2 t + m (tile t of the streamed side, map m), whose
+// scores alternate between two TMEM buffers, so the tensor pipe works on one
+// map while the elementwise warps work on the other.
+//
+// forward (128 query rows per CTA, 128-key tiles): online softmax of both
+//   maps, O^1 and O^2 in TMEM, the difference taken once in the epilogue in
+//   fp32.  V is loaded once for both products.
+// row pass (128 query rows, 128-key tiles): dQ of both maps.  dP is computed
+//   once per tile and stays in registers for the second map.
+// column pass (128 key rows, 64-query tiles): dK of both maps and dV, whose
+//   two products are one: W = P^1 - lam P^2 is formed in fp32 and multiplied
+//   with dO once.  A CTA loops over the query heads that share its key head.
+// The row and the column pass recompute the scores rather than exchange dQ
+// through atomics: every output is accumulated by one CTA in a fixed order.
+//
+// Probabilities, W and dS are rounded to bf16 as operands of the second
+// products, the precision of the tensors they are multiplied with; scores,
+// softmax statistics, row scalars and every accumulator are fp32.
+//
+// Warp roles as in the other tensor-core kernels: 16 elementwise warps (warp w:
+// TMEM lane quadrant w % 4, column slice w / 4), one TMA producer, one MMA
+// issuer.  Every wait is bounded, and every warp-collective operation sits in
+// warp-uniform control flow.
+#include <cuda.h>
+#include <cuda_bf16.h>
+#include <cuda_runtime.h>
+#include <cudaTypedefs.h>
+#include <math.h>
+
+#include "common.cuh"
+#include "internal.h"
+#include "ops.h"
+#include "sm103.cuh"
+#include "tc_common.cuh"
+
+namespace fbob {
+
+using namespace sm103;
+using namespace tc;
+
+namespace {
+
+constexpr int kWarps = 16;                 // elementwise warps
+constexpr int kConsumers = kWarps * 32;
+constexpr int kProducerWarp = kWarps;
+constexpr int kMmaWarp = kWarps + 1;
+constexpr int kThreads = (kWarps + 2) * 32;
+constexpr int kSlices = kWarps / 4;        // column slices per row
+constexpr float kLn2 = 0.6931471805599453f;
+constexpr uint64_t kDrainNs = 100000000ull;  // limit of the waits after an abort
+constexpr int kD = 64;                     // features of a query or key
+
+struct Common {
+  int* status;
+  unsigned long long wait_ns;  // limit of one bounded wait
+  int N, causal;
+  int H, G;        // query heads, and those per key head
+  int units, group;  // CTA grid: heads, heads per group (cta_coord)
+  float scale;
+  LamArg lam;
+};
+
+__device__ __forceinline__ float lam_value(const LamArg& l, size_t i) {
+  return l.bf16 ? __bfloat162float(static_cast<const __nv_bfloat16*>(l.p)[i])
+                : static_cast<const float*>(l.p)[i];
+}
+// lam of row n of head bh = b H + h
+__device__ __forceinline__ float lam_row(const LamArg& l, int bh, int H, int N, int n) {
+  return lam_value(l, l.kind == FBOB_LAM_ONE ? 0 : l.kind == FBOB_LAM_HEAD ? (size_t)(bh % H)
+                                                                           : (size_t)bh * N + n);
+}
+
+// One arrival for the whole warp: its lanes' earlier writes (shared memory, or
+// TMEM behind tc_fence_before) are ordered before it.
+__device__ __forceinline__ void warp_arrive(uint64_t* bar) {
+  __syncwarp();
+  if ((threadIdx.x & 31) == 0) mbar_arrive(bar);
+}
+
+// 32 fp32 TMEM columns, scaled, to 32 consecutive bf16 of global memory.
+__device__ __forceinline__ void store32(__nv_bfloat16* dst, const uint32_t (&v)[32], float mul) {
+  uint4* p = reinterpret_cast<uint4*>(dst);
+#pragma unroll
+  for (int q = 0; q < 4; ++q) {
+    uint32_t w[4];
+#pragma unroll
+    for (int e = 0; e < 4; ++e)
+      w[e] = pack_bf16(__uint_as_float(v[8 * q + 2 * e]) * mul,
+                       __uint_as_float(v[8 * q + 2 * e + 1]) * mul);
+    p[q] = make_uint4(w[0], w[1], w[2], w[3]);
+  }
+}
+
+// ===========================================================================
+// Forward
+// ===========================================================================
+template <int DV>
+struct Fwd {
+  static constexpr int BM = 128, BN = 128;
+  static constexpr int KS = 4, VS = 3;             // K subtile and V tile stages
+  static constexpr uint32_t QB = BM * kD * 2;      // Q or K subtile
+  static constexpr uint32_t VB = BN * DV * 2;
+  static constexpr uint32_t OFF_Q = 0, OFF_K = 2 * QB, OFF_V = OFF_K + KS * QB;
+  // [2][slices][128] subtile row maxima; the epilogue's [2][slices][128] sums
+  static constexpr uint32_t OFF_RED = OFF_V + VS * VB;
+  static constexpr uint32_t OFF_MISC = OFF_RED + 4 * kSlices * 128 * 4;
+  static constexpr uint32_t SMEM = OFF_MISC + 512;
+  static_assert(SMEM <= 232448, "forward shared memory budget");
+  // TMEM columns: two score buffers (map m in buffer m; bf16 P overwrites the
+  // first 16 of each thread's 32), O^1, O^2
+  static constexpr uint32_t TMEM_COLS = 512;
+  __host__ __device__ static constexpr uint32_t T_S(int m) { return 128u * m; }
+  __host__ __device__ static constexpr uint32_t T_O(int m) { return 256u + (uint32_t)DV * m; }
+  __host__ __device__ static constexpr uint32_t p_col(int k) { return 32u * (k >> 1) + 8u * (k & 1); }
+  // The reference maximum (log2 domain) moves only when a subtile's maximum
+  // exceeds it by more than this, so O is rescaled in TMEM rarely
+  static constexpr float kRescale = 8.f;
+};
+
+struct FwdParams : Common {
+  __nv_bfloat16 *o, *o2;
+  float* lse;
+};
+
+template <int DV>
+__global__ void __launch_bounds__(kThreads, 1)
+    diff_fwd_pass(const __grid_constant__ CUtensorMap mQ, const __grid_constant__ CUtensorMap mK,
+                  const __grid_constant__ CUtensorMap mV, FwdParams prm) {
+  using C = Fwd<DV>;
+  extern __shared__ __align__(1024) uint8_t smem[];
+  const uint32_t sb = smem_u32(smem);
+  if (sb & 1023u) {  // 128-byte swizzled tiles need a 1024-byte aligned base
+    if (threadIdx.x == 0) report_status(prm.status, FBOB_ERR_CUDA);
+    return;
+  }
+  uint64_t* q_full = reinterpret_cast<uint64_t*>(smem + C::OFF_MISC);
+  uint64_t* k_full = q_full + 1;             // [KS]
+  uint64_t* k_empty = k_full + C::KS;        // [KS]
+  uint64_t* v_full = k_empty + C::KS;        // [VS]
+  uint64_t* v_empty = v_full + C::VS;        // [VS]
+  uint64_t* s_full = v_empty + C::VS;        // [2]: scores of map m in TMEM
+  uint64_t* p_full = s_full + 2;             // [2]: bf16 P written, O^m rescaled
+  uint64_t* o_ready = p_full + 2;            // [2]: P V of map m done, one phase per tile
+  uint64_t* red_full = o_ready + 2;          // [2][4]: the slices' maxima, per lane quadrant
+  uint64_t* drain = red_full + 8;
+  static_assert((1 + 2 * C::KS + 2 * C::VS + 15) * 8 <= 256, "barriers end below the TMEM slot");
+  uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(smem + C::OFF_MISC + 256);
+  Abort* ab = reinterpret_cast<Abort*>(smem + C::OFF_MISC + 264);
+  float* red = reinterpret_cast<float*>(smem + C::OFF_RED);
+
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int N = prm.N;
+  const int nblk = (N + C::BM - 1) / C::BM;
+  const CtaCoord cc = cta_coord(prm.units, prm.group, nblk);
+  const int bh = cc.bh;
+  const int kvh = (bh / prm.H) * (prm.H / prm.G) + (bh % prm.H) / prm.G;
+  const int blk = prm.causal ? nblk - 1 - cc.blk : cc.blk;  // long rows first
+  const int i0 = blk * C::BM;
+  const int T = ((prm.causal ? min(N, i0 + C::BM) : N) + C::BN - 1) / C::BN;
+
+  if (threadIdx.x == 0) {
+    mbar_init(q_full, 1);
+    for (int s = 0; s < C::KS; ++s) {
+      mbar_init(k_full + s, 1);
+      mbar_init(k_empty + s, 1);
+    }
+    for (int s = 0; s < C::VS; ++s) {
+      mbar_init(v_full + s, 1);
+      mbar_init(v_empty + s, 1);
+    }
+    for (int m = 0; m < 2; ++m) {
+      mbar_init(s_full + m, 1);
+      mbar_init(p_full + m, kWarps);
+      mbar_init(o_ready + m, 1);
+    }
+    for (int i = 0; i < 8; ++i) mbar_init(red_full + i, kSlices);
+    mbar_init(drain, 1);
+    ab->flag = 0;
+    ab->limit_ns = prm.wait_ns;
+    fence_mbar_init();
+  }
+  if (warp == kMmaWarp) {
+    tmem_alloc(tmem_slot, C::TMEM_COLS);
+    tmem_relinquish();
+  }
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  const uint32_t tmem = *tmem_slot;
+
+  if (warp == kProducerWarp) {
+    if (lane == 0) {
+      mbar_arrive_expect_tx(q_full, 2 * C::QB);
+      load_tile(smem + C::OFF_Q, &mQ, q_full, i0, 2 * bh);
+      load_tile(smem + C::OFF_Q + C::QB, &mQ, q_full, i0, 2 * bh + 1);
+      int k_issued = 0, v_issued = 0;
+      auto load_k = [&](int u) -> bool {
+        const int s = u % C::KS;
+        if (u >= C::KS && !wait_bar(k_empty + s, ((u / C::KS) - 1) & 1, ab, prm.status)) return false;
+        mbar_arrive_expect_tx(k_full + s, C::QB);
+        load_tile(smem + C::OFF_K + s * C::QB, &mK, k_full + s, (u >> 1) * C::BN, 2 * kvh + (u & 1));
+        ++k_issued;
+        return true;
+      };
+      auto load_v = [&](int t) -> bool {
+        const int s = t % C::VS;
+        if (t >= C::VS && !wait_bar(v_empty + s, ((t / C::VS) - 1) & 1, ab, prm.status)) return false;
+        mbar_arrive_expect_tx(v_full + s, C::VB);
+        load_tile(smem + C::OFF_V + s * C::VB, &mV, v_full + s, t * C::BN, kvh);
+        ++v_issued;
+        return true;
+      };
+      // K runs a tile ahead of V
+      bool ok = load_k(0) && load_k(1);
+      for (int t = 0; ok && t < T; ++t) {
+        if (t + 1 < T && !(load_k(2 * t + 2) && load_k(2 * t + 3))) break;
+        if (!load_v(t)) break;
+      }
+      // every load this thread issued has landed before the CTA exits (after an
+      // abort some were never awaited); on the normal path these return at once
+      mbar_wait_bounded(q_full, 0, prm.status, kDrainNs);
+      for (int u = max(0, k_issued - C::KS); u < k_issued; ++u)
+        mbar_wait_bounded(k_full + (u % C::KS), (u / C::KS) & 1, prm.status, kDrainNs);
+      for (int t = max(0, v_issued - C::VS); t < v_issued; ++t)
+        mbar_wait_bounded(v_full + (t % C::VS), (t / C::VS) & 1, prm.status, kDrainNs);
+    }
+  } else if (warp == kMmaWarp) {
+    constexpr uint32_t id_s = idesc_bf16(128, C::BN, false, false);  // S = Q K^T
+    constexpr uint32_t id_o = idesc_bf16(128, DV, false, true);      // O += P V: B MN-major
+    bool ok = warp_wait(q_full, 0, ab, prm.status);
+    // O^m += P(u) V(t), A = bf16 P from TMEM
+    auto issue_pv = [&](int u) -> bool {
+      const int m = u & 1, t = u >> 1, vs = t % C::VS;
+      if (!warp_wait(p_full + m, t & 1, ab, prm.status)) return false;
+      if (m == 0 && !warp_wait(v_full + vs, (t / C::VS) & 1, ab, prm.status)) return false;
+      tc_fence_after();
+      const uint32_t v_mn = opaque(lo_mnmajor(sb + C::OFF_V + vs * C::VB, C::BN * 128));
+      const uint32_t t_p = tmem + C::T_S(m), t_o = tmem + C::T_O(m);
+#pragma unroll
+      for (int k = 0; k < C::BN / 16; ++k)
+        mma_ts_w(t_o, t_p + C::p_col(k), v_mn + kstep_off(k), id_o, (t > 0 || k > 0) ? 1u : 0u);
+      if (m == 1) mma_commit_w(v_empty + vs);
+      mma_commit_w(o_ready + m);
+      return true;
+    };
+    // S(u) overwrites the buffer of subtile u - 2, whose P V was issued after
+    // every warp had read its scores and written its P
+    const int U = 2 * T;
+    for (int u = 0; ok && u < U; ++u) {
+      const int s = u % C::KS, m = u & 1;
+      if (!warp_wait(k_full + s, (u / C::KS) & 1, ab, prm.status)) { ok = false; break; }
+      tc_fence_after();
+      const uint32_t q_lo = opaque(lo_kmajor(sb + C::OFF_Q + m * C::QB));
+      const uint32_t k_lo = opaque(lo_kmajor(sb + C::OFF_K + s * C::QB));
+#pragma unroll
+      for (int k = 0; k < kD / 16; ++k)
+        mma_ss_w(tmem + C::T_S(m), q_lo + kslice_off(C::BM, k), k_lo + kslice_off(C::BN, k), id_s,
+                 k > 0 ? 1u : 0u);
+      mma_commit_w(s_full + m);
+      mma_commit_w(k_empty + s);
+      if (u >= 1 && !issue_pv(u - 1)) { ok = false; break; }
+    }
+    if (ok) ok = issue_pv(U - 1);
+    // every MMA this thread issued has completed before TMEM is released
+    mma_commit_w(drain);
+    mbar_wait_bounded(drain, 0, prm.status, kDrainNs);
+  } else {
+    // ---------------- elementwise warps: thread = query row ----------------
+    constexpr int NC = C::BN / kSlices;  // key columns per thread
+    const int quad = warp & 3, slice = warp >> 2;
+    const int row = 32 * quad + lane;
+    const int i = i0 + row;
+    const float sc2 = prm.scale * kLog2e;
+    const f2 sc2_2 = {sc2, sc2};
+    const uint32_t lane_off = (uint32_t)(32 * quad) << 16;
+    bool ok = true;
+    // per map: the row's reference maximum (log2 domain), the same in all
+    // slices, and this slice's sum of 2^(S c log2 e - max)
+    float mx[2] = {-INFINITY, -INFINITY}, l[2] = {0.f, 0.f};
+    for (int t = 0; ok && t < T; ++t) {
+      const int j0 = t * C::BN + NC * slice;
+      const bool need_mask = (j0 + NC > N) || (prm.causal && j0 + NC - 1 > i0 + 32 * quad);
+#pragma unroll
+      for (int m = 0; m < 2; ++m) {
+        if (!ok) break;
+        if (!warp_wait(s_full + m, t & 1, ab, prm.status)) { ok = false; break; }
+        tc_fence_after();
+        const uint32_t ts = tmem + lane_off + C::T_S(m) + NC * slice;
+        uint32_t sr[NC];
+        tmem_ld32(ts, sr);
+        // this slice's maximum (c log2 e > 0 keeps the order); masked entries
+        // become -inf, so they give 2^-inf = 0 below
+        float top = -INFINITY;
+        if (need_mask) {
+#pragma unroll
+          for (int c = 0; c < NC; ++c) {
+            const int j = j0 + c;
+            const float v = (j < N && (!prm.causal || j <= i)) ? __uint_as_float(sr[c]) : -INFINITY;
+            sr[c] = __float_as_uint(v);
+            top = fmaxf(top, v);
+          }
+        } else {
+#pragma unroll
+          for (int c = 0; c < NC; ++c) top = fmaxf(top, __uint_as_float(sr[c]));
+        }
+        // exchanged between the slices of a row; a buffer is rewritten two
+        // subtiles later, after every slice has arrived for the next one and
+        // so has read this one
+        float* rt = red + m * kSlices * 128;
+        rt[slice * 128 + row] = top * sc2;
+        warp_arrive(red_full + 4 * m + quad);
+        uint32_t pw[NC / 2];
+        float sum;
+        auto exps = [&]() {
+          const f2 nm = {-mx[m], -mx[m]};
+          f2 acc = {0.f, 0.f};
+#pragma unroll
+          for (int c = 0; c < NC; c += 2) {
+            const f2 x = fma2({__uint_as_float(sr[c]), __uint_as_float(sr[c + 1])}, sc2_2, nm);
+            const f2 p = {ex2_approx(x.x), ex2_approx(x.y)};
+            acc = add2(acc, p);
+            pw[c >> 1] = pack_bf16(p.x, p.y);
+          }
+          sum = acc.x + acc.y;
+        };
+        // The maximum rarely moves after the first tile, so the probabilities
+        // are computed against the old one while the other slices' maxima
+        // arrive, and again where it did move
+        if (t > 0) exps();
+        if (!warp_wait(red_full + 4 * m + quad, t & 1, ab, prm.status)) { ok = false; break; }
+        float mt = rt[row];
+#pragma unroll
+        for (int s = 1; s < kSlices; ++s) mt = fmaxf(mt, rt[s * 128 + row]);
+        const bool move = mt > mx[m] + C::kRescale;
+        if (t == 0) {
+          mx[m] = mt;  // finite: key 0 is visible to every row
+          exps();
+          l[m] = sum;
+        } else if (__any_sync(0xffffffffu, move)) {
+          // the row's O^m holds the sums of the earlier tiles: rescale this
+          // slice's DV/4 columns once their MMAs are done (rows that did not
+          // move scale by 1)
+          const float alpha = move ? ex2_approx(mx[m] - mt) : 1.f;
+          if (!warp_wait(o_ready + m, (t - 1) & 1, ab, prm.status)) { ok = false; break; }
+          tc_fence_after();
+#pragma unroll
+          for (int c = 0; c < DV / kSlices; c += 16) {
+            uint32_t v[16];
+            const uint32_t ta = tmem + lane_off + C::T_O(m) + (DV / kSlices) * slice + c;
+            tmem_ld16(ta, v);
+#pragma unroll
+            for (int e = 0; e < 16; ++e) v[e] = __float_as_uint(__uint_as_float(v[e]) * alpha);
+            tmem_st16(ta, v);
+          }
+          if (move) mx[m] = mt;
+          exps();
+          l[m] = fmaf(l[m], alpha, sum);
+        } else {
+          l[m] += sum;
+        }
+        // bf16 P over the first 16 of the 32 columns this thread read
+        tmem_st16(ts, pw);
+        tc_fence_before();
+        warp_arrive(p_full + m);
+      }
+    }
+    // ---- epilogue: O = O^1 / l^1 - lam O^2 / l^2, and LSE (natural log) ----
+    // every elementwise thread gets to this barrier, also after a failed wait
+    float* part = red + 2 * kSlices * 128;
+#pragma unroll
+    for (int m = 0; m < 2; ++m) part[(m * kSlices + slice) * 128 + row] = l[m];
+    named_sync<kConsumers>(1);
+    float L[2];
+#pragma unroll
+    for (int m = 0; m < 2; ++m) {
+      L[m] = 0.f;
+#pragma unroll
+      for (int s = 0; s < kSlices; ++s) L[m] += part[(m * kSlices + s) * 128 + row];
+    }
+    ok = __all_sync(0xffffffffu, ok);
+    if (ok) ok = warp_wait(o_ready + 0, (T - 1) & 1, ab, prm.status);
+    if (ok) ok = warp_wait(o_ready + 1, (T - 1) & 1, ab, prm.status);
+    tc_fence_after();
+    if (ok) {
+      constexpr int PART = DV / kSlices;
+      const bool in = i < N;
+      const float inv1 = 1.f / L[0], inv2 = 1.f / L[1];
+      const float w = in ? lam_row(prm.lam, bh, prm.H, N, i) : 0.f;
+      const size_t at = ((size_t)bh * N + (in ? i : 0)) * DV + PART * slice;
+#pragma unroll
+      for (int c = 0; c < PART; c += 16) {
+        uint32_t a[16], b[16];
+        tmem_ld16x2(tmem + lane_off + C::T_O(0) + PART * slice + c,
+                    tmem + lane_off + C::T_O(1) + PART * slice + c, a, b);
+        uint32_t wo[8], w2[8];
+#pragma unroll
+        for (int e = 0; e < 8; ++e) {
+          const float x2 = __uint_as_float(b[2 * e]) * inv2, y2 = __uint_as_float(b[2 * e + 1]) * inv2;
+          wo[e] = pack_bf16(fmaf(-w, x2, __uint_as_float(a[2 * e]) * inv1),
+                            fmaf(-w, y2, __uint_as_float(a[2 * e + 1]) * inv1));
+          w2[e] = pack_bf16(x2, y2);
+        }
+        if (in) {
+          uint4* po = reinterpret_cast<uint4*>(prm.o + at + c);
+          po[0] = make_uint4(wo[0], wo[1], wo[2], wo[3]);
+          po[1] = make_uint4(wo[4], wo[5], wo[6], wo[7]);
+          if (prm.o2) {
+            uint4* p2 = reinterpret_cast<uint4*>(prm.o2 + at + c);
+            p2[0] = make_uint4(w2[0], w2[1], w2[2], w2[3]);
+            p2[1] = make_uint4(w2[4], w2[5], w2[6], w2[7]);
+          }
+        }
+      }
+      if (in && slice < 2) {
+        const float ms = slice == 0 ? mx[0] : mx[1], ls = slice == 0 ? L[0] : L[1];
+        prm.lse[((size_t)bh * 2 + slice) * N + i] = (ms + log2f(ls)) * kLn2;
+      }
+    }
+  }
+  tc_fence_before();
+  __syncthreads();
+  if (warp == kMmaWarp) {
+    tc_fence_after();
+    tmem_dealloc(tmem, C::TMEM_COLS);
+  }
+}
+
+// ===========================================================================
+// Row pass: dQ of both maps, and each row's sum_j P^2 dP
+// ===========================================================================
+template <int DV>
+struct Row {
+  static constexpr int BM = 128, BN = 128;
+  static constexpr int KS = 4, VS = 2;
+  static constexpr uint32_t QB = BM * kD * 2;
+  static constexpr uint32_t VB = BN * DV * 2;  // dO or V tile
+  static constexpr uint32_t OFF_Q = 0, OFF_DO = 2 * QB, OFF_K = OFF_DO + VB;
+  static constexpr uint32_t OFF_V = OFF_K + KS * QB;
+  static constexpr uint32_t OFF_RED = OFF_V + VS * VB;  // [slices][128]
+  static constexpr uint32_t OFF_MISC = OFF_RED + kSlices * 128 * 4;
+  static constexpr uint32_t SMEM = OFF_MISC + 512;
+  static_assert(SMEM <= 232448, "row pass shared memory budget");
+  // TMEM columns: two score buffers (bf16 dS over the first 16 of each
+  // thread's 32), dP, dQ^1, dQ^2
+  static constexpr uint32_t TMEM_COLS = 512, T_DP = 256;
+  __host__ __device__ static constexpr uint32_t T_S(int m) { return 128u * m; }
+  __host__ __device__ static constexpr uint32_t T_DQ(int m) { return 384u + (uint32_t)kD * m; }
+  __host__ __device__ static constexpr uint32_t a_col(int k) { return 32u * (k >> 1) + 8u * (k & 1); }
+};
+
+struct RowParams : Common {
+  __nv_bfloat16* dq;
+  const float *lse, *D;
+  float* d2;  // [B, H, N]: sum_j P^2_ij dP_ij
+};
+
+template <int DV>
+__global__ void __launch_bounds__(kThreads, 1)
+    diff_row_pass(const __grid_constant__ CUtensorMap mQ, const __grid_constant__ CUtensorMap mK,
+                  const __grid_constant__ CUtensorMap mV, const __grid_constant__ CUtensorMap mDO,
+                  RowParams prm) {
+  using C = Row<DV>;
+  extern __shared__ __align__(1024) uint8_t smem[];
+  const uint32_t sb = smem_u32(smem);
+  if (sb & 1023u) {
+    if (threadIdx.x == 0) report_status(prm.status, FBOB_ERR_CUDA);
+    return;
+  }
+  uint64_t* q_full = reinterpret_cast<uint64_t*>(smem + C::OFF_MISC);  // Q^1, Q^2, dO
+  uint64_t* k_full = q_full + 1;           // [KS]
+  uint64_t* k_empty = k_full + C::KS;      // [KS]
+  uint64_t* v_full = k_empty + C::KS;      // [VS]
+  uint64_t* v_empty = v_full + C::VS;      // [VS]
+  uint64_t* s_full = v_empty + C::VS;      // [2]
+  uint64_t* ds_full = s_full + 2;          // [2]: bf16 dS written over the scores
+  uint64_t* dp_full = ds_full + 2;
+  uint64_t* dp_read = dp_full + 1;         // the elementwise warps hold dP
+  uint64_t* acc_done = dp_read + 1;
+  uint64_t* drain = acc_done + 1;
+  static_assert((1 + 2 * C::KS + 2 * C::VS + 8) * 8 <= 256, "barriers end below the TMEM slot");
+  uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(smem + C::OFF_MISC + 256);
+  Abort* ab = reinterpret_cast<Abort*>(smem + C::OFF_MISC + 264);
+  float* red = reinterpret_cast<float*>(smem + C::OFF_RED);
+
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int N = prm.N;
+  const int nblk = (N + C::BM - 1) / C::BM;
+  const CtaCoord cc = cta_coord(prm.units, prm.group, nblk);
+  const int bh = cc.bh;
+  const int kvh = (bh / prm.H) * (prm.H / prm.G) + (bh % prm.H) / prm.G;
+  const int blk = prm.causal ? nblk - 1 - cc.blk : cc.blk;
+  const int i0 = blk * C::BM;
+  const int T = ((prm.causal ? min(N, i0 + C::BM) : N) + C::BN - 1) / C::BN;
+
+  if (threadIdx.x == 0) {
+    mbar_init(q_full, 1);
+    for (int s = 0; s < C::KS; ++s) {
+      mbar_init(k_full + s, 1);
+      mbar_init(k_empty + s, 1);
+    }
+    for (int s = 0; s < C::VS; ++s) {
+      mbar_init(v_full + s, 1);
+      mbar_init(v_empty + s, 1);
+    }
+    for (int m = 0; m < 2; ++m) {
+      mbar_init(s_full + m, 1);
+      mbar_init(ds_full + m, kWarps);
+    }
+    mbar_init(dp_full, 1);
+    mbar_init(dp_read, kWarps);
+    mbar_init(acc_done, 1);
+    mbar_init(drain, 1);
+    ab->flag = 0;
+    ab->limit_ns = prm.wait_ns;
+    fence_mbar_init();
+  }
+  if (warp == kMmaWarp) {
+    tmem_alloc(tmem_slot, C::TMEM_COLS);
+    tmem_relinquish();
+  }
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  const uint32_t tmem = *tmem_slot;
+
+  if (warp == kProducerWarp) {
+    if (lane == 0) {
+      mbar_arrive_expect_tx(q_full, 2 * C::QB + C::VB);
+      load_tile(smem + C::OFF_DO, &mDO, q_full, i0, bh);
+      load_tile(smem + C::OFF_Q, &mQ, q_full, i0, 2 * bh);
+      load_tile(smem + C::OFF_Q + C::QB, &mQ, q_full, i0, 2 * bh + 1);
+      int k_issued = 0, v_issued = 0;
+      bool ok = true;
+      for (int t = 0; ok && t < T; ++t) {
+        const int vs = t % C::VS;
+        if (t >= C::VS && !wait_bar(v_empty + vs, ((t / C::VS) - 1) & 1, ab, prm.status)) break;
+        mbar_arrive_expect_tx(v_full + vs, C::VB);
+        load_tile(smem + C::OFF_V + vs * C::VB, &mV, v_full + vs, t * C::BN, kvh);
+        ++v_issued;
+        for (int u = 2 * t; u < 2 * t + 2; ++u) {
+          const int s = u % C::KS;
+          if (u >= C::KS && !wait_bar(k_empty + s, ((u / C::KS) - 1) & 1, ab, prm.status)) {
+            ok = false;
+            break;
+          }
+          mbar_arrive_expect_tx(k_full + s, C::QB);
+          load_tile(smem + C::OFF_K + s * C::QB, &mK, k_full + s, t * C::BN, 2 * kvh + (u & 1));
+          ++k_issued;
+        }
+      }
+      mbar_wait_bounded(q_full, 0, prm.status, kDrainNs);
+      for (int u = max(0, k_issued - C::KS); u < k_issued; ++u)
+        mbar_wait_bounded(k_full + (u % C::KS), (u / C::KS) & 1, prm.status, kDrainNs);
+      for (int t = max(0, v_issued - C::VS); t < v_issued; ++t)
+        mbar_wait_bounded(v_full + (t % C::VS), (t / C::VS) & 1, prm.status, kDrainNs);
+    }
+  } else if (warp == kMmaWarp) {
+    constexpr uint32_t id_s = idesc_bf16(128, C::BN, false, false);  // S and dP
+    constexpr uint32_t id_q = idesc_bf16(128, kD, false, true);      // dQ += dS K: B MN-major
+    auto issue_dp = [&](int t) -> bool {
+      const int vs = t % C::VS;
+      if (!warp_wait(v_full + vs, (t / C::VS) & 1, ab, prm.status)) return false;
+      tc_fence_after();
+      const uint32_t do_lo = opaque(lo_kmajor(sb + C::OFF_DO));
+      const uint32_t v_lo = opaque(lo_kmajor(sb + C::OFF_V + vs * C::VB));
+#pragma unroll
+      for (int k = 0; k < DV / 16; ++k)
+        mma_ss_w(tmem + C::T_DP, do_lo + kslice_off(C::BM, k), v_lo + kslice_off(C::BN, k), id_s,
+                 k > 0 ? 1u : 0u);
+      mma_commit_w(dp_full);
+      mma_commit_w(v_empty + vs);
+      return true;
+    };
+    auto issue_s = [&](int u) -> bool {
+      const int s = u % C::KS, m = u & 1;
+      if (!warp_wait(k_full + s, (u / C::KS) & 1, ab, prm.status)) return false;
+      tc_fence_after();
+      const uint32_t q_lo = opaque(lo_kmajor(sb + C::OFF_Q + m * C::QB));
+      const uint32_t k_lo = opaque(lo_kmajor(sb + C::OFF_K + s * C::QB));
+#pragma unroll
+      for (int k = 0; k < kD / 16; ++k)
+        mma_ss_w(tmem + C::T_S(m), q_lo + kslice_off(C::BM, k), k_lo + kslice_off(C::BN, k), id_s,
+                 k > 0 ? 1u : 0u);
+      mma_commit_w(s_full + m);
+      return true;
+    };
+    const int U = 2 * T;
+    bool ok = warp_wait(q_full, 0, ab, prm.status) && issue_dp(0) && issue_s(0);
+    for (int u = 0; ok && u < U; ++u) {
+      const int m = u & 1, t = u >> 1, s = u % C::KS;
+      // the next subtile's scores go over the dS of subtile u - 1, whose dQ
+      // product was issued before; the next tile's dP once this one is read
+      if (u + 1 < U && !issue_s(u + 1)) { ok = false; break; }
+      if (m == 0 && t + 1 < T) {
+        if (!warp_wait(dp_read, t & 1, ab, prm.status)) { ok = false; break; }
+        tc_fence_after();
+        if (!issue_dp(t + 1)) { ok = false; break; }
+      }
+      if (!warp_wait(ds_full + m, t & 1, ab, prm.status)) { ok = false; break; }
+      tc_fence_after();
+      const uint32_t k_mn = opaque(lo_mnmajor(sb + C::OFF_K + s * C::QB, C::BN * 128));
+#pragma unroll
+      for (int k = 0; k < C::BN / 16; ++k)
+        mma_ts_w(tmem + C::T_DQ(m), tmem + C::T_S(m) + C::a_col(k), k_mn + kstep_off(k), id_q,
+                 (t > 0 || k > 0) ? 1u : 0u);
+      mma_commit_w(k_empty + s);
+    }
+    if (ok) mma_commit_w(acc_done);
+    mma_commit_w(drain);
+    mbar_wait_bounded(drain, 0, prm.status, kDrainNs);
+  } else {
+    // ---------------- elementwise warps: thread = query row ----------------
+    constexpr int NC = C::BN / kSlices;
+    const int quad = warp & 3, slice = warp >> 2;
+    const int row = 32 * quad + lane;
+    const int i = i0 + row;
+    const bool in = i < N;
+    const uint32_t lane_off = (uint32_t)(32 * quad) << 16;
+    const float sc2 = prm.scale * kLog2e;
+    const f2 sc2_2 = {sc2, sc2};
+    // dS^1 = P^1 (dP - D^1), dS^2 = P^2 (-lam dP + lam D^2): a factor and a
+    // summand per map; rows past the end have Q = dO = 0 and stay zero
+    const size_t r1 = ((size_t)bh * 2) * N + (in ? i : 0), r2 = r1 + N;
+    const float w = in ? lam_row(prm.lam, bh, prm.H, N, i) : 0.f;
+    const float nl[2] = {in ? -prm.lse[r1] * kLog2e : 0.f, in ? -prm.lse[r2] * kLog2e : 0.f};
+    const float mul[2] = {1.f, -w};
+    const float add[2] = {in ? -prm.D[r1] : 0.f, in ? w * prm.D[r2] : 0.f};
+    f2 d2 = {0.f, 0.f};
+    bool ok = true;
+    for (int t = 0; ok && t < T; ++t) {
+      const int j0 = t * C::BN + NC * slice;
+      const bool need_mask = (j0 + NC > N) || (prm.causal && j0 + NC - 1 > i0 + 32 * quad);
+      uint32_t dp[NC];
+#pragma unroll
+      for (int m = 0; m < 2; ++m) {
+        if (!ok) break;
+        if (!warp_wait(s_full + m, t & 1, ab, prm.status)) { ok = false; break; }
+        if (m == 0 && !warp_wait(dp_full, t & 1, ab, prm.status)) { ok = false; break; }
+        tc_fence_after();
+        const uint32_t ts = tmem + lane_off + C::T_S(m) + NC * slice;
+        uint32_t sr[NC];
+        if (m == 0) {
+          tmem_ld32x2(ts, tmem + lane_off + C::T_DP + NC * slice, sr, dp);
+          tc_fence_before();
+          warp_arrive(dp_read);
+        } else {
+          tmem_ld32(ts, sr);
+        }
+        const f2 nl2 = {nl[m], nl[m]}, mul2_ = {mul[m], mul[m]}, add2_ = {add[m], add[m]};
+        uint32_t dsw[NC / 2];
+#pragma unroll
+        for (int c = 0; c < NC; c += 2) {
+          const f2 x = fma2({__uint_as_float(sr[c]), __uint_as_float(sr[c + 1])}, sc2_2, nl2);
+          f2 p = {ex2_approx(x.x), ex2_approx(x.y)};
+          if (need_mask) {
+            const int j = j0 + c;
+            p.x = (j < N && (!prm.causal || j <= i)) ? p.x : 0.f;
+            p.y = (j + 1 < N && (!prm.causal || j + 1 <= i)) ? p.y : 0.f;
+          }
+          const f2 g = {__uint_as_float(dp[c]), __uint_as_float(dp[c + 1])};
+          if (m == 1) d2 = fma2(p, g, d2);
+          const f2 ds = mul2(p, fma2(g, mul2_, add2_));
+          dsw[c >> 1] = pack_bf16(ds.x, ds.y);
+        }
+        tmem_st16(ts, dsw);
+        tc_fence_before();
+        warp_arrive(ds_full + m);
+      }
+    }
+    // ---- epilogue: dQ (scaled): 32 features of one map per thread ----
+    red[slice * 128 + row] = d2.x + d2.y;
+    named_sync<kConsumers>(1);
+    ok = __all_sync(0xffffffffu, ok);
+    if (ok) ok = warp_wait(acc_done, 0, ab, prm.status);
+    tc_fence_after();
+    if (ok) {
+      const int m = slice >> 1, f = 32 * (slice & 1);
+      uint32_t v[32];
+      tmem_ld32(tmem + lane_off + C::T_DQ(0) + kD * m + f, v);
+      if (in) {
+        store32(prm.dq + (((size_t)bh * 2 + m) * N + i) * kD + f, v, prm.scale);
+        if (slice == 0) {
+          float s = 0.f;
+#pragma unroll
+          for (int u = 0; u < kSlices; ++u) s += red[u * 128 + row];
+          prm.d2[(size_t)bh * N + i] = s;
+        }
+      }
+    }
+  }
+  tc_fence_before();
+  __syncthreads();
+  if (warp == kMmaWarp) {
+    tc_fence_after();
+    tmem_dealloc(tmem, C::TMEM_COLS);
+  }
+}
+
+// ===========================================================================
+// Column pass: dK of both maps and dV
+// ===========================================================================
+template <int DV>
+struct Col {
+  static constexpr int BM = 128, BN = 64;
+  static constexpr int QS = 6, OS = 4;            // Q subtile and dO tile stages
+  static constexpr uint32_t KB = BM * kD * 2;     // stationary K subtile
+  static constexpr uint32_t VB = BM * DV * 2;
+  static constexpr uint32_t QB = BN * kD * 2;     // streamed Q subtile
+  static constexpr uint32_t OB = BN * DV * 2;     // streamed dO tile
+  static constexpr uint32_t OFF_K = 0, OFF_V = 2 * KB, OFF_Q = OFF_V + VB;
+  static constexpr uint32_t OFF_DO = OFF_Q + QS * QB;
+  // [OS][5][BN]: -LSE^1 log2 e, -LSE^2 log2 e, -D^1, -lam, lam D^2
+  static constexpr uint32_t OFF_SC = OFF_DO + OS * OB;
+  static constexpr uint32_t OFF_MISC = OFF_SC + OS * 5 * BN * 4;
+  static constexpr uint32_t SMEM = OFF_MISC + 512;
+  static_assert(SMEM <= 232448, "column pass shared memory budget");
+  // TMEM columns: two S^T buffers (each thread's 16 columns then hold bf16
+  // dS^T in the last 8 and, for map 2, W^T in the first 8), two dP^T buffers,
+  // dK^1, dK^2, dV
+  static constexpr uint32_t TMEM_COLS = 512, T_DV = 384;
+  __host__ __device__ static constexpr uint32_t T_S(int m) { return 64u * m; }
+  __host__ __device__ static constexpr uint32_t T_DP(int b) { return 128u + 64u * b; }
+  __host__ __device__ static constexpr uint32_t T_DK(int m) { return 256u + (uint32_t)kD * m; }
+};
+
+struct ColParams : Common {
+  __nv_bfloat16 *dk, *dv;
+  const float *lse, *D;
+};
+
+template <int DV>
+__global__ void __launch_bounds__(kThreads, 1)
+    diff_col_pass(const __grid_constant__ CUtensorMap mK, const __grid_constant__ CUtensorMap mV,
+                  const __grid_constant__ CUtensorMap mQ, const __grid_constant__ CUtensorMap mDO,
+                  ColParams prm) {
+  using C = Col<DV>;
+  extern __shared__ __align__(1024) uint8_t smem[];
+  const uint32_t sb = smem_u32(smem);
+  if (sb & 1023u) {
+    if (threadIdx.x == 0) report_status(prm.status, FBOB_ERR_CUDA);
+    return;
+  }
+  uint64_t* kv_full = reinterpret_cast<uint64_t*>(smem + C::OFF_MISC);
+  uint64_t* q_full = kv_full + 1;          // [QS]
+  uint64_t* q_empty = q_full + C::QS;      // [QS]
+  uint64_t* do_full = q_empty + C::QS;     // [OS]: dO landed, scalars written
+  uint64_t* do_empty = do_full + C::OS;    // [OS]
+  uint64_t* s_full = do_empty + C::OS;     // [2]
+  uint64_t* ds_full = s_full + 2;          // [2]: bf16 operands written over the scores
+  uint64_t* dp_full = ds_full + 2;         // [2]
+  uint64_t* acc_done = dp_full + 2;
+  uint64_t* drain = acc_done + 1;
+  static_assert((1 + 2 * C::QS + 2 * C::OS + 8) * 8 <= 256, "barriers end below the TMEM slot");
+  uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(smem + C::OFF_MISC + 256);
+  Abort* ab = reinterpret_cast<Abort*>(smem + C::OFF_MISC + 264);
+  float* scal = reinterpret_cast<float*>(smem + C::OFF_SC);
+
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int N = prm.N;
+  const CtaCoord cc = cta_coord(prm.units, prm.group, (N + C::BM - 1) / C::BM);
+  const int kvh = cc.bh, Hk = prm.H / prm.G;
+  const int bh0 = (kvh / Hk) * prm.H + (kvh % Hk) * prm.G;  // first query head
+  const int j0 = cc.blk * C::BM;
+  const int qstart = prm.causal ? j0 : 0;  // j0 is a multiple of BN
+  const int Tq = (N - qstart + C::BN - 1) / C::BN;
+  const int T = Tq * prm.G;  // query tiles of all the query heads
+
+  if (threadIdx.x == 0) {
+    mbar_init(kv_full, 1);
+    for (int s = 0; s < C::QS; ++s) {
+      mbar_init(q_full + s, 1);
+      mbar_init(q_empty + s, 1);
+    }
+    for (int s = 0; s < C::OS; ++s) {
+      mbar_init(do_full + s, 1);
+      mbar_init(do_empty + s, 1);
+    }
+    for (int m = 0; m < 2; ++m) {
+      mbar_init(s_full + m, 1);
+      mbar_init(ds_full + m, kWarps);
+      mbar_init(dp_full + m, 1);
+    }
+    mbar_init(acc_done, 1);
+    mbar_init(drain, 1);
+    ab->flag = 0;
+    ab->limit_ns = prm.wait_ns;
+    fence_mbar_init();
+  }
+  if (warp == kMmaWarp) {
+    tmem_alloc(tmem_slot, C::TMEM_COLS);
+    tmem_relinquish();
+  }
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  const uint32_t tmem = *tmem_slot;
+
+  if (warp == kProducerWarp) {
+    if (lane == 0) {
+      mbar_arrive_expect_tx(kv_full, 2 * C::KB + C::VB);
+      load_tile(smem + C::OFF_V, &mV, kv_full, j0, kvh);
+      load_tile(smem + C::OFF_K, &mK, kv_full, j0, 2 * kvh);
+      load_tile(smem + C::OFF_K + C::KB, &mK, kv_full, j0, 2 * kvh + 1);
+    }
+    // the next tile's row scalars are fetched into registers one tile ahead
+    constexpr int PER = C::BN / 32;
+    float pre[5][PER];
+    auto fetch = [&](int bh, int q0) {
+#pragma unroll
+      for (int e = 0; e < PER; ++e) {
+        const int q = q0 + lane + 32 * e;
+        const bool in = q < N;
+        const size_t r1 = (size_t)bh * 2 * N + (in ? q : 0), r2 = r1 + N;
+        const float w = in ? lam_row(prm.lam, bh, prm.H, N, q) : 0.f;
+        pre[0][e] = in ? -prm.lse[r1] * kLog2e : 0.f;
+        pre[1][e] = in ? -prm.lse[r2] * kLog2e : 0.f;
+        pre[2][e] = in ? -prm.D[r1] : 0.f;
+        pre[3][e] = -w;
+        pre[4][e] = in ? w * prm.D[r2] : 0.f;
+      }
+    };
+    int g = 0, t = 0;  // tile within head g
+    fetch(bh0, qstart);
+    int q_issued = 0, o_issued = 0;
+    for (int a = 0; a < T; ++a) {
+      const int os = a % C::OS, q0 = qstart + t * C::BN, bh = bh0 + g;
+      bool ok = true;
+      if (lane == 0 && a >= C::OS)
+        ok = wait_bar(do_empty + os, ((a / C::OS) - 1) & 1, ab, prm.status);
+      if (__shfl_sync(0xffffffffu, ok ? 1 : 0, 0) == 0) break;
+      // the stage's scalars were last read by the elementwise warps of tile
+      // a - OS, before the dV product that freed the stage
+      float* sc = scal + os * 5 * C::BN;
+#pragma unroll
+      for (int x = 0; x < 5; ++x)
+#pragma unroll
+        for (int e = 0; e < PER; ++e) sc[x * C::BN + lane + 32 * e] = pre[x][e];
+      __syncwarp();
+      if (lane == 0) {
+        mbar_arrive_expect_tx(do_full + os, C::OB);
+        load_tile(smem + C::OFF_DO + os * C::OB, &mDO, do_full + os, q0, bh);
+        ++o_issued;
+        for (int m = 0; ok && m < 2; ++m) {
+          const int u = 2 * a + m, s = u % C::QS;
+          if (u >= C::QS) ok = wait_bar(q_empty + s, ((u / C::QS) - 1) & 1, ab, prm.status);
+          if (ok) {
+            mbar_arrive_expect_tx(q_full + s, C::QB);
+            load_tile(smem + C::OFF_Q + s * C::QB, &mQ, q_full + s, q0, 2 * bh + m);
+            ++q_issued;
+          }
+        }
+      }
+      if (__shfl_sync(0xffffffffu, ok ? 1 : 0, 0) == 0) break;
+      if (++t == Tq) {
+        t = 0;
+        ++g;
+      }
+      if (a + 1 < T) fetch(bh0 + g, qstart + t * C::BN);
+    }
+    if (lane == 0) {
+      mbar_wait_bounded(kv_full, 0, prm.status, kDrainNs);
+      for (int u = max(0, q_issued - C::QS); u < q_issued; ++u)
+        mbar_wait_bounded(q_full + (u % C::QS), (u / C::QS) & 1, prm.status, kDrainNs);
+      for (int a = max(0, o_issued - C::OS); a < o_issued; ++a)
+        mbar_wait_bounded(do_full + (a % C::OS), (a / C::OS) & 1, prm.status, kDrainNs);
+    }
+  } else if (warp == kMmaWarp) {
+    constexpr uint32_t id_s = idesc_bf16(128, C::BN, false, false);  // S^T and dP^T
+    constexpr uint32_t id_k = idesc_bf16(128, kD, false, true);      // dK += dS^T Q
+    constexpr uint32_t id_v = idesc_bf16(128, DV, false, true);      // dV += W^T dO
+    auto issue_dp = [&](int a) -> bool {
+      const int os = a % C::OS;
+      if (!warp_wait(do_full + os, (a / C::OS) & 1, ab, prm.status)) return false;
+      tc_fence_after();
+      const uint32_t v_lo = opaque(lo_kmajor(sb + C::OFF_V));
+      const uint32_t do_lo = opaque(lo_kmajor(sb + C::OFF_DO + os * C::OB));
+#pragma unroll
+      for (int k = 0; k < DV / 16; ++k)
+        mma_ss_w(tmem + C::T_DP(a & 1), v_lo + kslice_off(C::BM, k), do_lo + kslice_off(C::BN, k),
+                 id_s, k > 0 ? 1u : 0u);
+      mma_commit_w(dp_full + (a & 1));
+      return true;
+    };
+    auto issue_s = [&](int u) -> bool {
+      const int s = u % C::QS, m = u & 1;
+      if (!warp_wait(q_full + s, (u / C::QS) & 1, ab, prm.status)) return false;
+      tc_fence_after();
+      const uint32_t k_lo = opaque(lo_kmajor(sb + C::OFF_K + m * C::KB));
+      const uint32_t q_lo = opaque(lo_kmajor(sb + C::OFF_Q + s * C::QB));
+#pragma unroll
+      for (int k = 0; k < kD / 16; ++k)
+        mma_ss_w(tmem + C::T_S(m), k_lo + kslice_off(C::BM, k), q_lo + kslice_off(C::BN, k), id_s,
+                 k > 0 ? 1u : 0u);
+      mma_commit_w(s_full + m);
+      return true;
+    };
+    const int U = 2 * T;
+    bool ok = warp_wait(kv_full, 0, ab, prm.status) && issue_dp(0) && issue_s(0);
+    for (int u = 0; ok && u < U; ++u) {
+      const int m = u & 1, a = u >> 1, s = u % C::QS, os = a % C::OS;
+      // the next subtile's scores go over the operands of subtile u - 1, whose
+      // products were issued before; the next tile's dP^T into the buffer of
+      // tile a - 1, read out before those operands were written
+      if (u + 1 < U && !issue_s(u + 1)) { ok = false; break; }
+      if (m == 0 && a + 1 < T && !issue_dp(a + 1)) { ok = false; break; }
+      if (!warp_wait(ds_full + m, a & 1, ab, prm.status)) { ok = false; break; }
+      tc_fence_after();
+      const uint32_t first = a > 0 ? 1u : 0u;
+      const uint32_t t_a = tmem + C::T_S(m);
+      const uint32_t q_mn = opaque(lo_mnmajor(sb + C::OFF_Q + s * C::QB, C::BN * 128));
+#pragma unroll
+      for (int k = 0; k < C::BN / 16; ++k)
+        mma_ts_w(tmem + C::T_DK(m), t_a + 16 * k + 8, q_mn + kstep_off(k), id_k, k > 0 ? 1u : first);
+      mma_commit_w(q_empty + s);
+      if (m == 1) {
+        const uint32_t do_mn = opaque(lo_mnmajor(sb + C::OFF_DO + os * C::OB, C::BN * 128));
+#pragma unroll
+        for (int k = 0; k < C::BN / 16; ++k)
+          mma_ts_w(tmem + C::T_DV, t_a + 16 * k, do_mn + kstep_off(k), id_v, k > 0 ? 1u : first);
+        mma_commit_w(do_empty + os);
+      }
+    }
+    if (ok) mma_commit_w(acc_done);
+    mma_commit_w(drain);
+    mbar_wait_bounded(drain, 0, prm.status, kDrainNs);
+  } else {
+    // ---------------- elementwise warps: thread = key row ------------------
+    constexpr int NC = C::BN / kSlices;  // query columns per thread: 16
+    const int quad = warp & 3, slice = warp >> 2;
+    const int row = 32 * quad + lane;
+    const int j = j0 + row;
+    const uint32_t lane_off = (uint32_t)(32 * quad) << 16;
+    const float sc2 = prm.scale * kLog2e;
+    const f2 sc2_2 = {sc2, sc2};
+    bool ok = true;
+    int t = 0;
+    for (int a = 0; ok && a < T; ++a) {
+      const int os = a % C::OS;
+      const int qa = qstart + t * C::BN + NC * slice;
+      if (++t == Tq) t = 0;
+      const bool need_mask = (qa + NC > N) || (prm.causal && qa < j0 + 32 * quad + 31);
+      const float4* sc4 = reinterpret_cast<const float4*>(scal + os * 5 * C::BN + NC * slice);
+      if (!warp_wait(do_full + os, (a / C::OS) & 1, ab, prm.status)) { ok = false; break; }
+      uint32_t dp[NC];
+      float p1[NC];
+#pragma unroll
+      for (int m = 0; m < 2; ++m) {
+        if (!ok) break;
+        if (!warp_wait(s_full + m, a & 1, ab, prm.status)) { ok = false; break; }
+        if (m == 0 && !warp_wait(dp_full + (a & 1), (a >> 1) & 1, ab, prm.status)) { ok = false; break; }
+        tc_fence_after();
+        const uint32_t ts = tmem + lane_off + C::T_S(m) + NC * slice;
+        uint32_t sr[NC];
+        if (m == 0) tmem_ld16x2(ts, tmem + lane_off + C::T_DP(a & 1) + NC * slice, sr, dp);
+        else tmem_ld16(ts, sr);
+        uint32_t dsw[NC / 2], ww[NC / 2];
+#pragma unroll
+        for (int c4 = 0; c4 < NC / 4; ++c4) {  // 4 query columns per step
+          const float4 L = sc4[m * (C::BN / 4) + c4];
+          const float4 A = sc4[(m == 0 ? 2 : 4) * (C::BN / 4) + c4];  // -D^1, or lam D^2
+          const float4 W = m == 0 ? make_float4(1.f, 1.f, 1.f, 1.f) : sc4[3 * (C::BN / 4) + c4];
+          const f2 nl[2] = {{L.x, L.y}, {L.z, L.w}}, ad[2] = {{A.x, A.y}, {A.z, A.w}};
+          const f2 nw[2] = {{W.x, W.y}, {W.z, W.w}};
+#pragma unroll
+          for (int h = 0; h < 2; ++h) {
+            const int c = 4 * c4 + 2 * h;
+            const f2 x = fma2({__uint_as_float(sr[c]), __uint_as_float(sr[c + 1])}, sc2_2, nl[h]);
+            f2 p = {ex2_approx(x.x), ex2_approx(x.y)};
+            if (need_mask) {
+              const int q = qa + c;
+              p.x = (q < N && (!prm.causal || q >= j)) ? p.x : 0.f;
+              p.y = (q + 1 < N && (!prm.causal || q + 1 >= j)) ? p.y : 0.f;
+            }
+            const f2 gdp = {__uint_as_float(dp[c]), __uint_as_float(dp[c + 1])};
+            f2 ds;
+            if (m == 0) {
+              p1[c] = p.x;
+              p1[c + 1] = p.y;
+              ds = mul2(p, add2(gdp, ad[h]));
+            } else {
+              const f2 wt = fma2(p, nw[h], {p1[c], p1[c + 1]});  // W = P^1 - lam P^2
+              ww[c >> 1] = pack_bf16(wt.x, wt.y);
+              ds = mul2(p, fma2(gdp, nw[h], ad[h]));
+            }
+            dsw[c >> 1] = pack_bf16(ds.x, ds.y);
+          }
+        }
+        if (m == 0) tmem_st8(ts + 8, dsw);
+        else tmem_st8x2(ts, ww, ts + 8, dsw);
+        tc_fence_before();
+        warp_arrive(ds_full + m);
+      }
+    }
+    // ---- epilogue: dK (scaled), 32 features of one map per thread, and dV ----
+    ok = __all_sync(0xffffffffu, ok);
+    if (ok) ok = warp_wait(acc_done, 0, ab, prm.status);
+    tc_fence_after();
+    if (ok) {
+      const int m = slice >> 1, f = 32 * (slice & 1);
+      uint32_t v[32];
+      tmem_ld32(tmem + lane_off + C::T_DK(0) + kD * m + f, v);
+      if (j < N) store32(prm.dk + (((size_t)kvh * 2 + m) * N + j) * kD + f, v, prm.scale);
+      if (DV == 128 || slice < 2) {
+        tmem_ld32(tmem + lane_off + C::T_DV + 32 * slice, v);
+        if (j < N) store32(prm.dv + ((size_t)kvh * N + j) * DV + 32 * slice, v, 1.f);
+      }
+    }
+  }
+  tc_fence_before();
+  __syncthreads();
+  if (warp == kMmaWarp) {
+    tc_fence_after();
+    tmem_dealloc(tmem, C::TMEM_COLS);
+  }
+}
+
+// ---------------------------------------------------------------------------
+// host side
+// ---------------------------------------------------------------------------
+Common common(const DiffProblem& p, const DiffTensors& t, const DiffWorkspace& ws, int units) {
+  Common c{};
+  c.status = ws.status;
+  c.wait_ns = wait_limit_ns();
+  c.N = p.N;
+  c.causal = p.causal;
+  c.H = p.H;
+  c.G = p.G();
+  c.units = units;
+  c.group = cta_group_heads(units, (p.N + 127) / 128, sm_count());
+  c.scale = p.scale;
+  c.lam = t.lam;
+  return c;
+}
+
+// [B, heads, N, width] as tiles of `rows` rows
+bool tiles(CUtensorMap* m, const void* ptr, const DiffProblem& p, int heads, int width, int rows) {
+  Problem q{};
+  q.B = p.B;
+  q.H = heads;
+  q.N = p.N;
+  q.d = width;
+  return make_map(m, ptr, q, rows);
+}
+
+template <typename K, typename P, typename... M>
+cudaError_t run(K kernel, int units, int N, uint32_t smem, LaunchLog& log, const P& prm,
+                const M&... maps) {
+  cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
+  if (e != cudaSuccess) return e;
+  kernel<<<(unsigned)(((N + 127) / 128) * units), kThreads, smem, log.stream>>>(maps..., prm);
+  e = cudaGetLastError();
+  log.mark();
+  return e;
+}
+
+template <int DV>
+cudaError_t forward_dv(const DiffProblem& p, const DiffTensors& t, const DiffWorkspace& ws,
+                       LaunchLog& log) {
+  CUtensorMap mQ, mK, mV;
+  if (!tiles(&mQ, t.q, p, 2 * p.H, kD, 128) || !tiles(&mK, t.k, p, 2 * p.Hk, kD, 128) ||
+      !tiles(&mV, t.v, p, p.Hk, DV, 128))
+    return cudaErrorInvalidValue;
+  FwdParams f;
+  static_cast<Common&>(f) = common(p, t, ws, p.B * p.H);
+  f.o = static_cast<__nv_bfloat16*>(t.o);
+  f.o2 = static_cast<__nv_bfloat16*>(t.o2);
+  f.lse = t.lse;
+  return run(diff_fwd_pass<DV>, f.units, p.N, Fwd<DV>::SMEM, log, f, mQ, mK, mV);
+}
+
+template <int DV>
+cudaError_t backward_dv(const DiffProblem& p, const DiffTensors& t, const DiffWorkspace& ws,
+                        LaunchLog& log) {
+  CUtensorMap mQ, mK, mV, mDO, sQ, sDO;  // 128-row tiles; sQ, sDO: the column pass's 64
+  if (!tiles(&mQ, t.q, p, 2 * p.H, kD, 128) || !tiles(&mK, t.k, p, 2 * p.Hk, kD, 128) ||
+      !tiles(&mV, t.v, p, p.Hk, DV, 128) || !tiles(&mDO, t.dO, p, p.H, DV, 128) ||
+      !tiles(&sQ, t.q, p, 2 * p.H, kD, 64) || !tiles(&sDO, t.dO, p, p.H, DV, 64))
+    return cudaErrorInvalidValue;
+  RowParams r;
+  static_cast<Common&>(r) = common(p, t, ws, p.B * p.H);
+  r.dq = static_cast<__nv_bfloat16*>(t.dq);
+  r.lse = t.lse;
+  r.D = ws.D;
+  r.d2 = ws.d2;
+  cudaError_t e = run(diff_row_pass<DV>, r.units, p.N, Row<DV>::SMEM, log, r, mQ, mK, mV, mDO);
+  if (e != cudaSuccess) return e;
+  ColParams c;
+  static_cast<Common&>(c) = common(p, t, ws, p.B * p.Hk);
+  c.dk = static_cast<__nv_bfloat16*>(t.dk);
+  c.dv = static_cast<__nv_bfloat16*>(t.dv);
+  c.lse = t.lse;
+  c.D = ws.D;
+  return run(diff_col_pass<DV>, c.units, p.N, Col<DV>::SMEM, log, c, mK, mV, sQ, sDO);
+}
+
+}  // namespace
+
+bool diff_tc_supported(const DiffProblem& p) {
+  return p.bf16 && p.d == kD && (p.dv == 64 || p.dv == 128);
+}
+
+cudaError_t diff_tc_forward(const DiffProblem& p, const DiffTensors& t, const DiffWorkspace& ws,
+                            LaunchLog& log) {
+  return p.dv == 128 ? forward_dv<128>(p, t, ws, log) : forward_dv<64>(p, t, ws, log);
+}
+
+cudaError_t diff_tc_backward(const DiffProblem& p, const DiffTensors& t, const DiffWorkspace& ws,
+                             LaunchLog& log) {
+  return p.dv == 128 ? backward_dv<128>(p, t, ws, log) : backward_dv<64>(p, t, ws, log);
+}
+
+}  // namespace fbob

@@ -36,7 +36,8 @@ struct LamArg {
 struct DiffWorkspace {
   int* status = nullptr;
   float* D = nullptr;        // [B, 2H, N]: D^1 and D^2 of each row
-  float* partial = nullptr;  // [B, H]: sums of D^2, for lam's gradient
+  float* d2 = nullptr;       // [B, H, N]: sum_j P^2_ij dP_ij, for lam's gradient
+  float* partial = nullptr;  // [B, H]: its sums
 };
 
 struct DiffTensors {
@@ -52,5 +53,12 @@ struct DiffTensors {
 cudaError_t diff_simt_forward(const DiffProblem& p, const DiffTensors& t, LaunchLog& log);
 cudaError_t diff_simt_backward(const DiffProblem& p, const DiffTensors& t, const DiffWorkspace& ws,
                                LaunchLog& log);
+
+// ---- tensor-core kernels: bf16, d = 64, dv = 64 or 128 ----------------------
+bool diff_tc_supported(const DiffProblem& p);
+cudaError_t diff_tc_forward(const DiffProblem& p, const DiffTensors& t, const DiffWorkspace& ws,
+                            LaunchLog& log);
+cudaError_t diff_tc_backward(const DiffProblem& p, const DiffTensors& t, const DiffWorkspace& ws,
+                             LaunchLog& log);
 
 }  // namespace fbob

@@ -168,6 +168,18 @@ class TestOnGpu:
         with torch.no_grad():
             assert torch.equal(fbob.diff_attention(*leaf, causal=causal, scale=scale), o)
 
+    def test_cuda_core_family_on_the_tensor_core_sizes(self):
+        q, k, v, w, do = inputs(1, 2, 1, 150, 64, 128, BF, ("head", BF), seed=3)
+        vals, errs = oracle(q, k, v, w, do, True, 0.125)
+        old = fbob.force_path(fbob.PATH_SIMT)
+        try:
+            o, o2, lse = fbob.diff_forward(q, k, v, w, True)
+            grads = fbob.diff_backward(q, k, v, w, o, o2, lse, do, True)
+        finally:
+            fbob.force_path(old)
+        check(dict(zip(("o", "o2", "lse", "dq", "dk", "dv", "dlam"), (o, o2, lse, *grads))), vals,
+              errs, ("o", "o2", "lse", "dq", "dk", "dv", "dlam"))
+
     @pytest.mark.parametrize("dtype", [BF, F32])
     def test_peaked_rows(self, dtype):
         """Scores of tens: probabilities near 0 and 1, maxima that move late."""
@@ -374,6 +386,31 @@ class TestOnGpu:
             graph.replay()
             assert all(torch.equal(a, b) for a, b in zip(got, both(*new)))
 
+    @pytest.mark.parametrize("dv", [128, 64])
+    def test_kernels_stop_cleanly_when_their_waits_run_out(self, dv):
+        """A 1 ns wait limit: each call reports the timeout in its workspace's
+        status word, and the next call with the default limit is as before."""
+        from exact_second_order_two_gb300.diff_attention import _shape, _workspace
+
+        q, k, v, w, do = inputs(1, 2, 1, 2048, 64, dv, BF, ("head", BF), seed=14)
+        shp = _shape(q, k, v, w, True, None)
+        fws, bws = (_workspace(op, shp, q.device) for op in (0, 1))
+        o, o2, lse = fbob.diff_forward(q, k, v, w, True, workspace=fws)
+        calls = ((fws, lambda: fbob.diff_forward(q, k, v, w, True, workspace=fws)),
+                 (bws, lambda: fbob.diff_backward(q, k, v, w, o, o2, lse, do, True, workspace=bws)))
+        for ws, call in calls:
+            want = call()
+            assert fbob.status(ws) == 0
+            old = fbob.set_wait_limit(1)
+            try:
+                call()
+                st = fbob.status(ws)
+            finally:
+                fbob.set_wait_limit(old)
+            assert st == 5  # FBOB_ERR_TIMEOUT
+            assert all(torch.equal(a, b) for a, b in zip(call(), want))
+            assert fbob.status(ws) == 0
+
     def test_refusals(self):
         q, k, v, w, do = inputs(1, 2, 2, 8, 64, 64, BF, ("head", BF))
         for bad in (lambda: fbob.diff_attention(q[:, :3], k, v, w),
@@ -457,6 +494,23 @@ def test_c_calls_refuse_bad_pointers_and_workspaces():
         assert lib.fbob_diff_backward(ctypes.byref(s), *args, good, n - 1, None) == 1
     assert lib.fbob_diff_backward(ctypes.byref(s), *[good] * 12, good, n - 1, None) == 3
     assert lib.fbob_diff_workspace_size(2, ctypes.byref(s)) == 0  # no backward-over-backward call
+
+
+def test_kernel_family_choice():
+    lib = B.lib()
+    for op in (0, 1):
+        def path(**kw):
+            return lib.fbob_diff_path(op, ctypes.byref(shape(**kw)))
+        assert path() == fbob.PATH_TCGEN05 and path(dv=64) == fbob.PATH_TCGEN05
+        for kw in (dict(dtype=1), dict(d=128), dict(d=32), dict(dv=96), dict(dv=32)):
+            assert path(**kw) == fbob.PATH_SIMT, kw
+        old = fbob.force_path(fbob.PATH_SIMT)
+        try:
+            assert path() == fbob.PATH_SIMT
+            fbob.force_path(fbob.PATH_TCGEN05)
+            assert path() == fbob.PATH_TCGEN05 and path(dtype=1) == -1
+        finally:
+            fbob.force_path(old)
 
 
 def test_oracle_matches_autograd():
