@@ -34,6 +34,7 @@
 #include <cuda_runtime.h>
 #include <cudaTypedefs.h>
 #include <math.h>
+#include <type_traits>
 
 #include "common.cuh"
 #include "internal.h"
@@ -53,7 +54,8 @@ constexpr int kConsumers = kWarps * 32;
 constexpr int kProducerWarp = kWarps;
 constexpr int kMmaWarp = kWarps + 1;
 constexpr int kThreads = (kWarps + 2) * 32;
-constexpr int kSlices = kWarps / 4;        // column slices per row
+constexpr int kSlices = 2;                 // column slices per row of a map
+constexpr int kRowSlices = 4;
 constexpr float kLn2 = 0.6931471805599453f;
 constexpr uint64_t kDrainNs = 100000000ull;  // limit of the waits after an abort
 constexpr int kD = 64;                     // features of a query or key
@@ -76,6 +78,19 @@ __device__ __forceinline__ float lam_value(const LamArg& l, size_t i) {
 __device__ __forceinline__ float lam_row(const LamArg& l, int bh, int H, int N, int n) {
   return lam_value(l, l.kind == FBOB_LAM_ONE ? 0 : l.kind == FBOB_LAM_HEAD ? (size_t)(bh % H)
                                                                            : (size_t)bh * N + n);
+}
+
+// Bounded, warp-uniform wait (as warp_wait) that first sleeps on the barrier
+// and only then looks at the clock: almost every wait ends in that sleep,
+// and a read of the global timer costs more than most of them last.
+__device__ __forceinline__ bool await(uint64_t* bar, uint32_t parity, Abort* ab, int* status) {
+  bool ok = mbar_try_wait(bar, parity);
+  if (!ok) {
+    const uint64_t limit = ab->limit_ns;
+    ok = mbar_try_wait_sleep(bar, parity, limit < kPollSleepNs ? (uint32_t)limit : kPollSleepNs);
+    if (!ok) ok = wait_bar(bar, parity, ab, status);
+  }
+  return __all_sync(0xffffffffu, ok);
 }
 
 // One arrival for the whole warp: its lanes' earlier writes (shared memory, or
@@ -109,9 +124,9 @@ struct Fwd {
   static constexpr uint32_t QB = BM * kD * 2;      // Q or K subtile
   static constexpr uint32_t VB = BN * DV * 2;
   static constexpr uint32_t OFF_Q = 0, OFF_K = 2 * QB, OFF_V = OFF_K + KS * QB;
-  // [2][slices][128] subtile row maxima; the epilogue's [2][slices][128] sums
+  // [2 buffers][2 maps][slices][128] row maxima; the epilogue's [2][slices][128] sums
   static constexpr uint32_t OFF_RED = OFF_V + VS * VB;
-  static constexpr uint32_t OFF_MISC = OFF_RED + 4 * kSlices * 128 * 4;
+  static constexpr uint32_t OFF_MISC = OFF_RED + 6 * kSlices * 128 * 4;
   static constexpr uint32_t SMEM = OFF_MISC + 512;
   static_assert(SMEM <= 232448, "forward shared memory budget");
   // TMEM columns: two score buffers (map m in buffer m; bf16 P overwrites the
@@ -147,11 +162,11 @@ __global__ void __launch_bounds__(kThreads, 1)
   uint64_t* v_full = k_empty + C::KS;        // [VS]
   uint64_t* v_empty = v_full + C::VS;        // [VS]
   uint64_t* s_full = v_empty + C::VS;        // [2]: scores of map m in TMEM
-  uint64_t* p_full = s_full + 2;             // [2]: bf16 P written, O^m rescaled
-  uint64_t* o_ready = p_full + 2;            // [2]: P V of map m done, one phase per tile
+  uint64_t* p_full = s_full + 2;             // [2][2]: a chunk's bf16 P written, O^m rescaled
+  uint64_t* o_ready = p_full + 4;            // [2]: P V of map m done, one phase per tile
   uint64_t* red_full = o_ready + 2;          // [2][4]: the slices' maxima, per lane quadrant
   uint64_t* drain = red_full + 8;
-  static_assert((1 + 2 * C::KS + 2 * C::VS + 15) * 8 <= 256, "barriers end below the TMEM slot");
+  static_assert((1 + 2 * C::KS + 2 * C::VS + 17) * 8 <= 256, "barriers end below the TMEM slot");
   uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(smem + C::OFF_MISC + 256);
   Abort* ab = reinterpret_cast<Abort*>(smem + C::OFF_MISC + 264);
   float* red = reinterpret_cast<float*>(smem + C::OFF_RED);
@@ -178,7 +193,8 @@ __global__ void __launch_bounds__(kThreads, 1)
     }
     for (int m = 0; m < 2; ++m) {
       mbar_init(s_full + m, 1);
-      mbar_init(p_full + m, kWarps);
+      mbar_init(p_full + 2 * m, kWarps / 2);
+      mbar_init(p_full + 2 * m + 1, kWarps / 2);
       mbar_init(o_ready + m, 1);
     }
     for (int i = 0; i < 8; ++i) mbar_init(red_full + i, kSlices);
@@ -235,28 +251,10 @@ __global__ void __launch_bounds__(kThreads, 1)
   } else if (warp == kMmaWarp) {
     constexpr uint32_t id_s = idesc_bf16(128, C::BN, false, false);  // S = Q K^T
     constexpr uint32_t id_o = idesc_bf16(128, DV, false, true);      // O += P V: B MN-major
-    bool ok = warp_wait(q_full, 0, ab, prm.status);
-    // O^m += P(u) V(t), A = bf16 P from TMEM
-    auto issue_pv = [&](int u) -> bool {
-      const int m = u & 1, t = u >> 1, vs = t % C::VS;
-      if (!warp_wait(p_full + m, t & 1, ab, prm.status)) return false;
-      if (m == 0 && !warp_wait(v_full + vs, (t / C::VS) & 1, ab, prm.status)) return false;
-      tc_fence_after();
-      const uint32_t v_mn = opaque(lo_mnmajor(sb + C::OFF_V + vs * C::VB, C::BN * 128));
-      const uint32_t t_p = tmem + C::T_S(m), t_o = tmem + C::T_O(m);
-#pragma unroll
-      for (int k = 0; k < C::BN / 16; ++k)
-        mma_ts_w(t_o, t_p + C::p_col(k), v_mn + kstep_off(k), id_o, (t > 0 || k > 0) ? 1u : 0u);
-      if (m == 1) mma_commit_w(v_empty + vs);
-      mma_commit_w(o_ready + m);
-      return true;
-    };
-    // S(u) overwrites the buffer of subtile u - 2, whose P V was issued after
-    // every warp had read its scores and written its P
-    const int U = 2 * T;
-    for (int u = 0; ok && u < U; ++u) {
-      const int s = u % C::KS, m = u & 1;
-      if (!warp_wait(k_full + s, (u / C::KS) & 1, ab, prm.status)) { ok = false; break; }
+    bool ok = await(q_full, 0, ab, prm.status);
+    auto issue_s = [&](int t, int m) -> bool {
+      const int u = 2 * t + m, s = u % C::KS;
+      if (!await(k_full + s, (u / C::KS) & 1, ab, prm.status)) return false;
       tc_fence_after();
       const uint32_t q_lo = opaque(lo_kmajor(sb + C::OFF_Q + m * C::QB));
       const uint32_t k_lo = opaque(lo_kmajor(sb + C::OFF_K + s * C::QB));
@@ -266,140 +264,168 @@ __global__ void __launch_bounds__(kThreads, 1)
                  k > 0 ? 1u : 0u);
       mma_commit_w(s_full + m);
       mma_commit_w(k_empty + s);
-      if (u >= 1 && !issue_pv(u - 1)) { ok = false; break; }
+      return true;
+    };
+    ok = ok && issue_s(0, 0) && issue_s(0, 1);
+    for (int t = 0; ok && t < T; ++t) {
+      const int vs = t % C::VS;
+      if (!await(v_full + vs, (t / C::VS) & 1, ab, prm.status)) { ok = false; break; }
+#pragma unroll
+      for (int m = 0; m < 2; ++m) {
+        if (!ok) break;
+        // O^m += P^m V, A = bf16 P from TMEM: the slices' first chunks of 32
+        // keys, then the second ones; then the next tile's scores over P
+        const uint32_t v_mn = opaque(lo_mnmajor(sb + C::OFF_V + vs * C::VB, C::BN * 128));
+#pragma unroll
+        for (int h = 0; h < 2; ++h) {
+          if (!ok) break;
+          if (!await(p_full + 2 * m + h, t & 1, ab, prm.status)) { ok = false; break; }
+          tc_fence_after();
+#pragma unroll
+          for (int x = 0; x < 4; ++x) {
+            const int k = 4 * (x >> 1) + 2 * h + (x & 1);
+            mma_ts_w(tmem + C::T_O(m), tmem + C::T_S(m) + C::p_col(k), v_mn + kstep_off(k), id_o,
+                     (t > 0 || h > 0 || x > 0) ? 1u : 0u);
+          }
+        }
+        if (!ok) break;
+        if (m == 1) mma_commit_w(v_empty + vs);
+        mma_commit_w(o_ready + m);
+        if (t + 1 < T) ok = issue_s(t + 1, m);
+      }
     }
-    if (ok) ok = issue_pv(U - 1);
     // every MMA this thread issued has completed before TMEM is released
     mma_commit_w(drain);
     mbar_wait_bounded(drain, 0, prm.status, kDrainNs);
   } else {
     // ---------------- elementwise warps: thread = query row ----------------
-    constexpr int NC = C::BN / kSlices;  // key columns per thread
-    const int quad = warp & 3, slice = warp >> 2;
+    // warps 0-7 own map 0, warps 8-15 map 1; two column slices of 64 keys each
+    constexpr int NC = C::BN / kSlices;  // 64: two chunks of 32
+    const int quad = warp & 3, slice = (warp >> 2) & 1, m = warp >> 3;
     const int row = 32 * quad + lane;
     const int i = i0 + row;
     const float sc2 = prm.scale * kLog2e;
     const f2 sc2_2 = {sc2, sc2};
     const uint32_t lane_off = (uint32_t)(32 * quad) << 16;
+    const uint32_t ts = tmem + lane_off + C::T_S(m) + NC * slice;
+    uint64_t* red_bar = red_full + 4 * m + quad;
     bool ok = true;
-    // per map: the row's reference maximum (log2 domain), the same in all
-    // slices, and this slice's sum of 2^(S c log2 e - max)
-    float mx[2] = {-INFINITY, -INFINITY}, l[2] = {0.f, 0.f};
-    for (int t = 0; ok && t < T; ++t) {
+    // the row's reference maximum (log2 domain), the same in both slices, and
+    // this slice's sum of 2^(S c log2 e - max)
+    float mx = -INFINITY, l = 0.f;
+    for (int t = 0; t < T; ++t) {
       const int j0 = t * C::BN + NC * slice;
       const bool need_mask = (j0 + NC > N) || (prm.causal && j0 + NC - 1 > i0 + 32 * quad);
+      if (!await(s_full + m, t & 1, ab, prm.status)) { ok = false; break; }
+      tc_fence_after();
+      // scores of both chunks; masked entries become -inf, so they give
+      // 2^-inf = 0 below
+      uint32_t s0[32], s1[32];
+      auto mask = [&](uint32_t (&sr)[32], int j) {
 #pragma unroll
-      for (int m = 0; m < 2; ++m) {
-        if (!ok) break;
-        if (!warp_wait(s_full + m, t & 1, ab, prm.status)) { ok = false; break; }
-        tc_fence_after();
-        const uint32_t ts = tmem + lane_off + C::T_S(m) + NC * slice;
-        uint32_t sr[NC];
-        tmem_ld32(ts, sr);
-        // this slice's maximum (c log2 e > 0 keeps the order); masked entries
-        // become -inf, so they give 2^-inf = 0 below
-        float top = -INFINITY;
-        if (need_mask) {
-#pragma unroll
-          for (int c = 0; c < NC; ++c) {
-            const int j = j0 + c;
-            const float v = (j < N && (!prm.causal || j <= i)) ? __uint_as_float(sr[c]) : -INFINITY;
-            sr[c] = __float_as_uint(v);
-            top = fmaxf(top, v);
-          }
-        } else {
-#pragma unroll
-          for (int c = 0; c < NC; ++c) top = fmaxf(top, __uint_as_float(sr[c]));
-        }
-        // exchanged between the slices of a row; a buffer is rewritten two
-        // subtiles later, after every slice has arrived for the next one and
-        // so has read this one
-        float* rt = red + m * kSlices * 128;
-        rt[slice * 128 + row] = top * sc2;
-        warp_arrive(red_full + 4 * m + quad);
-        uint32_t pw[NC / 2];
-        float sum;
-        auto exps = [&]() {
-          const f2 nm = {-mx[m], -mx[m]};
-          f2 acc = {0.f, 0.f};
-#pragma unroll
-          for (int c = 0; c < NC; c += 2) {
-            const f2 x = fma2({__uint_as_float(sr[c]), __uint_as_float(sr[c + 1])}, sc2_2, nm);
-            const f2 p = {ex2_approx(x.x), ex2_approx(x.y)};
-            acc = add2(acc, p);
-            pw[c >> 1] = pack_bf16(p.x, p.y);
-          }
-          sum = acc.x + acc.y;
-        };
-        // The maximum rarely moves after the first tile, so the probabilities
-        // are computed against the old one while the other slices' maxima
-        // arrive, and again where it did move
-        if (t > 0) exps();
-        if (!warp_wait(red_full + 4 * m + quad, t & 1, ab, prm.status)) { ok = false; break; }
-        float mt = rt[row];
-#pragma unroll
-        for (int s = 1; s < kSlices; ++s) mt = fmaxf(mt, rt[s * 128 + row]);
-        const bool move = mt > mx[m] + C::kRescale;
-        if (t == 0) {
-          mx[m] = mt;  // finite: key 0 is visible to every row
-          exps();
-          l[m] = sum;
-        } else if (__any_sync(0xffffffffu, move)) {
-          // the row's O^m holds the sums of the earlier tiles: rescale this
-          // slice's DV/4 columns once their MMAs are done (rows that did not
-          // move scale by 1)
-          const float alpha = move ? ex2_approx(mx[m] - mt) : 1.f;
-          if (!warp_wait(o_ready + m, (t - 1) & 1, ab, prm.status)) { ok = false; break; }
-          tc_fence_after();
-#pragma unroll
-          for (int c = 0; c < DV / kSlices; c += 16) {
-            uint32_t v[16];
-            const uint32_t ta = tmem + lane_off + C::T_O(m) + (DV / kSlices) * slice + c;
-            tmem_ld16(ta, v);
-#pragma unroll
-            for (int e = 0; e < 16; ++e) v[e] = __float_as_uint(__uint_as_float(v[e]) * alpha);
-            tmem_st16(ta, v);
-          }
-          if (move) mx[m] = mt;
-          exps();
-          l[m] = fmaf(l[m], alpha, sum);
-        } else {
-          l[m] += sum;
-        }
-        // bf16 P over the first 16 of the 32 columns this thread read
-        tmem_st16(ts, pw);
-        tc_fence_before();
-        warp_arrive(p_full + m);
+        for (int c = 0; c < 32; ++c)
+          if (!(j + c < N && (!prm.causal || j + c <= i))) sr[c] = 0xff800000u;
+      };
+      tmem_ld32x2(ts, ts + 32, s0, s1);
+      if (need_mask) {
+        mask(s0, j0);
+        mask(s1, j0 + 32);
       }
+      // this slice's maximum (c log2 e > 0 keeps the order), exchanged with the
+      // other slice; a buffer is rewritten two tiles later, after the other
+      // slice has arrived for the next one and so has read this one
+      float t0 = -INFINITY, t1 = -INFINITY;
+#pragma unroll
+      for (int c = 0; c < 32; ++c) {
+        t0 = fmaxf(t0, __uint_as_float(s0[c]));
+        t1 = fmaxf(t1, __uint_as_float(s1[c]));
+      }
+      const float mine = fmaxf(t0, t1) * sc2;
+      float* rt = red + ((t & 1) * 2 + m) * kSlices * 128;
+      rt[slice * 128 + row] = mine;
+      warp_arrive(red_bar);
+      uint32_t pw[16];
+      float sum;
+      auto exps = [&](const uint32_t (&sr)[32]) {
+        const f2 nm = {-mx, -mx};
+        f2 acc = {0.f, 0.f};
+#pragma unroll
+        for (int c = 0; c < 32; c += 2) {
+          const f2 x = fma2({__uint_as_float(sr[c]), __uint_as_float(sr[c + 1])}, sc2_2, nm);
+          const f2 p = {ex2_approx(x.x), ex2_approx(x.y)};
+          acc = add2(acc, p);
+          pw[c >> 1] = pack_bf16(p.x, p.y);
+        }
+        sum = acc.x + acc.y;
+      };
+      // The maximum rarely moves after the first tile, so the first chunk's
+      // probabilities are computed against the old one while the other slice's
+      // maximum arrives, and again where it did move
+      if (t > 0) exps(s0);
+      if (!await(red_bar, t & 1, ab, prm.status)) { ok = false; break; }
+      const float mt = fmaxf(mine, rt[(slice ^ 1) * 128 + row]);
+      const bool move = mt > mx + C::kRescale;
+      if (t == 0) {
+        mx = mt;  // finite: key 0 is visible to every row
+        exps(s0);
+      } else if (__any_sync(0xffffffffu, move)) {
+        // the row's O^m holds the sums of the earlier tiles: rescale this
+        // slice's DV/2 columns once their MMAs are done (rows that did not
+        // move scale by 1)
+        const float alpha = move ? ex2_approx(mx - mt) : 1.f;
+        if (!await(o_ready + m, (t - 1) & 1, ab, prm.status)) { ok = false; break; }
+        tc_fence_after();
+#pragma unroll
+        for (int c = 0; c < DV / kSlices; c += 16) {
+          uint32_t v[16];
+          const uint32_t ta = tmem + lane_off + C::T_O(m) + (DV / kSlices) * slice + c;
+          tmem_ld16(ta, v);
+#pragma unroll
+          for (int e = 0; e < 16; ++e) v[e] = __float_as_uint(__uint_as_float(v[e]) * alpha);
+          tmem_st16(ta, v);
+        }
+        if (move) mx = mt;
+        l *= alpha;
+        tmem_ld32(ts, s0);
+        if (need_mask) mask(s0, j0);
+        exps(s0);
+      }
+      // bf16 P over the first 16 of each chunk's 32 columns; the product with
+      // the first chunks starts while the second ones are computed
+      l += sum;
+      tmem_st16(ts, pw);
+      tc_fence_before();
+      warp_arrive(p_full + 2 * m);
+      exps(s1);
+      l += sum;
+      tmem_st16(ts + 32, pw);
+      tc_fence_before();
+      warp_arrive(p_full + 2 * m + 1);
     }
     // ---- epilogue: O = O^1 / l^1 - lam O^2 / l^2, and LSE (natural log) ----
     // every elementwise thread gets to this barrier, also after a failed wait
-    float* part = red + 2 * kSlices * 128;
-#pragma unroll
-    for (int m = 0; m < 2; ++m) part[(m * kSlices + slice) * 128 + row] = l[m];
+    float* part = red + 4 * kSlices * 128;
+    part[(m * kSlices + slice) * 128 + row] = l;
     named_sync<kConsumers>(1);
     float L[2];
 #pragma unroll
-    for (int m = 0; m < 2; ++m) {
-      L[m] = 0.f;
-#pragma unroll
-      for (int s = 0; s < kSlices; ++s) L[m] += part[(m * kSlices + s) * 128 + row];
-    }
+    for (int e = 0; e < 2; ++e)
+      L[e] = part[e * kSlices * 128 + row] + part[(e * kSlices + 1) * 128 + row];
     ok = __all_sync(0xffffffffu, ok);
-    if (ok) ok = warp_wait(o_ready + 0, (T - 1) & 1, ab, prm.status);
-    if (ok) ok = warp_wait(o_ready + 1, (T - 1) & 1, ab, prm.status);
+    if (ok) ok = await(o_ready + 0, (T - 1) & 1, ab, prm.status);
+    if (ok) ok = await(o_ready + 1, (T - 1) & 1, ab, prm.status);
     tc_fence_after();
     if (ok) {
-      constexpr int PART = DV / kSlices;
+      constexpr int PART = DV / 4;  // features per thread
+      const int f0 = PART * (warp >> 2);
       const bool in = i < N;
       const float inv1 = 1.f / L[0], inv2 = 1.f / L[1];
       const float w = in ? lam_row(prm.lam, bh, prm.H, N, i) : 0.f;
-      const size_t at = ((size_t)bh * N + (in ? i : 0)) * DV + PART * slice;
+      const size_t at = ((size_t)bh * N + (in ? i : 0)) * DV + f0;
 #pragma unroll
       for (int c = 0; c < PART; c += 16) {
         uint32_t a[16], b[16];
-        tmem_ld16x2(tmem + lane_off + C::T_O(0) + PART * slice + c,
-                    tmem + lane_off + C::T_O(1) + PART * slice + c, a, b);
+        tmem_ld16x2(tmem + lane_off + C::T_O(0) + f0 + c, tmem + lane_off + C::T_O(1) + f0 + c, a, b);
         uint32_t wo[8], w2[8];
 #pragma unroll
         for (int e = 0; e < 8; ++e) {
@@ -419,10 +445,8 @@ __global__ void __launch_bounds__(kThreads, 1)
           }
         }
       }
-      if (in && slice < 2) {
-        const float ms = slice == 0 ? mx[0] : mx[1], ls = slice == 0 ? L[0] : L[1];
-        prm.lse[((size_t)bh * 2 + slice) * N + i] = (ms + log2f(ls)) * kLn2;
-      }
+      if (in && slice == 0)
+        prm.lse[((size_t)bh * 2 + m) * N + i] = (mx + log2f(m == 0 ? L[0] : L[1])) * kLn2;
     }
   }
   tc_fence_before();
@@ -445,7 +469,7 @@ struct Row {
   static constexpr uint32_t OFF_Q = 0, OFF_DO = 2 * QB, OFF_K = OFF_DO + VB;
   static constexpr uint32_t OFF_V = OFF_K + KS * QB;
   static constexpr uint32_t OFF_RED = OFF_V + VS * VB;  // [slices][128]
-  static constexpr uint32_t OFF_MISC = OFF_RED + kSlices * 128 * 4;
+  static constexpr uint32_t OFF_MISC = OFF_RED + kRowSlices * 128 * 4;
   static constexpr uint32_t SMEM = OFF_MISC + 512;
   static_assert(SMEM <= 232448, "row pass shared memory budget");
   // TMEM columns: two score buffers (bf16 dS over the first 16 of each
@@ -567,7 +591,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     constexpr uint32_t id_q = idesc_bf16(128, kD, false, true);      // dQ += dS K: B MN-major
     auto issue_dp = [&](int t) -> bool {
       const int vs = t % C::VS;
-      if (!warp_wait(v_full + vs, (t / C::VS) & 1, ab, prm.status)) return false;
+      if (!await(v_full + vs, (t / C::VS) & 1, ab, prm.status)) return false;
       tc_fence_after();
       const uint32_t do_lo = opaque(lo_kmajor(sb + C::OFF_DO));
       const uint32_t v_lo = opaque(lo_kmajor(sb + C::OFF_V + vs * C::VB));
@@ -581,7 +605,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     };
     auto issue_s = [&](int u) -> bool {
       const int s = u % C::KS, m = u & 1;
-      if (!warp_wait(k_full + s, (u / C::KS) & 1, ab, prm.status)) return false;
+      if (!await(k_full + s, (u / C::KS) & 1, ab, prm.status)) return false;
       tc_fence_after();
       const uint32_t q_lo = opaque(lo_kmajor(sb + C::OFF_Q + m * C::QB));
       const uint32_t k_lo = opaque(lo_kmajor(sb + C::OFF_K + s * C::QB));
@@ -593,18 +617,18 @@ __global__ void __launch_bounds__(kThreads, 1)
       return true;
     };
     const int U = 2 * T;
-    bool ok = warp_wait(q_full, 0, ab, prm.status) && issue_dp(0) && issue_s(0);
+    bool ok = await(q_full, 0, ab, prm.status) && issue_dp(0) && issue_s(0);
     for (int u = 0; ok && u < U; ++u) {
       const int m = u & 1, t = u >> 1, s = u % C::KS;
       // the next subtile's scores go over the dS of subtile u - 1, whose dQ
       // product was issued before; the next tile's dP once this one is read
       if (u + 1 < U && !issue_s(u + 1)) { ok = false; break; }
       if (m == 0 && t + 1 < T) {
-        if (!warp_wait(dp_read, t & 1, ab, prm.status)) { ok = false; break; }
+        if (!await(dp_read, t & 1, ab, prm.status)) { ok = false; break; }
         tc_fence_after();
         if (!issue_dp(t + 1)) { ok = false; break; }
       }
-      if (!warp_wait(ds_full + m, t & 1, ab, prm.status)) { ok = false; break; }
+      if (!await(ds_full + m, t & 1, ab, prm.status)) { ok = false; break; }
       tc_fence_after();
       const uint32_t k_mn = opaque(lo_mnmajor(sb + C::OFF_K + s * C::QB, C::BN * 128));
 #pragma unroll
@@ -618,7 +642,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     mbar_wait_bounded(drain, 0, prm.status, kDrainNs);
   } else {
     // ---------------- elementwise warps: thread = query row ----------------
-    constexpr int NC = C::BN / kSlices;
+    constexpr int NC = C::BN / kRowSlices;
     const int quad = warp & 3, slice = warp >> 2;
     const int row = 32 * quad + lane;
     const int i = i0 + row;
@@ -642,8 +666,8 @@ __global__ void __launch_bounds__(kThreads, 1)
 #pragma unroll
       for (int m = 0; m < 2; ++m) {
         if (!ok) break;
-        if (!warp_wait(s_full + m, t & 1, ab, prm.status)) { ok = false; break; }
-        if (m == 0 && !warp_wait(dp_full, t & 1, ab, prm.status)) { ok = false; break; }
+        if (!await(s_full + m, t & 1, ab, prm.status)) { ok = false; break; }
+        if (m == 0 && !await(dp_full, t & 1, ab, prm.status)) { ok = false; break; }
         tc_fence_after();
         const uint32_t ts = tmem + lane_off + C::T_S(m) + NC * slice;
         uint32_t sr[NC];
@@ -656,20 +680,24 @@ __global__ void __launch_bounds__(kThreads, 1)
         }
         const f2 nl2 = {nl[m], nl[m]}, mul2_ = {mul[m], mul[m]}, add2_ = {add[m], add[m]};
         uint32_t dsw[NC / 2];
+        auto body = [&](auto masked) {
 #pragma unroll
-        for (int c = 0; c < NC; c += 2) {
-          const f2 x = fma2({__uint_as_float(sr[c]), __uint_as_float(sr[c + 1])}, sc2_2, nl2);
-          f2 p = {ex2_approx(x.x), ex2_approx(x.y)};
-          if (need_mask) {
-            const int j = j0 + c;
-            p.x = (j < N && (!prm.causal || j <= i)) ? p.x : 0.f;
-            p.y = (j + 1 < N && (!prm.causal || j + 1 <= i)) ? p.y : 0.f;
+          for (int c = 0; c < NC; c += 2) {
+            const f2 x = fma2({__uint_as_float(sr[c]), __uint_as_float(sr[c + 1])}, sc2_2, nl2);
+            f2 p = {ex2_approx(x.x), ex2_approx(x.y)};
+            if (decltype(masked)::value) {
+              const int j = j0 + c;
+              p.x = (j < N && (!prm.causal || j <= i)) ? p.x : 0.f;
+              p.y = (j + 1 < N && (!prm.causal || j + 1 <= i)) ? p.y : 0.f;
+            }
+            const f2 g = {__uint_as_float(dp[c]), __uint_as_float(dp[c + 1])};
+            if (m == 1) d2 = fma2(p, g, d2);
+            const f2 ds = mul2(p, fma2(g, mul2_, add2_));
+            dsw[c >> 1] = pack_bf16(ds.x, ds.y);
           }
-          const f2 g = {__uint_as_float(dp[c]), __uint_as_float(dp[c + 1])};
-          if (m == 1) d2 = fma2(p, g, d2);
-          const f2 ds = mul2(p, fma2(g, mul2_, add2_));
-          dsw[c >> 1] = pack_bf16(ds.x, ds.y);
-        }
+        };
+        if (need_mask) body(std::true_type{});
+        else body(std::false_type{});
         tmem_st16(ts, dsw);
         tc_fence_before();
         warp_arrive(ds_full + m);
@@ -679,7 +707,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     red[slice * 128 + row] = d2.x + d2.y;
     named_sync<kConsumers>(1);
     ok = __all_sync(0xffffffffu, ok);
-    if (ok) ok = warp_wait(acc_done, 0, ab, prm.status);
+    if (ok) ok = await(acc_done, 0, ab, prm.status);
     tc_fence_after();
     if (ok) {
       const int m = slice >> 1, f = 32 * (slice & 1);
@@ -690,7 +718,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         if (slice == 0) {
           float s = 0.f;
 #pragma unroll
-          for (int u = 0; u < kSlices; ++u) s += red[u * 128 + row];
+          for (int u = 0; u < kRowSlices; ++u) s += red[u * 128 + row];
           prm.d2[(size_t)bh * N + i] = s;
         }
       }
@@ -878,7 +906,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     constexpr uint32_t id_v = idesc_bf16(128, DV, false, true);      // dV += W^T dO
     auto issue_dp = [&](int a) -> bool {
       const int os = a % C::OS;
-      if (!warp_wait(do_full + os, (a / C::OS) & 1, ab, prm.status)) return false;
+      if (!await(do_full + os, (a / C::OS) & 1, ab, prm.status)) return false;
       tc_fence_after();
       const uint32_t v_lo = opaque(lo_kmajor(sb + C::OFF_V));
       const uint32_t do_lo = opaque(lo_kmajor(sb + C::OFF_DO + os * C::OB));
@@ -891,7 +919,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     };
     auto issue_s = [&](int u) -> bool {
       const int s = u % C::QS, m = u & 1;
-      if (!warp_wait(q_full + s, (u / C::QS) & 1, ab, prm.status)) return false;
+      if (!await(q_full + s, (u / C::QS) & 1, ab, prm.status)) return false;
       tc_fence_after();
       const uint32_t k_lo = opaque(lo_kmajor(sb + C::OFF_K + m * C::KB));
       const uint32_t q_lo = opaque(lo_kmajor(sb + C::OFF_Q + s * C::QB));
@@ -903,7 +931,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       return true;
     };
     const int U = 2 * T;
-    bool ok = warp_wait(kv_full, 0, ab, prm.status) && issue_dp(0) && issue_s(0);
+    bool ok = await(kv_full, 0, ab, prm.status) && issue_dp(0) && issue_s(0);
     for (int u = 0; ok && u < U; ++u) {
       const int m = u & 1, a = u >> 1, s = u % C::QS, os = a % C::OS;
       // the next subtile's scores go over the operands of subtile u - 1, whose
@@ -911,7 +939,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       // tile a - 1, read out before those operands were written
       if (u + 1 < U && !issue_s(u + 1)) { ok = false; break; }
       if (m == 0 && a + 1 < T && !issue_dp(a + 1)) { ok = false; break; }
-      if (!warp_wait(ds_full + m, a & 1, ab, prm.status)) { ok = false; break; }
+      if (!await(ds_full + m, a & 1, ab, prm.status)) { ok = false; break; }
       tc_fence_after();
       const uint32_t first = a > 0 ? 1u : 0u;
       const uint32_t t_a = tmem + C::T_S(m);
@@ -933,7 +961,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     mbar_wait_bounded(drain, 0, prm.status, kDrainNs);
   } else {
     // ---------------- elementwise warps: thread = key row ------------------
-    constexpr int NC = C::BN / kSlices;  // query columns per thread: 16
+    constexpr int NC = C::BN / kRowSlices;  // query columns per thread: 16
     const int quad = warp & 3, slice = warp >> 2;
     const int row = 32 * quad + lane;
     const int j = j0 + row;
@@ -948,51 +976,55 @@ __global__ void __launch_bounds__(kThreads, 1)
       if (++t == Tq) t = 0;
       const bool need_mask = (qa + NC > N) || (prm.causal && qa < j0 + 32 * quad + 31);
       const float4* sc4 = reinterpret_cast<const float4*>(scal + os * 5 * C::BN + NC * slice);
-      if (!warp_wait(do_full + os, (a / C::OS) & 1, ab, prm.status)) { ok = false; break; }
+      if (!await(do_full + os, (a / C::OS) & 1, ab, prm.status)) { ok = false; break; }
       uint32_t dp[NC];
       float p1[NC];
 #pragma unroll
       for (int m = 0; m < 2; ++m) {
         if (!ok) break;
-        if (!warp_wait(s_full + m, a & 1, ab, prm.status)) { ok = false; break; }
-        if (m == 0 && !warp_wait(dp_full + (a & 1), (a >> 1) & 1, ab, prm.status)) { ok = false; break; }
+        if (!await(s_full + m, a & 1, ab, prm.status)) { ok = false; break; }
+        if (m == 0 && !await(dp_full + (a & 1), (a >> 1) & 1, ab, prm.status)) { ok = false; break; }
         tc_fence_after();
         const uint32_t ts = tmem + lane_off + C::T_S(m) + NC * slice;
         uint32_t sr[NC];
         if (m == 0) tmem_ld16x2(ts, tmem + lane_off + C::T_DP(a & 1) + NC * slice, sr, dp);
         else tmem_ld16(ts, sr);
         uint32_t dsw[NC / 2], ww[NC / 2];
+        auto body = [&](auto masked) {
 #pragma unroll
-        for (int c4 = 0; c4 < NC / 4; ++c4) {  // 4 query columns per step
-          const float4 L = sc4[m * (C::BN / 4) + c4];
-          const float4 A = sc4[(m == 0 ? 2 : 4) * (C::BN / 4) + c4];  // -D^1, or lam D^2
-          const float4 W = m == 0 ? make_float4(1.f, 1.f, 1.f, 1.f) : sc4[3 * (C::BN / 4) + c4];
-          const f2 nl[2] = {{L.x, L.y}, {L.z, L.w}}, ad[2] = {{A.x, A.y}, {A.z, A.w}};
-          const f2 nw[2] = {{W.x, W.y}, {W.z, W.w}};
+          for (int c4 = 0; c4 < NC / 4; ++c4) {  // 4 query columns per step
+            const float4 L = sc4[m * (C::BN / 4) + c4];
+            const float4 A = sc4[(m == 0 ? 2 : 4) * (C::BN / 4) + c4];  // -D^1, or lam D^2
+            const float4 W = m == 0 ? make_float4(1.f, 1.f, 1.f, 1.f) : sc4[3 * (C::BN / 4) + c4];
+            const f2 nl[2] = {{L.x, L.y}, {L.z, L.w}}, ad[2] = {{A.x, A.y}, {A.z, A.w}};
+            const f2 nw[2] = {{W.x, W.y}, {W.z, W.w}};
 #pragma unroll
-          for (int h = 0; h < 2; ++h) {
-            const int c = 4 * c4 + 2 * h;
-            const f2 x = fma2({__uint_as_float(sr[c]), __uint_as_float(sr[c + 1])}, sc2_2, nl[h]);
-            f2 p = {ex2_approx(x.x), ex2_approx(x.y)};
-            if (need_mask) {
-              const int q = qa + c;
-              p.x = (q < N && (!prm.causal || q >= j)) ? p.x : 0.f;
-              p.y = (q + 1 < N && (!prm.causal || q + 1 >= j)) ? p.y : 0.f;
+            for (int h = 0; h < 2; ++h) {
+              const int c = 4 * c4 + 2 * h;
+              const f2 x = fma2({__uint_as_float(sr[c]), __uint_as_float(sr[c + 1])}, sc2_2, nl[h]);
+              f2 p = {ex2_approx(x.x), ex2_approx(x.y)};
+              if (decltype(masked)::value) {
+                const int q = qa + c;
+                p.x = (q < N && (!prm.causal || q >= j)) ? p.x : 0.f;
+                p.y = (q + 1 < N && (!prm.causal || q + 1 >= j)) ? p.y : 0.f;
+              }
+              const f2 gdp = {__uint_as_float(dp[c]), __uint_as_float(dp[c + 1])};
+              f2 ds;
+              if (m == 0) {
+                p1[c] = p.x;
+                p1[c + 1] = p.y;
+                ds = mul2(p, add2(gdp, ad[h]));
+              } else {
+                const f2 wt = fma2(p, nw[h], {p1[c], p1[c + 1]});  // W = P^1 - lam P^2
+                ww[c >> 1] = pack_bf16(wt.x, wt.y);
+                ds = mul2(p, fma2(gdp, nw[h], ad[h]));
+              }
+              dsw[c >> 1] = pack_bf16(ds.x, ds.y);
             }
-            const f2 gdp = {__uint_as_float(dp[c]), __uint_as_float(dp[c + 1])};
-            f2 ds;
-            if (m == 0) {
-              p1[c] = p.x;
-              p1[c + 1] = p.y;
-              ds = mul2(p, add2(gdp, ad[h]));
-            } else {
-              const f2 wt = fma2(p, nw[h], {p1[c], p1[c + 1]});  // W = P^1 - lam P^2
-              ww[c >> 1] = pack_bf16(wt.x, wt.y);
-              ds = mul2(p, fma2(gdp, nw[h], ad[h]));
-            }
-            dsw[c >> 1] = pack_bf16(ds.x, ds.y);
           }
-        }
+        };
+        if (need_mask) body(std::true_type{});
+        else body(std::false_type{});
         if (m == 0) tmem_st8(ts + 8, dsw);
         else tmem_st8x2(ts, ww, ts + 8, dsw);
         tc_fence_before();
@@ -1001,7 +1033,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     }
     // ---- epilogue: dK (scaled), 32 features of one map per thread, and dV ----
     ok = __all_sync(0xffffffffu, ok);
-    if (ok) ok = warp_wait(acc_done, 0, ab, prm.status);
+    if (ok) ok = await(acc_done, 0, ab, prm.status);
     tc_fence_after();
     if (ok) {
       const int m = slice >> 1, f = 32 * (slice & 1);
