@@ -54,8 +54,11 @@ constexpr int kConsumers = kWarps * 32;
 constexpr int kProducerWarp = kWarps;
 constexpr int kMmaWarp = kWarps + 1;
 constexpr int kThreads = (kWarps + 2) * 32;
-constexpr int kSlices = 2;                 // column slices per row of a map
-constexpr int kRowSlices = 4;
+constexpr int kRowSlices = kWarps / 4;     // column slices per row
+// Forward: 4 softmax warps per map, one thread per row of 128 scores (no
+// exchange between threads), a producer and an MMA warp; 200 registers each.
+constexpr int kSoftmax = 8 * 32;
+constexpr int kFwdProducer = 8, kFwdMma = 9, kFwdThreads = 10 * 32;
 constexpr float kLn2 = 0.6931471805599453f;
 constexpr uint64_t kDrainNs = 100000000ull;  // limit of the waits after an abort
 constexpr int kD = 64;                     // features of a query or key
@@ -93,6 +96,12 @@ __device__ __forceinline__ bool await(uint64_t* bar, uint32_t parity, Abort* ab,
   return __all_sync(0xffffffffu, ok);
 }
 
+__device__ __forceinline__ float max3(float a, float b, float c) {
+  float d;
+  asm("max.f32 %0, %1, %2, %3;" : "=f"(d) : "f"(a), "f"(b), "f"(c));
+  return d;
+}
+
 // One arrival for the whole warp: its lanes' earlier writes (shared memory, or
 // TMEM behind tc_fence_before) are ordered before it.
 __device__ __forceinline__ void warp_arrive(uint64_t* bar) {
@@ -124,9 +133,8 @@ struct Fwd {
   static constexpr uint32_t QB = BM * kD * 2;      // Q or K subtile
   static constexpr uint32_t VB = BN * DV * 2;
   static constexpr uint32_t OFF_Q = 0, OFF_K = 2 * QB, OFF_V = OFF_K + KS * QB;
-  // [2 buffers][2 maps][slices][128] row maxima; the epilogue's [2][slices][128] sums
-  static constexpr uint32_t OFF_RED = OFF_V + VS * VB;
-  static constexpr uint32_t OFF_MISC = OFF_RED + 6 * kSlices * 128 * 4;
+  static constexpr uint32_t OFF_RED = OFF_V + VS * VB;  // [2][128] row sums
+  static constexpr uint32_t OFF_MISC = OFF_RED + 2 * 128 * 4;
   static constexpr uint32_t SMEM = OFF_MISC + 512;
   static_assert(SMEM <= 232448, "forward shared memory budget");
   // TMEM columns: two score buffers (map m in buffer m; bf16 P overwrites the
@@ -146,7 +154,7 @@ struct FwdParams : Common {
 };
 
 template <int DV>
-__global__ void __launch_bounds__(kThreads, 1)
+__global__ void __launch_bounds__(kFwdThreads, 1)
     diff_fwd_pass(const __grid_constant__ CUtensorMap mQ, const __grid_constant__ CUtensorMap mK,
                   const __grid_constant__ CUtensorMap mV, FwdParams prm) {
   using C = Fwd<DV>;
@@ -162,11 +170,10 @@ __global__ void __launch_bounds__(kThreads, 1)
   uint64_t* v_full = k_empty + C::KS;        // [VS]
   uint64_t* v_empty = v_full + C::VS;        // [VS]
   uint64_t* s_full = v_empty + C::VS;        // [2]: scores of map m in TMEM
-  uint64_t* p_full = s_full + 2;             // [2][2]: a chunk's bf16 P written, O^m rescaled
+  uint64_t* p_full = s_full + 2;             // [2][2]: half a tile's bf16 P written, O^m rescaled
   uint64_t* o_ready = p_full + 4;            // [2]: P V of map m done, one phase per tile
-  uint64_t* red_full = o_ready + 2;          // [2][4]: the slices' maxima, per lane quadrant
-  uint64_t* drain = red_full + 8;
-  static_assert((1 + 2 * C::KS + 2 * C::VS + 17) * 8 <= 256, "barriers end below the TMEM slot");
+  uint64_t* drain = o_ready + 2;
+  static_assert((1 + 2 * C::KS + 2 * C::VS + 9) * 8 <= 256, "barriers end below the TMEM slot");
   uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(smem + C::OFF_MISC + 256);
   Abort* ab = reinterpret_cast<Abort*>(smem + C::OFF_MISC + 264);
   float* red = reinterpret_cast<float*>(smem + C::OFF_RED);
@@ -193,17 +200,16 @@ __global__ void __launch_bounds__(kThreads, 1)
     }
     for (int m = 0; m < 2; ++m) {
       mbar_init(s_full + m, 1);
-      mbar_init(p_full + 2 * m, kWarps / 2);
-      mbar_init(p_full + 2 * m + 1, kWarps / 2);
+      mbar_init(p_full + 2 * m, 4);
+      mbar_init(p_full + 2 * m + 1, 4);
       mbar_init(o_ready + m, 1);
     }
-    for (int i = 0; i < 8; ++i) mbar_init(red_full + i, kSlices);
     mbar_init(drain, 1);
     ab->flag = 0;
     ab->limit_ns = prm.wait_ns;
     fence_mbar_init();
   }
-  if (warp == kMmaWarp) {
+  if (warp == kFwdMma) {
     tmem_alloc(tmem_slot, C::TMEM_COLS);
     tmem_relinquish();
   }
@@ -212,7 +218,7 @@ __global__ void __launch_bounds__(kThreads, 1)
   tc_fence_after();
   const uint32_t tmem = *tmem_slot;
 
-  if (warp == kProducerWarp) {
+  if (warp == kFwdProducer) {
     if (lane == 0) {
       mbar_arrive_expect_tx(q_full, 2 * C::QB);
       load_tile(smem + C::OFF_Q, &mQ, q_full, i0, 2 * bh);
@@ -248,7 +254,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       for (int t = max(0, v_issued - C::VS); t < v_issued; ++t)
         mbar_wait_bounded(v_full + (t % C::VS), (t / C::VS) & 1, prm.status, kDrainNs);
     }
-  } else if (warp == kMmaWarp) {
+  } else if (warp == kFwdMma) {
     constexpr uint32_t id_s = idesc_bf16(128, C::BN, false, false);  // S = Q K^T
     constexpr uint32_t id_o = idesc_bf16(128, DV, false, true);      // O += P V: B MN-major
     bool ok = await(q_full, 0, ab, prm.status);
@@ -273,8 +279,8 @@ __global__ void __launch_bounds__(kThreads, 1)
 #pragma unroll
       for (int m = 0; m < 2; ++m) {
         if (!ok) break;
-        // O^m += P^m V, A = bf16 P from TMEM: the slices' first chunks of 32
-        // keys, then the second ones; then the next tile's scores over P
+        // O^m += P^m V, A = bf16 P from TMEM, in two halves of 64 keys; then
+        // the next tile's scores over P
         const uint32_t v_mn = opaque(lo_mnmajor(sb + C::OFF_V + vs * C::VB, C::BN * 128));
 #pragma unroll
         for (int h = 0; h < 2; ++h) {
@@ -282,11 +288,9 @@ __global__ void __launch_bounds__(kThreads, 1)
           if (!await(p_full + 2 * m + h, t & 1, ab, prm.status)) { ok = false; break; }
           tc_fence_after();
 #pragma unroll
-          for (int x = 0; x < 4; ++x) {
-            const int k = 4 * (x >> 1) + 2 * h + (x & 1);
+          for (int k = 4 * h; k < 4 * h + 4; ++k)
             mma_ts_w(tmem + C::T_O(m), tmem + C::T_S(m) + C::p_col(k), v_mn + kstep_off(k), id_o,
-                     (t > 0 || h > 0 || x > 0) ? 1u : 0u);
-          }
+                     (t > 0 || k > 0) ? 1u : 0u);
         }
         if (!ok) break;
         if (m == 1) mma_commit_w(v_empty + vs);
@@ -298,87 +302,56 @@ __global__ void __launch_bounds__(kThreads, 1)
     mma_commit_w(drain);
     mbar_wait_bounded(drain, 0, prm.status, kDrainNs);
   } else {
-    // ---------------- elementwise warps: thread = query row ----------------
-    // warps 0-7 own map 0, warps 8-15 map 1; two column slices of 64 keys each
-    constexpr int NC = C::BN / kSlices;  // 64: two chunks of 32
-    const int quad = warp & 3, slice = (warp >> 2) & 1, m = warp >> 3;
+    // ---------------- softmax warps: thread = query row of one map ----------
+    const int quad = warp & 3, m = warp >> 2;
     const int row = 32 * quad + lane;
     const int i = i0 + row;
     const float sc2 = prm.scale * kLog2e;
     const f2 sc2_2 = {sc2, sc2};
     const uint32_t lane_off = (uint32_t)(32 * quad) << 16;
-    const uint32_t ts = tmem + lane_off + C::T_S(m) + NC * slice;
-    uint64_t* red_bar = red_full + 4 * m + quad;
+    const uint32_t ts = tmem + lane_off + C::T_S(m);
     bool ok = true;
-    // the row's reference maximum (log2 domain), the same in both slices, and
-    // this slice's sum of 2^(S c log2 e - max)
+    // the row's reference maximum (log2 domain) and sum of 2^(S c log2 e - max)
     float mx = -INFINITY, l = 0.f;
     for (int t = 0; t < T; ++t) {
-      const int j0 = t * C::BN + NC * slice;
-      const bool need_mask = (j0 + NC > N) || (prm.causal && j0 + NC - 1 > i0 + 32 * quad);
+      const int j0 = t * C::BN;
       if (!await(s_full + m, t & 1, ab, prm.status)) { ok = false; break; }
       tc_fence_after();
-      // scores of both chunks; masked entries become -inf, so they give
-      // 2^-inf = 0 below
-      uint32_t s0[32], s1[32];
-      auto mask = [&](uint32_t (&sr)[32], int j) {
+      uint32_t s[4][32];
+      tmem_ld32x4(ts, ts + 32, ts + 64, ts + 96, s[0], s[1], s[2], s[3]);
+      // masked entries become -inf, so they give 2^-inf = 0 below
+      if (j0 + C::BN > N || (prm.causal && j0 + C::BN - 1 > i0 + 32 * quad)) {
+        const int end = prm.causal ? min(N, i + 1) : N;  // keys visible to this row
 #pragma unroll
-        for (int c = 0; c < 32; ++c)
-          if (!(j + c < N && (!prm.causal || j + c <= i))) sr[c] = 0xff800000u;
-      };
-      tmem_ld32x2(ts, ts + 32, s0, s1);
-      if (need_mask) {
-        mask(s0, j0);
-        mask(s1, j0 + 32);
+        for (int c = 0; c < 4; ++c)
+#pragma unroll
+          for (int e = 0; e < 32; ++e)
+            if (j0 + 32 * c + e >= end) s[c][e] = 0xff800000u;
       }
-      // this slice's maximum (c log2 e > 0 keeps the order), exchanged with the
-      // other slice; a buffer is rewritten two tiles later, after the other
-      // slice has arrived for the next one and so has read this one
-      float t0 = -INFINITY, t1 = -INFINITY;
+      // the row's maximum over the tile (c log2 e > 0 keeps the order)
+      float top[4];
 #pragma unroll
-      for (int c = 0; c < 32; ++c) {
-        t0 = fmaxf(t0, __uint_as_float(s0[c]));
-        t1 = fmaxf(t1, __uint_as_float(s1[c]));
+      for (int c = 0; c < 4; ++c) {
+        top[c] = __uint_as_float(s[c][0]);
+#pragma unroll
+        for (int e = 1; e < 31; e += 2)
+          top[c] = max3(top[c], __uint_as_float(s[c][e]), __uint_as_float(s[c][e + 1]));
+        top[c] = fmaxf(top[c], __uint_as_float(s[c][31]));
       }
-      const float mine = fmaxf(t0, t1) * sc2;
-      float* rt = red + ((t & 1) * 2 + m) * kSlices * 128;
-      rt[slice * 128 + row] = mine;
-      warp_arrive(red_bar);
-      uint32_t pw[16];
-      float sum;
-      auto exps = [&](const uint32_t (&sr)[32]) {
-        const f2 nm = {-mx, -mx};
-        f2 acc = {0.f, 0.f};
-#pragma unroll
-        for (int c = 0; c < 32; c += 2) {
-          const f2 x = fma2({__uint_as_float(sr[c]), __uint_as_float(sr[c + 1])}, sc2_2, nm);
-          const f2 p = {ex2_approx(x.x), ex2_approx(x.y)};
-          acc = add2(acc, p);
-          pw[c >> 1] = pack_bf16(p.x, p.y);
-        }
-        sum = acc.x + acc.y;
-      };
-      // The maximum rarely moves after the first tile, so the first chunk's
-      // probabilities are computed against the old one while the other slice's
-      // maximum arrives, and again where it did move
-      if (t > 0) exps(s0);
-      if (!await(red_bar, t & 1, ab, prm.status)) { ok = false; break; }
-      const float mt = fmaxf(mine, rt[(slice ^ 1) * 128 + row]);
+      const float mt = fmaxf(max3(top[0], top[1], top[2]), top[3]) * sc2;
       const bool move = mt > mx + C::kRescale;
       if (t == 0) {
         mx = mt;  // finite: key 0 is visible to every row
-        exps(s0);
       } else if (__any_sync(0xffffffffu, move)) {
-        // the row's O^m holds the sums of the earlier tiles: rescale this
-        // slice's DV/2 columns once their MMAs are done (rows that did not
-        // move scale by 1)
+        // O^m holds the sums of the earlier tiles: rescale the row once their
+        // MMAs are done (rows that did not move scale by 1)
         const float alpha = move ? ex2_approx(mx - mt) : 1.f;
         if (!await(o_ready + m, (t - 1) & 1, ab, prm.status)) { ok = false; break; }
         tc_fence_after();
-#pragma unroll
-        for (int c = 0; c < DV / kSlices; c += 16) {
+#pragma unroll 1
+        for (int c = 0; c < DV; c += 16) {
           uint32_t v[16];
-          const uint32_t ta = tmem + lane_off + C::T_O(m) + (DV / kSlices) * slice + c;
+          const uint32_t ta = tmem + lane_off + C::T_O(m) + c;
           tmem_ld16(ta, v);
 #pragma unroll
           for (int e = 0; e < 16; ++e) v[e] = __float_as_uint(__uint_as_float(v[e]) * alpha);
@@ -386,38 +359,41 @@ __global__ void __launch_bounds__(kThreads, 1)
         }
         if (move) mx = mt;
         l *= alpha;
-        tmem_ld32(ts, s0);
-        if (need_mask) mask(s0, j0);
-        exps(s0);
       }
-      // bf16 P over the first 16 of each chunk's 32 columns; the product with
-      // the first chunks starts while the second ones are computed
-      l += sum;
-      tmem_st16(ts, pw);
-      tc_fence_before();
-      warp_arrive(p_full + 2 * m);
-      exps(s1);
-      l += sum;
-      tmem_st16(ts + 32, pw);
-      tc_fence_before();
-      warp_arrive(p_full + 2 * m + 1);
+      const f2 nm = {-mx, -mx};
+      f2 acc = {0.f, 0.f};
+#pragma unroll
+      for (int c = 0; c < 4; ++c) {
+        uint32_t pw[16];
+#pragma unroll
+        for (int e = 0; e < 32; e += 2) {
+          const f2 x = fma2({__uint_as_float(s[c][e]), __uint_as_float(s[c][e + 1])}, sc2_2, nm);
+          const f2 p = {ex2_approx(x.x), ex2_approx(x.y)};
+          acc = add2(acc, p);
+          pw[e >> 1] = pack_bf16(p.x, p.y);
+        }
+        // bf16 P over the first 16 of the chunk's 32 columns; the product with
+        // the first half starts while the second one is computed
+        tmem_st16(ts + 32 * c, pw);
+        if (c & 1) {
+          tc_fence_before();
+          warp_arrive(p_full + 2 * m + (c >> 1));
+        }
+      }
+      l += acc.x + acc.y;
     }
     // ---- epilogue: O = O^1 / l^1 - lam O^2 / l^2, and LSE (natural log) ----
-    // every elementwise thread gets to this barrier, also after a failed wait
-    float* part = red + 4 * kSlices * 128;
-    part[(m * kSlices + slice) * 128 + row] = l;
-    named_sync<kConsumers>(1);
-    float L[2];
-#pragma unroll
-    for (int e = 0; e < 2; ++e)
-      L[e] = part[e * kSlices * 128 + row] + part[(e * kSlices + 1) * 128 + row];
+    // every softmax thread gets to this barrier, also after a failed wait
+    red[m * 128 + row] = l;
+    named_sync<kSoftmax>(1);
+    const float L[2] = {red[row], red[128 + row]};
     ok = __all_sync(0xffffffffu, ok);
     if (ok) ok = await(o_ready + 0, (T - 1) & 1, ab, prm.status);
     if (ok) ok = await(o_ready + 1, (T - 1) & 1, ab, prm.status);
     tc_fence_after();
     if (ok) {
-      constexpr int PART = DV / 4;  // features per thread
-      const int f0 = PART * (warp >> 2);
+      constexpr int PART = DV / 2;  // features per thread
+      const int f0 = PART * m;
       const bool in = i < N;
       const float inv1 = 1.f / L[0], inv2 = 1.f / L[1];
       const float w = in ? lam_row(prm.lam, bh, prm.H, N, i) : 0.f;
@@ -445,13 +421,13 @@ __global__ void __launch_bounds__(kThreads, 1)
           }
         }
       }
-      if (in && slice == 0)
+      if (in)
         prm.lse[((size_t)bh * 2 + m) * N + i] = (mx + log2f(m == 0 ? L[0] : L[1])) * kLn2;
     }
   }
   tc_fence_before();
   __syncthreads();
-  if (warp == kMmaWarp) {
+  if (warp == kFwdMma) {
     tc_fence_after();
     tmem_dealloc(tmem, C::TMEM_COLS);
   }
@@ -1083,11 +1059,11 @@ bool tiles(CUtensorMap* m, const void* ptr, const DiffProblem& p, int heads, int
 }
 
 template <typename K, typename P, typename... M>
-cudaError_t run(K kernel, int units, int N, uint32_t smem, LaunchLog& log, const P& prm,
+cudaError_t run(K kernel, int units, int N, int threads, uint32_t smem, LaunchLog& log, const P& prm,
                 const M&... maps) {
   cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
   if (e != cudaSuccess) return e;
-  kernel<<<(unsigned)(((N + 127) / 128) * units), kThreads, smem, log.stream>>>(maps..., prm);
+  kernel<<<(unsigned)(((N + 127) / 128) * units), threads, smem, log.stream>>>(maps..., prm);
   e = cudaGetLastError();
   log.mark();
   return e;
@@ -1105,7 +1081,7 @@ cudaError_t forward_dv(const DiffProblem& p, const DiffTensors& t, const DiffWor
   f.o = static_cast<__nv_bfloat16*>(t.o);
   f.o2 = static_cast<__nv_bfloat16*>(t.o2);
   f.lse = t.lse;
-  return run(diff_fwd_pass<DV>, f.units, p.N, Fwd<DV>::SMEM, log, f, mQ, mK, mV);
+  return run(diff_fwd_pass<DV>, f.units, p.N, kFwdThreads, Fwd<DV>::SMEM, log, f, mQ, mK, mV);
 }
 
 template <int DV>
@@ -1122,7 +1098,7 @@ cudaError_t backward_dv(const DiffProblem& p, const DiffTensors& t, const DiffWo
   r.lse = t.lse;
   r.D = ws.D;
   r.d2 = ws.d2;
-  cudaError_t e = run(diff_row_pass<DV>, r.units, p.N, Row<DV>::SMEM, log, r, mQ, mK, mV, mDO);
+  cudaError_t e = run(diff_row_pass<DV>, r.units, p.N, kThreads, Row<DV>::SMEM, log, r, mQ, mK, mV, mDO);
   if (e != cudaSuccess) return e;
   ColParams c;
   static_cast<Common&>(c) = common(p, t, ws, p.B * p.Hk);
@@ -1130,7 +1106,7 @@ cudaError_t backward_dv(const DiffProblem& p, const DiffTensors& t, const DiffWo
   c.dv = static_cast<__nv_bfloat16*>(t.dv);
   c.lse = t.lse;
   c.D = ws.D;
-  return run(diff_col_pass<DV>, c.units, p.N, Col<DV>::SMEM, log, c, mK, mV, sQ, sDO);
+  return run(diff_col_pass<DV>, c.units, p.N, kThreads, Col<DV>::SMEM, log, c, mK, mV, sQ, sDO);
 }
 
 }  // namespace
