@@ -59,6 +59,7 @@ constexpr int kRowSlices = kWarps / 4;     // column slices per row
 // exchange between threads), a producer and an MMA warp; 200 registers each.
 constexpr int kSoftmax = 8 * 32;
 constexpr int kFwdProducer = 8, kFwdMma = 9, kFwdThreads = 10 * 32;
+constexpr int kQueryWarp = kWarps + 2, kColThreads = (kWarps + 3) * 32;  // column pass
 constexpr float kLn2 = 0.6931471805599453f;
 constexpr uint64_t kDrainNs = 100000000ull;  // limit of the waits after an abort
 constexpr int kD = 64;                     // features of a query or key
@@ -714,7 +715,7 @@ __global__ void __launch_bounds__(kThreads, 1)
 template <int DV>
 struct Col {
   static constexpr int BM = 128, BN = 64;
-  static constexpr int QS = 6, OS = 4;            // Q subtile and dO tile stages
+  static constexpr int QS = 8, OS = 5;            // Q subtile and dO tile stages
   static constexpr uint32_t KB = BM * kD * 2;     // stationary K subtile
   static constexpr uint32_t VB = BM * DV * 2;
   static constexpr uint32_t QB = BN * kD * 2;     // streamed Q subtile
@@ -741,7 +742,7 @@ struct ColParams : Common {
 };
 
 template <int DV>
-__global__ void __launch_bounds__(kThreads, 1)
+__global__ void __launch_bounds__(kColThreads, 1)
     diff_col_pass(const __grid_constant__ CUtensorMap mK, const __grid_constant__ CUtensorMap mV,
                   const __grid_constant__ CUtensorMap mQ, const __grid_constant__ CUtensorMap mDO,
                   ColParams prm) {
@@ -762,9 +763,9 @@ __global__ void __launch_bounds__(kThreads, 1)
   uint64_t* dp_full = ds_full + 2;         // [2]
   uint64_t* acc_done = dp_full + 2;
   uint64_t* drain = acc_done + 1;
-  static_assert((1 + 2 * C::QS + 2 * C::OS + 8) * 8 <= 256, "barriers end below the TMEM slot");
-  uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(smem + C::OFF_MISC + 256);
-  Abort* ab = reinterpret_cast<Abort*>(smem + C::OFF_MISC + 264);
+  static_assert((1 + 2 * C::QS + 2 * C::OS + 8) * 8 <= 384, "barriers end below the TMEM slot");
+  uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(smem + C::OFF_MISC + 384);
+  Abort* ab = reinterpret_cast<Abort*>(smem + C::OFF_MISC + 392);
   float* scal = reinterpret_cast<float*>(smem + C::OFF_SC);
 
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
@@ -814,7 +815,8 @@ __global__ void __launch_bounds__(kThreads, 1)
       load_tile(smem + C::OFF_K, &mK, kv_full, j0, 2 * kvh);
       load_tile(smem + C::OFF_K + C::KB, &mK, kv_full, j0, 2 * kvh + 1);
     }
-    // the next tile's row scalars are fetched into registers one tile ahead
+    // dO tiles and the row scalars; the next tile's scalars are fetched into
+    // registers one tile ahead
     constexpr int PER = C::BN / 32;
     float pre[5][PER];
     auto fetch = [&](int bh, int q0) {
@@ -831,15 +833,12 @@ __global__ void __launch_bounds__(kThreads, 1)
         pre[4][e] = in ? w * prm.D[r2] : 0.f;
       }
     };
-    int g = 0, t = 0;  // tile within head g
+    int g = 0, t = 0;  // tile t within head g
     fetch(bh0, qstart);
-    int q_issued = 0, o_issued = 0;
+    int issued = 0;
     for (int a = 0; a < T; ++a) {
       const int os = a % C::OS, q0 = qstart + t * C::BN, bh = bh0 + g;
-      bool ok = true;
-      if (lane == 0 && a >= C::OS)
-        ok = wait_bar(do_empty + os, ((a / C::OS) - 1) & 1, ab, prm.status);
-      if (__shfl_sync(0xffffffffu, ok ? 1 : 0, 0) == 0) break;
+      if (a >= C::OS && !await(do_empty + os, ((a / C::OS) - 1) & 1, ab, prm.status)) break;
       // the stage's scalars were last read by the elementwise warps of tile
       // a - OS, before the dV product that freed the stage
       float* sc = scal + os * 5 * C::BN;
@@ -851,18 +850,8 @@ __global__ void __launch_bounds__(kThreads, 1)
       if (lane == 0) {
         mbar_arrive_expect_tx(do_full + os, C::OB);
         load_tile(smem + C::OFF_DO + os * C::OB, &mDO, do_full + os, q0, bh);
-        ++o_issued;
-        for (int m = 0; ok && m < 2; ++m) {
-          const int u = 2 * a + m, s = u % C::QS;
-          if (u >= C::QS) ok = wait_bar(q_empty + s, ((u / C::QS) - 1) & 1, ab, prm.status);
-          if (ok) {
-            mbar_arrive_expect_tx(q_full + s, C::QB);
-            load_tile(smem + C::OFF_Q + s * C::QB, &mQ, q_full + s, q0, 2 * bh + m);
-            ++q_issued;
-          }
-        }
+        ++issued;
       }
-      if (__shfl_sync(0xffffffffu, ok ? 1 : 0, 0) == 0) break;
       if (++t == Tq) {
         t = 0;
         ++g;
@@ -871,10 +860,33 @@ __global__ void __launch_bounds__(kThreads, 1)
     }
     if (lane == 0) {
       mbar_wait_bounded(kv_full, 0, prm.status, kDrainNs);
-      for (int u = max(0, q_issued - C::QS); u < q_issued; ++u)
-        mbar_wait_bounded(q_full + (u % C::QS), (u / C::QS) & 1, prm.status, kDrainNs);
-      for (int a = max(0, o_issued - C::OS); a < o_issued; ++a)
+      for (int a = max(0, issued - C::OS); a < issued; ++a)
         mbar_wait_bounded(do_full + (a % C::OS), (a / C::OS) & 1, prm.status, kDrainNs);
+    }
+  } else if (warp == kQueryWarp) {
+    // Q subtiles, in a warp of their own: behind the dO loads in one warp, each
+    // ring would run only as far ahead as the other lets it
+    if (lane == 0) {
+      int g = 0, t = 0, issued = 0;
+      bool ok = true;
+      for (int a = 0; ok && a < T; ++a) {
+        for (int m = 0; m < 2; ++m) {
+          const int u = 2 * a + m, s = u % C::QS;
+          if (u >= C::QS && !wait_bar(q_empty + s, ((u / C::QS) - 1) & 1, ab, prm.status)) {
+            ok = false;
+            break;
+          }
+          mbar_arrive_expect_tx(q_full + s, C::QB);
+          load_tile(smem + C::OFF_Q + s * C::QB, &mQ, q_full + s, qstart + t * C::BN, 2 * (bh0 + g) + m);
+          ++issued;
+        }
+        if (++t == Tq) {
+          t = 0;
+          ++g;
+        }
+      }
+      for (int u = max(0, issued - C::QS); u < issued; ++u)
+        mbar_wait_bounded(q_full + (u % C::QS), (u / C::QS) & 1, prm.status, kDrainNs);
     }
   } else if (warp == kMmaWarp) {
     constexpr uint32_t id_s = idesc_bf16(128, C::BN, false, false);  // S^T and dP^T
@@ -1106,7 +1118,7 @@ cudaError_t backward_dv(const DiffProblem& p, const DiffTensors& t, const DiffWo
   c.dv = static_cast<__nv_bfloat16*>(t.dv);
   c.lse = t.lse;
   c.D = ws.D;
-  return run(diff_col_pass<DV>, c.units, p.N, kThreads, Col<DV>::SMEM, log, c, mK, mV, sQ, sDO);
+  return run(diff_col_pass<DV>, c.units, p.N, kColThreads, Col<DV>::SMEM, log, c, mK, mV, sQ, sDO);
 }
 
 }  // namespace
