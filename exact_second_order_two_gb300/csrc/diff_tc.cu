@@ -59,7 +59,6 @@ constexpr int kRowSlices = kWarps / 4;     // column slices per row
 // exchange between threads), a producer and an MMA warp; 200 registers each.
 constexpr int kSoftmax = 8 * 32;
 constexpr int kFwdProducer = 8, kFwdMma = 9, kFwdThreads = 10 * 32;
-constexpr int kQueryWarp = kWarps + 2, kColThreads = (kWarps + 3) * 32;  // column pass
 constexpr float kLn2 = 0.6931471805599453f;
 constexpr uint64_t kDrainNs = 100000000ull;  // limit of the waits after an abort
 constexpr int kD = 64;                     // features of a query or key
@@ -130,11 +129,12 @@ __device__ __forceinline__ void store32(__nv_bfloat16* dst, const uint32_t (&v)[
 template <int DV>
 struct Fwd {
   static constexpr int BM = 128, BN = 128;
-  static constexpr int KS = 4, VS = 3;             // K subtile and V tile stages
-  static constexpr uint32_t QB = BM * kD * 2;      // Q or K subtile
+  static constexpr int ST = 3;                     // key tile stages: K^1, K^2, V
+  static constexpr uint32_t QB = BM * kD * 2;      // Q or K of one map
   static constexpr uint32_t VB = BN * DV * 2;
-  static constexpr uint32_t OFF_Q = 0, OFF_K = 2 * QB, OFF_V = OFF_K + KS * QB;
-  static constexpr uint32_t OFF_RED = OFF_V + VS * VB;  // [2][128] row sums
+  static constexpr uint32_t STB = 2 * QB + VB;
+  static constexpr uint32_t OFF_Q = 0, OFF_T = 2 * QB;
+  static constexpr uint32_t OFF_RED = OFF_T + ST * STB;  // [2][128] row sums
   static constexpr uint32_t OFF_MISC = OFF_RED + 2 * 128 * 4;
   static constexpr uint32_t SMEM = OFF_MISC + 512;
   static_assert(SMEM <= 232448, "forward shared memory budget");
@@ -166,15 +166,13 @@ __global__ void __launch_bounds__(kFwdThreads, 1)
     return;
   }
   uint64_t* q_full = reinterpret_cast<uint64_t*>(smem + C::OFF_MISC);
-  uint64_t* k_full = q_full + 1;             // [KS]
-  uint64_t* k_empty = k_full + C::KS;        // [KS]
-  uint64_t* v_full = k_empty + C::KS;        // [VS]
-  uint64_t* v_empty = v_full + C::VS;        // [VS]
-  uint64_t* s_full = v_empty + C::VS;        // [2]: scores of map m in TMEM
+  uint64_t* full = q_full + 1;               // [ST]: K^1, K^2 and V of a tile landed
+  uint64_t* empty = full + C::ST;            // [ST]: its last products done
+  uint64_t* s_full = empty + C::ST;          // [2]: scores of map m in TMEM
   uint64_t* p_full = s_full + 2;             // [2][2]: half a tile's bf16 P written, O^m rescaled
-  uint64_t* o_ready = p_full + 4;            // [2]: P V of map m done, one phase per tile
-  uint64_t* drain = o_ready + 2;
-  static_assert((1 + 2 * C::KS + 2 * C::VS + 9) * 8 <= 256, "barriers end below the TMEM slot");
+  uint64_t* o_done = p_full + 4;
+  uint64_t* drain = o_done + 1;
+  static_assert((1 + 2 * C::ST + 8) * 8 <= 256, "barriers end below the TMEM slot");
   uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(smem + C::OFF_MISC + 256);
   Abort* ab = reinterpret_cast<Abort*>(smem + C::OFF_MISC + 264);
   float* red = reinterpret_cast<float*>(smem + C::OFF_RED);
@@ -191,20 +189,16 @@ __global__ void __launch_bounds__(kFwdThreads, 1)
 
   if (threadIdx.x == 0) {
     mbar_init(q_full, 1);
-    for (int s = 0; s < C::KS; ++s) {
-      mbar_init(k_full + s, 1);
-      mbar_init(k_empty + s, 1);
-    }
-    for (int s = 0; s < C::VS; ++s) {
-      mbar_init(v_full + s, 1);
-      mbar_init(v_empty + s, 1);
+    for (int s = 0; s < C::ST; ++s) {
+      mbar_init(full + s, 1);
+      mbar_init(empty + s, 1);
     }
     for (int m = 0; m < 2; ++m) {
       mbar_init(s_full + m, 1);
       mbar_init(p_full + 2 * m, 4);
       mbar_init(p_full + 2 * m + 1, 4);
-      mbar_init(o_ready + m, 1);
     }
+    mbar_init(o_done, 1);
     mbar_init(drain, 1);
     ab->flag = 0;
     ab->limit_ns = prm.wait_ns;
@@ -224,65 +218,55 @@ __global__ void __launch_bounds__(kFwdThreads, 1)
       mbar_arrive_expect_tx(q_full, 2 * C::QB);
       load_tile(smem + C::OFF_Q, &mQ, q_full, i0, 2 * bh);
       load_tile(smem + C::OFF_Q + C::QB, &mQ, q_full, i0, 2 * bh + 1);
-      int k_issued = 0, v_issued = 0;
-      auto load_k = [&](int u) -> bool {
-        const int s = u % C::KS;
-        if (u >= C::KS && !wait_bar(k_empty + s, ((u / C::KS) - 1) & 1, ab, prm.status)) return false;
-        mbar_arrive_expect_tx(k_full + s, C::QB);
-        load_tile(smem + C::OFF_K + s * C::QB, &mK, k_full + s, (u >> 1) * C::BN, 2 * kvh + (u & 1));
-        ++k_issued;
-        return true;
-      };
-      auto load_v = [&](int t) -> bool {
-        const int s = t % C::VS;
-        if (t >= C::VS && !wait_bar(v_empty + s, ((t / C::VS) - 1) & 1, ab, prm.status)) return false;
-        mbar_arrive_expect_tx(v_full + s, C::VB);
-        load_tile(smem + C::OFF_V + s * C::VB, &mV, v_full + s, t * C::BN, kvh);
-        ++v_issued;
-        return true;
-      };
-      // K runs a tile ahead of V
-      bool ok = load_k(0) && load_k(1);
-      for (int t = 0; ok && t < T; ++t) {
-        if (t + 1 < T && !(load_k(2 * t + 2) && load_k(2 * t + 3))) break;
-        if (!load_v(t)) break;
+      int issued = 0;
+      for (int t = 0; t < T; ++t) {
+        const int st = t % C::ST;
+        if (t >= C::ST && !wait_bar(empty + st, ((t / C::ST) - 1) & 1, ab, prm.status)) break;
+        uint8_t* dst = smem + C::OFF_T + st * C::STB;
+        mbar_arrive_expect_tx(full + st, C::STB);
+        load_tile(dst, &mK, full + st, t * C::BN, 2 * kvh);
+        load_tile(dst + C::QB, &mK, full + st, t * C::BN, 2 * kvh + 1);
+        load_tile(dst + 2 * C::QB, &mV, full + st, t * C::BN, kvh);
+        ++issued;
       }
       // every load this thread issued has landed before the CTA exits (after an
       // abort some were never awaited); on the normal path these return at once
       mbar_wait_bounded(q_full, 0, prm.status, kDrainNs);
-      for (int u = max(0, k_issued - C::KS); u < k_issued; ++u)
-        mbar_wait_bounded(k_full + (u % C::KS), (u / C::KS) & 1, prm.status, kDrainNs);
-      for (int t = max(0, v_issued - C::VS); t < v_issued; ++t)
-        mbar_wait_bounded(v_full + (t % C::VS), (t / C::VS) & 1, prm.status, kDrainNs);
+      for (int t = max(0, issued - C::ST); t < issued; ++t)
+        mbar_wait_bounded(full + (t % C::ST), (t / C::ST) & 1, prm.status, kDrainNs);
     }
   } else if (warp == kFwdMma) {
     constexpr uint32_t id_s = idesc_bf16(128, C::BN, false, false);  // S = Q K^T
     constexpr uint32_t id_o = idesc_bf16(128, DV, false, true);      // O += P V: B MN-major
-    bool ok = await(q_full, 0, ab, prm.status);
-    auto issue_s = [&](int t, int m) -> bool {
-      const int u = 2 * t + m, s = u % C::KS;
-      if (!await(k_full + s, (u / C::KS) & 1, ab, prm.status)) return false;
-      tc_fence_after();
+    // A wait of this warp costs a few hundred cycles of a busy pipe and a commit
+    // some tens, so a tile's loads share one barrier and only what someone
+    // waits for is committed
+    auto tile = [&](int t) { return sb + C::OFF_T + (uint32_t)(t % C::ST) * C::STB; };
+    auto ready = [&](int t) { return await(full + t % C::ST, (t / C::ST) & 1, ab, prm.status); };
+    auto issue_s = [&](int t, int m) {
       const uint32_t q_lo = opaque(lo_kmajor(sb + C::OFF_Q + m * C::QB));
-      const uint32_t k_lo = opaque(lo_kmajor(sb + C::OFF_K + s * C::QB));
+      const uint32_t k_lo = opaque(lo_kmajor(tile(t) + m * C::QB));
 #pragma unroll
       for (int k = 0; k < kD / 16; ++k)
         mma_ss_w(tmem + C::T_S(m), q_lo + kslice_off(C::BM, k), k_lo + kslice_off(C::BN, k), id_s,
                  k > 0 ? 1u : 0u);
       mma_commit_w(s_full + m);
-      mma_commit_w(k_empty + s);
-      return true;
     };
-    ok = ok && issue_s(0, 0) && issue_s(0, 1);
+    bool ok = await(q_full, 0, ab, prm.status) && ready(0);
+    tc_fence_after();
+    if (ok) {
+      issue_s(0, 0);
+      issue_s(0, 1);
+    }
     for (int t = 0; ok && t < T; ++t) {
-      const int vs = t % C::VS;
-      if (!await(v_full + vs, (t / C::VS) & 1, ab, prm.status)) { ok = false; break; }
+      const bool more = t + 1 < T;
+      if (more && !ready(t + 1)) { ok = false; break; }
+      const uint32_t v_mn = opaque(lo_mnmajor(tile(t) + 2 * C::QB, C::BN * 128));
 #pragma unroll
       for (int m = 0; m < 2; ++m) {
-        if (!ok) break;
         // O^m += P^m V, A = bf16 P from TMEM, in two halves of 64 keys; then
-        // the next tile's scores over P
-        const uint32_t v_mn = opaque(lo_mnmajor(sb + C::OFF_V + vs * C::VB, C::BN * 128));
+        // the next tile's scores over P.  Their commit covers the product, so
+        // whoever sees S^m of a tile may rescale O^m.
 #pragma unroll
         for (int h = 0; h < 2; ++h) {
           if (!ok) break;
@@ -294,11 +278,11 @@ __global__ void __launch_bounds__(kFwdThreads, 1)
                      (t > 0 || k > 0) ? 1u : 0u);
         }
         if (!ok) break;
-        if (m == 1) mma_commit_w(v_empty + vs);
-        mma_commit_w(o_ready + m);
-        if (t + 1 < T) ok = issue_s(t + 1, m);
+        if (m == 1) mma_commit_w(empty + t % C::ST);
+        if (more) issue_s(t + 1, m);
       }
     }
+    if (ok) mma_commit_w(o_done);
     // every MMA this thread issued has completed before TMEM is released
     mma_commit_w(drain);
     mbar_wait_bounded(drain, 0, prm.status, kDrainNs);
@@ -344,11 +328,9 @@ __global__ void __launch_bounds__(kFwdThreads, 1)
       if (t == 0) {
         mx = mt;  // finite: key 0 is visible to every row
       } else if (__any_sync(0xffffffffu, move)) {
-        // O^m holds the sums of the earlier tiles: rescale the row once their
-        // MMAs are done (rows that did not move scale by 1)
+        // O^m holds the sums of the earlier tiles, whose products were committed
+        // with these scores: rescale the row (rows that did not move by 1)
         const float alpha = move ? ex2_approx(mx - mt) : 1.f;
-        if (!await(o_ready + m, (t - 1) & 1, ab, prm.status)) { ok = false; break; }
-        tc_fence_after();
 #pragma unroll 1
         for (int c = 0; c < DV; c += 16) {
           uint32_t v[16];
@@ -389,8 +371,7 @@ __global__ void __launch_bounds__(kFwdThreads, 1)
     named_sync<kSoftmax>(1);
     const float L[2] = {red[row], red[128 + row]};
     ok = __all_sync(0xffffffffu, ok);
-    if (ok) ok = await(o_ready + 0, (T - 1) & 1, ab, prm.status);
-    if (ok) ok = await(o_ready + 1, (T - 1) & 1, ab, prm.status);
+    if (ok) ok = await(o_done, 0, ab, prm.status);
     tc_fence_after();
     if (ok) {
       constexpr int PART = DV / 2;  // features per thread
@@ -440,11 +421,11 @@ __global__ void __launch_bounds__(kFwdThreads, 1)
 template <int DV>
 struct Row {
   static constexpr int BM = 128, BN = 128;
-  static constexpr int KS = 4, VS = 2;
+  static constexpr int KS = 3, VS = 2;         // stages of K^1 and K^2, and of V
   static constexpr uint32_t QB = BM * kD * 2;
   static constexpr uint32_t VB = BN * DV * 2;  // dO or V tile
   static constexpr uint32_t OFF_Q = 0, OFF_DO = 2 * QB, OFF_K = OFF_DO + VB;
-  static constexpr uint32_t OFF_V = OFF_K + KS * QB;
+  static constexpr uint32_t OFF_V = OFF_K + KS * 2 * QB;
   static constexpr uint32_t OFF_RED = OFF_V + VS * VB;  // [slices][128]
   static constexpr uint32_t OFF_MISC = OFF_RED + kRowSlices * 128 * 4;
   static constexpr uint32_t SMEM = OFF_MISC + 512;
@@ -476,17 +457,14 @@ __global__ void __launch_bounds__(kThreads, 1)
     return;
   }
   uint64_t* q_full = reinterpret_cast<uint64_t*>(smem + C::OFF_MISC);  // Q^1, Q^2, dO
-  uint64_t* k_full = q_full + 1;           // [KS]
-  uint64_t* k_empty = k_full + C::KS;      // [KS]
-  uint64_t* v_full = k_empty + C::KS;      // [VS]
-  uint64_t* v_empty = v_full + C::VS;      // [VS]
-  uint64_t* s_full = v_empty + C::VS;      // [2]
+  uint64_t* full = q_full + 1;             // [KS]: K^1, K^2 and V of a tile landed
+  uint64_t* k_empty = full + C::KS;        // [KS]
+  uint64_t* v_empty = k_empty + C::KS;     // [VS]
+  uint64_t* s_full = v_empty + C::VS;      // [2]: scores of map m in TMEM, for map 0 dP too
   uint64_t* ds_full = s_full + 2;          // [2]: bf16 dS written over the scores
-  uint64_t* dp_full = ds_full + 2;
-  uint64_t* dp_read = dp_full + 1;         // the elementwise warps hold dP
-  uint64_t* acc_done = dp_read + 1;
+  uint64_t* acc_done = ds_full + 2;
   uint64_t* drain = acc_done + 1;
-  static_assert((1 + 2 * C::KS + 2 * C::VS + 8) * 8 <= 256, "barriers end below the TMEM slot");
+  static_assert((1 + 2 * C::KS + C::VS + 6) * 8 <= 256, "barriers end below the TMEM slot");
   uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(smem + C::OFF_MISC + 256);
   Abort* ab = reinterpret_cast<Abort*>(smem + C::OFF_MISC + 264);
   float* red = reinterpret_cast<float*>(smem + C::OFF_RED);
@@ -504,19 +482,14 @@ __global__ void __launch_bounds__(kThreads, 1)
   if (threadIdx.x == 0) {
     mbar_init(q_full, 1);
     for (int s = 0; s < C::KS; ++s) {
-      mbar_init(k_full + s, 1);
+      mbar_init(full + s, 1);
       mbar_init(k_empty + s, 1);
     }
-    for (int s = 0; s < C::VS; ++s) {
-      mbar_init(v_full + s, 1);
-      mbar_init(v_empty + s, 1);
-    }
+    for (int s = 0; s < C::VS; ++s) mbar_init(v_empty + s, 1);
     for (int m = 0; m < 2; ++m) {
       mbar_init(s_full + m, 1);
       mbar_init(ds_full + m, kWarps);
     }
-    mbar_init(dp_full, 1);
-    mbar_init(dp_read, kWarps);
     mbar_init(acc_done, 1);
     mbar_init(drain, 1);
     ab->flag = 0;
@@ -538,81 +511,73 @@ __global__ void __launch_bounds__(kThreads, 1)
       load_tile(smem + C::OFF_DO, &mDO, q_full, i0, bh);
       load_tile(smem + C::OFF_Q, &mQ, q_full, i0, 2 * bh);
       load_tile(smem + C::OFF_Q + C::QB, &mQ, q_full, i0, 2 * bh + 1);
-      int k_issued = 0, v_issued = 0;
-      bool ok = true;
-      for (int t = 0; ok && t < T; ++t) {
-        const int vs = t % C::VS;
+      int issued = 0;
+      for (int t = 0; t < T; ++t) {
+        const int ks = t % C::KS, vs = t % C::VS;
         if (t >= C::VS && !wait_bar(v_empty + vs, ((t / C::VS) - 1) & 1, ab, prm.status)) break;
-        mbar_arrive_expect_tx(v_full + vs, C::VB);
-        load_tile(smem + C::OFF_V + vs * C::VB, &mV, v_full + vs, t * C::BN, kvh);
-        ++v_issued;
-        for (int u = 2 * t; u < 2 * t + 2; ++u) {
-          const int s = u % C::KS;
-          if (u >= C::KS && !wait_bar(k_empty + s, ((u / C::KS) - 1) & 1, ab, prm.status)) {
-            ok = false;
-            break;
-          }
-          mbar_arrive_expect_tx(k_full + s, C::QB);
-          load_tile(smem + C::OFF_K + s * C::QB, &mK, k_full + s, t * C::BN, 2 * kvh + (u & 1));
-          ++k_issued;
-        }
+        if (t >= C::KS && !wait_bar(k_empty + ks, ((t / C::KS) - 1) & 1, ab, prm.status)) break;
+        uint8_t* dst = smem + C::OFF_K + ks * 2 * C::QB;
+        mbar_arrive_expect_tx(full + ks, 2 * C::QB + C::VB);
+        load_tile(smem + C::OFF_V + vs * C::VB, &mV, full + ks, t * C::BN, kvh);
+        load_tile(dst, &mK, full + ks, t * C::BN, 2 * kvh);
+        load_tile(dst + C::QB, &mK, full + ks, t * C::BN, 2 * kvh + 1);
+        ++issued;
       }
       mbar_wait_bounded(q_full, 0, prm.status, kDrainNs);
-      for (int u = max(0, k_issued - C::KS); u < k_issued; ++u)
-        mbar_wait_bounded(k_full + (u % C::KS), (u / C::KS) & 1, prm.status, kDrainNs);
-      for (int t = max(0, v_issued - C::VS); t < v_issued; ++t)
-        mbar_wait_bounded(v_full + (t % C::VS), (t / C::VS) & 1, prm.status, kDrainNs);
+      for (int t = max(0, issued - C::KS); t < issued; ++t)
+        mbar_wait_bounded(full + (t % C::KS), (t / C::KS) & 1, prm.status, kDrainNs);
     }
   } else if (warp == kMmaWarp) {
     constexpr uint32_t id_s = idesc_bf16(128, C::BN, false, false);  // S and dP
     constexpr uint32_t id_q = idesc_bf16(128, kD, false, true);      // dQ += dS K: B MN-major
-    auto issue_dp = [&](int t) -> bool {
-      const int vs = t % C::VS;
-      if (!await(v_full + vs, (t / C::VS) & 1, ab, prm.status)) return false;
-      tc_fence_after();
-      const uint32_t do_lo = opaque(lo_kmajor(sb + C::OFF_DO));
-      const uint32_t v_lo = opaque(lo_kmajor(sb + C::OFF_V + vs * C::VB));
-#pragma unroll
-      for (int k = 0; k < DV / 16; ++k)
-        mma_ss_w(tmem + C::T_DP, do_lo + kslice_off(C::BM, k), v_lo + kslice_off(C::BN, k), id_s,
-                 k > 0 ? 1u : 0u);
-      mma_commit_w(dp_full);
-      mma_commit_w(v_empty + vs);
-      return true;
-    };
-    auto issue_s = [&](int u) -> bool {
-      const int s = u % C::KS, m = u & 1;
-      if (!await(k_full + s, (u / C::KS) & 1, ab, prm.status)) return false;
-      tc_fence_after();
+    auto k_tile = [&](int t, int m) { return sb + C::OFF_K + (uint32_t)(2 * (t % C::KS) + m) * C::QB; };
+    auto ready = [&](int t) { return await(full + t % C::KS, (t / C::KS) & 1, ab, prm.status); };
+    auto issue_s = [&](int t, int m) {
       const uint32_t q_lo = opaque(lo_kmajor(sb + C::OFF_Q + m * C::QB));
-      const uint32_t k_lo = opaque(lo_kmajor(sb + C::OFF_K + s * C::QB));
+      const uint32_t k_lo = opaque(lo_kmajor(k_tile(t, m)));
 #pragma unroll
       for (int k = 0; k < kD / 16; ++k)
         mma_ss_w(tmem + C::T_S(m), q_lo + kslice_off(C::BM, k), k_lo + kslice_off(C::BN, k), id_s,
                  k > 0 ? 1u : 0u);
-      mma_commit_w(s_full + m);
-      return true;
     };
-    const int U = 2 * T;
-    bool ok = await(q_full, 0, ab, prm.status) && issue_dp(0) && issue_s(0);
-    for (int u = 0; ok && u < U; ++u) {
-      const int m = u & 1, t = u >> 1, s = u % C::KS;
-      // the next subtile's scores go over the dS of subtile u - 1, whose dQ
-      // product was issued before; the next tile's dP once this one is read
-      if (u + 1 < U && !issue_s(u + 1)) { ok = false; break; }
-      if (m == 0 && t + 1 < T) {
-        if (!await(dp_read, t & 1, ab, prm.status)) { ok = false; break; }
-        tc_fence_after();
-        if (!issue_dp(t + 1)) { ok = false; break; }
-      }
-      if (!await(ds_full + m, t & 1, ab, prm.status)) { ok = false; break; }
-      tc_fence_after();
-      const uint32_t k_mn = opaque(lo_mnmajor(sb + C::OFF_K + s * C::QB, C::BN * 128));
+    // S^1 and dP of tile t, one commit
+    auto issue_first = [&](int t) {
+      issue_s(t, 0);
+      const uint32_t do_lo = opaque(lo_kmajor(sb + C::OFF_DO));
+      const uint32_t v_lo = opaque(lo_kmajor(sb + C::OFF_V + (t % C::VS) * C::VB));
+#pragma unroll
+      for (int k = 0; k < DV / 16; ++k)
+        mma_ss_w(tmem + C::T_DP, do_lo + kslice_off(C::BM, k), v_lo + kslice_off(C::BN, k), id_s,
+                 k > 0 ? 1u : 0u);
+      mma_commit_w(s_full);
+      mma_commit_w(v_empty + t % C::VS);
+    };
+    // dQ^m += dS^m K^m
+    auto issue_dq = [&](int t, int m) {
+      const uint32_t k_mn = opaque(lo_mnmajor(k_tile(t, m), C::BN * 128));
 #pragma unroll
       for (int k = 0; k < C::BN / 16; ++k)
         mma_ts_w(tmem + C::T_DQ(m), tmem + C::T_S(m) + C::a_col(k), k_mn + kstep_off(k), id_q,
                  (t > 0 || k > 0) ? 1u : 0u);
-      mma_commit_w(k_empty + s);
+    };
+    bool ok = await(q_full, 0, ab, prm.status) && ready(0);
+    tc_fence_after();
+    if (ok) issue_first(0);
+    for (int t = 0; ok && t < T; ++t) {
+      const bool more = t + 1 < T;
+      // scores go over the dS of the tile before, whose dQ product is issued
+      issue_s(t, 1);
+      mma_commit_w(s_full + 1);
+      ok = (!more || ready(t + 1)) && await(ds_full, t & 1, ab, prm.status);
+      if (!ok) break;
+      tc_fence_after();
+      issue_dq(t, 0);
+      // every thread took dP into registers before it wrote dS^1
+      if (more) issue_first(t + 1);
+      if (!await(ds_full + 1, t & 1, ab, prm.status)) { ok = false; break; }
+      tc_fence_after();
+      issue_dq(t, 1);
+      mma_commit_w(k_empty + t % C::KS);
     }
     if (ok) mma_commit_w(acc_done);
     mma_commit_w(drain);
@@ -644,17 +609,11 @@ __global__ void __launch_bounds__(kThreads, 1)
       for (int m = 0; m < 2; ++m) {
         if (!ok) break;
         if (!await(s_full + m, t & 1, ab, prm.status)) { ok = false; break; }
-        if (m == 0 && !await(dp_full, t & 1, ab, prm.status)) { ok = false; break; }
         tc_fence_after();
         const uint32_t ts = tmem + lane_off + C::T_S(m) + NC * slice;
         uint32_t sr[NC];
-        if (m == 0) {
-          tmem_ld32x2(ts, tmem + lane_off + C::T_DP + NC * slice, sr, dp);
-          tc_fence_before();
-          warp_arrive(dp_read);
-        } else {
-          tmem_ld32(ts, sr);
-        }
+        if (m == 0) tmem_ld32x2(ts, tmem + lane_off + C::T_DP + NC * slice, sr, dp);
+        else tmem_ld32(ts, sr);
         const f2 nl2 = {nl[m], nl[m]}, mul2_ = {mul[m], mul[m]}, add2_ = {add[m], add[m]};
         uint32_t dsw[NC / 2];
         auto body = [&](auto masked) {
@@ -715,24 +674,25 @@ __global__ void __launch_bounds__(kThreads, 1)
 template <int DV>
 struct Col {
   static constexpr int BM = 128, BN = 64;
-  static constexpr int QS = 8, OS = 5;            // Q subtile and dO tile stages
-  static constexpr uint32_t KB = BM * kD * 2;     // stationary K subtile
+  static constexpr int ST = 4;                    // query tile stages: Q^1, Q^2, dO
+  static constexpr uint32_t KB = BM * kD * 2;     // stationary K of one map
   static constexpr uint32_t VB = BM * DV * 2;
-  static constexpr uint32_t QB = BN * kD * 2;     // streamed Q subtile
-  static constexpr uint32_t OB = BN * DV * 2;     // streamed dO tile
-  static constexpr uint32_t OFF_K = 0, OFF_V = 2 * KB, OFF_Q = OFF_V + VB;
-  static constexpr uint32_t OFF_DO = OFF_Q + QS * QB;
-  // [OS][5][BN]: -LSE^1 log2 e, -LSE^2 log2 e, -D^1, -lam, lam D^2
-  static constexpr uint32_t OFF_SC = OFF_DO + OS * OB;
-  static constexpr uint32_t OFF_MISC = OFF_SC + OS * 5 * BN * 4;
+  static constexpr uint32_t QB = BN * kD * 2;     // streamed Q of one map
+  static constexpr uint32_t OB = BN * DV * 2;     // streamed dO
+  static constexpr uint32_t STB = 2 * QB + OB;
+  static constexpr uint32_t OFF_K = 0, OFF_V = 2 * KB, OFF_T = OFF_V + VB;
+  // [ST][5][BN]: -LSE^1 log2 e, -LSE^2 log2 e, -D^1, -lam, lam D^2
+  static constexpr uint32_t OFF_SC = OFF_T + ST * STB;
+  static constexpr uint32_t OFF_MISC = OFF_SC + ST * 5 * BN * 4;
   static constexpr uint32_t SMEM = OFF_MISC + 512;
   static_assert(SMEM <= 232448, "column pass shared memory budget");
-  // TMEM columns: two S^T buffers (each thread's 16 columns then hold bf16
-  // dS^T in the last 8 and, for map 2, W^T in the first 8), two dP^T buffers,
-  // dK^1, dK^2, dV
-  static constexpr uint32_t TMEM_COLS = 512, T_DV = 384;
-  __host__ __device__ static constexpr uint32_t T_S(int m) { return 64u * m; }
-  __host__ __device__ static constexpr uint32_t T_DP(int b) { return 128u + 64u * b; }
+  // TMEM columns: S^T of map 1, two buffers for that of map 2 (each thread's 16
+  // columns then hold bf16 dS^T in the last 8 and, for map 2, W^T in the first
+  // 8), dP^T, dK^1, dK^2, dV.  With the second buffer a tile's three score
+  // blocks are all computed while the elementwise warps are on map 2 of the
+  // tile before.
+  static constexpr uint32_t TMEM_COLS = 512, T_S1 = 0, T_DP = 192, T_DV = 384;
+  __host__ __device__ static constexpr uint32_t T_S2(int b) { return 64u + 64u * b; }
   __host__ __device__ static constexpr uint32_t T_DK(int m) { return 256u + (uint32_t)kD * m; }
 };
 
@@ -742,7 +702,7 @@ struct ColParams : Common {
 };
 
 template <int DV>
-__global__ void __launch_bounds__(kColThreads, 1)
+__global__ void __launch_bounds__(kThreads, 1)
     diff_col_pass(const __grid_constant__ CUtensorMap mK, const __grid_constant__ CUtensorMap mV,
                   const __grid_constant__ CUtensorMap mQ, const __grid_constant__ CUtensorMap mDO,
                   ColParams prm) {
@@ -754,18 +714,15 @@ __global__ void __launch_bounds__(kColThreads, 1)
     return;
   }
   uint64_t* kv_full = reinterpret_cast<uint64_t*>(smem + C::OFF_MISC);
-  uint64_t* q_full = kv_full + 1;          // [QS]
-  uint64_t* q_empty = q_full + C::QS;      // [QS]
-  uint64_t* do_full = q_empty + C::QS;     // [OS]: dO landed, scalars written
-  uint64_t* do_empty = do_full + C::OS;    // [OS]
-  uint64_t* s_full = do_empty + C::OS;     // [2]
+  uint64_t* full = kv_full + 1;            // [ST]: Q^1, Q^2, dO landed, scalars written
+  uint64_t* empty = full + C::ST;          // [ST]: the tile's last products done
+  uint64_t* s_full = empty + C::ST;        // [2]: S^T of map m in TMEM, for map 1 dP^T too
   uint64_t* ds_full = s_full + 2;          // [2]: bf16 operands written over the scores
-  uint64_t* dp_full = ds_full + 2;         // [2]
-  uint64_t* acc_done = dp_full + 2;
+  uint64_t* acc_done = ds_full + 2;
   uint64_t* drain = acc_done + 1;
-  static_assert((1 + 2 * C::QS + 2 * C::OS + 8) * 8 <= 384, "barriers end below the TMEM slot");
-  uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(smem + C::OFF_MISC + 384);
-  Abort* ab = reinterpret_cast<Abort*>(smem + C::OFF_MISC + 392);
+  static_assert((1 + 2 * C::ST + 6) * 8 <= 256, "barriers end below the TMEM slot");
+  uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(smem + C::OFF_MISC + 256);
+  Abort* ab = reinterpret_cast<Abort*>(smem + C::OFF_MISC + 264);
   float* scal = reinterpret_cast<float*>(smem + C::OFF_SC);
 
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
@@ -780,18 +737,13 @@ __global__ void __launch_bounds__(kColThreads, 1)
 
   if (threadIdx.x == 0) {
     mbar_init(kv_full, 1);
-    for (int s = 0; s < C::QS; ++s) {
-      mbar_init(q_full + s, 1);
-      mbar_init(q_empty + s, 1);
-    }
-    for (int s = 0; s < C::OS; ++s) {
-      mbar_init(do_full + s, 1);
-      mbar_init(do_empty + s, 1);
+    for (int s = 0; s < C::ST; ++s) {
+      mbar_init(full + s, 1);
+      mbar_init(empty + s, 1);
     }
     for (int m = 0; m < 2; ++m) {
       mbar_init(s_full + m, 1);
       mbar_init(ds_full + m, kWarps);
-      mbar_init(dp_full + m, 1);
     }
     mbar_init(acc_done, 1);
     mbar_init(drain, 1);
@@ -815,8 +767,7 @@ __global__ void __launch_bounds__(kColThreads, 1)
       load_tile(smem + C::OFF_K, &mK, kv_full, j0, 2 * kvh);
       load_tile(smem + C::OFF_K + C::KB, &mK, kv_full, j0, 2 * kvh + 1);
     }
-    // dO tiles and the row scalars; the next tile's scalars are fetched into
-    // registers one tile ahead
+    // the next tile's row scalars are fetched into registers one tile ahead
     constexpr int PER = C::BN / 32;
     float pre[5][PER];
     auto fetch = [&](int bh, int q0) {
@@ -837,21 +788,24 @@ __global__ void __launch_bounds__(kColThreads, 1)
     fetch(bh0, qstart);
     int issued = 0;
     for (int a = 0; a < T; ++a) {
-      const int os = a % C::OS, q0 = qstart + t * C::BN, bh = bh0 + g;
-      if (a >= C::OS && !await(do_empty + os, ((a / C::OS) - 1) & 1, ab, prm.status)) break;
+      const int st = a % C::ST, q0 = qstart + t * C::BN, bh = bh0 + g;
+      if (a >= C::ST && !await(empty + st, ((a / C::ST) - 1) & 1, ab, prm.status)) break;
       // the stage's scalars were last read by the elementwise warps of tile
-      // a - OS, before the dV product that freed the stage
-      float* sc = scal + os * 5 * C::BN;
+      // a - ST, before the products that freed the stage
+      float* sc = scal + st * 5 * C::BN;
 #pragma unroll
       for (int x = 0; x < 5; ++x)
 #pragma unroll
         for (int e = 0; e < PER; ++e) sc[x * C::BN + lane + 32 * e] = pre[x][e];
       __syncwarp();
       if (lane == 0) {
-        mbar_arrive_expect_tx(do_full + os, C::OB);
-        load_tile(smem + C::OFF_DO + os * C::OB, &mDO, do_full + os, q0, bh);
-        ++issued;
+        uint8_t* dst = smem + C::OFF_T + st * C::STB;
+        mbar_arrive_expect_tx(full + st, C::STB);
+        load_tile(dst, &mQ, full + st, q0, 2 * bh);
+        load_tile(dst + C::QB, &mQ, full + st, q0, 2 * bh + 1);
+        load_tile(dst + 2 * C::QB, &mDO, full + st, q0, bh);
       }
+      ++issued;
       if (++t == Tq) {
         t = 0;
         ++g;
@@ -860,89 +814,67 @@ __global__ void __launch_bounds__(kColThreads, 1)
     }
     if (lane == 0) {
       mbar_wait_bounded(kv_full, 0, prm.status, kDrainNs);
-      for (int a = max(0, issued - C::OS); a < issued; ++a)
-        mbar_wait_bounded(do_full + (a % C::OS), (a / C::OS) & 1, prm.status, kDrainNs);
-    }
-  } else if (warp == kQueryWarp) {
-    // Q subtiles, in a warp of their own: behind the dO loads in one warp, each
-    // ring would run only as far ahead as the other lets it
-    if (lane == 0) {
-      int g = 0, t = 0, issued = 0;
-      bool ok = true;
-      for (int a = 0; ok && a < T; ++a) {
-        for (int m = 0; m < 2; ++m) {
-          const int u = 2 * a + m, s = u % C::QS;
-          if (u >= C::QS && !wait_bar(q_empty + s, ((u / C::QS) - 1) & 1, ab, prm.status)) {
-            ok = false;
-            break;
-          }
-          mbar_arrive_expect_tx(q_full + s, C::QB);
-          load_tile(smem + C::OFF_Q + s * C::QB, &mQ, q_full + s, qstart + t * C::BN, 2 * (bh0 + g) + m);
-          ++issued;
-        }
-        if (++t == Tq) {
-          t = 0;
-          ++g;
-        }
-      }
-      for (int u = max(0, issued - C::QS); u < issued; ++u)
-        mbar_wait_bounded(q_full + (u % C::QS), (u / C::QS) & 1, prm.status, kDrainNs);
+      for (int a = max(0, issued - C::ST); a < issued; ++a)
+        mbar_wait_bounded(full + (a % C::ST), (a / C::ST) & 1, prm.status, kDrainNs);
     }
   } else if (warp == kMmaWarp) {
     constexpr uint32_t id_s = idesc_bf16(128, C::BN, false, false);  // S^T and dP^T
     constexpr uint32_t id_k = idesc_bf16(128, kD, false, true);      // dK += dS^T Q
     constexpr uint32_t id_v = idesc_bf16(128, DV, false, true);      // dV += W^T dO
-    auto issue_dp = [&](int a) -> bool {
-      const int os = a % C::OS;
-      if (!await(do_full + os, (a / C::OS) & 1, ab, prm.status)) return false;
-      tc_fence_after();
-      const uint32_t v_lo = opaque(lo_kmajor(sb + C::OFF_V));
-      const uint32_t do_lo = opaque(lo_kmajor(sb + C::OFF_DO + os * C::OB));
-#pragma unroll
-      for (int k = 0; k < DV / 16; ++k)
-        mma_ss_w(tmem + C::T_DP(a & 1), v_lo + kslice_off(C::BM, k), do_lo + kslice_off(C::BN, k),
-                 id_s, k > 0 ? 1u : 0u);
-      mma_commit_w(dp_full + (a & 1));
-      return true;
-    };
-    auto issue_s = [&](int u) -> bool {
-      const int s = u % C::QS, m = u & 1;
-      if (!await(q_full + s, (u / C::QS) & 1, ab, prm.status)) return false;
-      tc_fence_after();
+    auto tile = [&](int a) { return sb + C::OFF_T + (uint32_t)(a % C::ST) * C::STB; };
+    auto ready = [&](int a) { return await(full + a % C::ST, (a / C::ST) & 1, ab, prm.status); };
+    auto s_cols = [&](int a, int m) { return tmem + (m == 0 ? C::T_S1 : C::T_S2(a & 1)); };
+    auto issue_s = [&](int a, int m) {
       const uint32_t k_lo = opaque(lo_kmajor(sb + C::OFF_K + m * C::KB));
-      const uint32_t q_lo = opaque(lo_kmajor(sb + C::OFF_Q + s * C::QB));
+      const uint32_t q_lo = opaque(lo_kmajor(tile(a) + m * C::QB));
 #pragma unroll
       for (int k = 0; k < kD / 16; ++k)
-        mma_ss_w(tmem + C::T_S(m), k_lo + kslice_off(C::BM, k), q_lo + kslice_off(C::BN, k), id_s,
+        mma_ss_w(s_cols(a, m), k_lo + kslice_off(C::BM, k), q_lo + kslice_off(C::BN, k), id_s,
                  k > 0 ? 1u : 0u);
-      mma_commit_w(s_full + m);
-      return true;
     };
-    const int U = 2 * T;
-    bool ok = await(kv_full, 0, ab, prm.status) && issue_dp(0) && issue_s(0);
-    for (int u = 0; ok && u < U; ++u) {
-      const int m = u & 1, a = u >> 1, s = u % C::QS, os = a % C::OS;
-      // the next subtile's scores go over the operands of subtile u - 1, whose
-      // products were issued before; the next tile's dP^T into the buffer of
-      // tile a - 1, read out before those operands were written
-      if (u + 1 < U && !issue_s(u + 1)) { ok = false; break; }
-      if (m == 0 && a + 1 < T && !issue_dp(a + 1)) { ok = false; break; }
-      if (!await(ds_full + m, a & 1, ab, prm.status)) { ok = false; break; }
-      tc_fence_after();
-      const uint32_t first = a > 0 ? 1u : 0u;
-      const uint32_t t_a = tmem + C::T_S(m);
-      const uint32_t q_mn = opaque(lo_mnmajor(sb + C::OFF_Q + s * C::QB, C::BN * 128));
+    // the three score blocks of tile a
+    auto issue_scores = [&](int a) {
+      issue_s(a, 0);
+      const uint32_t v_lo = opaque(lo_kmajor(sb + C::OFF_V));
+      const uint32_t do_lo = opaque(lo_kmajor(tile(a) + 2 * C::QB));
+#pragma unroll
+      for (int k = 0; k < DV / 16; ++k)
+        mma_ss_w(tmem + C::T_DP, v_lo + kslice_off(C::BM, k), do_lo + kslice_off(C::BN, k), id_s,
+                 k > 0 ? 1u : 0u);
+      mma_commit_w(s_full);
+      issue_s(a, 1);
+      mma_commit_w(s_full + 1);
+    };
+    // dK^m += dS^m^T Q^m
+    auto issue_dk = [&](int a, int m) {
+      const uint32_t t_a = s_cols(a, m);
+      const uint32_t q_mn = opaque(lo_mnmajor(tile(a) + m * C::QB, C::BN * 128));
 #pragma unroll
       for (int k = 0; k < C::BN / 16; ++k)
-        mma_ts_w(tmem + C::T_DK(m), t_a + 16 * k + 8, q_mn + kstep_off(k), id_k, k > 0 ? 1u : first);
-      mma_commit_w(q_empty + s);
-      if (m == 1) {
-        const uint32_t do_mn = opaque(lo_mnmajor(sb + C::OFF_DO + os * C::OB, C::BN * 128));
+        mma_ts_w(tmem + C::T_DK(m), t_a + 16 * k + 8, q_mn + kstep_off(k), id_k, (a > 0 || k > 0) ? 1u : 0u);
+    };
+    bool ok = await(kv_full, 0, ab, prm.status) && ready(0);
+    tc_fence_after();
+    if (ok) issue_scores(0);
+    for (int a = 0; ok && a < T; ++a) {
+      const bool more = a + 1 < T;
+      ok = (!more || ready(a + 1)) && await(ds_full, a & 1, ab, prm.status);
+      if (!ok) break;
+      tc_fence_after();
+      // dK^1, then the next tile's scores: S^T of map 1 over the dS^T that
+      // product read, dP^T over the one every thread took into registers, S^T
+      // of map 2 over the operands of tile a - 1
+      issue_dk(a, 0);
+      if (more) issue_scores(a + 1);
+      if (!await(ds_full + 1, a & 1, ab, prm.status)) { ok = false; break; }
+      tc_fence_after();
+      issue_dk(a, 1);
+      const uint32_t do_mn = opaque(lo_mnmajor(tile(a) + 2 * C::QB, C::BN * 128));
 #pragma unroll
-        for (int k = 0; k < C::BN / 16; ++k)
-          mma_ts_w(tmem + C::T_DV, t_a + 16 * k, do_mn + kstep_off(k), id_v, k > 0 ? 1u : first);
-        mma_commit_w(do_empty + os);
-      }
+      for (int k = 0; k < C::BN / 16; ++k)
+        mma_ts_w(tmem + C::T_DV, s_cols(a, 1) + 16 * k, do_mn + kstep_off(k), id_v,
+                 (a > 0 || k > 0) ? 1u : 0u);
+      mma_commit_w(empty + a % C::ST);
     }
     if (ok) mma_commit_w(acc_done);
     mma_commit_w(drain);
@@ -959,23 +891,22 @@ __global__ void __launch_bounds__(kColThreads, 1)
     bool ok = true;
     int t = 0;
     for (int a = 0; ok && a < T; ++a) {
-      const int os = a % C::OS;
+      const int st = a % C::ST;
       const int qa = qstart + t * C::BN + NC * slice;
       if (++t == Tq) t = 0;
       const bool need_mask = (qa + NC > N) || (prm.causal && qa < j0 + 32 * quad + 31);
-      const float4* sc4 = reinterpret_cast<const float4*>(scal + os * 5 * C::BN + NC * slice);
-      if (!await(do_full + os, (a / C::OS) & 1, ab, prm.status)) { ok = false; break; }
+      const float4* sc4 = reinterpret_cast<const float4*>(scal + st * 5 * C::BN + NC * slice);
+      if (!await(full + st, (a / C::ST) & 1, ab, prm.status)) { ok = false; break; }
       uint32_t dp[NC];
       float p1[NC];
 #pragma unroll
       for (int m = 0; m < 2; ++m) {
         if (!ok) break;
         if (!await(s_full + m, a & 1, ab, prm.status)) { ok = false; break; }
-        if (m == 0 && !await(dp_full + (a & 1), (a >> 1) & 1, ab, prm.status)) { ok = false; break; }
         tc_fence_after();
-        const uint32_t ts = tmem + lane_off + C::T_S(m) + NC * slice;
+        const uint32_t ts = tmem + lane_off + (m == 0 ? C::T_S1 : C::T_S2(a & 1)) + NC * slice;
         uint32_t sr[NC];
-        if (m == 0) tmem_ld16x2(ts, tmem + lane_off + C::T_DP(a & 1) + NC * slice, sr, dp);
+        if (m == 0) tmem_ld16x2(ts, tmem + lane_off + C::T_DP + NC * slice, sr, dp);
         else tmem_ld16(ts, sr);
         uint32_t dsw[NC / 2], ww[NC / 2];
         auto body = [&](auto masked) {
@@ -1118,7 +1049,7 @@ cudaError_t backward_dv(const DiffProblem& p, const DiffTensors& t, const DiffWo
   c.dv = static_cast<__nv_bfloat16*>(t.dv);
   c.lse = t.lse;
   c.D = ws.D;
-  return run(diff_col_pass<DV>, c.units, p.N, kColThreads, Col<DV>::SMEM, log, c, mK, mV, sQ, sDO);
+  return run(diff_col_pass<DV>, c.units, p.N, kThreads, Col<DV>::SMEM, log, c, mK, mV, sQ, sDO);
 }
 
 }  // namespace
