@@ -85,9 +85,9 @@ _SIGNATURES = {
     "fbob_set_wait_limit": (ctypes.c_longlong, [ctypes.c_longlong]),
     "fbob_diff_workspace_size": (_SZ, [ctypes.c_int, _DSHP]),
     "fbob_diff_path": (ctypes.c_int, [ctypes.c_int, _DSHP]),
-    "fbob_diff_forward": (ctypes.c_int, [_DSHP] + [_P] * 8 + [_SZ, _P]),
-    "fbob_diff_backward": (ctypes.c_int, [_DSHP] + [_P] * 13 + [_SZ, _P]),
-    "fbob_rotary": (ctypes.c_int, [ctypes.POINTER(Rotary), _P, _P, _P, _P, _P]),
+    "fbob_diff_forward": (ctypes.c_int, [_P] * 9 + [_SZ, _P]),
+    "fbob_diff_backward": (ctypes.c_int, [_P] * 14 + [_SZ, _P]),
+    "fbob_rotary": (ctypes.c_int, [_P] * 6),
 }
 
 
@@ -159,20 +159,18 @@ def _stream(device) -> ctypes.c_void_p:
     return ctypes.c_void_p(torch.cuda.current_stream(device).cuda_stream)
 
 
-class on_device:
-    """Makes ``device`` current for a block; costs nothing where it already is."""
-
-    def __init__(self, device):
-        self.guard = (None if torch.cuda.current_device() == device.index
-                      else torch.cuda.device(device))
-
-    def __enter__(self):
-        if self.guard is not None:
-            self.guard.__enter__()
-
-    def __exit__(self, *exc):
-        if self.guard is not None:
-            self.guard.__exit__(*exc)
+def call_on(device, what: str, fn, *args) -> None:
+    """fn(*args, the device's current stream) with ``device`` current, its
+    status code checked.  Kernel launches need the stream's device to be the
+    current one."""
+    i = device.index
+    if i == torch.cuda.current_device():
+        code = fn(*args, torch._C._cuda_getCurrentRawStream(i))
+    else:
+        with torch.cuda.device(device):
+            code = fn(*args, torch._C._cuda_getCurrentRawStream(i))
+    if code:
+        _check(code, what)
 
 
 def workspace_size(op: int, shape: Shape) -> int:

@@ -54,14 +54,14 @@ int choose_path(const DiffProblem& p) {
   return tc ? FBOB_PATH_TCGEN05 : FBOB_PATH_SIMT;
 }
 
-// [status 256 B][D: B*2H*N fp32][d2: B*H*N fp32][partial: B*H fp32], each
-// region aligned
-size_t carve(int op, const DiffProblem& p, char* base, DiffWorkspace* ws) {
+// [status 256 B][D: B*2H*N fp32, or the tensor cores' row scalars][d2: B*H*N
+// fp32][partial: B*H fp32], each region aligned
+size_t carve(int op, const DiffProblem& p, int path, char* base, DiffWorkspace* ws) {
   size_t off = kAlign;
   if (ws) ws->status = reinterpret_cast<int*>(base);
   if (op == FBOB_OP_BACKWARD) {
-    if (ws) ws->D = reinterpret_cast<float*>(base + off);
-    off += align_up(2 * p.rows() * sizeof(float));
+    if (ws) ws->D = ws->scal = reinterpret_cast<float*>(base + off);
+    off += align_up((path == FBOB_PATH_TCGEN05 ? diff_tc_scalar_count(p) : 2 * p.rows()) * sizeof(float));
     if (ws) ws->d2 = reinterpret_cast<float*>(base + off);
     off += align_up(p.rows() * sizeof(float));
     if (ws) ws->partial = reinterpret_cast<float*>(base + off);
@@ -186,7 +186,7 @@ int prologue(int op, const fbob_diff_shape_t* shape, void* ws_ptr, size_t ws_byt
   *path = choose_path(*p);
   if (*path < 0) return FBOB_ERR_UNSUPPORTED;
   if (!ws_ptr || !aligned(ws_ptr, 16)) return FBOB_ERR_INVALID_ARG;
-  if (ws_bytes < carve(op, *p, static_cast<char*>(ws_ptr), ws)) return FBOB_ERR_WORKSPACE;
+  if (ws_bytes < carve(op, *p, *path, static_cast<char*>(ws_ptr), ws)) return FBOB_ERR_WORKSPACE;
   return cudaMemsetAsync(ws->status, 0, sizeof(int), stream) == cudaSuccess ? FBOB_OK : FBOB_ERR_CUDA;
 }
 
@@ -200,8 +200,9 @@ extern "C" {
 size_t fbob_diff_workspace_size(int op, const fbob_diff_shape_t* shape) {
   DiffProblem p;
   if (op != FBOB_OP_FORWARD && op != FBOB_OP_BACKWARD) return 0;
-  if (check_shape(shape, &p) != FBOB_OK || choose_path(p) < 0) return 0;
-  return carve(op, p, nullptr, nullptr);
+  if (check_shape(shape, &p) != FBOB_OK) return 0;
+  const int path = choose_path(p);
+  return path < 0 ? 0 : carve(op, p, path, nullptr, nullptr);
 }
 
 int fbob_diff_path(int op, const fbob_diff_shape_t* shape) {
@@ -253,10 +254,13 @@ int fbob_diff_backward(const fbob_diff_shape_t* shape, const void* q, const void
   t.dq = dq; t.dk = dk; t.dv = dv;
   t.lam = LamArg{lam, p.lam_kind, p.lam_bf16};
   begin_call(log);
-  cudaError_t e = p.bf16 ? row_scalars<__nv_bfloat16>(p, t, ws, log)
-                         : row_scalars<float>(p, t, ws, log);
-  if (e == cudaSuccess)
-    e = path == FBOB_PATH_TCGEN05 ? diff_tc_backward(p, t, ws, log) : diff_simt_backward(p, t, ws, log);
+  cudaError_t e;
+  if (path == FBOB_PATH_TCGEN05) {
+    e = diff_tc_backward(p, t, ws, log);
+  } else {
+    e = p.bf16 ? row_scalars<__nv_bfloat16>(p, t, ws, log) : row_scalars<float>(p, t, ws, log);
+    if (e == cudaSuccess) e = diff_simt_backward(p, t, ws, log);
+  }
   if (e == cudaSuccess) e = lam_gradient(p, ws, dlam, log);
   end_call(log);
   return e == cudaSuccess ? FBOB_OK : FBOB_ERR_CUDA;

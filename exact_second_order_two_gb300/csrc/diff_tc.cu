@@ -109,6 +109,25 @@ __device__ __forceinline__ void warp_arrive(uint64_t* bar) {
   if ((threadIdx.x & 31) == 0) mbar_arrive(bar);
 }
 
+// Row scalars of the backward, in blocks of 64 rows so that a query tile's are
+// one copy: [B H][ceil(N / 64)][5][64] fp32 of
+//   -LSE^1 log2 e, -LSE^2 log2 e, -D^1, -lam, lam D^2   (rows past N: zero)
+// P^m = 2^(S^m c log2 e - LSE^m log2 e), dS^1 = P^1 (dP - D^1) and
+// dS^2 = P^2 (-lam dP + lam D^2) take them as they are.
+__host__ __device__ __forceinline__ size_t scal_offset(int bh, int N, int n) {
+  return (((size_t)bh * ((N + 63) / 64) + n / 64) * 5) * 64 + n % 64;
+}
+
+// Untiled copy global -> shared (16-byte aligned, a multiple of 16 bytes),
+// counted on `bar`.
+__device__ __forceinline__ void bulk_load(void* dst, const void* src, uint32_t bytes, uint64_t* bar) {
+  asm volatile(
+      "cp.async.bulk.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1], %2, [%3];" ::"r"(
+          smem_u32(dst)),
+      "l"(__cvta_generic_to_global(src)), "r"(bytes), "r"(smem_u32(bar))
+      : "memory");
+}
+
 // 32 fp32 TMEM columns, scaled, to 32 consecutive bf16 of global memory.
 __device__ __forceinline__ void store32(__nv_bfloat16* dst, const uint32_t (&v)[32], float mul) {
   uint4* p = reinterpret_cast<uint4*>(dst);
@@ -276,6 +295,7 @@ __global__ void __launch_bounds__(kFwdThreads, 1)
           for (int k = 4 * h; k < 4 * h + 4; ++k)
             mma_ts_w(tmem + C::T_O(m), tmem + C::T_S(m) + C::p_col(k), v_mn + kstep_off(k), id_o,
                      (t > 0 || k > 0) ? 1u : 0u);
+          // (waited for with products in the pipe, which cover it)
         }
         if (!ok) break;
         if (m == 1) mma_commit_w(empty + t % C::ST);
@@ -416,6 +436,77 @@ __global__ void __launch_bounds__(kFwdThreads, 1)
 }
 
 // ===========================================================================
+// Row scalars: D^2 = dO . O^2, D^1 = dO . O + lam D^2 (O = O^1 - lam O^2)
+// ===========================================================================
+// acc + the dot product of 8 bf16 pairs, in fp32
+__device__ __forceinline__ float dot8(const uint4& a, const uint4& b, float acc) {
+  const __nv_bfloat162* x = reinterpret_cast<const __nv_bfloat162*>(&a);
+  const __nv_bfloat162* y = reinterpret_cast<const __nv_bfloat162*>(&b);
+#pragma unroll
+  for (int e = 0; e < 4; ++e) {
+    const float2 u = __bfloat1622float2(x[e]), v = __bfloat1622float2(y[e]);
+    acc = fmaf(u.x, v.x, fmaf(u.y, v.y, acc));
+  }
+  return acc;
+}
+
+// DV/8 lanes per row, 16 bytes of each tensor per lane; a block takes 64 rows
+// of one head.  Bound: memory (O, O^2 and dO read once).
+template <int DV>
+__global__ void __launch_bounds__(256, 4)
+    diff_tc_scalars(const uint4* __restrict__ o, const uint4* __restrict__ o2,
+                    const uint4* __restrict__ dO, const float* __restrict__ lse, LamArg lam,
+                    float* __restrict__ scal, int H, int N) {
+  constexpr int L = DV / 8, ROWS = 256 / L, STEPS = 64 / ROWS;
+  __shared__ float dots[2][64];
+  const int nb = (N + 63) / 64;
+  const int bh = blockIdx.x / nb, n0 = (blockIdx.x % nb) * 64;
+  const int sub = threadIdx.x / L, c = threadIdx.x % L;
+  // thread e < 64 writes the scalars of row n0 + e: fetched ahead
+  const int n = n0 + threadIdx.x;
+  float l1 = 0.f, l2 = 0.f, w = 0.f;
+  if (threadIdx.x < 64 && n < N) {
+    l1 = lse[(size_t)bh * 2 * N + n];
+    l2 = lse[((size_t)bh * 2 + 1) * N + n];
+    w = lam_row(lam, bh, H, N, n);
+  }
+  float s1[STEPS], s2[STEPS];
+#pragma unroll
+  for (int i = 0; i < STEPS; ++i) {
+    const int r = i * ROWS + sub;
+    s1[i] = s2[i] = 0.f;
+    if (n0 + r < N) {
+      const size_t e = ((size_t)bh * N + n0 + r) * L + c;
+      const uint4 g = dO[e];
+      s1[i] = dot8(o[e], g, 0.f);
+      s2[i] = dot8(o2[e], g, 0.f);
+    }
+  }
+#pragma unroll
+  for (int i = 0; i < STEPS; ++i) {
+#pragma unroll
+    for (int x = L / 2; x > 0; x >>= 1) {
+      s1[i] += __shfl_xor_sync(0xffffffffu, s1[i], x);
+      s2[i] += __shfl_xor_sync(0xffffffffu, s2[i], x);
+    }
+    if (c == 0) {
+      dots[0][i * ROWS + sub] = s1[i];
+      dots[1][i * ROWS + sub] = s2[i];
+    }
+  }
+  __syncthreads();
+  if (threadIdx.x < 64) {
+    float* dst = scal + scal_offset(bh, N, n0) + threadIdx.x;
+    const float d1 = dots[0][threadIdx.x], d2 = dots[1][threadIdx.x];
+    dst[0 * 64] = -l1 * kLog2e;
+    dst[1 * 64] = -l2 * kLog2e;
+    dst[2 * 64] = -fmaf(w, d2, d1);
+    dst[3 * 64] = -w;
+    dst[4 * 64] = w * d2;
+  }
+}
+
+// ===========================================================================
 // Row pass: dQ of both maps, and each row's sum_j P^2 dP
 // ===========================================================================
 template <int DV>
@@ -440,8 +531,8 @@ struct Row {
 
 struct RowParams : Common {
   __nv_bfloat16* dq;
-  const float *lse, *D;
-  float* d2;  // [B, H, N]: sum_j P^2_ij dP_ij
+  const float* scal;  // row scalars (diff_tc_scalars)
+  float* d2;          // [B, H, N]: sum_j P^2_ij dP_ij
 };
 
 template <int DV>
@@ -594,11 +685,10 @@ __global__ void __launch_bounds__(kThreads, 1)
     const f2 sc2_2 = {sc2, sc2};
     // dS^1 = P^1 (dP - D^1), dS^2 = P^2 (-lam dP + lam D^2): a factor and a
     // summand per map; rows past the end have Q = dO = 0 and stay zero
-    const size_t r1 = ((size_t)bh * 2) * N + (in ? i : 0), r2 = r1 + N;
-    const float w = in ? lam_row(prm.lam, bh, prm.H, N, i) : 0.f;
-    const float nl[2] = {in ? -prm.lse[r1] * kLog2e : 0.f, in ? -prm.lse[r2] * kLog2e : 0.f};
-    const float mul[2] = {1.f, -w};
-    const float add[2] = {in ? -prm.D[r1] : 0.f, in ? w * prm.D[r2] : 0.f};
+    const float* sc = prm.scal + scal_offset(bh, N, in ? i : 0);
+    const float nl[2] = {in ? sc[0] : 0.f, in ? sc[64] : 0.f};
+    const float mul[2] = {1.f, in ? sc[3 * 64] : 0.f};
+    const float add[2] = {in ? sc[2 * 64] : 0.f, in ? sc[4 * 64] : 0.f};
     f2 d2 = {0.f, 0.f};
     bool ok = true;
     for (int t = 0; ok && t < T; ++t) {
@@ -681,9 +771,9 @@ struct Col {
   static constexpr uint32_t OB = BN * DV * 2;     // streamed dO
   static constexpr uint32_t STB = 2 * QB + OB;
   static constexpr uint32_t OFF_K = 0, OFF_V = 2 * KB, OFF_T = OFF_V + VB;
-  // [ST][5][BN]: -LSE^1 log2 e, -LSE^2 log2 e, -D^1, -lam, lam D^2
+  static constexpr uint32_t SCB = 5 * BN * 4;     // its row scalars (diff_tc_scalars)
   static constexpr uint32_t OFF_SC = OFF_T + ST * STB;
-  static constexpr uint32_t OFF_MISC = OFF_SC + ST * 5 * BN * 4;
+  static constexpr uint32_t OFF_MISC = OFF_SC + ST * SCB;
   static constexpr uint32_t SMEM = OFF_MISC + 512;
   static_assert(SMEM <= 232448, "column pass shared memory budget");
   // TMEM columns: S^T of map 1, two buffers for that of map 2 (each thread's 16
@@ -698,7 +788,7 @@ struct Col {
 
 struct ColParams : Common {
   __nv_bfloat16 *dk, *dv;
-  const float *lse, *D;
+  const float* scal;  // row scalars (diff_tc_scalars)
 };
 
 template <int DV>
@@ -767,52 +857,23 @@ __global__ void __launch_bounds__(kThreads, 1)
       load_tile(smem + C::OFF_K, &mK, kv_full, j0, 2 * kvh);
       load_tile(smem + C::OFF_K + C::KB, &mK, kv_full, j0, 2 * kvh + 1);
     }
-    // the next tile's row scalars are fetched into registers one tile ahead
-    constexpr int PER = C::BN / 32;
-    float pre[5][PER];
-    auto fetch = [&](int bh, int q0) {
-#pragma unroll
-      for (int e = 0; e < PER; ++e) {
-        const int q = q0 + lane + 32 * e;
-        const bool in = q < N;
-        const size_t r1 = (size_t)bh * 2 * N + (in ? q : 0), r2 = r1 + N;
-        const float w = in ? lam_row(prm.lam, bh, prm.H, N, q) : 0.f;
-        pre[0][e] = in ? -prm.lse[r1] * kLog2e : 0.f;
-        pre[1][e] = in ? -prm.lse[r2] * kLog2e : 0.f;
-        pre[2][e] = in ? -prm.D[r1] : 0.f;
-        pre[3][e] = -w;
-        pre[4][e] = in ? w * prm.D[r2] : 0.f;
-      }
-    };
-    int g = 0, t = 0;  // tile t within head g
-    fetch(bh0, qstart);
-    int issued = 0;
-    for (int a = 0; a < T; ++a) {
-      const int st = a % C::ST, q0 = qstart + t * C::BN, bh = bh0 + g;
-      if (a >= C::ST && !await(empty + st, ((a / C::ST) - 1) & 1, ab, prm.status)) break;
-      // the stage's scalars were last read by the elementwise warps of tile
-      // a - ST, before the products that freed the stage
-      float* sc = scal + st * 5 * C::BN;
-#pragma unroll
-      for (int x = 0; x < 5; ++x)
-#pragma unroll
-        for (int e = 0; e < PER; ++e) sc[x * C::BN + lane + 32 * e] = pre[x][e];
-      __syncwarp();
-      if (lane == 0) {
+    if (lane == 0) {
+      int g = 0, t = 0, issued = 0;  // tile t within head g
+      for (int a = 0; a < T; ++a) {
+        const int st = a % C::ST, q0 = qstart + t * C::BN, bh = bh0 + g;
+        if (a >= C::ST && !wait_bar(empty + st, ((a / C::ST) - 1) & 1, ab, prm.status)) break;
         uint8_t* dst = smem + C::OFF_T + st * C::STB;
-        mbar_arrive_expect_tx(full + st, C::STB);
+        mbar_arrive_expect_tx(full + st, C::STB + C::SCB);
         load_tile(dst, &mQ, full + st, q0, 2 * bh);
         load_tile(dst + C::QB, &mQ, full + st, q0, 2 * bh + 1);
         load_tile(dst + 2 * C::QB, &mDO, full + st, q0, bh);
+        bulk_load(smem + C::OFF_SC + st * C::SCB, prm.scal + scal_offset(bh, N, q0), C::SCB, full + st);
+        ++issued;
+        if (++t == Tq) {
+          t = 0;
+          ++g;
+        }
       }
-      ++issued;
-      if (++t == Tq) {
-        t = 0;
-        ++g;
-      }
-      if (a + 1 < T) fetch(bh0 + g, qstart + t * C::BN);
-    }
-    if (lane == 0) {
       mbar_wait_bounded(kv_full, 0, prm.status, kDrainNs);
       for (int a = max(0, issued - C::ST); a < issued; ++a)
         mbar_wait_bounded(full + (a % C::ST), (a / C::ST) & 1, prm.status, kDrainNs);
@@ -1035,24 +1096,33 @@ cudaError_t backward_dv(const DiffProblem& p, const DiffTensors& t, const DiffWo
       !tiles(&mV, t.v, p, p.Hk, DV, 128) || !tiles(&mDO, t.dO, p, p.H, DV, 128) ||
       !tiles(&sQ, t.q, p, 2 * p.H, kD, 64) || !tiles(&sDO, t.dO, p, p.H, DV, 64))
     return cudaErrorInvalidValue;
+  const int blocks = (p.N + 63) / 64 * p.B * p.H;
+  diff_tc_scalars<DV><<<blocks, 256, 0, log.stream>>>(
+      static_cast<const uint4*>(t.o), static_cast<const uint4*>(t.o2),
+      static_cast<const uint4*>(t.dO), t.lse, t.lam, ws.scal, p.H, p.N);
+  cudaError_t e = cudaGetLastError();
+  log.mark();
+  if (e != cudaSuccess) return e;
   RowParams r;
   static_cast<Common&>(r) = common(p, t, ws, p.B * p.H);
   r.dq = static_cast<__nv_bfloat16*>(t.dq);
-  r.lse = t.lse;
-  r.D = ws.D;
+  r.scal = ws.scal;
   r.d2 = ws.d2;
-  cudaError_t e = run(diff_row_pass<DV>, r.units, p.N, kThreads, Row<DV>::SMEM, log, r, mQ, mK, mV, mDO);
+  e = run(diff_row_pass<DV>, r.units, p.N, kThreads, Row<DV>::SMEM, log, r, mQ, mK, mV, mDO);
   if (e != cudaSuccess) return e;
   ColParams c;
   static_cast<Common&>(c) = common(p, t, ws, p.B * p.Hk);
   c.dk = static_cast<__nv_bfloat16*>(t.dk);
   c.dv = static_cast<__nv_bfloat16*>(t.dv);
-  c.lse = t.lse;
-  c.D = ws.D;
+  c.scal = ws.scal;
   return run(diff_col_pass<DV>, c.units, p.N, kThreads, Col<DV>::SMEM, log, c, mK, mV, sQ, sDO);
 }
 
 }  // namespace
+
+size_t diff_tc_scalar_count(const DiffProblem& p) {
+  return (size_t)p.B * p.H * ((p.N + 63) / 64) * 5 * 64;
+}
 
 bool diff_tc_supported(const DiffProblem& p) {
   return p.bf16 && p.d == kD && (p.dv == 64 || p.dv == 128);

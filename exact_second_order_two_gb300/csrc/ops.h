@@ -35,7 +35,8 @@ struct LamArg {
 
 struct DiffWorkspace {
   int* status = nullptr;
-  float* D = nullptr;        // [B, 2H, N]: D^1 and D^2 of each row
+  float* D = nullptr;        // [B, 2H, N]: D^1 and D^2 of each row (CUDA cores)
+  float* scal = nullptr;     // the row scalars' blocks (tensor cores)
   float* d2 = nullptr;       // [B, H, N]: sum_j P^2_ij dP_ij, for lam's gradient
   float* partial = nullptr;  // [B, H]: its sums
 };
@@ -56,6 +57,7 @@ cudaError_t diff_simt_backward(const DiffProblem& p, const DiffTensors& t, const
 
 // ---- tensor-core kernels: bf16, d = 64, dv = 64 or 128 ----------------------
 bool diff_tc_supported(const DiffProblem& p);
+size_t diff_tc_scalar_count(const DiffProblem& p);  // fp32 values of DiffWorkspace::scal
 cudaError_t diff_tc_forward(const DiffProblem& p, const DiffTensors& t, const DiffWorkspace& ws,
                             LaunchLog& log);
 cudaError_t diff_tc_backward(const DiffProblem& p, const DiffTensors& t, const DiffWorkspace& ws,

@@ -102,12 +102,10 @@ def diff_forward(q, k, v, lam, causal: bool = False, scale: float | None = None,
     o = torch.empty((shp.B, shp.H, shp.N, shp.dv), dtype=q.dtype, device=q.device)
     o2 = torch.empty_like(o) if need_o2 else None
     lse = torch.empty((shp.B, 2 * shp.H, shp.N), dtype=torch.float32, device=q.device)
-    with _b.on_device(q.device):
-        ws = _workspace(_b.OP_FORWARD, shp, q.device) if workspace is None else workspace
-        _b._check(_b.lib().fbob_diff_forward(
-            ctypes.byref(shp), q.data_ptr(), k.data_ptr(), v.data_ptr(), lam.data_ptr(),
-            o.data_ptr(), None if o2 is None else o2.data_ptr(), lse.data_ptr(), ws.data_ptr(),
-            ws.numel(), _b._stream(q.device)), "fbob_diff_forward")
+    ws = _workspace(_b.OP_FORWARD, shp, q.device) if workspace is None else workspace
+    _b.call_on(q.device, "fbob_diff_forward", _b.lib().fbob_diff_forward, ctypes.byref(shp),
+               q.data_ptr(), k.data_ptr(), v.data_ptr(), lam.data_ptr(), o.data_ptr(),
+               None if o2 is None else o2.data_ptr(), lse.data_ptr(), ws.data_ptr(), ws.numel())
     return o, o2, lse
 
 
@@ -121,12 +119,10 @@ def diff_backward(q, k, v, lam, o, o2, lse, do, causal: bool = False,
         _match(name, t, rows, q.dtype, q.device)
     _match("lse", lse, (shp.B, 2 * shp.H, shp.N), torch.float32, q.device)
     dq, dk, dv, dlam = (torch.empty_like(t) for t in (q, k, v, lam))
-    with _b.on_device(q.device):
-        ws = _workspace(_b.OP_BACKWARD, shp, q.device) if workspace is None else workspace
-        _b._check(_b.lib().fbob_diff_backward(
-            ctypes.byref(shp), *(t.data_ptr() for t in (q, k, v, lam, o, o2, lse, do, dq, dk, dv,
-                                                        dlam, ws)),
-            ws.numel(), _b._stream(q.device)), "fbob_diff_backward")
+    ws = _workspace(_b.OP_BACKWARD, shp, q.device) if workspace is None else workspace
+    _b.call_on(q.device, "fbob_diff_backward", _b.lib().fbob_diff_backward, ctypes.byref(shp),
+               *(t.data_ptr() for t in (q, k, v, lam, o, o2, lse, do, dq, dk, dv, dlam, ws)),
+               ws.numel())
     return dq, dk, dv, dlam
 
 
@@ -221,11 +217,10 @@ class _DiffBackward(torch.autograd.Function):
 
 class _DiffAttention(torch.autograd.Function):
     @staticmethod
-    def forward(ctx, q, k, v, lam, causal, scale, need):
-        o, o2, lse = diff_forward(q, k, v, lam, causal, scale, need_o2=need)
-        if need:
-            ctx.save_for_backward(q, k, v, lam, o, o2, lse)
-            ctx.causal, ctx.scale = causal, scale
+    def forward(ctx, q, k, v, lam, causal, scale):
+        o, o2, lse = diff_forward(q, k, v, lam, causal, scale)
+        ctx.save_for_backward(q, k, v, lam, o, o2, lse)
+        ctx.causal, ctx.scale = causal, scale
         return o
 
     @staticmethod
@@ -233,8 +228,11 @@ class _DiffAttention(torch.autograd.Function):
         q, k, v, lam, o, o2, lse = ctx.saved_tensors
         # o, o2 and lse enter as values: the second derivative's paths through
         # them are part of what fbob_bob returns
-        grads = _DiffBackward.apply(q, k, v, lam, do, o.detach(), o2, lse, ctx.causal, ctx.scale)
-        return tuple(grads) + (None, None, None)
+        if torch.is_grad_enabled():
+            grads = _DiffBackward.apply(q, k, v, lam, do, o.detach(), o2, lse, ctx.causal, ctx.scale)
+        else:
+            grads = diff_backward(q, k, v, lam, o, o2, lse, _contig(do), ctx.causal, ctx.scale)
+        return tuple(grads) + (None, None)
 
 
 def diff_attention(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, lam: torch.Tensor,
@@ -251,6 +249,8 @@ def diff_attention(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, lam: torch
     q, k, v, lam = _contig(q), _contig(k), _contig(v), _contig(lam)
     if scale is None:
         scale = 1.0 / math.sqrt(q.shape[-1])
-    # O2 is only kept (and written) where a backward can follow
-    need = torch.is_grad_enabled() and any(t.requires_grad for t in (q, k, v, lam))
-    return _DiffAttention.apply(q, k, v, lam, bool(causal), float(scale), need)
+    if torch.is_grad_enabled() and (q.requires_grad or k.requires_grad or v.requires_grad
+                                    or lam.requires_grad):
+        return _DiffAttention.apply(q, k, v, lam, bool(causal), float(scale))
+    # no backward can follow: O2 is not written
+    return diff_forward(q, k, v, lam, bool(causal), float(scale), need_o2=False)[0]

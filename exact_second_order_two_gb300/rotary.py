@@ -11,8 +11,8 @@ longer than those a model was trained on.
 """
 from __future__ import annotations
 
-import ctypes
 import math
+import struct
 
 import torch
 
@@ -67,6 +67,11 @@ def rotary_frequencies(rotary_dim: int, base: float = 10000.0, scaling: str | No
     return freq.to(device), magnitude
 
 
+# fbob_rotary_t: nine ints, the magnitude, the strides of x and y, the stride of
+# the positions' batches and the first position
+_pack = struct.Struct("@9if8q").pack
+
+
 def _turn(x, inv_freq, positions, offset, interleaved, magnitude, dtype, inverse, strides):
     """One fbob_rotary call into a new tensor (dense, or with ``strides``)."""
     if x.stride(-1) != 1 and x.shape[-1] > 1:
@@ -76,15 +81,11 @@ def _turn(x, inv_freq, positions, offset, interleaved, magnitude, dtype, inverse
         y = torch.empty((B, H, N, d), dtype=dtype, device=x.device)
     else:
         y = torch.empty_strided((B, H, N, d), strides, dtype=dtype, device=x.device)
-    xs, ys = x.stride(), y.stride()
-    r = _b.Rotary(B, H, N, d, 2 * inv_freq.numel(), int(interleaved), int(inverse),
-                  _b.DTYPES[x.dtype], _b.DTYPES[dtype], magnitude,
-                  (ctypes.c_longlong * 3)(*xs[:3]), (ctypes.c_longlong * 3)(*ys[:3]),
-                  0 if positions is None else positions.stride(0), offset)
-    with _b.on_device(x.device):
-        _b._check(_b.lib().fbob_rotary(ctypes.byref(r), x.data_ptr(), inv_freq.data_ptr(),
-                                       None if positions is None else positions.data_ptr(),
-                                       y.data_ptr(), _b._stream(x.device)), "fbob_rotary")
+    r = _pack(B, H, N, d, 2 * inv_freq.numel(), interleaved, inverse, _b.DTYPES[x.dtype],
+              _b.DTYPES[dtype], magnitude, *x.stride()[:3], *y.stride()[:3],
+              0 if positions is None else positions.stride(0), offset)
+    _b.call_on(x.device, "fbob_rotary", _b.lib().fbob_rotary, r, x.data_ptr(), inv_freq.data_ptr(),
+               None if positions is None else positions.data_ptr(), y.data_ptr())
     return y
 
 
@@ -104,8 +105,9 @@ class _Rotary(torch.autograd.Function):
     @staticmethod
     def backward(ctx, dy):
         inv_freq, positions = ctx.saved_tensors
-        dx = _Rotary.apply(dy, inv_freq, positions, *ctx.how, ctx.strides)
-        return (dx,) + (None,) * 8
+        turn = _Rotary.apply if torch.is_grad_enabled() else _turn
+        dx = turn(dy, inv_freq, positions, *ctx.how, ctx.strides)
+        return dx, None, None, None, None, None, None, None, None
 
 
 def _dense(x: torch.Tensor) -> bool:
@@ -165,5 +167,6 @@ def rotary(x: torch.Tensor, inv_freq: torch.Tensor, positions=None, *, interleav
             positions = positions.expand(B, N)
         if positions.stride(1) != 1 and N > 1:
             positions = positions.contiguous()
-    return _Rotary.apply(x, inv_freq, positions, offset, bool(interleaved), float(magnitude),
-                         dtype, False, None)
+    turn = _Rotary.apply if x.requires_grad and torch.is_grad_enabled() else _turn
+    return turn(x, inv_freq, positions, offset, bool(interleaved), float(magnitude), dtype, False,
+                None)
