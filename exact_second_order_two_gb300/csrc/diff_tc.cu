@@ -83,17 +83,20 @@ __device__ __forceinline__ float lam_row(const LamArg& l, int bh, int H, int N, 
                                                                            : (size_t)bh * N + n);
 }
 
-// Bounded, warp-uniform wait (as warp_wait) that first sleeps on the barrier
-// and only then looks at the clock: almost every wait ends in that sleep,
-// and a read of the global timer costs more than most of them last.
-__device__ __forceinline__ bool await(uint64_t* bar, uint32_t parity, Abort* ab, int* status) {
-  bool ok = mbar_try_wait(bar, parity);
-  if (!ok) {
-    const uint64_t limit = ab->limit_ns;
-    ok = mbar_try_wait_sleep(bar, parity, limit < kPollSleepNs ? (uint32_t)limit : kPollSleepNs);
-    if (!ok) ok = wait_bar(bar, parity, ab, status);
-  }
-  return __all_sync(0xffffffffu, ok);
+// Bounded wait.  It sleeps on the barrier before it looks at the clock: almost
+// every wait ends in that sleep, and a read of the global timer costs more than
+// most of them last.  A wait that runs out records the timeout and sets the
+// CTA's abort flag; it returns all the same, and so do all later waits at
+// once.  So control flow stays the same in every lane without a vote (which
+// cost 3% to 4% of each kernel), the roles run to their ends on whatever the
+// buffers hold, and only the producers stop: the call's outputs are undefined,
+// every access stays in bounds, and the CTA drains its copies and MMAs and
+// frees its TMEM as ever.
+__device__ __forceinline__ void await(uint64_t* bar, uint32_t parity, Abort* ab, int* status) {
+  if (mbar_try_wait(bar, parity) || ab->flag) return;
+  const uint64_t limit = ab->limit_ns;
+  if (mbar_try_wait_sleep(bar, parity, limit < kPollSleepNs ? (uint32_t)limit : kPollSleepNs)) return;
+  wait_bar(bar, parity, ab, status);
 }
 
 __device__ __forceinline__ float max3(float a, float b, float c) {
@@ -258,10 +261,10 @@ __global__ void __launch_bounds__(kFwdThreads, 1)
     constexpr uint32_t id_s = idesc_bf16(128, C::BN, false, false);  // S = Q K^T
     constexpr uint32_t id_o = idesc_bf16(128, DV, false, true);      // O += P V: B MN-major
     // A wait of this warp costs a few hundred cycles of a busy pipe and a commit
-    // some tens, so a tile's loads share one barrier and only what someone
-    // waits for is committed
+    // some tens.  So only what someone waits for is committed, and the loads of
+    // a tile are awaited by a softmax warp, before its arrival for the tile
+    // before (only the first tile's here).
     auto tile = [&](int t) { return sb + C::OFF_T + (uint32_t)(t % C::ST) * C::STB; };
-    auto ready = [&](int t) { return await(full + t % C::ST, (t / C::ST) & 1, ab, prm.status); };
     auto issue_s = [&](int t, int m) {
       const uint32_t q_lo = opaque(lo_kmajor(sb + C::OFF_Q + m * C::QB));
       const uint32_t k_lo = opaque(lo_kmajor(tile(t) + m * C::QB));
@@ -271,15 +274,13 @@ __global__ void __launch_bounds__(kFwdThreads, 1)
                  k > 0 ? 1u : 0u);
       mma_commit_w(s_full + m);
     };
-    bool ok = await(q_full, 0, ab, prm.status) && ready(0);
+    await(q_full, 0, ab, prm.status);
+    await(full, 0, ab, prm.status);
     tc_fence_after();
-    if (ok) {
-      issue_s(0, 0);
-      issue_s(0, 1);
-    }
-    for (int t = 0; ok && t < T; ++t) {
+    issue_s(0, 0);
+    issue_s(0, 1);
+    for (int t = 0; t < T; ++t) {
       const bool more = t + 1 < T;
-      if (more && !ready(t + 1)) { ok = false; break; }
       const uint32_t v_mn = opaque(lo_mnmajor(tile(t) + 2 * C::QB, C::BN * 128));
 #pragma unroll
       for (int m = 0; m < 2; ++m) {
@@ -288,8 +289,7 @@ __global__ void __launch_bounds__(kFwdThreads, 1)
         // whoever sees S^m of a tile may rescale O^m.
 #pragma unroll
         for (int h = 0; h < 2; ++h) {
-          if (!ok) break;
-          if (!await(p_full + 2 * m + h, t & 1, ab, prm.status)) { ok = false; break; }
+          await(p_full + 2 * m + h, t & 1, ab, prm.status);
           tc_fence_after();
 #pragma unroll
           for (int k = 4 * h; k < 4 * h + 4; ++k)
@@ -297,12 +297,11 @@ __global__ void __launch_bounds__(kFwdThreads, 1)
                      (t > 0 || k > 0) ? 1u : 0u);
           // (waited for with products in the pipe, which cover it)
         }
-        if (!ok) break;
         if (m == 1) mma_commit_w(empty + t % C::ST);
         if (more) issue_s(t + 1, m);
       }
     }
-    if (ok) mma_commit_w(o_done);
+    mma_commit_w(o_done);
     // every MMA this thread issued has completed before TMEM is released
     mma_commit_w(drain);
     mbar_wait_bounded(drain, 0, prm.status, kDrainNs);
@@ -315,12 +314,13 @@ __global__ void __launch_bounds__(kFwdThreads, 1)
     const f2 sc2_2 = {sc2, sc2};
     const uint32_t lane_off = (uint32_t)(32 * quad) << 16;
     const uint32_t ts = tmem + lane_off + C::T_S(m);
-    bool ok = true;
     // the row's reference maximum (log2 domain) and sum of 2^(S c log2 e - max)
     float mx = -INFINITY, l = 0.f;
     for (int t = 0; t < T; ++t) {
       const int j0 = t * C::BN;
-      if (!await(s_full + m, t & 1, ab, prm.status)) { ok = false; break; }
+      // for the MMA warp: the next tile has landed
+      if (warp == 0 && t + 1 < T) await(full + (t + 1) % C::ST, ((t + 1) / C::ST) & 1, ab, prm.status);
+      await(s_full + m, t & 1, ab, prm.status);
       tc_fence_after();
       uint32_t s[4][32];
       tmem_ld32x4(ts, ts + 32, ts + 64, ts + 96, s[0], s[1], s[2], s[3]);
@@ -386,46 +386,42 @@ __global__ void __launch_bounds__(kFwdThreads, 1)
       l += acc.x + acc.y;
     }
     // ---- epilogue: O = O^1 / l^1 - lam O^2 / l^2, and LSE (natural log) ----
-    // every softmax thread gets to this barrier, also after a failed wait
     red[m * 128 + row] = l;
     named_sync<kSoftmax>(1);
     const float L[2] = {red[row], red[128 + row]};
-    ok = __all_sync(0xffffffffu, ok);
-    if (ok) ok = await(o_done, 0, ab, prm.status);
+    await(o_done, 0, ab, prm.status);
     tc_fence_after();
-    if (ok) {
-      constexpr int PART = DV / 2;  // features per thread
-      const int f0 = PART * m;
-      const bool in = i < N;
-      const float inv1 = 1.f / L[0], inv2 = 1.f / L[1];
-      const float w = in ? lam_row(prm.lam, bh, prm.H, N, i) : 0.f;
-      const size_t at = ((size_t)bh * N + (in ? i : 0)) * DV + f0;
+    constexpr int PART = DV / 2;  // features per thread
+    const int f0 = PART * m;
+    const bool in = i < N;
+    const float inv1 = 1.f / L[0], inv2 = 1.f / L[1];
+    const float w = in ? lam_row(prm.lam, bh, prm.H, N, i) : 0.f;
+    const size_t at = ((size_t)bh * N + (in ? i : 0)) * DV + f0;
 #pragma unroll
-      for (int c = 0; c < PART; c += 16) {
-        uint32_t a[16], b[16];
-        tmem_ld16x2(tmem + lane_off + C::T_O(0) + f0 + c, tmem + lane_off + C::T_O(1) + f0 + c, a, b);
-        uint32_t wo[8], w2[8];
+    for (int c = 0; c < PART; c += 16) {
+      uint32_t a[16], b[16];
+      tmem_ld16x2(tmem + lane_off + C::T_O(0) + f0 + c, tmem + lane_off + C::T_O(1) + f0 + c, a, b);
+      uint32_t wo[8], w2[8];
 #pragma unroll
-        for (int e = 0; e < 8; ++e) {
-          const float x2 = __uint_as_float(b[2 * e]) * inv2, y2 = __uint_as_float(b[2 * e + 1]) * inv2;
-          wo[e] = pack_bf16(fmaf(-w, x2, __uint_as_float(a[2 * e]) * inv1),
-                            fmaf(-w, y2, __uint_as_float(a[2 * e + 1]) * inv1));
-          w2[e] = pack_bf16(x2, y2);
-        }
-        if (in) {
-          uint4* po = reinterpret_cast<uint4*>(prm.o + at + c);
-          po[0] = make_uint4(wo[0], wo[1], wo[2], wo[3]);
-          po[1] = make_uint4(wo[4], wo[5], wo[6], wo[7]);
-          if (prm.o2) {
-            uint4* p2 = reinterpret_cast<uint4*>(prm.o2 + at + c);
-            p2[0] = make_uint4(w2[0], w2[1], w2[2], w2[3]);
-            p2[1] = make_uint4(w2[4], w2[5], w2[6], w2[7]);
-          }
+      for (int e = 0; e < 8; ++e) {
+        const float x2 = __uint_as_float(b[2 * e]) * inv2, y2 = __uint_as_float(b[2 * e + 1]) * inv2;
+        wo[e] = pack_bf16(fmaf(-w, x2, __uint_as_float(a[2 * e]) * inv1),
+                          fmaf(-w, y2, __uint_as_float(a[2 * e + 1]) * inv1));
+        w2[e] = pack_bf16(x2, y2);
+      }
+      if (in) {
+        uint4* po = reinterpret_cast<uint4*>(prm.o + at + c);
+        po[0] = make_uint4(wo[0], wo[1], wo[2], wo[3]);
+        po[1] = make_uint4(wo[4], wo[5], wo[6], wo[7]);
+        if (prm.o2) {
+          uint4* p2 = reinterpret_cast<uint4*>(prm.o2 + at + c);
+          p2[0] = make_uint4(w2[0], w2[1], w2[2], w2[3]);
+          p2[1] = make_uint4(w2[4], w2[5], w2[6], w2[7]);
         }
       }
-      if (in)
-        prm.lse[((size_t)bh * 2 + m) * N + i] = (mx + log2f(m == 0 ? L[0] : L[1])) * kLn2;
     }
+    if (in)
+      prm.lse[((size_t)bh * 2 + m) * N + i] = (mx + log2f(m == 0 ? L[0] : L[1])) * kLn2;
   }
   tc_fence_before();
   __syncthreads();
@@ -622,7 +618,6 @@ __global__ void __launch_bounds__(kThreads, 1)
     constexpr uint32_t id_s = idesc_bf16(128, C::BN, false, false);  // S and dP
     constexpr uint32_t id_q = idesc_bf16(128, kD, false, true);      // dQ += dS K: B MN-major
     auto k_tile = [&](int t, int m) { return sb + C::OFF_K + (uint32_t)(2 * (t % C::KS) + m) * C::QB; };
-    auto ready = [&](int t) { return await(full + t % C::KS, (t / C::KS) & 1, ab, prm.status); };
     auto issue_s = [&](int t, int m) {
       const uint32_t q_lo = opaque(lo_kmajor(sb + C::OFF_Q + m * C::QB));
       const uint32_t k_lo = opaque(lo_kmajor(k_tile(t, m)));
@@ -651,26 +646,27 @@ __global__ void __launch_bounds__(kThreads, 1)
         mma_ts_w(tmem + C::T_DQ(m), tmem + C::T_S(m) + C::a_col(k), k_mn + kstep_off(k), id_q,
                  (t > 0 || k > 0) ? 1u : 0u);
     };
-    bool ok = await(q_full, 0, ab, prm.status) && ready(0);
+    // (the loads of later tiles are awaited by an elementwise warp)
+    await(q_full, 0, ab, prm.status);
+    await(full, 0, ab, prm.status);
     tc_fence_after();
-    if (ok) issue_first(0);
-    for (int t = 0; ok && t < T; ++t) {
+    issue_first(0);
+    for (int t = 0; t < T; ++t) {
       const bool more = t + 1 < T;
       // scores go over the dS of the tile before, whose dQ product is issued
       issue_s(t, 1);
       mma_commit_w(s_full + 1);
-      ok = (!more || ready(t + 1)) && await(ds_full, t & 1, ab, prm.status);
-      if (!ok) break;
+      await(ds_full, t & 1, ab, prm.status);
       tc_fence_after();
       issue_dq(t, 0);
       // every thread took dP into registers before it wrote dS^1
       if (more) issue_first(t + 1);
-      if (!await(ds_full + 1, t & 1, ab, prm.status)) { ok = false; break; }
+      await(ds_full + 1, t & 1, ab, prm.status);
       tc_fence_after();
       issue_dq(t, 1);
       mma_commit_w(k_empty + t % C::KS);
     }
-    if (ok) mma_commit_w(acc_done);
+    mma_commit_w(acc_done);
     mma_commit_w(drain);
     mbar_wait_bounded(drain, 0, prm.status, kDrainNs);
   } else {
@@ -690,15 +686,15 @@ __global__ void __launch_bounds__(kThreads, 1)
     const float mul[2] = {1.f, in ? sc[3 * 64] : 0.f};
     const float add[2] = {in ? sc[2 * 64] : 0.f, in ? sc[4 * 64] : 0.f};
     f2 d2 = {0.f, 0.f};
-    bool ok = true;
-    for (int t = 0; ok && t < T; ++t) {
+    for (int t = 0; t < T; ++t) {
       const int j0 = t * C::BN + NC * slice;
       const bool need_mask = (j0 + NC > N) || (prm.causal && j0 + NC - 1 > i0 + 32 * quad);
+      // for the MMA warp: the next tile has landed
+      if (warp == 0 && t + 1 < T) await(full + (t + 1) % C::KS, ((t + 1) / C::KS) & 1, ab, prm.status);
       uint32_t dp[NC];
 #pragma unroll
       for (int m = 0; m < 2; ++m) {
-        if (!ok) break;
-        if (!await(s_full + m, t & 1, ab, prm.status)) { ok = false; break; }
+        await(s_full + m, t & 1, ab, prm.status);
         tc_fence_after();
         const uint32_t ts = tmem + lane_off + C::T_S(m) + NC * slice;
         uint32_t sr[NC];
@@ -732,21 +728,18 @@ __global__ void __launch_bounds__(kThreads, 1)
     // ---- epilogue: dQ (scaled): 32 features of one map per thread ----
     red[slice * 128 + row] = d2.x + d2.y;
     named_sync<kConsumers>(1);
-    ok = __all_sync(0xffffffffu, ok);
-    if (ok) ok = await(acc_done, 0, ab, prm.status);
+    await(acc_done, 0, ab, prm.status);
     tc_fence_after();
-    if (ok) {
-      const int m = slice >> 1, f = 32 * (slice & 1);
-      uint32_t v[32];
-      tmem_ld32(tmem + lane_off + C::T_DQ(0) + kD * m + f, v);
-      if (in) {
-        store32(prm.dq + (((size_t)bh * 2 + m) * N + i) * kD + f, v, prm.scale);
-        if (slice == 0) {
-          float s = 0.f;
+    const int m = slice >> 1, f = 32 * (slice & 1);
+    uint32_t v[32];
+    tmem_ld32(tmem + lane_off + C::T_DQ(0) + kD * m + f, v);
+    if (in) {
+      store32(prm.dq + (((size_t)bh * 2 + m) * N + i) * kD + f, v, prm.scale);
+      if (slice == 0) {
+        float s = 0.f;
 #pragma unroll
-          for (int u = 0; u < kRowSlices; ++u) s += red[u * 128 + row];
-          prm.d2[(size_t)bh * N + i] = s;
-        }
+        for (int u = 0; u < kRowSlices; ++u) s += red[u * 128 + row];
+        prm.d2[(size_t)bh * N + i] = s;
       }
     }
   }
@@ -883,7 +876,6 @@ __global__ void __launch_bounds__(kThreads, 1)
     constexpr uint32_t id_k = idesc_bf16(128, kD, false, true);      // dK += dS^T Q
     constexpr uint32_t id_v = idesc_bf16(128, DV, false, true);      // dV += W^T dO
     auto tile = [&](int a) { return sb + C::OFF_T + (uint32_t)(a % C::ST) * C::STB; };
-    auto ready = [&](int a) { return await(full + a % C::ST, (a / C::ST) & 1, ab, prm.status); };
     auto s_cols = [&](int a, int m) { return tmem + (m == 0 ? C::T_S1 : C::T_S2(a & 1)); };
     auto issue_s = [&](int a, int m) {
       const uint32_t k_lo = opaque(lo_kmajor(sb + C::OFF_K + m * C::KB));
@@ -914,20 +906,21 @@ __global__ void __launch_bounds__(kThreads, 1)
       for (int k = 0; k < C::BN / 16; ++k)
         mma_ts_w(tmem + C::T_DK(m), t_a + 16 * k + 8, q_mn + kstep_off(k), id_k, (a > 0 || k > 0) ? 1u : 0u);
     };
-    bool ok = await(kv_full, 0, ab, prm.status) && ready(0);
+    // (the loads of later tiles are awaited by the elementwise warps)
+    await(kv_full, 0, ab, prm.status);
+    await(full, 0, ab, prm.status);
     tc_fence_after();
-    if (ok) issue_scores(0);
-    for (int a = 0; ok && a < T; ++a) {
+    issue_scores(0);
+    for (int a = 0; a < T; ++a) {
       const bool more = a + 1 < T;
-      ok = (!more || ready(a + 1)) && await(ds_full, a & 1, ab, prm.status);
-      if (!ok) break;
+      await(ds_full, a & 1, ab, prm.status);
       tc_fence_after();
       // dK^1, then the next tile's scores: S^T of map 1 over the dS^T that
       // product read, dP^T over the one every thread took into registers, S^T
       // of map 2 over the operands of tile a - 1
       issue_dk(a, 0);
       if (more) issue_scores(a + 1);
-      if (!await(ds_full + 1, a & 1, ab, prm.status)) { ok = false; break; }
+      await(ds_full + 1, a & 1, ab, prm.status);
       tc_fence_after();
       issue_dk(a, 1);
       const uint32_t do_mn = opaque(lo_mnmajor(tile(a) + 2 * C::QB, C::BN * 128));
@@ -937,7 +930,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                  (a > 0 || k > 0) ? 1u : 0u);
       mma_commit_w(empty + a % C::ST);
     }
-    if (ok) mma_commit_w(acc_done);
+    mma_commit_w(acc_done);
     mma_commit_w(drain);
     mbar_wait_bounded(drain, 0, prm.status, kDrainNs);
   } else {
@@ -949,21 +942,21 @@ __global__ void __launch_bounds__(kThreads, 1)
     const uint32_t lane_off = (uint32_t)(32 * quad) << 16;
     const float sc2 = prm.scale * kLog2e;
     const f2 sc2_2 = {sc2, sc2};
-    bool ok = true;
     int t = 0;
-    for (int a = 0; ok && a < T; ++a) {
+    for (int a = 0; a < T; ++a) {
       const int st = a % C::ST;
       const int qa = qstart + t * C::BN + NC * slice;
       if (++t == Tq) t = 0;
       const bool need_mask = (qa + NC > N) || (prm.causal && qa < j0 + 32 * quad + 31);
       const float4* sc4 = reinterpret_cast<const float4*>(scal + st * 5 * C::BN + NC * slice);
-      if (!await(full + st, (a / C::ST) & 1, ab, prm.status)) { ok = false; break; }
+      // this tile's scalars (already there), and for the MMA warp the next tile
+      if (a == 0) await(full, 0, ab, prm.status);
+      if (a + 1 < T) await(full + (a + 1) % C::ST, ((a + 1) / C::ST) & 1, ab, prm.status);
       uint32_t dp[NC];
       float p1[NC];
 #pragma unroll
       for (int m = 0; m < 2; ++m) {
-        if (!ok) break;
-        if (!await(s_full + m, a & 1, ab, prm.status)) { ok = false; break; }
+        await(s_full + m, a & 1, ab, prm.status);
         tc_fence_after();
         const uint32_t ts = tmem + lane_off + (m == 0 ? C::T_S1 : C::T_S2(a & 1)) + NC * slice;
         uint32_t sr[NC];
@@ -1012,18 +1005,15 @@ __global__ void __launch_bounds__(kThreads, 1)
       }
     }
     // ---- epilogue: dK (scaled), 32 features of one map per thread, and dV ----
-    ok = __all_sync(0xffffffffu, ok);
-    if (ok) ok = await(acc_done, 0, ab, prm.status);
+    await(acc_done, 0, ab, prm.status);
     tc_fence_after();
-    if (ok) {
-      const int m = slice >> 1, f = 32 * (slice & 1);
-      uint32_t v[32];
-      tmem_ld32(tmem + lane_off + C::T_DK(0) + kD * m + f, v);
-      if (j < N) store32(prm.dk + (((size_t)kvh * 2 + m) * N + j) * kD + f, v, prm.scale);
-      if (DV == 128 || slice < 2) {
-        tmem_ld32(tmem + lane_off + C::T_DV + 32 * slice, v);
-        if (j < N) store32(prm.dv + ((size_t)kvh * N + j) * DV + 32 * slice, v, 1.f);
-      }
+    const int m = slice >> 1, f = 32 * (slice & 1);
+    uint32_t v[32];
+    tmem_ld32(tmem + lane_off + C::T_DK(0) + kD * m + f, v);
+    if (j < N) store32(prm.dk + (((size_t)kvh * 2 + m) * N + j) * kD + f, v, prm.scale);
+    if (DV == 128 || slice < 2) {
+      tmem_ld32(tmem + lane_off + C::T_DV + 32 * slice, v);
+      if (j < N) store32(prm.dv + ((size_t)kvh * N + j) * DV + 32 * slice, v, 1.f);
     }
   }
   tc_fence_before();
