@@ -5,14 +5,16 @@
 //   dS^2 = -lam P^2*(dP - D^2), dQ^m = c dS^m K^m, dK^m = c dS^mT Q^m,
 //   dV = (P^1 - lam P^2)^T dO, dlam_i = -sum_j P^2_ij dP_ij.
 //
-// Arithmetic is fp32 throughout.  A block of 16 x 16 threads holds a 64-row
+// Arithmetic is fp32 throughout.  A block of 8 x 16 threads holds a 32-row
 // tile (queries, or keys for dK and dV) and streams 64-row tiles of the other
 // side through shared memory; thread (ty, tx) computes the 4 x 4 scores of
 // rows 4 ty.. and columns tx + 16 j.  A row of scores lives in 16 lanes of one
 // warp, so row maxima and sums are shuffles, and the probabilities pass to
 // their product through shared memory inside the warp.  Bound: FFMA issue,
-// at 8 FFMA per 16-byte shared-memory read.  Everything a row or key
-// accumulates is summed by one block in a fixed order.
+// at 8 FFMA per 16-byte shared-memory read.  Two blocks share an SM at
+// d = 64, dv = 128, so one computes while the other loads, and short
+// sequences still give many blocks.  Everything a row or key accumulates is
+// summed by one block in a fixed order.
 #include <cuda_bf16.h>
 #include <math.h>
 
@@ -23,8 +25,9 @@
 namespace fbob {
 namespace {
 
-constexpr int kT = 64;       // rows of a tile
-constexpr int kThreads = 256;
+constexpr int kM = 32;       // rows of the stationary tile
+constexpr int kT = 64;       // rows of a streamed tile
+constexpr int kThreads = 128;
 constexpr int kLdp = kT + 4;  // row stride of the score tile
 
 // Row stride of a [64][width] tile in floats: whole 16-byte steps, and rows
@@ -42,6 +45,7 @@ struct Args {
   float* d2;
   LamArg lam;
   int H, G, N, d, dv_, causal;
+  int heads;  // of the grid: B H, or B Hk
   float scale;
 };
 
@@ -51,36 +55,61 @@ __device__ __forceinline__ float lam_at(const LamArg& l, int H, int N, int b, in
                 : static_cast<const float*>(l.p)[i];
 }
 
-// Rows row0.. of src [rows][width] into dst [64][ld]; rows past N and the
-// columns up to the next multiple of four read as zero.
-template <typename T>
+// Rows row0.. of src [N][width] into dst [ROWS][ld]; rows past N and the
+// columns up to the next multiple of four read as zero.  fp32 rows of whole
+// 16-byte steps go by asynchronous copies, which the caller awaits
+// (loads_done) before its barrier.
+template <int ROWS, typename T>
 __device__ __forceinline__ void load_rows(float* dst, int ld, const T* src, int row0, int N,
                                           int width) {
   const int w4 = (width + 3) / 4;
-  for (int e = threadIdx.x; e < kT * w4; e += kThreads) {
-    const int r = e / w4, c = (e - r * w4) * 4;
+  const bool whole = (width & 3) == 0;
+  const int sh = 32 - __clz(w4 - 1);  // a row takes 2^sh threads (w4 <= 32)
+  for (int e = threadIdx.x; e < ROWS << sh; e += kThreads) {
+    const int r = e >> sh, c = (e & ((1 << sh) - 1)) * 4;
+    if (c >= width) continue;
+    const bool in = row0 + r < N;
+    const T* p = src + (size_t)(in ? row0 + r : 0) * width + c;
+    float* d = dst + r * ld + c;
+    if (sizeof(T) == 4 && whole) {
+      asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(smem_u32(d)), "l"(p),
+                   "r"(in ? 16 : 0)
+                   : "memory");
+      continue;
+    }
     float4 f = make_float4(0.f, 0.f, 0.f, 0.f);
-    if (row0 + r < N) {
-      const T* p = src + (size_t)(row0 + r) * width + c;
+    if (in && sizeof(T) == 2 && whole) {
+      const uint2 v = *reinterpret_cast<const uint2*>(p);
+      const float2 a = __bfloat1622float2(*reinterpret_cast<const __nv_bfloat162*>(&v.x));
+      const float2 b = __bfloat1622float2(*reinterpret_cast<const __nv_bfloat162*>(&v.y));
+      f = make_float4(a.x, a.y, b.x, b.y);
+    } else if (in) {
       f.x = to_f32<T>(p[0]);
       if (c + 1 < width) f.y = to_f32<T>(p[1]);
       if (c + 2 < width) f.z = to_f32<T>(p[2]);
       if (c + 3 < width) f.w = to_f32<T>(p[3]);
     }
-    *reinterpret_cast<float4*>(dst + r * ld + c) = f;
+    *reinterpret_cast<float4*>(d) = f;
   }
 }
+__device__ __forceinline__ void loads_done() {
+  asm volatile("cp.async.commit_group;\n\tcp.async.wait_group 0;" ::: "memory");
+}
+
+// fp32 pairs: one instruction, each half rounded as the scalar form is
+__device__ __forceinline__ float2 fma2(float2 a, float2 b, float2 c) { return __ffma2_rn(a, b, c); }
 
 // s[i][j] = sum_c A[4 ty + i][c] B[tx + 16 j][c]
 __device__ __forceinline__ void tile_dot(float (&s)[4][4], const float* A, const float* B, int ld,
                                          int width, int ty, int tx) {
+  float2 acc[4][4];  // sums over even and odd pairs of c
 #pragma unroll
   for (int i = 0; i < 4; ++i)
 #pragma unroll
-    for (int j = 0; j < 4; ++j) s[i][j] = 0.f;
+    for (int j = 0; j < 4; ++j) acc[i][j] = make_float2(0.f, 0.f);
   const float* a0 = A + 4 * ty * ld;
   const float* b0 = B + tx * ld;
-#pragma unroll 2
+#pragma unroll 4
   for (int c = 0; c < width; c += 4) {
     float4 a[4], b[4];
 #pragma unroll
@@ -91,12 +120,14 @@ __device__ __forceinline__ void tile_dot(float (&s)[4][4], const float* A, const
     for (int i = 0; i < 4; ++i)
 #pragma unroll
       for (int j = 0; j < 4; ++j) {
-        s[i][j] = fmaf(a[i].x, b[j].x, s[i][j]);
-        s[i][j] = fmaf(a[i].y, b[j].y, s[i][j]);
-        s[i][j] = fmaf(a[i].z, b[j].z, s[i][j]);
-        s[i][j] = fmaf(a[i].w, b[j].w, s[i][j]);
+        acc[i][j] = fma2({a[i].x, a[i].y}, {b[j].x, b[j].y}, acc[i][j]);
+        acc[i][j] = fma2({a[i].z, a[i].w}, {b[j].z, b[j].w}, acc[i][j]);
       }
   }
+#pragma unroll
+  for (int i = 0; i < 4; ++i)
+#pragma unroll
+    for (int j = 0; j < 4; ++j) s[i][j] = acc[i][j].x + acc[i][j].y;
 }
 
 // acc[i][4 g + e] += sum_k P[4 ty + i][k] X[k][4 tx + 64 g + e], over the
@@ -120,10 +151,9 @@ __device__ __forceinline__ void tile_add(float (&acc)[4][4 * NG], const float* P
 #pragma unroll
           for (int i = 0; i < 4; ++i) {
             const float w = u == 0 ? p[i].x : u == 1 ? p[i].y : u == 2 ? p[i].z : p[i].w;
-            acc[i][4 * g + 0] = fmaf(w, x.x, acc[i][4 * g + 0]);
-            acc[i][4 * g + 1] = fmaf(w, x.y, acc[i][4 * g + 1]);
-            acc[i][4 * g + 2] = fmaf(w, x.z, acc[i][4 * g + 2]);
-            acc[i][4 * g + 3] = fmaf(w, x.w, acc[i][4 * g + 3]);
+            float2* a = reinterpret_cast<float2*>(&acc[i][4 * g]);
+            a[0] = fma2({w, w}, {x.x, x.y}, a[0]);
+            a[1] = fma2({w, w}, {x.z, x.w}, a[1]);
           }
         }
       }
@@ -169,25 +199,27 @@ __device__ __forceinline__ float row16_sum(float v) {
   return v;
 }
 
-// ---- forward: one block per 64 query rows of a head -----------------------
+// ---- forward: one block per 32 query rows of a head -----------------------
 template <typename T, int NGV>
 __global__ void __launch_bounds__(kThreads) diff_fwd(Args a) {
   extern __shared__ __align__(16) float sm[];
   const int ld = ld_of(a.d), ldv = ld_of(a.dv_), N = a.N;
-  float* qs = sm;                      // [2][64][ld]
-  float* ks = qs + 2 * kT * ld;        // [2][64][ld]
+  float* qs = sm;                      // [2][32][ld]
+  float* ks = qs + 2 * kM * ld;        // [2][64][ld]
   float* vs = ks + 2 * kT * ld;        // [64][ldv]
-  float* ps = vs + kT * ldv;           // [64][kLdp]
+  float* ps = vs + kT * ldv;           // [32][kLdp]
   const int ty = threadIdx.x >> 4, tx = threadIdx.x & 15;
-  const int bh = blockIdx.y, b = bh / a.H, h = bh % a.H;
+  const int bh = blockIdx.x % a.heads, b = bh / a.H, h = bh % a.H;
   const int kvh = b * (a.H / a.G) + h / a.G;
-  const int row0 = (a.causal ? (int)(gridDim.x - 1 - blockIdx.x) : (int)blockIdx.x) * kT;
+  // heads vary fastest, and the long rows of all of them start first
+  const int blk = blockIdx.x / a.heads;
+  const int row0 = (a.causal ? (int)(gridDim.x / a.heads) - 1 - blk : blk) * kM;
   const size_t qsz = (size_t)N * a.d;
   const T* q = static_cast<const T*>(a.q) + (size_t)bh * 2 * qsz;
   const T* k = static_cast<const T*>(a.k) + (size_t)kvh * 2 * qsz;
   const T* v = static_cast<const T*>(a.v) + (size_t)kvh * N * a.dv_;
-  load_rows(qs, ld, q, row0, N, a.d);
-  load_rows(qs + kT * ld, ld, q + qsz, row0, N, a.d);
+  load_rows<kM>(qs, ld, q, row0, N, a.d);
+  load_rows<kM>(qs + kM * ld, ld, q + qsz, row0, N, a.d);
 
   float acc[2][4][4 * NGV], mx[2][4], l[2][4];
 #pragma unroll
@@ -199,17 +231,18 @@ __global__ void __launch_bounds__(kThreads) diff_fwd(Args a) {
 #pragma unroll
       for (int e = 0; e < 4 * NGV; ++e) acc[m][i][e] = 0.f;
     }
-  const int kend = a.causal ? min(N, row0 + kT) : N;
+  const int kend = a.causal ? min(N, row0 + kM) : N;
   for (int j0 = 0; j0 < kend; j0 += kT) {
     __syncthreads();
-    load_rows(ks, ld, k, j0, N, a.d);
-    load_rows(ks + kT * ld, ld, k + qsz, j0, N, a.d);
-    load_rows(vs, ldv, v, j0, N, a.dv_);
+    load_rows<kT>(ks, ld, k, j0, N, a.d);
+    load_rows<kT>(ks + kT * ld, ld, k + qsz, j0, N, a.d);
+    load_rows<kT>(vs, ldv, v, j0, N, a.dv_);
+    loads_done();
     __syncthreads();
 #pragma unroll
     for (int m = 0; m < 2; ++m) {
       float s[4][4];
-      tile_dot(s, qs + m * kT * ld, ks + m * kT * ld, ld, a.d, ty, tx);
+      tile_dot(s, qs + m * kM * ld, ks + m * kT * ld, ld, a.d, ty, tx);
 #pragma unroll
       for (int i = 0; i < 4; ++i) {
         const int r = row0 + 4 * ty + i;
@@ -259,27 +292,29 @@ __global__ void __launch_bounds__(kThreads) diff_fwd(Args a) {
   if (a.o2) store_rows<T, NGV>(static_cast<T*>(a.o2) + ob, acc[1], 1.f, row0, N, a.dv_, ty, tx);
 }
 
-// ---- dQ: one block per 64 query rows of a head -----------------------------
+// ---- dQ: one block per 32 query rows of a head -----------------------------
 template <typename T, int NGD>
 __global__ void __launch_bounds__(kThreads) diff_bwd_row(Args a) {
   extern __shared__ __align__(16) float sm[];
   const int ld = ld_of(a.d), ldv = ld_of(a.dv_), N = a.N;
-  float* qs = sm;                      // [2][64][ld]
-  float* dos = qs + 2 * kT * ld;       // [64][ldv]
-  float* ks = dos + kT * ldv;          // [2][64][ld]
+  float* qs = sm;                      // [2][32][ld]
+  float* dos = qs + 2 * kM * ld;       // [32][ldv]
+  float* ks = dos + kM * ldv;          // [2][64][ld]
   float* vs = ks + 2 * kT * ld;        // [64][ldv]
-  float* ps = vs + kT * ldv;           // [64][kLdp]
+  float* ps = vs + kT * ldv;           // [32][kLdp]
   const int ty = threadIdx.x >> 4, tx = threadIdx.x & 15;
-  const int bh = blockIdx.y, b = bh / a.H, h = bh % a.H;
+  const int bh = blockIdx.x % a.heads, b = bh / a.H, h = bh % a.H;
   const int kvh = b * (a.H / a.G) + h / a.G;
-  const int row0 = (a.causal ? (int)(gridDim.x - 1 - blockIdx.x) : (int)blockIdx.x) * kT;
+  // heads vary fastest, and the long rows of all of them start first
+  const int blk = blockIdx.x / a.heads;
+  const int row0 = (a.causal ? (int)(gridDim.x / a.heads) - 1 - blk : blk) * kM;
   const size_t qsz = (size_t)N * a.d;
   const T* q = static_cast<const T*>(a.q) + (size_t)bh * 2 * qsz;
   const T* k = static_cast<const T*>(a.k) + (size_t)kvh * 2 * qsz;
   const T* v = static_cast<const T*>(a.v) + (size_t)kvh * N * a.dv_;
-  load_rows(qs, ld, q, row0, N, a.d);
-  load_rows(qs + kT * ld, ld, q + qsz, row0, N, a.d);
-  load_rows(dos, ldv, static_cast<const T*>(a.dO) + (size_t)bh * N * a.dv_, row0, N, a.dv_);
+  load_rows<kM>(qs, ld, q, row0, N, a.d);
+  load_rows<kM>(qs + kM * ld, ld, q + qsz, row0, N, a.d);
+  load_rows<kM>(dos, ldv, static_cast<const T*>(a.dO) + (size_t)bh * N * a.dv_, row0, N, a.dv_);
   float lse[2][4], D[2][4], w[4], d2[4], acc[2][4][4 * NGD];
 #pragma unroll
   for (int i = 0; i < 4; ++i) {
@@ -295,19 +330,20 @@ __global__ void __launch_bounds__(kThreads) diff_bwd_row(Args a) {
     }
     w[i] = lam_at(a.lam, a.H, N, b, h, r < N ? r : 0);
   }
-  const int kend = a.causal ? min(N, row0 + kT) : N;
+  const int kend = a.causal ? min(N, row0 + kM) : N;
   for (int j0 = 0; j0 < kend; j0 += kT) {
     __syncthreads();
-    load_rows(ks, ld, k, j0, N, a.d);
-    load_rows(ks + kT * ld, ld, k + qsz, j0, N, a.d);
-    load_rows(vs, ldv, v, j0, N, a.dv_);
+    load_rows<kT>(ks, ld, k, j0, N, a.d);
+    load_rows<kT>(ks + kT * ld, ld, k + qsz, j0, N, a.d);
+    load_rows<kT>(vs, ldv, v, j0, N, a.dv_);
+    loads_done();
     __syncthreads();
     float dp[4][4];
     tile_dot(dp, dos, vs, ldv, a.dv_, ty, tx);
 #pragma unroll
     for (int m = 0; m < 2; ++m) {
       float s[4][4];
-      tile_dot(s, qs + m * kT * ld, ks + m * kT * ld, ld, a.d, ty, tx);
+      tile_dot(s, qs + m * kM * ld, ks + m * kT * ld, ld, a.d, ty, tx);
 #pragma unroll
       for (int i = 0; i < 4; ++i) {
         const int r = row0 + 4 * ty + i;
@@ -337,26 +373,26 @@ __global__ void __launch_bounds__(kThreads) diff_bwd_row(Args a) {
                        a.d, ty, tx);
 }
 
-// ---- dK, dV: one block per 64 keys of a key head, over its query heads ------
+// ---- dK, dV: one block per 32 keys of a key head, over its query heads ------
 template <typename T, int NGD, int NGV>
 __global__ void __launch_bounds__(kThreads) diff_bwd_col(Args a) {
   extern __shared__ __align__(16) float sm[];
   const int ld = ld_of(a.d), ldv = ld_of(a.dv_), N = a.N;
-  float* ks = sm;                      // [2][64][ld]
-  float* vs = ks + 2 * kT * ld;        // [64][ldv]
-  float* qs = vs + kT * ldv;           // [2][64][ld]
+  float* ks = sm;                      // [2][32][ld]
+  float* vs = ks + 2 * kM * ld;        // [32][ldv]
+  float* qs = vs + kM * ldv;           // [2][64][ld]
   float* dos = qs + 2 * kT * ld;       // [64][ldv]
-  float* ps = dos + kT * ldv;          // [64][kLdp]
-  float* sc = ps + kT * kLdp;          // [5][64]: LSE^1, LSE^2, D^1, D^2, lam
+  float* ps = dos + kT * ldv;          // [32][kLdp]
+  float* sc = ps + kM * kLdp;          // [5][64]: LSE^1, LSE^2, D^1, D^2, lam
   const int ty = threadIdx.x >> 4, tx = threadIdx.x & 15;
-  const int kvh = blockIdx.y, Hk = a.H / a.G;
+  const int kvh = blockIdx.x % a.heads, Hk = a.H / a.G;
   const int b = kvh / Hk;
-  const int col0 = blockIdx.x * kT;
+  const int col0 = blockIdx.x / a.heads * kM;
   const size_t qsz = (size_t)N * a.d;
   const T* k = static_cast<const T*>(a.k) + (size_t)kvh * 2 * qsz;
-  load_rows(ks, ld, k, col0, N, a.d);
-  load_rows(ks + kT * ld, ld, k + qsz, col0, N, a.d);
-  load_rows(vs, ldv, static_cast<const T*>(a.v) + (size_t)kvh * N * a.dv_, col0, N, a.dv_);
+  load_rows<kM>(ks, ld, k, col0, N, a.d);
+  load_rows<kM>(ks + kM * ld, ld, k + qsz, col0, N, a.d);
+  load_rows<kM>(vs, ldv, static_cast<const T*>(a.v) + (size_t)kvh * N * a.dv_, col0, N, a.dv_);
   float ak[2][4][4 * NGD], av[4][4 * NGV];
 #pragma unroll
   for (int i = 0; i < 4; ++i) {
@@ -370,11 +406,11 @@ __global__ void __launch_bounds__(kThreads) diff_bwd_col(Args a) {
     const size_t bh = (size_t)b * a.H + h;
     const T* q = static_cast<const T*>(a.q) + bh * 2 * qsz;
     const T* dO = static_cast<const T*>(a.dO) + bh * N * a.dv_;
-    for (int i0 = a.causal ? col0 : 0; i0 < N; i0 += kT) {
+    for (int i0 = a.causal ? col0 / kT * kT : 0; i0 < N; i0 += kT) {
       __syncthreads();
-      load_rows(qs, ld, q, i0, N, a.d);
-      load_rows(qs + kT * ld, ld, q + qsz, i0, N, a.d);
-      load_rows(dos, ldv, dO, i0, N, a.dv_);
+      load_rows<kT>(qs, ld, q, i0, N, a.d);
+      load_rows<kT>(qs + kT * ld, ld, q + qsz, i0, N, a.d);
+      load_rows<kT>(dos, ldv, dO, i0, N, a.dv_);
       if (threadIdx.x < kT) {
         const int r = min(i0 + (int)threadIdx.x, N - 1);
         sc[0 * kT + threadIdx.x] = a.lse[(bh * 2 + 0) * N + r];
@@ -383,13 +419,14 @@ __global__ void __launch_bounds__(kThreads) diff_bwd_col(Args a) {
         sc[3 * kT + threadIdx.x] = a.D[(bh * 2 + 1) * N + r];
         sc[4 * kT + threadIdx.x] = lam_at(a.lam, a.H, N, b, h, r);
       }
+      loads_done();
       __syncthreads();
       float dp[4][4], wt[4][4];
       tile_dot(dp, vs, dos, ldv, a.dv_, ty, tx);
 #pragma unroll
       for (int m = 0; m < 2; ++m) {
         float s[4][4];
-        tile_dot(s, ks + m * kT * ld, qs + m * kT * ld, ld, a.d, ty, tx);
+        tile_dot(s, ks + m * kM * ld, qs + m * kT * ld, ld, a.d, ty, tx);
 #pragma unroll
         for (int i = 0; i < 4; ++i)
 #pragma unroll
@@ -428,11 +465,12 @@ Args make_args(const DiffProblem& p, const DiffTensors& t) {
 }
 
 template <typename K>
-cudaError_t run(K kernel, dim3 grid, size_t floats, const Args& a, LaunchLog& log) {
+cudaError_t run(K kernel, int blocks, int heads, size_t floats, Args a, LaunchLog& log) {
+  a.heads = heads;
   const size_t bytes = floats * sizeof(float);
   cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)bytes);
   if (e != cudaSuccess) return e;
-  kernel<<<grid, kThreads, bytes, log.stream>>>(a);
+  kernel<<<(unsigned)(blocks * heads), kThreads, bytes, log.stream>>>(a);
   e = cudaGetLastError();
   log.mark();
   return e;
@@ -440,11 +478,11 @@ cudaError_t run(K kernel, dim3 grid, size_t floats, const Args& a, LaunchLog& lo
 
 template <typename T>
 cudaError_t forward_t(const DiffProblem& p, const DiffTensors& t, LaunchLog& log) {
-  const dim3 grid((p.N + kT - 1) / kT, p.B * p.H);
-  const size_t floats = (size_t)kT * (4 * ld_of(p.d) + ld_of(p.dv) + kLdp);
+  const int blocks = (p.N + kM - 1) / kM, heads = p.B * p.H;
+  const size_t floats = (size_t)kT * (2 * ld_of(p.d) + ld_of(p.dv)) + kM * (2 * ld_of(p.d) + kLdp);
   const Args a = make_args(p, t);
-  return p.dv <= 64 ? run(diff_fwd<T, 1>, grid, floats, a, log)
-                    : run(diff_fwd<T, 2>, grid, floats, a, log);
+  return p.dv <= 64 ? run(diff_fwd<T, 1>, blocks, heads, floats, a, log)
+                    : run(diff_fwd<T, 2>, blocks, heads, floats, a, log);
 }
 
 template <typename T>
@@ -453,18 +491,19 @@ cudaError_t backward_t(const DiffProblem& p, const DiffTensors& t, const DiffWor
   Args a = make_args(p, t);
   a.D = ws.D;
   a.d2 = ws.d2;
-  const int blocks = (p.N + kT - 1) / kT;
-  const size_t floats = (size_t)kT * (4 * ld_of(p.d) + 2 * ld_of(p.dv) + kLdp);
-  const dim3 rows(blocks, p.B * p.H), cols(blocks, p.B * p.Hk);
-  cudaError_t e = p.d <= 64 ? run(diff_bwd_row<T, 1>, rows, floats, a, log)
-                            : run(diff_bwd_row<T, 2>, rows, floats, a, log);
+  const int blocks = (p.N + kM - 1) / kM;
+  const size_t floats =
+      (size_t)(kT + kM) * (2 * ld_of(p.d) + ld_of(p.dv)) + (size_t)kM * kLdp;
+  const int rows = p.B * p.H, cols = p.B * p.Hk;  // grids' heads
+  cudaError_t e = p.d <= 64 ? run(diff_bwd_row<T, 1>, blocks, rows, floats, a, log)
+                            : run(diff_bwd_row<T, 2>, blocks, rows, floats, a, log);
   if (e != cudaSuccess) return e;
   const size_t cf = floats + 5 * kT;
   if (p.d <= 64)
-    return p.dv <= 64 ? run(diff_bwd_col<T, 1, 1>, cols, cf, a, log)
-                      : run(diff_bwd_col<T, 1, 2>, cols, cf, a, log);
-  return p.dv <= 64 ? run(diff_bwd_col<T, 2, 1>, cols, cf, a, log)
-                    : run(diff_bwd_col<T, 2, 2>, cols, cf, a, log);
+    return p.dv <= 64 ? run(diff_bwd_col<T, 1, 1>, blocks, cols, cf, a, log)
+                      : run(diff_bwd_col<T, 1, 2>, blocks, cols, cf, a, log);
+  return p.dv <= 64 ? run(diff_bwd_col<T, 2, 1>, blocks, cols, cf, a, log)
+                    : run(diff_bwd_col<T, 2, 2>, blocks, cols, cf, a, log);
 }
 
 }  // namespace
