@@ -11,10 +11,11 @@
 // rows 4 ty.. and columns tx + 16 j.  A row of scores lives in 16 lanes of one
 // warp, so row maxima and sums are shuffles, and the probabilities pass to
 // their product through shared memory inside the warp.  Bound: FFMA issue,
-// at 8 FFMA per 16-byte shared-memory read.  Two blocks share an SM at
-// d = 64, dv = 128, so one computes while the other loads, and short
-// sequences still give many blocks.  Everything a row or key accumulates is
-// summed by one block in a fixed order.
+// at 8 FFMA per 16-byte shared-memory read; with one warp per scheduler it is
+// latency, so where shared memory allows (SPLIT = 2) two such groups of
+// threads share a block's stationary tile, take every other streamed tile each
+// with tiles of their own, and add up at the end.  Everything a row or key
+// accumulates is summed by one block in a fixed order.
 #include <cuda_bf16.h>
 #include <math.h>
 
@@ -27,7 +28,7 @@ namespace {
 
 constexpr int kM = 32;       // rows of the stationary tile
 constexpr int kT = 64;       // rows of a streamed tile
-constexpr int kThreads = 128;
+constexpr int kThreads = 128;  // of a group
 constexpr int kLdp = kT + 4;  // row stride of the score tile
 
 // Row stride of a [64][width] tile in floats: whole 16-byte steps, and rows
@@ -35,6 +36,12 @@ constexpr int kLdp = kT + 4;  // row stride of the score tile
 __host__ __device__ inline int ld_of(int width) {
   const int w = (width + 3) / 4 * 4;
   return (w % 32 == 0 || w % 8 == 0) ? w + 4 : w;
+}
+
+// Floats of one group's area: `tiles`, or the sums it hands over at the end
+// (`sums` per thread).
+__host__ __device__ inline int group_floats(int tiles, int sums) {
+  return tiles > sums * kThreads ? tiles : sums * kThreads;
 }
 
 struct Args {
@@ -60,12 +67,12 @@ __device__ __forceinline__ float lam_at(const LamArg& l, int H, int N, int b, in
 // 16-byte steps go by asynchronous copies, which the caller awaits
 // (loads_done) before its barrier.
 template <int ROWS, typename T>
-__device__ __forceinline__ void load_rows(float* dst, int ld, const T* src, int row0, int N,
+__device__ __forceinline__ void load_rows(int tid, float* dst, int ld, const T* src, int row0, int N,
                                           int width) {
   const int w4 = (width + 3) / 4;
   const bool whole = (width & 3) == 0;
   const int sh = 32 - __clz(w4 - 1);  // a row takes 2^sh threads (w4 <= 32)
-  for (int e = threadIdx.x; e < ROWS << sh; e += kThreads) {
+  for (int e = tid; e < ROWS << sh; e += kThreads) {
     const int r = e >> sh, c = (e & ((1 << sh) - 1)) * 4;
     if (c >= width) continue;
     const bool in = row0 + r < N;
@@ -119,10 +126,11 @@ __device__ __forceinline__ void tile_dot(float (&s)[4][4], const float* A, const
 #pragma unroll
     for (int i = 0; i < 4; ++i)
 #pragma unroll
-      for (int j = 0; j < 4; ++j) {
-        acc[i][j] = fma2({a[i].x, a[i].y}, {b[j].x, b[j].y}, acc[i][j]);
-        acc[i][j] = fma2({a[i].z, a[i].w}, {b[j].z, b[j].w}, acc[i][j]);
-      }
+      for (int j = 0; j < 4; ++j) acc[i][j] = fma2({a[i].x, a[i].y}, {b[j].x, b[j].y}, acc[i][j]);
+#pragma unroll
+    for (int i = 0; i < 4; ++i)
+#pragma unroll
+      for (int j = 0; j < 4; ++j) acc[i][j] = fma2({a[i].z, a[i].w}, {b[j].z, b[j].w}, acc[i][j]);
   }
 #pragma unroll
   for (int i = 0; i < 4; ++i)
@@ -188,6 +196,13 @@ __device__ __forceinline__ void store_rows(T* dst, const float (&acc)[4][4 * NG]
   }
 }
 
+// A group's threads only (the block's, where there is one group)
+template <int SPLIT>
+__device__ __forceinline__ void group_sync(int grp) {
+  if constexpr (SPLIT == 1) __syncthreads();
+  else asm volatile("bar.sync %0, %1;" ::"r"(1 + grp), "n"(kThreads) : "memory");
+}
+
 __device__ __forceinline__ float row16_max(float v) {
 #pragma unroll
   for (int o = 8; o > 0; o >>= 1) v = fmaxf(v, __shfl_xor_sync(0xffffffffu, v, o));
@@ -200,15 +215,20 @@ __device__ __forceinline__ float row16_sum(float v) {
 }
 
 // ---- forward: one block per 32 query rows of a head -----------------------
-template <typename T, int NGV>
-__global__ void __launch_bounds__(kThreads) diff_fwd(Args a) {
+template <typename T, int NGV, int SPLIT>
+__global__ void __launch_bounds__(SPLIT * kThreads) diff_fwd(Args a) {
   extern __shared__ __align__(16) float sm[];
   const int ld = ld_of(a.d), ldv = ld_of(a.dv_), N = a.N;
+  const int grp = threadIdx.x / kThreads, tid = threadIdx.x % kThreads;
+  const int ty = tid >> 4, tx = tid & 15;
   float* qs = sm;                      // [2][32][ld]
-  float* ks = qs + 2 * kM * ld;        // [2][64][ld]
+  float* mine = qs + 2 * kM * ld;      // the group's area
+  const int area = group_floats(kT * (2 * ld + ldv) + kM * kLdp, 32 * NGV + 16);
+  const float* other = mine + area;    // the second group's, for the first
+  if (grp == 1) mine += area;
+  float* ks = mine;                    // [2][64][ld]
   float* vs = ks + 2 * kT * ld;        // [64][ldv]
   float* ps = vs + kT * ldv;           // [32][kLdp]
-  const int ty = threadIdx.x >> 4, tx = threadIdx.x & 15;
   const int bh = blockIdx.x % a.heads, b = bh / a.H, h = bh % a.H;
   const int kvh = b * (a.H / a.G) + h / a.G;
   // heads vary fastest, and the long rows of all of them start first
@@ -218,8 +238,10 @@ __global__ void __launch_bounds__(kThreads) diff_fwd(Args a) {
   const T* q = static_cast<const T*>(a.q) + (size_t)bh * 2 * qsz;
   const T* k = static_cast<const T*>(a.k) + (size_t)kvh * 2 * qsz;
   const T* v = static_cast<const T*>(a.v) + (size_t)kvh * N * a.dv_;
-  load_rows<kM>(qs, ld, q, row0, N, a.d);
-  load_rows<kM>(qs + kM * ld, ld, q + qsz, row0, N, a.d);
+  if (grp == 0) load_rows<kM>(tid, qs, ld, q, row0, N, a.d);
+  if (grp == SPLIT - 1) load_rows<kM>(tid, qs + kM * ld, ld, q + qsz, row0, N, a.d);
+  loads_done();
+  __syncthreads();
 
   float acc[2][4][4 * NGV], mx[2][4], l[2][4];
 #pragma unroll
@@ -232,13 +254,13 @@ __global__ void __launch_bounds__(kThreads) diff_fwd(Args a) {
       for (int e = 0; e < 4 * NGV; ++e) acc[m][i][e] = 0.f;
     }
   const int kend = a.causal ? min(N, row0 + kM) : N;
-  for (int j0 = 0; j0 < kend; j0 += kT) {
-    __syncthreads();
-    load_rows<kT>(ks, ld, k, j0, N, a.d);
-    load_rows<kT>(ks + kT * ld, ld, k + qsz, j0, N, a.d);
-    load_rows<kT>(vs, ldv, v, j0, N, a.dv_);
+  for (int j0 = grp * kT; j0 < kend; j0 += SPLIT * kT) {
+    group_sync<SPLIT>(grp);
+    load_rows<kT>(tid, ks, ld, k, j0, N, a.d);
+    load_rows<kT>(tid, ks + kT * ld, ld, k + qsz, j0, N, a.d);
+    load_rows<kT>(tid, vs, ldv, v, j0, N, a.dv_);
     loads_done();
-    __syncthreads();
+    group_sync<SPLIT>(grp);
 #pragma unroll
     for (int m = 0; m < 2; ++m) {
       float s[4][4];
@@ -253,15 +275,18 @@ __global__ void __launch_bounds__(kThreads) diff_fwd(Args a) {
           s[i][j] = (col < N && (!a.causal || col <= r)) ? s[i][j] * a.scale : -INFINITY;
           t = fmaxf(t, s[i][j]);
         }
-        // every row sees a key of its first tile, so the maximum is finite
-        // from there on (rows past N see them too; they are not stored)
+        // the first group's rows see a key of its first tile (rows past N too;
+        // they are not stored).  A row that sees none of this tile, nor of the
+        // group's earlier ones, keeps a maximum of -inf: it counts as 0 then,
+        // and every term and sum stays 0
         t = fmaxf(mx[m][i], row16_max(t));
-        const float alpha = expf(mx[m][i] - t);
+        const float ref = SPLIT > 1 && t == -INFINITY ? 0.f : t;
+        const float alpha = expf(mx[m][i] - ref);
         mx[m][i] = t;
         float sum = 0.f;
 #pragma unroll
         for (int j = 0; j < 4; ++j) {
-          s[i][j] = expf(s[i][j] - t);
+          s[i][j] = expf(s[i][j] - ref);
           sum += s[i][j];
         }
         l[m][i] = l[m][i] * alpha + row16_sum(sum);
@@ -271,6 +296,37 @@ __global__ void __launch_bounds__(kThreads) diff_fwd(Args a) {
       put_tile(ps, s, ty, tx);
       tile_add<NGV>(acc[m], ps, vs, ldv, a.dv_, ty, tx);
     }
+  }
+  if constexpr (SPLIT > 1) {
+    // the second group hands over; the first combines against the joint maximum
+    group_sync<SPLIT>(grp);
+    if (grp == 1) {
+#pragma unroll
+      for (int m = 0; m < 2; ++m)
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+#pragma unroll
+          for (int e = 0; e < 4 * NGV; ++e)
+            mine[((m * 4 + i) * 4 * NGV + e) * kThreads + tid] = acc[m][i][e];
+          mine[(32 * NGV + m * 4 + i) * kThreads + tid] = mx[m][i];
+          mine[(32 * NGV + 8 + m * 4 + i) * kThreads + tid] = l[m][i];
+        }
+    }
+    __syncthreads();
+    if (grp == 1) return;
+#pragma unroll
+    for (int m = 0; m < 2; ++m)
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        const float m2 = other[(32 * NGV + m * 4 + i) * kThreads + tid];
+        const float top = fmaxf(mx[m][i], m2);
+        const float f1 = expf(mx[m][i] - top), f2 = expf(m2 - top);
+        mx[m][i] = top;
+        l[m][i] = l[m][i] * f1 + other[(32 * NGV + 8 + m * 4 + i) * kThreads + tid] * f2;
+#pragma unroll
+        for (int e = 0; e < 4 * NGV; ++e)
+          acc[m][i][e] = acc[m][i][e] * f1 + other[((m * 4 + i) * 4 * NGV + e) * kThreads + tid] * f2;
+      }
   }
 #pragma unroll
   for (int i = 0; i < 4; ++i) {
@@ -293,16 +349,21 @@ __global__ void __launch_bounds__(kThreads) diff_fwd(Args a) {
 }
 
 // ---- dQ: one block per 32 query rows of a head -----------------------------
-template <typename T, int NGD>
-__global__ void __launch_bounds__(kThreads) diff_bwd_row(Args a) {
+template <typename T, int NGD, int SPLIT>
+__global__ void __launch_bounds__(SPLIT * kThreads) diff_bwd_row(Args a) {
   extern __shared__ __align__(16) float sm[];
   const int ld = ld_of(a.d), ldv = ld_of(a.dv_), N = a.N;
+  const int grp = threadIdx.x / kThreads, tid = threadIdx.x % kThreads;
+  const int ty = tid >> 4, tx = tid & 15;
   float* qs = sm;                      // [2][32][ld]
   float* dos = qs + 2 * kM * ld;       // [32][ldv]
-  float* ks = dos + kM * ldv;          // [2][64][ld]
+  float* mine = dos + kM * ldv;        // the group's area
+  const int area = group_floats(kT * (2 * ld + ldv) + kM * kLdp, 32 * NGD + 4);
+  const float* other = mine + area;
+  if (grp == 1) mine += area;
+  float* ks = mine;                    // [2][64][ld]
   float* vs = ks + 2 * kT * ld;        // [64][ldv]
   float* ps = vs + kT * ldv;           // [32][kLdp]
-  const int ty = threadIdx.x >> 4, tx = threadIdx.x & 15;
   const int bh = blockIdx.x % a.heads, b = bh / a.H, h = bh % a.H;
   const int kvh = b * (a.H / a.G) + h / a.G;
   // heads vary fastest, and the long rows of all of them start first
@@ -312,9 +373,14 @@ __global__ void __launch_bounds__(kThreads) diff_bwd_row(Args a) {
   const T* q = static_cast<const T*>(a.q) + (size_t)bh * 2 * qsz;
   const T* k = static_cast<const T*>(a.k) + (size_t)kvh * 2 * qsz;
   const T* v = static_cast<const T*>(a.v) + (size_t)kvh * N * a.dv_;
-  load_rows<kM>(qs, ld, q, row0, N, a.d);
-  load_rows<kM>(qs + kM * ld, ld, q + qsz, row0, N, a.d);
-  load_rows<kM>(dos, ldv, static_cast<const T*>(a.dO) + (size_t)bh * N * a.dv_, row0, N, a.dv_);
+  if (grp == 0) {
+    load_rows<kM>(tid, qs, ld, q, row0, N, a.d);
+    load_rows<kM>(tid, qs + kM * ld, ld, q + qsz, row0, N, a.d);
+  }
+  if (grp == SPLIT - 1)
+    load_rows<kM>(tid, dos, ldv, static_cast<const T*>(a.dO) + (size_t)bh * N * a.dv_, row0, N, a.dv_);
+  loads_done();
+  __syncthreads();
   float lse[2][4], D[2][4], w[4], d2[4], acc[2][4][4 * NGD];
 #pragma unroll
   for (int i = 0; i < 4; ++i) {
@@ -331,13 +397,13 @@ __global__ void __launch_bounds__(kThreads) diff_bwd_row(Args a) {
     w[i] = lam_at(a.lam, a.H, N, b, h, r < N ? r : 0);
   }
   const int kend = a.causal ? min(N, row0 + kM) : N;
-  for (int j0 = 0; j0 < kend; j0 += kT) {
-    __syncthreads();
-    load_rows<kT>(ks, ld, k, j0, N, a.d);
-    load_rows<kT>(ks + kT * ld, ld, k + qsz, j0, N, a.d);
-    load_rows<kT>(vs, ldv, v, j0, N, a.dv_);
+  for (int j0 = grp * kT; j0 < kend; j0 += SPLIT * kT) {
+    group_sync<SPLIT>(grp);
+    load_rows<kT>(tid, ks, ld, k, j0, N, a.d);
+    load_rows<kT>(tid, ks + kT * ld, ld, k + qsz, j0, N, a.d);
+    load_rows<kT>(tid, vs, ldv, v, j0, N, a.dv_);
     loads_done();
-    __syncthreads();
+    group_sync<SPLIT>(grp);
     float dp[4][4];
     tile_dot(dp, dos, vs, ldv, a.dv_, ty, tx);
 #pragma unroll
@@ -361,6 +427,31 @@ __global__ void __launch_bounds__(kThreads) diff_bwd_row(Args a) {
       tile_add<NGD>(acc[m], ps, ks + m * kT * ld, ld, a.d, ty, tx);
     }
   }
+  if constexpr (SPLIT > 1) {
+    group_sync<SPLIT>(grp);
+    if (grp == 1) {
+#pragma unroll
+      for (int m = 0; m < 2; ++m)
+#pragma unroll
+        for (int i = 0; i < 4; ++i)
+#pragma unroll
+          for (int e = 0; e < 4 * NGD; ++e)
+            mine[((m * 4 + i) * 4 * NGD + e) * kThreads + tid] = acc[m][i][e];
+#pragma unroll
+      for (int i = 0; i < 4; ++i) mine[(32 * NGD + i) * kThreads + tid] = d2[i];
+    }
+    __syncthreads();
+    if (grp == 1) return;
+#pragma unroll
+    for (int m = 0; m < 2; ++m)
+#pragma unroll
+      for (int i = 0; i < 4; ++i)
+#pragma unroll
+        for (int e = 0; e < 4 * NGD; ++e)
+          acc[m][i][e] += other[((m * 4 + i) * 4 * NGD + e) * kThreads + tid];
+#pragma unroll
+    for (int i = 0; i < 4; ++i) d2[i] += other[(32 * NGD + i) * kThreads + tid];
+  }
 #pragma unroll
   for (int i = 0; i < 4; ++i) {
     const int r = row0 + 4 * ty + i;
@@ -374,25 +465,35 @@ __global__ void __launch_bounds__(kThreads) diff_bwd_row(Args a) {
 }
 
 // ---- dK, dV: one block per 32 keys of a key head, over its query heads ------
-template <typename T, int NGD, int NGV>
-__global__ void __launch_bounds__(kThreads) diff_bwd_col(Args a) {
+template <typename T, int NGD, int NGV, int SPLIT>
+__global__ void __launch_bounds__(SPLIT * kThreads) diff_bwd_col(Args a) {
   extern __shared__ __align__(16) float sm[];
   const int ld = ld_of(a.d), ldv = ld_of(a.dv_), N = a.N;
+  const int grp = threadIdx.x / kThreads, tid = threadIdx.x % kThreads;
+  const int ty = tid >> 4, tx = tid & 15;
   float* ks = sm;                      // [2][32][ld]
   float* vs = ks + 2 * kM * ld;        // [32][ldv]
-  float* qs = vs + kM * ldv;           // [2][64][ld]
+  float* mine = vs + kM * ldv;         // the group's area
+  const int area = group_floats(kT * (2 * ld + ldv + 5) + kM * kLdp, 32 * NGD + 16 * NGV);
+  const float* other = mine + area;
+  if (grp == 1) mine += area;
+  float* qs = mine;                    // [2][64][ld]
   float* dos = qs + 2 * kT * ld;       // [64][ldv]
   float* ps = dos + kT * ldv;          // [32][kLdp]
   float* sc = ps + kM * kLdp;          // [5][64]: LSE^1, LSE^2, D^1, D^2, lam
-  const int ty = threadIdx.x >> 4, tx = threadIdx.x & 15;
   const int kvh = blockIdx.x % a.heads, Hk = a.H / a.G;
   const int b = kvh / Hk;
   const int col0 = blockIdx.x / a.heads * kM;
   const size_t qsz = (size_t)N * a.d;
   const T* k = static_cast<const T*>(a.k) + (size_t)kvh * 2 * qsz;
-  load_rows<kM>(ks, ld, k, col0, N, a.d);
-  load_rows<kM>(ks + kM * ld, ld, k + qsz, col0, N, a.d);
-  load_rows<kM>(vs, ldv, static_cast<const T*>(a.v) + (size_t)kvh * N * a.dv_, col0, N, a.dv_);
+  if (grp == 0) {
+    load_rows<kM>(tid, ks, ld, k, col0, N, a.d);
+    load_rows<kM>(tid, ks + kM * ld, ld, k + qsz, col0, N, a.d);
+  }
+  if (grp == SPLIT - 1)
+    load_rows<kM>(tid, vs, ldv, static_cast<const T*>(a.v) + (size_t)kvh * N * a.dv_, col0, N, a.dv_);
+  loads_done();
+  __syncthreads();
   float ak[2][4][4 * NGD], av[4][4 * NGV];
 #pragma unroll
   for (int i = 0; i < 4; ++i) {
@@ -406,21 +507,21 @@ __global__ void __launch_bounds__(kThreads) diff_bwd_col(Args a) {
     const size_t bh = (size_t)b * a.H + h;
     const T* q = static_cast<const T*>(a.q) + bh * 2 * qsz;
     const T* dO = static_cast<const T*>(a.dO) + bh * N * a.dv_;
-    for (int i0 = a.causal ? col0 / kT * kT : 0; i0 < N; i0 += kT) {
-      __syncthreads();
-      load_rows<kT>(qs, ld, q, i0, N, a.d);
-      load_rows<kT>(qs + kT * ld, ld, q + qsz, i0, N, a.d);
-      load_rows<kT>(dos, ldv, dO, i0, N, a.dv_);
-      if (threadIdx.x < kT) {
-        const int r = min(i0 + (int)threadIdx.x, N - 1);
-        sc[0 * kT + threadIdx.x] = a.lse[(bh * 2 + 0) * N + r];
-        sc[1 * kT + threadIdx.x] = a.lse[(bh * 2 + 1) * N + r];
-        sc[2 * kT + threadIdx.x] = a.D[(bh * 2 + 0) * N + r];
-        sc[3 * kT + threadIdx.x] = a.D[(bh * 2 + 1) * N + r];
-        sc[4 * kT + threadIdx.x] = lam_at(a.lam, a.H, N, b, h, r);
+    for (int i0 = (a.causal ? col0 / kT * kT : 0) + grp * kT; i0 < N; i0 += SPLIT * kT) {
+      group_sync<SPLIT>(grp);
+      load_rows<kT>(tid, qs, ld, q, i0, N, a.d);
+      load_rows<kT>(tid, qs + kT * ld, ld, q + qsz, i0, N, a.d);
+      load_rows<kT>(tid, dos, ldv, dO, i0, N, a.dv_);
+      if (tid < kT) {
+        const int r = min(i0 + tid, N - 1);
+        sc[0 * kT + tid] = a.lse[(bh * 2 + 0) * N + r];
+        sc[1 * kT + tid] = a.lse[(bh * 2 + 1) * N + r];
+        sc[2 * kT + tid] = a.D[(bh * 2 + 0) * N + r];
+        sc[3 * kT + tid] = a.D[(bh * 2 + 1) * N + r];
+        sc[4 * kT + tid] = lam_at(a.lam, a.H, N, b, h, r);
       }
       loads_done();
-      __syncthreads();
+      group_sync<SPLIT>(grp);
       float dp[4][4], wt[4][4];
       tile_dot(dp, vs, dos, ldv, a.dv_, ty, tx);
 #pragma unroll
@@ -445,6 +546,35 @@ __global__ void __launch_bounds__(kThreads) diff_bwd_col(Args a) {
       tile_add<NGV>(av, ps, dos, ldv, a.dv_, ty, tx);
     }
   }
+  if constexpr (SPLIT > 1) {
+    group_sync<SPLIT>(grp);
+    if (grp == 1) {
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+#pragma unroll
+        for (int m = 0; m < 2; ++m)
+#pragma unroll
+          for (int e = 0; e < 4 * NGD; ++e)
+            mine[((m * 4 + i) * 4 * NGD + e) * kThreads + tid] = ak[m][i][e];
+#pragma unroll
+        for (int e = 0; e < 4 * NGV; ++e)
+          mine[(32 * NGD + i * 4 * NGV + e) * kThreads + tid] = av[i][e];
+      }
+    }
+    __syncthreads();
+    if (grp == 1) return;
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+#pragma unroll
+      for (int m = 0; m < 2; ++m)
+#pragma unroll
+        for (int e = 0; e < 4 * NGD; ++e)
+          ak[m][i][e] += other[((m * 4 + i) * 4 * NGD + e) * kThreads + tid];
+#pragma unroll
+      for (int e = 0; e < 4 * NGV; ++e)
+        av[i][e] += other[(32 * NGD + i * 4 * NGV + e) * kThreads + tid];
+    }
+  }
 #pragma unroll
   for (int m = 0; m < 2; ++m)
     store_rows<T, NGD>(static_cast<T*>(a.dk) + ((size_t)kvh * 2 + m) * qsz, ak[m], a.scale, col0, N,
@@ -464,25 +594,46 @@ Args make_args(const DiffProblem& p, const DiffTensors& t) {
   return a;
 }
 
+constexpr size_t kMaxShared = 232448;
+
 template <typename K>
-cudaError_t run(K kernel, int blocks, int heads, size_t floats, Args a, LaunchLog& log) {
-  a.heads = heads;
+cudaError_t launch(K kernel, int blocks, int split, size_t floats, const Args& a, LaunchLog& log) {
   const size_t bytes = floats * sizeof(float);
   cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)bytes);
   if (e != cudaSuccess) return e;
-  kernel<<<(unsigned)(blocks * heads), kThreads, bytes, log.stream>>>(a);
+  kernel<<<(unsigned)(blocks * a.heads), split * kThreads, bytes, log.stream>>>(a);
   e = cudaGetLastError();
   log.mark();
   return e;
 }
 
+// Two groups per block where their areas fit in shared memory.
+template <typename K1, typename K2>
+cudaError_t run(K1 one, K2 two, int blocks, int heads, size_t fixed, size_t area, Args a,
+                LaunchLog& log) {
+  a.heads = heads;
+  if ((fixed + 2 * area) * sizeof(float) <= kMaxShared)
+    return launch(two, blocks, 2, fixed + 2 * area, a, log);
+  return launch(one, blocks, 1, fixed + area, a, log);
+}
+
 template <typename T>
 cudaError_t forward_t(const DiffProblem& p, const DiffTensors& t, LaunchLog& log) {
+  const int ld = ld_of(p.d), ldv = ld_of(p.dv), tiles = kT * (2 * ld + ldv) + kM * kLdp;
   const int blocks = (p.N + kM - 1) / kM, heads = p.B * p.H;
-  const size_t floats = (size_t)kT * (2 * ld_of(p.d) + ld_of(p.dv)) + kM * (2 * ld_of(p.d) + kLdp);
+  const size_t fixed = (size_t)kM * 2 * ld;
   const Args a = make_args(p, t);
-  return p.dv <= 64 ? run(diff_fwd<T, 1>, blocks, heads, floats, a, log)
-                    : run(diff_fwd<T, 2>, blocks, heads, floats, a, log);
+  if (p.dv <= 64)
+    return run(diff_fwd<T, 1, 1>, diff_fwd<T, 1, 2>, blocks, heads, fixed,
+               group_floats(tiles, 32 + 16), a, log);
+  return run(diff_fwd<T, 2, 1>, diff_fwd<T, 2, 2>, blocks, heads, fixed,
+             group_floats(tiles, 64 + 16), a, log);
+}
+
+template <typename T, int NGD, int NGV>
+cudaError_t columns(int blocks, int heads, size_t fixed, int tiles, const Args& a, LaunchLog& log) {
+  return run(diff_bwd_col<T, NGD, NGV, 1>, diff_bwd_col<T, NGD, NGV, 2>, blocks, heads, fixed,
+             group_floats(tiles, 32 * NGD + 16 * NGV), a, log);
 }
 
 template <typename T>
@@ -491,19 +642,20 @@ cudaError_t backward_t(const DiffProblem& p, const DiffTensors& t, const DiffWor
   Args a = make_args(p, t);
   a.D = ws.D;
   a.d2 = ws.d2;
-  const int blocks = (p.N + kM - 1) / kM;
-  const size_t floats =
-      (size_t)(kT + kM) * (2 * ld_of(p.d) + ld_of(p.dv)) + (size_t)kM * kLdp;
-  const int rows = p.B * p.H, cols = p.B * p.Hk;  // grids' heads
-  cudaError_t e = p.d <= 64 ? run(diff_bwd_row<T, 1>, blocks, rows, floats, a, log)
-                            : run(diff_bwd_row<T, 2>, blocks, rows, floats, a, log);
+  const int ld = ld_of(p.d), ldv = ld_of(p.dv), tiles = kT * (2 * ld + ldv) + kM * kLdp;
+  const int blocks = (p.N + kM - 1) / kM, rows = p.B * p.H, cols = p.B * p.Hk;
+  const size_t fixed = (size_t)kM * (2 * ld + ldv);
+  const cudaError_t e = p.d <= 64 ? run(diff_bwd_row<T, 1, 1>, diff_bwd_row<T, 1, 2>, blocks, rows,
+                                        fixed, group_floats(tiles, 32 + 4), a, log)
+                                  : run(diff_bwd_row<T, 2, 1>, diff_bwd_row<T, 2, 2>, blocks, rows,
+                                        fixed, group_floats(tiles, 64 + 4), a, log);
   if (e != cudaSuccess) return e;
-  const size_t cf = floats + 5 * kT;
+  const int ct = tiles + 5 * kT;
   if (p.d <= 64)
-    return p.dv <= 64 ? run(diff_bwd_col<T, 1, 1>, blocks, cols, cf, a, log)
-                      : run(diff_bwd_col<T, 1, 2>, blocks, cols, cf, a, log);
-  return p.dv <= 64 ? run(diff_bwd_col<T, 2, 1>, blocks, cols, cf, a, log)
-                    : run(diff_bwd_col<T, 2, 2>, blocks, cols, cf, a, log);
+    return p.dv <= 64 ? columns<T, 1, 1>(blocks, cols, fixed, ct, a, log)
+                      : columns<T, 1, 2>(blocks, cols, fixed, ct, a, log);
+  return p.dv <= 64 ? columns<T, 2, 1>(blocks, cols, fixed, ct, a, log)
+                    : columns<T, 2, 2>(blocks, cols, fixed, ct, a, log);
 }
 
 }  // namespace
