@@ -10,11 +10,11 @@
 // from the fp64 frequency to a 64-bit fixed-point fraction of a turn (its
 // product with 1 / 2 pi in two doubles); the 64-bit integer product with p
 // then wraps exactly where whole turns drop out.  The error is p 2^-63
-// turns.  The top 32 bits give the angle to sincospif.
+// turns.  The top 32 bits give sine and cosine.
 //
 // Bound: memory (x read once, y written once; positions and frequencies are a
 // few KB that stay in cache).  A thread owns a chunk of pairs of one
-// position and walks over a group of heads, so a sine and cosine (about 40
+// position and walks over a group of heads, so a sine and cosine (about 30
 // instructions) serve several heads, with 16-byte accesses where the strides
 // allow.
 #include <cuda_bf16.h>
@@ -28,7 +28,8 @@
 namespace fbob {
 namespace {
 
-constexpr int kThreads = 256;
+constexpr int kThreads = 128;
+constexpr int kSms = 152;
 
 struct RotaryArgs {
   const void* x;
@@ -92,6 +93,26 @@ struct Vec<float, 4> {
   __device__ void get(float (&f)[4]) const { f[0] = v.x; f[1] = v.y; f[2] = v.z; f[3] = v.w; }
   __device__ void set(const float (&f)[4]) { v = make_float4(f[0], f[1], f[2], f[3]); }
 };
+template <>
+struct Vec<float, 8> {
+  float4 v[2];
+  __device__ void load(const float* p) {
+    v[0] = reinterpret_cast<const float4*>(p)[0];
+    v[1] = reinterpret_cast<const float4*>(p)[1];
+  }
+  __device__ void store(float* p) const {
+    reinterpret_cast<float4*>(p)[0] = v[0];
+    reinterpret_cast<float4*>(p)[1] = v[1];
+  }
+  __device__ void get(float (&f)[8]) const {
+    f[0] = v[0].x; f[1] = v[0].y; f[2] = v[0].z; f[3] = v[0].w;
+    f[4] = v[1].x; f[5] = v[1].y; f[6] = v[1].z; f[7] = v[1].w;
+  }
+  __device__ void set(const float (&f)[8]) {
+    v[0] = make_float4(f[0], f[1], f[2], f[3]);
+    v[1] = make_float4(f[4], f[5], f[6], f[7]);
+  }
+};
 template <typename T>
 struct Vec<T, 1> {
   T v;
@@ -100,10 +121,6 @@ struct Vec<T, 1> {
   __device__ void get(float (&f)[1]) const { f[0] = to_f32<T>(v); }
   __device__ void set(const float (&f)[1]) { v = from_f32<T>(f[0]); }
 };
-
-// Pairs per thread of the vector form: 16-byte accesses of the wider type.
-template <typename TI, typename TO>
-constexpr int kPairs = (sizeof(TI) == 2 && sizeof(TO) == 2) ? 8 : 4;
 
 // Turns a chunk of P pairs held as two runs of P elements: the pairs' first
 // and second members (half layout), or its first and last P elements with
@@ -130,14 +147,90 @@ __device__ __forceinline__ void turn(float (&u)[P], float (&w)[P], const float (
   }
 }
 
+// Sine and cosine of hi 2^-32 turns: the nearest quarter turn is taken off (two
+// bits), and the rest, |x| <= pi / 4, goes into the Taylor series up to x^9 and
+// x^10, whose next terms are below 2e-9 x and 2e-10.
+__device__ __forceinline__ void sincos_turns(uint32_t hi, float& s, float& c) {
+  const uint32_t q = (hi + 0x20000000u) >> 30;
+  const float x = (float)(int)(hi - (q << 30)) * 1.4629180792671596e-9f;  // 2 pi 2^-32
+  const float y = x * x;
+  float a = fmaf(y, 1.f / 362880.f, -1.f / 5040.f);
+  a = fmaf(a, y, 1.f / 120.f);
+  a = fmaf(a, y, -1.f / 6.f);
+  a = fmaf(a * y, x, x);
+  float b = fmaf(y, -1.f / 3628800.f, 1.f / 40320.f);
+  b = fmaf(b, y, -1.f / 720.f);
+  b = fmaf(b, y, 1.f / 24.f);
+  b = fmaf(b, y, -0.5f);
+  b = fmaf(b, y, 1.f);
+  const bool odd = q & 1u;
+  s = odd ? b : a;
+  c = odd ? a : b;
+  if (q & 2u) s = -s;
+  if ((q + 1u) & 2u) c = -c;
+}
+
+// Heads whose loads are in flight together.
+template <typename TI, typename TO>
+constexpr int kHeads = (sizeof(TI) == 2 && sizeof(TO) == 2) ? 4 : 2;
+
 template <typename TI, typename TO, int P, bool INTERLEAVED>
 __global__ void __launch_bounds__(kThreads) rotary_kernel(RotaryArgs a) {
   extern __shared__ unsigned long long turns[];  // [half]: 2^64 f / 2 pi mod 2^64
+  constexpr int U = kHeads<TI, TO>;
+  const int chunks = a.d / (2 * P) + (P == 1 ? (a.d & 1) : 0);
+  const int rot_chunks = a.half / P;
+  const long long items = (long long)a.B * a.N * chunks;
+  const int h0 = blockIdx.y * a.heads, h1 = min(a.H, h0 + a.heads);
+  const long long id = (long long)blockIdx.x * kThreads + threadIdx.x;
+  const bool active = id < items;
+  int c = 0, n = 0, b = 0;
+  if (active) {
+    if (items <= 0xffffffffll) {  // 32-bit divisions where they do
+      const unsigned bn = (unsigned)id / (unsigned)chunks;
+      c = (int)((unsigned)id - bn * (unsigned)chunks);
+      b = (int)(bn / (unsigned)a.N);
+      n = (int)(bn - (unsigned)b * (unsigned)a.N);
+    } else {
+      const long long bn = id / chunks;
+      c = (int)(id - bn * chunks);
+      b = (int)(bn / a.N);
+      n = (int)(bn - (long long)b * a.N);
+    }
+  }
+  const bool turned = active && c < rot_chunks;
+  // offsets of the chunk's two halves of P elements
+  int e0, e1;
+  bool two = active;  // not for an odd width's last feature: one element
+  if (c < rot_chunks) {
+    e0 = INTERLEAVED ? 2 * P * c : P * c;
+    e1 = INTERLEAVED ? e0 + P : e0 + a.half;
+  } else {
+    e0 = 2 * a.half + (c - rot_chunks) * 2 * P;
+    e1 = e0 + P;
+    two = two && e1 < a.d;
+  }
+  const TI* __restrict__ x = static_cast<const TI*>(a.x) + b * a.xs[0] + n * a.xs[2];
+  TO* __restrict__ y = static_cast<TO*>(a.y) + b * a.ys[0] + n * a.ys[2];
+  Vec<TI, P> u[U], w[U];
+  auto load = [&](int hb) {
+#pragma unroll
+    for (int i = 0; i < U; ++i)
+      if (active && hb + i < h1) {
+        const TI* xp = x + (hb + i) * a.xs[1];
+        u[i].load(xp + e0);
+        if (two) w[i].load(xp + e1);
+      }
+  };
+  // the first heads and the position are on their way while the block makes
+  // its table of frequencies
+  load(h0);
+  const long long p = !turned ? 0 : a.positions ? a.positions[b * a.pos_sb + n] : a.offset + n;
   for (int i = threadIdx.x; i < a.half; i += kThreads) {
     // 1 / (2 pi) as a sum of two doubles: the product keeps about 100 bits
-    const double f = a.inv_freq[i], c = 0.15915494309189535, c2 = -9.839338337591243e-18;
-    const double hi = f * c;
-    const double lo = fma(f, c, -hi) + f * c2;
+    const double f = a.inv_freq[i], c1 = 0.15915494309189535, c2 = -9.839338337591243e-18;
+    const double hi = f * c1;
+    const double lo = fma(f, c1, -hi) + f * c2;
     const double r = hi - rint(hi);  // exact
     // both parts in units of 2^-64 turns; |r| <= 1/2, and 2^64 r is taken
     // as twice 2^63 r (an integer below 2^53 times a power of two)
@@ -146,65 +239,31 @@ __global__ void __launch_bounds__(kThreads) rotary_kernel(RotaryArgs a) {
     turns[i] = ((unsigned long long)(long long)whole << 1) + (unsigned long long)(long long)rint(rest);
   }
   __syncthreads();
-
-  const int chunks = a.d / (2 * P) + (P == 1 ? (a.d & 1) : 0);
-  const int rot_chunks = a.half / P;
-  const long long id = (long long)blockIdx.x * kThreads + threadIdx.x;
-  if (id >= (long long)a.B * a.N * chunks) return;
-  const int c = (int)(id % chunks);
-  const long long bn = id / chunks;
-  const int n = (int)(bn % a.N), b = (int)(bn / a.N);
-  const int h0 = blockIdx.y * a.heads, h1 = min(a.H, h0 + a.heads);
-  const TI* __restrict__ x = static_cast<const TI*>(a.x) + b * a.xs[0] + n * a.xs[2];
-  TO* __restrict__ y = static_cast<TO*>(a.y) + b * a.ys[0] + n * a.ys[2];
-
-  // offsets of the chunk's two halves of P elements
-  int e0, e1;
-  bool one = false;  // an odd width's last feature: one element
-  if (c < rot_chunks) {
-    e0 = INTERLEAVED ? 2 * P * c : P * c;
-    e1 = INTERLEAVED ? e0 + P : e0 + a.half;
-  } else {
-    e0 = 2 * a.half + (c - rot_chunks) * 2 * P;
-    e1 = e0 + P;
-    one = e1 >= a.d;
-  }
   float cs[P], sn[P];
-  if (c < rot_chunks) {
-    const long long p = a.positions ? a.positions[b * a.pos_sb + n] : a.offset + n;
+  if (turned) {
 #pragma unroll
     for (int i = 0; i < P; ++i) {
       const unsigned long long t = (unsigned long long)p * turns[c * P + i];
-      const int hi = (int)((t + 0x80000000ull) >> 32);
       float s, co;
-      sincospif((float)hi * 4.656612873077393e-10f, &s, &co);  // half turns: hi 2^-31
+      sincos_turns((uint32_t)((t + 0x80000000ull) >> 32), s, co);
       cs[i] = co * a.magnitude;
       sn[i] = s * a.magnitude * a.sign;
     }
   }
-  // four heads at a time: their loads are in flight together
-  constexpr int U = 4;
   for (int hb = h0; hb < h1; hb += U) {
-    Vec<TI, P> u[U], w[U];
+    if (hb > h0) load(hb);
 #pragma unroll
     for (int i = 0; i < U; ++i)
-      if (hb + i < h1) {
-        const TI* xp = x + (hb + i) * a.xs[1];
-        u[i].load(xp + e0);
-        if (!one) w[i].load(xp + e1);
-      }
-#pragma unroll
-    for (int i = 0; i < U; ++i)
-      if (hb + i < h1) {
+      if (active && hb + i < h1) {
         float fu[P], fw[P];
         u[i].get(fu);
-        if (!one) w[i].get(fw);
-        if (c < rot_chunks) turn<P, INTERLEAVED>(fu, fw, cs, sn);
+        if (two) w[i].get(fw);
+        if (turned) turn<P, INTERLEAVED>(fu, fw, cs, sn);
         TO* yp = y + (hb + i) * a.ys[1];
         Vec<TO, P> r;
         r.set(fu);
         r.store(yp + e0);
-        if (!one) {
+        if (two) {
           r.set(fw);
           r.store(yp + e1);
         }
@@ -213,10 +272,14 @@ __global__ void __launch_bounds__(kThreads) rotary_kernel(RotaryArgs a) {
 }
 
 template <typename TI, typename TO, int P, bool INTERLEAVED>
-cudaError_t launch(const RotaryArgs& a, LaunchLog& log) {
-  const int chunks = a.d / (2 * P) + (P == 1 ? (a.d & 1) : 0);
-  const long long ids = (long long)a.B * a.N * chunks;
-  dim3 grid((unsigned)((ids + kThreads - 1) / kThreads), (unsigned)((a.H + a.heads - 1) / a.heads));
+cudaError_t launch(RotaryArgs a, LaunchLog& log) {
+  const long long items = (long long)a.B * a.N * (a.d / (2 * P) + (P == 1 ? (a.d & 1) : 0));
+  // heads per thread: as many as leave half a wave of threads, so that
+  // few sines are computed; one where the call is small and latency counts
+  a.heads = 16;
+  while (a.heads > 1 && items * ((a.H + a.heads - 1) / a.heads) < kSms * 1024ll) a.heads /= 2;
+  const int groups = (a.H + a.heads - 1) / a.heads;
+  dim3 grid((unsigned)((items + kThreads - 1) / kThreads), (unsigned)groups);
   rotary_kernel<TI, TO, P, INTERLEAVED>
       <<<grid, kThreads, sizeof(unsigned long long) * a.half, log.stream>>>(a);
   const cudaError_t e = cudaGetLastError();
@@ -224,23 +287,30 @@ cudaError_t launch(const RotaryArgs& a, LaunchLog& log) {
   return e;
 }
 
+// Whether chunks of P pairs tile the turned and the copied part and every
+// access is aligned (16 bytes, or all P elements where they are fewer).
+template <typename TI, typename TO, int P>
+bool chunked(const RotaryArgs& a) {
+  constexpr size_t ai = P * sizeof(TI) < 16 ? P * sizeof(TI) : 16;
+  constexpr size_t ao = P * sizeof(TO) < 16 ? P * sizeof(TO) : 16;
+  bool ok = a.half % P == 0 && (a.d - 2 * a.half) % (2 * P) == 0 &&
+            reinterpret_cast<uintptr_t>(a.x) % ai == 0 && reinterpret_cast<uintptr_t>(a.y) % ao == 0;
+  for (int i = 0; i < 3; ++i)
+    ok = ok && a.xs[i] * (long long)sizeof(TI) % (long long)ai == 0 &&
+         a.ys[i] * (long long)sizeof(TO) % (long long)ao == 0;
+  return ok;
+}
+
+template <typename TI, typename TO, bool INTERLEAVED>
+cudaError_t dispatch(const RotaryArgs& a, LaunchLog& log) {
+  if (chunked<TI, TO, 8>(a)) return launch<TI, TO, 8, INTERLEAVED>(a, log);
+  if (chunked<TI, TO, 4>(a)) return launch<TI, TO, 4, INTERLEAVED>(a, log);
+  return launch<TI, TO, 1, INTERLEAVED>(a, log);
+}
+
 template <typename TI, typename TO>
-cudaError_t dispatch(RotaryArgs a, bool interleaved, LaunchLog& log) {
-  constexpr int P = kPairs<TI, TO>;
-  // vector form: whole chunks in the turned and the copied part, and every
-  // access of P elements aligned to its size
-  bool vec = a.half % P == 0 && (a.d - 2 * a.half) % (2 * P) == 0 &&
-             reinterpret_cast<uintptr_t>(a.x) % (P * sizeof(TI)) == 0 &&
-             reinterpret_cast<uintptr_t>(a.y) % (P * sizeof(TO)) == 0;
-  for (int i = 0; i < 3; ++i) vec = vec && a.xs[i] % P == 0 && a.ys[i] % P == 0;
-  // heads per thread: as many as leave the GPU two waves of threads, so that
-  // few sines are computed; one where the call is small and latency counts
-  const long long ids = (long long)a.B * a.N * (vec ? a.d / (2 * P) : (a.d + 1) / 2);
-  a.heads = 16;
-  while (a.heads > 1 && ids * ((a.H + a.heads - 1) / a.heads) < 2ll * 152 * 2048) a.heads /= 2;
-  if (vec)
-    return interleaved ? launch<TI, TO, P, true>(a, log) : launch<TI, TO, P, false>(a, log);
-  return interleaved ? launch<TI, TO, 1, true>(a, log) : launch<TI, TO, 1, false>(a, log);
+cudaError_t dispatch(const RotaryArgs& a, bool interleaved, LaunchLog& log) {
+  return interleaved ? dispatch<TI, TO, true>(a, log) : dispatch<TI, TO, false>(a, log);
 }
 
 }  // namespace
