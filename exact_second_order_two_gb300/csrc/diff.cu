@@ -2,7 +2,10 @@
 // kernel family), the row scalars of its backward and the gradient of lam.
 //
 // D^m_i = dO_i . O^m_i comes from the saved O = O^1 - lam O^2 and O^2:
-// D^2 = dO . O^2 and D^1 = dO . O + lam D^2.  lam's gradient, dlam_i =
+// D^2 = dO . O^2 and D^1 = dO . O + lam D^2.  With O rounded to bf16, D^1 would
+// add the rounding to every dS of its row (the gradients of q and k then had
+// 1.49 times the error of their own rounding); so what the rounding left off is
+// kept beside O^2, and only O^2's is left (1.45 times).  lam's gradient, dlam_i =
 // -dO_i . O^2_i, is summed over what shares a value of lam (per head, or over
 // everything).  Those sums cancel, so a rounded O^2 is not good enough for
 // them: the pass that computes dQ also sums P^2_ij dP_ij over j in fp32, the
@@ -82,16 +85,19 @@ __device__ __forceinline__ void lam_store(void* p, int bf16, size_t i, float x) 
 // D^1 and D^2 of every row, one warp per row.
 template <typename T>
 __global__ void __launch_bounds__(256)
-    diff_row_scalars(const T* __restrict__ o, const T* __restrict__ o2, const T* __restrict__ dO,
+    diff_row_scalars(const T* __restrict__ o, const T* __restrict__ rest, const T* __restrict__ dO,
                      LamArg lam, float* __restrict__ D, size_t rows, int H, int N, int dv) {
+  constexpr int R = sizeof(T) == 2 ? 2 : 1;
   const size_t row = (size_t)blockIdx.x * 8 + (threadIdx.x >> 5);
   const int lane = threadIdx.x & 31;
   if (row >= rows) return;
   float s1 = 0.f, s2 = 0.f;
   for (int c = lane; c < dv; c += 32) {
     const float g = to_f32<T>(dO[row * dv + c]);
-    s1 = fmaf(g, to_f32<T>(o[row * dv + c]), s1);
-    s2 = fmaf(g, to_f32<T>(o2[row * dv + c]), s2);
+    float out = to_f32<T>(o[row * dv + c]);
+    if (R == 2) out += to_f32<T>(rest[(row * R + 1) * dv + c]);
+    s1 = fmaf(g, out, s1);
+    s2 = fmaf(g, to_f32<T>(rest[row * R * dv + c]), s2);
   }
   s1 = warp_sum(s1);
   s2 = warp_sum(s2);
@@ -151,7 +157,7 @@ cudaError_t row_scalars(const DiffProblem& p, const DiffTensors& t, const DiffWo
                         LaunchLog& log) {
   const size_t rows = p.rows();
   diff_row_scalars<T><<<(unsigned)((rows + 7) / 8), 256, 0, log.stream>>>(
-      static_cast<const T*>(t.o), static_cast<const T*>(t.o2), static_cast<const T*>(t.dO), t.lam,
+      static_cast<const T*>(t.o), static_cast<const T*>(t.rest), static_cast<const T*>(t.dO), t.lam,
       ws.D, rows, p.H, p.N, p.dv);
   const cudaError_t e = cudaGetLastError();
   log.mark();
@@ -213,18 +219,18 @@ int fbob_diff_path(int op, const fbob_diff_shape_t* shape) {
 }
 
 int fbob_diff_forward(const fbob_diff_shape_t* shape, const void* q, const void* k, const void* v,
-                      const void* lam, void* o, void* o2, float* lse, void* ws_ptr,
+                      const void* lam, void* o, void* rest, float* lse, void* ws_ptr,
                       size_t ws_bytes, void* stream) {
   DiffProblem p;
   int path;
   DiffWorkspace ws;
   LaunchLog log{static_cast<cudaStream_t>(stream)};
-  if (!given({q, k, v, o, lse}) || !aligned(o2, 16) || !lam) return FBOB_ERR_INVALID_ARG;
+  if (!given({q, k, v, o, lse}) || !aligned(rest, 16) || !lam) return FBOB_ERR_INVALID_ARG;
   const int st = prologue(FBOB_OP_FORWARD, shape, ws_ptr, ws_bytes, log.stream, &p, &path, &ws);
   if (st != FBOB_OK) return st;
   if (!aligned(lam, p.lam_bf16 ? 2 : 4)) return FBOB_ERR_INVALID_ARG;
   DiffTensors t{};
-  t.q = q; t.k = k; t.v = v; t.o = o; t.o2 = o2; t.lse = lse;
+  t.q = q; t.k = k; t.v = v; t.o = o; t.rest = rest; t.lse = lse;
   t.lam = LamArg{lam, p.lam_kind, p.lam_bf16};
   begin_call(log);
   const cudaError_t e = path == FBOB_PATH_TCGEN05 ? diff_tc_forward(p, t, ws, log)
@@ -234,14 +240,14 @@ int fbob_diff_forward(const fbob_diff_shape_t* shape, const void* q, const void*
 }
 
 int fbob_diff_backward(const fbob_diff_shape_t* shape, const void* q, const void* k, const void* v,
-                       const void* lam, const void* o, const void* o2, const float* lse,
+                       const void* lam, const void* o, const void* rest, const float* lse,
                        const void* dO, void* dq, void* dk, void* dv, void* dlam, void* ws_ptr,
                        size_t ws_bytes, void* stream) {
   DiffProblem p;
   int path;
   DiffWorkspace ws;
   LaunchLog log{static_cast<cudaStream_t>(stream)};
-  if (!given({q, k, v, o, o2, lse, dO, dq, dk, dv}) || !lam || !dlam) return FBOB_ERR_INVALID_ARG;
+  if (!given({q, k, v, o, rest, lse, dO, dq, dk, dv}) || !lam || !dlam) return FBOB_ERR_INVALID_ARG;
   const int st = prologue(FBOB_OP_BACKWARD, shape, ws_ptr, ws_bytes, log.stream, &p, &path, &ws);
   if (st != FBOB_OK) return st;
   const size_t la = p.lam_bf16 ? 2 : 4;
@@ -249,7 +255,7 @@ int fbob_diff_backward(const fbob_diff_shape_t* shape, const void* q, const void
   DiffTensors t{};
   t.q = q; t.k = k; t.v = v; t.dO = dO;
   t.o = const_cast<void*>(o);
-  t.o2 = const_cast<void*>(o2);
+  t.rest = const_cast<void*>(rest);
   t.lse = const_cast<float*>(lse);
   t.dq = dq; t.dk = dk; t.dv = dv;
   t.lam = LamArg{lam, p.lam_kind, p.lam_bf16};

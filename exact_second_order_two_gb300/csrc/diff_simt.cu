@@ -46,7 +46,7 @@ __host__ __device__ inline int group_floats(int tiles, int sums) {
 
 struct Args {
   const void *q, *k, *v, *dO;
-  void *o, *o2, *dq, *dk, *dv;
+  void *o, *rest, *dq, *dk, *dv;
   float* lse;
   const float* D;
   float* d2;
@@ -181,7 +181,7 @@ __device__ __forceinline__ void put_tile(float* P, const float (&s)[4][4], int t
 
 template <typename T, int NG>
 __device__ __forceinline__ void store_rows(T* dst, const float (&acc)[4][4 * NG], float mul, int row0,
-                                           int N, int width, int ty, int tx) {
+                                           int N, int width, int stride, int ty, int tx) {
 #pragma unroll
   for (int i = 0; i < 4; ++i) {
     const int r = row0 + 4 * ty + i;
@@ -191,7 +191,7 @@ __device__ __forceinline__ void store_rows(T* dst, const float (&acc)[4][4 * NG]
 #pragma unroll
       for (int e = 0; e < 4; ++e) {
         const int c = 4 * tx + 64 * g + e;
-        if (c < width) dst[(size_t)r * width + c] = from_f32<T>(mul * acc[i][4 * g + e]);
+        if (c < width) dst[(size_t)r * stride + c] = from_f32<T>(mul * acc[i][4 * g + e]);
       }
   }
 }
@@ -344,8 +344,18 @@ __global__ void __launch_bounds__(SPLIT * kThreads) diff_fwd(Args a) {
     }
   }
   const size_t ob = (size_t)bh * N * a.dv_;
-  store_rows<T, NGV>(static_cast<T*>(a.o) + ob, acc[0], 1.f, row0, N, a.dv_, ty, tx);
-  if (a.o2) store_rows<T, NGV>(static_cast<T*>(a.o2) + ob, acc[1], 1.f, row0, N, a.dv_, ty, tx);
+  store_rows<T, NGV>(static_cast<T*>(a.o) + ob, acc[0], 1.f, row0, N, a.dv_, a.dv_, ty, tx);
+  if (!a.rest) return;
+  constexpr int R = sizeof(T) == 2 ? 2 : 1;
+  T* rest = static_cast<T*>(a.rest) + R * ob;
+  store_rows<T, NGV>(rest, acc[1], 1.f, row0, N, a.dv_, R * a.dv_, ty, tx);
+  if constexpr (R == 2) {  // what the rounding of o left off
+#pragma unroll
+    for (int i = 0; i < 4; ++i)
+#pragma unroll
+      for (int e = 0; e < 4 * NGV; ++e) acc[0][i][e] -= to_f32<T>(from_f32<T>(acc[0][i][e]));
+    store_rows<T, NGV>(rest + a.dv_, acc[0], 1.f, row0, N, a.dv_, R * a.dv_, ty, tx);
+  }
 }
 
 // ---- dQ: one block per 32 query rows of a head -----------------------------
@@ -461,7 +471,7 @@ __global__ void __launch_bounds__(SPLIT * kThreads) diff_bwd_row(Args a) {
 #pragma unroll
   for (int m = 0; m < 2; ++m)
     store_rows<T, NGD>(static_cast<T*>(a.dq) + ((size_t)bh * 2 + m) * qsz, acc[m], a.scale, row0, N,
-                       a.d, ty, tx);
+                       a.d, a.d, ty, tx);
 }
 
 // ---- dK, dV: one block per 32 keys of a key head, over its query heads ------
@@ -578,15 +588,15 @@ __global__ void __launch_bounds__(SPLIT * kThreads) diff_bwd_col(Args a) {
 #pragma unroll
   for (int m = 0; m < 2; ++m)
     store_rows<T, NGD>(static_cast<T*>(a.dk) + ((size_t)kvh * 2 + m) * qsz, ak[m], a.scale, col0, N,
-                       a.d, ty, tx);
-  store_rows<T, NGV>(static_cast<T*>(a.dv) + (size_t)kvh * N * a.dv_, av, 1.f, col0, N, a.dv_, ty,
-                     tx);
+                       a.d, a.d, ty, tx);
+  store_rows<T, NGV>(static_cast<T*>(a.dv) + (size_t)kvh * N * a.dv_, av, 1.f, col0, N, a.dv_, a.dv_,
+                     ty, tx);
 }
 
 Args make_args(const DiffProblem& p, const DiffTensors& t) {
   Args a{};
   a.q = t.q; a.k = t.k; a.v = t.v; a.dO = t.dO;
-  a.o = t.o; a.o2 = t.o2; a.dq = t.dq; a.dk = t.dk; a.dv = t.dv;
+  a.o = t.o; a.rest = t.rest; a.dq = t.dq; a.dk = t.dk; a.dv = t.dv;
   a.lse = t.lse;
   a.lam = t.lam;
   a.H = p.H; a.G = p.G(); a.N = p.N; a.d = p.d; a.dv_ = p.dv; a.causal = p.causal;

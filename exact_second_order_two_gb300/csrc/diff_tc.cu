@@ -172,7 +172,7 @@ struct Fwd {
 };
 
 struct FwdParams : Common {
-  __nv_bfloat16 *o, *o2;
+  __nv_bfloat16 *o, *rest;  // rest: O^2, and what o's rounding left off (or null)
   float* lse;
 };
 
@@ -396,27 +396,31 @@ __global__ void __launch_bounds__(kFwdThreads, 1)
     const bool in = i < N;
     const float inv1 = 1.f / L[0], inv2 = 1.f / L[1];
     const float w = in ? lam_row(prm.lam, bh, prm.H, N, i) : 0.f;
-    const size_t at = ((size_t)bh * N + (in ? i : 0)) * DV + f0;
+    const size_t r = (size_t)bh * N + (in ? i : 0);
 #pragma unroll
-    for (int c = 0; c < PART; c += 16) {
+    for (int c = f0; c < f0 + PART; c += 16) {
       uint32_t a[16], b[16];
-      tmem_ld16x2(tmem + lane_off + C::T_O(0) + f0 + c, tmem + lane_off + C::T_O(1) + f0 + c, a, b);
-      uint32_t wo[8], w2[8];
+      tmem_ld16x2(tmem + lane_off + C::T_O(0) + c, tmem + lane_off + C::T_O(1) + c, a, b);
+      uint32_t wo[8], w2[8], wl[8];
 #pragma unroll
       for (int e = 0; e < 8; ++e) {
         const float x2 = __uint_as_float(b[2 * e]) * inv2, y2 = __uint_as_float(b[2 * e + 1]) * inv2;
-        wo[e] = pack_bf16(fmaf(-w, x2, __uint_as_float(a[2 * e]) * inv1),
-                          fmaf(-w, y2, __uint_as_float(a[2 * e + 1]) * inv1));
+        const float x = fmaf(-w, x2, __uint_as_float(a[2 * e]) * inv1);
+        const float y = fmaf(-w, y2, __uint_as_float(a[2 * e + 1]) * inv1);
+        wo[e] = pack_bf16(x, y);
         w2[e] = pack_bf16(x2, y2);
+        const float2 back = __bfloat1622float2(*reinterpret_cast<const __nv_bfloat162*>(&wo[e]));
+        wl[e] = pack_bf16(x - back.x, y - back.y);
       }
+      auto put = [&](__nv_bfloat16* dst, const uint32_t (&v)[8]) {
+        reinterpret_cast<uint4*>(dst)[0] = make_uint4(v[0], v[1], v[2], v[3]);
+        reinterpret_cast<uint4*>(dst)[1] = make_uint4(v[4], v[5], v[6], v[7]);
+      };
       if (in) {
-        uint4* po = reinterpret_cast<uint4*>(prm.o + at + c);
-        po[0] = make_uint4(wo[0], wo[1], wo[2], wo[3]);
-        po[1] = make_uint4(wo[4], wo[5], wo[6], wo[7]);
-        if (prm.o2) {
-          uint4* p2 = reinterpret_cast<uint4*>(prm.o2 + at + c);
-          p2[0] = make_uint4(w2[0], w2[1], w2[2], w2[3]);
-          p2[1] = make_uint4(w2[4], w2[5], w2[6], w2[7]);
+        put(prm.o + r * DV + c, wo);
+        if (prm.rest) {
+          put(prm.rest + 2 * r * DV + c, w2);
+          put(prm.rest + (2 * r + 1) * DV + c, wl);
         }
       }
     }
@@ -432,7 +436,8 @@ __global__ void __launch_bounds__(kFwdThreads, 1)
 }
 
 // ===========================================================================
-// Row scalars: D^2 = dO . O^2, D^1 = dO . O + lam D^2 (O = O^1 - lam O^2)
+// Row scalars: D^2 = dO . O^2, D^1 = dO . O + lam D^2 (O = O^1 - lam O^2, with
+// what its rounding left off)
 // ===========================================================================
 // acc + the dot product of 8 bf16 pairs, in fp32
 __device__ __forceinline__ float dot8(const uint4& a, const uint4& b, float acc) {
@@ -447,10 +452,10 @@ __device__ __forceinline__ float dot8(const uint4& a, const uint4& b, float acc)
 }
 
 // DV/8 lanes per row, 16 bytes of each tensor per lane; a block takes 64 rows
-// of one head.  Bound: memory (O, O^2 and dO read once).
+// of one head.  Bound: memory (O, rest and dO read once).
 template <int DV>
 __global__ void __launch_bounds__(256, 4)
-    diff_tc_scalars(const uint4* __restrict__ o, const uint4* __restrict__ o2,
+    diff_tc_scalars(const uint4* __restrict__ o, const uint4* __restrict__ rest,
                     const uint4* __restrict__ dO, const float* __restrict__ lse, LamArg lam,
                     float* __restrict__ scal, int H, int N) {
   constexpr int L = DV / 8, ROWS = 256 / L, STEPS = 64 / ROWS;
@@ -472,10 +477,10 @@ __global__ void __launch_bounds__(256, 4)
     const int r = i * ROWS + sub;
     s1[i] = s2[i] = 0.f;
     if (n0 + r < N) {
-      const size_t e = ((size_t)bh * N + n0 + r) * L + c;
-      const uint4 g = dO[e];
-      s1[i] = dot8(o[e], g, 0.f);
-      s2[i] = dot8(o2[e], g, 0.f);
+      const size_t row = (size_t)bh * N + n0 + r;
+      const uint4 g = dO[row * L + c];
+      s1[i] = dot8(o[row * L + c], g, dot8(rest[(2 * row + 1) * L + c], g, 0.f));
+      s2[i] = dot8(rest[2 * row * L + c], g, 0.f);
     }
   }
 #pragma unroll
@@ -1073,7 +1078,7 @@ cudaError_t forward_dv(const DiffProblem& p, const DiffTensors& t, const DiffWor
   FwdParams f;
   static_cast<Common&>(f) = common(p, t, ws, p.B * p.H);
   f.o = static_cast<__nv_bfloat16*>(t.o);
-  f.o2 = static_cast<__nv_bfloat16*>(t.o2);
+  f.rest = static_cast<__nv_bfloat16*>(t.rest);
   f.lse = t.lse;
   return run(diff_fwd_pass<DV>, f.units, p.N, kFwdThreads, Fwd<DV>::SMEM, log, f, mQ, mK, mV);
 }
@@ -1088,7 +1093,7 @@ cudaError_t backward_dv(const DiffProblem& p, const DiffTensors& t, const DiffWo
     return cudaErrorInvalidValue;
   const int blocks = (p.N + 63) / 64 * p.B * p.H;
   diff_tc_scalars<DV><<<blocks, 256, 0, log.stream>>>(
-      static_cast<const uint4*>(t.o), static_cast<const uint4*>(t.o2),
+      static_cast<const uint4*>(t.o), static_cast<const uint4*>(t.rest),
       static_cast<const uint4*>(t.dO), t.lse, t.lam, ws.scal, p.H, p.N);
   cudaError_t e = cudaGetLastError();
   log.mark();

@@ -44,7 +44,8 @@ struct DiffWorkspace {
 struct DiffTensors {
   const void *q, *k, *v;
   LamArg lam;
-  void *o, *o2;  // o2 may be null in the forward
+  // rest [B,H,N,R,dv]: P^2 V and, for bf16, O - o (null: not wanted)
+  void *o, *rest;
   float* lse;    // [B, 2H, N]
   const void* dO;
   void *dq, *dk, *dv;

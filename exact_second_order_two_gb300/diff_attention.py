@@ -79,6 +79,10 @@ def _match(name, t, shape, dtype, device):
         raise ValueError(f"{name} must be contiguous {dtype} {tuple(shape)} on {device}")
 
 
+def _rest_shape(shp):
+    return (shp.B, shp.H, shp.N, 2 if shp.dtype == _b.DTYPES[torch.bfloat16] else 1, shp.dv)
+
+
 def _workspace(op, shp, device):
     n = _b.lib().fbob_diff_workspace_size(op, ctypes.byref(shp))
     if n == 0:
@@ -87,10 +91,12 @@ def _workspace(op, shp, device):
 
 
 def diff_forward(q, k, v, lam, causal: bool = False, scale: float | None = None,
-                 need_o2: bool = True, workspace=None):
-    """Differential attention forward: returns (O, O2, LSE), with
-    O2 = softmax(c Q2 K2^T) V, or None where ``need_o2`` is false, and LSE
-    [B, 2H, N] the rows' log-sum-exp of both maps.
+                 need_rest: bool = True, workspace=None):
+    """Differential attention forward: returns (O, rest, LSE).  rest is what
+    else ``diff_backward`` reads, or None where ``need_rest`` is false:
+    [B, H, N, 1, dv] with O2 = softmax(c Q2 K2^T) V for fp32, [B, H, N, 2, dv]
+    with O2 and what the rounding of O left off for bf16.  LSE [B, 2H, N] holds
+    the rows' log-sum-exp of both maps.
 
     q: [B, 2H, N, d], the two queries of head h as heads 2h and 2h + 1;
     k: [B, 2Hk, N, d] likewise; v: [B, Hk, N, dv], with H a multiple of Hk
@@ -100,28 +106,28 @@ def diff_forward(q, k, v, lam, causal: bool = False, scale: float | None = None,
     """
     shp = _shape(q, k, v, lam, causal, scale)
     o = torch.empty((shp.B, shp.H, shp.N, shp.dv), dtype=q.dtype, device=q.device)
-    o2 = torch.empty_like(o) if need_o2 else None
+    rest = torch.empty(_rest_shape(shp), dtype=q.dtype, device=q.device) if need_rest else None
     lse = torch.empty((shp.B, 2 * shp.H, shp.N), dtype=torch.float32, device=q.device)
     ws = _workspace(_b.OP_FORWARD, shp, q.device) if workspace is None else workspace
     _b.call_on(q.device, "fbob_diff_forward", _b.lib().fbob_diff_forward, ctypes.byref(shp),
                q.data_ptr(), k.data_ptr(), v.data_ptr(), lam.data_ptr(), o.data_ptr(),
-               None if o2 is None else o2.data_ptr(), lse.data_ptr(), ws.data_ptr(), ws.numel())
-    return o, o2, lse
+               None if rest is None else rest.data_ptr(), lse.data_ptr(), ws.data_ptr(), ws.numel())
+    return o, rest, lse
 
 
-def diff_backward(q, k, v, lam, o, o2, lse, do, causal: bool = False,
+def diff_backward(q, k, v, lam, o, rest, lse, do, causal: bool = False,
                   scale: float | None = None, workspace=None):
     """First backward for upstream gradient ``do`` and the forward's results:
     returns (dQ, dK, dV, dlam), of the inputs' shapes and dtypes."""
     shp = _shape(q, k, v, lam, causal, scale)
     rows = (shp.B, shp.H, shp.N, shp.dv)
-    for name, t in (("o", o), ("o2", o2), ("do", do)):
-        _match(name, t, rows, q.dtype, q.device)
+    for name, t, shape in (("o", o, rows), ("rest", rest, _rest_shape(shp)), ("do", do, rows)):
+        _match(name, t, shape, q.dtype, q.device)
     _match("lse", lse, (shp.B, 2 * shp.H, shp.N), torch.float32, q.device)
     dq, dk, dv, dlam = (torch.empty_like(t) for t in (q, k, v, lam))
     ws = _workspace(_b.OP_BACKWARD, shp, q.device) if workspace is None else workspace
     _b.call_on(q.device, "fbob_diff_backward", _b.lib().fbob_diff_backward, ctypes.byref(shp),
-               *(t.data_ptr() for t in (q, k, v, lam, o, o2, lse, do, dq, dk, dv, dlam, ws)),
+               *(t.data_ptr() for t in (q, k, v, lam, o, rest, lse, do, dq, dk, dv, dlam, ws)),
                ws.numel())
     return dq, dk, dv, dlam
 
@@ -142,10 +148,10 @@ class _DiffBackward(torch.autograd.Function):
     on each map."""
 
     @staticmethod
-    def forward(ctx, q, k, v, lam, do, o, o2, lse, causal, scale):
+    def forward(ctx, q, k, v, lam, do, o, rest, lse, causal, scale):
         do = _contig(do)
-        grads = diff_backward(q, k, v, lam, o, o2, lse, do, causal, scale)
-        ctx.save_for_backward(q, k, v, lam, do, o, o2, lse)
+        grads = diff_backward(q, k, v, lam, o, rest, lse, do, causal, scale)
+        ctx.save_for_backward(q, k, v, lam, do, o, rest, lse)
         ctx.causal, ctx.scale = causal, scale
         ctx.set_materialize_grads(False)
         return grads
@@ -153,7 +159,8 @@ class _DiffBackward(torch.autograd.Function):
     @staticmethod
     @torch.autograd.function.once_differentiable
     def backward(ctx, gq, gk, gv, glam):
-        q, k, v, lam, do, o, o2, lse = ctx.saved_tensors
+        q, k, v, lam, do, o, rest, lse = ctx.saved_tensors
+        o2 = rest[..., 0, :].contiguous()
         none = (None,) * 5
         if gq is None and gk is None and gv is None and glam is None:
             return (None,) * 5 + none
@@ -174,7 +181,10 @@ class _DiffBackward(torch.autograd.Function):
 
         w = _rows(lam, B, H, N)
         vv, gvv = fit(v, Hk), fit(gv, Hk)
-        o1 = (o.float() + w * o2.float()).to(dtype)
+        o1 = o.float() + w * o2.float()
+        if rest.shape[3] == 2:
+            o1 += rest[..., 1, :].float()
+        o1 = o1.to(dtype)
         gdo = torch.zeros(do.shape, dtype=torch.float32, device=do.device)
         grad_lam = torch.zeros((B, H, N), dtype=torch.float32, device=do.device)
         gradq, gradk, gradv = [], [], torch.zeros((B, H, N, wide), dtype=torch.float32,
@@ -218,20 +228,20 @@ class _DiffBackward(torch.autograd.Function):
 class _DiffAttention(torch.autograd.Function):
     @staticmethod
     def forward(ctx, q, k, v, lam, causal, scale):
-        o, o2, lse = diff_forward(q, k, v, lam, causal, scale)
-        ctx.save_for_backward(q, k, v, lam, o, o2, lse)
+        o, rest, lse = diff_forward(q, k, v, lam, causal, scale)
+        ctx.save_for_backward(q, k, v, lam, o, rest, lse)
         ctx.causal, ctx.scale = causal, scale
         return o
 
     @staticmethod
     def backward(ctx, do):
-        q, k, v, lam, o, o2, lse = ctx.saved_tensors
-        # o, o2 and lse enter as values: the second derivative's paths through
+        q, k, v, lam, o, rest, lse = ctx.saved_tensors
+        # o, rest and lse enter as values: the second derivative's paths through
         # them are part of what fbob_bob returns
         if torch.is_grad_enabled():
-            grads = _DiffBackward.apply(q, k, v, lam, do, o.detach(), o2, lse, ctx.causal, ctx.scale)
+            grads = _DiffBackward.apply(q, k, v, lam, do, o.detach(), rest, lse, ctx.causal, ctx.scale)
         else:
-            grads = diff_backward(q, k, v, lam, o, o2, lse, _contig(do), ctx.causal, ctx.scale)
+            grads = diff_backward(q, k, v, lam, o, rest, lse, _contig(do), ctx.causal, ctx.scale)
         return tuple(grads) + (None, None)
 
 
@@ -252,5 +262,5 @@ def diff_attention(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, lam: torch
     if torch.is_grad_enabled() and (q.requires_grad or k.requires_grad or v.requires_grad
                                     or lam.requires_grad):
         return _DiffAttention.apply(q, k, v, lam, bool(causal), float(scale))
-    # no backward can follow: O2 is not written
-    return diff_forward(q, k, v, lam, bool(causal), float(scale), need_o2=False)[0]
+    # no backward can follow: rest is not written
+    return diff_forward(q, k, v, lam, bool(causal), float(scale), need_rest=False)[0]

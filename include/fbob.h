@@ -252,8 +252,9 @@ int fbob_rotary(const fbob_rotary_t* r, const void* x, const double* inv_freq,
  * difference:
  *   P^m = softmax(c Q^m K^mT),  m = 1, 2,   O = P^1 V - lam P^2 V.
  * Layouts, all dense and row-major: q [B,2H,N,d] with Q^1, Q^2 of head h as
- * heads 2h, 2h + 1; k [B,2Hk,N,d] likewise; v [B,Hk,N,dv]; o, o2, dO
- * [B,H,N,dv]; lse [B,2H,N] fp32.  H is a multiple of Hk: query head h reads
+ * heads 2h, 2h + 1; k [B,2Hk,N,d] likewise; v [B,Hk,N,dv]; o, dO
+ * [B,H,N,dv]; lse [B,2H,N] fp32; rest [B,H,N,R,dv], R = 1 for fp32: P^2 V, and
+ * R = 2 for bf16: P^2 V and O - o, what o's rounding left off.  H is a multiple of Hk: query head h reads
  * key head h / (H / Hk).  lam is one value, [H], or [B,H,N], bf16 or fp32.
  * Masking, ownership, asynchrony and alignment as above (lam to its own
  * size); scale > 0.  1 <= d, dv <= 128, B*H <= 32767.  fp32, and bf16 at head
@@ -275,10 +276,10 @@ typedef struct {
 size_t fbob_diff_workspace_size(int op, const fbob_diff_shape_t* shape);
 int fbob_diff_path(int op, const fbob_diff_shape_t* shape);
 
-/* o = O and lse = the log-sum-exp of both maps' rows.  o2 = P^2 V, which the
+/* o = O and lse = the log-sum-exp of both maps' rows.  rest is what else the
  * backward reads, or NULL where no backward follows. */
 int fbob_diff_forward(const fbob_diff_shape_t* shape, const void* q, const void* k, const void* v,
-                      const void* lam, void* o, void* o2, float* lse, void* ws, size_t ws_bytes,
+                      const void* lam, void* o, void* rest, float* lse, void* ws, size_t ws_bytes,
                       void* stream);
 
 /* Gradients of <dO, O>: with dP = dO V^T, D^m = rowsum(dO * P^m V),
@@ -288,7 +289,7 @@ int fbob_diff_forward(const fbob_diff_shape_t* shape, const void* q, const void*
  * dk and dv sum over the query heads that share a key head.  dlam has lam's
  * shape and dtype. */
 int fbob_diff_backward(const fbob_diff_shape_t* shape, const void* q, const void* k,
-                       const void* v, const void* lam, const void* o, const void* o2,
+                       const void* v, const void* lam, const void* o, const void* rest,
                        const float* lse, const void* dO, void* dq, void* dk, void* dv, void* dlam,
                        void* ws, size_t ws_bytes, void* stream);
 

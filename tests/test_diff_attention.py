@@ -4,11 +4,12 @@ second derivatives, layouts, masks and refusals.
 The bounds are elementwise and follow the roundings, each by at most half a
 step h of the tensors' type (2^-8 for bf16; for fp32 tensors nothing is held
 in fewer bits).  Probabilities, W = P1 - lam P2 and dS are operands of bf16
-products, O and O2 are stored and read back for D, results round once:
+products, O2 is stored and read back for D (O with what its rounding left
+off, in two bf16 numbers: h^2), results round once:
   |dO_err|  <= h (P1 |V| + lam P2 |V|) + h |O|
   |dV_err|  <= h |W|^T |dO| + h |dV|
   |dS_err|  <= h |dS| + P |D_err|, |D2_err| <= h |dO|.|O2|,
-               |D1_err| <= h |dO|.(|O| + 2 lam |O2|)
+               |D1_err| <= h |dO|.(lam |O2| + h |O|)
   |dQ_err|  <= c |dS_err| |K| + h |dQ|, dK likewise
 plus 32-bit arithmetic: sums of n terms are off by at most n u times the sum of
 their magnitudes (u = 2^-24), scores by (d + 4) u c |q|.|k| and the exponential
@@ -76,7 +77,7 @@ def oracle(q, k, v, lam, do, causal, scale):
     eO = eO + step * (O.abs() + eO)
     eD2 = (ado * (step * O2.abs() + (h + r) * PV[:, :, 1])).sum(-1, keepdim=True) \
         + dv * U * (ado * O2.abs()).sum(-1, keepdim=True)
-    eD1 = (ado * (step * (O.abs() + 2 * aw * O2.abs()) + (h + r) * (mix + aw * PV[:, :, 1]))).sum(
+    eD1 = (ado * (step * (step * O.abs() + aw * O2.abs()) + (h + r) * (mix + aw * PV[:, :, 1]))).sum(
         -1, keepdim=True) + dv * U * (ado * (O.abs() + aw * O2.abs())).sum(-1, keepdim=True)
     adP = ado @ av.transpose(-1, -2)
     eD = torch.stack((eD1, eD2), 2)
@@ -154,9 +155,9 @@ class TestOnGpu:
         q, k, v, w, do = inputs(Bt, H, Hk, N, d, dv, dtype, lam)
         scale = 0.7 / math.sqrt(d)
         vals, errs = oracle(q, k, v, w, do, causal, scale)
-        o, o2, lse = fbob.diff_forward(q, k, v, w, causal, scale)
-        check(dict(o=o, o2=o2, lse=lse), vals, errs, ("o", "o2", "lse"))
-        grads = fbob.diff_backward(q, k, v, w, o, o2, lse, do, causal, scale)
+        o, rest, lse = fbob.diff_forward(q, k, v, w, causal, scale)
+        check(dict(o=o, o2=rest[..., 0, :], lse=lse), vals, errs, ("o", "o2", "lse"))
+        grads = fbob.diff_backward(q, k, v, w, o, rest, lse, do, causal, scale)
         check(dict(zip(("dq", "dk", "dv", "dlam"), grads)), vals, errs, ("dq", "dk", "dv", "dlam"))
         # through autograd, from strided views of the same values
         leaf = [t.clone().requires_grad_() for t in (q, k, v, w)]
@@ -173,11 +174,11 @@ class TestOnGpu:
         vals, errs = oracle(q, k, v, w, do, True, 0.125)
         old = fbob.force_path(fbob.PATH_SIMT)
         try:
-            o, o2, lse = fbob.diff_forward(q, k, v, w, True)
-            grads = fbob.diff_backward(q, k, v, w, o, o2, lse, do, True)
+            o, rest, lse = fbob.diff_forward(q, k, v, w, True)
+            grads = fbob.diff_backward(q, k, v, w, o, rest, lse, do, True)
         finally:
             fbob.force_path(old)
-        check(dict(zip(("o", "o2", "lse", "dq", "dk", "dv", "dlam"), (o, o2, lse, *grads))), vals,
+        check(dict(zip(("o", "o2", "lse", "dq", "dk", "dv", "dlam"), (o, rest[..., 0, :], lse, *grads))), vals,
               errs, ("o", "o2", "lse", "dq", "dk", "dv", "dlam"))
 
     @pytest.mark.parametrize("dtype", [BF, F32])
@@ -186,9 +187,9 @@ class TestOnGpu:
         q, k, v, w, do = inputs(1, 2, 2, 300, 64, 128, dtype, ("head", dtype), seed=4, spread=4.0)
         k = k * torch.linspace(0.1, 1.0, 300, device="cuda").to(dtype)[:, None]
         vals, errs = oracle(q, k, v, w, do, True, 0.125)
-        o, o2, lse = fbob.diff_forward(q, k, v, w, True, 0.125)
-        check(dict(o=o, o2=o2, lse=lse), vals, errs, ("o", "o2", "lse"))
-        grads = fbob.diff_backward(q, k, v, w, o, o2, lse, do, True, 0.125)
+        o, rest, lse = fbob.diff_forward(q, k, v, w, True, 0.125)
+        check(dict(o=o, o2=rest[..., 0, :], lse=lse), vals, errs, ("o", "o2", "lse"))
+        grads = fbob.diff_backward(q, k, v, w, o, rest, lse, do, True, 0.125)
         check(dict(zip(("dq", "dk", "dv", "dlam"), grads)), vals, errs, ("dq", "dk", "dv", "dlam"))
 
     @pytest.mark.parametrize("dtype", [BF, F32])
@@ -198,9 +199,9 @@ class TestOnGpu:
         q[:, 1::2], k[:, 1::2] = q[:, 0::2], k[:, 0::2]
         w.fill_(1.0)
         vals, errs = oracle(q, k, v, w, do, True, 0.125)
-        o, o2, lse = fbob.diff_forward(q, k, v, w, True, 0.125)
+        o, rest, lse = fbob.diff_forward(q, k, v, w, True, 0.125)
         check(dict(o=o), vals, errs, ("o",))
-        grads = fbob.diff_backward(q, k, v, w, o, o2, lse, do, True, 0.125)
+        grads = fbob.diff_backward(q, k, v, w, o, rest, lse, do, True, 0.125)
         check(dict(zip(("dq", "dk", "dv", "dlam"), grads)), vals, errs, ("dq", "dk", "dv", "dlam"))
 
     @pytest.mark.parametrize("dtype,dv", [(BF, 128), (F32, 64)])
@@ -208,8 +209,8 @@ class TestOnGpu:
         q, k, v, w, do = inputs(2, 4, 2, 500, 64, dv, dtype, ("head", dtype), seed=6)
 
         def both():
-            o, o2, lse = fbob.diff_forward(q, k, v, w, True)
-            return (o, o2, lse) + fbob.diff_backward(q, k, v, w, o, o2, lse, do, True)
+            o, rest, lse = fbob.diff_forward(q, k, v, w, True)
+            return (o, rest, lse) + fbob.diff_backward(q, k, v, w, o, rest, lse, do, True)
 
         first = both()
         streams = [torch.cuda.Stream() for _ in range(2)]
@@ -242,19 +243,20 @@ class TestOnGpu:
             buf = torch.full((n + 4096,), 0xFF, dtype=torch.uint8, device="cuda")
             return buf, n
 
-        o, o2 = guarded((1, 2, 200, dv), dtype), guarded((1, 2, 200, dv), dtype)
+        o = guarded((1, 2, 200, dv), dtype)
+        rest = guarded((1, 2, 200, 2 if dtype == BF else 1, dv), dtype)
         lse = guarded((1, 4, 200), F32)
         fws, fn = workspace(0)
         args = [t.data_ptr() for t in (q, k, v, w)]
-        assert lib.fbob_diff_forward(ctypes.byref(shp), *args, o[1].data_ptr(), o2[1].data_ptr(),
+        assert lib.fbob_diff_forward(ctypes.byref(shp), *args, o[1].data_ptr(), rest[1].data_ptr(),
                                      lse[1].data_ptr(), fws.data_ptr(), fn, st) == 0
         grads = [guarded(t.shape, t.dtype) for t in (q, k, v, w)]
         bws, bn = workspace(1)
-        assert lib.fbob_diff_backward(ctypes.byref(shp), *args, o[1].data_ptr(), o2[1].data_ptr(),
+        assert lib.fbob_diff_backward(ctypes.byref(shp), *args, o[1].data_ptr(), rest[1].data_ptr(),
                                       lse[1].data_ptr(), do.data_ptr(),
                                       *(g[1].data_ptr() for g in grads), bws.data_ptr(), bn, st) == 0
         torch.cuda.synchronize()
-        for buf, view in [o, o2, lse] + grads:
+        for buf, view in [o, rest, lse] + grads:
             assert torch.isfinite(view.float()).all()
             assert torch.isnan(buf[view.numel():].float()).all()
         assert (fws[fn:] == 0xFF).all() and (bws[bn:] == 0xFF).all()
@@ -263,7 +265,7 @@ class TestOnGpu:
         check(dict(zip(("dq", "dk", "dv", "dlam"), (g[1] for g in grads))), vals, errs,
               ("dq", "dk", "dv", "dlam"))
         # a workspace one byte short is refused
-        assert lib.fbob_diff_backward(ctypes.byref(shp), *args, o[1].data_ptr(), o2[1].data_ptr(),
+        assert lib.fbob_diff_backward(ctypes.byref(shp), *args, o[1].data_ptr(), rest[1].data_ptr(),
                                       lse[1].data_ptr(), do.data_ptr(),
                                       *(g[1].data_ptr() for g in grads), bws.data_ptr(), bn - 1,
                                       st) == 3
@@ -370,8 +372,8 @@ class TestOnGpu:
         q, k, v, w, do = inputs(1, 2, 2, 200, 64, 128, BF, ("head", BF), seed=11)
 
         def both(q, k, v, w, do):
-            o, o2, lse = fbob.diff_forward(q, k, v, w, True)
-            return (o,) + fbob.diff_backward(q, k, v, w, o, o2, lse, do, True)
+            o, rest, lse = fbob.diff_forward(q, k, v, w, True)
+            return (o,) + fbob.diff_backward(q, k, v, w, o, rest, lse, do, True)
 
         static = [t.clone() for t in (q, k, v, w, do)]
         both(*static)
@@ -395,9 +397,9 @@ class TestOnGpu:
         q, k, v, w, do = inputs(1, 2, 1, 2048, 64, dv, BF, ("head", BF), seed=14)
         shp = _shape(q, k, v, w, True, None)
         fws, bws = (_workspace(op, shp, q.device) for op in (0, 1))
-        o, o2, lse = fbob.diff_forward(q, k, v, w, True, workspace=fws)
+        o, rest, lse = fbob.diff_forward(q, k, v, w, True, workspace=fws)
         calls = ((fws, lambda: fbob.diff_forward(q, k, v, w, True, workspace=fws)),
-                 (bws, lambda: fbob.diff_backward(q, k, v, w, o, o2, lse, do, True, workspace=bws)))
+                 (bws, lambda: fbob.diff_backward(q, k, v, w, o, rest, lse, do, True, workspace=bws)))
         for ws, call in calls:
             want = call()
             assert fbob.status(ws) == 0
@@ -435,11 +437,11 @@ class TestOnGpu:
         with pytest.raises(fbob.FbobError):
             wide = torch.zeros(1, 4, 8, 256, dtype=BF, device="cuda")
             fbob.diff_attention(wide, wide, v, w)
-        o, o2, lse = fbob.diff_forward(q, k, v, w)
+        o, rest, lse = fbob.diff_forward(q, k, v, w)
         with pytest.raises(ValueError):
-            fbob.diff_backward(q, k, v, w, o, o2, lse, do.float())
+            fbob.diff_backward(q, k, v, w, o, rest, lse, do.float())
         with pytest.raises(ValueError):
-            fbob.diff_backward(q, k, v, w, o, o2, lse[:, :2], do)
+            fbob.diff_backward(q, k, v, w, o, rest, lse[:, :2], do)
 
 
 def test_rejects_cpu_tensors():
@@ -476,7 +478,7 @@ def test_c_calls_refuse_bad_pointers_and_workspaces():
     good, off = ctypes.c_void_p(1 << 20), ctypes.c_void_p((1 << 20) + 8)
     odd = ctypes.c_void_p((1 << 20) + 1)
     n = lib.fbob_diff_workspace_size(0, ctypes.byref(s))
-    # q, k, v, lam, o, o2, lse; o2 may be null, lam needs its own alignment only
+    # q, k, v, lam, o, rest, lse; rest may be null, lam needs its own alignment only
     for i in range(7):
         for bad in (None, off, odd):
             args = [good] * 7
