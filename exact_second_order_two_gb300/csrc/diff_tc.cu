@@ -553,10 +553,11 @@ __global__ void __launch_bounds__(kThreads, 1)
   uint64_t* k_empty = full + C::KS;        // [KS]
   uint64_t* v_empty = k_empty + C::KS;     // [VS]
   uint64_t* s_full = v_empty + C::VS;      // [2]: scores of map m in TMEM, for map 0 dP too
-  uint64_t* ds_full = s_full + 2;          // [2]: bf16 dS written over the scores
+  uint64_t* dp_read = s_full + 2;          // every thread holds its dP
+  uint64_t* ds_full = dp_read + 1;         // [2]: bf16 dS written over the scores
   uint64_t* acc_done = ds_full + 2;
   uint64_t* drain = acc_done + 1;
-  static_assert((1 + 2 * C::KS + C::VS + 6) * 8 <= 256, "barriers end below the TMEM slot");
+  static_assert((1 + 2 * C::KS + C::VS + 7) * 8 <= 256, "barriers end below the TMEM slot");
   uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(smem + C::OFF_MISC + 256);
   Abort* ab = reinterpret_cast<Abort*>(smem + C::OFF_MISC + 264);
   float* red = reinterpret_cast<float*>(smem + C::OFF_RED);
@@ -582,6 +583,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       mbar_init(s_full + m, 1);
       mbar_init(ds_full + m, kWarps);
     }
+    mbar_init(dp_read, kWarps);
     mbar_init(acc_done, 1);
     mbar_init(drain, 1);
     ab->flag = 0;
@@ -631,16 +633,13 @@ __global__ void __launch_bounds__(kThreads, 1)
         mma_ss_w(tmem + C::T_S(m), q_lo + kslice_off(C::BM, k), k_lo + kslice_off(C::BN, k), id_s,
                  k > 0 ? 1u : 0u);
     };
-    // S^1 and dP of tile t, one commit
-    auto issue_first = [&](int t) {
-      issue_s(t, 0);
+    auto issue_dp = [&](int t) {
       const uint32_t do_lo = opaque(lo_kmajor(sb + C::OFF_DO));
       const uint32_t v_lo = opaque(lo_kmajor(sb + C::OFF_V + (t % C::VS) * C::VB));
 #pragma unroll
       for (int k = 0; k < DV / 16; ++k)
         mma_ss_w(tmem + C::T_DP, do_lo + kslice_off(C::BM, k), v_lo + kslice_off(C::BN, k), id_s,
                  k > 0 ? 1u : 0u);
-      mma_commit_w(s_full);
       mma_commit_w(v_empty + t % C::VS);
     };
     // dQ^m += dS^m K^m
@@ -655,17 +654,27 @@ __global__ void __launch_bounds__(kThreads, 1)
     await(q_full, 0, ab, prm.status);
     await(full, 0, ab, prm.status);
     tc_fence_after();
-    issue_first(0);
+    issue_dp(0);
+    issue_s(0, 0);
+    mma_commit_w(s_full);  // covers dP, issued before
     for (int t = 0; t < T; ++t) {
       const bool more = t + 1 < T;
-      // scores go over the dS of the tile before, whose dQ product is issued
+      // scores go over the dS of the tile before, whose dQ product is issued;
+      // the next dP over this one, as soon as every thread has read it
       issue_s(t, 1);
       mma_commit_w(s_full + 1);
+      if (more) {
+        await(dp_read, t & 1, ab, prm.status);
+        tc_fence_after();
+        issue_dp(t + 1);
+      }
       await(ds_full, t & 1, ab, prm.status);
       tc_fence_after();
       issue_dq(t, 0);
-      // every thread took dP into registers before it wrote dS^1
-      if (more) issue_first(t + 1);
+      if (more) {
+        issue_s(t + 1, 0);
+        mma_commit_w(s_full);
+      }
       await(ds_full + 1, t & 1, ab, prm.status);
       tc_fence_after();
       issue_dq(t, 1);
@@ -703,8 +712,13 @@ __global__ void __launch_bounds__(kThreads, 1)
         tc_fence_after();
         const uint32_t ts = tmem + lane_off + C::T_S(m) + NC * slice;
         uint32_t sr[NC];
-        if (m == 0) tmem_ld32x2(ts, tmem + lane_off + C::T_DP + NC * slice, sr, dp);
-        else tmem_ld32(ts, sr);
+        if (m == 0) {
+          tmem_ld32x2(ts, tmem + lane_off + C::T_DP + NC * slice, sr, dp);
+          tc_fence_before();
+          warp_arrive(dp_read);
+        } else {
+          tmem_ld32(ts, sr);
+        }
         const f2 nl2 = {nl[m], nl[m]}, mul2_ = {mul[m], mul[m]}, add2_ = {add[m], add[m]};
         uint32_t dsw[NC / 2];
         auto body = [&](auto masked) {
@@ -805,10 +819,11 @@ __global__ void __launch_bounds__(kThreads, 1)
   uint64_t* full = kv_full + 1;            // [ST]: Q^1, Q^2, dO landed, scalars written
   uint64_t* empty = full + C::ST;          // [ST]: the tile's last products done
   uint64_t* s_full = empty + C::ST;        // [2]: S^T of map m in TMEM, for map 1 dP^T too
-  uint64_t* ds_full = s_full + 2;          // [2]: bf16 operands written over the scores
+  uint64_t* dp_read = s_full + 2;          // every thread holds its dP
+  uint64_t* ds_full = dp_read + 1;         // [2]: bf16 operands written over the scores
   uint64_t* acc_done = ds_full + 2;
   uint64_t* drain = acc_done + 1;
-  static_assert((1 + 2 * C::ST + 6) * 8 <= 256, "barriers end below the TMEM slot");
+  static_assert((1 + 2 * C::ST + 7) * 8 <= 256, "barriers end below the TMEM slot");
   uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(smem + C::OFF_MISC + 256);
   Abort* ab = reinterpret_cast<Abort*>(smem + C::OFF_MISC + 264);
   float* scal = reinterpret_cast<float*>(smem + C::OFF_SC);
@@ -833,6 +848,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       mbar_init(s_full + m, 1);
       mbar_init(ds_full + m, kWarps);
     }
+    mbar_init(dp_read, kWarps);
     mbar_init(acc_done, 1);
     mbar_init(drain, 1);
     ab->flag = 0;
@@ -890,15 +906,17 @@ __global__ void __launch_bounds__(kThreads, 1)
         mma_ss_w(s_cols(a, m), k_lo + kslice_off(C::BM, k), q_lo + kslice_off(C::BN, k), id_s,
                  k > 0 ? 1u : 0u);
     };
-    // the three score blocks of tile a
-    auto issue_scores = [&](int a) {
-      issue_s(a, 0);
+    auto issue_dp = [&](int a) {
       const uint32_t v_lo = opaque(lo_kmajor(sb + C::OFF_V));
       const uint32_t do_lo = opaque(lo_kmajor(tile(a) + 2 * C::QB));
 #pragma unroll
       for (int k = 0; k < DV / 16; ++k)
         mma_ss_w(tmem + C::T_DP, v_lo + kslice_off(C::BM, k), do_lo + kslice_off(C::BN, k), id_s,
                  k > 0 ? 1u : 0u);
+    };
+    // S^T of both maps (the first commit covers dP^T, issued before)
+    auto issue_scores = [&](int a) {
+      issue_s(a, 0);
       mma_commit_w(s_full);
       issue_s(a, 1);
       mma_commit_w(s_full + 1);
@@ -915,14 +933,20 @@ __global__ void __launch_bounds__(kThreads, 1)
     await(kv_full, 0, ab, prm.status);
     await(full, 0, ab, prm.status);
     tc_fence_after();
+    issue_dp(0);
     issue_scores(0);
     for (int a = 0; a < T; ++a) {
       const bool more = a + 1 < T;
+      // the next dP^T over this one, as soon as every thread has read it
+      if (more) {
+        await(dp_read, a & 1, ab, prm.status);
+        tc_fence_after();
+        issue_dp(a + 1);
+      }
       await(ds_full, a & 1, ab, prm.status);
       tc_fence_after();
       // dK^1, then the next tile's scores: S^T of map 1 over the dS^T that
-      // product read, dP^T over the one every thread took into registers, S^T
-      // of map 2 over the operands of tile a - 1
+      // product read, that of map 2 over the operands of tile a - 1
       issue_dk(a, 0);
       if (more) issue_scores(a + 1);
       await(ds_full + 1, a & 1, ab, prm.status);
@@ -965,8 +989,13 @@ __global__ void __launch_bounds__(kThreads, 1)
         tc_fence_after();
         const uint32_t ts = tmem + lane_off + (m == 0 ? C::T_S1 : C::T_S2(a & 1)) + NC * slice;
         uint32_t sr[NC];
-        if (m == 0) tmem_ld16x2(ts, tmem + lane_off + C::T_DP + NC * slice, sr, dp);
-        else tmem_ld16(ts, sr);
+        if (m == 0) {
+          tmem_ld16x2(ts, tmem + lane_off + C::T_DP + NC * slice, sr, dp);
+          tc_fence_before();
+          warp_arrive(dp_read);
+        } else {
+          tmem_ld16(ts, sr);
+        }
         uint32_t dsw[NC / 2], ww[NC / 2];
         auto body = [&](auto masked) {
 #pragma unroll
