@@ -131,9 +131,29 @@ __device__ __forceinline__ void bulk_load(void* dst, const void* src, uint32_t b
       : "memory");
 }
 
-// 32 fp32 TMEM columns, scaled, to 32 consecutive bf16 of global memory.
-__device__ __forceinline__ void store32(__nv_bfloat16* dst, const uint32_t (&v)[32], float mul) {
-  uint4* p = reinterpret_cast<uint4*>(dst);
+// Tiled store shared -> global of the box that load_tile loads: [rows][64]
+// blocks with 128-byte swizzle; rows past N are left as they are.  The caller
+// fences its writes (fence_async_smem) and ends with stores_done.
+__device__ __forceinline__ void store_tile(const CUtensorMap* map, const void* src, int row, int bh) {
+  asm volatile(
+      "cp.async.bulk.tensor.4d.global.shared::cta.tile.bulk_group [%0, {%2, %3, %4, %5}], [%1];" ::"l"(
+          reinterpret_cast<uint64_t>(map)),
+      "r"(smem_u32(src)), "r"(0), "r"(row), "r"(0), "r"(bh)
+      : "memory");
+}
+// The stores of this thread have read their shared memory.
+__device__ __forceinline__ void stores_done() {
+  bulk_commit_group();
+  bulk_wait_read_all();
+}
+// 8 packed words (16 features) of a row into the tile, from 16-byte chunk c on.
+__device__ __forceinline__ void put16(uint32_t tile, int row, int c, const uint32_t (&v)[8]) {
+  st_shared_v4(tile + sw128_offset(row, c), v[0], v[1], v[2], v[3]);
+  st_shared_v4(tile + sw128_offset(row, c + 1), v[4], v[5], v[6], v[7]);
+}
+
+// 32 fp32 values, scaled, as 32 bf16 features of a row, from chunk c on.
+__device__ __forceinline__ void put32(uint32_t tile, int row, int c, const uint32_t (&v)[32], float mul) {
 #pragma unroll
   for (int q = 0; q < 4; ++q) {
     uint32_t w[4];
@@ -141,7 +161,7 @@ __device__ __forceinline__ void store32(__nv_bfloat16* dst, const uint32_t (&v)[
     for (int e = 0; e < 4; ++e)
       w[e] = pack_bf16(__uint_as_float(v[8 * q + 2 * e]) * mul,
                        __uint_as_float(v[8 * q + 2 * e + 1]) * mul);
-    p[q] = make_uint4(w[0], w[1], w[2], w[3]);
+    st_shared_v4(tile + sw128_offset(row, c + q), w[0], w[1], w[2], w[3]);
   }
 }
 
@@ -172,14 +192,15 @@ struct Fwd {
 };
 
 struct FwdParams : Common {
-  __nv_bfloat16 *o, *rest;  // rest: O^2, and what o's rounding left off (or null)
+  bool rest;  // whether O^2 and what o's rounding left off are wanted (mR)
   float* lse;
 };
 
 template <int DV>
 __global__ void __launch_bounds__(kFwdThreads, 1)
     diff_fwd_pass(const __grid_constant__ CUtensorMap mQ, const __grid_constant__ CUtensorMap mK,
-                  const __grid_constant__ CUtensorMap mV, FwdParams prm) {
+                  const __grid_constant__ CUtensorMap mV, const __grid_constant__ CUtensorMap mO,
+                  const __grid_constant__ CUtensorMap mR, FwdParams prm) {
   using C = Fwd<DV>;
   extern __shared__ __align__(1024) uint8_t smem[];
   const uint32_t sb = smem_u32(smem);
@@ -396,11 +417,13 @@ __global__ void __launch_bounds__(kFwdThreads, 1)
     const bool in = i < N;
     const float inv1 = 1.f / L[0], inv2 = 1.f / L[1];
     const float w = in ? lam_row(prm.lam, bh, prm.H, N, i) : 0.f;
-    const size_t r = (size_t)bh * N + (in ? i : 0);
+    // through shared memory (the tiles' stages are free) into whole lines: from
+    // the threads, each in a row of its own, the stores took 9000 cycles
+    const uint32_t so = sb + C::OFF_T, sr = so + C::BM * DV * 2;  // o; O^2 and the rest of o
 #pragma unroll
-    for (int c = f0; c < f0 + PART; c += 16) {
+    for (int c = 0; c < PART; c += 16) {
       uint32_t a[16], b[16];
-      tmem_ld16x2(tmem + lane_off + C::T_O(0) + c, tmem + lane_off + C::T_O(1) + c, a, b);
+      tmem_ld16x2(tmem + lane_off + C::T_O(0) + f0 + c, tmem + lane_off + C::T_O(1) + f0 + c, a, b);
       uint32_t wo[8], w2[8], wl[8];
 #pragma unroll
       for (int e = 0; e < 8; ++e) {
@@ -412,17 +435,20 @@ __global__ void __launch_bounds__(kFwdThreads, 1)
         const float2 back = __bfloat1622float2(*reinterpret_cast<const __nv_bfloat162*>(&wo[e]));
         wl[e] = pack_bf16(x - back.x, y - back.y);
       }
-      auto put = [&](__nv_bfloat16* dst, const uint32_t (&v)[8]) {
-        reinterpret_cast<uint4*>(dst)[0] = make_uint4(v[0], v[1], v[2], v[3]);
-        reinterpret_cast<uint4*>(dst)[1] = make_uint4(v[4], v[5], v[6], v[7]);
-      };
-      if (in) {
-        put(prm.o + r * DV + c, wo);
-        if (prm.rest) {
-          put(prm.rest + 2 * r * DV + c, w2);
-          put(prm.rest + (2 * r + 1) * DV + c, wl);
-        }
+      const uint32_t blk = (uint32_t)((f0 + c) / 64) * C::BM * 128;  // 64-feature block
+      const int chunk = (f0 + c) % 64 / 8;
+      put16(so + blk, row, chunk, wo);
+      if (prm.rest) {
+        put16(sr + blk, row, chunk, w2);
+        put16(sr + C::BM * DV * 2 + blk, row, chunk, wl);
       }
+    }
+    fence_async_smem();
+    named_sync<kSoftmax>(1);
+    if (threadIdx.x == 0) {
+      store_tile(&mO, smem + C::OFF_T, i0, bh);
+      if (prm.rest) store_tile(&mR, smem + C::OFF_T + C::BM * DV * 2, i0, bh);
+      stores_done();
     }
     if (in)
       prm.lse[((size_t)bh * 2 + m) * N + i] = (mx + log2f(m == 0 ? L[0] : L[1])) * kLn2;
@@ -531,7 +557,6 @@ struct Row {
 };
 
 struct RowParams : Common {
-  __nv_bfloat16* dq;
   const float* scal;  // row scalars (diff_tc_scalars)
   float* d2;          // [B, H, N]: sum_j P^2_ij dP_ij
 };
@@ -540,7 +565,7 @@ template <int DV>
 __global__ void __launch_bounds__(kThreads, 1)
     diff_row_pass(const __grid_constant__ CUtensorMap mQ, const __grid_constant__ CUtensorMap mK,
                   const __grid_constant__ CUtensorMap mV, const __grid_constant__ CUtensorMap mDO,
-                  RowParams prm) {
+                  const __grid_constant__ CUtensorMap mDQ, RowParams prm) {
   using C = Row<DV>;
   extern __shared__ __align__(1024) uint8_t smem[];
   const uint32_t sb = smem_u32(smem);
@@ -746,20 +771,24 @@ __global__ void __launch_bounds__(kThreads, 1)
     }
     // ---- epilogue: dQ (scaled): 32 features of one map per thread ----
     red[slice * 128 + row] = d2.x + d2.y;
-    named_sync<kConsumers>(1);
     await(acc_done, 0, ab, prm.status);
     tc_fence_after();
     const int m = slice >> 1, f = 32 * (slice & 1);
     uint32_t v[32];
-    tmem_ld32(tmem + lane_off + C::T_DQ(0) + kD * m + f, v);
-    if (in) {
-      store32(prm.dq + (((size_t)bh * 2 + m) * N + i) * kD + f, v, prm.scale);
-      if (slice == 0) {
-        float s = 0.f;
+    tmem_ld32(tmem + lane_off + C::T_DQ(m) + f, v);
+    put32(sb + C::OFF_K + m * C::QB, row, f / 8, v, prm.scale);
+    fence_async_smem();
+    named_sync<kConsumers>(1);
+    if (threadIdx.x == 0) {
+      store_tile(&mDQ, smem + C::OFF_K, i0, 2 * bh);
+      store_tile(&mDQ, smem + C::OFF_K + C::QB, i0, 2 * bh + 1);
+      stores_done();
+    }
+    if (slice == 0 && in) {
+      float s = 0.f;
 #pragma unroll
-        for (int u = 0; u < kRowSlices; ++u) s += red[u * 128 + row];
-        prm.d2[(size_t)bh * N + i] = s;
-      }
+      for (int u = 0; u < kRowSlices; ++u) s += red[u * 128 + row];
+      prm.d2[(size_t)bh * N + i] = s;
     }
   }
   tc_fence_before();
@@ -799,7 +828,6 @@ struct Col {
 };
 
 struct ColParams : Common {
-  __nv_bfloat16 *dk, *dv;
   const float* scal;  // row scalars (diff_tc_scalars)
 };
 
@@ -807,6 +835,7 @@ template <int DV>
 __global__ void __launch_bounds__(kThreads, 1)
     diff_col_pass(const __grid_constant__ CUtensorMap mK, const __grid_constant__ CUtensorMap mV,
                   const __grid_constant__ CUtensorMap mQ, const __grid_constant__ CUtensorMap mDO,
+                  const __grid_constant__ CUtensorMap mDK, const __grid_constant__ CUtensorMap mDV,
                   ColParams prm) {
   using C = Col<DV>;
   extern __shared__ __align__(1024) uint8_t smem[];
@@ -1043,11 +1072,19 @@ __global__ void __launch_bounds__(kThreads, 1)
     tc_fence_after();
     const int m = slice >> 1, f = 32 * (slice & 1);
     uint32_t v[32];
-    tmem_ld32(tmem + lane_off + C::T_DK(0) + kD * m + f, v);
-    if (j < N) store32(prm.dk + (((size_t)kvh * 2 + m) * N + j) * kD + f, v, prm.scale);
+    tmem_ld32(tmem + lane_off + C::T_DK(m) + f, v);
+    put32(sb + C::OFF_T + m * C::KB, row, f / 8, v, prm.scale);
     if (DV == 128 || slice < 2) {
       tmem_ld32(tmem + lane_off + C::T_DV + 32 * slice, v);
-      if (j < N) store32(prm.dv + ((size_t)kvh * N + j) * DV + 32 * slice, v, 1.f);
+      put32(sb + C::OFF_T + 2 * C::KB + m * C::KB, row, f / 8, v, 1.f);
+    }
+    fence_async_smem();
+    named_sync<kConsumers>(1);
+    if (threadIdx.x == 0) {
+      store_tile(&mDK, smem + C::OFF_T, j0, 2 * kvh);
+      store_tile(&mDK, smem + C::OFF_T + C::KB, j0, 2 * kvh + 1);
+      store_tile(&mDV, smem + C::OFF_T + 2 * C::KB, j0, kvh);
+      stores_done();
     }
   }
   tc_fence_before();
@@ -1100,25 +1137,27 @@ cudaError_t run(K kernel, int units, int N, int threads, uint32_t smem, LaunchLo
 template <int DV>
 cudaError_t forward_dv(const DiffProblem& p, const DiffTensors& t, const DiffWorkspace& ws,
                        LaunchLog& log) {
-  CUtensorMap mQ, mK, mV;
+  CUtensorMap mQ, mK, mV, mO, mR;  // without rest mR is a placeholder
   if (!tiles(&mQ, t.q, p, 2 * p.H, kD, 128) || !tiles(&mK, t.k, p, 2 * p.Hk, kD, 128) ||
-      !tiles(&mV, t.v, p, p.Hk, DV, 128))
+      !tiles(&mV, t.v, p, p.Hk, DV, 128) || !tiles(&mO, t.o, p, p.H, DV, 128) ||
+      !tiles(&mR, t.rest ? t.rest : t.o, p, p.H, t.rest ? 2 * DV : DV, 128))
     return cudaErrorInvalidValue;
   FwdParams f;
   static_cast<Common&>(f) = common(p, t, ws, p.B * p.H);
-  f.o = static_cast<__nv_bfloat16*>(t.o);
-  f.rest = static_cast<__nv_bfloat16*>(t.rest);
+  f.rest = t.rest != nullptr;
   f.lse = t.lse;
-  return run(diff_fwd_pass<DV>, f.units, p.N, kFwdThreads, Fwd<DV>::SMEM, log, f, mQ, mK, mV);
+  return run(diff_fwd_pass<DV>, f.units, p.N, kFwdThreads, Fwd<DV>::SMEM, log, f, mQ, mK, mV, mO, mR);
 }
 
 template <int DV>
 cudaError_t backward_dv(const DiffProblem& p, const DiffTensors& t, const DiffWorkspace& ws,
                         LaunchLog& log) {
-  CUtensorMap mQ, mK, mV, mDO, sQ, sDO;  // 128-row tiles; sQ, sDO: the column pass's 64
+  CUtensorMap mQ, mK, mV, mDO, sQ, sDO, mDQ, mDK, mDV;  // 128-row tiles; sQ, sDO: of 64
   if (!tiles(&mQ, t.q, p, 2 * p.H, kD, 128) || !tiles(&mK, t.k, p, 2 * p.Hk, kD, 128) ||
       !tiles(&mV, t.v, p, p.Hk, DV, 128) || !tiles(&mDO, t.dO, p, p.H, DV, 128) ||
-      !tiles(&sQ, t.q, p, 2 * p.H, kD, 64) || !tiles(&sDO, t.dO, p, p.H, DV, 64))
+      !tiles(&sQ, t.q, p, 2 * p.H, kD, 64) || !tiles(&sDO, t.dO, p, p.H, DV, 64) ||
+      !tiles(&mDQ, t.dq, p, 2 * p.H, kD, 128) || !tiles(&mDK, t.dk, p, 2 * p.Hk, kD, 128) ||
+      !tiles(&mDV, t.dv, p, p.Hk, DV, 128))
     return cudaErrorInvalidValue;
   const int blocks = (p.N + 63) / 64 * p.B * p.H;
   diff_tc_scalars<DV><<<blocks, 256, 0, log.stream>>>(
@@ -1129,17 +1168,14 @@ cudaError_t backward_dv(const DiffProblem& p, const DiffTensors& t, const DiffWo
   if (e != cudaSuccess) return e;
   RowParams r;
   static_cast<Common&>(r) = common(p, t, ws, p.B * p.H);
-  r.dq = static_cast<__nv_bfloat16*>(t.dq);
   r.scal = ws.scal;
   r.d2 = ws.d2;
-  e = run(diff_row_pass<DV>, r.units, p.N, kThreads, Row<DV>::SMEM, log, r, mQ, mK, mV, mDO);
+  e = run(diff_row_pass<DV>, r.units, p.N, kThreads, Row<DV>::SMEM, log, r, mQ, mK, mV, mDO, mDQ);
   if (e != cudaSuccess) return e;
   ColParams c;
   static_cast<Common&>(c) = common(p, t, ws, p.B * p.Hk);
-  c.dk = static_cast<__nv_bfloat16*>(t.dk);
-  c.dv = static_cast<__nv_bfloat16*>(t.dv);
   c.scal = ws.scal;
-  return run(diff_col_pass<DV>, c.units, p.N, kThreads, Col<DV>::SMEM, log, c, mK, mV, sQ, sDO);
+  return run(diff_col_pass<DV>, c.units, p.N, kThreads, Col<DV>::SMEM, log, c, mK, mV, sQ, sDO, mDK, mDV);
 }
 
 }  // namespace
