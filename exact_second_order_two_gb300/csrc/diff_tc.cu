@@ -1,20 +1,20 @@
 // Differential attention on the tensor cores (tcgen05 / TMEM / TMA), bf16,
-// d = 64, dv = 64 or 128.  Per head, with m = 1, 2 (code: 0, 1) and c the scale,
+// d and dv = 64 or 128.  Per head, with m = 1, 2 (code: 0, 1) and c the scale,
 //   S^m = c Q^m K^mT, P^m = softmax(S^m), O = P^1 V - lam P^2 V;
 //   dP = dO V^T, D^m = dO . O^m, dS^1 = P^1*(dP - D^1),
 //   dS^2 = -lam P^2*(dP - D^2), dQ^m = c dS^m K^m, dK^m = c dS^mT Q^m,
 //   dV = (P^1 - lam P^2)^T dO, dlam_i = -sum_j P^2_ij dP_ij.
 //
-// The two maps are two score streams over one stream of values: the kernels
-// walk "subtiles" u = 2 t + m (tile t of the streamed side, map m), whose
-// scores alternate between two TMEM buffers, so the tensor pipe works on one
-// map while the elementwise warps work on the other.
+// The two maps are two score streams over one stream of values: scores of map m
+// have a TMEM buffer of their own, so the tensor pipe works on one map while the
+// elementwise warps work on the other.
 //
 // forward (128 query rows per CTA, 128-key tiles): online softmax of both
 //   maps, O^1 and O^2 in TMEM, the difference taken once in the epilogue in
 //   fp32.  V is loaded once for both products.
-// row pass (128 query rows, 128-key tiles): dQ of both maps.  dP is computed
-//   once per tile and stays in registers for the second map.
+// row pass (128 query rows, key tiles of 128 at d = 64 and 64 at d = 128): dQ of
+//   both maps.  dP is computed once per tile and stays in registers for the
+//   second map.
 // column pass (128 key rows, 64-query tiles): dK of both maps and dV, whose
 //   two products are one: W = P^1 - lam P^2 is formed in fp32 and multiplied
 //   with dO once.  A CTA loops over the query heads that share its key head.
@@ -25,10 +25,23 @@
 // products, the precision of the tensors they are multiplied with; scores,
 // softmax statistics, row scalars and every accumulator are fp32.
 //
-// Warp roles as in the other tensor-core kernels: 16 elementwise warps (warp w:
-// TMEM lane quadrant w % 4, column slice w / 4), one TMA producer, one MMA
-// issuer.  Every wait is bounded, and every warp-collective operation sits in
-// warp-uniform control flow.
+// Warp roles: elementwise warps (warp w: TMEM lane quadrant w % 4; 16 of them in
+// the backward passes, each thread a quarter of a row; 8 in the forward, each
+// thread a row of one map), one TMA producer, one MMA issuer.  Every wait is
+// bounded, and every warp-collective operation sits in warp-uniform control
+// flow.
+//
+// What bounds the passes (B = 1, H = 8, N = 16384, causal, dv = 128; time, and
+// the share of the measured 1917 TFLOP/s that the products it runs come to):
+//            forward        row pass        column pass
+//   d = 64   573 us, 75%    574 us, 62%     948 us, 59%
+//   d = 128  654 us, 88%    947 us, 61%     1358 us, 63%
+// All three are bound by the chain scores -> exponentials -> product within a
+// tile: the tensor pipe has to wait for the elementwise warps wherever only one
+// buffer per map fits into TMEM, and a wait of the MMA warp costs 100 to 250
+// cycles.  At d = 64 a tile of the forward takes 2335 cycles against 1536 of
+// products, one of the row pass 2360 against 1738, and two 64-query tiles of the
+// column pass 4400 against 2760.
 #include <cuda.h>
 #include <cuda_bf16.h>
 #include <cuda_runtime.h>
@@ -56,12 +69,14 @@ constexpr int kMmaWarp = kWarps + 1;
 constexpr int kThreads = (kWarps + 2) * 32;
 constexpr int kRowSlices = kWarps / 4;     // column slices per row
 // Forward: 4 softmax warps per map, one thread per row of 128 scores (no
-// exchange between threads), a producer and an MMA warp; 200 registers each.
+// exchange between threads), a producer and an MMA warp, so that a thread has
+// 168 registers.  16 warps of 96 registers, which exchanged each row's maximum,
+// took 733 us at N = 16384 where this then took 605.
 constexpr int kSoftmax = 8 * 32;
 constexpr int kFwdProducer = 8, kFwdMma = 9, kFwdThreads = 10 * 32;
 constexpr float kLn2 = 0.6931471805599453f;
 constexpr uint64_t kDrainNs = 100000000ull;  // limit of the waits after an abort
-constexpr int kD = 64;                     // features of a query or key
+constexpr uint32_t kMinusInf = 0xff800000u;
 
 struct Common {
   int* status;
@@ -168,15 +183,17 @@ __device__ __forceinline__ void put32(uint32_t tile, int row, int c, const uint3
 // ===========================================================================
 // Forward
 // ===========================================================================
-template <int DV>
+template <int D, int DV>
 struct Fwd {
   static constexpr int BM = 128, BN = 128;
-  static constexpr int ST = 3;                     // key tile stages: K^1, K^2, V
-  static constexpr uint32_t QB = BM * kD * 2;      // Q or K of one map
+  static constexpr uint32_t QB = BM * D * 2;       // Q or K of one map
   static constexpr uint32_t VB = BN * DV * 2;
-  static constexpr uint32_t STB = 2 * QB + VB;
-  static constexpr uint32_t OFF_Q = 0, OFF_T = 2 * QB;
-  static constexpr uint32_t OFF_RED = OFF_T + ST * STB;  // [2][128] row sums
+  // d = 64: stages of a whole key tile (K^1, K^2, V) on one barrier.  d = 128:
+  // K and V do not fit three times; a ring of three K^m and one of two V
+  static constexpr bool ONE = D == 64;
+  static constexpr int KS = ONE ? 6 : 3, VS = ONE ? 3 : 2;
+  static constexpr uint32_t OFF_Q = 0, OFF_K = 2 * QB, OFF_V = OFF_K + KS * QB;
+  static constexpr uint32_t OFF_RED = OFF_V + VS * VB;  // [2][128] row sums
   static constexpr uint32_t OFF_MISC = OFF_RED + 2 * 128 * 4;
   static constexpr uint32_t SMEM = OFF_MISC + 512;
   static_assert(SMEM <= 232448, "forward shared memory budget");
@@ -186,7 +203,7 @@ struct Fwd {
   __host__ __device__ static constexpr uint32_t T_S(int m) { return 128u * m; }
   __host__ __device__ static constexpr uint32_t T_O(int m) { return 256u + (uint32_t)DV * m; }
   __host__ __device__ static constexpr uint32_t p_col(int k) { return 32u * (k >> 1) + 8u * (k & 1); }
-  // The reference maximum (log2 domain) moves only when a subtile's maximum
+  // The reference maximum (log2 domain) moves only when a tile's maximum
   // exceeds it by more than this, so O is rescaled in TMEM rarely
   static constexpr float kRescale = 8.f;
 };
@@ -196,12 +213,12 @@ struct FwdParams : Common {
   float* lse;
 };
 
-template <int DV>
+template <int D, int DV>
 __global__ void __launch_bounds__(kFwdThreads, 1)
     diff_fwd_pass(const __grid_constant__ CUtensorMap mQ, const __grid_constant__ CUtensorMap mK,
                   const __grid_constant__ CUtensorMap mV, const __grid_constant__ CUtensorMap mO,
                   const __grid_constant__ CUtensorMap mR, FwdParams prm) {
-  using C = Fwd<DV>;
+  using C = Fwd<D, DV>;
   extern __shared__ __align__(1024) uint8_t smem[];
   const uint32_t sb = smem_u32(smem);
   if (sb & 1023u) {  // 128-byte swizzled tiles need a 1024-byte aligned base
@@ -209,13 +226,16 @@ __global__ void __launch_bounds__(kFwdThreads, 1)
     return;
   }
   uint64_t* q_full = reinterpret_cast<uint64_t*>(smem + C::OFF_MISC);
-  uint64_t* full = q_full + 1;               // [ST]: K^1, K^2 and V of a tile landed
-  uint64_t* empty = full + C::ST;            // [ST]: its last products done
-  uint64_t* s_full = empty + C::ST;          // [2]: scores of map m in TMEM
+  // one barrier per tile stage (v_full, v_empty), or per K^m and per V stage
+  uint64_t* v_full = q_full + 1;             // [VS]
+  uint64_t* v_empty = v_full + C::VS;        // [VS]: a tile's last products done
+  uint64_t* k_full = v_empty + C::VS;        // [KS] (d = 128)
+  uint64_t* k_empty = k_full + C::KS;        // [KS] (d = 128)
+  uint64_t* s_full = k_empty + C::KS;        // [2]: scores of map m in TMEM
   uint64_t* p_full = s_full + 2;             // [2][2]: half a tile's bf16 P written, O^m rescaled
   uint64_t* o_done = p_full + 4;
   uint64_t* drain = o_done + 1;
-  static_assert((1 + 2 * C::ST + 8) * 8 <= 256, "barriers end below the TMEM slot");
+  static_assert((1 + 2 * C::VS + 2 * C::KS + 8) * 8 <= 256, "barriers end below the TMEM slot");
   uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(smem + C::OFF_MISC + 256);
   Abort* ab = reinterpret_cast<Abort*>(smem + C::OFF_MISC + 264);
   float* red = reinterpret_cast<float*>(smem + C::OFF_RED);
@@ -232,9 +252,13 @@ __global__ void __launch_bounds__(kFwdThreads, 1)
 
   if (threadIdx.x == 0) {
     mbar_init(q_full, 1);
-    for (int s = 0; s < C::ST; ++s) {
-      mbar_init(full + s, 1);
-      mbar_init(empty + s, 1);
+    for (int s = 0; s < C::VS; ++s) {
+      mbar_init(v_full + s, 1);
+      mbar_init(v_empty + s, 1);
+    }
+    for (int s = 0; s < C::KS; ++s) {
+      mbar_init(k_full + s, 1);
+      mbar_init(k_empty + s, 1);
     }
     for (int m = 0; m < 2; ++m) {
       mbar_init(s_full + m, 1);
@@ -255,28 +279,43 @@ __global__ void __launch_bounds__(kFwdThreads, 1)
   __syncthreads();
   tc_fence_after();
   const uint32_t tmem = *tmem_slot;
+  // K^m of tile t is subtile u = 2 t + m of its ring
+  auto k_at = [&](int u) { return C::OFF_K + (uint32_t)(u % C::KS) * C::QB; };
+  auto v_at = [&](int t) { return C::OFF_V + (uint32_t)(t % C::VS) * C::VB; };
 
   if (warp == kFwdProducer) {
     if (lane == 0) {
       mbar_arrive_expect_tx(q_full, 2 * C::QB);
       load_tile(smem + C::OFF_Q, &mQ, q_full, i0, 2 * bh);
       load_tile(smem + C::OFF_Q + C::QB, &mQ, q_full, i0, 2 * bh + 1);
-      int issued = 0;
+      int k_issued = 0, v_issued = 0;
       for (int t = 0; t < T; ++t) {
-        const int st = t % C::ST;
-        if (t >= C::ST && !wait_bar(empty + st, ((t / C::ST) - 1) & 1, ab, prm.status)) break;
-        uint8_t* dst = smem + C::OFF_T + st * C::STB;
-        mbar_arrive_expect_tx(full + st, C::STB);
-        load_tile(dst, &mK, full + st, t * C::BN, 2 * kvh);
-        load_tile(dst + C::QB, &mK, full + st, t * C::BN, 2 * kvh + 1);
-        load_tile(dst + 2 * C::QB, &mV, full + st, t * C::BN, kvh);
-        ++issued;
+        if (!C::ONE) {
+          for (; k_issued < 2 * t + 2; ++k_issued) {
+            const int u = k_issued, ks = u % C::KS;
+            if (u >= C::KS && !wait_bar(k_empty + ks, ((u / C::KS) - 1) & 1, ab, prm.status)) break;
+            mbar_arrive_expect_tx(k_full + ks, C::QB);
+            load_tile(smem + k_at(u), &mK, k_full + ks, t * C::BN, 2 * kvh + (u & 1));
+          }
+          if (k_issued < 2 * t + 2) break;
+        }
+        const int vs = t % C::VS;
+        if (t >= C::VS && !wait_bar(v_empty + vs, ((t / C::VS) - 1) & 1, ab, prm.status)) break;
+        mbar_arrive_expect_tx(v_full + vs, C::VB + (C::ONE ? 2 * C::QB : 0));
+        if (C::ONE) {
+          load_tile(smem + k_at(2 * t), &mK, v_full + vs, t * C::BN, 2 * kvh);
+          load_tile(smem + k_at(2 * t + 1), &mK, v_full + vs, t * C::BN, 2 * kvh + 1);
+        }
+        load_tile(smem + v_at(t), &mV, v_full + vs, t * C::BN, kvh);
+        ++v_issued;
       }
       // every load this thread issued has landed before the CTA exits (after an
       // abort some were never awaited); on the normal path these return at once
       mbar_wait_bounded(q_full, 0, prm.status, kDrainNs);
-      for (int t = max(0, issued - C::ST); t < issued; ++t)
-        mbar_wait_bounded(full + (t % C::ST), (t / C::ST) & 1, prm.status, kDrainNs);
+      for (int u = max(0, k_issued - C::KS); u < k_issued; ++u)
+        mbar_wait_bounded(k_full + (u % C::KS), (u / C::KS) & 1, prm.status, kDrainNs);
+      for (int t = max(0, v_issued - C::VS); t < v_issued; ++t)
+        mbar_wait_bounded(v_full + (t % C::VS), (t / C::VS) & 1, prm.status, kDrainNs);
     }
   } else if (warp == kFwdMma) {
     constexpr uint32_t id_s = idesc_bf16(128, C::BN, false, false);  // S = Q K^T
@@ -285,24 +324,30 @@ __global__ void __launch_bounds__(kFwdThreads, 1)
     // some tens.  So only what someone waits for is committed, and the loads of
     // a tile are awaited by a softmax warp, before its arrival for the tile
     // before (only the first tile's here).
-    auto tile = [&](int t) { return sb + C::OFF_T + (uint32_t)(t % C::ST) * C::STB; };
     auto issue_s = [&](int t, int m) {
+      const int u = 2 * t + m;
       const uint32_t q_lo = opaque(lo_kmajor(sb + C::OFF_Q + m * C::QB));
-      const uint32_t k_lo = opaque(lo_kmajor(tile(t) + m * C::QB));
+      const uint32_t k_lo = opaque(lo_kmajor(sb + k_at(u)));
 #pragma unroll
-      for (int k = 0; k < kD / 16; ++k)
+      for (int k = 0; k < D / 16; ++k)
         mma_ss_w(tmem + C::T_S(m), q_lo + kslice_off(C::BM, k), k_lo + kslice_off(C::BN, k), id_s,
                  k > 0 ? 1u : 0u);
       mma_commit_w(s_full + m);
+      if (!C::ONE) mma_commit_w(k_empty + u % C::KS);
     };
     await(q_full, 0, ab, prm.status);
-    await(full, 0, ab, prm.status);
+    if (C::ONE) {
+      await(v_full, 0, ab, prm.status);
+    } else {
+      await(k_full, 0, ab, prm.status);
+      await(k_full + 1, 0, ab, prm.status);
+    }
     tc_fence_after();
     issue_s(0, 0);
     issue_s(0, 1);
     for (int t = 0; t < T; ++t) {
       const bool more = t + 1 < T;
-      const uint32_t v_mn = opaque(lo_mnmajor(tile(t) + 2 * C::QB, C::BN * 128));
+      const uint32_t v_mn = opaque(lo_mnmajor(sb + v_at(t), C::BN * 128));
 #pragma unroll
       for (int m = 0; m < 2; ++m) {
         // O^m += P^m V, A = bf16 P from TMEM, in two halves of 64 keys; then
@@ -316,9 +361,8 @@ __global__ void __launch_bounds__(kFwdThreads, 1)
           for (int k = 4 * h; k < 4 * h + 4; ++k)
             mma_ts_w(tmem + C::T_O(m), tmem + C::T_S(m) + C::p_col(k), v_mn + kstep_off(k), id_o,
                      (t > 0 || k > 0) ? 1u : 0u);
-          // (waited for with products in the pipe, which cover it)
         }
-        if (m == 1) mma_commit_w(empty + t % C::ST);
+        if (m == 1) mma_commit_w(v_empty + t % C::VS);
         if (more) issue_s(t + 1, m);
       }
     }
@@ -339,8 +383,15 @@ __global__ void __launch_bounds__(kFwdThreads, 1)
     float mx = -INFINITY, l = 0.f;
     for (int t = 0; t < T; ++t) {
       const int j0 = t * C::BN;
-      // for the MMA warp: the next tile has landed
-      if (warp == 0 && t + 1 < T) await(full + (t + 1) % C::ST, ((t + 1) / C::ST) & 1, ab, prm.status);
+      // for the MMA warp: what it reads after this warp's arrivals has landed
+      if (C::ONE) {
+        if (warp == 0 && t + 1 < T)
+          await(v_full + (t + 1) % C::VS, ((t + 1) / C::VS) & 1, ab, prm.status);
+      } else if (quad == 0) {
+        const int u = 2 * (t + 1) + m;
+        if (m == 0) await(v_full + t % C::VS, (t / C::VS) & 1, ab, prm.status);
+        if (t + 1 < T) await(k_full + u % C::KS, (u / C::KS) & 1, ab, prm.status);
+      }
       await(s_full + m, t & 1, ab, prm.status);
       tc_fence_after();
       uint32_t s[4][32];
@@ -352,7 +403,7 @@ __global__ void __launch_bounds__(kFwdThreads, 1)
         for (int c = 0; c < 4; ++c)
 #pragma unroll
           for (int e = 0; e < 32; ++e)
-            if (j0 + 32 * c + e >= end) s[c][e] = 0xff800000u;
+            if (j0 + 32 * c + e >= end) s[c][e] = kMinusInf;
       }
       // the row's maximum over the tile (c log2 e > 0 keeps the order)
       float top[4];
@@ -419,7 +470,7 @@ __global__ void __launch_bounds__(kFwdThreads, 1)
     const float w = in ? lam_row(prm.lam, bh, prm.H, N, i) : 0.f;
     // through shared memory (the tiles' stages are free) into whole lines: from
     // the threads, each in a row of its own, the stores took 9000 cycles
-    const uint32_t so = sb + C::OFF_T, sr = so + C::BM * DV * 2;  // o; O^2 and the rest of o
+    const uint32_t so = sb + C::OFF_K, sr = so + C::BM * DV * 2;  // o; O^2 and the rest of o
 #pragma unroll
     for (int c = 0; c < PART; c += 16) {
       uint32_t a[16], b[16];
@@ -446,8 +497,8 @@ __global__ void __launch_bounds__(kFwdThreads, 1)
     fence_async_smem();
     named_sync<kSoftmax>(1);
     if (threadIdx.x == 0) {
-      store_tile(&mO, smem + C::OFF_T, i0, bh);
-      if (prm.rest) store_tile(&mR, smem + C::OFF_T + C::BM * DV * 2, i0, bh);
+      store_tile(&mO, smem + C::OFF_K, i0, bh);
+      if (prm.rest) store_tile(&mR, smem + C::OFF_K + C::BM * DV * 2, i0, bh);
       stores_done();
     }
     if (in)
@@ -536,24 +587,30 @@ __global__ void __launch_bounds__(256, 4)
 // ===========================================================================
 // Row pass: dQ of both maps, and each row's sum_j P^2 dP
 // ===========================================================================
-template <int DV>
+template <int D, int DV>
 struct Row {
-  static constexpr int BM = 128, BN = 128;
+  // d = 128: dQ^1 and dQ^2 take half of TMEM, so the key tiles are halved
+  static constexpr int BM = 128, BN = D == 64 ? 128 : 64;
+  static constexpr int NC = BN / kRowSlices;   // key columns per thread
   static constexpr int KS = 3, VS = 2;         // stages of K^1 and K^2, and of V
-  static constexpr uint32_t QB = BM * kD * 2;
-  static constexpr uint32_t VB = BN * DV * 2;  // dO or V tile
-  static constexpr uint32_t OFF_Q = 0, OFF_DO = 2 * QB, OFF_K = OFF_DO + VB;
-  static constexpr uint32_t OFF_V = OFF_K + KS * 2 * QB;
+  static constexpr uint32_t QB = BM * D * 2, OB = BM * DV * 2;  // Q of one map, dO
+  static constexpr uint32_t KB = BN * D * 2, VB = BN * DV * 2;  // K of one map, V
+  static constexpr uint32_t OFF_Q = 0, OFF_DO = 2 * QB, OFF_K = OFF_DO + OB;
+  static constexpr uint32_t OFF_V = OFF_K + KS * 2 * KB;
   static constexpr uint32_t OFF_RED = OFF_V + VS * VB;  // [slices][128]
   static constexpr uint32_t OFF_MISC = OFF_RED + kRowSlices * 128 * 4;
   static constexpr uint32_t SMEM = OFF_MISC + 512;
   static_assert(SMEM <= 232448, "row pass shared memory budget");
-  // TMEM columns: two score buffers (bf16 dS over the first 16 of each
-  // thread's 32), dP, dQ^1, dQ^2
-  static constexpr uint32_t TMEM_COLS = 512, T_DP = 256;
-  __host__ __device__ static constexpr uint32_t T_S(int m) { return 128u * m; }
-  __host__ __device__ static constexpr uint32_t T_DQ(int m) { return 384u + (uint32_t)kD * m; }
-  __host__ __device__ static constexpr uint32_t a_col(int k) { return 32u * (k >> 1) + 8u * (k & 1); }
+  static_assert(2 * QB <= KS * 2 * KB, "dQ is staged over the K ring");
+  // TMEM columns: two score buffers (bf16 dS over the first half of each
+  // thread's columns), dP, dQ^1, dQ^2
+  static constexpr uint32_t TMEM_COLS = 512, T_DP = 2 * BN;
+  __host__ __device__ static constexpr uint32_t T_S(int m) { return (uint32_t)BN * m; }
+  __host__ __device__ static constexpr uint32_t T_DQ(int m) { return 3u * BN + (uint32_t)D * m; }
+  __host__ __device__ static constexpr uint32_t a_col(int k) {
+    return NC == 32 ? 32u * (k >> 1) + 8u * (k & 1) : 16u * k;
+  }
+  static_assert(3 * BN + 2 * D <= TMEM_COLS, "row pass TMEM budget");
 };
 
 struct RowParams : Common {
@@ -561,12 +618,12 @@ struct RowParams : Common {
   float* d2;          // [B, H, N]: sum_j P^2_ij dP_ij
 };
 
-template <int DV>
+template <int D, int DV>
 __global__ void __launch_bounds__(kThreads, 1)
     diff_row_pass(const __grid_constant__ CUtensorMap mQ, const __grid_constant__ CUtensorMap mK,
                   const __grid_constant__ CUtensorMap mV, const __grid_constant__ CUtensorMap mDO,
                   const __grid_constant__ CUtensorMap mDQ, RowParams prm) {
-  using C = Row<DV>;
+  using C = Row<D, DV>;
   extern __shared__ __align__(1024) uint8_t smem[];
   const uint32_t sb = smem_u32(smem);
   if (sb & 1023u) {
@@ -626,7 +683,7 @@ __global__ void __launch_bounds__(kThreads, 1)
 
   if (warp == kProducerWarp) {
     if (lane == 0) {
-      mbar_arrive_expect_tx(q_full, 2 * C::QB + C::VB);
+      mbar_arrive_expect_tx(q_full, 2 * C::QB + C::OB);
       load_tile(smem + C::OFF_DO, &mDO, q_full, i0, bh);
       load_tile(smem + C::OFF_Q, &mQ, q_full, i0, 2 * bh);
       load_tile(smem + C::OFF_Q + C::QB, &mQ, q_full, i0, 2 * bh + 1);
@@ -635,11 +692,11 @@ __global__ void __launch_bounds__(kThreads, 1)
         const int ks = t % C::KS, vs = t % C::VS;
         if (t >= C::VS && !wait_bar(v_empty + vs, ((t / C::VS) - 1) & 1, ab, prm.status)) break;
         if (t >= C::KS && !wait_bar(k_empty + ks, ((t / C::KS) - 1) & 1, ab, prm.status)) break;
-        uint8_t* dst = smem + C::OFF_K + ks * 2 * C::QB;
-        mbar_arrive_expect_tx(full + ks, 2 * C::QB + C::VB);
+        uint8_t* dst = smem + C::OFF_K + ks * 2 * C::KB;
+        mbar_arrive_expect_tx(full + ks, 2 * C::KB + C::VB);
         load_tile(smem + C::OFF_V + vs * C::VB, &mV, full + ks, t * C::BN, kvh);
         load_tile(dst, &mK, full + ks, t * C::BN, 2 * kvh);
-        load_tile(dst + C::QB, &mK, full + ks, t * C::BN, 2 * kvh + 1);
+        load_tile(dst + C::KB, &mK, full + ks, t * C::BN, 2 * kvh + 1);
         ++issued;
       }
       mbar_wait_bounded(q_full, 0, prm.status, kDrainNs);
@@ -648,13 +705,13 @@ __global__ void __launch_bounds__(kThreads, 1)
     }
   } else if (warp == kMmaWarp) {
     constexpr uint32_t id_s = idesc_bf16(128, C::BN, false, false);  // S and dP
-    constexpr uint32_t id_q = idesc_bf16(128, kD, false, true);      // dQ += dS K: B MN-major
-    auto k_tile = [&](int t, int m) { return sb + C::OFF_K + (uint32_t)(2 * (t % C::KS) + m) * C::QB; };
+    constexpr uint32_t id_q = idesc_bf16(128, D, false, true);       // dQ += dS K: B MN-major
+    auto k_tile = [&](int t, int m) { return sb + C::OFF_K + (uint32_t)(2 * (t % C::KS) + m) * C::KB; };
     auto issue_s = [&](int t, int m) {
       const uint32_t q_lo = opaque(lo_kmajor(sb + C::OFF_Q + m * C::QB));
       const uint32_t k_lo = opaque(lo_kmajor(k_tile(t, m)));
 #pragma unroll
-      for (int k = 0; k < kD / 16; ++k)
+      for (int k = 0; k < D / 16; ++k)
         mma_ss_w(tmem + C::T_S(m), q_lo + kslice_off(C::BM, k), k_lo + kslice_off(C::BN, k), id_s,
                  k > 0 ? 1u : 0u);
     };
@@ -710,7 +767,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     mbar_wait_bounded(drain, 0, prm.status, kDrainNs);
   } else {
     // ---------------- elementwise warps: thread = query row ----------------
-    constexpr int NC = C::BN / kRowSlices;
+    constexpr int NC = C::NC;
     const int quad = warp & 3, slice = warp >> 2;
     const int row = 32 * quad + lane;
     const int i = i0 + row;
@@ -738,11 +795,14 @@ __global__ void __launch_bounds__(kThreads, 1)
         const uint32_t ts = tmem + lane_off + C::T_S(m) + NC * slice;
         uint32_t sr[NC];
         if (m == 0) {
-          tmem_ld32x2(ts, tmem + lane_off + C::T_DP + NC * slice, sr, dp);
+          const uint32_t tp = tmem + lane_off + C::T_DP + NC * slice;
+          if constexpr (NC == 32) tmem_ld32x2(ts, tp, sr, dp);
+          else tmem_ld16x2(ts, tp, sr, dp);
           tc_fence_before();
           warp_arrive(dp_read);
         } else {
-          tmem_ld32(ts, sr);
+          if constexpr (NC == 32) tmem_ld32(ts, sr);
+          else tmem_ld16(ts, sr);
         }
         const f2 nl2 = {nl[m], nl[m]}, mul2_ = {mul[m], mul[m]}, add2_ = {add[m], add[m]};
         uint32_t dsw[NC / 2];
@@ -764,19 +824,24 @@ __global__ void __launch_bounds__(kThreads, 1)
         };
         if (need_mask) body(std::true_type{});
         else body(std::false_type{});
-        tmem_st16(ts, dsw);
+        if constexpr (NC == 32) tmem_st16(ts, dsw);
+        else tmem_st8(ts, dsw);
         tc_fence_before();
         warp_arrive(ds_full + m);
       }
     }
-    // ---- epilogue: dQ (scaled): 32 features of one map per thread ----
+    // ---- epilogue: dQ (scaled): half the features of one map per thread ----
     red[slice * 128 + row] = d2.x + d2.y;
     await(acc_done, 0, ab, prm.status);
     tc_fence_after();
-    const int m = slice >> 1, f = 32 * (slice & 1);
-    uint32_t v[32];
-    tmem_ld32(tmem + lane_off + C::T_DQ(m) + f, v);
-    put32(sb + C::OFF_K + m * C::QB, row, f / 8, v, prm.scale);
+    const int m = slice >> 1;
+#pragma unroll
+    for (int x = 0; x < D / 64; ++x) {
+      const int f = D / 2 * (slice & 1) + 32 * x;
+      uint32_t v[32];
+      tmem_ld32(tmem + lane_off + C::T_DQ(0) + D * m + f, v);
+      put32(sb + C::OFF_K + m * C::QB + f / 64 * C::BM * 128, row, f % 64 / 8, v, prm.scale);
+    }
     fence_async_smem();
     named_sync<kConsumers>(1);
     if (threadIdx.x == 0) {
@@ -802,13 +867,13 @@ __global__ void __launch_bounds__(kThreads, 1)
 // ===========================================================================
 // Column pass: dK of both maps and dV
 // ===========================================================================
-template <int DV>
+template <int D, int DV>
 struct Col {
   static constexpr int BM = 128, BN = 64;
-  static constexpr int ST = 4;                    // query tile stages: Q^1, Q^2, dO
-  static constexpr uint32_t KB = BM * kD * 2;     // stationary K of one map
+  static constexpr int ST = D == 64 ? 4 : 2;      // query tile stages: Q^1, Q^2, dO
+  static constexpr uint32_t KB = BM * D * 2;     // stationary K of one map
   static constexpr uint32_t VB = BM * DV * 2;
-  static constexpr uint32_t QB = BN * kD * 2;     // streamed Q of one map
+  static constexpr uint32_t QB = BN * D * 2;     // streamed Q of one map
   static constexpr uint32_t OB = BN * DV * 2;     // streamed dO
   static constexpr uint32_t STB = 2 * QB + OB;
   static constexpr uint32_t OFF_K = 0, OFF_V = 2 * KB, OFF_T = OFF_V + VB;
@@ -817,27 +882,32 @@ struct Col {
   static constexpr uint32_t OFF_MISC = OFF_SC + ST * SCB;
   static constexpr uint32_t SMEM = OFF_MISC + 512;
   static_assert(SMEM <= 232448, "column pass shared memory budget");
-  // TMEM columns: S^T of map 1, two buffers for that of map 2 (each thread's 16
-  // columns then hold bf16 dS^T in the last 8 and, for map 2, W^T in the first
-  // 8), dP^T, dK^1, dK^2, dV.  With the second buffer a tile's three score
-  // blocks are all computed while the elementwise warps are on map 2 of the
-  // tile before.
-  static constexpr uint32_t TMEM_COLS = 512, T_S1 = 0, T_DP = 192, T_DV = 384;
-  __host__ __device__ static constexpr uint32_t T_S2(int b) { return 64u + 64u * b; }
-  __host__ __device__ static constexpr uint32_t T_DK(int m) { return 256u + (uint32_t)kD * m; }
+  static_assert(2 * KB + VB <= ST * STB, "dK and dV are staged over the tiles");
+  // TMEM columns.  d = 64: S^T of map 1, two buffers for that of map 2, dP^T,
+  // dK^1, dK^2, dV.  Each thread's 16 columns then hold bf16 dS^T in the last 8
+  // and, for map 2, W^T in the first 8.  With the second buffer a tile's three
+  // score blocks are all computed while the elementwise warps are on map 2 of
+  // the tile before.  d = 128: the accumulators leave two blocks: S^T of map 1,
+  // and dP^T, over which S^T of map 2 goes once dP^T has been read.
+  static constexpr bool WIDE = D == 128;
+  static constexpr uint32_t TMEM_COLS = 512, T_S1 = 0, T_DP = WIDE ? 64 : 192, T_DV = 384;
+  __host__ __device__ static constexpr uint32_t T_S2(int b) { return WIDE ? 64u : 64u + 64u * b; }
+  __host__ __device__ static constexpr uint32_t T_DK(int m) {
+    return (WIDE ? 128u : 256u) + (uint32_t)D * m;
+  }
 };
 
 struct ColParams : Common {
   const float* scal;  // row scalars (diff_tc_scalars)
 };
 
-template <int DV>
+template <int D, int DV>
 __global__ void __launch_bounds__(kThreads, 1)
     diff_col_pass(const __grid_constant__ CUtensorMap mK, const __grid_constant__ CUtensorMap mV,
                   const __grid_constant__ CUtensorMap mQ, const __grid_constant__ CUtensorMap mDO,
                   const __grid_constant__ CUtensorMap mDK, const __grid_constant__ CUtensorMap mDV,
                   ColParams prm) {
-  using C = Col<DV>;
+  using C = Col<D, DV>;
   extern __shared__ __align__(1024) uint8_t smem[];
   const uint32_t sb = smem_u32(smem);
   if (sb & 1023u) {
@@ -923,7 +993,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     }
   } else if (warp == kMmaWarp) {
     constexpr uint32_t id_s = idesc_bf16(128, C::BN, false, false);  // S^T and dP^T
-    constexpr uint32_t id_k = idesc_bf16(128, kD, false, true);      // dK += dS^T Q
+    constexpr uint32_t id_k = idesc_bf16(128, D, false, true);       // dK += dS^T Q
     constexpr uint32_t id_v = idesc_bf16(128, DV, false, true);      // dV += W^T dO
     auto tile = [&](int a) { return sb + C::OFF_T + (uint32_t)(a % C::ST) * C::STB; };
     auto s_cols = [&](int a, int m) { return tmem + (m == 0 ? C::T_S1 : C::T_S2(a & 1)); };
@@ -931,7 +1001,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       const uint32_t k_lo = opaque(lo_kmajor(sb + C::OFF_K + m * C::KB));
       const uint32_t q_lo = opaque(lo_kmajor(tile(a) + m * C::QB));
 #pragma unroll
-      for (int k = 0; k < kD / 16; ++k)
+      for (int k = 0; k < D / 16; ++k)
         mma_ss_w(s_cols(a, m), k_lo + kslice_off(C::BM, k), q_lo + kslice_off(C::BN, k), id_s,
                  k > 0 ? 1u : 0u);
     };
@@ -958,13 +1028,51 @@ __global__ void __launch_bounds__(kThreads, 1)
       for (int k = 0; k < C::BN / 16; ++k)
         mma_ts_w(tmem + C::T_DK(m), t_a + 16 * k + 8, q_mn + kstep_off(k), id_k, (a > 0 || k > 0) ? 1u : 0u);
     };
-    // (the loads of later tiles are awaited by the elementwise warps)
+    // dV += W^T dO
+    auto issue_dv = [&](int a) {
+      const uint32_t do_mn = opaque(lo_mnmajor(tile(a) + 2 * C::QB, C::BN * 128));
+#pragma unroll
+      for (int k = 0; k < C::BN / 16; ++k)
+        mma_ts_w(tmem + C::T_DV, s_cols(a, 1) + 16 * k, do_mn + kstep_off(k), id_v,
+                 (a > 0 || k > 0) ? 1u : 0u);
+    };
     await(kv_full, 0, ab, prm.status);
     await(full, 0, ab, prm.status);
     tc_fence_after();
-    issue_dp(0);
-    issue_scores(0);
-    for (int a = 0; a < T; ++a) {
+    if (C::WIDE) {
+      issue_s(0, 0);
+      issue_dp(0);
+      mma_commit_w(s_full);
+      for (int a = 0; a < T; ++a) {
+        const bool more = a + 1 < T;
+        // S^T of map 2 over dP^T, once every thread has read it
+        await(dp_read, a & 1, ab, prm.status);
+        tc_fence_after();
+        issue_s(a, 1);
+        mma_commit_w(s_full + 1);
+        // dK^1, then the next tile's S^T of map 1 over the dS^T it read
+        if (more) await(full + (a + 1) % C::ST, ((a + 1) / C::ST) & 1, ab, prm.status);
+        await(ds_full, a & 1, ab, prm.status);
+        tc_fence_after();
+        issue_dk(a, 0);
+        if (more) issue_s(a + 1, 0);
+        // dK^2 and dV, then the next dP^T over their operands
+        await(ds_full + 1, a & 1, ab, prm.status);
+        tc_fence_after();
+        issue_dk(a, 1);
+        issue_dv(a);
+        mma_commit_w(empty + a % C::ST);
+        if (more) {
+          issue_dp(a + 1);
+          mma_commit_w(s_full);
+        }
+      }
+    }
+    if (!C::WIDE) {  // (the loads of later tiles are awaited by the elementwise warps)
+      issue_dp(0);
+      issue_scores(0);
+    }
+    for (int a = 0; !C::WIDE && a < T; ++a) {
       const bool more = a + 1 < T;
       // the next dP^T over this one, as soon as every thread has read it
       if (more) {
@@ -981,11 +1089,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       await(ds_full + 1, a & 1, ab, prm.status);
       tc_fence_after();
       issue_dk(a, 1);
-      const uint32_t do_mn = opaque(lo_mnmajor(tile(a) + 2 * C::QB, C::BN * 128));
-#pragma unroll
-      for (int k = 0; k < C::BN / 16; ++k)
-        mma_ts_w(tmem + C::T_DV, s_cols(a, 1) + 16 * k, do_mn + kstep_off(k), id_v,
-                 (a > 0 || k > 0) ? 1u : 0u);
+      issue_dv(a);
       mma_commit_w(empty + a % C::ST);
     }
     mma_commit_w(acc_done);
@@ -1008,8 +1112,9 @@ __global__ void __launch_bounds__(kThreads, 1)
       const bool need_mask = (qa + NC > N) || (prm.causal && qa < j0 + 32 * quad + 31);
       const float4* sc4 = reinterpret_cast<const float4*>(scal + st * 5 * C::BN + NC * slice);
       // this tile's scalars (already there), and for the MMA warp the next tile
-      if (a == 0) await(full, 0, ab, prm.status);
-      if (a + 1 < T) await(full + (a + 1) % C::ST, ((a + 1) / C::ST) & 1, ab, prm.status);
+      if (a == 0 || C::WIDE) await(full + st, (a / C::ST) & 1, ab, prm.status);
+      if (!C::WIDE && a + 1 < T)
+        await(full + (a + 1) % C::ST, ((a + 1) / C::ST) & 1, ab, prm.status);
       uint32_t dp[NC];
       float p1[NC];
 #pragma unroll
@@ -1067,16 +1172,20 @@ __global__ void __launch_bounds__(kThreads, 1)
         warp_arrive(ds_full + m);
       }
     }
-    // ---- epilogue: dK (scaled), 32 features of one map per thread, and dV ----
+    // ---- epilogue: dK (scaled), half the features of one map per thread, and dV ----
     await(acc_done, 0, ab, prm.status);
     tc_fence_after();
-    const int m = slice >> 1, f = 32 * (slice & 1);
+    const int m = slice >> 1;
     uint32_t v[32];
-    tmem_ld32(tmem + lane_off + C::T_DK(m) + f, v);
-    put32(sb + C::OFF_T + m * C::KB, row, f / 8, v, prm.scale);
+#pragma unroll
+    for (int x = 0; x < D / 64; ++x) {
+      const int f = D / 2 * (slice & 1) + 32 * x;
+      tmem_ld32(tmem + lane_off + C::T_DK(0) + D * m + f, v);
+      put32(sb + C::OFF_T + m * C::KB + f / 64 * C::BM * 128, row, f % 64 / 8, v, prm.scale);
+    }
     if (DV == 128 || slice < 2) {
       tmem_ld32(tmem + lane_off + C::T_DV + 32 * slice, v);
-      put32(sb + C::OFF_T + 2 * C::KB + m * C::KB, row, f / 8, v, 1.f);
+      put32(sb + C::OFF_T + 2 * C::KB + m * C::BM * 128, row, 32 * (slice & 1) / 8, v, 1.f);
     }
     fence_async_smem();
     named_sync<kConsumers>(1);
@@ -1134,11 +1243,11 @@ cudaError_t run(K kernel, int units, int N, int threads, uint32_t smem, LaunchLo
   return e;
 }
 
-template <int DV>
-cudaError_t forward_dv(const DiffProblem& p, const DiffTensors& t, const DiffWorkspace& ws,
-                       LaunchLog& log) {
+template <int D, int DV>
+cudaError_t forward_d(const DiffProblem& p, const DiffTensors& t, const DiffWorkspace& ws,
+                      LaunchLog& log) {
   CUtensorMap mQ, mK, mV, mO, mR;  // without rest mR is a placeholder
-  if (!tiles(&mQ, t.q, p, 2 * p.H, kD, 128) || !tiles(&mK, t.k, p, 2 * p.Hk, kD, 128) ||
+  if (!tiles(&mQ, t.q, p, 2 * p.H, D, 128) || !tiles(&mK, t.k, p, 2 * p.Hk, D, 128) ||
       !tiles(&mV, t.v, p, p.Hk, DV, 128) || !tiles(&mO, t.o, p, p.H, DV, 128) ||
       !tiles(&mR, t.rest ? t.rest : t.o, p, p.H, t.rest ? 2 * DV : DV, 128))
     return cudaErrorInvalidValue;
@@ -1146,18 +1255,23 @@ cudaError_t forward_dv(const DiffProblem& p, const DiffTensors& t, const DiffWor
   static_cast<Common&>(f) = common(p, t, ws, p.B * p.H);
   f.rest = t.rest != nullptr;
   f.lse = t.lse;
-  return run(diff_fwd_pass<DV>, f.units, p.N, kFwdThreads, Fwd<DV>::SMEM, log, f, mQ, mK, mV, mO, mR);
+  return run(diff_fwd_pass<D, DV>, f.units, p.N, kFwdThreads, Fwd<D, DV>::SMEM, log, f, mQ, mK, mV,
+             mO, mR);
 }
 
-template <int DV>
-cudaError_t backward_dv(const DiffProblem& p, const DiffTensors& t, const DiffWorkspace& ws,
-                        LaunchLog& log) {
-  CUtensorMap mQ, mK, mV, mDO, sQ, sDO, mDQ, mDK, mDV;  // 128-row tiles; sQ, sDO: of 64
-  if (!tiles(&mQ, t.q, p, 2 * p.H, kD, 128) || !tiles(&mK, t.k, p, 2 * p.Hk, kD, 128) ||
-      !tiles(&mV, t.v, p, p.Hk, DV, 128) || !tiles(&mDO, t.dO, p, p.H, DV, 128) ||
-      !tiles(&sQ, t.q, p, 2 * p.H, kD, 64) || !tiles(&sDO, t.dO, p, p.H, DV, 64) ||
-      !tiles(&mDQ, t.dq, p, 2 * p.H, kD, 128) || !tiles(&mDK, t.dk, p, 2 * p.Hk, kD, 128) ||
-      !tiles(&mDV, t.dv, p, p.Hk, DV, 128))
+template <int D, int DV>
+cudaError_t backward_d(const DiffProblem& p, const DiffTensors& t, const DiffWorkspace& ws,
+                       LaunchLog& log) {
+  using Rw = Row<D, DV>;
+  using Cl = Col<D, DV>;
+  // r: the row pass's, c: the column pass's
+  CUtensorMap rQ, rK, rV, rDO, rDQ, cK, cV, cQ, cDO, cDK, cDV;
+  if (!tiles(&rQ, t.q, p, 2 * p.H, D, Rw::BM) || !tiles(&rK, t.k, p, 2 * p.Hk, D, Rw::BN) ||
+      !tiles(&rV, t.v, p, p.Hk, DV, Rw::BN) || !tiles(&rDO, t.dO, p, p.H, DV, Rw::BM) ||
+      !tiles(&rDQ, t.dq, p, 2 * p.H, D, Rw::BM) || !tiles(&cK, t.k, p, 2 * p.Hk, D, Cl::BM) ||
+      !tiles(&cV, t.v, p, p.Hk, DV, Cl::BM) || !tiles(&cQ, t.q, p, 2 * p.H, D, Cl::BN) ||
+      !tiles(&cDO, t.dO, p, p.H, DV, Cl::BN) || !tiles(&cDK, t.dk, p, 2 * p.Hk, D, Cl::BM) ||
+      !tiles(&cDV, t.dv, p, p.Hk, DV, Cl::BM))
     return cudaErrorInvalidValue;
   const int blocks = (p.N + 63) / 64 * p.B * p.H;
   diff_tc_scalars<DV><<<blocks, 256, 0, log.stream>>>(
@@ -1170,12 +1284,13 @@ cudaError_t backward_dv(const DiffProblem& p, const DiffTensors& t, const DiffWo
   static_cast<Common&>(r) = common(p, t, ws, p.B * p.H);
   r.scal = ws.scal;
   r.d2 = ws.d2;
-  e = run(diff_row_pass<DV>, r.units, p.N, kThreads, Row<DV>::SMEM, log, r, mQ, mK, mV, mDO, mDQ);
+  e = run(diff_row_pass<D, DV>, r.units, p.N, kThreads, Rw::SMEM, log, r, rQ, rK, rV, rDO, rDQ);
   if (e != cudaSuccess) return e;
   ColParams c;
   static_cast<Common&>(c) = common(p, t, ws, p.B * p.Hk);
   c.scal = ws.scal;
-  return run(diff_col_pass<DV>, c.units, p.N, kThreads, Col<DV>::SMEM, log, c, mK, mV, sQ, sDO, mDK, mDV);
+  return run(diff_col_pass<D, DV>, c.units, p.N, kThreads, Cl::SMEM, log, c, cK, cV, cQ, cDO, cDK,
+             cDV);
 }
 
 }  // namespace
@@ -1185,17 +1300,21 @@ size_t diff_tc_scalar_count(const DiffProblem& p) {
 }
 
 bool diff_tc_supported(const DiffProblem& p) {
-  return p.bf16 && p.d == kD && (p.dv == 64 || p.dv == 128);
+  return p.bf16 && (p.d == 64 || p.d == 128) && (p.dv == 64 || p.dv == 128);
 }
 
 cudaError_t diff_tc_forward(const DiffProblem& p, const DiffTensors& t, const DiffWorkspace& ws,
                             LaunchLog& log) {
-  return p.dv == 128 ? forward_dv<128>(p, t, ws, log) : forward_dv<64>(p, t, ws, log);
+  if (p.d == 64)
+    return p.dv == 128 ? forward_d<64, 128>(p, t, ws, log) : forward_d<64, 64>(p, t, ws, log);
+  return p.dv == 128 ? forward_d<128, 128>(p, t, ws, log) : forward_d<128, 64>(p, t, ws, log);
 }
 
 cudaError_t diff_tc_backward(const DiffProblem& p, const DiffTensors& t, const DiffWorkspace& ws,
                              LaunchLog& log) {
-  return p.dv == 128 ? backward_dv<128>(p, t, ws, log) : backward_dv<64>(p, t, ws, log);
+  if (p.d == 64)
+    return p.dv == 128 ? backward_d<64, 128>(p, t, ws, log) : backward_d<64, 64>(p, t, ws, log);
+  return p.dv == 128 ? backward_d<128, 128>(p, t, ws, log) : backward_d<128, 64>(p, t, ws, log);
 }
 
 }  // namespace fbob

@@ -191,7 +191,8 @@ int fbob_set_profile_events(void* const* events, int count);
 /* Process-wide limit, in nanoseconds, of one device-side bounded wait in the
  * tensor-core kernels (default 2 s, far above any legitimate wait).  A wait
  * that runs out records FBOB_ERR_TIMEOUT in the call's status word; every
- * role of that thread block then stops early, waits (with a fixed 100 ms
+ * role of that thread block then stops early (those of fbob_diff_* stop
+ * loading, and run to their end without waiting), waits (with a fixed 100 ms
  * limit of its own) for the copies and MMAs it has in flight, and exits, and
  * the call's outputs are undefined.  The limit is checked each time the
  * waiting thread wakes, at least every 10 us.  ns = 0 restores the default;
@@ -254,11 +255,12 @@ int fbob_rotary(const fbob_rotary_t* r, const void* x, const double* inv_freq,
  * Layouts, all dense and row-major: q [B,2H,N,d] with Q^1, Q^2 of head h as
  * heads 2h, 2h + 1; k [B,2Hk,N,d] likewise; v [B,Hk,N,dv]; o, dO
  * [B,H,N,dv]; lse [B,2H,N] fp32; rest [B,H,N,R,dv], R = 1 for fp32: P^2 V, and
- * R = 2 for bf16: P^2 V and O - o, what o's rounding left off.  H is a multiple of Hk: query head h reads
- * key head h / (H / Hk).  lam is one value, [H], or [B,H,N], bf16 or fp32.
- * Masking, ownership, asynchrony and alignment as above (lam to its own
- * size); scale > 0.  1 <= d, dv <= 128, B*H <= 32767.  fp32, and bf16 at head
- * sizes without a tensor-core kernel (fbob_diff_path), run on CUDA cores.
+ * R = 2 for bf16: P^2 V and O - o, what o's rounding left off.  H is a
+ * multiple of Hk: query head h reads key head h / (H / Hk).  lam is one value,
+ * [H], or [B,H,N], bf16 or fp32.  Masking, ownership, asynchrony and alignment
+ * as above (lam to its own size); scale > 0.  1 <= d, dv <= 128,
+ * B*H <= 32767.  bf16 at d and dv of 64 or 128 runs the tensor-core kernels,
+ * the rest runs on CUDA cores (fbob_diff_path).
  * Every output is summed in a fixed order: equal inputs give equal bits. */
 typedef enum { FBOB_LAM_ONE = 0, FBOB_LAM_HEAD = 1, FBOB_LAM_ROW = 2 } fbob_lam_t;
 

@@ -136,7 +136,13 @@ CASES = [
     (3, 3, 3, 257, 64, 128, BF, False, ("one", BF)),
     (1, 2, 1, 641, 64, 128, BF, True, ("head", BF)),
     (1, 2, 2, 70, 40, 80, BF, True, ("head", BF)),
+    (1, 1, 1, 1, 128, 128, BF, True, ("one", BF)),
     (1, 1, 1, 65, 128, 128, BF, False, ("row", BF)),
+    (2, 4, 2, 129, 128, 64, BF, True, ("head", BF)),
+    (1, 4, 1, 300, 128, 128, BF, False, ("head", F32)),
+    (1, 2, 2, 641, 128, 128, BF, True, ("row", BF)),
+    (1, 2, 1, 640, 128, 64, BF, False, ("one", F32)),
+    (1, 2, 2, 90, 96, 128, BF, True, ("head", BF)),
     (1, 1, 1, 1, 64, 64, F32, True, ("one", F32)),
     (2, 2, 1, 65, 64, 128, F32, True, ("head", F32)),
     (1, 2, 2, 200, 32, 64, F32, False, ("row", F32)),
@@ -181,10 +187,10 @@ class TestOnGpu:
         check(dict(zip(("o", "o2", "lse", "dq", "dk", "dv", "dlam"), (o, rest[..., 0, :], lse, *grads))), vals,
               errs, ("o", "o2", "lse", "dq", "dk", "dv", "dlam"))
 
-    @pytest.mark.parametrize("dtype", [BF, F32])
-    def test_peaked_rows(self, dtype):
+    @pytest.mark.parametrize("dtype,d", [(BF, 64), (BF, 128), (F32, 64)])
+    def test_peaked_rows(self, dtype, d):
         """Scores of tens: probabilities near 0 and 1, maxima that move late."""
-        q, k, v, w, do = inputs(1, 2, 2, 300, 64, 128, dtype, ("head", dtype), seed=4, spread=4.0)
+        q, k, v, w, do = inputs(1, 2, 2, 300, d, 128, dtype, ("head", dtype), seed=4, spread=4.0)
         k = k * torch.linspace(0.1, 1.0, 300, device="cuda").to(dtype)[:, None]
         vals, errs = oracle(q, k, v, w, do, True, 0.125)
         o, rest, lse = fbob.diff_forward(q, k, v, w, True, 0.125)
@@ -204,9 +210,9 @@ class TestOnGpu:
         grads = fbob.diff_backward(q, k, v, w, o, rest, lse, do, True, 0.125)
         check(dict(zip(("dq", "dk", "dv", "dlam"), grads)), vals, errs, ("dq", "dk", "dv", "dlam"))
 
-    @pytest.mark.parametrize("dtype,dv", [(BF, 128), (F32, 64)])
-    def test_same_bits_every_time_and_on_two_streams(self, dtype, dv):
-        q, k, v, w, do = inputs(2, 4, 2, 500, 64, dv, dtype, ("head", dtype), seed=6)
+    @pytest.mark.parametrize("dtype,d,dv", [(BF, 64, 128), (BF, 128, 128), (F32, 64, 64)])
+    def test_same_bits_every_time_and_on_two_streams(self, dtype, d, dv):
+        q, k, v, w, do = inputs(2, 4, 2, 500, d, dv, dtype, ("head", dtype), seed=6)
 
         def both():
             o, rest, lse = fbob.diff_forward(q, k, v, w, True)
@@ -223,11 +229,12 @@ class TestOnGpu:
         for r in results:
             assert all(torch.equal(a, b) for a, b in zip(first, r))
 
-    @pytest.mark.parametrize("dtype,dv", [(BF, 128), (BF, 64), (F32, 64)])
-    def test_outputs_fully_written_and_guards_intact(self, dtype, dv):
+    @pytest.mark.parametrize("dtype,d,dv", [(BF, 64, 128), (BF, 64, 64), (BF, 128, 128), (BF, 128, 64),
+                                            (F32, 64, 64)])
+    def test_outputs_fully_written_and_guards_intact(self, dtype, d, dv):
         """NaN-filled outputs and workspace with guards behind them, through the
         C calls: everything inside is written, nothing outside."""
-        q, k, v, w, do = inputs(1, 2, 1, 200, 64, dv, dtype, ("head", dtype), seed=7)
+        q, k, v, w, do = inputs(1, 2, 1, 200, d, dv, dtype, ("head", dtype), seed=7)
         from exact_second_order_two_gb300.diff_attention import _shape
 
         shp = _shape(q, k, v, w, True, None)
@@ -261,7 +268,7 @@ class TestOnGpu:
             assert torch.isnan(buf[view.numel():].float()).all()
         assert (fws[fn:] == 0xFF).all() and (bws[bn:] == 0xFF).all()
         assert fbob.status(fws) == 0 and fbob.status(bws) == 0
-        vals, errs = oracle(q, k, v, w, do, True, 0.125)
+        vals, errs = oracle(q, k, v, w, do, True, d**-0.5)
         check(dict(zip(("dq", "dk", "dv", "dlam"), (g[1] for g in grads))), vals, errs,
               ("dq", "dk", "dv", "dlam"))
         # a workspace one byte short is refused
@@ -503,8 +510,9 @@ def test_kernel_family_choice():
     for op in (0, 1):
         def path(**kw):
             return lib.fbob_diff_path(op, ctypes.byref(shape(**kw)))
-        assert path() == fbob.PATH_TCGEN05 and path(dv=64) == fbob.PATH_TCGEN05
-        for kw in (dict(dtype=1), dict(d=128), dict(d=32), dict(dv=96), dict(dv=32)):
+        for kw in (dict(), dict(dv=64), dict(d=128), dict(d=128, dv=64)):
+            assert path(**kw) == fbob.PATH_TCGEN05, kw
+        for kw in (dict(dtype=1), dict(d=96), dict(d=32), dict(dv=96), dict(dv=32)):
             assert path(**kw) == fbob.PATH_SIMT, kw
         old = fbob.force_path(fbob.PATH_SIMT)
         try:
