@@ -275,12 +275,11 @@ __global__ void __launch_bounds__(SPLIT * kThreads) diff_fwd(Args a) {
           s[i][j] = (col < N && (!a.causal || col <= r)) ? s[i][j] * a.scale : -INFINITY;
           t = fmaxf(t, s[i][j]);
         }
-        // the first group's rows see a key of its first tile (rows past N too;
-        // they are not stored).  A row that sees none of this tile, nor of the
-        // group's earlier ones, keeps a maximum of -inf: it counts as 0 then,
-        // and every term and sum stays 0
+        // A row that sees no key of this tile, nor of the group's earlier ones
+        // (the second group's at the diagonal; keys of infinite features), keeps
+        // a maximum of -inf: it counts as 0 then, and every term and sum stays 0
         t = fmaxf(mx[m][i], row16_max(t));
-        const float ref = SPLIT > 1 && t == -INFINITY ? 0.f : t;
+        const float ref = t == -INFINITY ? 0.f : t;
         const float alpha = expf(mx[m][i] - ref);
         mx[m][i] = t;
         float sum = 0.f;

@@ -46,6 +46,7 @@
 #include <cuda_bf16.h>
 #include <cuda_runtime.h>
 #include <cudaTypedefs.h>
+#include <float.h>
 #include <math.h>
 #include <type_traits>
 
@@ -418,7 +419,9 @@ __global__ void __launch_bounds__(kFwdThreads, 1)
       const float mt = fmaxf(max3(top[0], top[1], top[2]), top[3]) * sc2;
       const bool move = mt > mx + C::kRescale;
       if (t == 0) {
-        mx = mt;  // finite: key 0 is visible to every row
+        // key 0 is visible to every row, but infinite features can make every
+        // score of the tile -inf, and -inf - -inf would reach the later tiles
+        mx = fmaxf(mt, -FLT_MAX);
       } else if (__any_sync(0xffffffffu, move)) {
         // O^m holds the sums of the earlier tiles, whose products were committed
         // with these scores: rescale the row (rows that did not move by 1)

@@ -53,6 +53,8 @@ def _shape(q, k, v, lam, causal, scale) -> _b.DiffShape:
         raise ValueError(f"v must be [{B}, heads, {N}, width] to go with q")
     if Hk == 0 or H % Hk:
         raise ValueError(f"{H} query heads cannot share {Hk} key heads evenly")
+    if not torch.is_tensor(lam):
+        raise TypeError(f"lam must be a tensor, got {type(lam).__name__}")
     if lam.device != q.device:
         raise ValueError(f"lam is on {lam.device}, expected {q.device}")
     if lam.dtype not in _b.DTYPES:
@@ -83,7 +85,13 @@ def _rest_shape(shp):
     return (shp.B, shp.H, shp.N, 2 if shp.dtype == _b.DTYPES[torch.bfloat16] else 1, shp.dv)
 
 
-def _workspace(op, shp, device):
+def _workspace(op, shp, device, given=None):
+    """The caller's workspace, checked (its size is the library's to check), or
+    a new one."""
+    if given is not None:
+        if given.dtype != torch.uint8 or given.device != device or not given.is_contiguous():
+            raise ValueError(f"workspace must be contiguous uint8 on {device}")
+        return given
     n = _b.lib().fbob_diff_workspace_size(op, ctypes.byref(shp))
     if n == 0:
         raise _b.FbobError(2, "fbob_diff_workspace_size")
@@ -102,13 +110,19 @@ def diff_forward(q, k, v, lam, causal: bool = False, scale: float | None = None,
     k: [B, 2Hk, N, d] likewise; v: [B, Hk, N, dv], with H a multiple of Hk
     (query head h reads key head h // (H / Hk)); bf16 or fp32, contiguous.
     lam: no dimensions, [H] or [B, H, N], bf16 or fp32.  scale > 0 defaults to
-    1/sqrt(d); with ``causal`` key j is visible to query i iff j <= i.
+    1/sqrt(d); with ``causal`` key j is visible to query i iff j <= i.  A key
+    whose score is -inf has no weight; but as in the dense product, an infinite
+    or NaN value reaches rows that give it none (0 times it is NaN): v and
+    upstream gradients are to be finite in padded rows too.
+
+    workspace: uint8 tensor of ``fbob_diff_workspace_size`` bytes for one call
+    at a time, whose ``status`` can be read afterwards; by default a new one.
     """
     shp = _shape(q, k, v, lam, causal, scale)
     o = torch.empty((shp.B, shp.H, shp.N, shp.dv), dtype=q.dtype, device=q.device)
     rest = torch.empty(_rest_shape(shp), dtype=q.dtype, device=q.device) if need_rest else None
     lse = torch.empty((shp.B, 2 * shp.H, shp.N), dtype=torch.float32, device=q.device)
-    ws = _workspace(_b.OP_FORWARD, shp, q.device) if workspace is None else workspace
+    ws = _workspace(_b.OP_FORWARD, shp, q.device, workspace)
     _b.call_on(q.device, "fbob_diff_forward", _b.lib().fbob_diff_forward, ctypes.byref(shp),
                q.data_ptr(), k.data_ptr(), v.data_ptr(), lam.data_ptr(), o.data_ptr(),
                None if rest is None else rest.data_ptr(), lse.data_ptr(), ws.data_ptr(), ws.numel())
@@ -125,7 +139,7 @@ def diff_backward(q, k, v, lam, o, rest, lse, do, causal: bool = False,
         _match(name, t, shape, q.dtype, q.device)
     _match("lse", lse, (shp.B, 2 * shp.H, shp.N), torch.float32, q.device)
     dq, dk, dv, dlam = (torch.empty_like(t) for t in (q, k, v, lam))
-    ws = _workspace(_b.OP_BACKWARD, shp, q.device) if workspace is None else workspace
+    ws = _workspace(_b.OP_BACKWARD, shp, q.device, workspace)
     _b.call_on(q.device, "fbob_diff_backward", _b.lib().fbob_diff_backward, ctypes.byref(shp),
                *(t.data_ptr() for t in (q, k, v, lam, o, rest, lse, do, dq, dk, dv, dlam, ws)),
                ws.numel())
@@ -254,8 +268,12 @@ def diff_attention(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, lam: torch
     q [B, 2H, N, d], k [B, 2Hk, N, d], v [B, Hk, N, dv] and lam as for
     ``diff_forward`` (non-contiguous inputs are copied first).  Returns
     [B, H, N, dv].  Differentiable twice in q, k, v and lam; scale is not
-    differentiated.
+    differentiated.  Backward passes can be captured into a CUDA graph together
+    with their forward, from leaves that no live eager graph was built from
+    (autograd would tie the capture to that graph's stream).
     """
+    if not torch.is_tensor(lam):
+        raise TypeError(f"lam must be a tensor, got {type(lam).__name__}")
     q, k, v, lam = _contig(q), _contig(k), _contig(v), _contig(lam)
     if scale is None:
         scale = 1.0 / math.sqrt(q.shape[-1])

@@ -395,13 +395,78 @@ class TestOnGpu:
             graph.replay()
             assert all(torch.equal(a, b) for a, b in zip(got, both(*new)))
 
-    @pytest.mark.parametrize("dv", [128, 64])
-    def test_kernels_stop_cleanly_when_their_waits_run_out(self, dv):
+    @pytest.mark.parametrize("dtype,d", [(BF, 64), (F32, 64)])
+    def test_captured_training_step(self, dtype, d):
+        """Forward and gradients through autograd, captured twice from fresh
+        leaves and replayed in turn: each graph has its own workspaces."""
+        graphs = []
+        stream = torch.cuda.Stream()
+        for seed in (15, 16):
+            q, k, v, w, do = inputs(1, 2, 1, 150, d, 64, dtype, ("head", dtype), seed=seed)
+            stream.wait_stream(torch.cuda.current_stream())
+            with torch.cuda.stream(stream):
+                leaves = [t.clone().requires_grad_() for t in (q, k, v, w)]
+                torch.autograd.grad(fbob.diff_attention(*leaves, causal=True), leaves, do)
+            torch.cuda.current_stream().wait_stream(stream)
+            torch.cuda.synchronize()
+            leaves = [t.clone().requires_grad_() for t in (q, k, v, w)]
+            graph = torch.cuda.CUDAGraph()
+            with torch.cuda.graph(graph, stream=stream):
+                out = fbob.diff_attention(*leaves, causal=True)
+                got = (out.detach(),) + torch.autograd.grad(out, leaves, do)
+            del out
+            graphs.append((graph, leaves, do, got))
+        for _ in range(2):
+            for graph, *_ in graphs:
+                graph.replay()
+        torch.cuda.synchronize()
+        for _, leaves, do, got in graphs:
+            q, k, v, w = (t.detach() for t in leaves)
+            o, rest, lse = fbob.diff_forward(q, k, v, w, True)
+            want = (o,) + fbob.diff_backward(q, k, v, w, o, rest, lse, do, True)
+            assert all(torch.equal(a, b) for a, b in zip(got, want))
+
+    @pytest.mark.parametrize("dtype,d,dv", [(BF, 64, 128), (BF, 128, 64), (F32, 64, 64), (BF, 40, 24)])
+    def test_keys_whose_scores_are_minus_infinity(self, dtype, d, dv):
+        """Keys with an infinite feature, the first 300 of 350: whole tiles of
+        -inf before the first key that counts give what the other keys give."""
+        q, k, v, w, do = inputs(1, 2, 2, 350, d, dv, dtype, ("head", dtype), seed=17)
+        q[..., 0] = 0.5
+        k[..., 0] = 0.25
+        k[:, :, :300, 0] = -math.inf
+        o, rest, lse = fbob.diff_forward(q, k, v, w)
+        assert torch.isfinite(o.float()).all() and torch.isfinite(lse).all()
+        # the same values densely, in 64 bits, over the last 50 keys; a key's
+        # weight is off by a rounding of P (bf16) and by those of its score
+        S = q.double().view(1, 2, 2, 350, d) @ k[:, :, 300:].double().view(1, 2, 2, 50, d).transpose(-1, -2)
+        P = torch.softmax(S / math.sqrt(d), -1)
+        ww = w.double()[:, None, None]
+        O12 = P @ v[:, :, None, 300:].double()
+        PV = P @ v[:, :, None, 300:].double().abs()
+        eps = torch.finfo(dtype).eps / 2
+        smax = (q.double().abs().amax() * k[:, :, 300:].double().abs().sum(-1).amax() / math.sqrt(d)).item()
+        r = (2 * (d + 4) * smax + 8 + 350 + dv) * U * 2  # as in the oracle
+        mix = PV[:, :, 0] + ww.abs() * PV[:, :, 1]
+        want = O12[:, :, 0] - ww * O12[:, :, 1]
+        err = ((0 if dtype == F32 else eps) + r) * mix
+        err = err + eps * (want.abs() + err)
+        assert ((o.double() - want).abs() <= err).all()
+
+    def test_third_derivative_is_refused(self):
+        q, k, v, w, do = inputs(1, 1, 1, 8, 16, 16, F32, ("one", F32))
+        q.requires_grad_()
+        first, = torch.autograd.grad(fbob.diff_attention(q, k, v, w), q, do, create_graph=True)
+        second, = torch.autograd.grad(first.square().sum(), q, create_graph=True)
+        with pytest.raises(RuntimeError):
+            torch.autograd.grad(second.sum(), q)
+
+    @pytest.mark.parametrize("d,dv", [(64, 128), (64, 64), (128, 128)])
+    def test_kernels_stop_cleanly_when_their_waits_run_out(self, d, dv):
         """A 1 ns wait limit: each call reports the timeout in its workspace's
         status word, and the next call with the default limit is as before."""
         from exact_second_order_two_gb300.diff_attention import _shape, _workspace
 
-        q, k, v, w, do = inputs(1, 2, 1, 2048, 64, dv, BF, ("head", BF), seed=14)
+        q, k, v, w, do = inputs(1, 2, 1, 2048, d, dv, BF, ("head", BF), seed=14)
         shp = _shape(q, k, v, w, True, None)
         fws, bws = (_workspace(op, shp, q.device) for op in (0, 1))
         o, rest, lse = fbob.diff_forward(q, k, v, w, True, workspace=fws)
@@ -438,6 +503,15 @@ class TestOnGpu:
             fbob.diff_attention(q.half(), k.half(), v.half(), w)
         with pytest.raises(TypeError):
             fbob.diff_attention(q, k, v, w.double())
+        with pytest.raises(TypeError):
+            fbob.diff_attention(q, k, v, 0.5)
+        for ws in (torch.empty(1 << 20, dtype=torch.uint8),
+                   torch.empty(1 << 20, dtype=torch.int8, device="cuda"),
+                   torch.empty(1 << 21, dtype=torch.uint8, device="cuda")[::2]):
+            with pytest.raises(ValueError):
+                fbob.diff_forward(q, k, v, w, workspace=ws)
+        with pytest.raises(fbob.FbobError):
+            fbob.diff_forward(q, k, v, w, workspace=torch.empty(16, dtype=torch.uint8, device="cuda"))
         for scale in (0.0, -1.0, float("nan"), float("inf")):
             with pytest.raises(fbob.FbobError):
                 fbob.diff_attention(q, k, v, w, scale=scale)
