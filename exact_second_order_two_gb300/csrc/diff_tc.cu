@@ -17,7 +17,8 @@
 //   second map.
 // column pass (128 key rows, 64-query tiles): dK of both maps and dV, whose
 //   two products are one: W = P^1 - lam P^2 is formed in fp32 and multiplied
-//   with dO once.  A CTA loops over the query heads that share its key head.
+//   with dO once.  A CTA loops over the query heads that share its key head, or
+//   over a part of their queries (col_parts).
 // The row and the column pass recompute the scores rather than exchange dQ
 // through atomics: every output is accumulated by one CTA in a fixed order.
 //
@@ -179,6 +180,13 @@ __device__ __forceinline__ void put32(uint32_t tile, int row, int c, const uint3
                        __uint_as_float(v[8 * q + 2 * e + 1]) * mul);
     st_shared_v4(tile + sw128_offset(row, c + q), w[0], w[1], w[2], w[3]);
   }
+}
+
+// 32 fp32 values to 128 bytes of one row (16-byte aligned)
+__device__ __forceinline__ void put32_global(float* dst, const uint32_t (&v)[32]) {
+#pragma unroll
+  for (int q = 0; q < 8; ++q)
+    reinterpret_cast<uint4*>(dst)[q] = make_uint4(v[4 * q], v[4 * q + 1], v[4 * q + 2], v[4 * q + 3]);
 }
 
 // ===========================================================================
@@ -902,9 +910,12 @@ struct Col {
 
 struct ColParams : Common {
   const float* scal;  // row scalars (diff_tc_scalars)
+  float* parts;       // [gridDim.y][B Hk][N][2 D + DV]: partial dK^1, dK^2, dV
 };
 
-template <int D, int DV>
+// PARTS: gridDim.y CTAs share a key block (the branches of one kernel for both
+// cost the whole blocks 1%)
+template <int D, int DV, bool PARTS>
 __global__ void __launch_bounds__(kThreads, 1)
     diff_col_pass(const __grid_constant__ CUtensorMap mK, const __grid_constant__ CUtensorMap mV,
                   const __grid_constant__ CUtensorMap mQ, const __grid_constant__ CUtensorMap mDO,
@@ -938,7 +949,17 @@ __global__ void __launch_bounds__(kThreads, 1)
   const int j0 = cc.blk * C::BM;
   const int qstart = prm.causal ? j0 : 0;  // j0 is a multiple of BN
   const int Tq = (N - qstart + C::BN - 1) / C::BN;
-  const int T = Tq * prm.G;  // query tiles of all the query heads
+  // query tiles of all the query heads; this CTA's: a0 .. a0 + T - 1
+  const int all = Tq * prm.G, part = blockIdx.y, split = gridDim.y;
+  const int a0 = PARTS ? (int)((long long)all * part / split) : 0;
+  const int T = PARTS ? (int)((long long)all * (part + 1) / split) - a0 : all;
+  float* part_rows = prm.parts + ((size_t)part * prm.units + kvh) * N * (2 * D + DV);
+  if (PARTS && T == 0) {  // the mask leaves this part nothing
+    const int rows = min(C::BM, N - j0);
+    for (int e = threadIdx.x; e < rows * (2 * D + DV); e += kThreads)
+      part_rows[(size_t)j0 * (2 * D + DV) + e] = 0.f;
+    return;
+  }
 
   if (threadIdx.x == 0) {
     mbar_init(kv_full, 1);
@@ -974,7 +995,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       load_tile(smem + C::OFF_K + C::KB, &mK, kv_full, j0, 2 * kvh + 1);
     }
     if (lane == 0) {
-      int g = 0, t = 0, issued = 0;  // tile t within head g
+      int g = PARTS ? a0 / Tq : 0, t = PARTS ? a0 % Tq : 0, issued = 0;  // tile t within head g
       for (int a = 0; a < T; ++a) {
         const int st = a % C::ST, q0 = qstart + t * C::BN, bh = bh0 + g;
         if (a >= C::ST && !wait_bar(empty + st, ((a / C::ST) - 1) & 1, ab, prm.status)) break;
@@ -1107,7 +1128,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     const uint32_t lane_off = (uint32_t)(32 * quad) << 16;
     const float sc2 = prm.scale * kLog2e;
     const f2 sc2_2 = {sc2, sc2};
-    int t = 0;
+    int t = PARTS ? a0 % Tq : 0;
     for (int a = 0; a < T; ++a) {
       const int st = a % C::ST;
       const int qa = qstart + t * C::BN + NC * slice;
@@ -1180,19 +1201,27 @@ __global__ void __launch_bounds__(kThreads, 1)
     tc_fence_after();
     const int m = slice >> 1;
     uint32_t v[32];
+    // a part's sums go out in fp32, for diff_col_join
+    float* mine = part_rows + (size_t)j * (2 * D + DV);
 #pragma unroll
     for (int x = 0; x < D / 64; ++x) {
       const int f = D / 2 * (slice & 1) + 32 * x;
       tmem_ld32(tmem + lane_off + C::T_DK(0) + D * m + f, v);
-      put32(sb + C::OFF_T + m * C::KB + f / 64 * C::BM * 128, row, f % 64 / 8, v, prm.scale);
+      if (!PARTS)
+        put32(sb + C::OFF_T + m * C::KB + f / 64 * C::BM * 128, row, f % 64 / 8, v, prm.scale);
+      else if (j < N)
+        put32_global(mine + D * m + f, v);
     }
     if (DV == 128 || slice < 2) {
       tmem_ld32(tmem + lane_off + C::T_DV + 32 * slice, v);
-      put32(sb + C::OFF_T + 2 * C::KB + m * C::BM * 128, row, 32 * (slice & 1) / 8, v, 1.f);
+      if (!PARTS)
+        put32(sb + C::OFF_T + 2 * C::KB + m * C::BM * 128, row, 32 * (slice & 1) / 8, v, 1.f);
+      else if (j < N)
+        put32_global(mine + 2 * D + 32 * slice, v);
     }
     fence_async_smem();
     named_sync<kConsumers>(1);
-    if (threadIdx.x == 0) {
+    if (!PARTS && threadIdx.x == 0) {
       store_tile(&mDK, smem + C::OFF_T, j0, 2 * kvh);
       store_tile(&mDK, smem + C::OFF_T + C::KB, j0, 2 * kvh + 1);
       store_tile(&mDV, smem + C::OFF_T + 2 * C::KB, j0, kvh);
@@ -1207,9 +1236,51 @@ __global__ void __launch_bounds__(kThreads, 1)
   }
 }
 
+// dK (scaled) and dV from the column pass's parts, added in their order: a
+// thread per 4 features of a key row.
+template <int D, int DV>
+__global__ void __launch_bounds__(256)
+    diff_col_join(const float4* __restrict__ parts, uint2* __restrict__ dk, uint2* __restrict__ dv,
+                  int split, int N, size_t rows, float scale) {
+  constexpr int W = (2 * D + DV) / 4;
+  const size_t e = (size_t)blockIdx.x * 256 + threadIdx.x;
+  if (e >= rows * W) return;
+  float4 x = parts[e];
+  for (int s = 1; s < split; ++s) {
+    const float4 y = parts[(size_t)s * rows * W + e];
+    x.x += y.x;
+    x.y += y.y;
+    x.z += y.z;
+    x.w += y.w;
+  }
+  const size_t row = e / W, kvh = row / N, j = row - kvh * N;
+  const int f = (int)(e - row * W);
+  if (f < 2 * D / 4) {
+    const int m = f / (D / 4);
+    dk[((2 * kvh + m) * N + j) * (D / 4) + f % (D / 4)] =
+        make_uint2(pack_bf16(x.x * scale, x.y * scale), pack_bf16(x.z * scale, x.w * scale));
+  } else {
+    dv[row * (DV / 4) + f - 2 * D / 4] = make_uint2(pack_bf16(x.x, x.y), pack_bf16(x.z, x.w));
+  }
+}
+
 // ---------------------------------------------------------------------------
 // host side
 // ---------------------------------------------------------------------------
+// Parts of the column pass: with few key heads or keys its blocks leave SMs
+// idle, while each walks over the queries of every head of its group.  So it is
+// cut into as many parts as the SMs take, of 8 or more 64-query tiles each, and
+// their sums are joined.  dK and dV at d = 64, dv = 128, causal, in one part and
+// cut: 2 key heads of 16 heads, 2048 tokens 276 -> 82 + 4 us; 1 of 8, 512 tokens
+// 77 -> 24 + 4; 2 of 2, 2048 tokens 43 -> 24 + 4; but with 16 tiles to cut (8 of
+// 8 heads, 1024 tokens) 26 -> 25 + 4, so fewer than 24 stay whole.
+int col_parts(const DiffProblem& p) {
+  constexpr long long kSms = 152, kTiles = 8;
+  const long long blocks = (long long)((p.N + 127) / 128) * p.B * p.Hk;
+  const long long tiles = (long long)((p.N + 63) / 64) * p.G();
+  return tiles < 3 * kTiles ? 1 : (int)max(1ll, min(kSms / blocks, tiles / kTiles));
+}
+
 Common common(const DiffProblem& p, const DiffTensors& t, const DiffWorkspace& ws, int units) {
   Common c{};
   c.status = ws.status;
@@ -1236,11 +1307,11 @@ bool tiles(CUtensorMap* m, const void* ptr, const DiffProblem& p, int heads, int
 }
 
 template <typename K, typename P, typename... M>
-cudaError_t run(K kernel, int units, int N, int threads, uint32_t smem, LaunchLog& log, const P& prm,
-                const M&... maps) {
+cudaError_t run(K kernel, int units, int parts, int N, int threads, uint32_t smem, LaunchLog& log,
+                const P& prm, const M&... maps) {
   cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
   if (e != cudaSuccess) return e;
-  kernel<<<(unsigned)(((N + 127) / 128) * units), threads, smem, log.stream>>>(maps..., prm);
+  kernel<<<dim3(((N + 127) / 128) * units, parts), threads, smem, log.stream>>>(maps..., prm);
   e = cudaGetLastError();
   log.mark();
   return e;
@@ -1258,7 +1329,7 @@ cudaError_t forward_d(const DiffProblem& p, const DiffTensors& t, const DiffWork
   static_cast<Common&>(f) = common(p, t, ws, p.B * p.H);
   f.rest = t.rest != nullptr;
   f.lse = t.lse;
-  return run(diff_fwd_pass<D, DV>, f.units, p.N, kFwdThreads, Fwd<D, DV>::SMEM, log, f, mQ, mK, mV,
+  return run(diff_fwd_pass<D, DV>, f.units, 1, p.N, kFwdThreads, Fwd<D, DV>::SMEM, log, f, mQ, mK, mV,
              mO, mR);
 }
 
@@ -1287,19 +1358,37 @@ cudaError_t backward_d(const DiffProblem& p, const DiffTensors& t, const DiffWor
   static_cast<Common&>(r) = common(p, t, ws, p.B * p.H);
   r.scal = ws.scal;
   r.d2 = ws.d2;
-  e = run(diff_row_pass<D, DV>, r.units, p.N, kThreads, Rw::SMEM, log, r, rQ, rK, rV, rDO, rDQ);
+  e = run(diff_row_pass<D, DV>, r.units, 1, p.N, kThreads, Rw::SMEM, log, r, rQ, rK, rV, rDO, rDQ);
   if (e != cudaSuccess) return e;
   ColParams c;
   static_cast<Common&>(c) = common(p, t, ws, p.B * p.Hk);
   c.scal = ws.scal;
-  return run(diff_col_pass<D, DV>, c.units, p.N, kThreads, Cl::SMEM, log, c, cK, cV, cQ, cDO, cDK,
-             cDV);
+  c.parts = ws.parts;
+  const int parts = col_parts(p);
+  if (parts == 1)
+    return run(diff_col_pass<D, DV, false>, c.units, 1, p.N, kThreads, Cl::SMEM, log, c, cK, cV, cQ,
+               cDO, cDK, cDV);
+  e = run(diff_col_pass<D, DV, true>, c.units, parts, p.N, kThreads, Cl::SMEM, log, c, cK, cV, cQ,
+          cDO, cDK, cDV);
+  if (e != cudaSuccess) return e;
+  const size_t rows = (size_t)c.units * p.N, quads = rows * ((2 * D + DV) / 4);
+  diff_col_join<D, DV><<<(unsigned)((quads + 255) / 256), 256, 0, log.stream>>>(
+      reinterpret_cast<const float4*>(ws.parts), static_cast<uint2*>(t.dk),
+      static_cast<uint2*>(t.dv), parts, p.N, rows, p.scale);
+  e = cudaGetLastError();
+  log.mark();
+  return e;
 }
 
 }  // namespace
 
 size_t diff_tc_scalar_count(const DiffProblem& p) {
   return (size_t)p.B * p.H * ((p.N + 63) / 64) * 5 * 64;
+}
+
+size_t diff_tc_part_count(const DiffProblem& p) {
+  const int parts = col_parts(p);
+  return parts == 1 ? 0 : (size_t)parts * p.B * p.Hk * p.N * (2 * p.d + p.dv);
 }
 
 bool diff_tc_supported(const DiffProblem& p) {

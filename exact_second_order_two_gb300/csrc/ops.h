@@ -39,6 +39,7 @@ struct DiffWorkspace {
   float* scal = nullptr;     // the row scalars' blocks (tensor cores)
   float* d2 = nullptr;       // [B, H, N]: sum_j P^2_ij dP_ij, for lam's gradient
   float* partial = nullptr;  // [B, H]: its sums
+  float* parts = nullptr;    // parts of dK and dV (tensor cores, few blocks)
 };
 
 struct DiffTensors {
@@ -59,6 +60,7 @@ cudaError_t diff_simt_backward(const DiffProblem& p, const DiffTensors& t, const
 // ---- tensor-core kernels: bf16, d and dv = 64 or 128 ------------------------
 bool diff_tc_supported(const DiffProblem& p);
 size_t diff_tc_scalar_count(const DiffProblem& p);  // fp32 values of DiffWorkspace::scal
+size_t diff_tc_part_count(const DiffProblem& p);    // fp32 values of DiffWorkspace::parts
 cudaError_t diff_tc_forward(const DiffProblem& p, const DiffTensors& t, const DiffWorkspace& ws,
                             LaunchLog& log);
 cudaError_t diff_tc_backward(const DiffProblem& p, const DiffTensors& t, const DiffWorkspace& ws,

@@ -135,6 +135,11 @@ CASES = [
     (1, 4, 1, 300, 64, 64, BF, True, ("row", F32)),
     (3, 3, 3, 257, 64, 128, BF, False, ("one", BF)),
     (1, 2, 1, 641, 64, 128, BF, True, ("head", BF)),
+    # dK and dV in parts: over the heads of a group, and over the queries, with
+    # parts that a causal mask leaves empty
+    (1, 8, 2, 1000, 64, 64, BF, False, ("one", BF)),
+    (1, 1, 1, 2050, 64, 128, BF, True, ("head", F32)),
+    (1, 2, 1, 1500, 128, 128, BF, True, ("head", BF)),
     (1, 2, 2, 70, 40, 80, BF, True, ("head", BF)),
     (1, 1, 1, 1, 128, 128, BF, True, ("one", BF)),
     (1, 1, 1, 65, 128, 128, BF, False, ("row", BF)),
@@ -212,7 +217,7 @@ class TestOnGpu:
 
     @pytest.mark.parametrize("dtype,d,dv", [(BF, 64, 128), (BF, 128, 128), (F32, 64, 64)])
     def test_same_bits_every_time_and_on_two_streams(self, dtype, d, dv):
-        q, k, v, w, do = inputs(2, 4, 2, 500, d, dv, dtype, ("head", dtype), seed=6)
+        q, k, v, w, do = inputs(2, 4, 1, 500, d, dv, dtype, ("head", dtype), seed=6)
 
         def both():
             o, rest, lse = fbob.diff_forward(q, k, v, w, True)
@@ -234,7 +239,7 @@ class TestOnGpu:
     def test_outputs_fully_written_and_guards_intact(self, dtype, d, dv):
         """NaN-filled outputs and workspace with guards behind them, through the
         C calls: everything inside is written, nothing outside."""
-        q, k, v, w, do = inputs(1, 2, 1, 200, d, dv, dtype, ("head", dtype), seed=7)
+        q, k, v, w, do = inputs(1, 8, 1, 200, d, dv, dtype, ("head", dtype), seed=7)
         from exact_second_order_two_gb300.diff_attention import _shape
 
         shp = _shape(q, k, v, w, True, None)
@@ -250,9 +255,9 @@ class TestOnGpu:
             buf = torch.full((n + 4096,), 0xFF, dtype=torch.uint8, device="cuda")
             return buf, n
 
-        o = guarded((1, 2, 200, dv), dtype)
-        rest = guarded((1, 2, 200, 2 if dtype == BF else 1, dv), dtype)
-        lse = guarded((1, 4, 200), F32)
+        o = guarded((1, 8, 200, dv), dtype)
+        rest = guarded((1, 8, 200, 2 if dtype == BF else 1, dv), dtype)
+        lse = guarded((1, 16, 200), F32)
         fws, fn = workspace(0)
         args = [t.data_ptr() for t in (q, k, v, w)]
         assert lib.fbob_diff_forward(ctypes.byref(shp), *args, o[1].data_ptr(), rest[1].data_ptr(),
