@@ -5,21 +5,23 @@
 //   dS^2 = -lam P^2*(dP - D^2), dQ^m = c dS^m K^m, dK^m = c dS^mT Q^m,
 //   dV = (P^1 - lam P^2)^T dO, dlam_i = -sum_j P^2_ij dP_ij.
 //
-// Arithmetic is fp32 throughout.  A block of 8 x 16 threads holds a 32-row
-// tile (queries, or keys for dK and dV) and streams 64-row tiles of the other
-// side through shared memory; thread (ty, tx) computes the 4 x 4 scores of
-// rows 4 ty.. and columns tx + 16 j.  A row of scores lives in 16 lanes of one
-// warp, so row maxima and sums are shuffles, and the probabilities pass to
-// their product through shared memory inside the warp.  Bound: FFMA issue,
-// at 8 FFMA per 16-byte shared-memory read; with one warp per scheduler it is
-// latency, so where shared memory allows (SPLIT = 2) two such groups of
-// threads share a block's stationary tile, take every other streamed tile each
-// with tiles of their own, and add up at the end.  Everything a row or key
-// accumulates is summed by one block in a fixed order.
+// Arithmetic is fp32 throughout.  A group of 8 x 16 threads holds a 32-row
+// tile (queries, or keys for dK and dV) against 64-row tiles of the other side
+// in shared memory; thread (ty, tx) computes the 4 x 4 scores of rows 4 ty.. and
+// columns tx + 16 j.  A row of scores lives in 16 lanes of one warp, so row
+// maxima and sums are shuffles, and the probabilities pass to their product
+// through shared memory inside the warp.  The floor is FFMA issue, at 8 FFMA per
+// 16-byte shared-memory read; with one or two warps per scheduler latency counts
+// more, so several groups share a stationary tile: in the forward one per map,
+// which read the same values; and where shared memory allows (SPLIT = 2) twice
+// as many, which take every other streamed tile with tiles of their own, and
+// add up at the end.  Everything a row or key accumulates is summed by one block
+// in a fixed order.
 //
-// Measured, fp32: forward at 4 heads x 2049 tokens, d = 64, dv = 128, causal
-// 254 us (25 TFLOP/s; 573 us with 64-row tiles and plain loads, 371 us with one
-// group of threads); forward, dQ, dK/dV at 4 x 256, d = dv = 64 26, 32, 35 us.
+// Measured, fp32, d = 64: forward at 4 heads x 2049 tokens, dv = 128, causal
+// 208 us (31 TFLOP/s; 254 us with both maps in one group and two groups), dQ 249,
+// dK and dV 320; at 2 x 8 heads x 4096 tokens, dv = 64 1.86 ms (2.39), 2.90 and
+// 3.45 ms.
 #include <cuda_bf16.h>
 #include <math.h>
 
@@ -30,6 +32,7 @@
 namespace fbob {
 namespace {
 
+constexpr int kSms = 152;    // of a GB300
 constexpr int kM = 32;       // rows of the stationary tile
 constexpr int kT = 64;       // rows of a streamed tile
 constexpr int kThreads = 128;  // of a group
@@ -148,7 +151,7 @@ template <int NG>
 __device__ __forceinline__ void tile_add(float (&acc)[4][4 * NG], const float* P, const float* X,
                                          int ld, int width, int ty, int tx) {
   const float* p0 = P + 4 * ty * kLdp;
-#pragma unroll 2
+#pragma unroll 4
   for (int k = 0; k < kT; k += 4) {
     float4 p[4];
 #pragma unroll
@@ -218,146 +221,164 @@ __device__ __forceinline__ float row16_sum(float v) {
   return v;
 }
 
-// ---- forward: one block per 32 query rows of a head -----------------------
+// Floats of one pair's area: its tiles, or what it hands over at the end.
+__host__ __device__ inline int fwd_area(int d, int dv) {
+  const int tiles = kT * (2 * ld_of(d) + ld_of(dv)) + 2 * kM * kLdp;
+  const int sums = (16 * (dv <= 64 ? 1 : 2) + 8) * 2 * kThreads;
+  return tiles > sums ? tiles : sums;
+}
+
+// ---- forward: one block per 32 query rows of a head, a group of threads per
+// map; SPLIT = 2: two such pairs of groups take every other key tile, and the
+// first adds up --------------------------------------------------------------
 template <typename T, int NGV, int SPLIT>
-__global__ void __launch_bounds__(SPLIT * kThreads) diff_fwd(Args a) {
+__global__ void __launch_bounds__(SPLIT * 2 * kThreads, 2 / SPLIT) diff_fwd(Args a) {
   extern __shared__ __align__(16) float sm[];
   const int ld = ld_of(a.d), ldv = ld_of(a.dv_), N = a.N;
-  const int grp = threadIdx.x / kThreads, tid = threadIdx.x % kThreads;
+  const int m = threadIdx.x / kThreads % 2, tid = threadIdx.x % kThreads;
+  const int half = threadIdx.x / (2 * kThreads);
   const int ty = tid >> 4, tx = tid & 15;
-  float* qs = sm;                      // [2][32][ld]
-  float* mine = qs + 2 * kM * ld;      // the group's area
-  const int area = group_floats(kT * (2 * ld + ldv) + kM * kLdp, 32 * NGV + 16);
-  const float* other = mine + area;    // the second group's, for the first
-  if (grp == 1) mine += area;
-  float* ks = mine;                    // [2][64][ld]
-  float* vs = ks + 2 * kT * ld;        // [64][ldv]
-  float* ps = vs + kT * ldv;           // [32][kLdp]
+  float* qs = sm + m * kM * ld;                    // [2][32][ld]
+  float* pair = sm + 2 * kM * ld;                  // the pair's area
+  const int area = fwd_area(a.d, a.dv_);
+  const float* other = pair + area;                // the second pair's, for the first
+  if (half == 1) pair += area;
+  float* ks = pair + m * kT * ld;                  // [2][64][ld]
+  float* vs = pair + 2 * kT * ld;                  // [64][ldv]
+  float* ps = vs + kT * ldv + m * kM * kLdp;       // [2][32][kLdp]
+  // barrier of the pair
+  auto pair_sync = [&] {
+    if constexpr (SPLIT == 1) __syncthreads();
+    else asm volatile("bar.sync %0, %1;" ::"r"(1 + half), "n"(2 * kThreads) : "memory");
+  };
+  // heads vary fastest, and the long rows of all of them start first
   const int bh = blockIdx.x % a.heads, b = bh / a.H, h = bh % a.H;
   const int kvh = b * (a.H / a.G) + h / a.G;
-  // heads vary fastest, and the long rows of all of them start first
   const int blk = blockIdx.x / a.heads;
   const int row0 = (a.causal ? (int)(gridDim.x / a.heads) - 1 - blk : blk) * kM;
   const size_t qsz = (size_t)N * a.d;
-  const T* q = static_cast<const T*>(a.q) + (size_t)bh * 2 * qsz;
-  const T* k = static_cast<const T*>(a.k) + (size_t)kvh * 2 * qsz;
+  const T* q = static_cast<const T*>(a.q) + ((size_t)bh * 2 + m) * qsz;
+  const T* k = static_cast<const T*>(a.k) + ((size_t)kvh * 2 + m) * qsz;
   const T* v = static_cast<const T*>(a.v) + (size_t)kvh * N * a.dv_;
-  if (grp == 0) load_rows<kM>(tid, qs, ld, q, row0, N, a.d);
-  if (grp == SPLIT - 1) load_rows<kM>(tid, qs + kM * ld, ld, q + qsz, row0, N, a.d);
-  loads_done();
-  __syncthreads();
+  if (half == 0) load_rows<kM>(tid, qs, ld, q, row0, N, a.d);
+  if (SPLIT > 1) {
+    loads_done();
+    __syncthreads();
+  }
 
-  float acc[2][4][4 * NGV], mx[2][4], l[2][4];
+  float acc[4][4 * NGV], mx[4], l[4];
 #pragma unroll
-  for (int m = 0; m < 2; ++m)
+  for (int i = 0; i < 4; ++i) {
+    mx[i] = -INFINITY;
+    l[i] = 0.f;
+#pragma unroll
+    for (int e = 0; e < 4 * NGV; ++e) acc[i][e] = 0.f;
+  }
+  const int kend = a.causal ? min(N, row0 + kM) : N;
+  for (int j0 = half * kT; j0 < kend; j0 += SPLIT * kT) {
+    pair_sync();
+    load_rows<kT>(tid, ks, ld, k, j0, N, a.d);
+    load_rows<kT / 2>(tid, vs + m * (kT / 2) * ldv, ldv, v, j0 + m * (kT / 2), N, a.dv_);
+    loads_done();
+    pair_sync();
+    float s[4][4];
+    tile_dot(s, qs, ks, ld, a.d, ty, tx);
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
-      mx[m][i] = -INFINITY;
-      l[m][i] = 0.f;
+      const int r = row0 + 4 * ty + i;
+      float t = -INFINITY;
 #pragma unroll
-      for (int e = 0; e < 4 * NGV; ++e) acc[m][i][e] = 0.f;
-    }
-  const int kend = a.causal ? min(N, row0 + kM) : N;
-  for (int j0 = grp * kT; j0 < kend; j0 += SPLIT * kT) {
-    group_sync<SPLIT>(grp);
-    load_rows<kT>(tid, ks, ld, k, j0, N, a.d);
-    load_rows<kT>(tid, ks + kT * ld, ld, k + qsz, j0, N, a.d);
-    load_rows<kT>(tid, vs, ldv, v, j0, N, a.dv_);
-    loads_done();
-    group_sync<SPLIT>(grp);
-#pragma unroll
-    for (int m = 0; m < 2; ++m) {
-      float s[4][4];
-      tile_dot(s, qs + m * kM * ld, ks + m * kT * ld, ld, a.d, ty, tx);
-#pragma unroll
-      for (int i = 0; i < 4; ++i) {
-        const int r = row0 + 4 * ty + i;
-        float t = -INFINITY;
-#pragma unroll
-        for (int j = 0; j < 4; ++j) {
-          const int col = j0 + tx + 16 * j;
-          s[i][j] = (col < N && (!a.causal || col <= r)) ? s[i][j] * a.scale : -INFINITY;
-          t = fmaxf(t, s[i][j]);
-        }
-        // A row that sees no key of this tile, nor of the group's earlier ones
-        // (the second group's at the diagonal; keys of infinite features), keeps
-        // a maximum of -inf: it counts as 0 then, and every term and sum stays 0
-        t = fmaxf(mx[m][i], row16_max(t));
-        const float ref = t == -INFINITY ? 0.f : t;
-        const float alpha = expf(mx[m][i] - ref);
-        mx[m][i] = t;
-        float sum = 0.f;
-#pragma unroll
-        for (int j = 0; j < 4; ++j) {
-          s[i][j] = expf(s[i][j] - ref);
-          sum += s[i][j];
-        }
-        l[m][i] = l[m][i] * alpha + row16_sum(sum);
-#pragma unroll
-        for (int e = 0; e < 4 * NGV; ++e) acc[m][i][e] *= alpha;
+      for (int j = 0; j < 4; ++j) {
+        const int col = j0 + tx + 16 * j;
+        s[i][j] = (col < N && (!a.causal || col <= r)) ? s[i][j] * a.scale : -INFINITY;
+        t = fmaxf(t, s[i][j]);
       }
-      put_tile(ps, s, ty, tx);
-      tile_add<NGV>(acc[m], ps, vs, ldv, a.dv_, ty, tx);
+      // A row that has seen no key yet (the second pair's at the diagonal; keys
+      // of infinite features) keeps a maximum of -inf: it counts as 0 then, and
+      // every term and sum stays 0
+      t = fmaxf(mx[i], row16_max(t));
+      const float ref = t == -INFINITY ? 0.f : t;
+      const float alpha = expf(mx[i] - ref);
+      mx[i] = t;
+      float sum = 0.f;
+#pragma unroll
+      for (int j = 0; j < 4; ++j) {
+        s[i][j] = expf(s[i][j] - ref);
+        sum += s[i][j];
+      }
+      l[i] = l[i] * alpha + row16_sum(sum);
+#pragma unroll
+      for (int e = 0; e < 4 * NGV; ++e) acc[i][e] *= alpha;
     }
+    put_tile(ps, s, ty, tx);
+    tile_add<NGV>(acc, ps, vs, ldv, a.dv_, ty, tx);
   }
   if constexpr (SPLIT > 1) {
-    // the second group hands over; the first combines against the joint maximum
-    group_sync<SPLIT>(grp);
-    if (grp == 1) {
-#pragma unroll
-      for (int m = 0; m < 2; ++m)
-#pragma unroll
-        for (int i = 0; i < 4; ++i) {
-#pragma unroll
-          for (int e = 0; e < 4 * NGV; ++e)
-            mine[((m * 4 + i) * 4 * NGV + e) * kThreads + tid] = acc[m][i][e];
-          mine[(32 * NGV + m * 4 + i) * kThreads + tid] = mx[m][i];
-          mine[(32 * NGV + 8 + m * 4 + i) * kThreads + tid] = l[m][i];
-        }
-    }
-    __syncthreads();
-    if (grp == 1) return;
-#pragma unroll
-    for (int m = 0; m < 2; ++m)
+    // the second pair hands over; the first combines against the joint maximum
+    constexpr int S = 2 * kThreads;
+    const int at = m * kThreads + tid;
+    pair_sync();
+    if (half == 1) {
 #pragma unroll
       for (int i = 0; i < 4; ++i) {
-        const float m2 = other[(32 * NGV + m * 4 + i) * kThreads + tid];
-        const float top = fmaxf(mx[m][i], m2);
-        const float f1 = expf(mx[m][i] - top), f2 = expf(m2 - top);
-        mx[m][i] = top;
-        l[m][i] = l[m][i] * f1 + other[(32 * NGV + 8 + m * 4 + i) * kThreads + tid] * f2;
 #pragma unroll
-        for (int e = 0; e < 4 * NGV; ++e)
-          acc[m][i][e] = acc[m][i][e] * f1 + other[((m * 4 + i) * 4 * NGV + e) * kThreads + tid] * f2;
+        for (int e = 0; e < 4 * NGV; ++e) pair[(i * 4 * NGV + e) * S + at] = acc[i][e];
+        pair[(16 * NGV + i) * S + at] = mx[i];
+        pair[(16 * NGV + 4 + i) * S + at] = l[i];
       }
+    }
+    __syncthreads();
+    if (half == 1) return;
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      const float m2 = other[(16 * NGV + i) * S + at];
+      const float top = fmaxf(mx[i], m2);
+      const float f1 = expf(mx[i] - top), f2 = expf(m2 - top);
+      mx[i] = top;
+      l[i] = l[i] * f1 + other[(16 * NGV + 4 + i) * S + at] * f2;
+#pragma unroll
+      for (int e = 0; e < 4 * NGV; ++e)
+        acc[i][e] = acc[i][e] * f1 + other[(i * 4 * NGV + e) * S + at] * f2;
+    }
+  }
+  const size_t ob = (size_t)bh * N * a.dv_;
+  constexpr int R = sizeof(T) == 2 ? 2 : 1;
+  T* rest = static_cast<T*>(a.rest) + R * ob;
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    const int r = row0 + 4 * ty + i;
+    const float inv = 1.f / l[i];
+#pragma unroll
+    for (int e = 0; e < 4 * NGV; ++e) acc[i][e] *= inv;
+    if (r < N && tx == 0 && a.lse) a.lse[((size_t)bh * 2 + m) * N + r] = mx[i] + logf(l[i]);
+  }
+  pair_sync();
+  if (m == 1) {
+#pragma unroll
+    for (int i = 0; i < 4; ++i)
+#pragma unroll
+      for (int e = 0; e < 4 * NGV; ++e) pair[(i * 4 * NGV + e) * kThreads + tid] = acc[i][e];
+  }
+  pair_sync();
+  if (m == 1) {
+    if (a.rest) store_rows<T, NGV>(rest, acc, 1.f, row0, N, a.dv_, R * a.dv_, ty, tx);
+    return;
   }
 #pragma unroll
   for (int i = 0; i < 4; ++i) {
     const int r = row0 + 4 * ty + i;
     const float w = r < N ? lam_at(a.lam, a.H, N, b, h, r) : 0.f;
-    const float i1 = 1.f / l[0][i], i2 = 1.f / l[1][i];
 #pragma unroll
-    for (int e = 0; e < 4 * NGV; ++e) {
-      acc[1][i][e] *= i2;
-      acc[0][i][e] = acc[0][i][e] * i1 - w * acc[1][i][e];
-    }
-    if (r < N && tx == 0 && a.lse) {
-      a.lse[((size_t)bh * 2 + 0) * N + r] = mx[0][i] + logf(l[0][i]);
-      a.lse[((size_t)bh * 2 + 1) * N + r] = mx[1][i] + logf(l[1][i]);
-    }
+    for (int e = 0; e < 4 * NGV; ++e) acc[i][e] -= w * pair[(i * 4 * NGV + e) * kThreads + tid];
   }
-  const size_t ob = (size_t)bh * N * a.dv_;
-  store_rows<T, NGV>(static_cast<T*>(a.o) + ob, acc[0], 1.f, row0, N, a.dv_, a.dv_, ty, tx);
-  if (!a.rest) return;
-  constexpr int R = sizeof(T) == 2 ? 2 : 1;
-  T* rest = static_cast<T*>(a.rest) + R * ob;
-  store_rows<T, NGV>(rest, acc[1], 1.f, row0, N, a.dv_, R * a.dv_, ty, tx);
+  store_rows<T, NGV>(static_cast<T*>(a.o) + ob, acc, 1.f, row0, N, a.dv_, a.dv_, ty, tx);
   if constexpr (R == 2) {  // what the rounding of o left off
+    if (!a.rest) return;
 #pragma unroll
     for (int i = 0; i < 4; ++i)
 #pragma unroll
-      for (int e = 0; e < 4 * NGV; ++e) acc[0][i][e] -= to_f32<T>(from_f32<T>(acc[0][i][e]));
-    store_rows<T, NGV>(rest + a.dv_, acc[0], 1.f, row0, N, a.dv_, R * a.dv_, ty, tx);
+      for (int e = 0; e < 4 * NGV; ++e) acc[i][e] -= to_f32<T>(from_f32<T>(acc[i][e]));
+    store_rows<T, NGV>(rest + a.dv_, acc, 1.f, row0, N, a.dv_, R * a.dv_, ty, tx);
   }
 }
 
@@ -632,15 +653,21 @@ cudaError_t run(K1 one, K2 two, int blocks, int heads, size_t fixed, size_t area
 
 template <typename T>
 cudaError_t forward_t(const DiffProblem& p, const DiffTensors& t, LaunchLog& log) {
-  const int ld = ld_of(p.d), ldv = ld_of(p.dv), tiles = kT * (2 * ld + ldv) + kM * kLdp;
-  const int blocks = (p.N + kM - 1) / kM, heads = p.B * p.H;
-  const size_t fixed = (size_t)kM * 2 * ld;
-  const Args a = make_args(p, t);
-  if (p.dv <= 64)
-    return run(diff_fwd<T, 1, 1>, diff_fwd<T, 1, 2>, blocks, heads, fixed,
-               group_floats(tiles, 32 + 16), a, log);
-  return run(diff_fwd<T, 2, 1>, diff_fwd<T, 2, 2>, blocks, heads, fixed,
-             group_floats(tiles, 64 + 16), a, log);
+  const int blocks = (p.N + kM - 1) / kM;
+  const size_t q = (size_t)2 * kM * ld_of(p.d), area = fwd_area(p.d, p.dv);
+  Args a = make_args(p, t);
+  a.heads = p.B * p.H;
+  // With few blocks the longest row's time counts: two pairs of groups share
+  // one.  With more the SMs' throughput does: two blocks of a pair per SM, which
+  // need not add up.  One pair, two: 260 blocks, causal 254, 212 us; 256 blocks
+  // of equal length 204, 209 us.
+  const bool split = (long long)blocks * a.heads <= 2 * kSms &&
+                     (q + 2 * area) * sizeof(float) <= kMaxShared;
+  if (split)
+    return p.dv <= 64 ? launch(diff_fwd<T, 1, 2>, blocks, 4, q + 2 * area, a, log)
+                      : launch(diff_fwd<T, 2, 2>, blocks, 4, q + 2 * area, a, log);
+  return p.dv <= 64 ? launch(diff_fwd<T, 1, 1>, blocks, 2, q + area, a, log)
+                    : launch(diff_fwd<T, 2, 1>, blocks, 2, q + area, a, log);
 }
 
 template <typename T, int NGD, int NGV>
