@@ -164,7 +164,7 @@ def call_on(device, what: str, fn, *args) -> None:
     status code checked.  Kernel launches need the stream's device to be the
     current one."""
     i = device.index
-    if i == torch.cuda.current_device():
+    if i == torch._C._cuda_getDevice():
         code = fn(*args, torch._C._cuda_getCurrentRawStream(i))
     else:
         with torch.cuda.device(device):

@@ -128,6 +128,26 @@ __global__ void __launch_bounds__(256)
   if (i < rows) lam_store(dlam, bf16, i, -d2[i]);
 }
 
+// dlam per head (a block each), or of the one value, in a single launch: for as
+// many rows as a block adds up in a few us
+constexpr long long kOneBlock = 65536;
+__global__ void __launch_bounds__(1024)
+    diff_lam_sums(const float* __restrict__ d2, void* dlam, int bf16, int kind, int B, int H, int N) {
+  __shared__ float sm[32];
+  float s = 0.f;
+  if (kind == FBOB_LAM_HEAD) {
+    for (int b = 0; b < B; ++b) {
+      const float* rows = d2 + ((size_t)b * H + blockIdx.x) * N;
+      for (int i = threadIdx.x; i < N; i += 1024) s += rows[i];
+    }
+  } else {
+    const int rows = B * H * N;
+    for (int i = threadIdx.x; i < rows; i += 1024) s += d2[i];
+  }
+  s = block_sum(s, sm);
+  if (threadIdx.x == 0) lam_store(dlam, bf16, blockIdx.x, -s);
+}
+
 // partial[b, h] = sum over rows of d2: one block per (batch, head)
 __global__ void __launch_bounds__(256)
     diff_head_sums(const float* __restrict__ d2, float* __restrict__ partial, int N) {
@@ -178,6 +198,14 @@ cudaError_t lam_gradient(const DiffProblem& p, const DiffWorkspace& ws, void* dl
     log.mark();
     return e;
   }
+  const bool head = p.lam_kind == FBOB_LAM_HEAD;
+  if ((head ? (long long)p.B * p.N : (long long)p.rows()) <= kOneBlock) {
+    diff_lam_sums<<<head ? p.H : 1, 1024, 0, log.stream>>>(ws.d2, dlam, p.lam_bf16, p.lam_kind, p.B,
+                                                           p.H, p.N);
+    e = cudaGetLastError();
+    log.mark();
+    return e;
+  }
   diff_head_sums<<<p.B * p.H, 256, 0, log.stream>>>(ws.d2, ws.partial, p.N);
   e = cudaGetLastError();
   log.mark();
@@ -189,7 +217,7 @@ cudaError_t lam_gradient(const DiffProblem& p, const DiffWorkspace& ws, void* dl
 }
 
 // Common prologue: validate, pick the path, carve the workspace, reset the
-// status word.
+// status word (in a thread new to the GPU also what makes its context current).
 int prologue(int op, const fbob_diff_shape_t* shape, void* ws_ptr, size_t ws_bytes,
              cudaStream_t stream, DiffProblem* p, int* path, DiffWorkspace* ws) {
   const int st = check_shape(shape, p);

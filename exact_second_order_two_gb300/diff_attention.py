@@ -118,12 +118,16 @@ def diff_forward(q, k, v, lam, causal: bool = False, scale: float | None = None,
     workspace: uint8 tensor of ``fbob_diff_workspace_size`` bytes for one call
     at a time, whose ``status`` can be read afterwards; by default a new one.
     """
-    shp = _shape(q, k, v, lam, causal, scale)
-    o = torch.empty((shp.B, shp.H, shp.N, shp.dv), dtype=q.dtype, device=q.device)
-    rest = torch.empty(_rest_shape(shp), dtype=q.dtype, device=q.device) if need_rest else None
-    lse = torch.empty((shp.B, 2 * shp.H, shp.N), dtype=torch.float32, device=q.device)
-    ws = _workspace(_b.OP_FORWARD, shp, q.device, workspace)
-    _b.call_on(q.device, "fbob_diff_forward", _b.lib().fbob_diff_forward, ctypes.byref(shp),
+    return _forward(_shape(q, k, v, lam, causal, scale), q, k, v, lam, need_rest, workspace)
+
+
+def _forward(shp, q, k, v, lam, need_rest, workspace=None):
+    dev = q.device
+    o = torch.empty((shp.B, shp.H, shp.N, shp.dv), dtype=q.dtype, device=dev)
+    rest = torch.empty(_rest_shape(shp), dtype=q.dtype, device=dev) if need_rest else None
+    lse = torch.empty((shp.B, 2 * shp.H, shp.N), dtype=torch.float32, device=dev)
+    ws = _workspace(_b.OP_FORWARD, shp, dev, workspace)
+    _b.call_on(dev, "fbob_diff_forward", _b.lib().fbob_diff_forward, ctypes.byref(shp),
                q.data_ptr(), k.data_ptr(), v.data_ptr(), lam.data_ptr(), o.data_ptr(),
                None if rest is None else rest.data_ptr(), lse.data_ptr(), ws.data_ptr(), ws.numel())
     return o, rest, lse
@@ -138,11 +142,18 @@ def diff_backward(q, k, v, lam, o, rest, lse, do, causal: bool = False,
     for name, t, shape in (("o", o, rows), ("rest", rest, _rest_shape(shp)), ("do", do, rows)):
         _match(name, t, shape, q.dtype, q.device)
     _match("lse", lse, (shp.B, 2 * shp.H, shp.N), torch.float32, q.device)
-    dq, dk, dv, dlam = (torch.empty_like(t) for t in (q, k, v, lam))
-    ws = _workspace(_b.OP_BACKWARD, shp, q.device, workspace)
-    _b.call_on(q.device, "fbob_diff_backward", _b.lib().fbob_diff_backward, ctypes.byref(shp),
-               *(t.data_ptr() for t in (q, k, v, lam, o, rest, lse, do, dq, dk, dv, dlam, ws)),
-               ws.numel())
+    return _backward(shp, q, k, v, lam, o, rest, lse, do, workspace)
+
+
+def _backward(shp, q, k, v, lam, o, rest, lse, do, workspace=None):
+    dev = q.device
+    dq, dk = torch.empty_like(q), torch.empty_like(k)
+    dv, dlam = torch.empty_like(v), torch.empty_like(lam)
+    ws = _workspace(_b.OP_BACKWARD, shp, dev, workspace)
+    _b.call_on(dev, "fbob_diff_backward", _b.lib().fbob_diff_backward, ctypes.byref(shp),
+               q.data_ptr(), k.data_ptr(), v.data_ptr(), lam.data_ptr(), o.data_ptr(),
+               rest.data_ptr(), lse.data_ptr(), do.data_ptr(), dq.data_ptr(), dk.data_ptr(),
+               dv.data_ptr(), dlam.data_ptr(), ws.data_ptr(), ws.numel())
     return dq, dk, dv, dlam
 
 
@@ -162,11 +173,11 @@ class _DiffBackward(torch.autograd.Function):
     on each map."""
 
     @staticmethod
-    def forward(ctx, q, k, v, lam, do, o, rest, lse, causal, scale):
+    def forward(ctx, q, k, v, lam, do, o, rest, lse, shp):
         do = _contig(do)
-        grads = diff_backward(q, k, v, lam, o, rest, lse, do, causal, scale)
+        grads = _backward(shp, q, k, v, lam, o, rest, lse, do)
         ctx.save_for_backward(q, k, v, lam, do, o, rest, lse)
-        ctx.causal, ctx.scale = causal, scale
+        ctx.causal, ctx.scale = bool(shp.causal), shp.scale
         ctx.set_materialize_grads(False)
         return grads
 
@@ -175,7 +186,7 @@ class _DiffBackward(torch.autograd.Function):
     def backward(ctx, gq, gk, gv, glam):
         q, k, v, lam, do, o, rest, lse = ctx.saved_tensors
         o2 = rest[..., 0, :].contiguous()
-        none = (None,) * 5
+        none = (None,) * 4
         if gq is None and gk is None and gv is None and glam is None:
             return (None,) * 5 + none
         B, H2, N, d = q.shape
@@ -241,10 +252,10 @@ class _DiffBackward(torch.autograd.Function):
 
 class _DiffAttention(torch.autograd.Function):
     @staticmethod
-    def forward(ctx, q, k, v, lam, causal, scale):
-        o, rest, lse = diff_forward(q, k, v, lam, causal, scale)
+    def forward(ctx, q, k, v, lam, shp):
+        o, rest, lse = _forward(shp, q, k, v, lam, True)
         ctx.save_for_backward(q, k, v, lam, o, rest, lse)
-        ctx.causal, ctx.scale = causal, scale
+        ctx.shp = shp
         return o
 
     @staticmethod
@@ -253,10 +264,10 @@ class _DiffAttention(torch.autograd.Function):
         # o, rest and lse enter as values: the second derivative's paths through
         # them are part of what fbob_bob returns
         if torch.is_grad_enabled():
-            grads = _DiffBackward.apply(q, k, v, lam, do, o.detach(), rest, lse, ctx.causal, ctx.scale)
+            grads = _DiffBackward.apply(q, k, v, lam, do, o.detach(), rest, lse, ctx.shp)
         else:
-            grads = diff_backward(q, k, v, lam, o, rest, lse, _contig(do), ctx.causal, ctx.scale)
-        return tuple(grads) + (None, None)
+            grads = _backward(ctx.shp, q, k, v, lam, o, rest, lse, _contig(do))
+        return *grads, None
 
 
 def diff_attention(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, lam: torch.Tensor,
@@ -275,10 +286,9 @@ def diff_attention(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, lam: torch
     if not torch.is_tensor(lam):
         raise TypeError(f"lam must be a tensor, got {type(lam).__name__}")
     q, k, v, lam = _contig(q), _contig(k), _contig(v), _contig(lam)
-    if scale is None:
-        scale = 1.0 / math.sqrt(q.shape[-1])
+    shp = _shape(q, k, v, lam, causal, scale)
     if torch.is_grad_enabled() and (q.requires_grad or k.requires_grad or v.requires_grad
                                     or lam.requires_grad):
-        return _DiffAttention.apply(q, k, v, lam, bool(causal), float(scale))
+        return _DiffAttention.apply(q, k, v, lam, shp)
     # no backward can follow: rest is not written
-    return diff_forward(q, k, v, lam, bool(causal), float(scale), need_rest=False)[0]
+    return _forward(shp, q, k, v, lam, False)[0]

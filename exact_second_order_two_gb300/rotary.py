@@ -72,16 +72,18 @@ def rotary_frequencies(rotary_dim: int, base: float = 10000.0, scaling: str | No
 _pack = struct.Struct("@9if8q").pack
 
 
-def _turn(x, inv_freq, positions, offset, interleaved, magnitude, dtype, inverse, strides):
-    """One fbob_rotary call into a new tensor (dense, or with ``strides``)."""
+def _turn(x, inv_freq, positions, how, strides):
+    """One fbob_rotary call into a new tensor (dense, or with ``strides``);
+    how: offset, interleaved, magnitude, output dtype, inverse."""
     if x.stride(-1) != 1 and x.shape[-1] > 1:
         x = x.contiguous()
-    B, H, N, d = x.shape
+    shape = x.shape
+    offset, interleaved, magnitude, dtype, inverse = how
     if strides is None:
-        y = torch.empty((B, H, N, d), dtype=dtype, device=x.device)
+        y = torch.empty(shape, dtype=dtype, device=x.device)
     else:
-        y = torch.empty_strided((B, H, N, d), strides, dtype=dtype, device=x.device)
-    r = _pack(B, H, N, d, 2 * inv_freq.numel(), interleaved, inverse, _b.DTYPES[x.dtype],
+        y = torch.empty_strided(shape, strides, dtype=dtype, device=x.device)
+    r = _pack(*shape, 2 * inv_freq.shape[0], interleaved, inverse, _b.DTYPES[x.dtype],
               _b.DTYPES[dtype], magnitude, *x.stride()[:3], *y.stride()[:3],
               0 if positions is None else positions.stride(0), offset)
     _b.call_on(x.device, "fbob_rotary", _b.lib().fbob_rotary, r, x.data_ptr(), inv_freq.data_ptr(),
@@ -93,33 +95,20 @@ class _Rotary(torch.autograd.Function):
     """x -> rotary(x); its backward is itself with the angle negated."""
 
     @staticmethod
-    def forward(ctx, x, inv_freq, positions, offset, interleaved, magnitude, dtype, inverse,
-                strides):
+    def forward(ctx, x, inv_freq, positions, how, strides):
         ctx.save_for_backward(inv_freq, positions)
-        ctx.how = (offset, interleaved, magnitude, x.dtype, not inverse)
-        # the gradient takes the input's own layout where that is dense
-        ctx.strides = x.stride() if _dense(x) else None
-        return _turn(x, inv_freq, positions, offset, interleaved, magnitude, dtype, inverse,
-                     strides)
+        ctx.how = (*how[:3], x.dtype, not how[4])
+        # the gradient takes the layout of a dense projection, read as [B, H, N, d]
+        # or as [B, N, H, d], and is dense otherwise
+        ctx.strides = None if x.is_contiguous() or not x.transpose(1, 2).is_contiguous() \
+            else x.stride()
+        return _turn(x, inv_freq, positions, how, strides)
 
     @staticmethod
     def backward(ctx, dy):
         inv_freq, positions = ctx.saved_tensors
         turn = _Rotary.apply if torch.is_grad_enabled() else _turn
-        dx = turn(dy, inv_freq, positions, *ctx.how, ctx.strides)
-        return dx, None, None, None, None, None, None, None, None
-
-
-def _dense(x: torch.Tensor) -> bool:
-    """Whether x fills its memory once, with feature stride 1."""
-    want = 1
-    for size, stride in sorted(zip(x.shape, x.stride()), key=lambda p: p[1]):
-        if size == 1:
-            continue
-        if stride != want:
-            return False
-        want *= size
-    return x.stride(-1) == 1
+        return turn(dy, inv_freq, positions, ctx.how, ctx.strides), None, None, None, None
 
 
 def rotary(x: torch.Tensor, inv_freq: torch.Tensor, positions=None, *, interleaved: bool = False,
@@ -142,9 +131,8 @@ def rotary(x: torch.Tensor, inv_freq: torch.Tensor, positions=None, *, interleav
     if x.dim() != 4:
         raise ValueError("x must be [B, H, N, d]")
     dtype = x.dtype if dtype is None else dtype
-    for t in (x.dtype, dtype):
-        if t not in _b.DTYPES:
-            raise TypeError(f"unsupported dtype {t}; use bfloat16 or float32")
+    if x.dtype not in _b.DTYPES or dtype not in _b.DTYPES:
+        raise TypeError(f"unsupported dtypes {x.dtype}, {dtype}; use bfloat16 or float32")
     if inv_freq.dtype != torch.float64 or inv_freq.dim() != 1 or inv_freq.device != x.device:
         raise ValueError(f"inv_freq must be a float64 vector on {x.device}")
     if inv_freq.requires_grad:
@@ -168,5 +156,5 @@ def rotary(x: torch.Tensor, inv_freq: torch.Tensor, positions=None, *, interleav
         if positions.stride(1) != 1 and N > 1:
             positions = positions.contiguous()
     turn = _Rotary.apply if x.requires_grad and torch.is_grad_enabled() else _turn
-    return turn(x, inv_freq, positions, offset, bool(interleaved), float(magnitude), dtype, False,
-                None)
+    how = (offset, bool(interleaved), float(magnitude), dtype, False)
+    return turn(x, inv_freq, positions, how, None)
