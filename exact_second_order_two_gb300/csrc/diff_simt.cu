@@ -1,5 +1,5 @@
 // CUDA-core kernels of differential attention: fp32 tensors, and bf16 with
-// head sizes the tensor-core kernels do not serve.  Per head, with m = 1, 2,
+// head sizes that are no multiples of 8.  Per head, with m = 1, 2,
 //   S^m = c Q^m K^mT, P^m = softmax(S^m), O = P^1 V - lam P^2 V;
 //   dP = dO V^T, D^m = dO . O^m, dS^1 = P^1*(dP - D^1),
 //   dS^2 = -lam P^2*(dP - D^2), dQ^m = c dS^m K^m, dK^m = c dS^mT Q^m,

@@ -1,5 +1,7 @@
-// Differential attention on the tensor cores (tcgen05 / TMEM / TMA), bf16,
-// d and dv = 64 or 128.  Per head, with m = 1, 2 (code: 0, 1) and c the scale,
+// Differential attention on the tensor cores (tcgen05 / TMEM / TMA), bf16, d and
+// dv multiples of 8 up to 128.  The kernels are built for widths D and DV of 64
+// and 128; narrower rows arrive with zeros behind them (the copies fill in what
+// is past a row's end, and leave it out when they store).  Per head, with m = 1, 2 (code: 0, 1) and c the scale,
 //   S^m = c Q^m K^mT, P^m = softmax(S^m), O = P^1 V - lam P^2 V;
 //   dP = dO V^T, D^m = dO . O^m, dS^1 = P^1*(dP - D^1),
 //   dS^2 = -lam P^2*(dP - D^2), dQ^m = c dS^m K^m, dK^m = c dS^mT Q^m,
@@ -90,6 +92,8 @@ struct Common {
   int H, G;        // query heads, and those per key head
   int units, group;  // CTA grid: heads, heads per group (cta_coord)
   float scale;
+  bool narrow_d, narrow_v;  // d < D, dv < DV (kernels with NARROW: a test of
+                            // these in all cost the others 1%)
   LamArg lam;
 };
 
@@ -151,15 +155,32 @@ __device__ __forceinline__ void bulk_load(void* dst, const void* src, uint32_t b
       : "memory");
 }
 
-// Tiled store shared -> global of the box that load_tile loads: [rows][64]
-// blocks with 128-byte swizzle; rows past N are left as they are.  The caller
-// fences its writes (fence_async_smem) and ends with stores_done.
-__device__ __forceinline__ void store_tile(const CUtensorMap* map, const void* src, int row, int bh) {
+// [rows][W] tile of rows row.. of head bh, as [rows][64] blocks with 128-byte
+// swizzle: one box where the tensor's rows are W wide, else one per block, with
+// zeros past the row's end.  Either way the barrier counts rows x W elements.
+template <int W, int ROWS>
+__device__ __forceinline__ void load_rows(uint8_t* dst, const CUtensorMap* map, uint64_t* bar, int row,
+                                          int bh, bool narrow) {
+  load_tile(dst, map, bar, row, bh);
+  if (W == 128 && narrow) tma_load_4d(dst + ROWS * 128, map, bar, 64, row, 0, bh);
+}
+
+__device__ __forceinline__ void store_box(const CUtensorMap* map, const void* src, int x, int row, int r,
+                                          int bh) {
   asm volatile(
       "cp.async.bulk.tensor.4d.global.shared::cta.tile.bulk_group [%0, {%2, %3, %4, %5}], [%1];" ::"l"(
           reinterpret_cast<uint64_t>(map)),
-      "r"(smem_u32(src)), "r"(0), "r"(row), "r"(0), "r"(bh)
+      "r"(smem_u32(src)), "r"(x), "r"(row), "r"(r), "r"(bh)
       : "memory");
+}
+// The tile of load_rows back: rows past N, and elements past a row's end, are
+// left as they are.  r: third coordinate of a narrow tensor's map.  The caller
+// fences its writes (fence_async_smem) and ends with stores_done.
+template <int W, int ROWS>
+__device__ __forceinline__ void store_rows(const CUtensorMap* map, const uint8_t* src, int row, int bh,
+                                           bool narrow, int r = 0) {
+  store_box(map, src, 0, row, r, bh);
+  if (W == 128 && narrow) store_box(map, src + ROWS * 128, 64, row, r, bh);
 }
 // The stores of this thread have read their shared memory.
 __device__ __forceinline__ void stores_done() {
@@ -225,7 +246,7 @@ struct FwdParams : Common {
   float* lse;
 };
 
-template <int D, int DV>
+template <int D, int DV, bool NARROW>
 __global__ void __launch_bounds__(kFwdThreads, 1)
     diff_fwd_pass(const __grid_constant__ CUtensorMap mQ, const __grid_constant__ CUtensorMap mK,
                   const __grid_constant__ CUtensorMap mV, const __grid_constant__ CUtensorMap mO,
@@ -254,6 +275,7 @@ __global__ void __launch_bounds__(kFwdThreads, 1)
 
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int N = prm.N;
+  const bool nd = NARROW && prm.narrow_d, nv = NARROW && prm.narrow_v;
   const int nblk = (N + C::BM - 1) / C::BM;
   const CtaCoord cc = cta_coord(prm.units, prm.group, nblk);
   const int bh = cc.bh;
@@ -298,8 +320,8 @@ __global__ void __launch_bounds__(kFwdThreads, 1)
   if (warp == kFwdProducer) {
     if (lane == 0) {
       mbar_arrive_expect_tx(q_full, 2 * C::QB);
-      load_tile(smem + C::OFF_Q, &mQ, q_full, i0, 2 * bh);
-      load_tile(smem + C::OFF_Q + C::QB, &mQ, q_full, i0, 2 * bh + 1);
+      load_rows<D, C::BM>(smem + C::OFF_Q, &mQ, q_full, i0, 2 * bh, nd);
+      load_rows<D, C::BM>(smem + C::OFF_Q + C::QB, &mQ, q_full, i0, 2 * bh + 1, nd);
       int k_issued = 0, v_issued = 0;
       for (int t = 0; t < T; ++t) {
         if (!C::ONE) {
@@ -307,7 +329,7 @@ __global__ void __launch_bounds__(kFwdThreads, 1)
             const int u = k_issued, ks = u % C::KS;
             if (u >= C::KS && !wait_bar(k_empty + ks, ((u / C::KS) - 1) & 1, ab, prm.status)) break;
             mbar_arrive_expect_tx(k_full + ks, C::QB);
-            load_tile(smem + k_at(u), &mK, k_full + ks, t * C::BN, 2 * kvh + (u & 1));
+            load_rows<D, C::BN>(smem + k_at(u), &mK, k_full + ks, t * C::BN, 2 * kvh + (u & 1), nd);
           }
           if (k_issued < 2 * t + 2) break;
         }
@@ -315,10 +337,10 @@ __global__ void __launch_bounds__(kFwdThreads, 1)
         if (t >= C::VS && !wait_bar(v_empty + vs, ((t / C::VS) - 1) & 1, ab, prm.status)) break;
         mbar_arrive_expect_tx(v_full + vs, C::VB + (C::ONE ? 2 * C::QB : 0));
         if (C::ONE) {
-          load_tile(smem + k_at(2 * t), &mK, v_full + vs, t * C::BN, 2 * kvh);
-          load_tile(smem + k_at(2 * t + 1), &mK, v_full + vs, t * C::BN, 2 * kvh + 1);
+          load_rows<D, C::BN>(smem + k_at(2 * t), &mK, v_full + vs, t * C::BN, 2 * kvh, nd);
+          load_rows<D, C::BN>(smem + k_at(2 * t + 1), &mK, v_full + vs, t * C::BN, 2 * kvh + 1, nd);
         }
-        load_tile(smem + v_at(t), &mV, v_full + vs, t * C::BN, kvh);
+        load_rows<DV, C::BN>(smem + v_at(t), &mV, v_full + vs, t * C::BN, kvh, nv);
         ++v_issued;
       }
       // every load this thread issued has landed before the CTA exits (after an
@@ -511,8 +533,12 @@ __global__ void __launch_bounds__(kFwdThreads, 1)
     fence_async_smem();
     named_sync<kSoftmax>(1);
     if (threadIdx.x == 0) {
-      store_tile(&mO, smem + C::OFF_K, i0, bh);
-      if (prm.rest) store_tile(&mR, smem + C::OFF_K + C::BM * DV * 2, i0, bh);
+      store_rows<DV, C::BM>(&mO, smem + C::OFF_K, i0, bh, nv);
+      if (prm.rest) {  // one box for both parts where they are DV wide
+        const uint8_t* src = smem + C::OFF_K + C::BM * DV * 2;
+        store_rows<DV, C::BM>(&mR, src, i0, bh, nv);
+        if (nv) store_rows<DV, C::BM>(&mR, src + C::BM * DV * 2, i0, bh, true, 1);
+      }
       stores_done();
     }
     if (in)
@@ -542,13 +568,13 @@ __device__ __forceinline__ float dot8(const uint4& a, const uint4& b, float acc)
   return acc;
 }
 
-// DV/8 lanes per row, 16 bytes of each tensor per lane; a block takes 64 rows
+// DV/8 lanes per row, 16 bytes of each tensor per lane (vecs = dv/8 of them); a block takes 64 rows
 // of one head.  Bound: memory (O, rest and dO read once).
 template <int DV>
 __global__ void __launch_bounds__(256, 4)
     diff_tc_scalars(const uint4* __restrict__ o, const uint4* __restrict__ rest,
                     const uint4* __restrict__ dO, const float* __restrict__ lse, LamArg lam,
-                    float* __restrict__ scal, int H, int N) {
+                    float* __restrict__ scal, int H, int N, int vecs) {
   constexpr int L = DV / 8, ROWS = 256 / L, STEPS = 64 / ROWS;
   __shared__ float dots[2][64];
   const int nb = (N + 63) / 64;
@@ -567,11 +593,11 @@ __global__ void __launch_bounds__(256, 4)
   for (int i = 0; i < STEPS; ++i) {
     const int r = i * ROWS + sub;
     s1[i] = s2[i] = 0.f;
-    if (n0 + r < N) {
+    if (n0 + r < N && c < vecs) {
       const size_t row = (size_t)bh * N + n0 + r;
-      const uint4 g = dO[row * L + c];
-      s1[i] = dot8(o[row * L + c], g, dot8(rest[(2 * row + 1) * L + c], g, 0.f));
-      s2[i] = dot8(rest[2 * row * L + c], g, 0.f);
+      const uint4 g = dO[row * vecs + c];
+      s1[i] = dot8(o[row * vecs + c], g, dot8(rest[(2 * row + 1) * vecs + c], g, 0.f));
+      s2[i] = dot8(rest[2 * row * vecs + c], g, 0.f);
     }
   }
 #pragma unroll
@@ -632,7 +658,7 @@ struct RowParams : Common {
   float* d2;          // [B, H, N]: sum_j P^2_ij dP_ij
 };
 
-template <int D, int DV>
+template <int D, int DV, bool NARROW>
 __global__ void __launch_bounds__(kThreads, 1)
     diff_row_pass(const __grid_constant__ CUtensorMap mQ, const __grid_constant__ CUtensorMap mK,
                   const __grid_constant__ CUtensorMap mV, const __grid_constant__ CUtensorMap mDO,
@@ -660,6 +686,7 @@ __global__ void __launch_bounds__(kThreads, 1)
 
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int N = prm.N;
+  const bool nd = NARROW && prm.narrow_d, nv = NARROW && prm.narrow_v;
   const int nblk = (N + C::BM - 1) / C::BM;
   const CtaCoord cc = cta_coord(prm.units, prm.group, nblk);
   const int bh = cc.bh;
@@ -698,9 +725,9 @@ __global__ void __launch_bounds__(kThreads, 1)
   if (warp == kProducerWarp) {
     if (lane == 0) {
       mbar_arrive_expect_tx(q_full, 2 * C::QB + C::OB);
-      load_tile(smem + C::OFF_DO, &mDO, q_full, i0, bh);
-      load_tile(smem + C::OFF_Q, &mQ, q_full, i0, 2 * bh);
-      load_tile(smem + C::OFF_Q + C::QB, &mQ, q_full, i0, 2 * bh + 1);
+      load_rows<DV, C::BM>(smem + C::OFF_DO, &mDO, q_full, i0, bh, nv);
+      load_rows<D, C::BM>(smem + C::OFF_Q, &mQ, q_full, i0, 2 * bh, nd);
+      load_rows<D, C::BM>(smem + C::OFF_Q + C::QB, &mQ, q_full, i0, 2 * bh + 1, nd);
       int issued = 0;
       for (int t = 0; t < T; ++t) {
         const int ks = t % C::KS, vs = t % C::VS;
@@ -708,9 +735,9 @@ __global__ void __launch_bounds__(kThreads, 1)
         if (t >= C::KS && !wait_bar(k_empty + ks, ((t / C::KS) - 1) & 1, ab, prm.status)) break;
         uint8_t* dst = smem + C::OFF_K + ks * 2 * C::KB;
         mbar_arrive_expect_tx(full + ks, 2 * C::KB + C::VB);
-        load_tile(smem + C::OFF_V + vs * C::VB, &mV, full + ks, t * C::BN, kvh);
-        load_tile(dst, &mK, full + ks, t * C::BN, 2 * kvh);
-        load_tile(dst + C::KB, &mK, full + ks, t * C::BN, 2 * kvh + 1);
+        load_rows<DV, C::BN>(smem + C::OFF_V + vs * C::VB, &mV, full + ks, t * C::BN, kvh, nv);
+        load_rows<D, C::BN>(dst, &mK, full + ks, t * C::BN, 2 * kvh, nd);
+        load_rows<D, C::BN>(dst + C::KB, &mK, full + ks, t * C::BN, 2 * kvh + 1, nd);
         ++issued;
       }
       mbar_wait_bounded(q_full, 0, prm.status, kDrainNs);
@@ -859,8 +886,8 @@ __global__ void __launch_bounds__(kThreads, 1)
     fence_async_smem();
     named_sync<kConsumers>(1);
     if (threadIdx.x == 0) {
-      store_tile(&mDQ, smem + C::OFF_K, i0, 2 * bh);
-      store_tile(&mDQ, smem + C::OFF_K + C::QB, i0, 2 * bh + 1);
+      store_rows<D, C::BM>(&mDQ, smem + C::OFF_K, i0, 2 * bh, nd);
+      store_rows<D, C::BM>(&mDQ, smem + C::OFF_K + C::QB, i0, 2 * bh + 1, nd);
       stores_done();
     }
     if (slice == 0 && in) {
@@ -918,7 +945,7 @@ struct ColParams : Common {
 
 // PARTS: gridDim.y CTAs share a key block (the branches of one kernel for both
 // cost the whole blocks 1%)
-template <int D, int DV, bool PARTS>
+template <int D, int DV, bool NARROW, bool PARTS>
 __global__ void __launch_bounds__(kThreads, 1)
     diff_col_pass(const __grid_constant__ CUtensorMap mK, const __grid_constant__ CUtensorMap mV,
                   const __grid_constant__ CUtensorMap mQ, const __grid_constant__ CUtensorMap mDO,
@@ -946,6 +973,7 @@ __global__ void __launch_bounds__(kThreads, 1)
 
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int N = prm.N;
+  const bool nd = NARROW && prm.narrow_d, nv = NARROW && prm.narrow_v;
   const CtaCoord cc = cta_coord(prm.units, prm.group, (N + C::BM - 1) / C::BM);
   const int kvh = cc.bh, Hk = prm.H / prm.G;
   const int bh0 = (kvh / Hk) * prm.H + (kvh % Hk) * prm.G;  // first query head
@@ -993,9 +1021,9 @@ __global__ void __launch_bounds__(kThreads, 1)
   if (warp == kProducerWarp) {
     if (lane == 0) {
       mbar_arrive_expect_tx(kv_full, 2 * C::KB + C::VB);
-      load_tile(smem + C::OFF_V, &mV, kv_full, j0, kvh);
-      load_tile(smem + C::OFF_K, &mK, kv_full, j0, 2 * kvh);
-      load_tile(smem + C::OFF_K + C::KB, &mK, kv_full, j0, 2 * kvh + 1);
+      load_rows<DV, C::BM>(smem + C::OFF_V, &mV, kv_full, j0, kvh, nv);
+      load_rows<D, C::BM>(smem + C::OFF_K, &mK, kv_full, j0, 2 * kvh, nd);
+      load_rows<D, C::BM>(smem + C::OFF_K + C::KB, &mK, kv_full, j0, 2 * kvh + 1, nd);
     }
     if (lane == 0) {
       int g = PARTS ? a0 / Tq : 0, t = PARTS ? a0 % Tq : 0, issued = 0;  // tile t within head g
@@ -1004,9 +1032,9 @@ __global__ void __launch_bounds__(kThreads, 1)
         if (a >= C::ST && !wait_bar(empty + st, ((a / C::ST) - 1) & 1, ab, prm.status)) break;
         uint8_t* dst = smem + C::OFF_T + st * C::STB;
         mbar_arrive_expect_tx(full + st, C::STB + C::SCB);
-        load_tile(dst, &mQ, full + st, q0, 2 * bh);
-        load_tile(dst + C::QB, &mQ, full + st, q0, 2 * bh + 1);
-        load_tile(dst + 2 * C::QB, &mDO, full + st, q0, bh);
+        load_rows<D, C::BN>(dst, &mQ, full + st, q0, 2 * bh, nd);
+        load_rows<D, C::BN>(dst + C::QB, &mQ, full + st, q0, 2 * bh + 1, nd);
+        load_rows<DV, C::BN>(dst + 2 * C::QB, &mDO, full + st, q0, bh, nv);
         bulk_load(smem + C::OFF_SC + st * C::SCB, prm.scal + scal_offset(bh, N, q0), C::SCB, full + st);
         ++issued;
         if (++t == Tq) {
@@ -1225,9 +1253,9 @@ __global__ void __launch_bounds__(kThreads, 1)
     fence_async_smem();
     named_sync<kConsumers>(1);
     if (!PARTS && threadIdx.x == 0) {
-      store_tile(&mDK, smem + C::OFF_T, j0, 2 * kvh);
-      store_tile(&mDK, smem + C::OFF_T + C::KB, j0, 2 * kvh + 1);
-      store_tile(&mDV, smem + C::OFF_T + 2 * C::KB, j0, kvh);
+      store_rows<D, C::BM>(&mDK, smem + C::OFF_T, j0, 2 * kvh, nd);
+      store_rows<D, C::BM>(&mDK, smem + C::OFF_T + C::KB, j0, 2 * kvh + 1, nd);
+      store_rows<DV, C::BM>(&mDV, smem + C::OFF_T + 2 * C::KB, j0, kvh, nv);
       stores_done();
     }
   }
@@ -1244,7 +1272,7 @@ __global__ void __launch_bounds__(kThreads, 1)
 template <int D, int DV>
 __global__ void __launch_bounds__(256)
     diff_col_join(const float4* __restrict__ parts, uint2* __restrict__ dk, uint2* __restrict__ dv,
-                  int split, int N, size_t rows, float scale) {
+                  int split, int N, size_t rows, int d, int dv_, float scale) {
   constexpr int W = (2 * D + DV) / 4;
   const size_t e = (size_t)blockIdx.x * 256 + threadIdx.x;
   if (e >= rows * W) return;
@@ -1259,11 +1287,13 @@ __global__ void __launch_bounds__(256)
   const size_t row = e / W, kvh = row / N, j = row - kvh * N;
   const int f = (int)(e - row * W);
   if (f < 2 * D / 4) {
-    const int m = f / (D / 4);
-    dk[((2 * kvh + m) * N + j) * (D / 4) + f % (D / 4)] =
-        make_uint2(pack_bf16(x.x * scale, x.y * scale), pack_bf16(x.z * scale, x.w * scale));
+    const int m = f / (D / 4), c = f % (D / 4);
+    if (4 * c < d)
+      dk[((2 * kvh + m) * N + j) * (d / 4) + c] =
+          make_uint2(pack_bf16(x.x * scale, x.y * scale), pack_bf16(x.z * scale, x.w * scale));
   } else {
-    dv[row * (DV / 4) + f - 2 * D / 4] = make_uint2(pack_bf16(x.x, x.y), pack_bf16(x.z, x.w));
+    const int c = f - 2 * D / 4;
+    if (4 * c < dv_) dv[row * (dv_ / 4) + c] = make_uint2(pack_bf16(x.x, x.y), pack_bf16(x.z, x.w));
   }
 }
 
@@ -1284,6 +1314,9 @@ int col_parts(const DiffProblem& p) {
   return tiles < 3 * kTiles ? 1 : (int)max(1ll, min(kSms / blocks, tiles / kTiles));
 }
 
+// The kernels' width for rows of `width`
+int built(int width) { return width <= 64 ? 64 : 128; }
+
 Common common(const DiffProblem& p, const DiffTensors& t, const DiffWorkspace& ws, int units) {
   Common c{};
   c.status = ws.status;
@@ -1295,18 +1328,33 @@ Common common(const DiffProblem& p, const DiffTensors& t, const DiffWorkspace& w
   c.units = units;
   c.group = cta_group_heads(units, (p.N + 127) / 128, sm_count());
   c.scale = p.scale;
+  c.narrow_d = p.d != built(p.d);
+  c.narrow_v = p.dv != built(p.dv);
   c.lam = t.lam;
   return c;
 }
 
-// [B, heads, N, width] as tiles of `rows` rows
-bool tiles(CUtensorMap* m, const void* ptr, const DiffProblem& p, int heads, int width, int rows) {
-  Problem q{};
-  q.B = p.B;
-  q.H = heads;
-  q.N = p.N;
-  q.d = width;
-  return make_map(m, ptr, q, rows);
+// [B, heads, N, parts, width] as boxes of `rows` rows: all 64-feature blocks of a
+// row where it is as wide as the kernel (of all parts, then), else one block
+bool tiles(CUtensorMap* m, const void* ptr, const DiffProblem& p, int heads, int width, int rows,
+           int parts = 1) {
+  if (width == built(width)) {
+    Problem q{};
+    q.B = p.B;
+    q.H = heads;
+    q.N = p.N;
+    q.d = parts * width;
+    return make_map(m, ptr, q, rows);
+  }
+  auto fn = encode_fn();
+  if (!fn) return false;
+  const cuuint64_t w = width, n = p.N, r = parts;
+  const cuuint64_t dims[4] = {w, n, r, (cuuint64_t)p.B * heads};
+  const cuuint64_t strides[3] = {r * w * 2, w * 2, n * r * w * 2};
+  const cuuint32_t box[4] = {64, (cuuint32_t)rows, 1, 1}, es[4] = {1, 1, 1, 1};
+  return fn(m, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 4, const_cast<void*>(ptr), dims, strides, box, es,
+            CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
+            CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
 template <typename K, typename P, typename... M>
@@ -1324,16 +1372,16 @@ template <int D, int DV>
 cudaError_t forward_d(const DiffProblem& p, const DiffTensors& t, const DiffWorkspace& ws,
                       LaunchLog& log) {
   CUtensorMap mQ, mK, mV, mO, mR;  // without rest mR is a placeholder
-  if (!tiles(&mQ, t.q, p, 2 * p.H, D, 128) || !tiles(&mK, t.k, p, 2 * p.Hk, D, 128) ||
-      !tiles(&mV, t.v, p, p.Hk, DV, 128) || !tiles(&mO, t.o, p, p.H, DV, 128) ||
-      !tiles(&mR, t.rest ? t.rest : t.o, p, p.H, t.rest ? 2 * DV : DV, 128))
+  if (!tiles(&mQ, t.q, p, 2 * p.H, p.d, 128) || !tiles(&mK, t.k, p, 2 * p.Hk, p.d, 128) ||
+      !tiles(&mV, t.v, p, p.Hk, p.dv, 128) || !tiles(&mO, t.o, p, p.H, p.dv, 128) ||
+      !tiles(&mR, t.rest ? t.rest : t.o, p, p.H, p.dv, 128, t.rest ? 2 : 1))
     return cudaErrorInvalidValue;
   FwdParams f;
   static_cast<Common&>(f) = common(p, t, ws, p.B * p.H);
   f.rest = t.rest != nullptr;
   f.lse = t.lse;
-  return run(diff_fwd_pass<D, DV>, f.units, 1, p.N, kFwdThreads, Fwd<D, DV>::SMEM, log, f, mQ, mK, mV,
-             mO, mR);
+  const auto kernel = f.narrow_d || f.narrow_v ? diff_fwd_pass<D, DV, true> : diff_fwd_pass<D, DV, false>;
+  return run(kernel, f.units, 1, p.N, kFwdThreads, Fwd<D, DV>::SMEM, log, f, mQ, mK, mV, mO, mR);
 }
 
 template <int D, int DV>
@@ -1343,17 +1391,17 @@ cudaError_t backward_d(const DiffProblem& p, const DiffTensors& t, const DiffWor
   using Cl = Col<D, DV>;
   // r: the row pass's, c: the column pass's
   CUtensorMap rQ, rK, rV, rDO, rDQ, cK, cV, cQ, cDO, cDK, cDV;
-  if (!tiles(&rQ, t.q, p, 2 * p.H, D, Rw::BM) || !tiles(&rK, t.k, p, 2 * p.Hk, D, Rw::BN) ||
-      !tiles(&rV, t.v, p, p.Hk, DV, Rw::BN) || !tiles(&rDO, t.dO, p, p.H, DV, Rw::BM) ||
-      !tiles(&rDQ, t.dq, p, 2 * p.H, D, Rw::BM) || !tiles(&cK, t.k, p, 2 * p.Hk, D, Cl::BM) ||
-      !tiles(&cV, t.v, p, p.Hk, DV, Cl::BM) || !tiles(&cQ, t.q, p, 2 * p.H, D, Cl::BN) ||
-      !tiles(&cDO, t.dO, p, p.H, DV, Cl::BN) || !tiles(&cDK, t.dk, p, 2 * p.Hk, D, Cl::BM) ||
-      !tiles(&cDV, t.dv, p, p.Hk, DV, Cl::BM))
+  if (!tiles(&rQ, t.q, p, 2 * p.H, p.d, Rw::BM) || !tiles(&rK, t.k, p, 2 * p.Hk, p.d, Rw::BN) ||
+      !tiles(&rV, t.v, p, p.Hk, p.dv, Rw::BN) || !tiles(&rDO, t.dO, p, p.H, p.dv, Rw::BM) ||
+      !tiles(&rDQ, t.dq, p, 2 * p.H, p.d, Rw::BM) || !tiles(&cK, t.k, p, 2 * p.Hk, p.d, Cl::BM) ||
+      !tiles(&cV, t.v, p, p.Hk, p.dv, Cl::BM) || !tiles(&cQ, t.q, p, 2 * p.H, p.d, Cl::BN) ||
+      !tiles(&cDO, t.dO, p, p.H, p.dv, Cl::BN) || !tiles(&cDK, t.dk, p, 2 * p.Hk, p.d, Cl::BM) ||
+      !tiles(&cDV, t.dv, p, p.Hk, p.dv, Cl::BM))
     return cudaErrorInvalidValue;
   const int blocks = (p.N + 63) / 64 * p.B * p.H;
   diff_tc_scalars<DV><<<blocks, 256, 0, log.stream>>>(
       static_cast<const uint4*>(t.o), static_cast<const uint4*>(t.rest),
-      static_cast<const uint4*>(t.dO), t.lse, t.lam, ws.scal, p.H, p.N);
+      static_cast<const uint4*>(t.dO), t.lse, t.lam, ws.scal, p.H, p.N, p.dv / 8);
   cudaError_t e = cudaGetLastError();
   log.mark();
   if (e != cudaSuccess) return e;
@@ -1361,7 +1409,8 @@ cudaError_t backward_d(const DiffProblem& p, const DiffTensors& t, const DiffWor
   static_cast<Common&>(r) = common(p, t, ws, p.B * p.H);
   r.scal = ws.scal;
   r.d2 = ws.d2;
-  e = run(diff_row_pass<D, DV>, r.units, 1, p.N, kThreads, Rw::SMEM, log, r, rQ, rK, rV, rDO, rDQ);
+  const bool narrow = r.narrow_d || r.narrow_v;
+  e = run(narrow ? diff_row_pass<D, DV, true> : diff_row_pass<D, DV, false>, r.units, 1, p.N, kThreads, Rw::SMEM, log, r, rQ, rK, rV, rDO, rDQ);
   if (e != cudaSuccess) return e;
   ColParams c;
   static_cast<Common&>(c) = common(p, t, ws, p.B * p.Hk);
@@ -1369,15 +1418,15 @@ cudaError_t backward_d(const DiffProblem& p, const DiffTensors& t, const DiffWor
   c.parts = ws.parts;
   const int parts = col_parts(p);
   if (parts == 1)
-    return run(diff_col_pass<D, DV, false>, c.units, 1, p.N, kThreads, Cl::SMEM, log, c, cK, cV, cQ,
-               cDO, cDK, cDV);
-  e = run(diff_col_pass<D, DV, true>, c.units, parts, p.N, kThreads, Cl::SMEM, log, c, cK, cV, cQ,
+    return run(narrow ? diff_col_pass<D, DV, true, false> : diff_col_pass<D, DV, false, false>, c.units,
+               1, p.N, kThreads, Cl::SMEM, log, c, cK, cV, cQ, cDO, cDK, cDV);
+  e = run(narrow ? diff_col_pass<D, DV, true, true> : diff_col_pass<D, DV, false, true>, c.units, parts, p.N, kThreads, Cl::SMEM, log, c, cK, cV, cQ,
           cDO, cDK, cDV);
   if (e != cudaSuccess) return e;
   const size_t rows = (size_t)c.units * p.N, quads = rows * ((2 * D + DV) / 4);
   diff_col_join<D, DV><<<(unsigned)((quads + 255) / 256), 256, 0, log.stream>>>(
       reinterpret_cast<const float4*>(ws.parts), static_cast<uint2*>(t.dk),
-      static_cast<uint2*>(t.dv), parts, p.N, rows, p.scale);
+      static_cast<uint2*>(t.dv), parts, p.N, rows, p.d, p.dv, p.scale);
   e = cudaGetLastError();
   log.mark();
   return e;
@@ -1391,25 +1440,25 @@ size_t diff_tc_scalar_count(const DiffProblem& p) {
 
 size_t diff_tc_part_count(const DiffProblem& p) {
   const int parts = col_parts(p);
-  return parts == 1 ? 0 : (size_t)parts * p.B * p.Hk * p.N * (2 * p.d + p.dv);
+  return parts == 1 ? 0 : (size_t)parts * p.B * p.Hk * p.N * (2 * built(p.d) + built(p.dv));
 }
 
 bool diff_tc_supported(const DiffProblem& p) {
-  return p.bf16 && (p.d == 64 || p.d == 128) && (p.dv == 64 || p.dv == 128);
+  return p.bf16 && p.d % 8 == 0 && p.dv % 8 == 0 && p.d <= 128 && p.dv <= 128;
 }
 
 cudaError_t diff_tc_forward(const DiffProblem& p, const DiffTensors& t, const DiffWorkspace& ws,
                             LaunchLog& log) {
-  if (p.d == 64)
-    return p.dv == 128 ? forward_d<64, 128>(p, t, ws, log) : forward_d<64, 64>(p, t, ws, log);
-  return p.dv == 128 ? forward_d<128, 128>(p, t, ws, log) : forward_d<128, 64>(p, t, ws, log);
+  if (p.d <= 64)
+    return p.dv <= 64 ? forward_d<64, 64>(p, t, ws, log) : forward_d<64, 128>(p, t, ws, log);
+  return p.dv <= 64 ? forward_d<128, 64>(p, t, ws, log) : forward_d<128, 128>(p, t, ws, log);
 }
 
 cudaError_t diff_tc_backward(const DiffProblem& p, const DiffTensors& t, const DiffWorkspace& ws,
                              LaunchLog& log) {
-  if (p.d == 64)
-    return p.dv == 128 ? backward_d<64, 128>(p, t, ws, log) : backward_d<64, 64>(p, t, ws, log);
-  return p.dv == 128 ? backward_d<128, 128>(p, t, ws, log) : backward_d<128, 64>(p, t, ws, log);
+  if (p.d <= 64)
+    return p.dv <= 64 ? backward_d<64, 64>(p, t, ws, log) : backward_d<64, 128>(p, t, ws, log);
+  return p.dv <= 64 ? backward_d<128, 64>(p, t, ws, log) : backward_d<128, 128>(p, t, ws, log);
 }
 
 }  // namespace fbob

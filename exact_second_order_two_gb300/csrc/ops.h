@@ -57,7 +57,7 @@ cudaError_t diff_simt_forward(const DiffProblem& p, const DiffTensors& t, Launch
 cudaError_t diff_simt_backward(const DiffProblem& p, const DiffTensors& t, const DiffWorkspace& ws,
                                LaunchLog& log);
 
-// ---- tensor-core kernels: bf16, d and dv = 64 or 128 ------------------------
+// ---- tensor-core kernels: bf16, d and dv multiples of 8 ---------------------
 bool diff_tc_supported(const DiffProblem& p);
 size_t diff_tc_scalar_count(const DiffProblem& p);  // fp32 values of DiffWorkspace::scal
 size_t diff_tc_part_count(const DiffProblem& p);    // fp32 values of DiffWorkspace::parts

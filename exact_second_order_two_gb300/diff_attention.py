@@ -108,7 +108,8 @@ def diff_forward(q, k, v, lam, causal: bool = False, scale: float | None = None,
 
     q: [B, 2H, N, d], the two queries of head h as heads 2h and 2h + 1;
     k: [B, 2Hk, N, d] likewise; v: [B, Hk, N, dv], with H a multiple of Hk
-    (query head h reads key head h // (H / Hk)); bf16 or fp32, contiguous.
+    (query head h reads key head h // (H / Hk)); bf16 or fp32, contiguous, d and
+    dv up to 128 (bf16 multiples of 8 run on the tensor cores).
     lam: no dimensions, [H] or [B, H, N], bf16 or fp32.  scale > 0 defaults to
     1/sqrt(d); with ``causal`` key j is visible to query i iff j <= i.  A key
     whose score is -inf has no weight; but as in the dense product, an infinite

@@ -259,8 +259,8 @@ int fbob_rotary(const fbob_rotary_t* r, const void* x, const double* inv_freq,
  * multiple of Hk: query head h reads key head h / (H / Hk).  lam is one value,
  * [H], or [B,H,N], bf16 or fp32.  Masking, ownership, asynchrony and alignment
  * as above (lam to its own size); scale > 0.  1 <= d, dv <= 128,
- * B*H <= 32767.  bf16 at d and dv of 64 or 128 runs the tensor-core kernels,
- * the rest runs on CUDA cores (fbob_diff_path).
+ * B*H <= 32767.  bf16 at d and dv that are multiples of 8 runs the
+ * tensor-core kernels, the rest runs on CUDA cores (fbob_diff_path).
  * Every output is summed in a fixed order: equal inputs give equal bits. */
 typedef enum { FBOB_LAM_ONE = 0, FBOB_LAM_HEAD = 1, FBOB_LAM_ROW = 2 } fbob_lam_t;
 

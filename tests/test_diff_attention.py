@@ -148,6 +148,16 @@ CASES = [
     (1, 2, 2, 641, 128, 128, BF, True, ("row", BF)),
     (1, 2, 1, 640, 128, 64, BF, False, ("one", F32)),
     (1, 2, 2, 90, 96, 128, BF, True, ("head", BF)),
+    # rows narrower than the kernels' widths, on one and on both sides, cut and whole
+    (2, 2, 1, 300, 40, 40, BF, True, ("row", BF)),
+    (1, 4, 2, 200, 24, 128, BF, False, ("head", F32)),
+    (1, 2, 2, 257, 8, 8, BF, True, ("one", BF)),
+    (1, 8, 2, 500, 128, 72, BF, True, ("head", BF)),
+    (1, 1, 1, 130, 104, 120, BF, False, ("row", F32)),
+    (1, 4, 1, 420, 80, 56, BF, True, ("head", BF)),
+    # and sizes that run on CUDA cores
+    (1, 2, 1, 90, 60, 100, BF, True, ("head", BF)),
+    (1, 2, 2, 33, 7, 33, BF, False, ("one", F32)),
     (1, 1, 1, 1, 64, 64, F32, True, ("one", F32)),
     (2, 2, 1, 65, 64, 128, F32, True, ("head", F32)),
     (1, 2, 2, 200, 32, 64, F32, False, ("row", F32)),
@@ -235,7 +245,7 @@ class TestOnGpu:
             assert all(torch.equal(a, b) for a, b in zip(first, r))
 
     @pytest.mark.parametrize("dtype,d,dv", [(BF, 64, 128), (BF, 64, 64), (BF, 128, 128), (BF, 128, 64),
-                                            (F32, 64, 64)])
+                                            (BF, 40, 72), (BF, 104, 24), (BF, 20, 12), (F32, 64, 64)])
     def test_outputs_fully_written_and_guards_intact(self, dtype, d, dv):
         """NaN-filled outputs and workspace with guards behind them, through the
         C calls: everything inside is written, nothing outside."""
@@ -589,9 +599,9 @@ def test_kernel_family_choice():
     for op in (0, 1):
         def path(**kw):
             return lib.fbob_diff_path(op, ctypes.byref(shape(**kw)))
-        for kw in (dict(), dict(dv=64), dict(d=128), dict(d=128, dv=64)):
+        for kw in (dict(), dict(dv=64), dict(d=128), dict(d=128, dv=64), dict(d=96), dict(d=8, dv=40)):
             assert path(**kw) == fbob.PATH_TCGEN05, kw
-        for kw in (dict(dtype=1), dict(d=96), dict(d=32), dict(dv=96), dict(dv=32)):
+        for kw in (dict(dtype=1), dict(d=60), dict(dv=97), dict(d=1, dv=4)):
             assert path(**kw) == fbob.PATH_SIMT, kw
         old = fbob.force_path(fbob.PATH_SIMT)
         try:
