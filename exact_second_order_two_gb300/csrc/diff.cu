@@ -58,8 +58,7 @@ int choose_path(const DiffProblem& p) {
 }
 
 // [status 256 B][D: B*2H*N fp32, or the tensor cores' row scalars][d2: B*H*N
-// fp32][partial: B*H fp32][the tensor cores' partial dK and dV], each region
-// aligned
+// fp32][partial: B*H fp32][parts of dK and dV], each region aligned
 size_t carve(int op, const DiffProblem& p, int path, char* base, DiffWorkspace* ws) {
   size_t off = kAlign;
   if (ws) ws->status = reinterpret_cast<int*>(base);
@@ -70,10 +69,9 @@ size_t carve(int op, const DiffProblem& p, int path, char* base, DiffWorkspace* 
     off += align_up(p.rows() * sizeof(float));
     if (ws) ws->partial = reinterpret_cast<float*>(base + off);
     off += align_up((size_t)p.B * p.H * sizeof(float));
-    if (path == FBOB_PATH_TCGEN05) {
-      if (ws) ws->parts = reinterpret_cast<float*>(base + off);
-      off += align_up(diff_tc_part_count(p) * sizeof(float));
-    }
+    if (ws) ws->parts = reinterpret_cast<float*>(base + off);
+    off += align_up((path == FBOB_PATH_TCGEN05 ? diff_tc_part_count(p) : diff_simt_part_count(p)) *
+                    sizeof(float));
   }
   return off;
 }

@@ -57,6 +57,7 @@ struct Args {
   float* lse;
   const float* D;
   float* d2;
+  float* parts;  // [gridDim.y][heads][N][2 d + dv]: partial dK^1, dK^2, dV
   LamArg lam;
   int H, G, N, d, dv_, causal;
   int heads;  // of the grid: B H, or B Hk
@@ -498,7 +499,8 @@ __global__ void __launch_bounds__(SPLIT * kThreads) diff_bwd_row(Args a) {
                        a.d, a.d, ty, tx);
 }
 
-// ---- dK, dV: one block per 32 keys of a key head, over its query heads ------
+// ---- dK, dV: one block per 32 keys of a key head, over its query heads, or over
+// one of gridDim.y parts of their tiles ---------------------------------------
 template <typename T, int NGD, int NGV, int SPLIT>
 __global__ void __launch_bounds__(SPLIT * kThreads) diff_bwd_col(Args a) {
   extern __shared__ __align__(16) float sm[];
@@ -536,12 +538,19 @@ __global__ void __launch_bounds__(SPLIT * kThreads) diff_bwd_col(Args a) {
 #pragma unroll
     for (int e = 0; e < 4 * NGV; ++e) av[i][e] = 0.f;
   }
-  for (int g = 0; g < a.G; ++g) {
+  const int start = a.causal ? col0 / kT * kT : 0, per_head = (N - start + kT - 1) / kT;
+  const int split = gridDim.y, part = blockIdx.y;
+  const int t0 = (int)((long long)per_head * a.G * part / split);
+  const int t1 = (int)((long long)per_head * a.G * (part + 1) / split);
+  for (int g = t0 / per_head; g * per_head < t1; ++g) {
     const int h = (kvh % Hk) * a.G + g;
     const size_t bh = (size_t)b * a.H + h;
     const T* q = static_cast<const T*>(a.q) + bh * 2 * qsz;
     const T* dO = static_cast<const T*>(a.dO) + bh * N * a.dv_;
-    for (int i0 = (a.causal ? col0 / kT * kT : 0) + grp * kT; i0 < N; i0 += SPLIT * kT) {
+    // the part's rows of this head
+    const int first = start + max(t0 - g * per_head, 0) * kT;
+    const int end = min(N, start + (t1 - g * per_head) * kT);
+    for (int i0 = first + grp * kT; i0 < end; i0 += SPLIT * kT) {
       group_sync<SPLIT>(grp);
       load_rows<kT>(tid, qs, ld, q, i0, N, a.d);
       load_rows<kT>(tid, qs + kT * ld, ld, q + qsz, i0, N, a.d);
@@ -609,12 +618,48 @@ __global__ void __launch_bounds__(SPLIT * kThreads) diff_bwd_col(Args a) {
         av[i][e] += other[(32 * NGD + i * 4 * NGV + e) * kThreads + tid];
     }
   }
+  if (split > 1) {
+    const int W = 2 * a.d + a.dv_;
+    float* dst = a.parts + ((size_t)part * a.heads + kvh) * N * W;
+    store_rows<float, NGD>(dst, ak[0], 1.f, col0, N, a.d, W, ty, tx);
+    store_rows<float, NGD>(dst + a.d, ak[1], 1.f, col0, N, a.d, W, ty, tx);
+    store_rows<float, NGV>(dst + 2 * a.d, av, 1.f, col0, N, a.dv_, W, ty, tx);
+    return;
+  }
 #pragma unroll
   for (int m = 0; m < 2; ++m)
     store_rows<T, NGD>(static_cast<T*>(a.dk) + ((size_t)kvh * 2 + m) * qsz, ak[m], a.scale, col0, N,
                        a.d, a.d, ty, tx);
   store_rows<T, NGV>(static_cast<T*>(a.dv) + (size_t)kvh * N * a.dv_, av, 1.f, col0, N, a.dv_, a.dv_,
                      ty, tx);
+}
+
+// dK (scaled) and dV from the parts, added in their order: a thread per element.
+template <typename T>
+__global__ void __launch_bounds__(256) diff_join(Args a, int split) {
+  const size_t W = 2 * a.d + a.dv_, total = (size_t)a.heads * a.N * W;
+  const size_t e = (size_t)blockIdx.x * 256 + threadIdx.x;
+  if (e >= total) return;
+  float x = a.parts[e];
+  for (int s = 1; s < split; ++s) x += a.parts[s * total + e];
+  const size_t row = e / W, kvh = row / a.N, j = row - kvh * a.N;
+  const int f = (int)(e - row * W);
+  if (f < 2 * a.d) {
+    const int m = f / a.d;
+    static_cast<T*>(a.dk)[((2 * kvh + m) * a.N + j) * a.d + f - m * a.d] = from_f32<T>(x * a.scale);
+  } else {
+    static_cast<T*>(a.dv)[row * a.dv_ + f - 2 * a.d] = from_f32<T>(x);
+  }
+}
+
+// Parts of the dK/dV pass, where its blocks are fewer than the SMs: as many as
+// leave each 4 or more tiles.  Whole and cut, fp32: 2 x 4 heads on one key head x
+// 796, d = 40, dv = 128 489, 176 + 4 us; 1 x 4 on one x 1500, d = 64 900, 303 + 4;
+// 2 heads x 700 116, 64 + 4.
+int col_parts(const DiffProblem& p) {
+  const long long blocks = (long long)((p.N + kM - 1) / kM) * p.B * p.Hk;
+  const long long tiles = (long long)((p.N + kT - 1) / kT) * p.G();
+  return (int)max(1ll, min(kSms / blocks, tiles / 4));
 }
 
 Args make_args(const DiffProblem& p, const DiffTensors& t) {
@@ -631,11 +676,12 @@ Args make_args(const DiffProblem& p, const DiffTensors& t) {
 constexpr size_t kMaxShared = 232448;
 
 template <typename K>
-cudaError_t launch(K kernel, int blocks, int split, size_t floats, const Args& a, LaunchLog& log) {
+cudaError_t launch(K kernel, int blocks, int split, size_t floats, const Args& a, LaunchLog& log,
+                   int parts = 1) {
   const size_t bytes = floats * sizeof(float);
   cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)bytes);
   if (e != cudaSuccess) return e;
-  kernel<<<(unsigned)(blocks * a.heads), split * kThreads, bytes, log.stream>>>(a);
+  kernel<<<dim3(blocks * a.heads, parts), split * kThreads, bytes, log.stream>>>(a);
   e = cudaGetLastError();
   log.mark();
   return e;
@@ -644,11 +690,11 @@ cudaError_t launch(K kernel, int blocks, int split, size_t floats, const Args& a
 // Two groups per block where their areas fit in shared memory.
 template <typename K1, typename K2>
 cudaError_t run(K1 one, K2 two, int blocks, int heads, size_t fixed, size_t area, Args a,
-                LaunchLog& log) {
+                LaunchLog& log, int parts = 1) {
   a.heads = heads;
   if ((fixed + 2 * area) * sizeof(float) <= kMaxShared)
-    return launch(two, blocks, 2, fixed + 2 * area, a, log);
-  return launch(one, blocks, 1, fixed + area, a, log);
+    return launch(two, blocks, 2, fixed + 2 * area, a, log, parts);
+  return launch(one, blocks, 1, fixed + area, a, log, parts);
 }
 
 template <typename T>
@@ -671,9 +717,10 @@ cudaError_t forward_t(const DiffProblem& p, const DiffTensors& t, LaunchLog& log
 }
 
 template <typename T, int NGD, int NGV>
-cudaError_t columns(int blocks, int heads, size_t fixed, int tiles, const Args& a, LaunchLog& log) {
+cudaError_t columns(int blocks, int heads, size_t fixed, int tiles, const Args& a, LaunchLog& log,
+                    int parts) {
   return run(diff_bwd_col<T, NGD, NGV, 1>, diff_bwd_col<T, NGD, NGV, 2>, blocks, heads, fixed,
-             group_floats(tiles, 32 * NGD + 16 * NGV), a, log);
+             group_floats(tiles, 32 * NGD + 16 * NGV), a, log, parts);
 }
 
 template <typename T>
@@ -682,23 +729,35 @@ cudaError_t backward_t(const DiffProblem& p, const DiffTensors& t, const DiffWor
   Args a = make_args(p, t);
   a.D = ws.D;
   a.d2 = ws.d2;
+  a.parts = ws.parts;
   const int ld = ld_of(p.d), ldv = ld_of(p.dv), tiles = kT * (2 * ld + ldv) + kM * kLdp;
   const int blocks = (p.N + kM - 1) / kM, rows = p.B * p.H, cols = p.B * p.Hk;
   const size_t fixed = (size_t)kM * (2 * ld + ldv);
-  const cudaError_t e = p.d <= 64 ? run(diff_bwd_row<T, 1, 1>, diff_bwd_row<T, 1, 2>, blocks, rows,
-                                        fixed, group_floats(tiles, 32 + 4), a, log)
-                                  : run(diff_bwd_row<T, 2, 1>, diff_bwd_row<T, 2, 2>, blocks, rows,
-                                        fixed, group_floats(tiles, 64 + 4), a, log);
+  cudaError_t e = p.d <= 64 ? run(diff_bwd_row<T, 1, 1>, diff_bwd_row<T, 1, 2>, blocks, rows, fixed,
+                                  group_floats(tiles, 32 + 4), a, log)
+                            : run(diff_bwd_row<T, 2, 1>, diff_bwd_row<T, 2, 2>, blocks, rows, fixed,
+                                  group_floats(tiles, 64 + 4), a, log);
   if (e != cudaSuccess) return e;
-  const int ct = tiles + 5 * kT;
-  if (p.d <= 64)
-    return p.dv <= 64 ? columns<T, 1, 1>(blocks, cols, fixed, ct, a, log)
-                      : columns<T, 1, 2>(blocks, cols, fixed, ct, a, log);
-  return p.dv <= 64 ? columns<T, 2, 1>(blocks, cols, fixed, ct, a, log)
-                    : columns<T, 2, 2>(blocks, cols, fixed, ct, a, log);
+  const int ct = tiles + 5 * kT, parts = col_parts(p);
+  e = p.d <= 64 ? p.dv <= 64 ? columns<T, 1, 1>(blocks, cols, fixed, ct, a, log, parts)
+                             : columns<T, 1, 2>(blocks, cols, fixed, ct, a, log, parts)
+      : p.dv <= 64 ? columns<T, 2, 1>(blocks, cols, fixed, ct, a, log, parts)
+                   : columns<T, 2, 2>(blocks, cols, fixed, ct, a, log, parts);
+  if (e != cudaSuccess || parts == 1) return e;
+  a.heads = cols;
+  const size_t total = (size_t)cols * p.N * (2 * p.d + p.dv);
+  diff_join<T><<<(unsigned)((total + 255) / 256), 256, 0, log.stream>>>(a, parts);
+  e = cudaGetLastError();
+  log.mark();
+  return e;
 }
 
 }  // namespace
+
+size_t diff_simt_part_count(const DiffProblem& p) {
+  const int parts = col_parts(p);
+  return parts == 1 ? 0 : (size_t)parts * p.B * p.Hk * p.N * (2 * p.d + p.dv);
+}
 
 cudaError_t diff_simt_forward(const DiffProblem& p, const DiffTensors& t, LaunchLog& log) {
   return p.bf16 ? forward_t<__nv_bfloat16>(p, t, log) : forward_t<float>(p, t, log);

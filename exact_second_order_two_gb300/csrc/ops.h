@@ -39,7 +39,7 @@ struct DiffWorkspace {
   float* scal = nullptr;     // the row scalars' blocks (tensor cores)
   float* d2 = nullptr;       // [B, H, N]: sum_j P^2_ij dP_ij, for lam's gradient
   float* partial = nullptr;  // [B, H]: its sums
-  float* parts = nullptr;    // parts of dK and dV (tensor cores, few blocks)
+  float* parts = nullptr;    // parts of dK and dV, where blocks are few
 };
 
 struct DiffTensors {
@@ -53,6 +53,7 @@ struct DiffTensors {
 };
 
 // ---- CUDA-core kernels: fp32 or bf16, any d and dv up to 128 -------------
+size_t diff_simt_part_count(const DiffProblem& p);  // fp32 values of DiffWorkspace::parts
 cudaError_t diff_simt_forward(const DiffProblem& p, const DiffTensors& t, LaunchLog& log);
 cudaError_t diff_simt_backward(const DiffProblem& p, const DiffTensors& t, const DiffWorkspace& ws,
                                LaunchLog& log);

@@ -164,6 +164,10 @@ CASES = [
     (1, 2, 1, 63, 1, 3, F32, True, ("head", F32)),
     (1, 1, 1, 130, 128, 128, F32, True, ("one", BF)),
     (1, 2, 2, 77, 70, 50, F32, False, ("head", F32)),
+    # dK and dV in parts, some of them empty
+    (1, 4, 1, 300, 40, 72, F32, True, ("one", F32)),
+    (1, 1, 1, 700, 16, 20, F32, True, ("head", F32)),
+    (2, 2, 1, 260, 10, 3, BF, False, ("head", BF)),
 ]
 
 
