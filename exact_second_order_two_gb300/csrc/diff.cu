@@ -2,15 +2,15 @@
 // kernel family), the row scalars of its backward and the gradient of lam.
 //
 // D^m_i = dO_i . O^m_i comes from the saved O = O^1 - lam O^2 and O^2:
-// D^2 = dO . O^2 and D^1 = dO . O + lam D^2.  With O rounded to bf16, D^1 would
-// add the rounding to every dS of its row (the gradients of q and k then had
-// 1.49 times the error of their own rounding); so what the rounding left off is
-// kept beside O^2, and only O^2's is left (1.45 times).  lam's gradient, dlam_i =
-// -dO_i . O^2_i, is summed over what shares a value of lam (per head, or over
-// everything).  Those sums cancel, so a rounded O^2 is not good enough for
-// them: the pass that computes dQ also sums P^2_ij dP_ij over j in fp32, the
-// same number from unrounded factors, and the sums here add them up in a
-// fixed order.
+// D^2 = dO . O^2 and D^1 = dO . O + lam D^2.  With both rounded to bf16 the
+// roundings would reach every dS of the row (and more so where the maps nearly
+// cancel: with 16 keys and lam = 1 the gradients of q and k had 1.8 times the
+// error of their own rounding, with 2048 keys 1.49 times); so what they left off
+// is kept beside them, and the scalars are as good as fp32 (1.42 to 1.5 times,
+// from dS as a bf16 operand).  lam's gradient, dlam_i = -D^2_i, is summed over
+// what shares a value of lam (per head, or over everything): the pass that
+// computes dQ sums P^2_ij dP_ij over j in fp32, the same number from unrounded
+// factors, and the sums here add them up in a fixed order.
 #include <cuda_bf16.h>
 #include <cuda_runtime.h>
 #include <stdint.h>
@@ -90,17 +90,20 @@ template <typename T>
 __global__ void __launch_bounds__(256)
     diff_row_scalars(const T* __restrict__ o, const T* __restrict__ rest, const T* __restrict__ dO,
                      LamArg lam, float* __restrict__ D, size_t rows, int H, int N, int dv) {
-  constexpr int R = sizeof(T) == 2 ? 2 : 1;
+  constexpr int R = sizeof(T) == 2 ? 3 : 1;
   const size_t row = (size_t)blockIdx.x * 8 + (threadIdx.x >> 5);
   const int lane = threadIdx.x & 31;
   if (row >= rows) return;
   float s1 = 0.f, s2 = 0.f;
   for (int c = lane; c < dv; c += 32) {
     const float g = to_f32<T>(dO[row * dv + c]);
-    float out = to_f32<T>(o[row * dv + c]);
-    if (R == 2) out += to_f32<T>(rest[(row * R + 1) * dv + c]);
+    float out = to_f32<T>(o[row * dv + c]), o2 = to_f32<T>(rest[row * R * dv + c]);
+    if (R == 3) {
+      o2 += to_f32<T>(rest[(row * R + 1) * dv + c]);
+      out += to_f32<T>(rest[(row * R + 2) * dv + c]);
+    }
     s1 = fmaf(g, out, s1);
-    s2 = fmaf(g, to_f32<T>(rest[row * R * dv + c]), s2);
+    s2 = fmaf(g, o2, s2);
   }
   s1 = warp_sum(s1);
   s2 = warp_sum(s2);

@@ -204,6 +204,15 @@ __device__ __forceinline__ void store_rows(T* dst, const float (&acc)[4][4 * NG]
   }
 }
 
+// What rounding to T leaves off.
+template <typename T, int NG>
+__device__ __forceinline__ void left_off(float (&acc)[4][4 * NG]) {
+#pragma unroll
+  for (int i = 0; i < 4; ++i)
+#pragma unroll
+    for (int e = 0; e < 4 * NG; ++e) acc[i][e] -= to_f32<T>(from_f32<T>(acc[i][e]));
+}
+
 // A group's threads only (the block's, where there is one group)
 template <int SPLIT>
 __device__ __forceinline__ void group_sync(int grp) {
@@ -343,7 +352,7 @@ __global__ void __launch_bounds__(SPLIT * 2 * kThreads, 2 / SPLIT) diff_fwd(Args
     }
   }
   const size_t ob = (size_t)bh * N * a.dv_;
-  constexpr int R = sizeof(T) == 2 ? 2 : 1;
+  constexpr int R = sizeof(T) == 2 ? 3 : 1;
   T* rest = static_cast<T*>(a.rest) + R * ob;
 #pragma unroll
   for (int i = 0; i < 4; ++i) {
@@ -362,7 +371,12 @@ __global__ void __launch_bounds__(SPLIT * 2 * kThreads, 2 / SPLIT) diff_fwd(Args
   }
   pair_sync();
   if (m == 1) {
-    if (a.rest) store_rows<T, NGV>(rest, acc, 1.f, row0, N, a.dv_, R * a.dv_, ty, tx);
+    if (!a.rest) return;
+    store_rows<T, NGV>(rest, acc, 1.f, row0, N, a.dv_, R * a.dv_, ty, tx);
+    if constexpr (R == 3) {
+      left_off<T, NGV>(acc);
+      store_rows<T, NGV>(rest + a.dv_, acc, 1.f, row0, N, a.dv_, R * a.dv_, ty, tx);
+    }
     return;
   }
 #pragma unroll
@@ -373,13 +387,10 @@ __global__ void __launch_bounds__(SPLIT * 2 * kThreads, 2 / SPLIT) diff_fwd(Args
     for (int e = 0; e < 4 * NGV; ++e) acc[i][e] -= w * pair[(i * 4 * NGV + e) * kThreads + tid];
   }
   store_rows<T, NGV>(static_cast<T*>(a.o) + ob, acc, 1.f, row0, N, a.dv_, a.dv_, ty, tx);
-  if constexpr (R == 2) {  // what the rounding of o left off
+  if constexpr (R == 3) {
     if (!a.rest) return;
-#pragma unroll
-    for (int i = 0; i < 4; ++i)
-#pragma unroll
-      for (int e = 0; e < 4 * NGV; ++e) acc[i][e] -= to_f32<T>(from_f32<T>(acc[i][e]));
-    store_rows<T, NGV>(rest + a.dv_, acc, 1.f, row0, N, a.dv_, R * a.dv_, ty, tx);
+    left_off<T, NGV>(acc);
+    store_rows<T, NGV>(rest + 2 * a.dv_, acc, 1.f, row0, N, a.dv_, R * a.dv_, ty, tx);
   }
 }
 

@@ -174,7 +174,7 @@ __device__ __forceinline__ void store_box(const CUtensorMap* map, const void* sr
       : "memory");
 }
 // The tile of load_rows back: rows past N, and elements past a row's end, are
-// left as they are.  r: third coordinate of a narrow tensor's map.  The caller
+// left as they are.  r: third coordinate of the map.  The caller
 // fences its writes (fence_async_smem) and ends with stores_done.
 template <int W, int ROWS>
 __device__ __forceinline__ void store_rows(const CUtensorMap* map, const uint8_t* src, int row, int bh,
@@ -230,6 +230,7 @@ struct Fwd {
   static constexpr uint32_t OFF_MISC = OFF_RED + 2 * 128 * 4;
   static constexpr uint32_t SMEM = OFF_MISC + 512;
   static_assert(SMEM <= 232448, "forward shared memory budget");
+  static_assert(4 * BM * DV * 2 <= OFF_RED - OFF_K, "o and rest are staged over the tiles");
   // TMEM columns: two score buffers (map m in buffer m; bf16 P overwrites the
   // first 16 of each thread's 32), O^1, O^2
   static constexpr uint32_t TMEM_COLS = 512;
@@ -242,7 +243,7 @@ struct Fwd {
 };
 
 struct FwdParams : Common {
-  bool rest;  // whether O^2 and what o's rounding left off are wanted (mR)
+  bool rest;  // whether O^2 and what its and o's rounding left off are wanted (mR)
   float* lse;
 };
 
@@ -506,12 +507,16 @@ __global__ void __launch_bounds__(kFwdThreads, 1)
     const float w = in ? lam_row(prm.lam, bh, prm.H, N, i) : 0.f;
     // through shared memory (the tiles' stages are free) into whole lines: from
     // the threads, each in a row of its own, the stores took 9000 cycles
-    const uint32_t so = sb + C::OFF_K, sr = so + C::BM * DV * 2;  // o; O^2 and the rest of o
+    const uint32_t so = sb + C::OFF_K, sr = so + C::BM * DV * 2;  // o; rest's three parts
 #pragma unroll
     for (int c = 0; c < PART; c += 16) {
       uint32_t a[16], b[16];
       tmem_ld16x2(tmem + lane_off + C::T_O(0) + f0 + c, tmem + lane_off + C::T_O(1) + f0 + c, a, b);
-      uint32_t wo[8], w2[8], wl[8];
+      auto left = [](uint32_t w, float x, float y) {  // what the rounding to w left off
+        const float2 back = __bfloat1622float2(*reinterpret_cast<const __nv_bfloat162*>(&w));
+        return pack_bf16(x - back.x, y - back.y);
+      };
+      uint32_t wo[8], w2[8], l2[8], wl[8];
 #pragma unroll
       for (int e = 0; e < 8; ++e) {
         const float x2 = __uint_as_float(b[2 * e]) * inv2, y2 = __uint_as_float(b[2 * e + 1]) * inv2;
@@ -519,25 +524,26 @@ __global__ void __launch_bounds__(kFwdThreads, 1)
         const float y = fmaf(-w, y2, __uint_as_float(a[2 * e + 1]) * inv1);
         wo[e] = pack_bf16(x, y);
         w2[e] = pack_bf16(x2, y2);
-        const float2 back = __bfloat1622float2(*reinterpret_cast<const __nv_bfloat162*>(&wo[e]));
-        wl[e] = pack_bf16(x - back.x, y - back.y);
+        l2[e] = left(w2[e], x2, y2);
+        wl[e] = left(wo[e], x, y);
       }
       const uint32_t blk = (uint32_t)((f0 + c) / 64) * C::BM * 128;  // 64-feature block
       const int chunk = (f0 + c) % 64 / 8;
       put16(so + blk, row, chunk, wo);
       if (prm.rest) {
         put16(sr + blk, row, chunk, w2);
-        put16(sr + C::BM * DV * 2 + blk, row, chunk, wl);
+        put16(sr + C::BM * DV * 2 + blk, row, chunk, l2);
+        put16(sr + 2 * C::BM * DV * 2 + blk, row, chunk, wl);
       }
     }
     fence_async_smem();
     named_sync<kSoftmax>(1);
     if (threadIdx.x == 0) {
       store_rows<DV, C::BM>(&mO, smem + C::OFF_K, i0, bh, nv);
-      if (prm.rest) {  // one box for both parts where they are DV wide
+      if (prm.rest) {
         const uint8_t* src = smem + C::OFF_K + C::BM * DV * 2;
-        store_rows<DV, C::BM>(&mR, src, i0, bh, nv);
-        if (nv) store_rows<DV, C::BM>(&mR, src + C::BM * DV * 2, i0, bh, true, 1);
+        for (int r = 0; r < 3; ++r)  // a wide row's 64-feature blocks follow one another
+          store_rows<DV, C::BM>(&mR, src + r * C::BM * DV * 2, i0, bh, nv, nv ? r : r * (DV / 64));
       }
       stores_done();
     }
@@ -553,8 +559,8 @@ __global__ void __launch_bounds__(kFwdThreads, 1)
 }
 
 // ===========================================================================
-// Row scalars: D^2 = dO . O^2, D^1 = dO . O + lam D^2 (O = O^1 - lam O^2, with
-// what its rounding left off)
+// Row scalars: D^2 = dO . O^2, D^1 = dO . O + lam D^2 (O = O^1 - lam O^2; both
+// with what their rounding left off)
 // ===========================================================================
 // acc + the dot product of 8 bf16 pairs, in fp32
 __device__ __forceinline__ float dot8(const uint4& a, const uint4& b, float acc) {
@@ -596,8 +602,8 @@ __global__ void __launch_bounds__(256, 4)
     if (n0 + r < N && c < vecs) {
       const size_t row = (size_t)bh * N + n0 + r;
       const uint4 g = dO[row * vecs + c];
-      s1[i] = dot8(o[row * vecs + c], g, dot8(rest[(2 * row + 1) * vecs + c], g, 0.f));
-      s2[i] = dot8(rest[2 * row * vecs + c], g, 0.f);
+      s1[i] = dot8(o[row * vecs + c], g, dot8(rest[(3 * row + 2) * vecs + c], g, 0.f));
+      s2[i] = dot8(rest[3 * row * vecs + c], g, dot8(rest[(3 * row + 1) * vecs + c], g, 0.f));
     }
   }
 #pragma unroll
@@ -1334,24 +1340,18 @@ Common common(const DiffProblem& p, const DiffTensors& t, const DiffWorkspace& w
   return c;
 }
 
-// [B, heads, N, parts, width] as boxes of `rows` rows: all 64-feature blocks of a
-// row where it is as wide as the kernel (of all parts, then), else one block
+// [B, heads, N, parts, width] as boxes of `rows` rows of one part: all 64-feature
+// blocks where a row is as wide as the kernel (then the third coordinate counts
+// blocks), else one block (it counts parts)
 bool tiles(CUtensorMap* m, const void* ptr, const DiffProblem& p, int heads, int width, int rows,
            int parts = 1) {
-  if (width == built(width)) {
-    Problem q{};
-    q.B = p.B;
-    q.H = heads;
-    q.N = p.N;
-    q.d = parts * width;
-    return make_map(m, ptr, q, rows);
-  }
+  const bool wide = width == built(width);
   auto fn = encode_fn();
   if (!fn) return false;
-  const cuuint64_t w = width, n = p.N, r = parts;
+  const cuuint64_t blocks = wide ? width / 64 : 1, w = width / blocks, n = p.N, r = parts * blocks;
   const cuuint64_t dims[4] = {w, n, r, (cuuint64_t)p.B * heads};
   const cuuint64_t strides[3] = {r * w * 2, w * 2, n * r * w * 2};
-  const cuuint32_t box[4] = {64, (cuuint32_t)rows, 1, 1}, es[4] = {1, 1, 1, 1};
+  const cuuint32_t box[4] = {64, (cuuint32_t)rows, (cuuint32_t)blocks, 1}, es[4] = {1, 1, 1, 1};
   return fn(m, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 4, const_cast<void*>(ptr), dims, strides, box, es,
             CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
             CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
@@ -1374,7 +1374,7 @@ cudaError_t forward_d(const DiffProblem& p, const DiffTensors& t, const DiffWork
   CUtensorMap mQ, mK, mV, mO, mR;  // without rest mR is a placeholder
   if (!tiles(&mQ, t.q, p, 2 * p.H, p.d, 128) || !tiles(&mK, t.k, p, 2 * p.Hk, p.d, 128) ||
       !tiles(&mV, t.v, p, p.Hk, p.dv, 128) || !tiles(&mO, t.o, p, p.H, p.dv, 128) ||
-      !tiles(&mR, t.rest ? t.rest : t.o, p, p.H, p.dv, 128, t.rest ? 2 : 1))
+      !tiles(&mR, t.rest ? t.rest : t.o, p, p.H, p.dv, 128, t.rest ? 3 : 1))
     return cudaErrorInvalidValue;
   FwdParams f;
   static_cast<Common&>(f) = common(p, t, ws, p.B * p.H);

@@ -45,7 +45,8 @@ struct DiffWorkspace {
 struct DiffTensors {
   const void *q, *k, *v;
   LamArg lam;
-  // rest [B,H,N,R,dv]: P^2 V and, for bf16, O - o (null: not wanted)
+  // rest [B,H,N,R,dv]: P^2 V and, for bf16, what its and o's rounding left off
+  // (null: not wanted)
   void *o, *rest;
   float* lse;    // [B, 2H, N]
   const void* dO;

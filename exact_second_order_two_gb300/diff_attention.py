@@ -82,7 +82,7 @@ def _match(name, t, shape, dtype, device):
 
 
 def _rest_shape(shp):
-    return (shp.B, shp.H, shp.N, 2 if shp.dtype == _b.DTYPES[torch.bfloat16] else 1, shp.dv)
+    return (shp.B, shp.H, shp.N, 3 if shp.dtype == _b.DTYPES[torch.bfloat16] else 1, shp.dv)
 
 
 def _workspace(op, shp, device, given=None):
@@ -102,8 +102,8 @@ def diff_forward(q, k, v, lam, causal: bool = False, scale: float | None = None,
                  need_rest: bool = True, workspace=None):
     """Differential attention forward: returns (O, rest, LSE).  rest is what
     else ``diff_backward`` reads, or None where ``need_rest`` is false:
-    [B, H, N, 1, dv] with O2 = softmax(c Q2 K2^T) V for fp32, [B, H, N, 2, dv]
-    with O2 and what the rounding of O left off for bf16.  LSE [B, 2H, N] holds
+    [B, H, N, 1, dv] with O2 = softmax(c Q2 K2^T) V for fp32, [B, H, N, 3, dv]
+    with O2 and what its and O's rounding left off for bf16.  LSE [B, 2H, N] holds
     the rows' log-sum-exp of both maps.
 
     q: [B, 2H, N, d], the two queries of head h as heads 2h and 2h + 1;
@@ -208,8 +208,8 @@ class _DiffBackward(torch.autograd.Function):
         w = _rows(lam, B, H, N)
         vv, gvv = fit(v, Hk), fit(gv, Hk)
         o1 = o.float() + w * o2.float()
-        if rest.shape[3] == 2:
-            o1 += rest[..., 1, :].float()
+        if rest.shape[3] == 3:
+            o1 += w * rest[..., 1, :].float() + rest[..., 2, :].float()
         o1 = o1.to(dtype)
         gdo = torch.zeros(do.shape, dtype=torch.float32, device=do.device)
         grad_lam = torch.zeros((B, H, N), dtype=torch.float32, device=do.device)

@@ -255,12 +255,12 @@ int fbob_rotary(const fbob_rotary_t* r, const void* x, const double* inv_freq,
  * Layouts, all dense and row-major: q [B,2H,N,d] with Q^1, Q^2 of head h as
  * heads 2h, 2h + 1; k [B,2Hk,N,d] likewise; v [B,Hk,N,dv]; o, dO
  * [B,H,N,dv]; lse [B,2H,N] fp32; rest [B,H,N,R,dv], R = 1 for fp32: P^2 V, and
- * R = 2 for bf16: P^2 V and O - o, what o's rounding left off.  H is a
- * multiple of Hk: query head h reads key head h / (H / Hk).  lam is one value,
- * [H], or [B,H,N], bf16 or fp32.  Masking, ownership, asynchrony and alignment
- * as above (lam to its own size); scale > 0.  1 <= d, dv <= 128,
- * B*H <= 32767.  bf16 at d and dv that are multiples of 8 runs the
- * tensor-core kernels, the rest runs on CUDA cores (fbob_diff_path).
+ * R = 3 for bf16: P^2 V, what its rounding left off, and what o's rounding
+ * left off.  H is a multiple of Hk: query head h reads key head h / (H / Hk).
+ * lam is one value, [H], or [B,H,N], bf16 or fp32.  Masking, ownership,
+ * asynchrony and alignment as above (lam to its own size); scale > 0.
+ * 1 <= d, dv <= 128, B*H <= 32767.  bf16 at d and dv that are multiples of 8
+ * runs the tensor-core kernels, the rest runs on CUDA cores (fbob_diff_path).
  * Every output is summed in a fixed order: equal inputs give equal bits. */
 typedef enum { FBOB_LAM_ONE = 0, FBOB_LAM_HEAD = 1, FBOB_LAM_ROW = 2 } fbob_lam_t;
 
