@@ -38,7 +38,7 @@
 // what the products they run come to as a share of the measured matmul rate of
 // 1917 TFLOP/s):
 //            forward        row pass        column pass
-//   d = 64   573 us, 75%    574 us, 75%     948 us, 61%
+//   d = 64   570 us, 75%    572 us, 75%     948 us, 61%
 //   d = 128  654 us, 88%    947 us, 76%     1358 us, 63%
 // The chain scores -> exponentials -> product within a tile: the accumulators
 // leave TMEM for one or two buffers per map, so pipe and elementwise warps wait
