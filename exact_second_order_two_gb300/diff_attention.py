@@ -76,7 +76,7 @@ def _shape(q, k, v, lam, causal, scale) -> _b.DiffShape:
 
 
 def _match(name, t, shape, dtype, device):
-    if tuple(t.shape) != tuple(shape) or t.dtype != dtype or t.device != device or \
+    if t is None or tuple(t.shape) != tuple(shape) or t.dtype != dtype or t.device != device or \
             not t.is_contiguous():
         raise ValueError(f"{name} must be contiguous {dtype} {tuple(shape)} on {device}")
 

@@ -543,6 +543,8 @@ class TestOnGpu:
             fbob.diff_backward(q, k, v, w, o, rest, lse, do.float())
         with pytest.raises(ValueError):
             fbob.diff_backward(q, k, v, w, o, rest, lse[:, :2], do)
+        with pytest.raises(ValueError):  # of a forward that no backward was to follow
+            fbob.diff_backward(q, k, v, w, o, fbob.diff_forward(q, k, v, w, need_rest=False)[1], lse, do)
 
 
 def test_rejects_cpu_tensors():
