@@ -938,7 +938,11 @@ struct Col {
   // and dP^T, over which S^T of map 2 goes once dP^T has been read.
   static constexpr bool WIDE = D == 128;
   static constexpr uint32_t TMEM_COLS = 512, T_S1 = 0, T_DP = WIDE ? 64 : 192, T_DV = 384;
-  __host__ __device__ static constexpr uint32_t T_S2(int b) { return WIDE ? 64u : 64u + 64u * b; }
+  static constexpr int S2 = WIDE ? 1 : 2;  // buffers of S^T of map 2
+  // that of tile a, and the parity of the phase of its barriers
+  __host__ __device__ static constexpr int buf(int a) { return a & (S2 - 1); }
+  __host__ __device__ static constexpr uint32_t phase(int a) { return (uint32_t)(a >> (S2 - 1)) & 1u; }
+  __host__ __device__ static constexpr uint32_t T_S2(int b) { return 64u + 64u * b; }
   __host__ __device__ static constexpr uint32_t T_DK(int m) {
     return (WIDE ? 128u : 256u) + (uint32_t)D * m;
   }
@@ -967,12 +971,19 @@ __global__ void __launch_bounds__(kThreads, 1)
   uint64_t* kv_full = reinterpret_cast<uint64_t*>(smem + C::OFF_MISC);
   uint64_t* full = kv_full + 1;            // [ST]: Q^1, Q^2, dO landed, scalars written
   uint64_t* empty = full + C::ST;          // [ST]: the tile's last products done
-  uint64_t* s_full = empty + C::ST;        // [2]: S^T of map m in TMEM, for map 1 dP^T too
-  uint64_t* dp_read = s_full + 2;          // every thread holds its dP
-  uint64_t* ds_full = dp_read + 1;         // [2]: bf16 operands written over the scores
-  uint64_t* acc_done = ds_full + 2;
+  // S^T of map 2 is a tile ahead of the warps where it has two TMEM buffers
+  // (!WIDE).  Each then has a barrier of its own, for the scores and for the
+  // operands over them, so that none runs two phases ahead of a waiter and no
+  // warp's arrival for the next tile counts for this one: a buffer's next scores
+  // are committed behind the wait for its operands.
+  uint64_t* s_full = empty + C::ST;        // S^T of map 1 and dP^T in TMEM
+  uint64_t* s2_full = s_full + 1;          // [S2]: S^T of map 2
+  uint64_t* dp_read = s2_full + C::S2;     // every thread holds its dP
+  uint64_t* ds_full = dp_read + 1;         // bf16 dS^T of map 1 written over the scores
+  uint64_t* ds2_full = ds_full + 1;        // [S2]: bf16 operands of map 2
+  uint64_t* acc_done = ds2_full + C::S2;
   uint64_t* drain = acc_done + 1;
-  static_assert((1 + 2 * C::ST + 7) * 8 <= 256, "barriers end below the TMEM slot");
+  static_assert((1 + 2 * C::ST + 5 + 2 * C::S2) * 8 <= 256, "barriers end below the TMEM slot");
   uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(smem + C::OFF_MISC + 256);
   Abort* ab = reinterpret_cast<Abort*>(smem + C::OFF_MISC + 264);
   float* scal = reinterpret_cast<float*>(smem + C::OFF_SC);
@@ -1004,9 +1015,11 @@ __global__ void __launch_bounds__(kThreads, 1)
       mbar_init(full + s, 1);
       mbar_init(empty + s, 1);
     }
-    for (int m = 0; m < 2; ++m) {
-      mbar_init(s_full + m, 1);
-      mbar_init(ds_full + m, kWarps);
+    mbar_init(s_full, 1);
+    mbar_init(ds_full, kWarps);
+    for (int s = 0; s < C::S2; ++s) {
+      mbar_init(s2_full + s, 1);
+      mbar_init(ds2_full + s, kWarps);
     }
     mbar_init(dp_read, kWarps);
     mbar_init(acc_done, 1);
@@ -1057,7 +1070,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     constexpr uint32_t id_k = idesc_bf16(128, D, false, true);       // dK += dS^T Q
     constexpr uint32_t id_v = idesc_bf16(128, DV, false, true);      // dV += W^T dO
     auto tile = [&](int a) { return sb + C::OFF_T + (uint32_t)(a % C::ST) * C::STB; };
-    auto s_cols = [&](int a, int m) { return tmem + (m == 0 ? C::T_S1 : C::T_S2(a & 1)); };
+    auto s_cols = [&](int a, int m) { return tmem + (m == 0 ? C::T_S1 : C::T_S2(C::buf(a))); };
     auto issue_s = [&](int a, int m) {
       const uint32_t k_lo = opaque(lo_kmajor(sb + C::OFF_K + m * C::KB));
       const uint32_t q_lo = opaque(lo_kmajor(tile(a) + m * C::QB));
@@ -1079,7 +1092,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       issue_s(a, 0);
       mma_commit_w(s_full);
       issue_s(a, 1);
-      mma_commit_w(s_full + 1);
+      mma_commit_w(s2_full + C::buf(a));
     };
     // dK^m += dS^m^T Q^m
     auto issue_dk = [&](int a, int m) {
@@ -1110,7 +1123,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         await(dp_read, a & 1, ab, prm.status);
         tc_fence_after();
         issue_s(a, 1);
-        mma_commit_w(s_full + 1);
+        mma_commit_w(s2_full + C::buf(a));
         // dK^1, then the next tile's S^T of map 1 over the dS^T it read
         if (more) await(full + (a + 1) % C::ST, ((a + 1) / C::ST) & 1, ab, prm.status);
         await(ds_full, a & 1, ab, prm.status);
@@ -1118,7 +1131,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         issue_dk(a, 0);
         if (more) issue_s(a + 1, 0);
         // dK^2 and dV, then the next dP^T over their operands
-        await(ds_full + 1, a & 1, ab, prm.status);
+        await(ds2_full + C::buf(a), C::phase(a), ab, prm.status);
         tc_fence_after();
         issue_dk(a, 1);
         issue_dv(a);
@@ -1147,7 +1160,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       // product read, that of map 2 over the operands of tile a - 1
       issue_dk(a, 0);
       if (more) issue_scores(a + 1);
-      await(ds_full + 1, a & 1, ab, prm.status);
+      await(ds2_full + C::buf(a), C::phase(a), ab, prm.status);
       tc_fence_after();
       issue_dk(a, 1);
       issue_dv(a);
@@ -1180,9 +1193,10 @@ __global__ void __launch_bounds__(kThreads, 1)
       float p1[NC];
 #pragma unroll
       for (int m = 0; m < 2; ++m) {
-        await(s_full + m, a & 1, ab, prm.status);
+        if (m == 0) await(s_full, a & 1, ab, prm.status);
+        else await(s2_full + C::buf(a), C::phase(a), ab, prm.status);
         tc_fence_after();
-        const uint32_t ts = tmem + lane_off + (m == 0 ? C::T_S1 : C::T_S2(a & 1)) + NC * slice;
+        const uint32_t ts = tmem + lane_off + (m == 0 ? C::T_S1 : C::T_S2(C::buf(a))) + NC * slice;
         uint32_t sr[NC];
         if (m == 0) {
           tmem_ld16x2(ts, tmem + lane_off + C::T_DP + NC * slice, sr, dp);
@@ -1230,7 +1244,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         if (m == 0) tmem_st8(ts + 8, dsw);
         else tmem_st8x2(ts, ww, ts + 8, dsw);
         tc_fence_before();
-        warp_arrive(ds_full + m);
+        warp_arrive(m == 0 ? ds_full : ds2_full + C::buf(a));
       }
     }
     // ---- epilogue: dK (scaled), half the features of one map per thread, and dV ----
