@@ -138,6 +138,15 @@ def _ptr(t: torch.Tensor | None):
     return None if t is None else ctypes.c_void_p(t.data_ptr())
 
 
+def dense(t: torch.Tensor) -> torch.Tensor:
+    """t, where the C calls can read it as it is (contiguous, at a 16-byte
+    boundary), else a copy that autograd sees.  A contiguous view can start
+    anywhere: a slice of a flat buffer, or of the gradient of a concatenation."""
+    if t.is_contiguous() and t.data_ptr() % 16 == 0:
+        return t
+    return t.clone(memory_format=torch.contiguous_format)
+
+
 def _check_tensors(ref: torch.Tensor, named: dict, scalar_names=()):
     if not ref.is_cuda:
         raise ValueError("tensors must be CUDA tensors")

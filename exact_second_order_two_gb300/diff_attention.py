@@ -108,8 +108,9 @@ def diff_forward(q, k, v, lam, causal: bool = False, scale: float | None = None,
 
     q: [B, 2H, N, d], the two queries of head h as heads 2h and 2h + 1;
     k: [B, 2Hk, N, d] likewise; v: [B, Hk, N, dv], with H a multiple of Hk
-    (query head h reads key head h // (H / Hk)); bf16 or fp32, contiguous, d and
-    dv up to 128 (bf16 multiples of 8 run on the tensor cores).
+    (query head h reads key head h // (H / Hk)); bf16 or fp32, contiguous and at
+    16-byte boundaries, d and dv up to 128 (bf16 multiples of 8 run on the tensor
+    cores).
     lam: no dimensions, [H] or [B, H, N], bf16 or fp32.  scale > 0 defaults to
     1/sqrt(d); with ``causal`` key j is visible to query i iff j <= i.  A key
     whose score is -inf has no weight; but as in the dense product, an infinite
@@ -175,7 +176,7 @@ class _DiffBackward(torch.autograd.Function):
 
     @staticmethod
     def forward(ctx, q, k, v, lam, do, o, rest, lse, shp):
-        do = _contig(do)
+        do = _b.dense(do)
         grads = _backward(shp, q, k, v, lam, o, rest, lse, do)
         ctx.save_for_backward(q, k, v, lam, do, o, rest, lse)
         ctx.causal, ctx.scale = bool(shp.causal), shp.scale
@@ -267,7 +268,7 @@ class _DiffAttention(torch.autograd.Function):
         if torch.is_grad_enabled():
             grads = _DiffBackward.apply(q, k, v, lam, do, o.detach(), rest, lse, ctx.shp)
         else:
-            grads = _backward(ctx.shp, q, k, v, lam, o, rest, lse, _contig(do))
+            grads = _backward(ctx.shp, q, k, v, lam, o, rest, lse, _b.dense(do))
         return *grads, None
 
 
@@ -278,7 +279,8 @@ def diff_attention(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, lam: torch
     masked to j <= i when causal.
 
     q [B, 2H, N, d], k [B, 2Hk, N, d], v [B, Hk, N, dv] and lam as for
-    ``diff_forward`` (non-contiguous inputs are copied first).  Returns
+    ``diff_forward`` (inputs that are not contiguous, or not at a 16-byte
+    boundary, are copied first).  Returns
     [B, H, N, dv].  Differentiable twice in q, k, v and lam; scale is not
     differentiated.  Backward passes can be captured into a CUDA graph together
     with their forward, from leaves that no live eager graph was built from
@@ -286,7 +288,7 @@ def diff_attention(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, lam: torch
     """
     if not torch.is_tensor(lam):
         raise TypeError(f"lam must be a tensor, got {type(lam).__name__}")
-    q, k, v, lam = _contig(q), _contig(k), _contig(v), _contig(lam)
+    q, k, v, lam = _b.dense(q), _b.dense(k), _b.dense(v), _contig(lam)
     shp = _shape(q, k, v, lam, causal, scale)
     if torch.is_grad_enabled() and (q.requires_grad or k.requires_grad or v.requires_grad
                                     or lam.requires_grad):

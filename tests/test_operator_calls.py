@@ -1,0 +1,80 @@
+"""Calls of the layer operators (rotary positions, differential attention) that
+their documentation allows, at the edges: tensors at any address, one batch and
+one head, forward-mode derivatives, second derivatives that round no more than
+they have to, and sizes whose offsets pass 32 bits."""
+import math
+
+import pytest
+import torch
+
+import exact_second_order_two_gb300 as fbob
+import test_diff_attention as diff
+
+BF, F32 = torch.bfloat16, torch.float32
+gpu = pytest.mark.gpu
+needs_gpu = pytest.mark.skipif(not torch.cuda.is_available(), reason="needs a GPU")
+
+
+def shifted(t):
+    """t at an address one element behind a 16-byte boundary."""
+    flat = torch.empty(t.numel() + 1, dtype=t.dtype, device=t.device)
+    flat[1:] = t.detach().flatten()
+    out = flat[1:].view(t.shape)
+    assert out.is_contiguous() and out.data_ptr() % 16
+    return out
+
+
+def dense_diff(q, k, v, w, causal):
+    """Differential attention in elementary operations, differentiable."""
+    B, H2, N, d = q.shape
+    H, Hk = H2 // 2, v.shape[1]
+    kk = k.view(B, Hk, 2, N, d).repeat_interleave(H // Hk, 1)
+    s = q.view(B, H, 2, N, d) @ kk.transpose(-1, -2) / math.sqrt(d)
+    if causal:
+        s = s.masked_fill(torch.ones(N, N, dtype=torch.bool, device=q.device).triu(1), -math.inf)
+    o = torch.softmax(s, -1) @ v.repeat_interleave(H // Hk, 1)[:, :, None]
+    ww = (w[:, None] if w.dim() == 1 else w).expand(B, H, N)[..., None]
+    return o[:, :, 0] - ww * o[:, :, 1]
+
+
+def dense_attention(q, k, v, causal):
+    s = q @ k.transpose(-1, -2) / math.sqrt(q.shape[-1])
+    if causal:
+        n = q.shape[2]
+        s = s.masked_fill(torch.ones(n, n, dtype=torch.bool, device=q.device).triu(1), -math.inf)
+    return torch.softmax(s, -1) @ v
+
+
+def second(args, cots, attn):
+    """The gradient of <cots, first gradients> in every argument; args end with
+    the upstream gradient, and a None in cots leaves a gradient out."""
+    leaves = [t.clone().requires_grad_() for t in args]
+    first = torch.autograd.grad(attn(*leaves[:-1]), leaves[:-1], leaves[-1], create_graph=True)
+    loss = sum((c * g).sum() for c, g in zip(cots, first) if c is not None)
+    return torch.autograd.grad(loss, leaves, allow_unused=True, materialize_grads=True)
+
+
+# ---- tensors at any address ---------------------------------------------------
+@gpu
+@needs_gpu
+@pytest.mark.parametrize("dtype,d,dv", [(BF, 64, 128), (BF, 40, 20), (F32, 64, 64), (F32, 10, 3)])
+def test_diff_attention_of_unaligned_tensors(dtype, d, dv):
+    """Inputs sliced from a flat buffer, and an upstream gradient that is a slice
+    of the gradient of a concatenation: the same bits as from aligned copies."""
+    ins = diff.inputs(1, 2, 1, 70, d, dv, dtype, ("head", dtype), seed=20)
+    q, k, v, w, do = ins
+    leaves = [t.clone().requires_grad_() for t in (q, k, v, w)]
+    out = fbob.diff_attention(*leaves, causal=True)
+    want = torch.autograd.grad(out, leaves, do)
+    moved = [shifted(t).requires_grad_() for t in (q, k, v, w)]
+    got = fbob.diff_attention(*moved, causal=True)
+    assert torch.equal(got, out)
+    with torch.no_grad():
+        assert torch.equal(fbob.diff_attention(*moved, causal=True), out)
+    assert all(torch.equal(a, b) for a, b in zip(torch.autograd.grad(got, moved, shifted(do)), want))
+    # what autograd hands back behind a cat along batch or heads
+    scalar = torch.zeros(1, dtype=dtype, device="cuda", requires_grad=True)
+    out = fbob.diff_attention(*leaves, causal=True)
+    joined = torch.cat((scalar, out.flatten()))
+    again = torch.autograd.grad(joined, leaves, torch.cat((torch.ones_like(scalar), do.flatten())))
+    assert all(torch.equal(a, b) for a, b in zip(again, want))
