@@ -204,7 +204,7 @@ class _DiffBackward(torch.autograd.Function):
                 t = t.repeat_interleave(G, 1)
             if t.shape[-1] < wide:
                 t = torch.nn.functional.pad(t, (0, wide - t.shape[-1]))
-            return _contig(t)
+            return _b.dense(t)
 
         w = _rows(lam, B, H, N)
         vv, gvv = fit(v, Hk), fit(gv, Hk)
@@ -219,7 +219,7 @@ class _DiffBackward(torch.autograd.Function):
         for m in (0, 1):
             qm, km = fit(q[:, m::2], H), fit(k[:, m::2], Hk)
             om = fit(o2 if m else o1, H)
-            lm = lse[:, m::2].contiguous()
+            lm = _b.dense(lse[:, m::2])  # at B = H = 1 contiguous as it is, at any address
             up = (-w * do.float()).to(dtype) if m else do
             gqm = None if gq is None else fit(gq[:, m::2], H)
             gkm = None if gk is None else fit(gk[:, m::2], Hk)

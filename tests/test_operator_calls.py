@@ -78,3 +78,38 @@ def test_diff_attention_of_unaligned_tensors(dtype, d, dv):
     joined = torch.cat((scalar, out.flatten()))
     again = torch.autograd.grad(joined, leaves, torch.cat((torch.ones_like(scalar), do.flatten())))
     assert all(torch.equal(a, b) for a, b in zip(again, want))
+
+
+# ---- one batch, one head ------------------------------------------------------
+@gpu
+@needs_gpu
+@pytest.mark.parametrize("dtype,N,d,dv,tol", [
+    (F32, 7, 16, 24, 3e-4), (F32, 13, 10, 3, 3e-4), (F32, 50, 64, 64, 3e-4),
+    (BF, 50, 64, 64, 4e-2), (BF, 131, 20, 12, 4e-2)])
+@pytest.mark.parametrize("lam", ["one", "row"])
+def test_second_derivative_of_one_head(dtype, N, d, dv, tol, lam):
+    """B = H = 1, where a map's slice of the log-sum-exps is contiguous as it
+    is, at any offset.  Cotangents come as slices of a flat buffer.  Bounds as
+    for more heads: 3e-4 and 4e-2 of each result's largest value; lam's
+    gradient in bf16 is a sum that cancels, held by the sum of magnitudes."""
+    args = diff.inputs(1, 1, 1, N, d, dv, dtype, (lam, dtype), seed=22)
+    g = torch.Generator("cuda").manual_seed(23)
+    cots = [0.5 * torch.randn(t.shape, generator=g, device="cuda").to(dtype) for t in args[:4]]
+    got = second([shifted(t) for t in args], [shifted(c) for c in cots],
+                 lambda *a: fbob.diff_attention(*a, causal=True))
+    want = second([t.double() for t in args], [c.double() for c in cots],
+                  lambda *a: dense_diff(*a, True))
+    for name, a, b in zip(("q", "k", "v", "lam", "do"), got, want):
+        err, top = (a.double() - b).abs().max(), b.abs().max()
+        if name == "lam":
+            # -sum dO . U, U the gradient in the second map's upstream
+            x = [t.double() for t in args]
+            lo, up = [c.double() for c in cots], -(x[3][:, None] if x[3].dim() == 1 else x[3])
+            up = up.expand(1, 1, N)[..., None] * x[4]
+            lo[0], lo[1] = lo[0][:, 1:], lo[1][:, 1:]
+            U = second([x[0][:, 1:], x[1][:, 1:], x[2], up], lo[:3], lambda *a: dense_attention(*a, True))[3]
+            mag = x[4].abs().sum(-1)
+            mag = mag.sum() if lam == "one" else mag.max()
+            assert err <= tol * U.abs().max() * mag + 2.0 ** -8 * top, (name, err.item())
+        else:
+            assert err <= tol * top, (name, err.item(), top.item())
