@@ -14,8 +14,9 @@ with respect to Q, K, V and dO, including the paths through O and LSE.
 The forward's O and LSE therefore enter the backward node as detached
 values, so those paths are not counted a second time.
 
-Every step runs in the CUDA library.  Tensors are [B, H, N, d], contiguous,
-bf16 or fp32, on one CUDA device.  There is no CPU path: anything else raises.
+Every step runs in the CUDA library.  Tensors are [B, H, N, d], bf16 or fp32,
+on one CUDA device; those that are not contiguous, or not at a 16-byte boundary,
+are copied first.  There is no CPU path: anything else raises.
 """
 from __future__ import annotations
 
@@ -24,16 +25,12 @@ import torch
 from . import _binding as _b
 
 
-def _contig(t: torch.Tensor) -> torch.Tensor:
-    return t if t.is_contiguous() else t.contiguous()
-
-
 class _AttentionBackward(torch.autograd.Function):
     """(q, k, v, dO) -> (dQ, dK, dV); its own backward is fbob_bob."""
 
     @staticmethod
     def forward(ctx, q, k, v, do, o, lse, causal, scale):
-        do = _contig(do)
+        do = _b.dense(do)
         dq, dk, dv = _b.backward(q, k, v, o, lse, do, causal, scale)
         ctx.save_for_backward(q, k, v, do, o, lse)
         ctx.causal, ctx.scale = causal, scale
@@ -47,7 +44,7 @@ class _AttentionBackward(torch.autograd.Function):
         q, k, v, do, o, lse = ctx.saved_tensors
         if gq is None and gk is None and gv is None:
             return None, None, None, None, None, None, None, None
-        gq, gk, gv = (None if g is None else _contig(g) for g in (gq, gk, gv))
+        gq, gk, gv = (None if g is None else _b.dense(g) for g in (gq, gk, gv))
         gradq, gradk, gradv, graddo = _b.bob(q, k, v, o, lse, do, gq, gk, gv,
                                              ctx.causal, ctx.scale)
         return gradq, gradk, gradv, graddo, None, None, None, None
@@ -81,7 +78,7 @@ def attention(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, causal: bool = 
     for name, t in (("q", q), ("k", k), ("v", v)):
         if not t.is_cuda:
             raise _b.FbobError(1, f"attention: {name} must be a CUDA tensor")
-    q, k, v = _contig(q), _contig(k), _contig(v)
+    q, k, v = _b.dense(q), _b.dense(k), _b.dense(v)
     if scale is None:
         scale = 1.0 / float(q.shape[-1]) ** 0.5
     return _Attention.apply(q, k, v, bool(causal), float(scale))

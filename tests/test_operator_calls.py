@@ -80,6 +80,29 @@ def test_diff_attention_of_unaligned_tensors(dtype, d, dv):
     assert all(torch.equal(a, b) for a, b in zip(again, want))
 
 
+@gpu
+@needs_gpu
+@pytest.mark.parametrize("dtype,d", [(BF, 64), (F32, 10)])
+def test_attention_of_unaligned_tensors(dtype, d):
+    """Plain attention likewise, through its second derivative."""
+    g = torch.Generator("cuda").manual_seed(21)
+    q, k, v, do, gq, gk, gv = (torch.randn(1, 2, 70, d, generator=g, device="cuda").to(dtype)
+                               for _ in range(7))
+
+    def grads(args, up, cots):
+        leaves = [t.requires_grad_() for t in args]
+        up = up.requires_grad_()
+        out = fbob.attention(*leaves, causal=True)
+        first = torch.autograd.grad(out, leaves, up, create_graph=True)
+        return (out, *first, *torch.autograd.grad(first, leaves + [up], cots))
+
+    want = grads([t.clone() for t in (q, k, v)], do.clone(), [gq, gk, gv])
+    got = grads([shifted(t) for t in (q, k, v)], shifted(do), [shifted(t) for t in (gq, gk, gv)])
+    assert torch.equal(got[0], want[0])
+    for a, b in zip(got[1:], want[1:]):  # (sums of bf16 dQ and gradQ have no fixed order)
+        torch.testing.assert_close(a.float(), b.float(), rtol=2.0 ** -7, atol=1e-3)
+
+
 # ---- one batch, one head ------------------------------------------------------
 @gpu
 @needs_gpu
