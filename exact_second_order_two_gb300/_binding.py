@@ -13,6 +13,7 @@ import math
 import os
 
 import torch
+from torch.autograd import forward_ad
 
 from .build import LIB_PATH
 
@@ -145,6 +146,19 @@ def dense(t: torch.Tensor) -> torch.Tensor:
     if t.is_contiguous() and t.data_ptr() % 16 == 0:
         return t
     return t.clone(memory_format=torch.contiguous_format)
+
+
+def dual(*tensors) -> bool:
+    """Whether one of them carries a forward-mode tangent.  None of the
+    operators has a forward-mode derivative: a call that would drop the tangent
+    goes through its autograd function instead, which refuses it."""
+    return any(forward_ad.unpack_dual(t).tangent is not None for t in tensors if t is not None)
+
+
+def refuse_dual(what: str, *tensors) -> None:
+    """Raises where a call that autograd does not see would drop a tangent."""
+    if dual(*tensors):
+        raise NotImplementedError(f"{what} has no forward-mode derivative")
 
 
 def _check_tensors(ref: torch.Tensor, named: dict, scalar_names=()):

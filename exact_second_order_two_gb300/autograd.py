@@ -44,6 +44,7 @@ class _AttentionBackward(torch.autograd.Function):
         q, k, v, do, o, lse = ctx.saved_tensors
         if gq is None and gk is None and gv is None:
             return None, None, None, None, None, None, None, None
+        _b.refuse_dual("attention's second derivative", gq, gk, gv)
         gq, gk, gv = (None if g is None else _b.dense(g) for g in (gq, gk, gv))
         gradq, gradk, gradv, graddo = _b.bob(q, k, v, o, lse, do, gq, gk, gv,
                                              ctx.causal, ctx.scale)
@@ -73,7 +74,8 @@ def attention(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, causal: bool = 
     """Softmax attention whose first and second derivatives run in the
     library: O = softmax(scale * q k^T, masked to j <= i when causal) v.
 
-    scale defaults to 1/sqrt(d) and is not differentiated.
+    scale defaults to 1/sqrt(d) and is not differentiated.  Derivatives are
+    reverse-mode; forward-mode ones raise NotImplementedError.
     """
     for name, t in (("q", q), ("k", k), ("v", v)):
         if not t.is_cuda:

@@ -191,6 +191,7 @@ class _DiffBackward(torch.autograd.Function):
         none = (None,) * 4
         if gq is None and gk is None and gv is None and glam is None:
             return (None,) * 5 + none
+        _b.refuse_dual("diff_attention's second derivative", gq, gk, gv, glam)
         B, H2, N, d = q.shape
         H, Hk, dv = H2 // 2, v.shape[1], v.shape[3]
         G, wide = H // Hk, max(d, dv)
@@ -265,7 +266,7 @@ class _DiffAttention(torch.autograd.Function):
         q, k, v, lam, o, rest, lse = ctx.saved_tensors
         # o, rest and lse enter as values: the second derivative's paths through
         # them are part of what fbob_bob returns
-        if torch.is_grad_enabled():
+        if torch.is_grad_enabled() or _b.dual(do):
             grads = _DiffBackward.apply(q, k, v, lam, do, o.detach(), rest, lse, ctx.shp)
         else:
             grads = _backward(ctx.shp, q, k, v, lam, o, rest, lse, _b.dense(do))
@@ -281,7 +282,8 @@ def diff_attention(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, lam: torch
     q [B, 2H, N, d], k [B, 2Hk, N, d], v [B, Hk, N, dv] and lam as for
     ``diff_forward`` (inputs that are not contiguous, or not at a 16-byte
     boundary, are copied first).  Returns
-    [B, H, N, dv].  Differentiable twice in q, k, v and lam; scale is not
+    [B, H, N, dv].  Differentiable twice in q, k, v and lam, in reverse mode
+    (forward-mode derivatives raise NotImplementedError); scale is not
     differentiated.  Backward passes can be captured into a CUDA graph together
     with their forward, from leaves that no live eager graph was built from
     (autograd would tie the capture to that graph's stream).
@@ -290,8 +292,8 @@ def diff_attention(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, lam: torch
         raise TypeError(f"lam must be a tensor, got {type(lam).__name__}")
     q, k, v, lam = _b.dense(q), _b.dense(k), _b.dense(v), _contig(lam)
     shp = _shape(q, k, v, lam, causal, scale)
-    if torch.is_grad_enabled() and (q.requires_grad or k.requires_grad or v.requires_grad
-                                    or lam.requires_grad):
+    if (torch.is_grad_enabled() and (q.requires_grad or k.requires_grad or v.requires_grad
+                                     or lam.requires_grad)) or _b.dual(q, k, v, lam):
         return _DiffAttention.apply(q, k, v, lam, shp)
     # no backward can follow: rest is not written
     return _forward(shp, q, k, v, lam, False)[0]

@@ -107,7 +107,7 @@ class _Rotary(torch.autograd.Function):
     @staticmethod
     def backward(ctx, dy):
         inv_freq, positions = ctx.saved_tensors
-        turn = _Rotary.apply if torch.is_grad_enabled() else _turn
+        turn = _Rotary.apply if torch.is_grad_enabled() or _b.dual(dy) else _turn
         return turn(dy, inv_freq, positions, ctx.how, ctx.strides), None, None, None, None
 
 
@@ -124,7 +124,8 @@ def rotary(x: torch.Tensor, inv_freq: torch.Tensor, positions=None, *, interleav
     frequencies (``rotary_frequencies``), not differentiated.  positions:
     None (0 .. N-1), an int (that position on), or an int64 CUDA tensor
     [N] or [B, N].  Returns a dense [B, H, N, d] tensor of ``dtype`` (default
-    x.dtype), differentiable in x to any order.
+    x.dtype), differentiable in x to any order in reverse mode; forward-mode
+    derivatives raise NotImplementedError.
     """
     if not x.is_cuda:
         raise _b.FbobError(1, "rotary: x must be a CUDA tensor")
@@ -135,7 +136,7 @@ def rotary(x: torch.Tensor, inv_freq: torch.Tensor, positions=None, *, interleav
         raise TypeError(f"unsupported dtypes {x.dtype}, {dtype}; use bfloat16 or float32")
     if inv_freq.dtype != torch.float64 or inv_freq.dim() != 1 or inv_freq.device != x.device:
         raise ValueError(f"inv_freq must be a float64 vector on {x.device}")
-    if inv_freq.requires_grad:
+    if inv_freq.requires_grad or _b.dual(inv_freq):
         raise ValueError("inv_freq is not differentiated: pass it detached")
     if 2 * inv_freq.numel() > x.shape[-1]:
         raise ValueError(f"inv_freq turns {2 * inv_freq.numel()} features of {x.shape[-1]}")
@@ -155,6 +156,8 @@ def rotary(x: torch.Tensor, inv_freq: torch.Tensor, positions=None, *, interleav
             positions = positions.expand(B, N)
         if positions.stride(1) != 1 and N > 1:
             positions = positions.contiguous()
-    turn = _Rotary.apply if x.requires_grad and torch.is_grad_enabled() else _turn
+    # without autograd's node where no derivative can follow
+    seen = (x.requires_grad and torch.is_grad_enabled()) or _b.dual(x)
+    turn = _Rotary.apply if seen else _turn
     how = (offset, bool(interleaved), float(magnitude), dtype, False)
     return turn(x, inv_freq, positions, how, None)

@@ -136,3 +136,68 @@ def test_second_derivative_of_one_head(dtype, N, d, dv, tol, lam):
             assert err <= tol * U.abs().max() * mag + 2.0 ** -8 * top, (name, err.item())
         else:
             assert err <= tol * top, (name, err.item(), top.item())
+
+
+# ---- forward-mode derivatives ---------------------------------------------------
+@gpu
+@needs_gpu
+class TestForwardMode:
+    """Neither operator has a forward-mode derivative: it is refused, and a
+    tangent never dropped."""
+
+    def test_rotary(self):
+        x = torch.randn(1, 2, 5, 64, device="cuda")
+        f, _ = fbob.rotary_frequencies(64)
+        t = torch.randn_like(x)
+        with torch.autograd.forward_ad.dual_level():
+            dual = torch.autograd.forward_ad.make_dual(x, t)
+            with pytest.raises(NotImplementedError):
+                fbob.rotary(dual, f)
+            with torch.no_grad(), pytest.raises(NotImplementedError):
+                fbob.rotary(dual, f)
+            with pytest.raises(ValueError):  # frequencies are not differentiated
+                fbob.rotary(x, torch.autograd.forward_ad.make_dual(f, torch.ones_like(f)))
+            y = fbob.rotary(x, f)  # no tangent, none lost
+            assert torch.autograd.forward_ad.unpack_dual(y).tangent is None
+            # forward over reverse
+            leaf = x.clone().requires_grad_()
+            y = fbob.rotary(leaf, f)
+            up = torch.autograd.forward_ad.make_dual(torch.ones_like(y), t)
+            with pytest.raises(NotImplementedError):
+                torch.autograd.grad(y, leaf, up)
+        with pytest.raises((NotImplementedError, RuntimeError)):
+            torch.func.jvp(lambda a: fbob.rotary(a, f), (x,), (t,))
+
+    @pytest.mark.parametrize("which", range(4))
+    def test_diff_attention(self, which):
+        args = list(diff.inputs(1, 2, 1, 9, 16, 24, F32, ("head", F32), seed=24))
+        do = args.pop()
+        t = torch.ones_like(args[which])
+        with torch.autograd.forward_ad.dual_level():
+            dual = list(args)
+            dual[which] = torch.autograd.forward_ad.make_dual(args[which], t)
+            with pytest.raises(NotImplementedError):
+                fbob.diff_attention(*dual)
+            with torch.no_grad(), pytest.raises(NotImplementedError):
+                fbob.diff_attention(*dual)
+            leaves = [a.clone().requires_grad_() for a in args]
+            out = fbob.diff_attention(*leaves)
+            up = torch.autograd.forward_ad.make_dual(do, torch.ones_like(do))
+            with pytest.raises(NotImplementedError):
+                torch.autograd.grad(out, leaves, up)
+        with pytest.raises((NotImplementedError, RuntimeError)):
+            torch.func.jvp(lambda a: fbob.diff_attention(*args[:which], a, *args[which + 1:]),
+                           (args[which],), (t,))
+
+    @pytest.mark.parametrize("op", ["attention", "differential"])
+    def test_second_derivative(self, op):
+        """A tangent on the cotangent of a first gradient."""
+        q, k, v, w, do = diff.inputs(1, 1, 1, 9, 16, 16, F32, ("head", F32), seed=25)
+        args = (q, k, v, w) if op == "differential" else (q[:, :1].clone(), k[:, :1].clone(), v)
+        fn = fbob.diff_attention if op == "differential" else fbob.attention
+        leaves = [a.clone().requires_grad_() for a in args]
+        first = torch.autograd.grad(fn(*leaves), leaves, do, create_graph=True)
+        with torch.autograd.forward_ad.dual_level():
+            c = torch.autograd.forward_ad.make_dual(torch.ones_like(first[0]), torch.ones_like(first[0]))
+            with pytest.raises(NotImplementedError):
+                torch.autograd.grad(first[0], leaves, c, allow_unused=True)
