@@ -201,3 +201,44 @@ class TestForwardMode:
             c = torch.autograd.forward_ad.make_dual(torch.ones_like(first[0]), torch.ones_like(first[0]))
             with pytest.raises(NotImplementedError):
                 torch.autograd.grad(first[0], leaves, c, allow_unused=True)
+
+
+# ---- roundings of the second derivative -----------------------------------------
+@gpu
+@needs_gpu
+@pytest.mark.parametrize("kind", ["one", "head"])
+@pytest.mark.parametrize("d,dv", [(20, 12), (40, 80)])
+def test_second_derivative_scales_with_lam(kind, d, dv):
+    """The second map's part of a second derivative in q is lam times that at
+    lam = 1, rounded once: 0.75 R, with R in bf16 already."""
+    q, k, v, w, do = diff.inputs(1, 2, 2, 150, d, dv, BF, (kind, BF), seed=26)
+    c = torch.randn(q.shape, generator=torch.Generator("cuda").manual_seed(27), device="cuda").to(BF)
+
+    def grad_q2(value):
+        return second((q, k, v, torch.full_like(w, value), do), (c, None, None, None),
+                      lambda *a: fbob.diff_attention(*a, causal=True))[0][:, 1::2]
+
+    assert torch.equal(grad_q2(0.75), (0.75 * grad_q2(1.0).float()).to(BF))
+
+
+@gpu
+@needs_gpu
+def test_second_derivative_in_the_upstream_gradient_rounds_once():
+    """A loss of dlam alone, sum g dlam: its gradient in dO is -g O2.  On CUDA
+    cores O2 is as good as fp32 before it is rounded, and what the rounding left
+    off is kept, so -g O2 is off by half a step of bf16 (2^-8), by the square of
+    one, and by sums of 32 bits: N + d + 20 steps of 2^-24 of P |V|."""
+    N, d, dv = 90, 20, 12
+    q, k, v, w, do = diff.inputs(1, 2, 2, N, d, dv, BF, ("row", F32), seed=28)
+    g = torch.Generator("cuda").manual_seed(29)
+    c = torch.randn(w.shape, generator=g, device="cuda")
+    got = second((q, k, v, w, do), (None, None, None, c), lambda *a: fbob.diff_attention(*a))[4]
+    s = q[:, 1::2].double() @ k[:, 1::2].double().transpose(-1, -2) / math.sqrt(d)
+    P = torch.softmax(s, -1)
+    want = -c.double()[..., None] * (P @ v.double())
+    mag = c.double().abs()[..., None] * (P @ v.double().abs())
+    smax = (q.double().abs() @ k.double().abs().transpose(-1, -2)).max().item() / math.sqrt(d)
+    small = 2.0 ** -24 * (N + 2 * (d + 4) * smax + 20) + 2.0 ** -16
+    bound = 2.0 ** -8 * (want.abs() + small * mag) + small * mag
+    err = (got.double() - want).abs()
+    assert (err <= bound).all(), (err / bound).max().item()
