@@ -12,6 +12,7 @@ longer than those a model was trained on.
 from __future__ import annotations
 
 import math
+import operator
 import struct
 
 import torch
@@ -37,7 +38,7 @@ def rotary_frequencies(rotary_dim: int, base: float = 10000.0, scaling: str | No
                 magnitude is 0.1 ln(factor) + 1
     Returns (float64 tensor [rotary_dim / 2] on ``device``, magnitude).
     """
-    r = int(rotary_dim)
+    r = operator.index(rotary_dim)
     if r < 2 or r % 2:
         raise ValueError(f"rotary_dim must be even and at least 2, got {rotary_dim}")
     if not (base > 0 and math.isfinite(base)):
@@ -144,7 +145,7 @@ def rotary(x: torch.Tensor, inv_freq: torch.Tensor, positions=None, *, interleav
         inv_freq = inv_freq.contiguous()
     offset = 0
     if positions is not None and not torch.is_tensor(positions):
-        offset, positions = int(positions), None
+        offset, positions = operator.index(positions), None
         if not -(1 << 62) <= offset < 1 << 62:
             raise ValueError(f"position {offset} is out of range")
     if positions is not None:

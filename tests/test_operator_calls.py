@@ -242,3 +242,19 @@ def test_second_derivative_in_the_upstream_gradient_rounds_once():
     bound = 2.0 ** -8 * (want.abs() + small * mag) + small * mag
     err = (got.double() - want).abs()
     assert (err <= bound).all(), (err / bound).max().item()
+
+
+# ---- positions -------------------------------------------------------------------
+@gpu
+@needs_gpu
+def test_rotary_refuses_a_fractional_position():
+    x = torch.randn(1, 2, 5, 64, device="cuda")
+    f, _ = fbob.rotary_frequencies(64)
+    for bad in (2.5, 2.0, "2"):
+        with pytest.raises(TypeError):
+            fbob.rotary(x, f, bad)
+
+
+def test_frequencies_refuse_a_fractional_width():
+    with pytest.raises(TypeError):
+        fbob.rotary_frequencies(64.5, device="cpu")
