@@ -26,6 +26,7 @@
 #include <math.h>
 
 #include "common.cuh"
+#include "diff_rows.h"
 #include "internal.h"
 #include "ops.h"
 
@@ -558,10 +559,8 @@ __global__ void __launch_bounds__(SPLIT * kThreads) diff_bwd_col(Args a) {
     const size_t bh = (size_t)b * a.H + h;
     const T* q = static_cast<const T*>(a.q) + bh * 2 * qsz;
     const T* dO = static_cast<const T*>(a.dO) + bh * N * a.dv_;
-    // the part's rows of this head
-    const int first = start + max(t0 - g * per_head, 0) * kT;
-    const int end = min(N, start + (t1 - g * per_head) * kT);
-    for (int i0 = first + grp * kT; i0 < end; i0 += SPLIT * kT) {
+    const RowRange rows = part_rows(t0, t1, g, per_head, start, N, kT);
+    for (int i0 = rows.first + grp * kT; i0 < rows.end; i0 += SPLIT * kT) {
       group_sync<SPLIT>(grp);
       load_rows<kT>(tid, qs, ld, q, i0, N, a.d);
       load_rows<kT>(tid, qs + kT * ld, ld, q + qsz, i0, N, a.d);
