@@ -37,7 +37,8 @@ int check_shape(const fbob_diff_shape_t* s, DiffProblem* out) {
   if (s->B < 1 || s->H < 1 || s->Hk < 1 || s->N < 1 || s->d < 1 || s->dv < 1 || s->H % s->Hk)
     return FBOB_ERR_INVALID_ARG;
   if (s->causal != 0 && s->causal != 1) return FBOB_ERR_INVALID_ARG;
-  if (!(s->scale > 0.f) || s->scale > 3.0e38f) return FBOB_ERR_INVALID_ARG;
+  // (the kernels take scale log2 e, which is finite then)
+  if (!(s->scale > 0.f) || s->scale > 2.0e38f) return FBOB_ERR_INVALID_ARG;
   if (s->lam_kind < FBOB_LAM_ONE || s->lam_kind > FBOB_LAM_ROW) return FBOB_ERR_INVALID_ARG;
   for (int dt : {s->dtype, s->lam_dtype})
     if (dt != FBOB_BF16 && dt != FBOB_FP32) return FBOB_ERR_UNSUPPORTED;

@@ -111,8 +111,8 @@ def diff_forward(q, k, v, lam, causal: bool = False, scale: float | None = None,
     (query head h reads key head h // (H / Hk)); bf16 or fp32, contiguous and at
     16-byte boundaries, d and dv up to 128 (bf16 multiples of 8 run on the tensor
     cores).
-    lam: no dimensions, [H] or [B, H, N], bf16 or fp32.  scale > 0 defaults to
-    1/sqrt(d); with ``causal`` key j is visible to query i iff j <= i.  A key
+    lam: no dimensions, [H] or [B, H, N], bf16 or fp32.  scale, above 0 and up to 2e38,
+    defaults to 1/sqrt(d); with ``causal`` key j is visible to query i iff j <= i.  A key
     whose score is -inf has no weight; but as in the dense product, an infinite
     or NaN value reaches rows that give it none (0 times it is NaN): v and
     upstream gradients are to be finite in padded rows too.

@@ -258,7 +258,7 @@ int fbob_rotary(const fbob_rotary_t* r, const void* x, const double* inv_freq,
  * R = 3 for bf16: P^2 V, what its rounding left off, and what o's rounding
  * left off.  H is a multiple of Hk: query head h reads key head h / (H / Hk).
  * lam is one value, [H], or [B,H,N], bf16 or fp32.  Masking, ownership,
- * asynchrony and alignment as above (lam to its own size); scale > 0.
+ * asynchrony and alignment as above (lam to its own size); 0 < scale <= 2e38.
  * 1 <= d, dv <= 128, B*H <= 32767.  bf16 at d and dv that are multiples of 8
  * runs the tensor-core kernels, the rest runs on CUDA cores (fbob_diff_path).
  * Every output is summed in a fixed order: equal inputs give equal bits. */

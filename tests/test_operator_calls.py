@@ -258,3 +258,32 @@ def test_rotary_refuses_a_fractional_position():
 def test_frequencies_refuse_a_fractional_width():
     with pytest.raises(TypeError):
         fbob.rotary_frequencies(64.5, device="cpu")
+
+
+# ---- scale -----------------------------------------------------------------------
+def test_scale_up_to_its_limit():
+    """scale log2 e, which the kernels multiply with, is to be finite."""
+    import ctypes
+
+    lib = fbob.lib()
+    for scale, ok in ((2.0e38, True), (2.4e38, False), (3.0e38, False), (1e-30, True)):
+        assert (lib.fbob_diff_workspace_size(0, ctypes.byref(diff.shape(scale=scale))) > 0) == ok
+
+
+@gpu
+@needs_gpu
+@pytest.mark.parametrize("dtype", [BF, F32])
+@pytest.mark.parametrize("scale", [2.0e38, 1e-30])
+def test_extreme_scales_of_zero_scores(dtype, scale):
+    """Queries of zeros: every score is 0 at any scale, and a row the mean of
+    the values it sees, up to roundings (half a step of the type, and for P)."""
+    q, k, v, w, do = diff.inputs(1, 2, 1, 130, 64, 64, dtype, ("head", dtype), seed=33)
+    got = fbob.diff_attention(torch.zeros_like(q), k, v, w, causal=True, scale=scale)
+    n = torch.arange(1, 131, device="cuda")[:, None]
+    mean, mag = v.double().cumsum(2) / n, v.double().abs().cumsum(2) / n
+    ww = w.double()[:, None, None]
+    h = torch.finfo(dtype).eps / 2 if dtype == BF else 0
+    err = (h + 200 * 2.0 ** -24) * (1 + ww.abs()) * mag
+    want = (1 - ww) * mean
+    err = err + torch.finfo(dtype).eps / 2 * (want.abs() + err)
+    assert ((got.double() - want).abs() <= err).all()
