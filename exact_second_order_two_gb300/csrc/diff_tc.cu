@@ -419,16 +419,19 @@ __global__ void __launch_bounds__(kFwdThreads, 1)
     for (int t = 0; t < T; ++t) {
       const int j0 = t * C::BN;
       // for the MMA warp: what it reads after this warp's arrivals has landed
-      if (C::ONE) {
-        if (warp == 0 && t + 1 < T)
-          await(v_full + (t + 1) % C::VS, ((t + 1) / C::VS) & 1, ab, prm.status);
-      } else if (quad == 0) {
+      if (C::ONE && warp == 0 && t + 1 < T)
+        await(v_full + (t + 1) % C::VS, ((t + 1) / C::VS) & 1, ab, prm.status);
+      await(s_full + m, t & 1, ab, prm.status);
+      tc_fence_after();
+      // K^m behind the scores, no earlier: they tell that the slot's load before
+      // this one has landed (its products were issued before them).  One phase
+      // short of the awaited one the parity reads as if that were over, and the
+      // products would take keys that are still on their way.
+      if (!C::ONE && quad == 0) {
         const int u = 2 * (t + 1) + m;
         if (m == 0) await(v_full + t % C::VS, (t / C::VS) & 1, ab, prm.status);
         if (t + 1 < T) await(k_full + u % C::KS, (u / C::KS) & 1, ab, prm.status);
       }
-      await(s_full + m, t & 1, ab, prm.status);
-      tc_fence_after();
       uint32_t s[4][32];
       tmem_ld32x4(ts, ts + 32, ts + 64, ts + 96, s[0], s[1], s[2], s[3]);
       // masked entries become -inf, so they give 2^-inf = 0 below

@@ -2,13 +2,15 @@
 (csrc/diff_tc.cu), explored on the CPU over every order in which their roles
 can run.
 
-A model of one thread block: a producer, an MMA issuer, the tensor pipe (which
-runs what is issued in order, at any later time) and two elementwise warps, one
-of which may fall behind the other without limit.  mbarriers behave as on the
+A model of one thread block: a producer whose loads land at any later time and
+in any order, an MMA issuer, the tensor pipe (which runs what is issued in order,
+at any later time) and two elementwise warps, one of which may fall behind the
+other without limit.  mbarriers behave as on the
 device: a wait knows its phase by parity only, and an arrival counts for
 whatever phase is current.  Every reachable state is held to:
-  - a waiter finds its barrier in the awaited phase or the one after, never
-    further on (two phases ahead it would wait for what cannot come);
+  - a waiter finds its barrier in the awaited phase or the one after: further on
+    it would wait for what cannot come, and one phase short of it the parity
+    reads as if the awaited phase were over;
   - an arrival for tile a lands in the phase of tile a;
   - products and warps find in tensor memory and in the ring of stages what
     the tile they work on put there;
@@ -27,13 +29,14 @@ def explore(roles, counts):
     """Runs `roles` (name -> list of steps) in every order.  Steps:
       ("wait", bar, n)         until phase n of bar has completed
       ("arrive", bar, n)       one of counts[bar] arrivals of phase n
+      ("load", bar, n, writes) a copy, which arrives when it lands
       ("issue", reads, writes) a product, run later in order by the pipe
       ("commit", bar, n)       an arrival behind everything issued before
       ("read", cell, value) and ("write", cell, value)
     Returns the number of states."""
     names = list(roles)
     bars = list(counts)
-    start = (tuple(0 for _ in names), tuple((0, 0) for _ in bars), (), frozenset())
+    start = (tuple(0 for _ in names), tuple((0, 0) for _ in bars), (), frozenset(), frozenset())
     at = {b: i for i, b in enumerate(bars)}
     seen, todo = {start}, [start]
 
@@ -52,7 +55,7 @@ def explore(roles, counts):
                 raise Violation(f"{who}: {cell} holds {cells.get(cell)}, not {value}")
 
     while todo:
-        pcs, bs, queue, mem = todo.pop()
+        pcs, bs, queue, mem, flying = todo.pop()
         cells = dict(mem)
         out = []
         for r, name in enumerate(names):
@@ -60,15 +63,18 @@ def explore(roles, counts):
                 continue
             step = roles[name][pcs[r]]
             kind = step[0]
-            nbs, nq, nm = bs, queue, mem
+            nbs, nq, nm, nf = bs, queue, mem, flying
             if kind == "wait":
                 done = bs[at[step[1]]][0]
-                if done > step[2] + 1:
+                if done not in (step[2], step[2] + 1):
                     raise Violation(f"{name} waits for phase {step[2]} of {step[1]}, which is in {done}")
-                if done <= step[2]:
+                if done == step[2]:
                     continue
             elif kind == "arrive":
                 nbs = arrive(bs, step[1], step[2])
+            elif kind == "load":
+                nf = flying | {(r, pcs[r])}
+                nm = frozenset({**cells, **{cell: "on its way" for cell, _ in step[3]}}.items())
             elif kind in ("issue", "commit"):
                 nq = queue + ((r, pcs[r]),)
             elif kind == "read":
@@ -77,7 +83,11 @@ def explore(roles, counts):
                 new = dict(cells)
                 new[step[1]] = step[2]
                 nm = frozenset(new.items())
-            out.append((pcs[:r] + (pcs[r] + 1,) + pcs[r + 1:], nbs, nq, nm))
+            out.append((pcs[:r] + (pcs[r] + 1,) + pcs[r + 1:], nbs, nq, nm, nf))
+        for role, pc in flying:
+            _, bar, n, writes = roles[names[role]][pc]
+            out.append((pcs, arrive(bs, bar, n), queue, frozenset({**cells, **dict(writes)}.items()),
+                        flying - {(role, pc)}))
         if queue:
             role, pc = queue[0]
             step, nbs, nm = roles[names[role]][pc], bs, mem
@@ -88,7 +98,7 @@ def explore(roles, counts):
                 new = dict(cells)
                 new.update(step[2])
                 nm = frozenset(new.items())
-            out.append((pcs, nbs, queue[1:], nm))
+            out.append((pcs, nbs, queue[1:], nm, flying))
         if not out and any(pcs[r] < len(roles[n]) for r, n in enumerate(names)):
             stuck = [f"{n}: {roles[n][pcs[r]]}" for r, n in enumerate(names) if pcs[r] < len(roles[n])]
             raise Violation("nothing can run: " + "; ".join(stuck))
@@ -110,7 +120,7 @@ def producer(T, stages):
     for a in range(T):
         if a >= stages:
             steps.append(("wait", ("empty", a % stages), a // stages - 1))
-        steps += [("write", ("tile", a % stages), a), ("arrive", ("full", a % stages), a // stages)]
+        steps.append(("load", ("full", a % stages), a // stages, ((("tile", a % stages), a),)))
     return steps
 
 
@@ -238,7 +248,7 @@ def row(T, k_stages=3, v_stages=2):
             load.append(("wait", ("v_empty", t % v_stages), t // v_stages - 1))
         if t >= k_stages:
             load.append(("wait", ("k_empty", t % k_stages), t // k_stages - 1))
-        load += [("write", *v(t)), ("write", *k(t)), ("arrive", ("full", t % k_stages), t // k_stages)]
+        load.append(("load", ("full", t % k_stages), t // k_stages, (v(t), k(t))))
     roles = {"producer": load, "mma": mma}
     for w in range(WARPS):
         steps = []
@@ -256,10 +266,11 @@ def row(T, k_stages=3, v_stages=2):
     return roles, counts
 
 
-def forward(T, one, k_stages=None, v_stages=None):
-    """Warp m holds map m's rows.  one: a stage holds K^1, K^2 and V."""
-    vs = v_stages or (3 if one else 2)
-    ks = k_stages or 3
+def forward(T, one, early=False):
+    """Warp m holds map m's rows.  one: a stage holds K^1, K^2 and V; otherwise
+    a ring of three K^m and one of two V, whose loads a warp awaits behind its
+    scores (early: before them)."""
+    vs, ks = 3 if one else 2, 3
 
     def k(t, m):
         return (("v", t % vs), t) if one else (("k", (2 * t + m) % ks), 2 * t + m)
@@ -290,25 +301,27 @@ def forward(T, one, k_stages=None, v_stages=None):
             for u in (2 * t, 2 * t + 1):
                 if u >= ks:
                     load.append(("wait", ("k_empty", u % ks), u // ks - 1))
-                load += [("write", ("k", u % ks), u), ("arrive", ("k_full", u % ks), u // ks)]
+                load.append(("load", ("k_full", u % ks), u // ks, ((("k", u % ks), u),)))
         if t >= vs:
             load.append(("wait", ("v_empty", t % vs), t // vs - 1))
-        load += [("write", ("v", t % vs), t), ("arrive", ("v_full", t % vs), t // vs)]
+        load.append(("load", ("v_full", t % vs), t // vs, ((("v", t % vs), t),)))
     roles = {"producer": load, "mma": mma}
     for m in (0, 1):
         steps = []
         for t in range(T):
+            loads = []
             if one:
                 if m == 0 and t + 1 < T:
-                    steps.append(("wait", ("v_full", (t + 1) % vs), (t + 1) // vs))
+                    loads.append(("wait", ("v_full", (t + 1) % vs), (t + 1) // vs))
             else:
                 u = 2 * (t + 1) + m
                 if m == 0:
-                    steps.append(("wait", ("v_full", t % vs), t // vs))
+                    loads.append(("wait", ("v_full", t % vs), t // vs))
                 if t + 1 < T:
-                    steps.append(("wait", ("k_full", u % ks), u // ks))
-            steps += [("wait", ("s_full", m), t), ("read", ("S", m), ("S", t, 0)),
-                      ("read", ("Sb", m), ("S", t, 1))]
+                    loads.append(("wait", ("k_full", u % ks), u // ks))
+            scores = [("wait", ("s_full", m), t)]
+            steps += loads + scores if one or early else scores + loads
+            steps += [("read", ("S", m), ("S", t, 0)), ("read", ("Sb", m), ("S", t, 1))]
             if t > 0:  # O is rescaled where the maximum moves
                 steps.append(("read", ("O", m), t - 1))
             steps += [("write", ("S", m), ("P", t, 0)), ("arrive", ("p_full", m, 0), t),
@@ -338,6 +351,14 @@ def test_one_barrier_for_two_buffers_is_found(s2_full, ds2_full):
     arrival for the next tile counts for this one."""
     with pytest.raises(Violation):
         explore(*column_narrow(5, s2_full=s2_full, ds2_full=ds2_full))
+
+
+def test_a_load_awaited_too_early_is_found():
+    """Before its scores a warp does not know that the ring slot's earlier load
+    has landed: the parity of the phase before the awaited one is that of the
+    phase after it, and the wait returns with the keys still on their way."""
+    with pytest.raises(Violation, match="k_full"):
+        explore(*forward(5, False, early=True))
 
 
 def test_planted_mistakes_are_found():

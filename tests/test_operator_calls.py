@@ -287,3 +287,38 @@ def test_extreme_scales_of_zero_scores(dtype, scale):
     want = (1 - ww) * mean
     err = err + torch.finfo(dtype).eps / 2 * (want.abs() + err)
     assert ((got.double() - want).abs() <= err).all()
+
+
+@gpu
+@needs_gpu
+@pytest.mark.parametrize("d", [64, 96, 128])
+def test_every_head_where_loads_are_waited_for(d):
+    """2000 heads of keys of their own, as many bytes as the memory can bring:
+    tiles land later than the warps want them.  Every element of both maps'
+    products against plain attention over the same map, whose kernels round
+    alike: each is off by h P|V| (P a bf16 operand, h = 2^-8), by half a step of
+    its result, and by 32-bit sums; P|V| comes from plain attention over |V|,
+    itself within 2 h of it."""
+    H, N, h = 2000, 1024, 2.0 ** -8
+    g = torch.Generator("cuda").manual_seed(35)
+    q, k = (torch.randn(1, 2 * H, N, d, generator=g, device="cuda", dtype=BF) for _ in range(2))
+    v = torch.randn(1, H, N, d, generator=g, device="cuda", dtype=BF)
+    w = torch.rand(H, generator=g, device="cuda")
+    scale = d ** -0.5
+    o, rest, lse = fbob.diff_forward(q, k, v, w, True, scale)
+    o2 = rest[..., 0, :]
+    got = (o.float() + w[:, None, None] * (o2.float() + rest[..., 1, :].float()) + rest[..., 2, :].float(), o2)
+    del rest, o
+    wide = 64 if d == 64 else 128
+    pad = lambda t: torch.nn.functional.pad(t, (0, wide - d)).contiguous()
+    small = 2.0 ** -24 * (N + 20 * d)
+    for m in (0, 1):
+        qm, km = pad(q[:, m::2]), pad(k[:, m::2])
+        want, want_lse = fbob.forward(qm, km, pad(v), True, scale)
+        mag, _ = fbob.forward(qm, km, pad(v.abs()), True, scale)
+        err = 2 * (h + small) * (1 + 2 * h) * mag[..., :d].float() + 2 * h * want[..., :d].float().abs() + 1e-6
+        off = (got[m].float() - want[..., :d].float()).abs()
+        assert (off <= err).all(), (m, int((off > err).sum()), (off / err).max().item())
+        assert ((lse[:, m::2] - want_lse).abs() <= 2.0 ** -24 * 40 * (d + 8)).all()
+    del got, q, k, v
+    torch.cuda.empty_cache()
