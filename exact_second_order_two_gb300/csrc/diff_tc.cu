@@ -418,20 +418,11 @@ __global__ void __launch_bounds__(kFwdThreads, 1)
     float mx = -INFINITY, l = 0.f;
     for (int t = 0; t < T; ++t) {
       const int j0 = t * C::BN;
-      // for the MMA warp: what it reads after this warp's arrivals has landed
+      // for the MMA warp: the next tile has landed
       if (C::ONE && warp == 0 && t + 1 < T)
         await(v_full + (t + 1) % C::VS, ((t + 1) / C::VS) & 1, ab, prm.status);
       await(s_full + m, t & 1, ab, prm.status);
       tc_fence_after();
-      // K^m behind the scores, no earlier: they tell that the slot's load before
-      // this one has landed (its products were issued before them).  One phase
-      // short of the awaited one the parity reads as if that were over, and the
-      // products would take keys that are still on their way.
-      if (!C::ONE && quad == 0) {
-        const int u = 2 * (t + 1) + m;
-        if (m == 0) await(v_full + t % C::VS, (t / C::VS) & 1, ab, prm.status);
-        if (t + 1 < T) await(k_full + u % C::KS, (u / C::KS) & 1, ab, prm.status);
-      }
       uint32_t s[4][32];
       tmem_ld32x4(ts, ts + 32, ts + 64, ts + 96, s[0], s[1], s[2], s[3]);
       // masked entries become -inf, so they give 2^-inf = 0 below
@@ -491,6 +482,16 @@ __global__ void __launch_bounds__(kFwdThreads, 1)
         // the first half starts while the second one is computed
         tmem_st16(ts + 32 * c, pw);
         if (c & 1) {
+          // for the MMA warp, at d = 128: V of this tile and K^m of the next have
+          // landed.  Behind the scores, no earlier: they tell that the slot's load
+          // before this one has landed (its products were issued before them).
+          // One phase short of the awaited one the parity reads as if that were
+          // over, and the products would take keys that are still on their way.
+          if (!C::ONE && quad == 0) {
+            const int u = 2 * (t + 1) + m;
+            if (c == 1 && m == 0) await(v_full + t % C::VS, (t / C::VS) & 1, ab, prm.status);
+            if (c == 3 && t + 1 < T) await(k_full + u % C::KS, (u / C::KS) & 1, ab, prm.status);
+          }
           tc_fence_before();
           warp_arrive(p_full + 2 * m + (c >> 1));
         }

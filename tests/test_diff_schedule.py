@@ -295,7 +295,7 @@ def forward(T, one, early=False):
                 mma.append(("commit", ("v_empty", t % vs), t // vs))
             if t + 1 < T:
                 mma += s(t + 1, m)
-    load, issued = [], 0
+    load = []
     for t in range(T):
         if not one:
             for u in (2 * t, 2 * t + 1):
@@ -309,23 +309,24 @@ def forward(T, one, early=False):
     for m in (0, 1):
         steps = []
         for t in range(T):
-            loads = []
-            if one:
-                if m == 0 and t + 1 < T:
-                    loads.append(("wait", ("v_full", (t + 1) % vs), (t + 1) // vs))
-            else:
-                u = 2 * (t + 1) + m
-                if m == 0:
-                    loads.append(("wait", ("v_full", t % vs), t // vs))
-                if t + 1 < T:
-                    loads.append(("wait", ("k_full", u % ks), u // ks))
-            scores = [("wait", ("s_full", m), t)]
-            steps += loads + scores if one or early else scores + loads
-            steps += [("read", ("S", m), ("S", t, 0)), ("read", ("Sb", m), ("S", t, 1))]
+            scores = [("wait", ("s_full", m), t), ("read", ("S", m), ("S", t, 0)),
+                      ("read", ("Sb", m), ("S", t, 1))]
             if t > 0:  # O is rescaled where the maximum moves
-                steps.append(("read", ("O", m), t - 1))
-            steps += [("write", ("S", m), ("P", t, 0)), ("arrive", ("p_full", m, 0), t),
-                      ("write", ("Sb", m), ("P", t, 1)), ("arrive", ("p_full", m, 1), t)]
+                scores.append(("read", ("O", m), t - 1))
+            tile, key = [], []
+            if one and m == 0 and t + 1 < T:
+                tile = [("wait", ("v_full", (t + 1) % vs), (t + 1) // vs)]
+            elif not one:
+                u = 2 * (t + 1) + m
+                tile = [("wait", ("v_full", t % vs), t // vs)] if m == 0 else []
+                key = [("wait", ("k_full", u % ks), u // ks)] if t + 1 < T else []
+            if one or early:
+                steps += tile + key + scores
+                tile, key = [], []
+            else:
+                steps += scores
+            steps += [("write", ("S", m), ("P", t, 0))] + tile + [("arrive", ("p_full", m, 0), t)]
+            steps += [("write", ("Sb", m), ("P", t, 1))] + key + [("arrive", ("p_full", m, 1), t)]
         roles[f"map {m}"] = steps
     counts = {("s_full", m): 1 for m in (0, 1)}
     counts.update({("p_full", m, h): 1 for m in (0, 1) for h in (0, 1)})
