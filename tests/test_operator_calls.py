@@ -322,3 +322,58 @@ def test_every_head_where_loads_are_waited_for(d):
         assert ((lse[:, m::2] - want_lse).abs() <= 2.0 ** -24 * 40 * (d + 8)).all()
     del got, q, k, v
     torch.cuda.empty_cache()
+# ---- offsets past 32 bits --------------------------------------------------------
+def needs_memory(gb):
+    return pytest.mark.skipif(
+        torch.cuda.is_available() and torch.cuda.get_device_properties(0).total_memory < gb * 2 ** 30,
+        reason=f"needs {gb} GB of device memory")
+
+
+@gpu
+@needs_gpu
+@needs_memory(60)
+def test_rotary_of_more_than_2_to_the_32_elements():
+    """8 heads of 2^22 + 3 tokens, as [B, N, H, d] and dense: the last rows, of
+    values and gradients, are those of a call on the last rows alone."""
+    n, tail = (1 << 22) + 3, 5
+    f, _ = fbob.rotary_frequencies(128)
+    for layout in ("bnhd", "bhnd"):
+        shape = (1, n, 8, 128) if layout == "bnhd" else (1, 8, n, 128)
+        x = torch.randn(shape, device="cuda", dtype=BF)
+        x = (x.transpose(1, 2) if layout == "bnhd" else x).requires_grad_()
+        y = fbob.rotary(x, f)
+        end = x.detach()[:, :, -tail:].clone().requires_grad_()
+        want = fbob.rotary(end, f, n - tail)
+        assert torch.equal(y[:, :, -tail:], want)
+        assert torch.equal(torch.autograd.grad(y, x, y.detach())[0][:, :, -tail:],
+                           torch.autograd.grad(want, end, want.detach())[0])
+        del x, y
+    torch.cuda.empty_cache()
+
+
+@gpu
+@needs_gpu
+@needs_memory(160)
+@pytest.mark.parametrize("dtype,H,N", [(BF, 16400, 1024), (F32, 32767, 520)])
+def test_diff_attention_of_more_than_2_to_the_32_elements(dtype, H, N):
+    """Queries and keys of 2^32 elements and more: the first, a middle and the
+    last head against the definition in 64 bits."""
+    import test_diff_finite as finite
+
+    g = torch.Generator("cuda").manual_seed(34)
+    q, k = (torch.randn(1, 2 * H, N, 128, generator=g, device="cuda", dtype=dtype) for _ in range(2))
+    v, do = (torch.randn(1, H, N, 128, generator=g, device="cuda", dtype=dtype) for _ in range(2))
+    w = torch.rand(1, H, N, generator=g, device="cuda").to(dtype)
+    assert q.numel() > 1 << 32
+    scale = 128 ** -0.5
+    o, rest, lse = fbob.diff_forward(q, k, v, w, True, scale)
+    grads = fbob.diff_backward(q, k, v, w, o, rest, lse, do, True, scale)
+    for h in (0, H // 2, H - 1):
+        maps, one = slice(2 * h, 2 * h + 2), slice(h, h + 1)
+        part = (q[:, maps], k[:, maps], v[:, one], w[:, one], do[:, one])
+        vals, errs = diff.oracle(*part, True, scale)
+        got = (o[:, one], rest[:, one, :, 0], lse[:, maps], grads[0][:, maps], grads[1][:, maps],
+               grads[2][:, one], grads[3][:, one])
+        finite.hold(dict(zip(finite.NAMES, got)), vals, errs, finite.underflow(*part, scale))
+    del q, k, v, do, w, o, rest, lse, grads, part, got
+    torch.cuda.empty_cache()
