@@ -322,6 +322,29 @@ def test_every_head_where_loads_are_waited_for(d):
         assert ((lse[:, m::2] - want_lse).abs() <= 2.0 ** -24 * 40 * (d + 8)).all()
     del got, q, k, v
     torch.cuda.empty_cache()
+
+
+@gpu
+@needs_gpu
+@pytest.mark.parametrize("d,dv", [(64, 128), (128, 128)])
+def test_every_gradient_where_loads_are_waited_for(d, dv):
+    """608 heads of keys of their own, forward and backward, every element against
+    the definition in 64 bits, 38 heads at a time."""
+    import test_diff_finite as finite
+
+    H, N, step, scale = 608, 1024, 38, d ** -0.5
+    q, k, v, w, do = diff.inputs(1, H, H, N, d, dv, BF, ("row", F32), seed=36)
+    o, rest, lse = fbob.diff_forward(q, k, v, w, True, scale)
+    grads = fbob.diff_backward(q, k, v, w, o, rest, lse, do, True, scale)
+    for h in range(0, H, step):
+        maps, some = slice(2 * h, 2 * (h + step)), slice(h, h + step)
+        part = tuple(t.contiguous() for t in (q[:, maps], k[:, maps], v[:, some], w[:, some], do[:, some]))
+        vals, errs = diff.oracle(*part, True, scale)
+        got = (o[:, some], rest[:, some, :, 0], lse[:, maps], grads[0][:, maps], grads[1][:, maps],
+               grads[2][:, some], grads[3][:, some])
+        finite.hold(dict(zip(finite.NAMES, got)), vals, errs, finite.underflow(*part, scale))
+    del vals, errs
+    torch.cuda.empty_cache()
 # ---- offsets past 32 bits --------------------------------------------------------
 def needs_memory(gb):
     return pytest.mark.skipif(
