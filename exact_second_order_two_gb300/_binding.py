@@ -151,8 +151,10 @@ def dense(t: torch.Tensor) -> torch.Tensor:
 def dual(*tensors) -> bool:
     """Whether one of them carries a forward-mode tangent.  None of the
     operators has a forward-mode derivative: a call that would drop the tangent
-    goes through its autograd function instead, which refuses it."""
-    return any(forward_ad.unpack_dual(t).tangent is not None for t in tensors if t is not None)
+    goes through its autograd function instead, which refuses it.  Outside of a
+    dual level there are none, and a small call has no time to look."""
+    return forward_ad._current_level >= 0 and any(
+        forward_ad.unpack_dual(t).tangent is not None for t in tensors if t is not None)
 
 
 def refuse_dual(what: str, *tensors) -> None:
