@@ -43,7 +43,8 @@ int check_shape(const fbob_diff_shape_t* s, DiffProblem* out) {
   for (int dt : {s->dtype, s->lam_dtype})
     if (dt != FBOB_BF16 && dt != FBOB_FP32) return FBOB_ERR_UNSUPPORTED;
   if (s->d > 128 || s->dv > 128) return FBOB_ERR_UNSUPPORTED;
-  // grids put heads in y; N leaves room for a tile past the end
+  // 2 B H maps, within the 65,535 heads of the other calls; N leaves room for a
+  // tile past the end
   if ((long long)s->B * s->H > 32767 || s->N > (1 << 30)) return FBOB_ERR_UNSUPPORTED;
   if ((double)s->B * s->H * s->N * 128.0 > (double)(1ll << 40)) return FBOB_ERR_UNSUPPORTED;
   *out = DiffProblem{s->B, s->H, s->Hk, s->N, s->d, s->dv, s->dtype == FBOB_BF16, s->causal,

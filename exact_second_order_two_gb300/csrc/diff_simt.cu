@@ -15,8 +15,9 @@
 // more, so several groups share a stationary tile: in the forward one per map,
 // which read the same values; and where shared memory allows (SPLIT = 2) twice
 // as many, which take every other streamed tile with tiles of their own, and
-// add up at the end.  Everything a row or key accumulates is summed by one block
-// in a fixed order.
+// add up at the end.  Everything a row accumulates is summed by one block in a
+// fixed order; a key's sums too, or by one block per part (col_parts), with the
+// parts added in their order.
 //
 // Measured, fp32, d = 64: forward at 4 heads x 2049 tokens, dv = 128, causal
 // 208 us (31 TFLOP/s; 254 us with both maps in one group and two groups), dQ 249,
@@ -33,7 +34,6 @@
 namespace fbob {
 namespace {
 
-constexpr int kSms = 152;    // of a GB300
 constexpr int kM = 32;       // rows of the stationary tile
 constexpr int kT = 64;       // rows of a streamed tile
 constexpr int kThreads = 128;  // of a group
@@ -714,9 +714,12 @@ cudaError_t forward_t(const DiffProblem& p, const DiffTensors& t, LaunchLog& log
   Args a = make_args(p, t);
   a.heads = p.B * p.H;
   // With few blocks the longest row's time counts: two pairs of groups share
-  // one.  With more the SMs' throughput does: two blocks of a pair per SM, which
-  // need not add up.  One pair, two: 260 blocks, causal 254, 212 us; 256 blocks
-  // of equal length 204, 209 us.
+  // one.  With many the SMs' throughput does: two blocks of a pair per SM, which
+  // need not add up.  One pair, two, in us (fp32, d = 64, dv = 128): causal, 128
+  // blocks 262, 204; 192 209, 157; 256 296, 205; 288 339, 230; 368 466, 395; 512
+  // 723, 712; 1024 1315, 1355; without mask 128 264, 204; 192 305, 304; 256 404,
+  // 400; 288 452, 448; 512 1551, 1524.  At dv = 64 without mask two are 3% slower
+  // from 192 to 288 blocks.
   const bool split = (long long)blocks * a.heads <= 2 * kSms &&
                      (q + 2 * area) * sizeof(float) <= kMaxShared;
   if (split)

@@ -1,7 +1,8 @@
 // Differential attention on the tensor cores (tcgen05 / TMEM / TMA), bf16, d and
 // dv multiples of 8 up to 128.  The kernels are built for widths D and DV of 64
 // and 128; narrower rows arrive with zeros behind them (the copies fill in what
-// is past a row's end, and leave it out when they store).  Per head, with m = 1, 2 (code: 0, 1) and c the scale,
+// is past a row's end, and leave it out when they store).  Per head, with
+// m = 1, 2 (code: 0, 1) and c the scale,
 //   S^m = c Q^m K^mT, P^m = softmax(S^m), O = P^1 V - lam P^2 V;
 //   dP = dO V^T, D^m = dO . O^m, dS^1 = P^1*(dP - D^1),
 //   dS^2 = -lam P^2*(dP - D^2), dQ^m = c dS^m K^m, dK^m = c dS^mT Q^m,
@@ -22,7 +23,8 @@
 //   with dO once.  A CTA loops over the query heads that share its key head, or
 //   over a part of their queries (col_parts).
 // The row and the column pass recompute the scores rather than exchange dQ
-// through atomics: every output is accumulated by one CTA in a fixed order.
+// through atomics: every output is accumulated by one CTA in a fixed order, or by
+// one per part, with the parts added in their order.
 //
 // Probabilities, W and dS are rounded to bf16 as operands of the second
 // products, the precision of the tensors they are multiplied with; scores,
@@ -578,8 +580,8 @@ __device__ __forceinline__ float dot8(const uint4& a, const uint4& b, float acc)
   return acc;
 }
 
-// DV/8 lanes per row, 16 bytes of each tensor per lane (vecs = dv/8 of them); a block takes 64 rows
-// of one head.  Bound: memory (O, rest and dO read once).
+// DV/8 lanes per row, 16 bytes of each tensor per lane (vecs = dv/8 of them); a
+// block takes 64 rows of one head.  Bound: memory (O, rest and dO read once).
 template <int DV>
 __global__ void __launch_bounds__(256, 4)
     diff_tc_scalars(const uint4* __restrict__ o, const uint4* __restrict__ rest,
@@ -1332,10 +1334,10 @@ __global__ void __launch_bounds__(256)
 // 77 -> 24 + 4; 2 of 2, 2048 tokens 43 -> 24 + 4; but with 16 tiles to cut (8 of
 // 8 heads, 1024 tokens) 26 -> 25 + 4, so fewer than 24 stay whole.
 int col_parts(const DiffProblem& p) {
-  constexpr long long kSms = 152, kTiles = 8;
+  constexpr long long kTiles = 8;
   const long long blocks = (long long)((p.N + 127) / 128) * p.B * p.Hk;
   const long long tiles = (long long)((p.N + 63) / 64) * p.G();
-  return tiles < 3 * kTiles ? 1 : (int)max(1ll, min(kSms / blocks, tiles / kTiles));
+  return tiles < 3 * kTiles ? 1 : (int)max(1ll, min((long long)kSms / blocks, tiles / kTiles));
 }
 
 // The kernels' width for rows of `width`
@@ -1350,7 +1352,7 @@ Common common(const DiffProblem& p, const DiffTensors& t, const DiffWorkspace& w
   c.H = p.H;
   c.G = p.G();
   c.units = units;
-  c.group = cta_group_heads(units, (p.N + 127) / 128, sm_count());
+  c.group = cta_group_heads(units, (p.N + 127) / 128, kSms);
   c.scale = p.scale;
   c.narrow_d = p.d != built(p.d);
   c.narrow_v = p.dv != built(p.dv);
@@ -1428,7 +1430,8 @@ cudaError_t backward_d(const DiffProblem& p, const DiffTensors& t, const DiffWor
   r.scal = ws.scal;
   r.d2 = ws.d2;
   const bool narrow = r.narrow_d || r.narrow_v;
-  e = run(narrow ? diff_row_pass<D, DV, true> : diff_row_pass<D, DV, false>, r.units, 1, p.N, kThreads, Rw::SMEM, log, r, rQ, rK, rV, rDO, rDQ);
+  e = run(narrow ? diff_row_pass<D, DV, true> : diff_row_pass<D, DV, false>, r.units, 1, p.N,
+          kThreads, Rw::SMEM, log, r, rQ, rK, rV, rDO, rDQ);
   if (e != cudaSuccess) return e;
   ColParams c;
   static_cast<Common&>(c) = common(p, t, ws, p.B * p.Hk);
@@ -1436,10 +1439,10 @@ cudaError_t backward_d(const DiffProblem& p, const DiffTensors& t, const DiffWor
   c.parts = ws.parts;
   const int parts = col_parts(p);
   if (parts == 1)
-    return run(narrow ? diff_col_pass<D, DV, true, false> : diff_col_pass<D, DV, false, false>, c.units,
-               1, p.N, kThreads, Cl::SMEM, log, c, cK, cV, cQ, cDO, cDK, cDV);
-  e = run(narrow ? diff_col_pass<D, DV, true, true> : diff_col_pass<D, DV, false, true>, c.units, parts, p.N, kThreads, Cl::SMEM, log, c, cK, cV, cQ,
-          cDO, cDK, cDV);
+    return run(narrow ? diff_col_pass<D, DV, true, false> : diff_col_pass<D, DV, false, false>,
+               c.units, 1, p.N, kThreads, Cl::SMEM, log, c, cK, cV, cQ, cDO, cDK, cDV);
+  e = run(narrow ? diff_col_pass<D, DV, true, true> : diff_col_pass<D, DV, false, true>, c.units,
+          parts, p.N, kThreads, Cl::SMEM, log, c, cK, cV, cQ, cDO, cDK, cDV);
   if (e != cudaSuccess) return e;
   const size_t rows = (size_t)c.units * p.N, quads = rows * ((2 * D + DV) / 4);
   diff_col_join<D, DV><<<(unsigned)((quads + 255) / 256), 256, 0, log.stream>>>(

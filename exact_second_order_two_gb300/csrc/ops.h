@@ -11,6 +11,9 @@
 
 namespace fbob {
 
+// SMs of a GB300: what these operators' launch rules are made for and measured on.
+constexpr int kSms = 152;
+
 // Profiling-event and launch-count bookkeeping around one entry point's work.
 void begin_call(LaunchLog& log);
 void end_call(const LaunchLog& log);

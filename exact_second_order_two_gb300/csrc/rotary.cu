@@ -32,7 +32,6 @@ namespace fbob {
 namespace {
 
 constexpr int kThreads = 128;
-constexpr int kSms = 152;  // of a GB300
 
 struct RotaryArgs {
   const void* x;

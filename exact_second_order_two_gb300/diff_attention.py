@@ -138,7 +138,9 @@ def _forward(shp, q, k, v, lam, need_rest, workspace=None):
 def diff_backward(q, k, v, lam, o, rest, lse, do, causal: bool = False,
                   scale: float | None = None, workspace=None):
     """First backward for upstream gradient ``do`` and the forward's results:
-    returns (dQ, dK, dV, dlam), of the inputs' shapes and dtypes."""
+    returns (dQ, dK, dV, dlam), of the inputs' shapes and dtypes.  As in the dense
+    products, an infinite or NaN query or key reaches the gradients of rows that
+    give it no weight."""
     shp = _shape(q, k, v, lam, causal, scale)
     rows = (shp.B, shp.H, shp.N, shp.dv)
     for name, t, shape in (("o", o, rows), ("rest", rest, _rest_shape(shp)), ("do", do, rows)):

@@ -261,6 +261,9 @@ int fbob_rotary(const fbob_rotary_t* r, const void* x, const double* inv_freq,
  * asynchrony and alignment as above (lam to its own size); 0 < scale <= 2e38.
  * 1 <= d, dv <= 128, B*H <= 32767.  bf16 at d and dv that are multiples of 8
  * runs the tensor-core kernels, the rest runs on CUDA cores (fbob_diff_path).
+ * Scores, softmax statistics and sums are fp32 in both; the tensor-core kernels
+ * take P, P^1 - lam P^2 and dS as bf16 operands of the second products, the
+ * CUDA-core kernels keep them in fp32.
  * Every output is summed in a fixed order: equal inputs give equal bits. */
 typedef enum { FBOB_LAM_ONE = 0, FBOB_LAM_HEAD = 1, FBOB_LAM_ROW = 2 } fbob_lam_t;
 
