@@ -125,6 +125,14 @@ __device__ __forceinline__ void await(uint64_t* bar, uint32_t parity, Abort* ab,
   wait_bar(bar, parity, ab, status);
 }
 
+// The producers' wait for a free stage.  Behind the abort flag the MMA warp's
+// commits free stages whose copies have not landed yet, and another copy would
+// arrive on their barrier once more than it counts (which ends the context): the
+// flag is up before such a commit, so it is looked at behind the wait.
+__device__ __forceinline__ bool stage_free(uint64_t* bar, uint32_t parity, Abort* ab, int* status) {
+  return wait_bar(bar, parity, ab, status) && !ab->flag;
+}
+
 __device__ __forceinline__ float max3(float a, float b, float c) {
   float d;
   asm("max.f32 %0, %1, %2, %3;" : "=f"(d) : "f"(a), "f"(b), "f"(c));
@@ -330,14 +338,14 @@ __global__ void __launch_bounds__(kFwdThreads, 1)
         if (!C::ONE) {
           for (; k_issued < 2 * t + 2; ++k_issued) {
             const int u = k_issued, ks = u % C::KS;
-            if (u >= C::KS && !wait_bar(k_empty + ks, ((u / C::KS) - 1) & 1, ab, prm.status)) break;
+            if (u >= C::KS && !stage_free(k_empty + ks, ((u / C::KS) - 1) & 1, ab, prm.status)) break;
             mbar_arrive_expect_tx(k_full + ks, C::QB);
             load_rows<D, C::BN>(smem + k_at(u), &mK, k_full + ks, t * C::BN, 2 * kvh + (u & 1), nd);
           }
           if (k_issued < 2 * t + 2) break;
         }
         const int vs = t % C::VS;
-        if (t >= C::VS && !wait_bar(v_empty + vs, ((t / C::VS) - 1) & 1, ab, prm.status)) break;
+        if (t >= C::VS && !stage_free(v_empty + vs, ((t / C::VS) - 1) & 1, ab, prm.status)) break;
         mbar_arrive_expect_tx(v_full + vs, C::VB + (C::ONE ? 2 * C::QB : 0));
         if (C::ONE) {
           load_rows<D, C::BN>(smem + k_at(2 * t), &mK, v_full + vs, t * C::BN, 2 * kvh, nd);
@@ -743,8 +751,8 @@ __global__ void __launch_bounds__(kThreads, 1)
       int issued = 0;
       for (int t = 0; t < T; ++t) {
         const int ks = t % C::KS, vs = t % C::VS;
-        if (t >= C::VS && !wait_bar(v_empty + vs, ((t / C::VS) - 1) & 1, ab, prm.status)) break;
-        if (t >= C::KS && !wait_bar(k_empty + ks, ((t / C::KS) - 1) & 1, ab, prm.status)) break;
+        if (t >= C::VS && !stage_free(v_empty + vs, ((t / C::VS) - 1) & 1, ab, prm.status)) break;
+        if (t >= C::KS && !stage_free(k_empty + ks, ((t / C::KS) - 1) & 1, ab, prm.status)) break;
         uint8_t* dst = smem + C::OFF_K + ks * 2 * C::KB;
         mbar_arrive_expect_tx(full + ks, 2 * C::KB + C::VB);
         load_rows<DV, C::BN>(smem + C::OFF_V + vs * C::VB, &mV, full + ks, t * C::BN, kvh, nv);
@@ -1054,7 +1062,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       int g = PARTS ? a0 / Tq : 0, t = PARTS ? a0 % Tq : 0, issued = 0;  // tile t within head g
       for (int a = 0; a < T; ++a) {
         const int st = a % C::ST, q0 = qstart + t * C::BN, bh = bh0 + g;
-        if (a >= C::ST && !wait_bar(empty + st, ((a / C::ST) - 1) & 1, ab, prm.status)) break;
+        if (a >= C::ST && !stage_free(empty + st, ((a / C::ST) - 1) & 1, ab, prm.status)) break;
         uint8_t* dst = smem + C::OFF_T + st * C::STB;
         mbar_arrive_expect_tx(full + st, C::STB + C::SCB);
         load_rows<D, C::BN>(dst, &mQ, full + st, q0, 2 * bh, nd);

@@ -109,6 +109,59 @@ def explore(roles, counts):
     return len(seen)
 
 
+def explore_abort(roles, counts, producer_looks):
+    """Any wait may run out and raise the block's flag.  From then on the MMA
+    warp's waits return at once, and it goes on with whatever the buffers hold;
+    the producer stops at a wait that runs out, and (where it looks) behind one
+    that did not if the flag is up.  No copy may be started on a barrier whose
+    last copy has not landed: it would arrive once more than the barrier counts.
+    Contents do not matter any more, nor what the elementwise warps do (the first
+    wait for them runs out), and a commit may as well arrive when it is issued:
+    the MMA warp takes as long as it likes."""
+    names = ["producer", "mma"]
+    steps = {n: [x for x in roles[n] if x[0] not in ("issue", "read", "write")] for n in names}
+    bars = list(counts)
+    at = {b: i for i, b in enumerate(bars)}
+    start = ((0, 0), tuple((0, 0) for _ in bars), frozenset(), False)
+    seen, todo = {start}, [start]
+
+    def arrive(bs, bar):
+        done, have = bs[at[bar]]
+        new = (done + 1, 0) if have + 1 == counts[bar] else (done, have + 1)
+        return bs[:at[bar]] + (new,) + bs[at[bar] + 1:]
+
+    while todo:
+        pcs, bs, flying, flag = todo.pop()
+        out = []
+        for r, name in enumerate(names):
+            if pcs[r] == len(steps[name]):
+                continue
+            step = steps[name][pcs[r]]
+            nbs, nf, after = bs, flying, [(pcs[r] + 1, flag)]
+            if step[0] == "wait":
+                over = (bs[at[step[1]]][0] & 1) != (step[2] & 1)  # what the parity tells
+                if name == "producer":
+                    end = len(steps[name])
+                    after = [(end if flag and producer_looks else pcs[r] + 1, flag)] if over else [(end, True)]
+                elif not over and not flag:
+                    after = [(pcs[r] + 1, True)]
+            elif step[0] == "load":
+                if any(steps["producer"][pc][1] == step[1] for pc in flying):
+                    raise Violation(f"a copy on {step[1]} is started before the last one has landed")
+                nf = flying | {pcs[r]}
+            else:
+                nbs = arrive(bs, step[1])
+            for pc, f in after:
+                out.append((pcs[:r] + (pc,) + pcs[r + 1:], nbs, nf, f))
+        for pc in flying:
+            out.append((pcs, arrive(bs, steps["producer"][pc][1]), flying - {pc}, flag))
+        for s in out:
+            if s not in seen:
+                seen.add(s)
+                todo.append(s)
+    return len(seen)
+
+
 # A tensor-memory block is one cell per warp (its columns or lanes); a product
 # reads and writes all of them.
 def block(name, value):
@@ -376,3 +429,20 @@ def test_planted_mistakes_are_found():
     roles["mma"].remove(("wait", ("p_full", 1, 1), 1))
     with pytest.raises(Violation):
         explore(roles, counts)
+
+
+# tiles enough that every ring is filled once more
+ABORTING = {"dK_dV": lambda: column_narrow(6), "dK_dV_wide": lambda: column_wide(4), "dQ": lambda: row(5),
+            "forward": lambda: forward(5, True), "forward_wide": lambda: forward(4, False)}
+
+
+@pytest.mark.parametrize("name", ABORTING)
+def test_a_wait_that_runs_out_starts_no_copy_too_many(name):
+    assert explore_abort(*ABORTING[name](), producer_looks=True) > 100
+
+
+@pytest.mark.parametrize("name", ABORTING)
+def test_a_producer_that_does_not_look_is_found(name):
+    """Behind the flag the MMA warp's commits free stages that are not filled yet."""
+    with pytest.raises(Violation, match="before the last one has landed"):
+        explore_abort(*ABORTING[name](), producer_looks=False)
