@@ -40,8 +40,10 @@
 // what the products they run come to as a share of the measured matmul rate of
 // 1917 TFLOP/s):
 //            forward        row pass        column pass
-//   d = 64   570 us, 75%    572 us, 75%     948 us, 61%
-//   d = 128  654 us, 88%    947 us, 76%     1358 us, 63%
+//   d = 64   582 us, 74%    572 us, 75%     960 us, 60%
+//   d = 128  645 us, 89%    949 us, 76%     1371 us, 63%
+// (of which the producers' look at the abort flag is 6 us of the forward at d = 64
+// and 15 us of the column pass at d = 128).
 // The chain scores -> exponentials -> product within a tile: the accumulators
 // leave TMEM for one or two buffers per map, so pipe and elementwise warps wait
 // for each other, and each hand-over costs 100 to 250 cycles on either side.  At
