@@ -61,6 +61,21 @@ class DiffShape(ctypes.Structure):
                 ("scale", ctypes.c_float)]
 
 
+class QkNorm(ctypes.Structure):
+    _fields_ = [("B", ctypes.c_int), ("N", ctypes.c_int), ("d", ctypes.c_int),
+                ("rotary_dim", ctypes.c_int), ("interleaved", ctypes.c_int),
+                ("in_dtype", ctypes.c_int), ("out_dtype", ctypes.c_int),
+                ("weight_dtype", ctypes.c_int), ("eps", ctypes.c_float),
+                ("magnitude", ctypes.c_float), ("pos_stride", ctypes.c_longlong),
+                ("offset", ctypes.c_longlong)]
+
+
+class NormSide(ctypes.Structure):
+    _fields_ = [("H", ctypes.c_int)] + \
+        [(n, ctypes.c_void_p) for n in ("x", "weight", "dy", "a", "c", "y", "dweight", "ddy")] + \
+        [(n + "_strides", ctypes.c_longlong * 3) for n in ("x", "dy", "a", "y", "ddy")]
+
+
 _LIB = None
 _P = ctypes.c_void_p
 _SZ = ctypes.c_size_t
@@ -89,6 +104,10 @@ _SIGNATURES = {
     "fbob_diff_forward": (ctypes.c_int, [_P] * 9 + [_SZ, _P]),
     "fbob_diff_backward": (ctypes.c_int, [_P] * 14 + [_SZ, _P]),
     "fbob_rotary": (ctypes.c_int, [_P] * 6),
+    "fbob_qk_norm_workspace_size": (_SZ, [_P]),
+    "fbob_qk_norm_forward": (ctypes.c_int, [_P] * 6),
+    "fbob_qk_norm_backward": (ctypes.c_int, [_P] * 6 + [_SZ, _P]),
+    "fbob_qk_norm_bob": (ctypes.c_int, [_P] * 6 + [_SZ, _P]),
 }
 
 

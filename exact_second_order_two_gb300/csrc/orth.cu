@@ -1,0 +1,1064 @@
+// Orthogonalised updates: Newton-Schulz products and their gradient.
+//
+// X_0 = s G, s = 1 / (|G|_F + eps), with the shorter side first (p <= q; a tall G
+// is transposed on the way in and out).  A step with polynomial a x + b x^3 + c x^5:
+//   A = X X^T,   B = b A + c A^2,   X' = a X + B X.
+// For an upstream gradient H of X', with A and B symmetric,
+//   S = H X^T + X H^T,   T = b S + c (A S + S A),   H' = a H + B H + T X,
+// and at the end dG = s (H_0 - G <H_0, G> s / |G|_F).
+//
+// All of these are products P Q^T or P Q of matrices stored by rows, summed in one
+// accumulator and finished by alpha acc + beta E: one kernel (product) serves them
+// all.  A, B, S and T are symmetric: only tiles on and below the diagonal are computed,
+// and written in both places.  S and A S + S A are sums of a product and its transpose: as
+// one accumulation [H | X] [X | H]^T they need half the tiles, too.
+//
+// Numbers.  Operands are fp16 with exponents chosen for each matrix, accumulation
+// is fp32.  X has singular values up to M (bounded on the host from the
+// polynomials), so that one power of two for all of X, A and B keeps them inside fp16's
+// range, with 11 bits down to 2^-26 of the bound; H is rescaled every step by the norm
+// that it was measured to have.  fp32 tensors are held as the sum of two fp16 (22 bits)
+// and multiplied in three products; bf16 tensors in one, except that X takes two terms
+// in steps whose rounding later steps would multiply by more than 16: a rounding
+// error of X off its strong directions grows by a every step.
+#include <cuda.h>
+#include <cuda_bf16.h>
+#include <cuda_fp16.h>
+#include <cuda_runtime.h>
+#include <math.h>
+#include <stdint.h>
+
+#include "common.cuh"
+#include "fbob.h"
+#include "internal.h"
+#include "ops.h"
+#include "sm103.cuh"
+#include "tc_common.cuh"
+
+namespace fbob {
+namespace {
+
+using namespace tc;
+
+constexpr size_t kAlign = 256;
+size_t align_up(size_t x) { return (x + kAlign - 1) / kAlign * kAlign; }
+
+// ---------------------------------------------------------------------------
+// What is kept of a matrix
+// ---------------------------------------------------------------------------
+struct MatInfo {
+  float norm, s;  // |G|_F and 1 / (norm + eps)
+  float f;        // X_0 = f G 2^k: f in [1, 2)
+  int k;
+};
+
+// A matrix in one or two fp16 terms: rows of ld elements, [count] matrices.
+struct Terms {
+  __half *hi = nullptr, *lo = nullptr;
+  int rows = 0, cols = 0, ld = 0;
+  int terms() const { return lo ? 2 : 1; }
+};
+
+// ---------------------------------------------------------------------------
+// The product kernel
+// ---------------------------------------------------------------------------
+constexpr int kTile = 128;        // rows, and columns, of a CTA's operand tiles
+constexpr int kDepth = 64;        // contraction elements of a stage (128-byte rows)
+constexpr int kStages = 6;
+constexpr uint32_t kTileBytes = kTile * kDepth * 2;
+constexpr uint32_t kStageBytes = 2 * kTileBytes;
+constexpr uint32_t kOffMisc = kStages * kStageBytes;
+constexpr uint32_t kSmem = kOffMisc + 512;
+constexpr int kEpiWarps = 4, kProducerWarp = 4, kMmaWarp = 5;
+constexpr int kThreads = 192;
+constexpr int kMaxSegs = 6;
+
+struct Epilogue {
+  float alpha, beta;            // value = (alpha acc + beta E) f^fpow, times the rescaling
+  const __half *ehi, *elo;      // E, or null
+  int elds;
+  const MatInfo* info;          // f of each matrix
+  int fpow;
+  // outputs: terms by rows (and mirrored), or fp32 by rows, or the caller's tensor
+  __half *ohi, *olo;
+  int olds;
+  float* of32;
+  void* y;
+  int y_bf16, y_transposed;
+  // sums: squares of the values written, or their product with D's
+  float* sums;                  // [count][parts of a matrix]
+  const __half *dhi, *dlo;
+  // rescaling by the norm of the step's input: [count][scale_parts] squares
+  const float* scale_sums;
+  int scale_parts, target;
+  const int* exp_in;
+  int* exp_out;
+};
+
+struct __align__(64) ProductArgs {
+  CUtensorMap a[4], b[4];
+  unsigned char seg_a[kMaxSegs], seg_b[kMaxSegs];
+  int nseg;
+  int rows, cols, depth, count;
+  int sym;
+  Epilogue e;
+  int* status;
+  unsigned long long wait_ns;
+};
+
+// Instruction descriptor: fp16 operands (formats 0), fp32 accumulator.
+__host__ __device__ constexpr uint32_t idesc_f16(int M, int N, bool b_mn_major) {
+  return (1u << 4) | ((b_mn_major ? 1u : 0u) << 16) | ((uint32_t)(N >> 3) << 17) |
+         ((uint32_t)(M >> 4) << 24);
+}
+
+struct TileAt {
+  int l, i, j, index;  // matrix, tile row and column, its number within the matrix
+};
+__device__ __forceinline__ TileAt tile_at(const ProductArgs& g, int t, int side) {
+  const int tm = (g.rows + side - 1) / side, tn = (g.cols + side - 1) / side;
+  const int per = g.sym ? tm * (tm + 1) / 2 : tm * tn;
+  TileAt r;
+  r.l = t / per;
+  r.index = t - r.l * per;
+  if (g.sym) {
+    int i = (int)((sqrtf(8.f * r.index + 1.f) - 1.f) * 0.5f);
+    while (i * (i + 1) / 2 > r.index) --i;
+    while ((i + 1) * (i + 2) / 2 <= r.index) ++i;
+    r.i = i;
+    r.j = r.index - i * (i + 1) / 2;
+  } else {  // a column of tiles after the other: its operand tile is shared
+    r.j = r.index / tm;
+    r.i = r.index - r.j * tm;
+  }
+  return r;
+}
+
+__device__ __forceinline__ void split(float v, __half& hi, __half& lo) {
+  hi = __float2half_rn(v);
+  lo = __float2half_rn(v - __half2float(hi));
+}
+
+__device__ __forceinline__ uint32_t pack2(__half a, __half b) {
+  return (uint32_t)__half_as_ushort(a) | ((uint32_t)__half_as_ushort(b) << 16);
+}
+
+// v[c] += beta * (hi + lo) of 32 consecutive elements, of which those below `valid` exist.
+template <typename F>
+__device__ __forceinline__ void each_of_terms(const __half* hi, const __half* lo, int valid, F f) {
+#pragma unroll
+  for (int q = 0; q < 4; ++q) {
+    if (8 * q >= valid) break;
+    const uint4 h = *reinterpret_cast<const uint4*>(hi + 8 * q);
+    uint4 l = make_uint4(0, 0, 0, 0);
+    if (lo) l = *reinterpret_cast<const uint4*>(lo + 8 * q);
+    const uint32_t hw[4] = {h.x, h.y, h.z, h.w}, lw[4] = {l.x, l.y, l.z, l.w};
+#pragma unroll
+    for (int k = 0; k < 4; ++k) {
+      const float2 a = __half22float2(*reinterpret_cast<const __half2*>(&hw[k]));
+      const float2 b = __half22float2(*reinterpret_cast<const __half2*>(&lw[k]));
+      f(8 * q + 2 * k, a.x + b.x);
+      f(8 * q + 2 * k + 1, a.y + b.y);
+    }
+  }
+}
+
+// One row's 32 columns of a tile: finish the values and write them.  Returns the row's
+// part of the sums.
+__device__ __forceinline__ float finish(const ProductArgs& g, const uint32_t (&acc)[32], int l, int row,
+                                        int col, bool mirror, float alpha, float beta) {
+  const Epilogue& e = g.e;
+  const int valid = min(32, g.cols - col);
+  if (row >= g.rows || valid <= 0) return 0.f;
+  float v[32];
+#pragma unroll
+  for (int c = 0; c < 32; ++c) v[c] = c < valid ? alpha * __uint_as_float(acc[c]) : 0.f;
+  if (e.ehi) {
+    const size_t at = ((size_t)l * g.rows + row) * e.elds + col;
+    each_of_terms(e.ehi + at, e.elo ? e.elo + at : nullptr, valid, [&](int c, float x) {
+      if (c < valid) v[c] = fmaf(beta, x, v[c]);
+    });
+  }
+  float sum = 0.f;
+  if (e.sums) {
+    if (e.dhi) {
+      const size_t at = ((size_t)l * g.rows + row) * e.elds + col;
+      each_of_terms(e.dhi + at, e.dlo ? e.dlo + at : nullptr, valid, [&](int c, float x) {
+        if (c < valid) sum = fmaf(v[c], x, sum);
+      });
+    } else {
+#pragma unroll
+      for (int c = 0; c < 32; ++c) sum = fmaf(v[c], v[c], sum);
+    }
+  }
+  if (e.ohi) {
+    __half hi[32], lo[32];
+#pragma unroll
+    for (int c = 0; c < 32; ++c) split(v[c], hi[c], lo[c]);
+    const size_t base = (size_t)l * g.rows * e.olds;
+    const size_t at = base + (size_t)row * e.olds + col;
+#pragma unroll
+    for (int q = 0; q < 4; ++q) {
+      if (8 * q >= valid) break;
+      const int c = 8 * q;
+      *reinterpret_cast<uint4*>(e.ohi + at + c) =
+          make_uint4(pack2(hi[c], hi[c + 1]), pack2(hi[c + 2], hi[c + 3]), pack2(hi[c + 4], hi[c + 5]),
+                     pack2(hi[c + 6], hi[c + 7]));
+      if (e.olo)
+        *reinterpret_cast<uint4*>(e.olo + at + c) =
+            make_uint4(pack2(lo[c], lo[c + 1]), pack2(lo[c + 2], lo[c + 3]), pack2(lo[c + 4], lo[c + 5]),
+                       pack2(lo[c + 6], lo[c + 7]));
+    }
+    if (mirror) {
+#pragma unroll
+      for (int c = 0; c < 32; ++c)
+        if (c < valid) {
+          const size_t to = base + (size_t)(col + c) * e.olds + row;
+          e.ohi[to] = hi[c];
+          if (e.olo) e.olo[to] = lo[c];
+        }
+    }
+  } else if (e.of32) {
+    float* o = e.of32 + ((size_t)l * g.rows + row) * e.olds + col;
+#pragma unroll
+    for (int q = 0; q < 8; ++q) {
+      if (4 * q >= valid) break;
+      *reinterpret_cast<float4*>(o + 4 * q) = make_float4(v[4 * q], v[4 * q + 1], v[4 * q + 2], v[4 * q + 3]);
+    }
+  } else {
+    const size_t n = (size_t)g.rows * g.cols;
+    const size_t first = l * n + (e.y_transposed ? (size_t)col * g.rows + row : (size_t)row * g.cols + col);
+    const size_t step = e.y_transposed ? g.rows : 1;
+    if (e.y_bf16) {
+      __nv_bfloat16* o = static_cast<__nv_bfloat16*>(e.y) + first;
+      if (step == 1 && valid == 32 && (reinterpret_cast<uintptr_t>(o) & 15u) == 0) {
+#pragma unroll
+        for (int q = 0; q < 4; ++q)
+          reinterpret_cast<uint4*>(o)[q] =
+              make_uint4(pack_bf16(v[8 * q], v[8 * q + 1]), pack_bf16(v[8 * q + 2], v[8 * q + 3]),
+                         pack_bf16(v[8 * q + 4], v[8 * q + 5]), pack_bf16(v[8 * q + 6], v[8 * q + 7]));
+      } else {
+#pragma unroll
+        for (int c = 0; c < 32; ++c)
+          if (c < valid) o[c * step] = __float2bfloat16_rn(v[c]);
+      }
+    } else {
+      float* o = static_cast<float*>(e.y) + first;
+      if (step == 1 && valid == 32 && (reinterpret_cast<uintptr_t>(o) & 15u) == 0) {
+#pragma unroll
+        for (int q = 0; q < 8; ++q)
+          reinterpret_cast<float4*>(o)[q] = make_float4(v[4 * q], v[4 * q + 1], v[4 * q + 2], v[4 * q + 3]);
+      } else {
+#pragma unroll
+        for (int c = 0; c < 32; ++c)
+          if (c < valid) o[c * step] = v[c];
+      }
+    }
+  }
+  return sum;
+}
+
+// The exponent that brings a matrix with sum of squares nu2 to a norm in
+// (2^(target - 1), 2^target], or nearly; 0 for zeros and for what is not finite.
+__device__ __forceinline__ int rescaling(float nu2, int target) {
+  if (!(nu2 > 0.f) || nu2 > 3.0e38f) return 0;
+  int e;
+  frexpf(nu2, &e);  // nu2 < 2^e
+  return target - ((e + 1) >> 1);
+}
+
+// acc = sum over segments of P Q^T (Q stored [cols, depth]) or P Q (NN: Q stored
+// [depth, cols]); blocks stay and take tiles in turn.  Warps: 4 finish tiles, one
+// loads, one multiplies; two accumulators, so that a tile is finished while the next
+// is multiplied.
+template <bool NN>
+__global__ void __launch_bounds__(kThreads, 1) product(const __grid_constant__ ProductArgs g) {
+  extern __shared__ __align__(1024) uint8_t smem[];
+  const uint32_t sb = smem_u32(smem);
+  if (sb & 1023u) {  // 128-byte swizzled tiles need a 1024-byte aligned base
+    if (threadIdx.x == 0) report_status(g.status, FBOB_ERR_CUDA);
+    return;
+  }
+  uint64_t* full = reinterpret_cast<uint64_t*>(smem + kOffMisc);  // [kStages]
+  uint64_t* empty = full + kStages;                               // [kStages]
+  uint64_t* t_full = empty + kStages;                             // [2]
+  uint64_t* t_empty = t_full + 2;                                 // [2]
+  uint64_t* drain = t_empty + 2;
+  uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(smem + kOffMisc + 256);
+  Abort* ab = reinterpret_cast<Abort*>(smem + kOffMisc + 264);
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  constexpr uint32_t kCols = 2 * kTile;
+  if (threadIdx.x == 0) {
+    for (int s = 0; s < kStages; ++s) {
+      mbar_init(full + s, 1);
+      mbar_init(empty + s, 1);
+    }
+    for (int b = 0; b < 2; ++b) {
+      mbar_init(t_full + b, 1);
+      mbar_init(t_empty + b, kEpiWarps);
+    }
+    mbar_init(drain, 1);
+    ab->flag = 0;
+    ab->limit_ns = g.wait_ns;
+    fence_mbar_init();
+  }
+  if (warp == kMmaWarp) {
+    tmem_alloc(tmem_slot, kCols);
+    tmem_relinquish();
+  }
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  const uint32_t tmem = *tmem_slot;
+  const int tm = (g.rows + kTile - 1) / kTile, tn = (g.cols + kTile - 1) / kTile;
+  const int tiles = g.count * (g.sym ? tm * (tm + 1) / 2 : tm * tn);
+  const int blocks = (g.depth + kDepth - 1) / kDepth;
+
+  if (warp == kProducerWarp) {
+    if (lane == 0) {
+      int it = 0;
+      bool ok = true;
+      for (int t = blockIdx.x; ok && t < tiles; t += gridDim.x) {
+        const TileAt at = tile_at(g, t, kTile);
+        const int row = at.i * kTile, col = at.j * kTile;
+        for (int sg = 0; ok && sg < g.nseg; ++sg) {
+          const CUtensorMap* ma = &g.a[g.seg_a[sg]];
+          const CUtensorMap* mb = &g.b[g.seg_b[sg]];
+          for (int k = 0; k < blocks; ++k, ++it) {
+            const int s = it % kStages;
+            if (it >= kStages && !wait_bar(empty + s, ((it / kStages) - 1) & 1, ab, g.status)) {
+              ok = false;
+              break;
+            }
+            if (ab->flag) {
+              ok = false;
+              break;
+            }
+            uint8_t* dst = smem + s * kStageBytes;
+            mbar_arrive_expect_tx(full + s, kStageBytes);
+            tma_load_3d(dst, ma, full + s, k * kDepth, row, at.l);
+            if (NN) {
+              tma_load_3d(dst + kTileBytes, mb, full + s, col, k * kDepth, at.l);
+              tma_load_3d(dst + kTileBytes + kTileBytes / 2, mb, full + s, col + 64, k * kDepth, at.l);
+            } else {
+              tma_load_3d(dst + kTileBytes, mb, full + s, k * kDepth, col, at.l);
+            }
+          }
+        }
+      }
+      // every load this thread issued has landed before the block exits
+      for (int u = max(0, it - kStages); u < it; ++u)
+        mbar_wait_bounded(full + u % kStages, (u / kStages) & 1, g.status, 100000000ull);
+    }
+  } else if (warp == kMmaWarp) {
+    constexpr uint32_t id = idesc_f16(kTile, kTile, NN);
+    int it = 0, n = 0;
+    bool ok = true;
+    for (int t = blockIdx.x; ok && t < tiles; t += gridDim.x, ++n) {
+      const uint32_t d = tmem + (n & 1) * kTile;
+      if (n >= 2 && !warp_wait(t_empty + (n & 1), ((n >> 1) - 1) & 1, ab, g.status)) break;
+      tc_fence_after();
+      const int total = g.nseg * blocks;
+      for (int k = 0; k < total; ++k, ++it) {
+        const int s = it % kStages;
+        if (!warp_wait(full + s, (it / kStages) & 1, ab, g.status)) {
+          ok = false;
+          break;
+        }
+        tc_fence_after();
+        const uint32_t a_lo = opaque(lo_kmajor(sb + s * kStageBytes));
+        const uint32_t b_at = sb + s * kStageBytes + kTileBytes;
+        const uint32_t b_lo = opaque(NN ? lo_mnmajor(b_at, kTileBytes / 2) : lo_kmajor(b_at));
+#pragma unroll
+        for (int u = 0; u < kDepth / 16; ++u)
+          mma_ss_w(d, a_lo + 2 * u, b_lo + (NN ? kstep_off(u) : 2 * u), id, k + u > 0 ? 1u : 0u);
+        mma_commit_w(empty + s);
+      }
+      if (ok) mma_commit_w(t_full + (n & 1));
+    }
+    // every MMA this warp issued has completed before TMEM is released
+    mma_commit_w(drain);
+    mbar_wait_bounded(drain, 0, g.status, 100000000ull);
+  } else {
+    const Epilogue& e = g.e;
+    const uint32_t lane_off = (uint32_t)(32 * warp) << 16;
+    int n = 0, scaled = -1, shift = 0;
+    for (int t = blockIdx.x; t < tiles; t += gridDim.x, ++n) {
+      const TileAt at = tile_at(g, t, kTile);
+      float alpha = e.alpha, beta = e.beta;
+      if (e.fpow) {
+        const float f = e.info[at.l].f, ff = e.fpow == 2 ? f * f : f;
+        alpha *= ff;
+        beta *= ff;
+      }
+      if (e.scale_sums) {
+        if (scaled != at.l) {
+          const float* p = e.scale_sums + (size_t)at.l * e.scale_parts;
+          float nu2 = 0.f;
+          for (int i = lane; i < e.scale_parts; i += 32) nu2 += p[i];
+          shift = rescaling(warp_sum(nu2), e.target);
+          scaled = at.l;
+        }
+        alpha = ldexpf(alpha, shift);
+        beta = ldexpf(beta, shift);
+        if (at.index == 0 && threadIdx.x == 0) e.exp_out[at.l] = e.exp_in[at.l] + shift;
+      }
+      if (!warp_wait(t_full + (n & 1), (n >> 1) & 1, ab, g.status)) break;
+      tc_fence_after();
+      float sum = 0.f;
+      const int row = at.i * kTile + 32 * warp + lane;
+#pragma unroll 1
+      for (int c = 0; c < kTile; c += 32) {
+        uint32_t acc[32];
+        tmem_ld32(tmem + lane_off + (n & 1) * kTile + c, acc);
+        sum += finish(g, acc, at.l, row, at.j * kTile + c, g.sym && at.i != at.j, alpha, beta);
+      }
+      tc_fence_before();
+      __syncwarp();
+      if (lane == 0) mbar_arrive(t_empty + (n & 1));
+      if (e.sums) {
+        sum = warp_sum(sum);
+        const int per = (g.sym ? tm * (tm + 1) / 2 : tm * tn) * kEpiWarps;
+        if (lane == 0) e.sums[(size_t)at.l * per + at.index * kEpiWarps + warp] = sum;
+      }
+    }
+  }
+  tc_fence_before();
+  __syncthreads();
+  if (warp == kMmaWarp) {
+    tc_fence_after();
+    tmem_dealloc(tmem, kCols);
+  }
+}
+
+// ---------------------------------------------------------------------------
+// Norms, packing, and the end of the gradient
+// ---------------------------------------------------------------------------
+constexpr int kSumThreads = 256;
+
+// partial[l][block] = sum of squares of a slice of matrix l; also clears the call's
+// status word, before every kernel that may write it.
+template <typename T>
+__global__ void __launch_bounds__(kSumThreads)
+    square_sums(const T* __restrict__ x, float* __restrict__ partial, size_t elems, int* status) {
+  __shared__ float sm[kSumThreads / 32];
+  if (blockIdx.x == 0 && blockIdx.y == 0 && threadIdx.x == 0) *status = 0;
+  x += (size_t)blockIdx.y * elems;
+  const size_t per = (elems + gridDim.x - 1) / gridDim.x;
+  const size_t first = blockIdx.x * per, last = min(elems, first + per);
+  float s[4] = {0.f, 0.f, 0.f, 0.f};
+  size_t i = first + threadIdx.x;
+  for (; i + 3 * kSumThreads < last; i += 4 * kSumThreads) {
+#pragma unroll
+    for (int u = 0; u < 4; ++u) {
+      const float v = to_f32<T>(x[i + u * kSumThreads]);
+      s[u] = fmaf(v, v, s[u]);
+    }
+  }
+  for (; i < last; i += kSumThreads) {
+    const float v = to_f32<T>(x[i]);
+    s[0] = fmaf(v, v, s[0]);
+  }
+  const float w = warp_sum((s[0] + s[1]) + (s[2] + s[3]));
+  if ((threadIdx.x & 31) == 0) sm[threadIdx.x >> 5] = w;
+  __syncthreads();
+  if (threadIdx.x == 0) {
+    float t = 0.f;
+    for (int k = 0; k < kSumThreads / 32; ++k) t += sm[k];
+    partial[(size_t)blockIdx.y * gridDim.x + blockIdx.x] = t;
+  }
+}
+
+// Sum of `parts` values, the same in every thread of the block.
+__device__ __forceinline__ float parts_sum(const float* p, int parts, float* sm) {
+  float s = 0.f;
+  for (int i = threadIdx.x; i < parts; i += kSumThreads) s += p[i];
+  s = warp_sum(s);
+  __syncthreads();
+  if ((threadIdx.x & 31) == 0) sm[threadIdx.x >> 5] = s;
+  __syncthreads();
+  s = 0.f;
+  for (int k = 0; k < kSumThreads / 32; ++k) s += sm[k];
+  return s;
+}
+
+struct PackArgs {
+  const void* x;       // [count][m][n]
+  const float* sums;   // [count][parts] squares
+  int parts;
+  __half *hi, *lo;     // [count][p][ld]
+  int p, q, ld, tall;
+  float eps;
+  int target;
+  // forward: the matrices' scales; backward (info null): their exponents and square sums
+  MatInfo* info;
+  int* exp_out;
+  float* sums_out;
+};
+
+constexpr int kPack = 64;  // rows and columns of a block's tile
+
+// x times a power of two, in fp16 terms, the shorter side first.
+template <typename T>
+__global__ void __launch_bounds__(kSumThreads) pack(PackArgs a) {
+  __shared__ float sm[kSumThreads / 32];
+  __shared__ float tile[kPack][kPack + 1];
+  const int l = blockIdx.z;
+  const float nu2 = parts_sum(a.sums + (size_t)l * a.parts, a.parts, sm);
+  const bool writer = blockIdx.x == 0 && blockIdx.y == 0 && threadIdx.x == 0;
+  float factor;
+  if (a.info) {
+    MatInfo r;
+    r.norm = sqrtf(nu2);
+    r.s = 1.f / (r.norm + a.eps);
+    if (r.s > 0.f && r.s < 3.0e38f) {
+      int e;
+      r.f = 2.f * frexpf(r.s, &e);  // s = f 2^(e - 1)
+      r.k = e - 1;
+      factor = ldexpf(1.f, r.k + a.target);
+    } else {  // an infinite or NaN norm, or 0 and eps = 0: zeros and NaN as s G gives them
+      r.f = 1.f;
+      r.k = 0;
+      factor = r.s;
+    }
+    if (writer) a.info[l] = r;
+  } else {
+    const int e = rescaling(nu2, a.target);
+    factor = ldexpf(1.f, e);
+    if (writer) {
+      a.exp_out[l] = e;
+      a.sums_out[l] = nu2 * factor * factor;
+    }
+  }
+  const T* x = static_cast<const T*>(a.x) + (size_t)l * a.p * a.q;
+  const size_t base = (size_t)l * a.p * a.ld;
+  const int r0 = blockIdx.y * kPack, c0 = blockIdx.x * kPack;  // of the packed matrix
+  if (a.tall) {
+    for (int i = threadIdx.x; i < kPack * kPack; i += kSumThreads) {
+      const int c = i / kPack, r = i % kPack;  // x is [q][p]
+      if (c0 + c < a.q && r0 + r < a.p) tile[r][c] = to_f32<T>(x[(size_t)(c0 + c) * a.p + r0 + r]);
+    }
+    __syncthreads();
+  }
+  for (int i = threadIdx.x; i < kPack * kPack; i += kSumThreads) {
+    const int r = i / kPack, c = i % kPack;
+    if (r0 + r >= a.p || c0 + c >= a.q) continue;
+    const float v = (a.tall ? tile[r][c] : to_f32<T>(x[(size_t)(r0 + r) * a.q + c0 + c])) * factor;
+    __half hi, lo;
+    split(v, hi, lo);
+    a.hi[base + (size_t)(r0 + r) * a.ld + c0 + c] = hi;
+    if (a.lo) a.lo[base + (size_t)(r0 + r) * a.ld + c0 + c] = lo;
+  }
+}
+
+struct EndArgs {
+  const void* g;      // [count][m][n]
+  void* dg;
+  const float* h;     // [count][p][ld]: dX_0 2^exp
+  const float* dots;  // [count][parts]: <h, X_0's terms>
+  int parts;
+  int p, q, ld, tall, x_exp;
+  const MatInfo* info;
+  const int* exp;
+};
+
+// dG = s (H_0 - G <H_0, G> s / norm)
+template <typename T>
+__global__ void __launch_bounds__(kSumThreads) end_gradient(EndArgs a) {
+  __shared__ float sm[kSumThreads / 32];
+  __shared__ float tile[kPack][kPack + 1];
+  const int l = blockIdx.z;
+  const MatInfo r = a.info[l];
+  const float dot = parts_sum(a.dots + (size_t)l * a.parts, a.parts, sm);
+  // <h, G> = dot 2^-(k + x_exp); a zero matrix has no direction to take off
+  const double along = r.norm > 0.f ? ldexp((double)dot, -(r.k + a.x_exp)) * r.s / r.norm : 0.0;
+  const double scale = ldexp((double)r.s, -a.exp[l]);
+  const float by_h = (float)scale, by_g = (float)(scale * along);
+  const size_t n = (size_t)l * a.p * a.q;
+  const int r0 = blockIdx.y * kPack, c0 = blockIdx.x * kPack;  // of h
+  const float* h = a.h + (size_t)l * a.p * a.ld;
+  const T* g = static_cast<const T*>(a.g) + n;
+  T* dg = static_cast<T*>(a.dg) + n;
+  if (a.tall) {
+    for (int i = threadIdx.x; i < kPack * kPack; i += kSumThreads) {
+      const int rr = i / kPack, c = i % kPack;
+      if (r0 + rr < a.p && c0 + c < a.q) tile[rr][c] = h[(size_t)(r0 + rr) * a.ld + c0 + c];
+    }
+    __syncthreads();
+  }
+  for (int i = threadIdx.x; i < kPack * kPack; i += kSumThreads) {
+    const int rr = a.tall ? i % kPack : i / kPack, c = a.tall ? i / kPack : i % kPack;
+    if (r0 + rr >= a.p || c0 + c >= a.q) continue;
+    const size_t at = a.tall ? (size_t)(c0 + c) * a.p + r0 + rr : (size_t)(r0 + rr) * a.q + c0 + c;
+    const float v = a.tall ? tile[rr][c] : h[(size_t)(r0 + rr) * a.ld + c0 + c];
+    dg[at] = from_f32<T>(fmaf(-by_g, to_f32<T>(g[at]), by_h * v));
+  }
+}
+
+// ---------------------------------------------------------------------------
+// Host: scales, workspace, launches
+// ---------------------------------------------------------------------------
+constexpr int kMaxSteps = 16;
+
+struct Plan {
+  int L, m, n, p, q, ldq, ldp, steps, bf16, keep, tall;
+  float eps;
+  float a[kMaxSteps], b[kMaxSteps], c[kMaxSteps];
+  int xe[kMaxSteps], ae[kMaxSteps], be[kMaxSteps];  // exponents of X, A, B as stored
+  int xt[kMaxSteps];                                // terms of X
+  double M[kMaxSteps + 1];                          // bound on X's singular values
+  int square_parts;
+  int kept() const { return keep ? steps : 1; }
+};
+
+int floor_log2(double x) { return (int)floor(log2(x)); }
+int store_exp(double bound) {  // entries up to 2^15
+  const int e = bound > 0 ? floor_log2(32768.0 / bound) : 12;
+  return e < 12 ? e : 12;
+}
+
+int make_plan(const fbob_orth_t* o, Plan* out) {
+  if (!o || !o->coefficients) return FBOB_ERR_INVALID_ARG;
+  if (o->L < 1 || o->m < 1 || o->n < 1 || o->steps < 1 || (o->keep & ~1)) return FBOB_ERR_INVALID_ARG;
+  if (!(o->eps >= 0.f) || o->eps > 3.0e38f) return FBOB_ERR_INVALID_ARG;
+  if (o->dtype != FBOB_BF16 && o->dtype != FBOB_FP32) return FBOB_ERR_UNSUPPORTED;
+  if (o->steps > kMaxSteps || o->L > 65535) return FBOB_ERR_UNSUPPORTED;
+  Plan p;
+  p.L = o->L; p.m = o->m; p.n = o->n;
+  p.p = o->m < o->n ? o->m : o->n;
+  p.q = o->m < o->n ? o->n : o->m;
+  p.tall = o->m > o->n;
+  // tiles and 64-wide pieces are counted in 32 bits, pieces of rows in a grid's y
+  if (p.p > (1 << 16) || p.q > (1 << 22) || (double)p.L * p.p * p.q > (double)(1ll << 36))
+    return FBOB_ERR_UNSUPPORTED;
+  p.ldq = (p.q + 7) / 8 * 8;
+  p.ldp = (p.p + 7) / 8 * 8;
+  p.steps = o->steps;
+  p.bf16 = o->dtype == FBOB_BF16;
+  p.keep = o->keep;
+  p.eps = o->eps;
+  double M = 1.0;
+  p.M[0] = M;
+  for (int i = 0; i < p.steps; ++i) {
+    const double a = o->coefficients[3 * i], b = o->coefficients[3 * i + 1], c = o->coefficients[3 * i + 2];
+    if (!(fabs(a) < 1e6 && fabs(b) < 1e6 && fabs(c) < 1e6)) return FBOB_ERR_INVALID_ARG;
+    p.a[i] = (float)a; p.b[i] = (float)b; p.c[i] = (float)c;
+    p.xe[i] = store_exp(M);
+    p.ae[i] = store_exp(M * M);
+    p.be[i] = store_exp(fabs(b) * M * M + fabs(c) * M * M * M * M);
+    double most = 0;  // of the polynomial up to M, which rounding may pass a little
+    for (int k = 0; k <= 1024; ++k) {
+      const double x = 1.01 * M * k / 1024, y = fabs(x * (a + x * x * (b + x * x * c)));
+      if (y > most) most = y;
+    }
+    M = 1.01 * most;
+    if (!(M < 64.0)) return FBOB_ERR_INVALID_ARG;  // singular values that run away
+    p.M[i + 1] = M;
+  }
+  // terms of X: the growth of a rounding error by the steps that follow
+  double growth = 1;
+  for (int i = p.steps - 1; i >= 0; --i) {
+    growth *= fabs(p.a[i]) > 1 ? fabs(p.a[i]) : 1;
+    // (a bf16 G is one fp16 term, times a power of two)
+    p.xt[i] = !p.bf16 || (growth > 16 && i > 0) ? 2 : 1;
+  }
+  const long long elems = (long long)p.p * p.q;
+  const long long parts = (elems + 8191) / 8192;
+  p.square_parts = (int)(parts < 1024 ? parts : 1024);
+  *out = p;
+  return FBOB_OK;
+}
+
+size_t terms_bytes(const Plan& p, int ld, int terms) {
+  return align_up((size_t)p.L * p.p * ld * sizeof(__half)) * terms;
+}
+
+struct Carver {
+  char* base;
+  size_t off;
+  void* take(size_t bytes) {
+    void* r = base ? base + off : nullptr;
+    off += align_up(bytes);
+    return r;
+  }
+  Terms terms(const Plan& p, int cols, int ld, int n) {
+    Terms t;
+    const size_t one = (size_t)p.L * p.p * ld * sizeof(__half);
+    t.hi = static_cast<__half*>(take(one));
+    t.lo = n == 2 ? static_cast<__half*>(take(one)) : nullptr;
+    t.rows = p.p; t.cols = cols; t.ld = ld;
+    return t;
+  }
+};
+
+int product_parts(const Plan& p) {  // sums of a [p, q] product
+  return ((p.p + kTile - 1) / kTile) * ((p.q + kTile - 1) / kTile) * kEpiWarps;
+}
+
+// Forward: [status][info][square sums], then X, A and B of each step (kept), or of two
+// and one (X in turn).
+struct Forward {
+  int* status;
+  MatInfo* info;
+  float* sums;
+  Terms X[kMaxSteps], A[kMaxSteps], B[kMaxSteps];
+  size_t bytes;
+};
+Forward carve_forward(const Plan& p, char* base) {
+  Forward w;
+  Carver c{base, 0};
+  w.status = static_cast<int*>(c.take(sizeof(int)));
+  w.info = static_cast<MatInfo*>(c.take(sizeof(MatInfo) * p.L));
+  w.sums = static_cast<float*>(c.take(sizeof(float) * p.L * p.square_parts));
+  const int small = p.bf16 ? 1 : 2;
+  for (int i = 0; i < p.steps; ++i) {
+    if (p.keep || i < 2) {
+      int t = p.xt[i];
+      if (!p.keep)  // room for every step that shares it
+        for (int k = i; k < p.steps; k += 2) t = p.xt[k] > t ? p.xt[k] : t;
+      w.X[i] = c.terms(p, p.q, p.ldq, t);
+    } else {
+      w.X[i] = w.X[i & 1];
+    }
+    if (p.xt[i] == 1) w.X[i].lo = nullptr;
+    if (p.keep || i == 0) {
+      w.A[i] = c.terms(p, p.p, p.ldp, small);
+      w.B[i] = c.terms(p, p.p, p.ldp, small);
+    } else {
+      w.A[i] = w.A[0];
+      w.B[i] = w.B[0];
+    }
+  }
+  w.bytes = c.off;
+  return w;
+}
+
+// Backward: [status][square sums of dY][exponents: steps + 1][sums of the steps'
+// results: two in turn], H in turn, S, T, dX_0 in fp32.
+struct Backward {
+  int* status;
+  float *sums, *first, *step_sums[2];
+  int* exp[kMaxSteps + 1];
+  Terms H[2], S, T;
+  float* h0;
+  size_t bytes;
+};
+Backward carve_backward(const Plan& p, char* base) {
+  Backward w;
+  Carver c{base, 0};
+  const int t = p.bf16 ? 1 : 2;
+  w.status = static_cast<int*>(c.take(sizeof(int)));
+  w.sums = static_cast<float*>(c.take(sizeof(float) * p.L * p.square_parts));
+  w.first = static_cast<float*>(c.take(sizeof(float) * p.L));
+  for (float*& s : w.step_sums) s = static_cast<float*>(c.take(sizeof(float) * p.L * product_parts(p)));
+  for (int i = 0; i <= p.steps; ++i) w.exp[i] = static_cast<int*>(c.take(sizeof(int) * p.L));
+  for (Terms& h : w.H) h = c.terms(p, p.q, p.ldq, t);
+  w.S = c.terms(p, p.p, p.ldp, t);
+  w.T = c.terms(p, p.p, p.ldp, t);
+  w.h0 = static_cast<float*>(c.take(sizeof(float) * p.L * p.p * p.ldq));
+  w.bytes = c.off;
+  return w;
+}
+
+// A map of [count][rows][ld] fp16, cols of each row; box: 64 columns, box_rows rows.
+bool make_half_map(CUtensorMap* m, const __half* ptr, int L, int rows, int cols, int ld, int box_rows) {
+  auto fn = encode_fn();
+  if (!fn) return false;
+  cuuint64_t dims[3] = {(cuuint64_t)cols, (cuuint64_t)rows, (cuuint64_t)L};
+  cuuint64_t strides[2] = {(cuuint64_t)ld * 2, (cuuint64_t)rows * ld * 2};
+  cuuint32_t box[3] = {kDepth, (cuuint32_t)box_rows, 1};
+  cuuint32_t es[3] = {1, 1, 1};
+  return fn(m, CU_TENSOR_MAP_DATA_TYPE_FLOAT16, 3, const_cast<__half*>(ptr), dims, strides, box, es,
+            CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
+            CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
+// Builds and launches one product.
+struct Product {
+  ProductArgs g;
+  int na = 0, nb = 0;
+  bool nn, ok = true;
+  Product(const Plan& p, const Terms& out, int depth, bool nn_, bool sym, int* status) : nn(nn_) {
+    memset(&g, 0, sizeof g);
+    g.rows = out.rows;
+    g.cols = out.cols;
+    g.depth = depth;
+    g.count = p.L;
+    g.sym = sym;
+    g.status = status;
+    g.wait_ns = wait_limit_ns();
+  }
+  // acc += P Q^T (or P Q): every pair of terms but the two low ones
+  void add(const Terms& P, const Terms& Q) {
+    const int a0 = na, b0 = nb;
+    const int b_rows = nn ? kDepth : kTile;
+    ok = ok && make_half_map(&g.a[na++], P.hi, g.count, P.rows, P.cols, P.ld, kTile);
+    if (P.lo) ok = ok && make_half_map(&g.a[na++], P.lo, g.count, P.rows, P.cols, P.ld, kTile);
+    ok = ok && make_half_map(&g.b[nb++], Q.hi, g.count, Q.rows, Q.cols, Q.ld, b_rows);
+    if (Q.lo) ok = ok && make_half_map(&g.b[nb++], Q.lo, g.count, Q.rows, Q.cols, Q.ld, b_rows);
+    pair(a0, b0);
+    if (Q.lo) pair(a0, b0 + 1);
+    if (P.lo) pair(a0 + 1, b0);
+  }
+  void pair(int a, int b) {
+    g.seg_a[g.nseg] = (unsigned char)a;
+    g.seg_b[g.nseg++] = (unsigned char)b;
+  }
+  void plus(const Terms& E) {
+    g.e.ehi = E.hi;
+    g.e.elo = E.lo;
+    g.e.elds = E.ld;
+  }
+  void to(const Terms& O) {
+    g.e.ohi = O.hi;
+    g.e.olo = O.lo;
+    g.e.olds = O.ld;
+  }
+  cudaError_t launch(LaunchLog& log) {
+    if (!ok) return cudaErrorUnknown;
+    const int tm = (g.rows + kTile - 1) / kTile, tn = (g.cols + kTile - 1) / kTile;
+    const long long tiles = (long long)g.count * (g.sym ? (long long)tm * (tm + 1) / 2 : (long long)tm * tn);
+    const int grid = (int)(tiles < kSms ? tiles : kSms);
+    cudaError_t e = cudaFuncSetAttribute(nn ? product<true> : product<false>,
+                                         cudaFuncAttributeMaxDynamicSharedMemorySize, kSmem);
+    if (e != cudaSuccess) return e;
+    if (nn) product<true><<<grid, kThreads, kSmem, log.stream>>>(g);
+    else product<false><<<grid, kThreads, kSmem, log.stream>>>(g);
+    e = cudaGetLastError();
+    log.mark();
+    return e;
+  }
+};
+
+cudaError_t squares_and_pack(const Plan& p, const void* x, float* sums, int* status, PackArgs a,
+                             LaunchLog& log) {
+  const size_t elems = (size_t)p.p * p.q;
+  const dim3 grid((unsigned)p.square_parts, (unsigned)p.L);
+  if (p.bf16)
+    square_sums<<<grid, kSumThreads, 0, log.stream>>>(static_cast<const __nv_bfloat16*>(x), sums, elems, status);
+  else
+    square_sums<<<grid, kSumThreads, 0, log.stream>>>(static_cast<const float*>(x), sums, elems, status);
+  cudaError_t e = cudaGetLastError();
+  log.mark();
+  if (e != cudaSuccess) return e;
+  a.x = x;
+  a.sums = sums;
+  a.parts = p.square_parts;
+  a.p = p.p; a.q = p.q; a.ld = p.ldq; a.tall = p.tall;
+  a.eps = p.eps;
+  const dim3 tiles((unsigned)((p.q + kPack - 1) / kPack), (unsigned)((p.p + kPack - 1) / kPack), (unsigned)p.L);
+  if (p.bf16) pack<__nv_bfloat16><<<tiles, kSumThreads, 0, log.stream>>>(a);
+  else pack<float><<<tiles, kSumThreads, 0, log.stream>>>(a);
+  e = cudaGetLastError();
+  log.mark();
+  return e;
+}
+
+float pow2(int e) { return ldexpf(1.f, e); }
+
+cudaError_t forward(const Plan& p, const void* G, void* Y, const Forward& w, LaunchLog& log) {
+  PackArgs a = {};
+  a.hi = w.X[0].hi;
+  a.lo = w.X[0].lo;
+  a.target = p.xe[0];
+  a.info = w.info;
+  cudaError_t e = squares_and_pack(p, G, w.sums, w.status, a, log);
+  for (int i = 0; e == cudaSuccess && i < p.steps; ++i) {
+    const Terms &X = w.X[i], &A = w.A[i], &B = w.B[i];
+    {
+      Product g(p, A, p.q, false, true, w.status);
+      g.add(X, X);
+      g.g.e.alpha = pow2(p.ae[i] - 2 * p.xe[i]);
+      if (i == 0) {
+        g.g.e.info = w.info;
+        g.g.e.fpow = 2;
+      }
+      g.to(A);
+      e = g.launch(log);
+    }
+    if (e != cudaSuccess) break;
+    {
+      Product g(p, B, p.p, false, true, w.status);
+      g.add(A, A);
+      g.plus(A);
+      g.g.e.alpha = p.c[i] * pow2(p.be[i] - 2 * p.ae[i]);
+      g.g.e.beta = p.b[i] * pow2(p.be[i] - p.ae[i]);
+      g.to(B);
+      e = g.launch(log);
+    }
+    if (e != cudaSuccess) break;
+    const bool last = i + 1 == p.steps;
+    Product g(p, X, p.p, true, false, w.status);
+    g.add(B, X);
+    g.plus(X);
+    const int out = last ? 0 : p.xe[i + 1];
+    g.g.e.alpha = pow2(out - p.be[i] - p.xe[i]);
+    g.g.e.beta = p.a[i] * pow2(out - p.xe[i]);
+    if (i == 0) {
+      g.g.e.info = w.info;
+      g.g.e.fpow = 1;
+    }
+    if (last) {
+      g.g.e.y = Y;
+      g.g.e.y_bf16 = p.bf16;
+      g.g.e.y_transposed = p.tall;
+    } else {
+      g.to(w.X[i + 1]);
+    }
+    e = g.launch(log);
+  }
+  return e;
+}
+
+cudaError_t backward(const Plan& p, const void* G, const void* dY, void* dG, const Forward& f,
+                     const Backward& w, LaunchLog& log) {
+  // H's norm is brought to 2^target: every entry of H, S, T and of the next H stays below
+  // 2^15 whatever their directions
+  int target[kMaxSteps], se[kMaxSteps];
+  for (int i = 0; i < p.steps; ++i) {
+    const double M = p.M[i], a = fabs(p.a[i]), b = fabs(p.b[i]), c = fabs(p.c[i]);
+    const double growth = a + 3 * b * M * M + 5 * c * M * M * M * M;
+    const double t = (b + 2 * c * M * M) * 2 * M;
+    double most = 15 - log2(growth > 1 ? growth : 1);
+    const double by_t = 15 - log2(t > 1e-30 ? t : 1e-30) - (p.be[i] - p.xe[i]);
+    if (by_t < most) most = by_t;
+    target[i] = (int)floor(most) < 12 ? (int)floor(most) : 12;
+    se[i] = store_exp(pow2(target[i]) * 2 * M);
+  }
+  const int top = p.steps - 1;
+  PackArgs a = {};
+  a.hi = w.H[0].hi;
+  a.lo = w.H[0].lo;
+  a.target = target[top];
+  a.exp_out = w.exp[p.steps];
+  a.sums_out = w.first;
+  cudaError_t e = squares_and_pack(p, dY, w.sums, w.status, a, log);
+  const float* sums = w.first;
+  int parts = 1, turn = 0;
+  for (int i = top; e == cudaSuccess && i >= 0; --i, turn ^= 1) {
+    const Terms &H = w.H[turn], &A = f.A[i], &B = f.B[i];
+    Terms X = f.X[i];
+    if (p.bf16) X.lo = nullptr;  // its rounding is not multiplied by later steps here
+    {
+      Product g(p, w.S, p.q, false, true, w.status);
+      g.add(H, X);
+      g.add(X, H);
+      g.g.e.alpha = pow2(se[i] - p.xe[i]);
+      if (i == 0) {
+        g.g.e.info = f.info;
+        g.g.e.fpow = 1;
+      }
+      g.to(w.S);
+      e = g.launch(log);
+    }
+    if (e != cudaSuccess) break;
+    const int te = p.be[i] - p.xe[i];  // T X and B H share an accumulator
+    {
+      Product g(p, w.T, p.p, false, true, w.status);
+      g.add(A, w.S);
+      g.add(w.S, A);
+      g.plus(w.S);
+      g.g.e.alpha = p.c[i] * pow2(te - p.ae[i] - se[i]);
+      g.g.e.beta = p.b[i] * pow2(te - se[i]);
+      if (i == 0) {  // X_0 is f times what is stored
+        g.g.e.info = f.info;
+        g.g.e.fpow = 1;
+      }
+      g.to(w.T);
+      e = g.launch(log);
+    }
+    if (e != cudaSuccess) break;
+    Product g(p, H, p.p, true, false, w.status);
+    g.add(B, H);
+    g.add(w.T, X);
+    g.plus(H);
+    g.g.e.alpha = pow2(-p.be[i]);
+    g.g.e.beta = p.a[i];
+    g.g.e.sums = w.step_sums[turn];
+    if (i > 0) {
+      g.g.e.scale_sums = sums;
+      g.g.e.scale_parts = parts;
+      g.g.e.target = target[i - 1];
+      g.g.e.exp_in = w.exp[i + 1];
+      g.g.e.exp_out = w.exp[i];
+      g.to(w.H[turn ^ 1]);
+    } else {
+      g.g.e.of32 = w.h0;
+      g.g.e.olds = p.ldq;
+      g.g.e.dhi = f.X[0].hi;
+      g.g.e.dlo = f.X[0].lo;
+    }
+    sums = w.step_sums[turn];
+    parts = product_parts(p);
+    e = g.launch(log);
+  }
+  if (e != cudaSuccess) return e;
+  EndArgs n = {};
+  n.g = G;
+  n.dg = dG;
+  n.h = w.h0;
+  n.dots = sums;
+  n.parts = parts;
+  n.p = p.p; n.q = p.q; n.ld = p.ldq; n.tall = p.tall; n.x_exp = p.xe[0];
+  n.info = f.info;
+  n.exp = w.exp[1];
+  const dim3 tiles((unsigned)((p.q + kPack - 1) / kPack), (unsigned)((p.p + kPack - 1) / kPack), (unsigned)p.L);
+  if (p.bf16) end_gradient<__nv_bfloat16><<<tiles, kSumThreads, 0, log.stream>>>(n);
+  else end_gradient<float><<<tiles, kSumThreads, 0, log.stream>>>(n);
+  e = cudaGetLastError();
+  log.mark();
+  return e;
+}
+
+bool off(const void* p, size_t n) { return reinterpret_cast<uintptr_t>(p) % n != 0; }
+
+}  // namespace
+}  // namespace fbob
+
+using namespace fbob;
+
+extern "C" {
+
+size_t fbob_orth_workspace_size(int op, const fbob_orth_t* o) {
+  Plan p;
+  if (op != FBOB_OP_FORWARD && op != FBOB_OP_BACKWARD) return 0;
+  if (make_plan(o, &p) != FBOB_OK) return 0;
+  return op == FBOB_OP_FORWARD ? carve_forward(p, nullptr).bytes : carve_backward(p, nullptr).bytes;
+}
+
+int fbob_orth_forward(const fbob_orth_t* o, const void* g, void* y, void* ws, size_t ws_bytes,
+                      void* stream) {
+  Plan p;
+  const int st = make_plan(o, &p);
+  if (st != FBOB_OK) return st;
+  const size_t size = p.bf16 ? 2 : 4;
+  if (!g || !y || !ws || off(g, size) || off(y, size) || off(ws, 256)) return FBOB_ERR_INVALID_ARG;
+  const Forward w = carve_forward(p, static_cast<char*>(ws));
+  if (ws_bytes < w.bytes) return FBOB_ERR_WORKSPACE;
+  LaunchLog log{static_cast<cudaStream_t>(stream)};
+  begin_call(log);
+  const cudaError_t e = forward(p, g, y, w, log);
+  end_call(log);
+  return e == cudaSuccess ? FBOB_OK : FBOB_ERR_CUDA;
+}
+
+int fbob_orth_backward(const fbob_orth_t* o, const void* g, const void* dy, void* dg, const void* kept,
+                       size_t kept_bytes, void* ws, size_t ws_bytes, void* stream) {
+  Plan p;
+  const int st = make_plan(o, &p);
+  if (st != FBOB_OK) return st;
+  const size_t size = p.bf16 ? 2 : 4;
+  if (!p.keep || !g || !dy || !dg || !kept || !ws || off(g, size) || off(dy, size) || off(dg, size) ||
+      off(kept, 256) || off(ws, 256))
+    return FBOB_ERR_INVALID_ARG;
+  const Forward f = carve_forward(p, const_cast<char*>(static_cast<const char*>(kept)));
+  const Backward w = carve_backward(p, static_cast<char*>(ws));
+  if (kept_bytes < f.bytes || ws_bytes < w.bytes) return FBOB_ERR_WORKSPACE;
+  LaunchLog log{static_cast<cudaStream_t>(stream)};
+  begin_call(log);
+  const cudaError_t e = backward(p, g, dy, dg, f, w, log);
+  end_call(log);
+  return e == cudaSuccess ? FBOB_OK : FBOB_ERR_CUDA;
+}
+
+}  // extern "C"

@@ -1,0 +1,596 @@
+// Norms of queries and keys for each head, with the rotary positions in the
+// same pass.  A row x of d features at position p becomes
+//   y = R (w . n),   n = r x,   r = (<x, x> / d + eps)^(-1/2),
+// with R the rotation of its feature pairs by p (times the magnitude; features
+// that are not turned stay).  With g = R^T dy and h = w . g, the gradients are
+//   dx = r (h - n <h, n> / d),   dw = sum over rows of g . n,
+// and for cotangents a of dx and c of dw, with t = r (a - n <a, n> / d) and
+// u = c . g - (r / d) (<a, n> h + <h, n> a), those of x, w and dy are
+//   gx = r (u - n <u, n> / d) - (r / d) <h, t> n,   gw = sum over rows of g . t,
+//   gdy = R (w . t + c . n).
+// Every inner product is one with x, times a power of r, or <h, a>: all of a row's
+// sums are made in one exchange, before r is known, and each row is read once.
+//
+// Bound: memory.  A group of lanes holds a row (two runs of P elements a lane, as
+// the rotation pairs them) and walks over heads of one position, so that a sine and
+// cosine serve them all; queries and keys are one launch.  The sums over rows
+// are carried in registers by blocks that stay (a few per SM), added up in the block
+// through shared memory, and over the blocks by a second launch: every sum in a
+// fixed order.
+#include <cuda_bf16.h>
+#include <cuda_runtime.h>
+#include <stdint.h>
+
+#include "common.cuh"
+#include "internal.h"
+#include "ops.h"
+#include "rotary.cuh"
+
+namespace fbob {
+namespace {
+
+using namespace rope;
+
+constexpr int kThreads = 128;
+constexpr int kMaxDim = 256;
+
+// One tensor's part of a call, as the kernels read it.
+struct Side {
+  const void *x, *w, *dy, *a, *c;
+  void *y, *ddy;
+  long long xs[3], dys[3], as[3], ys[3], ddys[3];  // over batch, head, position, in elements
+  int H, heads, groups;  // heads per unit, units per block of positions
+  int blocks;            // thread blocks that work on it
+  long long units;
+  bool sums;             // the gradient of w is wanted
+};
+
+struct NormArgs {
+  Side side[2];
+  const double* inv_freq;
+  const long long* positions;  // null: offset + n
+  long long pos_sb, offset;
+  float* partial;              // [blocks with sums][d]
+  int B, N, d, half;           // half = rotary_dim / 2 pairs
+  int lanes;                   // lanes of a row: a power of two
+  int w_bf16;
+  float eps, inv_d, magnitude;
+};
+
+// A lane's features of a row: C chunks of two runs of P.
+template <int P, int C>
+struct Row {
+  float u[C][P], v[C][P];
+};
+
+// Which features a lane holds.
+template <int P, int C>
+struct Place {
+  int e0[C], e1[C];
+  bool one[C], two[C], turned[C];
+  __device__ __forceinline__ Place(const NormArgs& a, int lane, bool interleaved) {
+    const int chunks = a.d / (2 * P) + (P == 1 ? (a.d & 1) : 0), rot = a.half / P;
+#pragma unroll
+    for (int j = 0; j < C; ++j) {
+      const int c = lane + j * a.lanes;
+      one[j] = c < chunks;
+      turned[j] = c < rot;
+      if (turned[j]) {
+        e0[j] = interleaved ? 2 * P * c : P * c;
+        e1[j] = interleaved ? e0[j] + P : e0[j] + a.half;
+      } else {
+        e0[j] = 2 * a.half + (c - rot) * 2 * P;
+        e1[j] = e0[j] + P;
+      }
+      two[j] = one[j] && e1[j] < a.d;  // not for an odd width's last feature
+    }
+  }
+};
+
+template <typename T, int P, int C>
+struct Raw {
+  Vec<T, P> u[C], v[C];
+  __device__ __forceinline__ void load(const T* p, const Place<P, C>& at) {
+#pragma unroll
+    for (int j = 0; j < C; ++j) {
+      if (at.one[j]) u[j].load(p + at.e0[j]);
+      if (at.two[j]) v[j].load(p + at.e1[j]);
+    }
+  }
+  __device__ __forceinline__ void get(Row<P, C>& r, const Place<P, C>& at) const {
+#pragma unroll
+    for (int j = 0; j < C; ++j) {
+#pragma unroll
+      for (int i = 0; i < P; ++i) r.u[j][i] = r.v[j][i] = 0.f;
+      if (at.one[j]) u[j].get(r.u[j]);
+      if (at.two[j]) v[j].get(r.v[j]);
+    }
+  }
+};
+
+template <typename T, int P, int C>
+__device__ __forceinline__ void put(T* p, const Row<P, C>& r, const Place<P, C>& at) {
+#pragma unroll
+  for (int j = 0; j < C; ++j) {
+    Vec<T, P> t;
+    if (at.one[j]) {
+      t.set(r.u[j]);
+      t.store(p + at.e0[j]);
+    }
+    if (at.two[j]) {
+      t.set(r.v[j]);
+      t.store(p + at.e1[j]);
+    }
+  }
+}
+
+// f of each of the lane's features, with its index i in the run
+#define FBOB_EACH(j, i) \
+  _Pragma("unroll") for (int j = 0; j < C; ++j) _Pragma("unroll") for (int i = 0; i < P; ++i)
+
+template <int P, int C>
+__device__ __forceinline__ float dot(const Row<P, C>& a, const Row<P, C>& b) {
+  float s = 0.f;
+  FBOB_EACH(j, i) s = fmaf(a.u[j][i], b.u[j][i], fmaf(a.v[j][i], b.v[j][i], s));
+  return s;
+}
+
+// Sums over the lanes of a row, every lane its own copy.
+template <int K>
+__device__ __forceinline__ void row_sums(float (&s)[K], int lanes) {
+  for (int o = lanes >> 1; o > 0; o >>= 1) {
+#pragma unroll
+    for (int k = 0; k < K; ++k) s[k] += __shfl_xor_sync(0xffffffffu, s[k], o);
+  }
+}
+
+// The turning of a row at one position: cosines and sines (with the magnitude).
+template <int P, int C>
+struct Angles {
+  float cs[C][P], sn[C][P];
+  __device__ __forceinline__ void at(long long p, const unsigned long long* turns, int lane, int lanes,
+                                     const Place<P, C>& place, float magnitude) {
+#pragma unroll
+    for (int j = 0; j < C; ++j) {
+      if (!place.turned[j]) continue;
+#pragma unroll
+      for (int i = 0; i < P; ++i) {
+        const unsigned long long t =
+            (unsigned long long)p * turns[(lane + j * lanes) * P + i];
+        float s, c;
+        sincos_turns((uint32_t)((t + 0x80000000ull) >> 32), s, c);
+        cs[j][i] = c * magnitude;
+        sn[j][i] = s * magnitude;
+      }
+    }
+  }
+  template <bool INTERLEAVED, bool INVERSE>
+  __device__ __forceinline__ void apply(Row<P, C>& r, const Place<P, C>& place) const {
+#pragma unroll
+    for (int j = 0; j < C; ++j) {
+      if (!place.turned[j]) continue;
+      if (INVERSE) {
+        float back[P];
+#pragma unroll
+        for (int i = 0; i < P; ++i) back[i] = -sn[j][i];
+        turn<P, INTERLEAVED>(r.u[j], r.v[j], cs[j], back);
+      } else {
+        turn<P, INTERLEAVED>(r.u[j], r.v[j], cs[j], sn[j]);
+      }
+    }
+  }
+};
+
+__device__ __forceinline__ float vector_at(const void* p, int bf16, int i) {
+  return bf16 ? __bfloat162float(static_cast<const __nv_bfloat16*>(p)[i])
+              : static_cast<const float*>(p)[i];
+}
+
+// A [d] vector from shared memory, at the lane's features.
+template <int P, int C>
+__device__ __forceinline__ void from_shared(Row<P, C>& r, const float* v, const Place<P, C>& at) {
+  FBOB_EACH(j, i) {
+    r.u[j][i] = at.one[j] ? v[at.e0[j] + i] : 0.f;
+    r.v[j][i] = at.two[j] ? v[at.e1[j] + i] : 0.f;
+  }
+}
+
+enum { kForward, kBackward, kSecond };
+
+// Rows whose loads are in flight together.
+template <int OP, typename TI, typename TO, int P, int C>
+constexpr int kRows = C > 1 ? 1 : OP == kForward ? (sizeof(TI) == 2 ? 4 : 2)
+                              : OP == kBackward  ? 2
+                                                 : 1;
+
+// Shared memory: [half] angles of one position, [d] w, [d] c; then, for the sums
+// at the end, [rows of a block][d].
+template <int OP, typename TI, typename TO, int P, int C, bool INTERLEAVED>
+__global__ void __launch_bounds__(kThreads) norm_kernel(const __grid_constant__ NormArgs a) {
+  extern __shared__ unsigned long long turns[];
+  float* const sw = reinterpret_cast<float*>(turns + a.half);
+  float* const sc = sw + a.d;
+  constexpr int U = kRows<OP, TI, TO, P, C>;
+  const bool second_side = blockIdx.x >= (unsigned)a.side[0].blocks;
+  const Side& s = a.side[second_side];
+  const int block = blockIdx.x - (second_side ? a.side[0].blocks : 0);
+  const int lane = threadIdx.x & (a.lanes - 1), group = threadIdx.x / a.lanes;
+  const int per_block = kThreads / a.lanes;  // positions of a unit
+  const Place<P, C> place(a, lane, INTERLEAVED);
+
+  turns_table<kThreads>(turns, a.inv_freq, a.half);
+  for (int i = threadIdx.x; i < a.d; i += kThreads) {
+    sw[i] = s.w ? vector_at(s.w, a.w_bf16, i) : 1.f;
+    if (OP == kSecond) sc[i] = s.c ? vector_at(s.c, a.w_bf16, i) : 0.f;
+  }
+  __syncthreads();
+  Row<P, C> w, c, acc;
+  from_shared(w, sw, place);
+  if (OP == kSecond) from_shared(c, sc, place);
+  FBOB_EACH(j, i) acc.u[j][i] = acc.v[j][i] = 0.f;
+
+  const long long items = (long long)a.B * a.N;
+  for (long long unit = block; unit < s.units; unit += s.blocks) {
+    const long long ib = unit / s.groups;
+    const int h0 = (int)(unit - ib * s.groups) * s.heads, h1 = min(s.H, h0 + s.heads);
+    const long long item = ib * per_block + group;
+    const bool active = item < items;  // the other groups' lanes only take part in exchanges
+    const long long b = active ? item / a.N : 0, n = active ? item - b * a.N : 0;
+    const TI* __restrict__ x = static_cast<const TI*>(s.x) + b * s.xs[0] + n * s.xs[2];
+    const TO* __restrict__ dy = static_cast<const TO*>(s.dy) + b * s.dys[0] + n * s.dys[2];
+    const TI* __restrict__ ca = static_cast<const TI*>(s.a) + b * s.as[0] + n * s.as[2];
+    Angles<P, C> angles;
+    const long long pos = !active ? 0 : a.positions ? a.positions[b * a.pos_sb + n] : a.offset + n;
+    for (int hb = h0; hb < h1; hb += U) {
+      Raw<TI, P, C> rx[U], ra[U];
+      Raw<TO, P, C> rdy[U];
+#pragma unroll
+      for (int i = 0; i < U; ++i)
+        if (active && hb + i < h1) {
+          rx[i].load(x + (hb + i) * s.xs[1], place);
+          if (OP != kForward) rdy[i].load(dy + (hb + i) * s.dys[1], place);
+          if (OP == kSecond && s.a) ra[i].load(ca + (hb + i) * s.as[1], place);
+        }
+      if (hb == h0) angles.at(pos, turns, lane, a.lanes, place, a.magnitude);
+#pragma unroll
+      for (int k = 0; k < U; ++k) {
+        if (hb + k >= h1) break;  // the same for the whole block
+        Row<P, C> xv, g, av;
+        if (active) {
+          rx[k].get(xv, place);
+          if (OP != kForward) rdy[k].get(g, place);
+        } else {
+          FBOB_EACH(j, i) xv.u[j][i] = xv.v[j][i] = g.u[j][i] = g.v[j][i] = 0.f;
+        }
+        if (OP == kForward) {
+          float sum[1] = {dot(xv, xv)};
+          row_sums(sum, a.lanes);
+          const float r = rsqrtf(fmaf(sum[0], a.inv_d, a.eps));
+          FBOB_EACH(j, i) {
+            xv.u[j][i] *= r * w.u[j][i];
+            xv.v[j][i] *= r * w.v[j][i];
+          }
+          angles.template apply<INTERLEAVED, false>(xv, place);
+          if (active)
+            put<TO, P, C>(static_cast<TO*>(s.y) + b * s.ys[0] + (hb + k) * s.ys[1] + n * s.ys[2], xv,
+                          place);
+        } else if (OP == kBackward) {
+          angles.template apply<INTERLEAVED, true>(g, place);
+          float sum[2] = {dot(xv, xv), 0.f};
+          FBOB_EACH(j, i) sum[1] = fmaf(w.u[j][i] * g.u[j][i], xv.u[j][i],
+                                        fmaf(w.v[j][i] * g.v[j][i], xv.v[j][i], sum[1]));
+          row_sums(sum, a.lanes);
+          const float r = rsqrtf(fmaf(sum[0], a.inv_d, a.eps));
+          const float back = r * r * sum[1] * a.inv_d;  // dx = r (h - back x)
+          FBOB_EACH(j, i) {
+            acc.u[j][i] = fmaf(g.u[j][i], r * xv.u[j][i], acc.u[j][i]);
+            acc.v[j][i] = fmaf(g.v[j][i], r * xv.v[j][i], acc.v[j][i]);
+            xv.u[j][i] = r * fmaf(-back, xv.u[j][i], w.u[j][i] * g.u[j][i]);
+            xv.v[j][i] = r * fmaf(-back, xv.v[j][i], w.v[j][i] * g.v[j][i]);
+          }
+          if (active)
+            put<TI, P, C>(static_cast<TI*>(s.y) + b * s.ys[0] + (hb + k) * s.ys[1] + n * s.ys[2], xv,
+                          place);
+        } else {
+          if (active && s.a) {
+            ra[k].get(av, place);
+          } else {
+            FBOB_EACH(j, i) av.u[j][i] = av.v[j][i] = 0.f;
+          }
+          angles.template apply<INTERLEAVED, true>(g, place);
+          // <x, x>, <h, x>, <a, x>, <h, a>, <c . g, x>
+          float sum[5] = {dot(xv, xv), 0.f, dot(av, xv), 0.f, 0.f};
+          FBOB_EACH(j, i) {
+            const float hu = w.u[j][i] * g.u[j][i], hv = w.v[j][i] * g.v[j][i];
+            sum[1] = fmaf(hu, xv.u[j][i], fmaf(hv, xv.v[j][i], sum[1]));
+            sum[3] = fmaf(hu, av.u[j][i], fmaf(hv, av.v[j][i], sum[3]));
+            sum[4] = fmaf(c.u[j][i] * g.u[j][i], xv.u[j][i],
+                          fmaf(c.v[j][i] * g.v[j][i], xv.v[j][i], sum[4]));
+          }
+          row_sums(sum, a.lanes);
+          const float r = rsqrtf(fmaf(sum[0], a.inv_d, a.eps));
+          const float hn = r * sum[1] * a.inv_d, an = r * sum[2] * a.inv_d;  // <h, n> / d, <a, n> / d
+          const float ht = r * (sum[3] - r * sum[1] * an);                   // <h, t>
+          const float un = r * a.inv_d * sum[4] - 2.f * r * an * hn;         // <u, n> / d
+          // gx = r (u - back x), t = r (a - at x)
+          const float back = r * (un + ht * a.inv_d), at = an * r;
+          FBOB_EACH(j, i) {
+            const float xu = xv.u[j][i], xw = xv.v[j][i], au = av.u[j][i], aw = av.v[j][i];
+            const float gu = g.u[j][i], gw = g.v[j][i];
+            const float tu = r * fmaf(-at, xu, au), tw = r * fmaf(-at, xw, aw);
+            acc.u[j][i] = fmaf(gu, tu, acc.u[j][i]);
+            acc.v[j][i] = fmaf(gw, tw, acc.v[j][i]);
+            const float uu = c.u[j][i] * gu - r * (an * (w.u[j][i] * gu) + hn * au);
+            const float uw = c.v[j][i] * gw - r * (an * (w.v[j][i] * gw) + hn * aw);
+            g.u[j][i] = fmaf(w.u[j][i], tu, c.u[j][i] * (r * xu));
+            g.v[j][i] = fmaf(w.v[j][i], tw, c.v[j][i] * (r * xw));
+            xv.u[j][i] = r * fmaf(-back, xu, uu);
+            xv.v[j][i] = r * fmaf(-back, xw, uw);
+          }
+          angles.template apply<INTERLEAVED, false>(g, place);
+          if (active) {
+            put<TI, P, C>(static_cast<TI*>(s.y) + b * s.ys[0] + (hb + k) * s.ys[1] + n * s.ys[2], xv,
+                          place);
+            put<TO, P, C>(
+                static_cast<TO*>(s.ddy) + b * s.ddys[0] + (hb + k) * s.ddys[1] + n * s.ddys[2], g,
+                place);
+          }
+        }
+      }
+    }
+  }
+  if (OP == kForward || !s.sums) return;
+  float* const red = sc + (OP == kSecond ? a.d : 0);  // [per_block][d]
+  FBOB_EACH(j, i) {
+    if (place.one[j]) red[group * a.d + place.e0[j] + i] = acc.u[j][i];
+    if (place.two[j]) red[group * a.d + place.e1[j] + i] = acc.v[j][i];
+  }
+  __syncthreads();
+  float* const out = a.partial + ((size_t)(second_side && a.side[0].sums ? a.side[0].blocks : 0) + block) * a.d;
+  for (int i = threadIdx.x; i < a.d; i += kThreads) {
+    float t = 0.f;
+    for (int k = 0; k < per_block; ++k) t += red[k * a.d + i];
+    out[i] = t;
+  }
+}
+
+// dw[i] = sum over the blocks' partial sums: 32 features and 32 parts of the blocks
+// to a thread block.
+struct SumArgs {
+  void* out[2];
+  int first[2], blocks[2];
+  const float* partial;
+  int d, bf16;
+};
+__global__ void __launch_bounds__(1024) norm_sums(SumArgs a) {
+  __shared__ float sm[32][33];
+  const int t = blockIdx.y, f = blockIdx.x * 32 + (threadIdx.x & 31), part = threadIdx.x >> 5;
+  float s = 0.f;
+  if (f < a.d)
+    for (int b = part; b < a.blocks[t]; b += 32) s += a.partial[((size_t)a.first[t] + b) * a.d + f];
+  sm[part][threadIdx.x & 31] = s;
+  __syncthreads();
+  s = warp_sum(sm[threadIdx.x & 31][part]);
+  const int g = blockIdx.x * 32 + part;
+  if ((threadIdx.x & 31) == 0 && g < a.d && a.out[t]) {
+    if (a.bf16) static_cast<__nv_bfloat16*>(a.out[t])[g] = __float2bfloat16_rn(s);
+    else static_cast<float*>(a.out[t])[g] = s;
+  }
+}
+
+// Blocks that carry sums: this many per SM in all.
+constexpr int kBlocksPerSm = 6;
+
+// Lanes of a row, heads of a unit and blocks of each tensor.  A unit takes as
+// many heads (up to 16) as leave half a wave of threads, so that few sines are
+// computed; one where the call is small and latency counts.  Without sums a block
+// takes one unit.
+void plan(NormArgs& a, int P, int C, bool stay) {
+  const int chunks = a.d / (2 * P) + (P == 1 ? (a.d & 1) : 0);
+  int lanes = 1;
+  while (lanes < 32 && lanes < (chunks + C - 1) / C) lanes *= 2;
+  a.lanes = lanes;
+  const long long blocks = ((long long)a.B * a.N * lanes + kThreads - 1) / kThreads;
+  int heads = 16;
+  long long units = 0;
+  for (;; heads /= 2) {
+    units = 0;
+    for (Side& s : a.side) {
+      s.heads = heads;
+      s.groups = (s.H + heads - 1) / heads;
+      s.units = blocks * s.groups;
+      units += s.units;
+    }
+    if (heads == 1 || units * kThreads >= kSms * 1024ll) break;
+  }
+  const long long most = kSms * kBlocksPerSm;
+  for (Side& s : a.side) {
+    long long n = s.units;
+    if (!stay) n = n < (1ll << 30) ? n : 1ll << 30;
+    else if (units > most) n = s.units * most / units;
+    s.blocks = (int)(n > 0 ? n : s.units > 0 ? 1 : 0);
+  }
+}
+
+template <int OP, typename TI, typename TO, int P, int C, bool INTERLEAVED>
+cudaError_t launch(NormArgs& a, LaunchLog& log) {
+  plan(a, P, C, OP != kForward && (a.side[0].sums || a.side[1].sums));
+  size_t smem = sizeof(unsigned long long) * a.half + sizeof(float) * a.d * (OP == kSecond ? 2 : 1);
+  smem += OP == kForward ? 0 : sizeof(float) * a.d * (kThreads / a.lanes);
+  norm_kernel<OP, TI, TO, P, C, INTERLEAVED>
+      <<<(unsigned)(a.side[0].blocks + a.side[1].blocks), kThreads, smem, log.stream>>>(a);
+  const cudaError_t e = cudaGetLastError();
+  log.mark();
+  return e;
+}
+
+template <typename T>
+bool aligned_rows(const void* p, const long long (&st)[3], int P) {
+  const long long bytes = P * (long long)sizeof(T) < 16 ? P * (long long)sizeof(T) : 16;
+  if (!p) return true;
+  bool ok = reinterpret_cast<uintptr_t>(p) % bytes == 0;
+  for (long long x : st) ok = ok && x * (long long)sizeof(T) % bytes == 0;
+  return ok;
+}
+
+// Whether chunks of P pairs tile the turned and the other part, and every access is
+// aligned (16 bytes, or all P elements where they are fewer).  32 lanes hold a row of
+// kMaxDim features at P = 4.
+template <int OP, typename TI, typename TO, int P>
+bool chunked(const NormArgs& a) {
+  bool ok = a.half % P == 0 && (a.d - 2 * a.half) % (2 * P) == 0;
+  for (const Side& s : a.side) {
+    if (!s.H) continue;
+    ok = ok && aligned_rows<TI>(s.x, s.xs, P);
+    ok = ok && (OP == kForward ? aligned_rows<TO>(s.y, s.ys, P) : aligned_rows<TI>(s.y, s.ys, P));
+    if (OP != kForward) ok = ok && aligned_rows<TO>(s.dy, s.dys, P);
+    if (OP == kSecond)
+      ok = ok && aligned_rows<TI>(s.a, s.as, P) && aligned_rows<TO>(s.ddy, s.ddys, P);
+  }
+  return ok;
+}
+
+template <int OP, typename TI, typename TO, bool IL>
+cudaError_t dispatch(NormArgs& a, LaunchLog& log) {
+  if (chunked<OP, TI, TO, 8>(a)) return launch<OP, TI, TO, 8, 1, IL>(a, log);
+  if (chunked<OP, TI, TO, 4>(a)) return launch<OP, TI, TO, 4, 1, IL>(a, log);
+  return launch<OP, TI, TO, 1, 4, IL>(a, log);
+}
+
+template <int OP>
+cudaError_t dispatch(NormArgs& a, bool bi, bool bo, bool il, LaunchLog& log) {
+  using H = __nv_bfloat16;
+  if (bi && bo) return il ? dispatch<OP, H, H, true>(a, log) : dispatch<OP, H, H, false>(a, log);
+  if (bi) return il ? dispatch<OP, H, float, true>(a, log) : dispatch<OP, H, float, false>(a, log);
+  if (bo) return il ? dispatch<OP, float, H, true>(a, log) : dispatch<OP, float, H, false>(a, log);
+  return il ? dispatch<OP, float, float, true>(a, log) : dispatch<OP, float, float, false>(a, log);
+}
+
+size_t workspace_bytes(const fbob_qk_norm_t* s) {
+  return ((size_t)kSms * kBlocksPerSm + 2) * s->d * sizeof(float);
+}
+
+bool off(const void* p, size_t n) { return reinterpret_cast<uintptr_t>(p) % n != 0; }
+
+int check(const fbob_qk_norm_t* s) {
+  if (!s) return FBOB_ERR_INVALID_ARG;
+  if (s->B < 1 || s->N < 1 || s->d < 1 || s->rotary_dim < 0 || s->rotary_dim > s->d ||
+      (s->rotary_dim & 1) || (s->interleaved & ~1))
+    return FBOB_ERR_INVALID_ARG;
+  if (!(s->eps >= 0.f) || !(s->magnitude == s->magnitude)) return FBOB_ERR_INVALID_ARG;
+  for (int dt : {s->in_dtype, s->out_dtype, s->weight_dtype})
+    if (dt != FBOB_BF16 && dt != FBOB_FP32) return FBOB_ERR_UNSUPPORTED;
+  return s->d > kMaxDim ? FBOB_ERR_UNSUPPORTED : FBOB_OK;
+}
+
+int call(int op, const fbob_qk_norm_t* s, const fbob_norm_side_t* q, const fbob_norm_side_t* k,
+         const double* inv_freq, const long long* positions, void* ws, size_t ws_bytes, void* stream) {
+  const int st = check(s);
+  if (st != FBOB_OK) return st;
+  if (!q || (s->rotary_dim > 0 && !inv_freq) || off(inv_freq, 8) || off(positions, 8))
+    return FBOB_ERR_INVALID_ARG;
+  const size_t si = s->in_dtype == FBOB_BF16 ? 2 : 4, so = s->out_dtype == FBOB_BF16 ? 2 : 4;
+  const size_t sw = s->weight_dtype == FBOB_BF16 ? 2 : 4;
+  NormArgs a = {};
+  double heads = 0;
+  bool sums = false;
+  for (int i = 0; i < 2; ++i) {
+    const fbob_norm_side_t* f = i ? k : q;
+    if (!f) continue;
+    Side& t = a.side[i];
+    if (f->H < 1 || !f->x || !f->y) return FBOB_ERR_INVALID_ARG;
+    if (off(f->x, si) || off(f->y, op == kForward ? so : si) || off(f->weight, sw))
+      return FBOB_ERR_INVALID_ARG;
+    if (op != kForward && (!f->dy || off(f->dy, so) || off(f->dweight, sw))) return FBOB_ERR_INVALID_ARG;
+    if (op == kSecond && (!f->ddy || off(f->ddy, so) || off(f->a, si) || off(f->c, sw)))
+      return FBOB_ERR_INVALID_ARG;
+    t.H = f->H;
+    t.x = f->x; t.w = f->weight; t.y = f->y;
+    if (op != kForward) {
+      t.dy = f->dy;
+      t.sums = f->dweight != nullptr;
+    }
+    if (op == kSecond) {
+      t.a = f->a; t.c = f->c; t.ddy = f->ddy;
+    }
+    for (int j = 0; j < 3; ++j) {
+      t.xs[j] = f->x_strides[j];
+      t.dys[j] = f->dy_strides[j];
+      t.as[j] = f->a_strides[j];
+      t.ys[j] = f->y_strides[j];
+      t.ddys[j] = f->ddy_strides[j];
+    }
+    heads += f->H;
+    sums = sums || t.sums;
+  }
+  if (heads > 65535.0 || heads * s->B * s->N * s->d > (double)(1ll << 38)) return FBOB_ERR_UNSUPPORTED;
+  if (sums) {
+    if (!ws || off(ws, 16)) return FBOB_ERR_INVALID_ARG;
+    if (ws_bytes < workspace_bytes(s)) return FBOB_ERR_WORKSPACE;
+  }
+  a.inv_freq = inv_freq;
+  a.positions = positions;
+  a.pos_sb = s->pos_stride;
+  a.offset = s->offset;
+  a.partial = static_cast<float*>(ws);
+  a.B = s->B; a.N = s->N; a.d = s->d;
+  a.half = s->rotary_dim / 2;
+  a.w_bf16 = s->weight_dtype == FBOB_BF16;
+  a.eps = s->eps;
+  a.inv_d = 1.f / (float)s->d;
+  a.magnitude = s->magnitude;
+  LaunchLog log{static_cast<cudaStream_t>(stream)};
+  begin_call(log);
+  const bool bi = s->in_dtype == FBOB_BF16, bo = s->out_dtype == FBOB_BF16, il = s->interleaved != 0;
+  cudaError_t e = op == kForward    ? dispatch<kForward>(a, bi, bo, il, log)
+                  : op == kBackward ? dispatch<kBackward>(a, bi, bo, il, log)
+                                    : dispatch<kSecond>(a, bi, bo, il, log);
+  if (e == cudaSuccess && sums) {
+    SumArgs r = {};
+    int first = 0;
+    for (int i = 0; i < 2; ++i) {
+      r.out[i] = a.side[i].sums ? (i ? k : q)->dweight : nullptr;
+      r.first[i] = first;
+      r.blocks[i] = a.side[i].sums ? a.side[i].blocks : 0;
+      first += r.blocks[i];
+    }
+    r.partial = a.partial;
+    r.d = a.d;
+    r.bf16 = a.w_bf16;
+    norm_sums<<<dim3((unsigned)(a.d + 31) / 32, 2), 1024, 0, log.stream>>>(r);
+    e = cudaGetLastError();
+    log.mark();
+  }
+  end_call(log);
+  return e == cudaSuccess ? FBOB_OK : FBOB_ERR_CUDA;
+}
+
+}  // namespace
+}  // namespace fbob
+
+using namespace fbob;
+
+extern "C" {
+
+size_t fbob_qk_norm_workspace_size(const fbob_qk_norm_t* s) {
+  return check(s) == FBOB_OK ? workspace_bytes(s) : 0;
+}
+
+int fbob_qk_norm_forward(const fbob_qk_norm_t* s, const fbob_norm_side_t* q, const fbob_norm_side_t* k,
+                         const double* inv_freq, const long long* positions, void* stream) {
+  return call(kForward, s, q, k, inv_freq, positions, nullptr, 0, stream);
+}
+
+int fbob_qk_norm_backward(const fbob_qk_norm_t* s, const fbob_norm_side_t* q, const fbob_norm_side_t* k,
+                          const double* inv_freq, const long long* positions, void* ws,
+                          size_t ws_bytes, void* stream) {
+  return call(kBackward, s, q, k, inv_freq, positions, ws, ws_bytes, stream);
+}
+
+int fbob_qk_norm_bob(const fbob_qk_norm_t* s, const fbob_norm_side_t* q, const fbob_norm_side_t* k,
+                     const double* inv_freq, const long long* positions, void* ws, size_t ws_bytes,
+                     void* stream) {
+  return call(kSecond, s, q, k, inv_freq, positions, ws, ws_bytes, stream);
+}
+
+}  // extern "C"

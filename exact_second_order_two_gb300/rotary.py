@@ -92,6 +92,34 @@ def _turn(x, inv_freq, positions, how, strides):
     return y
 
 
+def _angles(inv_freq, positions, x):
+    """inv_freq and positions checked for x [B, H, N, d], as the calls read
+    them: (inv_freq, positions [B, N] or None, the first position without)."""
+    if inv_freq.dtype != torch.float64 or inv_freq.dim() != 1 or inv_freq.device != x.device:
+        raise ValueError(f"inv_freq must be a float64 vector on {x.device}")
+    if inv_freq.requires_grad or _b.dual(inv_freq):
+        raise ValueError("inv_freq is not differentiated: pass it detached")
+    if 2 * inv_freq.numel() > x.shape[-1]:
+        raise ValueError(f"inv_freq turns {2 * inv_freq.numel()} features of {x.shape[-1]}")
+    if not inv_freq.is_contiguous():
+        inv_freq = inv_freq.contiguous()
+    offset = 0
+    if positions is not None and not torch.is_tensor(positions):
+        offset, positions = operator.index(positions), None
+        if not -(1 << 62) <= offset < 1 << 62:
+            raise ValueError(f"position {offset} is out of range")
+    if positions is not None:
+        B, N = x.shape[0], x.shape[2]
+        if positions.dtype != torch.int64 or positions.device != x.device or \
+                tuple(positions.shape) not in ((N,), (B, N)):
+            raise ValueError(f"positions must be int64 [{N}] or [{B}, {N}] on {x.device}")
+        if positions.dim() == 1:
+            positions = positions.expand(B, N)
+        if positions.stride(1) != 1 and N > 1:
+            positions = positions.contiguous()
+    return inv_freq, positions, offset
+
+
 class _Rotary(torch.autograd.Function):
     """x -> rotary(x); its backward is itself with the angle negated."""
 
@@ -135,28 +163,7 @@ def rotary(x: torch.Tensor, inv_freq: torch.Tensor, positions=None, *, interleav
     dtype = x.dtype if dtype is None else dtype
     if x.dtype not in _b.DTYPES or dtype not in _b.DTYPES:
         raise TypeError(f"unsupported dtypes {x.dtype}, {dtype}; use bfloat16 or float32")
-    if inv_freq.dtype != torch.float64 or inv_freq.dim() != 1 or inv_freq.device != x.device:
-        raise ValueError(f"inv_freq must be a float64 vector on {x.device}")
-    if inv_freq.requires_grad or _b.dual(inv_freq):
-        raise ValueError("inv_freq is not differentiated: pass it detached")
-    if 2 * inv_freq.numel() > x.shape[-1]:
-        raise ValueError(f"inv_freq turns {2 * inv_freq.numel()} features of {x.shape[-1]}")
-    if not inv_freq.is_contiguous():
-        inv_freq = inv_freq.contiguous()
-    offset = 0
-    if positions is not None and not torch.is_tensor(positions):
-        offset, positions = operator.index(positions), None
-        if not -(1 << 62) <= offset < 1 << 62:
-            raise ValueError(f"position {offset} is out of range")
-    if positions is not None:
-        B, N = x.shape[0], x.shape[2]
-        if positions.dtype != torch.int64 or positions.device != x.device or \
-                tuple(positions.shape) not in ((N,), (B, N)):
-            raise ValueError(f"positions must be int64 [{N}] or [{B}, {N}] on {x.device}")
-        if positions.dim() == 1:
-            positions = positions.expand(B, N)
-        if positions.stride(1) != 1 and N > 1:
-            positions = positions.contiguous()
+    inv_freq, positions, offset = _angles(inv_freq, positions, x)
     # without autograd's node where no derivative can follow
     seen = (x.requires_grad and torch.is_grad_enabled()) or _b.dual(x)
     turn = _Rotary.apply if seen else _turn

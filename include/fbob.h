@@ -298,6 +298,64 @@ int fbob_diff_backward(const fbob_diff_shape_t* shape, const void* q, const void
                        const float* lse, const void* dO, void* dq, void* dk, void* dv, void* dlam,
                        void* ws, size_t ws_bytes, void* stream);
 
+/* ------------------------------------------------------------------------
+ * Norms of queries and keys for each head, with rotary positions
+ * ------------------------------------------------------------------------
+ * Each row x of d features becomes y = R (w * n), n = x (<x, x> / d + eps)^-1/2,
+ * with w one weight per feature and R the turn by position of fbob_rotary
+ * (magnitude included; features past rotary_dim are not turned).  One call
+ * takes queries and keys, which share batch, length, width, types and positions
+ * and differ in heads; either can come alone, as `q` with `k` NULL.
+ *
+ * Tensors are [B,H,N,d] with feature stride 1 and strides over batch, head and
+ * position in elements: x, its gradients and a in in_dtype; y, dy and ddy in
+ * out_dtype; weights, their gradients and c in weight_dtype, [d].  Outputs
+ * overlap neither inputs nor one another.  Arithmetic is fp32, rounded once;
+ * sums over rows are added in a fixed order: equal inputs give equal bits.
+ * d <= 256, all heads together <= 65535, elements together <= 2^38. */
+typedef struct {
+  int B, N, d;
+  int rotary_dim;          /* even, 0 <= rotary_dim <= d                     */
+  int interleaved;         /* 0 or 1                                         */
+  int in_dtype, out_dtype, weight_dtype; /* fbob_dtype_t                     */
+  float eps;               /* >= 0                                           */
+  float magnitude;
+  long long pos_stride;    /* elements between the batches of `positions`    */
+  long long offset;        /* position of row 0 where `positions` is NULL    */
+} fbob_qk_norm_t;
+
+/* One tensor of a call.  What a call does not name is not read. */
+typedef struct {
+  int H;
+  const void *x, *weight;  /* weight NULL: ones                              */
+  const void *dy;          /* backward, bob                                  */
+  const void *a, *c;       /* bob: cotangents of dx and dweight, NULL: zero  */
+  void *y;                 /* out: y, or dx, or the gradient of x            */
+  void *dweight;           /* out, NULL: not wanted                          */
+  void *ddy;               /* bob, out: the gradient of dy                   */
+  long long x_strides[3], dy_strides[3], a_strides[3], y_strides[3], ddy_strides[3];
+} fbob_norm_side_t;
+
+/* Bytes of workspace for a call that writes a dweight (others need none, and
+ * take ws NULL); 0 if the problem is invalid. */
+size_t fbob_qk_norm_workspace_size(const fbob_qk_norm_t* s);
+
+/* y of each tensor. */
+int fbob_qk_norm_forward(const fbob_qk_norm_t* s, const fbob_norm_side_t* q,
+                         const fbob_norm_side_t* k, const double* inv_freq,
+                         const long long* positions, void* stream);
+
+/* Gradients of <dy, y>: dx into `y`, and dweight. */
+int fbob_qk_norm_backward(const fbob_qk_norm_t* s, const fbob_norm_side_t* q,
+                          const fbob_norm_side_t* k, const double* inv_freq,
+                          const long long* positions, void* ws, size_t ws_bytes, void* stream);
+
+/* Gradients of <a, dx> + <c, dweight>: of x into `y`, of the weight into
+ * `dweight`, of dy into `ddy`. */
+int fbob_qk_norm_bob(const fbob_qk_norm_t* s, const fbob_norm_side_t* q,
+                     const fbob_norm_side_t* k, const double* inv_freq,
+                     const long long* positions, void* ws, size_t ws_bytes, void* stream);
+
 /* Library ABI version (major*100 + minor). */
 int fbob_version(void);
 
