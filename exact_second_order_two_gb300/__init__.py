@@ -31,6 +31,7 @@ from ._binding import (  # noqa: F401
 )
 from .autograd import attention  # noqa: F401
 from .diff_attention import diff_attention, diff_backward, diff_forward  # noqa: F401
+from .orthogonalize import orthogonalize  # noqa: F401
 from .qk_norm import qk_norm_rotary  # noqa: F401
 from .rotary import rotary, rotary_frequencies  # noqa: F401
 from . import meta  # noqa: F401

@@ -70,6 +70,12 @@ class QkNorm(ctypes.Structure):
                 ("offset", ctypes.c_longlong)]
 
 
+class Orth(ctypes.Structure):
+    _fields_ = [("L", ctypes.c_int), ("m", ctypes.c_int), ("n", ctypes.c_int),
+                ("dtype", ctypes.c_int), ("steps", ctypes.c_int), ("keep", ctypes.c_int),
+                ("eps", ctypes.c_float), ("coefficients", ctypes.c_void_p)]
+
+
 class NormSide(ctypes.Structure):
     _fields_ = [("H", ctypes.c_int)] + \
         [(n, ctypes.c_void_p) for n in ("x", "weight", "dy", "a", "c", "y", "dweight", "ddy")] + \
@@ -104,6 +110,9 @@ _SIGNATURES = {
     "fbob_diff_forward": (ctypes.c_int, [_P] * 9 + [_SZ, _P]),
     "fbob_diff_backward": (ctypes.c_int, [_P] * 14 + [_SZ, _P]),
     "fbob_rotary": (ctypes.c_int, [_P] * 6),
+    "fbob_orth_workspace_size": (_SZ, [ctypes.c_int, _P]),
+    "fbob_orth_forward": (ctypes.c_int, [_P] * 4 + [_SZ, _P]),
+    "fbob_orth_backward": (ctypes.c_int, [_P] * 5 + [_SZ, _P, _SZ, _P]),
     "fbob_qk_norm_workspace_size": (_SZ, [_P]),
     "fbob_qk_norm_forward": (ctypes.c_int, [_P] * 6),
     "fbob_qk_norm_backward": (ctypes.c_int, [_P] * 6 + [_SZ, _P]),

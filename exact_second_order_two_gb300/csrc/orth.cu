@@ -26,6 +26,7 @@
 #include <cuda_fp16.h>
 #include <cuda_runtime.h>
 #include <math.h>
+#include <string.h>
 #include <stdint.h>
 
 #include "common.cuh"
@@ -56,7 +57,6 @@ struct MatInfo {
 struct Terms {
   __half *hi = nullptr, *lo = nullptr;
   int rows = 0, cols = 0, ld = 0;
-  int terms() const { return lo ? 2 : 1; }
 };
 
 // ---------------------------------------------------------------------------
@@ -95,7 +95,7 @@ struct Epilogue {
   int* exp_out;
 };
 
-struct __align__(64) ProductArgs {
+struct ProductArgs {
   CUtensorMap a[4], b[4];
   unsigned char seg_a[kMaxSegs], seg_b[kMaxSegs];
   int nseg;
@@ -608,7 +608,6 @@ struct Plan {
   int xt[kMaxSteps];                                // terms of X
   double M[kMaxSteps + 1];                          // bound on X's singular values
   int square_parts;
-  int kept() const { return keep ? steps : 1; }
 };
 
 int floor_log2(double x) { return (int)floor(log2(x)); }
@@ -669,10 +668,6 @@ int make_plan(const fbob_orth_t* o, Plan* out) {
   return FBOB_OK;
 }
 
-size_t terms_bytes(const Plan& p, int ld, int terms) {
-  return align_up((size_t)p.L * p.p * ld * sizeof(__half)) * terms;
-}
-
 struct Carver {
   char* base;
   size_t off;
@@ -711,15 +706,14 @@ Forward carve_forward(const Plan& p, char* base) {
   w.info = static_cast<MatInfo*>(c.take(sizeof(MatInfo) * p.L));
   w.sums = static_cast<float*>(c.take(sizeof(float) * p.L * p.square_parts));
   const int small = p.bf16 ? 1 : 2;
+  Terms turn[2];  // without keep: room for every step that shares one
+  for (int i = 0; !p.keep && i < 2; ++i) {
+    int t = 1;
+    for (int k = i; k < p.steps; k += 2) t = p.xt[k] > t ? p.xt[k] : t;
+    turn[i] = c.terms(p, p.q, p.ldq, t);
+  }
   for (int i = 0; i < p.steps; ++i) {
-    if (p.keep || i < 2) {
-      int t = p.xt[i];
-      if (!p.keep)  // room for every step that shares it
-        for (int k = i; k < p.steps; k += 2) t = p.xt[k] > t ? p.xt[k] : t;
-      w.X[i] = c.terms(p, p.q, p.ldq, t);
-    } else {
-      w.X[i] = w.X[i & 1];
-    }
+    w.X[i] = p.keep ? c.terms(p, p.q, p.ldq, p.xt[i]) : turn[i & 1];
     if (p.xt[i] == 1) w.X[i].lo = nullptr;
     if (p.keep || i == 0) {
       w.A[i] = c.terms(p, p.p, p.ldp, small);
@@ -776,7 +770,7 @@ bool make_half_map(CUtensorMap* m, const __half* ptr, int L, int rows, int cols,
 // Builds and launches one product.
 struct Product {
   ProductArgs g;
-  int na = 0, nb = 0;
+  int na = 0, nb = 0, high_a[2], high_b[2], highs = 0;
   bool nn, ok = true;
   Product(const Plan& p, const Terms& out, int depth, bool nn_, bool sym, int* status) : nn(nn_) {
     memset(&g, 0, sizeof g);
@@ -796,9 +790,10 @@ struct Product {
     if (P.lo) ok = ok && make_half_map(&g.a[na++], P.lo, g.count, P.rows, P.cols, P.ld, kTile);
     ok = ok && make_half_map(&g.b[nb++], Q.hi, g.count, Q.rows, Q.cols, Q.ld, b_rows);
     if (Q.lo) ok = ok && make_half_map(&g.b[nb++], Q.lo, g.count, Q.rows, Q.cols, Q.ld, b_rows);
-    pair(a0, b0);
     if (Q.lo) pair(a0, b0 + 1);
     if (P.lo) pair(a0 + 1, b0);
+    high_a[highs] = a0;
+    high_b[highs++] = b0;
   }
   void pair(int a, int b) {
     g.seg_a[g.nseg] = (unsigned char)a;
@@ -816,6 +811,9 @@ struct Product {
   }
   cudaError_t launch(LaunchLog& log) {
     if (!ok) return cudaErrorUnknown;
+    // The products of high terms come last: the tensor cores cut every addition off to the
+    // accumulator's 24 bits, which costs nothing while it holds the small ones only.
+    for (int i = 0; i < highs; ++i) pair(high_a[i], high_b[i]);
     const int tm = (g.rows + kTile - 1) / kTile, tn = (g.cols + kTile - 1) / kTile;
     const long long tiles = (long long)g.count * (g.sym ? (long long)tm * (tm + 1) / 2 : (long long)tm * tn);
     const int grid = (int)(tiles < kSms ? tiles : kSms);

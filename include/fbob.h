@@ -356,6 +356,44 @@ int fbob_qk_norm_bob(const fbob_qk_norm_t* s, const fbob_norm_side_t* q,
                      const fbob_norm_side_t* k, const double* inv_freq,
                      const long long* positions, void* ws, size_t ws_bytes, void* stream);
 
+/* ------------------------------------------------------------------------
+ * Orthogonalised updates
+ * ------------------------------------------------------------------------
+ * Newton-Schulz products of each of L matrices G [m,n]:
+ *   X = G / (|G|_F + eps);   steps times:  A = X X^T, X = a X + (b A + c A^2) X
+ * (A = X^T X, from the other side, where m > n).  coefficients: a, b, c of each
+ * step, 3 * steps floats in host memory, read during the call.  They must
+ * hold singular values that start in [0, 1] below 64; an infinite or NaN
+ * entry spoils its matrix.
+ * g, y, dy and dg are dense [L,m,n] of `dtype`, aligned to their elements;
+ * workspaces to 256 bytes.  Operands are fp16, one term for bf16 tensors (two for X
+ * where later steps would enlarge its rounding), two for fp32; sums are fp32,
+ * in a fixed order: equal inputs give equal bits.
+ * steps <= 16, min(m, n) <= 65536, max(m, n) <= 2^22, L <= 65535,
+ * L*m*n <= 2^36. */
+typedef struct {
+  int L, m, n;
+  int dtype;               /* fbob_dtype_t                                   */
+  int steps;
+  int keep;                /* 1: a backward follows                          */
+  float eps;               /* >= 0                                           */
+  const float* coefficients;
+} fbob_orth_t;
+
+/* Bytes of workspace of `op` (FBOB_OP_FORWARD or FBOB_OP_BACKWARD), 0 if the
+ * problem is invalid.  Status words are read with fbob_status(). */
+size_t fbob_orth_workspace_size(int op, const fbob_orth_t* o);
+
+/* y = G orthogonalised.  With keep = 1 the workspace holds what the backward
+ * reads until then. */
+int fbob_orth_forward(const fbob_orth_t* o, const void* g, void* y, void* ws, size_t ws_bytes,
+                      void* stream);
+
+/* Gradient of <dy, y> with respect to g; `kept` is the forward's workspace. */
+int fbob_orth_backward(const fbob_orth_t* o, const void* g, const void* dy, void* dg,
+                       const void* kept, size_t kept_bytes, void* ws, size_t ws_bytes,
+                       void* stream);
+
 /* Library ABI version (major*100 + minor). */
 int fbob_version(void);
 
