@@ -18,14 +18,19 @@
 // polynomials), so that one power of two for all of X, A and B keeps them inside fp16's
 // range, with 11 bits down to 2^-26 of the bound; H is rescaled every step by the norm
 // that it was measured to have.  fp32 tensors are held as the sum of two fp16 (22 bits)
-// and multiplied in three products; bf16 tensors in one, except that X takes two terms
-// in steps whose rounding later steps would multiply by more than 16: a rounding
-// error of X off its strong directions grows by a every step.
+// and multiplied in three products; bf16 tensors in one.  There, a rounding error of X
+// between its weak directions grows by a every step.  It reaches them through a X alone
+// (B is small there, and an error of A or of B X lies in a strong direction on one side),
+// so that X is kept in two terms, of which the products take the first and a X
+// both, in steps whose rounding later steps would multiply by more than 16.
+// (256 x 1024 of rank 16 with noise of a hundredth: 1.6e-2 of the norm off with one term,
+// 2.2e-3 with two, 1.7e-3 for the result's own rounding.)
 #include <cuda.h>
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
 #include <cuda_runtime.h>
 #include <math.h>
+#include <stdlib.h>
 #include <string.h>
 #include <stdint.h>
 
@@ -69,8 +74,8 @@ constexpr uint32_t kTileBytes = kTile * kDepth * 2;
 constexpr uint32_t kStageBytes = 2 * kTileBytes;
 constexpr uint32_t kOffMisc = kStages * kStageBytes;
 constexpr uint32_t kSmem = kOffMisc + 512;
-constexpr int kEpiWarps = 4, kProducerWarp = 4, kMmaWarp = 5;
-constexpr int kThreads = 192;
+constexpr int kEpiWarps = 8, kProducerWarp = 8, kMmaWarp = 9;
+constexpr int kThreads = 320;
 constexpr int kMaxSegs = 6;
 
 struct Epilogue {
@@ -268,10 +273,11 @@ __device__ __forceinline__ int rescaling(float nu2, int target) {
 }
 
 // acc = sum over segments of P Q^T (Q stored [cols, depth]) or P Q (NN: Q stored
-// [depth, cols]); blocks stay and take tiles in turn.  Warps: 4 finish tiles, one
+// [depth, cols]); blocks stay and take tiles in turn.  Warps: 8 finish tiles, one
 // loads, one multiplies; two accumulators, so that a tile is finished while the next
-// is multiplied.
-template <bool NN>
+// is multiplied.  CTAS = 2: a pair of CTAs multiplies a tile of 256 x 256, each loading its
+// 128 rows of P and 128 columns of Q, CTA 0 issuing for both.
+template <int CTAS, bool NN>
 __global__ void __launch_bounds__(kThreads, 1) product(const __grid_constant__ ProductArgs g) {
   extern __shared__ __align__(1024) uint8_t smem[];
   const uint32_t sb = smem_u32(smem);
@@ -287,7 +293,9 @@ __global__ void __launch_bounds__(kThreads, 1) product(const __grid_constant__ P
   uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(smem + kOffMisc + 256);
   Abort* ab = reinterpret_cast<Abort*>(smem + kOffMisc + 264);
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  constexpr uint32_t kCols = 2 * kTile;
+  const uint32_t rank = CTAS == 2 ? cluster_rank() : 0;
+  constexpr int kSide = kTile * CTAS;
+  constexpr uint32_t kCols = 2 * kSide;
   if (threadIdx.x == 0) {
     for (int s = 0; s < kStages; ++s) {
       mbar_init(full + s, 1);
@@ -295,7 +303,7 @@ __global__ void __launch_bounds__(kThreads, 1) product(const __grid_constant__ P
     }
     for (int b = 0; b < 2; ++b) {
       mbar_init(t_full + b, 1);
-      mbar_init(t_empty + b, kEpiWarps);
+      mbar_init(t_empty + b, kEpiWarps * CTAS);
     }
     mbar_init(drain, 1);
     ab->flag = 0;
@@ -303,24 +311,32 @@ __global__ void __launch_bounds__(kThreads, 1) product(const __grid_constant__ P
     fence_mbar_init();
   }
   if (warp == kMmaWarp) {
-    tmem_alloc(tmem_slot, kCols);
-    tmem_relinquish();
+    if (CTAS == 2) {
+      tmem_alloc_pair(tmem_slot, kCols);
+      tmem_relinquish_pair();
+    } else {
+      tmem_alloc(tmem_slot, kCols);
+      tmem_relinquish();
+    }
   }
   tc_fence_before();
   __syncthreads();
+  if (CTAS == 2) cluster_sync();  // the other's barriers are there
   tc_fence_after();
   const uint32_t tmem = *tmem_slot;
-  const int tm = (g.rows + kTile - 1) / kTile, tn = (g.cols + kTile - 1) / kTile;
-  const int tiles = g.count * (g.sym ? tm * (tm + 1) / 2 : tm * tn);
+  const int tm = (g.rows + kSide - 1) / kSide, tn = (g.cols + kSide - 1) / kSide;
+  const int per = g.sym ? tm * (tm + 1) / 2 : tm * tn;
+  const int tiles = g.count * per;
   const int blocks = (g.depth + kDepth - 1) / kDepth;
+  const int first = blockIdx.x / CTAS, step = gridDim.x / CTAS;
 
   if (warp == kProducerWarp) {
     if (lane == 0) {
       int it = 0;
       bool ok = true;
-      for (int t = blockIdx.x; ok && t < tiles; t += gridDim.x) {
-        const TileAt at = tile_at(g, t, kTile);
-        const int row = at.i * kTile, col = at.j * kTile;
+      for (int t = first; ok && t < tiles; t += step) {
+        const TileAt at = tile_at(g, t, kSide);
+        const int row = at.i * kSide + rank * kTile, col = at.j * kSide + rank * kTile;
         for (int sg = 0; ok && sg < g.nseg; ++sg) {
           const CUtensorMap* ma = &g.a[g.seg_a[sg]];
           const CUtensorMap* mb = &g.b[g.seg_b[sg]];
@@ -334,57 +350,84 @@ __global__ void __launch_bounds__(kThreads, 1) product(const __grid_constant__ P
               ok = false;
               break;
             }
-            uint8_t* dst = smem + s * kStageBytes;
-            mbar_arrive_expect_tx(full + s, kStageBytes);
-            tma_load_3d(dst, ma, full + s, k * kDepth, row, at.l);
-            if (NN) {
-              tma_load_3d(dst + kTileBytes, mb, full + s, col, k * kDepth, at.l);
-              tma_load_3d(dst + kTileBytes + kTileBytes / 2, mb, full + s, col + 64, k * kDepth, at.l);
+            uint8_t *pa = smem + s * kStageBytes, *pb = pa + kTileBytes;
+            if (rank == 0) mbar_arrive_expect_tx(full + s, CTAS * kStageBytes);
+            if (CTAS == 2) {
+              const uint32_t bar = cluster_addr(full + s, 0);
+              tma_load_3d_pair(pa, ma, bar, k * kDepth, row, at.l);
+              if (NN) {
+                tma_load_3d_pair(pb, mb, bar, col, k * kDepth, at.l);
+                tma_load_3d_pair(pb + kTileBytes / 2, mb, bar, col + 64, k * kDepth, at.l);
+              } else {
+                tma_load_3d_pair(pb, mb, bar, k * kDepth, col, at.l);
+              }
             } else {
-              tma_load_3d(dst + kTileBytes, mb, full + s, k * kDepth, col, at.l);
+              tma_load_3d(pa, ma, full + s, k * kDepth, row, at.l);
+              if (NN) {
+                tma_load_3d(pb, mb, full + s, col, k * kDepth, at.l);
+                tma_load_3d(pb + kTileBytes / 2, mb, full + s, col + 64, k * kDepth, at.l);
+              } else {
+                tma_load_3d(pb, mb, full + s, k * kDepth, col, at.l);
+              }
             }
           }
         }
       }
-      // every load this thread issued has landed before the block exits
-      for (int u = max(0, it - kStages); u < it; ++u)
-        mbar_wait_bounded(full + u % kStages, (u / kStages) & 1, g.status, 100000000ull);
+      // every load issued has landed before the block exits: CTA 0 sees the barriers
+      // that count both CTAs' loads; what an abort leaves uncounted gets a fixed time
+      if (rank == 0)
+        for (int u = max(0, it - kStages); u < it; ++u)
+          mbar_wait_bounded(full + u % kStages, (u / kStages) & 1, g.status, 100000000ull);
+      if (CTAS == 2 && ab->flag) {
+        const uint64_t t0 = global_ns();
+        while (global_ns() - t0 < 10000000ull) __nanosleep(10000);
+      }
     }
   } else if (warp == kMmaWarp) {
-    constexpr uint32_t id = idesc_f16(kTile, kTile, NN);
-    int it = 0, n = 0;
-    bool ok = true;
-    for (int t = blockIdx.x; ok && t < tiles; t += gridDim.x, ++n) {
-      const uint32_t d = tmem + (n & 1) * kTile;
-      if (n >= 2 && !warp_wait(t_empty + (n & 1), ((n >> 1) - 1) & 1, ab, g.status)) break;
-      tc_fence_after();
-      const int total = g.nseg * blocks;
-      for (int k = 0; k < total; ++k, ++it) {
-        const int s = it % kStages;
-        if (!warp_wait(full + s, (it / kStages) & 1, ab, g.status)) {
-          ok = false;
-          break;
-        }
+    if (rank == 0) {
+      constexpr uint32_t id = idesc_f16(kSide, kSide, NN);
+      int it = 0, n = 0;
+      bool ok = true;
+      for (int t = first; ok && t < tiles; t += step, ++n) {
+        const uint32_t d = tmem + (n & 1) * kSide;
+        if (n >= 2 && !warp_wait(t_empty + (n & 1), ((n >> 1) - 1) & 1, ab, g.status)) break;
         tc_fence_after();
-        const uint32_t a_lo = opaque(lo_kmajor(sb + s * kStageBytes));
-        const uint32_t b_at = sb + s * kStageBytes + kTileBytes;
-        const uint32_t b_lo = opaque(NN ? lo_mnmajor(b_at, kTileBytes / 2) : lo_kmajor(b_at));
+        const int total = g.nseg * blocks;
+        for (int k = 0; k < total; ++k, ++it) {
+          const int s = it % kStages;
+          if (!warp_wait(full + s, (it / kStages) & 1, ab, g.status)) {
+            ok = false;
+            break;
+          }
+          tc_fence_after();
+          const uint32_t a_lo = opaque(lo_kmajor(sb + s * kStageBytes));
+          const uint32_t b_at = sb + s * kStageBytes + kTileBytes;
+          const uint32_t b_lo = opaque(NN ? lo_mnmajor(b_at, kTileBytes / 2) : lo_kmajor(b_at));
 #pragma unroll
-        for (int u = 0; u < kDepth / 16; ++u)
-          mma_ss_w(d, a_lo + 2 * u, b_lo + (NN ? kstep_off(u) : 2 * u), id, k + u > 0 ? 1u : 0u);
-        mma_commit_w(empty + s);
+          for (int u = 0; u < kDepth / 16; ++u) {
+            const uint32_t al = a_lo + 2 * u, bl = b_lo + (NN ? kstep_off(u) : 2 * u);
+            if (CTAS == 2) mma_ss_pair_w(d, al, bl, id, k + u > 0 ? 1u : 0u);
+            else mma_ss_w(d, al, bl, id, k + u > 0 ? 1u : 0u);
+          }
+          if (CTAS == 2) mma_commit_pair_w(empty + s, 3);
+          else mma_commit_w(empty + s);
+        }
+        if (!ok) break;
+        if (CTAS == 2) mma_commit_pair_w(t_full + (n & 1), 3);
+        else mma_commit_w(t_full + (n & 1));
       }
-      if (ok) mma_commit_w(t_full + (n & 1));
+      // every MMA this warp issued has completed before TMEM is released
+      if (CTAS == 2) mma_commit_pair_w(drain, 1);
+      else mma_commit_w(drain);
+      mbar_wait_bounded(drain, 0, g.status, 100000000ull);
     }
-    // every MMA this warp issued has completed before TMEM is released
-    mma_commit_w(drain);
-    mbar_wait_bounded(drain, 0, g.status, 100000000ull);
   } else {
     const Epilogue& e = g.e;
-    const uint32_t lane_off = (uint32_t)(32 * warp) << 16;
+    const uint32_t lane_off = (uint32_t)(32 * (warp & 3)) << 16;
+    const int half = (warp >> 2) * (kSide / 2);  // of the columns
     int n = 0, scaled = -1, shift = 0;
-    for (int t = blockIdx.x; t < tiles; t += gridDim.x, ++n) {
-      const TileAt at = tile_at(g, t, kTile);
+    for (int t = first; t < tiles; t += step, ++n) {
+      const TileAt at = tile_at(g, t, kSide);
       float alpha = e.alpha, beta = e.beta;
       if (e.fpow) {
         const float f = e.info[at.l].f, ff = e.fpow == 2 ? f * f : f;
@@ -401,33 +444,39 @@ __global__ void __launch_bounds__(kThreads, 1) product(const __grid_constant__ P
         }
         alpha = ldexpf(alpha, shift);
         beta = ldexpf(beta, shift);
-        if (at.index == 0 && threadIdx.x == 0) e.exp_out[at.l] = e.exp_in[at.l] + shift;
+        if (at.index == 0 && threadIdx.x == 0 && rank == 0) e.exp_out[at.l] = e.exp_in[at.l] + shift;
       }
       if (!warp_wait(t_full + (n & 1), (n >> 1) & 1, ab, g.status)) break;
       tc_fence_after();
       float sum = 0.f;
-      const int row = at.i * kTile + 32 * warp + lane;
+      const int row = at.i * kSide + rank * kTile + 32 * (warp & 3) + lane;
 #pragma unroll 1
-      for (int c = 0; c < kTile; c += 32) {
+      for (int c = half; c < half + kSide / 2; c += 32) {
         uint32_t acc[32];
-        tmem_ld32(tmem + lane_off + (n & 1) * kTile + c, acc);
-        sum += finish(g, acc, at.l, row, at.j * kTile + c, g.sym && at.i != at.j, alpha, beta);
+        tmem_ld32(tmem + lane_off + (n & 1) * kSide + c, acc);
+        sum += finish(g, acc, at.l, row, at.j * kSide + c, g.sym && at.i != at.j, alpha, beta);
       }
       tc_fence_before();
       __syncwarp();
-      if (lane == 0) mbar_arrive(t_empty + (n & 1));
+      if (lane == 0) {
+        if (CTAS == 2) mbar_arrive_cluster(cluster_addr(t_empty + (n & 1), 0));
+        else mbar_arrive(t_empty + (n & 1));
+      }
       if (e.sums) {
         sum = warp_sum(sum);
-        const int per = (g.sym ? tm * (tm + 1) / 2 : tm * tn) * kEpiWarps;
-        if (lane == 0) e.sums[(size_t)at.l * per + at.index * kEpiWarps + warp] = sum;
+        if (lane == 0)
+          e.sums[((size_t)at.l * per + at.index) * (CTAS * kEpiWarps) + rank * kEpiWarps + warp] = sum;
       }
     }
   }
   tc_fence_before();
   __syncthreads();
+  __syncwarp();
+  if (CTAS == 2) cluster_sync();  // neither leaves before the other's last use of it
   if (warp == kMmaWarp) {
     tc_fence_after();
-    tmem_dealloc(tmem, kCols);
+    if (CTAS == 2) tmem_dealloc_pair(tmem, kCols);
+    else tmem_dealloc(tmem, kCols);
   }
 }
 
@@ -686,8 +735,17 @@ struct Carver {
   }
 };
 
+// CTAs that share a tile of a rows x cols product.
+int product_ctas(const Plan& p, int rows, int cols, bool sym) {
+  return getenv("ORTH_CTAS") ? atoi(getenv("ORTH_CTAS")) : 2;
+}
+int product_tiles(int rows, int cols, bool sym, int ctas) {  // of one matrix
+  const int side = kTile * ctas, tm = (rows + side - 1) / side, tn = (cols + side - 1) / side;
+  return sym ? tm * (tm + 1) / 2 : tm * tn;
+}
 int product_parts(const Plan& p) {  // sums of a [p, q] product
-  return ((p.p + kTile - 1) / kTile) * ((p.q + kTile - 1) / kTile) * kEpiWarps;
+  const int ctas = product_ctas(p, p.p, p.q, false);
+  return product_tiles(p.p, p.q, false, ctas) * ctas * kEpiWarps;
 }
 
 // Forward: [status][info][square sums], then X, A and B of each step (kept), or of two
@@ -770,10 +828,11 @@ bool make_half_map(CUtensorMap* m, const __half* ptr, int L, int rows, int cols,
 // Builds and launches one product.
 struct Product {
   ProductArgs g;
-  int na = 0, nb = 0, high_a[2], high_b[2], highs = 0;
+  int na = 0, nb = 0, high_a[2], high_b[2], highs = 0, ctas;
   bool nn, ok = true;
   Product(const Plan& p, const Terms& out, int depth, bool nn_, bool sym, int* status) : nn(nn_) {
     memset(&g, 0, sizeof g);
+    ctas = product_ctas(p, out.rows, out.cols, sym);
     g.rows = out.rows;
     g.cols = out.cols;
     g.depth = depth;
@@ -814,15 +873,25 @@ struct Product {
     // The products of high terms come last: the tensor cores cut every addition off to the
     // accumulator's 24 bits, which costs nothing while it holds the small ones only.
     for (int i = 0; i < highs; ++i) pair(high_a[i], high_b[i]);
-    const int tm = (g.rows + kTile - 1) / kTile, tn = (g.cols + kTile - 1) / kTile;
-    const long long tiles = (long long)g.count * (g.sym ? (long long)tm * (tm + 1) / 2 : (long long)tm * tn);
-    const int grid = (int)(tiles < kSms ? tiles : kSms);
-    cudaError_t e = cudaFuncSetAttribute(nn ? product<true> : product<false>,
-                                         cudaFuncAttributeMaxDynamicSharedMemorySize, kSmem);
+    const long long tiles = (long long)g.count * product_tiles(g.rows, g.cols, g.sym, ctas);
+    const long long most = kSms / ctas;
+    const int grid = (int)(tiles < most ? tiles : most) * ctas;
+    auto kernel = ctas == 2 ? (nn ? product<2, true> : product<2, false>)
+                            : (nn ? product<1, true> : product<1, false>);
+    cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmem);
     if (e != cudaSuccess) return e;
-    if (nn) product<true><<<grid, kThreads, kSmem, log.stream>>>(g);
-    else product<false><<<grid, kThreads, kSmem, log.stream>>>(g);
-    e = cudaGetLastError();
+    cudaLaunchConfig_t c = {};
+    c.gridDim = dim3((unsigned)grid);
+    c.blockDim = dim3(kThreads);
+    c.dynamicSmemBytes = kSmem;
+    c.stream = log.stream;
+    cudaLaunchAttribute attr[1];
+    attr[0].id = cudaLaunchAttributeClusterDimension;
+    attr[0].val.clusterDim.x = (unsigned)ctas;
+    attr[0].val.clusterDim.y = attr[0].val.clusterDim.z = 1;
+    c.attrs = attr;
+    c.numAttrs = 1;
+    e = cudaLaunchKernelEx(&c, kernel, g);
     log.mark();
     return e;
   }
@@ -863,9 +932,11 @@ cudaError_t forward(const Plan& p, const void* G, void* Y, const Forward& w, Lau
   cudaError_t e = squares_and_pack(p, G, w.sums, w.status, a, log);
   for (int i = 0; e == cudaSuccess && i < p.steps; ++i) {
     const Terms &X = w.X[i], &A = w.A[i], &B = w.B[i];
+    Terms Xm = X;  // as it is multiplied
+    if (p.bf16) Xm.lo = nullptr;
     {
       Product g(p, A, p.q, false, true, w.status);
-      g.add(X, X);
+      g.add(Xm, Xm);
       g.g.e.alpha = pow2(p.ae[i] - 2 * p.xe[i]);
       if (i == 0) {
         g.g.e.info = w.info;
@@ -887,7 +958,7 @@ cudaError_t forward(const Plan& p, const void* G, void* Y, const Forward& w, Lau
     if (e != cudaSuccess) break;
     const bool last = i + 1 == p.steps;
     Product g(p, X, p.p, true, false, w.status);
-    g.add(B, X);
+    g.add(B, Xm);
     g.plus(X);
     const int out = last ? 0 : p.xe[i + 1];
     g.g.e.alpha = pow2(out - p.be[i] - p.xe[i]);
@@ -936,7 +1007,7 @@ cudaError_t backward(const Plan& p, const void* G, const void* dY, void* dG, con
   for (int i = top; e == cudaSuccess && i >= 0; --i, turn ^= 1) {
     const Terms &H = w.H[turn], &A = f.A[i], &B = f.B[i];
     Terms X = f.X[i];
-    if (p.bf16) X.lo = nullptr;  // its rounding is not multiplied by later steps here
+    if (p.bf16) X.lo = nullptr;
     {
       Product g(p, w.S, p.q, false, true, w.status);
       g.add(H, X);

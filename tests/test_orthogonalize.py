@@ -40,8 +40,8 @@ def rounded(x, terms):
 
 def model(G, dY, polynomials, eps=1e-7):
     """(X, dG) with the roundings that the operator documents and exact sums: operands
-    in fp16 terms, one for bf16 tensors (two for X where the steps from it on enlarge a
-    rounding by more than 16), two for fp32."""
+    in fp16 terms, one for bf16 tensors (and X in two where it is added and the steps from
+    it on enlarge a rounding by more than 16), two for fp32."""
     bf16 = G.dtype == torch.bfloat16
     one = 1 if bf16 else 2
     g = G.detach().double()
@@ -51,11 +51,12 @@ def model(G, dY, polynomials, eps=1e-7):
     X, kept = g / (norm + eps), []
     for i, (a, b, c) in enumerate(polynomials):
         grow = math.prod(max(1.0, abs(p[0])) for p in polynomials[i:])
-        X = rounded(X, one) if not (bf16 and (i == 0 or grow > 16)) else rounded(X, 2)
-        A = rounded(X @ X.mT, one)
+        X = rounded(X, 2 if grow > 16 else one)
+        Xm = rounded(X, one)
+        A = rounded(Xm @ Xm.mT, one)
         P = rounded(b * A + c * (A @ A), one)
-        kept.append((rounded(X, one), A, P))
-        X = a * X + P @ X
+        kept.append((Xm, A, P))
+        X = a * X + P @ Xm
     Y = (X.mT if tall else X).to(G.dtype)
     if dY is None:
         return Y, None
