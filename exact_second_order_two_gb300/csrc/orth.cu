@@ -58,10 +58,13 @@ struct MatInfo {
   int k;
 };
 
-// A matrix in one or two fp16 terms: rows of ld elements, [count] matrices.
+// A matrix in one or two fp16 terms: rows of ld elements, [count] matrices.  Its maps:
+// tiles of 128 rows and 64 columns (left operands, right ones of P Q^T, what is added,
+// results) and of 64 rows and 64 columns (right operands of P Q).
 struct Terms {
   __half *hi = nullptr, *lo = nullptr;
   int rows = 0, cols = 0, ld = 0;
+  CUtensorMap tile[2], step[2];
 };
 
 // ---------------------------------------------------------------------------
@@ -69,30 +72,34 @@ struct Terms {
 // ---------------------------------------------------------------------------
 constexpr int kTile = 128;        // rows, and columns, of a CTA's operand tiles
 constexpr int kDepth = 64;        // contraction elements of a stage (128-byte rows)
-constexpr int kStages = 6;
+constexpr int kStages = 5;
 constexpr uint32_t kTileBytes = kTile * kDepth * 2;
 constexpr uint32_t kStageBytes = 2 * kTileBytes;
-constexpr uint32_t kOffMisc = kStages * kStageBytes;
-constexpr uint32_t kSmem = kOffMisc + 512;
 constexpr int kEpiWarps = 8, kProducerWarp = 8, kMmaWarp = 9;
 constexpr int kThreads = 320;
 constexpr int kMaxSegs = 6;
+// Two groups of four warps finish 64 columns at a time, each through two slots of
+// 128 rows x 64 columns: what is added comes in by TMA, the result is written in its place and
+// leaves by TMA.  Values of two terms take both slots.
+constexpr int kGroups = 2;
+constexpr uint32_t kOffSlots = kStages * kStageBytes;
+constexpr uint32_t kOffMisc = kOffSlots + kGroups * 2 * kTileBytes;
+constexpr uint32_t kSmem = kOffMisc + 512;
+static_assert(kSmem <= 232448, "shared memory budget");
 
 struct Epilogue {
   float alpha, beta;            // value = (alpha acc + beta E) f^fpow, times the rescaling
-  const __half *ehi, *elo;      // E, or null
-  int elds;
+  int e_terms;                  // of E: 0 without
   const MatInfo* info;          // f of each matrix
   int fpow;
-  // outputs: terms by rows (and mirrored), or fp32 by rows, or the caller's tensor
-  __half *ohi, *olo;
-  int olds;
-  float* of32;
+  // results: o_terms terms by rows (sym: also mirrored, at o), or the caller's tensor y,
+  // through maps as well where its rows are at 16-byte steps (o_terms 0)
+  int o_terms;
+  __half* o[2];
+  int old;
   void* y;
-  int y_bf16, y_transposed;
-  // sums: squares of the values written, or their product with D's
-  float* sums;                  // [count][parts of a matrix]
-  const __half *dhi, *dlo;
+  int y_bf16, y_transposed, y_mapped;
+  float* sums;                  // [count][parts of a matrix]: squares of the values, or null
   // rescaling by the norm of the step's input: [count][scale_parts] squares
   const float* scale_sums;
   int scale_parts, target;
@@ -101,12 +108,12 @@ struct Epilogue {
 };
 
 struct ProductArgs {
-  CUtensorMap a[4], b[4];
+  CUtensorMap a[4], b[4], e[2], o[2];
   unsigned char seg_a[kMaxSegs], seg_b[kMaxSegs];
   int nseg;
   int rows, cols, depth, count;
   int sym;
-  Epilogue e;
+  Epilogue ep;
   int* status;
   unsigned long long wait_ns;
 };
@@ -148,119 +155,73 @@ __device__ __forceinline__ uint32_t pack2(__half a, __half b) {
   return (uint32_t)__half_as_ushort(a) | ((uint32_t)__half_as_ushort(b) << 16);
 }
 
-// v[c] += beta * (hi + lo) of 32 consecutive elements, of which those below `valid` exist.
-template <typename F>
-__device__ __forceinline__ void each_of_terms(const __half* hi, const __half* lo, int valid, F f) {
+// 32 columns (half h) of a thread's row in a slot: 16-byte chunks 4 h .. 4 h + 3.
+__device__ __forceinline__ uint4* slot_chunk(uint8_t* slot, int row, int c) {
+  return reinterpret_cast<uint4*>(slot + sw128_offset(row, c));
+}
+__device__ __forceinline__ void add_slot(float (&v)[32], uint8_t* slot, int row, int h, float beta) {
 #pragma unroll
   for (int q = 0; q < 4; ++q) {
-    if (8 * q >= valid) break;
-    const uint4 h = *reinterpret_cast<const uint4*>(hi + 8 * q);
-    uint4 l = make_uint4(0, 0, 0, 0);
-    if (lo) l = *reinterpret_cast<const uint4*>(lo + 8 * q);
-    const uint32_t hw[4] = {h.x, h.y, h.z, h.w}, lw[4] = {l.x, l.y, l.z, l.w};
+    const uint4 x = *slot_chunk(slot, row, 4 * h + q);
+    const uint32_t w[4] = {x.x, x.y, x.z, x.w};
 #pragma unroll
     for (int k = 0; k < 4; ++k) {
-      const float2 a = __half22float2(*reinterpret_cast<const __half2*>(&hw[k]));
-      const float2 b = __half22float2(*reinterpret_cast<const __half2*>(&lw[k]));
-      f(8 * q + 2 * k, a.x + b.x);
-      f(8 * q + 2 * k + 1, a.y + b.y);
+      const float2 t = __half22float2(*reinterpret_cast<const __half2*>(&w[k]));
+      v[8 * q + 2 * k] = fmaf(beta, t.x, v[8 * q + 2 * k]);
+      v[8 * q + 2 * k + 1] = fmaf(beta, t.y, v[8 * q + 2 * k + 1]);
+    }
+  }
+}
+__device__ __forceinline__ void put_slot(const uint32_t (&w)[16], uint8_t* slot, int row, int h) {
+#pragma unroll
+  for (int q = 0; q < 4; ++q)
+    *slot_chunk(slot, row, 4 * h + q) = make_uint4(w[4 * q], w[4 * q + 1], w[4 * q + 2], w[4 * q + 3]);
+}
+
+__device__ __forceinline__ void put_floats(const float (&v)[32], uint8_t* slot, int row) {
+#pragma unroll
+  for (int k = 0; k < 8; ++k)
+    *reinterpret_cast<float4*>(slot_chunk(slot, row, k)) =
+        make_float4(v[4 * k], v[4 * k + 1], v[4 * k + 2], v[4 * k + 3]);
+}
+
+// Writes 32 columns of a row to the mirrored place.  Neighbouring lanes hold
+// neighbouring rows: they exchange halves, so that each writes two rows of every other
+// column at once.  (An odd matrix's last pair reaches into the padding of its rows.)
+__device__ __forceinline__ void put_mirrored(const uint32_t (&hi)[16], const uint32_t (&lo)[16],
+                                             const Epilogue& e, size_t base, int row, int col, int rows,
+                                             int cols) {
+  const bool odd = row & 1;
+  const int pair = row & ~1;
+#pragma unroll
+  for (int k = 0; k < 16; ++k) {  // columns 2k (low half) and 2k + 1
+    // hi and lo of the column that the partner writes
+    const uint32_t mine = odd ? (hi[k] & 0xffffu) | (lo[k] << 16) : (hi[k] >> 16) | (lo[k] & 0xffff0000u);
+    const uint32_t other = __shfl_xor_sync(0xffffffffu, mine, 1);
+    const int c = col + 2 * k + odd;
+    const uint32_t h = odd ? (other & 0xffffu) | (hi[k] & 0xffff0000u) : (hi[k] & 0xffffu) | (other << 16);
+    const uint32_t l = odd ? (other >> 16) | (lo[k] & 0xffff0000u) : (lo[k] & 0xffffu) | (other & 0xffff0000u);
+    if (pair < rows && c < cols) {
+      const size_t at = base + (size_t)c * e.old + pair;
+      *reinterpret_cast<uint32_t*>(e.o[0] + at) = h;
+      if (e.o_terms == 2) *reinterpret_cast<uint32_t*>(e.o[1] + at) = l;
     }
   }
 }
 
-// One row's 32 columns of a tile: finish the values and write them.  Returns the row's
-// part of the sums.
-__device__ __forceinline__ float finish(const ProductArgs& g, const uint32_t (&acc)[32], int l, int row,
-                                        int col, bool mirror, float alpha, float beta) {
-  const Epilogue& e = g.e;
-  const int valid = min(32, g.cols - col);
-  if (row >= g.rows || valid <= 0) return 0.f;
-  float v[32];
+// 32 values of a row straight to the caller's tensor, where no map can take them.
+__device__ __forceinline__ void put_caller(const float (&v)[32], const ProductArgs& g, int l, int row, int col) {
+  const Epilogue& e = g.ep;
+  if (row >= g.rows) return;
+  const size_t first = (size_t)l * g.rows * g.cols +
+                       (e.y_transposed ? (size_t)col * g.rows + row : (size_t)row * g.cols + col);
+  const size_t step = e.y_transposed ? g.rows : 1;
 #pragma unroll
-  for (int c = 0; c < 32; ++c) v[c] = c < valid ? alpha * __uint_as_float(acc[c]) : 0.f;
-  if (e.ehi) {
-    const size_t at = ((size_t)l * g.rows + row) * e.elds + col;
-    each_of_terms(e.ehi + at, e.elo ? e.elo + at : nullptr, valid, [&](int c, float x) {
-      if (c < valid) v[c] = fmaf(beta, x, v[c]);
-    });
-  }
-  float sum = 0.f;
-  if (e.sums) {
-    if (e.dhi) {
-      const size_t at = ((size_t)l * g.rows + row) * e.elds + col;
-      each_of_terms(e.dhi + at, e.dlo ? e.dlo + at : nullptr, valid, [&](int c, float x) {
-        if (c < valid) sum = fmaf(v[c], x, sum);
-      });
-    } else {
-#pragma unroll
-      for (int c = 0; c < 32; ++c) sum = fmaf(v[c], v[c], sum);
+  for (int c = 0; c < 32; ++c)
+    if (col + c < g.cols) {
+      if (e.y_bf16) static_cast<__nv_bfloat16*>(e.y)[first + c * step] = __float2bfloat16_rn(v[c]);
+      else static_cast<float*>(e.y)[first + c * step] = v[c];
     }
-  }
-  if (e.ohi) {
-    __half hi[32], lo[32];
-#pragma unroll
-    for (int c = 0; c < 32; ++c) split(v[c], hi[c], lo[c]);
-    const size_t base = (size_t)l * g.rows * e.olds;
-    const size_t at = base + (size_t)row * e.olds + col;
-#pragma unroll
-    for (int q = 0; q < 4; ++q) {
-      if (8 * q >= valid) break;
-      const int c = 8 * q;
-      *reinterpret_cast<uint4*>(e.ohi + at + c) =
-          make_uint4(pack2(hi[c], hi[c + 1]), pack2(hi[c + 2], hi[c + 3]), pack2(hi[c + 4], hi[c + 5]),
-                     pack2(hi[c + 6], hi[c + 7]));
-      if (e.olo)
-        *reinterpret_cast<uint4*>(e.olo + at + c) =
-            make_uint4(pack2(lo[c], lo[c + 1]), pack2(lo[c + 2], lo[c + 3]), pack2(lo[c + 4], lo[c + 5]),
-                       pack2(lo[c + 6], lo[c + 7]));
-    }
-    if (mirror) {
-#pragma unroll
-      for (int c = 0; c < 32; ++c)
-        if (c < valid) {
-          const size_t to = base + (size_t)(col + c) * e.olds + row;
-          e.ohi[to] = hi[c];
-          if (e.olo) e.olo[to] = lo[c];
-        }
-    }
-  } else if (e.of32) {
-    float* o = e.of32 + ((size_t)l * g.rows + row) * e.olds + col;
-#pragma unroll
-    for (int q = 0; q < 8; ++q) {
-      if (4 * q >= valid) break;
-      *reinterpret_cast<float4*>(o + 4 * q) = make_float4(v[4 * q], v[4 * q + 1], v[4 * q + 2], v[4 * q + 3]);
-    }
-  } else {
-    const size_t n = (size_t)g.rows * g.cols;
-    const size_t first = l * n + (e.y_transposed ? (size_t)col * g.rows + row : (size_t)row * g.cols + col);
-    const size_t step = e.y_transposed ? g.rows : 1;
-    if (e.y_bf16) {
-      __nv_bfloat16* o = static_cast<__nv_bfloat16*>(e.y) + first;
-      if (step == 1 && valid == 32 && (reinterpret_cast<uintptr_t>(o) & 15u) == 0) {
-#pragma unroll
-        for (int q = 0; q < 4; ++q)
-          reinterpret_cast<uint4*>(o)[q] =
-              make_uint4(pack_bf16(v[8 * q], v[8 * q + 1]), pack_bf16(v[8 * q + 2], v[8 * q + 3]),
-                         pack_bf16(v[8 * q + 4], v[8 * q + 5]), pack_bf16(v[8 * q + 6], v[8 * q + 7]));
-      } else {
-#pragma unroll
-        for (int c = 0; c < 32; ++c)
-          if (c < valid) o[c * step] = __float2bfloat16_rn(v[c]);
-      }
-    } else {
-      float* o = static_cast<float*>(e.y) + first;
-      if (step == 1 && valid == 32 && (reinterpret_cast<uintptr_t>(o) & 15u) == 0) {
-#pragma unroll
-        for (int q = 0; q < 8; ++q)
-          reinterpret_cast<float4*>(o)[q] = make_float4(v[4 * q], v[4 * q + 1], v[4 * q + 2], v[4 * q + 3]);
-      } else {
-#pragma unroll
-        for (int c = 0; c < 32; ++c)
-          if (c < valid) o[c * step] = v[c];
-      }
-    }
-  }
-  return sum;
 }
 
 // The exponent that brings a matrix with sum of squares nu2 to a norm in
@@ -289,7 +250,8 @@ __global__ void __launch_bounds__(kThreads, 1) product(const __grid_constant__ P
   uint64_t* empty = full + kStages;                               // [kStages]
   uint64_t* t_full = empty + kStages;                             // [2]
   uint64_t* t_empty = t_full + 2;                                 // [2]
-  uint64_t* drain = t_empty + 2;
+  uint64_t* e_full = t_empty + 2;                                 // [kGroups][2]
+  uint64_t* drain = e_full + 2 * kGroups;
   uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(smem + kOffMisc + 256);
   Abort* ab = reinterpret_cast<Abort*>(smem + kOffMisc + 264);
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
@@ -305,6 +267,7 @@ __global__ void __launch_bounds__(kThreads, 1) product(const __grid_constant__ P
       mbar_init(t_full + b, 1);
       mbar_init(t_empty + b, kEpiWarps * CTAS);
     }
+    for (int i = 0; i < 2 * kGroups; ++i) mbar_init(e_full + i, 1);
     mbar_init(drain, 1);
     ab->flag = 0;
     ab->limit_ns = g.wait_ns;
@@ -422,10 +385,38 @@ __global__ void __launch_bounds__(kThreads, 1) product(const __grid_constant__ P
       mbar_wait_bounded(drain, 0, g.status, 100000000ull);
     }
   } else {
-    const Epilogue& e = g.e;
+    const Epilogue& e = g.ep;
     const uint32_t lane_off = (uint32_t)(32 * (warp & 3)) << 16;
-    const int half = (warp >> 2) * (kSide / 2);  // of the columns
-    int n = 0, scaled = -1, shift = 0;
+    const int group = warp >> 2, r = 32 * (warp & 3) + lane;
+    const bool issuer = (threadIdx.x & 127) == 0;
+    uint8_t* const slots = smem + kOffSlots + group * 2 * kTileBytes;
+    uint64_t* const e_bar = e_full + 2 * group;
+    constexpr int kChunks = kSide / 64 / kGroups;  // of a tile, for each group
+    const bool two = e.e_terms == 2 || e.o_terms == 2 || (e.y_mapped && !e.y_bf16);
+    const int nslots = two ? 1 : 2;
+    const int mine = first < tiles ? ((tiles - 1 - first) / step + 1) * kChunks : 0;
+    // the slot of chunk u is free once the result before it has left; then what is
+    // added comes in
+    auto prepare = [&](int u) {
+      const int s = u % nslots;
+      if (e.e_terms) {
+        const TileAt at = tile_at(g, first + u / kChunks * step, kSide);
+        const int row = at.i * kSide + rank * kTile;
+        const int col = at.j * kSide + (group + u % kChunks * kGroups) * 64;
+        mbar_arrive_expect_tx(e_bar + s, e.e_terms * kTileBytes);
+        tma_load_3d(slots + s * kTileBytes, &g.e[0], e_bar + s, col, row, at.l);
+        if (e.e_terms == 2) tma_load_3d(slots + kTileBytes, &g.e[1], e_bar + s, col, row, at.l);
+      } else {
+        mbar_arrive(e_bar + s);
+      }
+    };
+    int ahead = 0;  // chunks prepared
+    if (issuer)
+      for (; ahead < nslots && ahead < mine; ++ahead) prepare(ahead);
+    int n = 0, u = 0, scaled = -1, shift = 0;
+    bool ok = true;
+    // after an abort the loops run to their end without waiting, so that a group's warps
+    // keep meeting at its barrier
     for (int t = first; t < tiles; t += step, ++n) {
       const TileAt at = tile_at(g, t, kSide);
       float alpha = e.alpha, beta = e.beta;
@@ -446,27 +437,93 @@ __global__ void __launch_bounds__(kThreads, 1) product(const __grid_constant__ P
         beta = ldexpf(beta, shift);
         if (at.index == 0 && threadIdx.x == 0 && rank == 0) e.exp_out[at.l] = e.exp_in[at.l] + shift;
       }
-      if (!warp_wait(t_full + (n & 1), (n >> 1) & 1, ab, g.status)) break;
+      ok = ok && warp_wait(t_full + (n & 1), (n >> 1) & 1, ab, g.status);
       tc_fence_after();
       float sum = 0.f;
-      const int row = at.i * kSide + rank * kTile + 32 * (warp & 3) + lane;
+      const int row0 = at.i * kSide + rank * kTile, row = row0 + r;
 #pragma unroll 1
-      for (int c = half; c < half + kSide / 2; c += 32) {
-        uint32_t acc[32];
-        tmem_ld32(tmem + lane_off + (n & 1) * kSide + c, acc);
-        sum += finish(g, acc, at.l, row, at.j * kSide + c, g.sym && at.i != at.j, alpha, beta);
-      }
-      tc_fence_before();
-      __syncwarp();
-      if (lane == 0) {
-        if (CTAS == 2) mbar_arrive_cluster(cluster_addr(t_empty + (n & 1), 0));
-        else mbar_arrive(t_empty + (n & 1));
+      for (int c = 0; c < kChunks; ++c, ++u) {
+        const int in_tile = (group + c * kGroups) * 64, col0 = at.j * kSide + in_tile;
+        const int s = u % nslots;
+        uint8_t* const slot = slots + s * kTileBytes;
+        ok = ok && warp_wait(e_bar + s, (u / nslots) & 1, ab, g.status);
+        float kept[32];
+#pragma unroll
+        for (int h = 0; h < 2; ++h) {
+          const int col = col0 + 32 * h;
+          uint32_t acc[32];
+          tmem_ld32(tmem + lane_off + (n & 1) * kSide + in_tile + 32 * h, acc);
+          float v[32];
+#pragma unroll
+          for (int k = 0; k < 32; ++k) v[k] = alpha * __uint_as_float(acc[k]);
+          if (e.e_terms) add_slot(v, slot, r, h, beta);
+          if (e.e_terms == 2) add_slot(v, slot + kTileBytes, r, h, beta);
+          if (e.sums) {  // (what lies outside is zero)
+#pragma unroll
+            for (int k = 0; k < 32; ++k) sum = fmaf(v[k], v[k], sum);
+          }
+          uint32_t w[16];
+          if (e.o_terms) {
+            uint32_t lo[16];
+#pragma unroll
+            for (int k = 0; k < 16; ++k) {
+              __half ha, la, hb, lb;
+              split(v[2 * k], ha, la);
+              split(v[2 * k + 1], hb, lb);
+              w[k] = pack2(ha, hb);
+              lo[k] = pack2(la, lb);
+            }
+            put_slot(w, slot, r, h);
+            if (e.o_terms == 2) put_slot(lo, slot + kTileBytes, r, h);
+            if (g.sym && at.i != at.j)
+              put_mirrored(w, lo, e, (size_t)at.l * g.rows * e.old, row, col, g.rows, g.cols);
+          } else if (!e.y_mapped) {
+            put_caller(v, g, at.l, row, col);
+          } else if (e.y_bf16) {
+#pragma unroll
+            for (int k = 0; k < 16; ++k) w[k] = pack_bf16(v[2 * k], v[2 * k + 1]);
+            put_slot(w, slot, r, h);
+          } else if (h == 0) {  // 32 fp32 columns fill a slot's rows: after the second half is read
+#pragma unroll
+            for (int k = 0; k < 32; ++k) kept[k] = v[k];
+          } else {
+            put_floats(kept, slot, r);
+            put_floats(v, slot + kTileBytes, r);
+          }
+        }
+        if (c == kChunks - 1) {
+          tc_fence_before();
+          __syncwarp();
+          if (lane == 0) {
+            if (CTAS == 2) mbar_arrive_cluster(cluster_addr(t_empty + (n & 1), 0));
+            else mbar_arrive(t_empty + (n & 1));
+          }
+        }
+        fence_async_smem();
+        named_sync<128>(1 + group);
+        if (issuer) {
+          if ((e.o_terms || e.y_mapped) && row0 < g.rows && col0 < g.cols && !ab->flag) {
+            tma_store_3d(&g.o[0], slot, col0, row0, at.l);
+            if (e.o_terms == 2) tma_store_3d(&g.o[1], slot + kTileBytes, col0, row0, at.l);
+            if (!e.o_terms && !e.y_bf16 && col0 + 32 < g.cols)
+              tma_store_3d(&g.o[0], slot + kTileBytes, col0 + 32, row0, at.l);
+            bulk_commit_group();
+            bulk_wait_read_all();
+          }
+          if (ahead < mine && !ab->flag) prepare(ahead++);
+        }
       }
       if (e.sums) {
         sum = warp_sum(sum);
         if (lane == 0)
           e.sums[((size_t)at.l * per + at.index) * (CTAS * kEpiWarps) + rank * kEpiWarps + warp] = sum;
       }
+    }
+    if (issuer) {
+      bulk_wait_all();
+      // what was loaded ahead has landed (after an abort some was never awaited)
+      for (int k = max(0, ahead - nslots); k < ahead; ++k)
+        mbar_wait_bounded(e_bar + k % nslots, (k / nslots) & 1, g.status, 100000000ull);
     }
   }
   tc_fence_before();
@@ -600,10 +657,56 @@ __global__ void __launch_bounds__(kSumThreads) pack(PackArgs a) {
   }
 }
 
+// partial[l][block] = part of <H, X> over a slice of rows of matrix l, both in terms.
+struct DotArgs {
+  const __half *h[2], *x[2];  // [count][p][ld]
+  float* partial;
+  int p, q, ld;
+};
+__global__ void __launch_bounds__(kSumThreads) term_dots(DotArgs a) {
+  __shared__ float sm[kSumThreads / 32];
+  const size_t base = (size_t)blockIdx.y * a.p * a.ld;
+  const int chunks = a.ld / 8;
+  const long long all = (long long)a.p * chunks, per = (all + gridDim.x - 1) / gridDim.x;
+  const long long first = blockIdx.x * per, last = min(all, first + per);
+  float s = 0.f;
+  for (long long i = first + threadIdx.x; i < last; i += kSumThreads) {
+    const int row = (int)(i / chunks), c = (int)(i - (long long)row * chunks) * 8;
+    const size_t at = base + (size_t)row * a.ld + c;
+    float h[8] = {}, x[8] = {};
+#pragma unroll
+    for (int t = 0; t < 2; ++t) {
+      if (a.h[t]) {
+        const uint4 v = *reinterpret_cast<const uint4*>(a.h[t] + at);
+        const __half* w = reinterpret_cast<const __half*>(&v);
+#pragma unroll
+        for (int k = 0; k < 8; ++k) h[k] += __half2float(w[k]);
+      }
+      if (a.x[t]) {
+        const uint4 v = *reinterpret_cast<const uint4*>(a.x[t] + at);
+        const __half* w = reinterpret_cast<const __half*>(&v);
+#pragma unroll
+        for (int k = 0; k < 8; ++k) x[k] += __half2float(w[k]);
+      }
+    }
+#pragma unroll
+    for (int k = 0; k < 8; ++k)  // (the padding of a row holds anything)
+      if (c + k < a.q) s = fmaf(h[k], x[k], s);
+  }
+  s = warp_sum(s);
+  if ((threadIdx.x & 31) == 0) sm[threadIdx.x >> 5] = s;
+  __syncthreads();
+  if (threadIdx.x == 0) {
+    float t = 0.f;
+    for (int k = 0; k < kSumThreads / 32; ++k) t += sm[k];
+    a.partial[(size_t)blockIdx.y * gridDim.x + blockIdx.x] = t;
+  }
+}
+
 struct EndArgs {
   const void* g;      // [count][m][n]
   void* dg;
-  const float* h;     // [count][p][ld]: dX_0 2^exp
+  const __half* h[2]; // [count][p][ld]: dX_0 2^exp
   const float* dots;  // [count][parts]: <h, X_0's terms>
   int parts;
   int p, q, ld, tall, x_exp;
@@ -625,13 +728,17 @@ __global__ void __launch_bounds__(kSumThreads) end_gradient(EndArgs a) {
   const float by_h = (float)scale, by_g = (float)(scale * along);
   const size_t n = (size_t)l * a.p * a.q;
   const int r0 = blockIdx.y * kPack, c0 = blockIdx.x * kPack;  // of h
-  const float* h = a.h + (size_t)l * a.p * a.ld;
+  const size_t base = (size_t)l * a.p * a.ld;
   const T* g = static_cast<const T*>(a.g) + n;
   T* dg = static_cast<T*>(a.dg) + n;
+  auto value = [&](int rr, int c) {
+    const size_t at = base + (size_t)(r0 + rr) * a.ld + c0 + c;
+    return __half2float(a.h[0][at]) + (a.h[1] ? __half2float(a.h[1][at]) : 0.f);
+  };
   if (a.tall) {
     for (int i = threadIdx.x; i < kPack * kPack; i += kSumThreads) {
       const int rr = i / kPack, c = i % kPack;
-      if (r0 + rr < a.p && c0 + c < a.q) tile[rr][c] = h[(size_t)(r0 + rr) * a.ld + c0 + c];
+      if (r0 + rr < a.p && c0 + c < a.q) tile[rr][c] = value(rr, c);
     }
     __syncthreads();
   }
@@ -639,7 +746,7 @@ __global__ void __launch_bounds__(kSumThreads) end_gradient(EndArgs a) {
     const int rr = a.tall ? i % kPack : i / kPack, c = a.tall ? i / kPack : i % kPack;
     if (r0 + rr >= a.p || c0 + c >= a.q) continue;
     const size_t at = a.tall ? (size_t)(c0 + c) * a.p + r0 + rr : (size_t)(r0 + rr) * a.q + c0 + c;
-    const float v = a.tall ? tile[rr][c] : h[(size_t)(r0 + rr) * a.ld + c0 + c];
+    const float v = a.tall ? tile[rr][c] : value(rr, c);
     dg[at] = from_f32<T>(fmaf(-by_g, to_f32<T>(g[at]), by_h * v));
   }
 }
@@ -717,20 +824,42 @@ int make_plan(const fbob_orth_t* o, Plan* out) {
   return FBOB_OK;
 }
 
+// A map of [count][rows][ld] elements, cols of each row; a box: 128 bytes of box_rows rows.
+bool make_tile_map(CUtensorMap* m, CUtensorMapDataType type, int size, const void* ptr, int L, int rows,
+                   int cols, long long ld, int box_rows) {
+  auto fn = encode_fn();
+  if (!fn) return false;
+  cuuint64_t dims[3] = {(cuuint64_t)cols, (cuuint64_t)rows, (cuuint64_t)L};
+  cuuint64_t strides[2] = {(cuuint64_t)ld * size, (cuuint64_t)rows * ld * size};
+  cuuint32_t box[3] = {(cuuint32_t)(128 / size), (cuuint32_t)box_rows, 1};
+  cuuint32_t es[3] = {1, 1, 1};
+  return fn(m, type, 3, const_cast<void*>(ptr), dims, strides, box, es, CU_TENSOR_MAP_INTERLEAVE_NONE,
+            CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+            CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
 struct Carver {
   char* base;
   size_t off;
+  bool ok;
   void* take(size_t bytes) {
     void* r = base ? base + off : nullptr;
     off += align_up(bytes);
     return r;
   }
-  Terms terms(const Plan& p, int cols, int ld, int n) {
+  // right: also a right operand of P Q
+  Terms terms(const Plan& p, int cols, int ld, int n, bool right) {
     Terms t;
     const size_t one = (size_t)p.L * p.p * ld * sizeof(__half);
     t.hi = static_cast<__half*>(take(one));
     t.lo = n == 2 ? static_cast<__half*>(take(one)) : nullptr;
     t.rows = p.p; t.cols = cols; t.ld = ld;
+    for (int i = 0; base && i < n; ++i) {
+      const __half* at = i ? t.lo : t.hi;
+      const auto half = CU_TENSOR_MAP_DATA_TYPE_FLOAT16;
+      ok = ok && make_tile_map(&t.tile[i], half, 2, at, p.L, p.p, cols, ld, kTile);
+      ok = ok && (!right || make_tile_map(&t.step[i], half, 2, at, p.L, p.p, cols, ld, kDepth));
+    }
     return t;
   }
 };
@@ -755,11 +884,12 @@ struct Forward {
   MatInfo* info;
   float* sums;
   Terms X[kMaxSteps], A[kMaxSteps], B[kMaxSteps];
+  bool ok;
   size_t bytes;
 };
 Forward carve_forward(const Plan& p, char* base) {
   Forward w;
-  Carver c{base, 0};
+  Carver c{base, 0, true};
   w.status = static_cast<int*>(c.take(sizeof(int)));
   w.info = static_cast<MatInfo*>(c.take(sizeof(MatInfo) * p.L));
   w.sums = static_cast<float*>(c.take(sizeof(float) * p.L * p.square_parts));
@@ -768,68 +898,56 @@ Forward carve_forward(const Plan& p, char* base) {
   for (int i = 0; !p.keep && i < 2; ++i) {
     int t = 1;
     for (int k = i; k < p.steps; k += 2) t = p.xt[k] > t ? p.xt[k] : t;
-    turn[i] = c.terms(p, p.q, p.ldq, t);
+    turn[i] = c.terms(p, p.q, p.ldq, t, true);
   }
   for (int i = 0; i < p.steps; ++i) {
-    w.X[i] = p.keep ? c.terms(p, p.q, p.ldq, p.xt[i]) : turn[i & 1];
+    w.X[i] = p.keep ? c.terms(p, p.q, p.ldq, p.xt[i], true) : turn[i & 1];
     if (p.xt[i] == 1) w.X[i].lo = nullptr;
     if (p.keep || i == 0) {
-      w.A[i] = c.terms(p, p.p, p.ldp, small);
-      w.B[i] = c.terms(p, p.p, p.ldp, small);
+      w.A[i] = c.terms(p, p.p, p.ldp, small, false);
+      w.B[i] = c.terms(p, p.p, p.ldp, small, false);
     } else {
       w.A[i] = w.A[0];
       w.B[i] = w.B[0];
     }
   }
+  w.ok = c.ok;
   w.bytes = c.off;
   return w;
 }
 
 // Backward: [status][square sums of dY][exponents: steps + 1][sums of the steps'
-// results: two in turn], H in turn, S, T, dX_0 in fp32.
+// results: two in turn], H in turn, S, T.
 struct Backward {
   int* status;
   float *sums, *first, *step_sums[2];
   int* exp[kMaxSteps + 1];
   Terms H[2], S, T;
-  float* h0;
+  bool ok;
   size_t bytes;
 };
 Backward carve_backward(const Plan& p, char* base) {
   Backward w;
-  Carver c{base, 0};
+  Carver c{base, 0, true};
   const int t = p.bf16 ? 1 : 2;
   w.status = static_cast<int*>(c.take(sizeof(int)));
   w.sums = static_cast<float*>(c.take(sizeof(float) * p.L * p.square_parts));
   w.first = static_cast<float*>(c.take(sizeof(float) * p.L));
   for (float*& s : w.step_sums) s = static_cast<float*>(c.take(sizeof(float) * p.L * product_parts(p)));
   for (int i = 0; i <= p.steps; ++i) w.exp[i] = static_cast<int*>(c.take(sizeof(int) * p.L));
-  for (Terms& h : w.H) h = c.terms(p, p.q, p.ldq, t);
-  w.S = c.terms(p, p.p, p.ldp, t);
-  w.T = c.terms(p, p.p, p.ldp, t);
-  w.h0 = static_cast<float*>(c.take(sizeof(float) * p.L * p.p * p.ldq));
+  for (Terms& h : w.H) h = c.terms(p, p.q, p.ldq, t, true);
+  w.S = c.terms(p, p.p, p.ldp, t, false);
+  w.T = c.terms(p, p.p, p.ldp, t, false);
+  w.ok = c.ok;
   w.bytes = c.off;
   return w;
-}
-
-// A map of [count][rows][ld] fp16, cols of each row; box: 64 columns, box_rows rows.
-bool make_half_map(CUtensorMap* m, const __half* ptr, int L, int rows, int cols, int ld, int box_rows) {
-  auto fn = encode_fn();
-  if (!fn) return false;
-  cuuint64_t dims[3] = {(cuuint64_t)cols, (cuuint64_t)rows, (cuuint64_t)L};
-  cuuint64_t strides[2] = {(cuuint64_t)ld * 2, (cuuint64_t)rows * ld * 2};
-  cuuint32_t box[3] = {kDepth, (cuuint32_t)box_rows, 1};
-  cuuint32_t es[3] = {1, 1, 1};
-  return fn(m, CU_TENSOR_MAP_DATA_TYPE_FLOAT16, 3, const_cast<__half*>(ptr), dims, strides, box, es,
-            CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
-            CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
 // Builds and launches one product.
 struct Product {
   ProductArgs g;
   int na = 0, nb = 0, high_a[2], high_b[2], highs = 0, ctas;
-  bool nn, ok = true;
+  bool nn;
   Product(const Plan& p, const Terms& out, int depth, bool nn_, bool sym, int* status) : nn(nn_) {
     memset(&g, 0, sizeof g);
     ctas = product_ctas(p, out.rows, out.cols, sym);
@@ -844,11 +962,10 @@ struct Product {
   // acc += P Q^T (or P Q): every pair of terms but the two low ones
   void add(const Terms& P, const Terms& Q) {
     const int a0 = na, b0 = nb;
-    const int b_rows = nn ? kDepth : kTile;
-    ok = ok && make_half_map(&g.a[na++], P.hi, g.count, P.rows, P.cols, P.ld, kTile);
-    if (P.lo) ok = ok && make_half_map(&g.a[na++], P.lo, g.count, P.rows, P.cols, P.ld, kTile);
-    ok = ok && make_half_map(&g.b[nb++], Q.hi, g.count, Q.rows, Q.cols, Q.ld, b_rows);
-    if (Q.lo) ok = ok && make_half_map(&g.b[nb++], Q.lo, g.count, Q.rows, Q.cols, Q.ld, b_rows);
+    g.a[na++] = P.tile[0];
+    if (P.lo) g.a[na++] = P.tile[1];
+    g.b[nb++] = nn ? Q.step[0] : Q.tile[0];
+    if (Q.lo) g.b[nb++] = nn ? Q.step[1] : Q.tile[1];
     if (Q.lo) pair(a0, b0 + 1);
     if (P.lo) pair(a0 + 1, b0);
     high_a[highs] = a0;
@@ -859,17 +976,30 @@ struct Product {
     g.seg_b[g.nseg++] = (unsigned char)b;
   }
   void plus(const Terms& E) {
-    g.e.ehi = E.hi;
-    g.e.elo = E.lo;
-    g.e.elds = E.ld;
+    g.ep.e_terms = E.lo ? 2 : 1;
+    g.e[0] = E.tile[0];
+    g.e[1] = E.tile[1];
   }
   void to(const Terms& O) {
-    g.e.ohi = O.hi;
-    g.e.olo = O.lo;
-    g.e.olds = O.ld;
+    g.ep.o_terms = O.lo ? 2 : 1;
+    g.o[0] = O.tile[0];
+    g.o[1] = O.tile[1];
+    g.ep.o[0] = O.hi;
+    g.ep.o[1] = O.lo;
+    g.ep.old = O.ld;
+  }
+  // the caller's tensor, by rows (its map where one can be made) or transposed
+  void to_caller(const Plan& p, void* y) {
+    const int size = p.bf16 ? 2 : 4;
+    g.ep.y = y;
+    g.ep.y_bf16 = p.bf16;
+    g.ep.y_transposed = p.tall;
+    g.ep.y_mapped = !p.tall && (reinterpret_cast<uintptr_t>(y) & 15u) == 0 && p.q * size % 16 == 0 &&
+                    make_tile_map(&g.o[0], p.bf16 ? CU_TENSOR_MAP_DATA_TYPE_BFLOAT16
+                                                  : CU_TENSOR_MAP_DATA_TYPE_FLOAT32,
+                                  size, y, p.L, p.p, p.q, p.q, kTile);
   }
   cudaError_t launch(LaunchLog& log) {
-    if (!ok) return cudaErrorUnknown;
     // The products of high terms come last: the tensor cores cut every addition off to the
     // accumulator's 24 bits, which costs nothing while it holds the small ones only.
     for (int i = 0; i < highs; ++i) pair(high_a[i], high_b[i]);
@@ -937,10 +1067,10 @@ cudaError_t forward(const Plan& p, const void* G, void* Y, const Forward& w, Lau
     {
       Product g(p, A, p.q, false, true, w.status);
       g.add(Xm, Xm);
-      g.g.e.alpha = pow2(p.ae[i] - 2 * p.xe[i]);
+      g.g.ep.alpha = pow2(p.ae[i] - 2 * p.xe[i]);
       if (i == 0) {
-        g.g.e.info = w.info;
-        g.g.e.fpow = 2;
+        g.g.ep.info = w.info;
+        g.g.ep.fpow = 2;
       }
       g.to(A);
       e = g.launch(log);
@@ -950,8 +1080,8 @@ cudaError_t forward(const Plan& p, const void* G, void* Y, const Forward& w, Lau
       Product g(p, B, p.p, false, true, w.status);
       g.add(A, A);
       g.plus(A);
-      g.g.e.alpha = p.c[i] * pow2(p.be[i] - 2 * p.ae[i]);
-      g.g.e.beta = p.b[i] * pow2(p.be[i] - p.ae[i]);
+      g.g.ep.alpha = p.c[i] * pow2(p.be[i] - 2 * p.ae[i]);
+      g.g.ep.beta = p.b[i] * pow2(p.be[i] - p.ae[i]);
       g.to(B);
       e = g.launch(log);
     }
@@ -961,16 +1091,14 @@ cudaError_t forward(const Plan& p, const void* G, void* Y, const Forward& w, Lau
     g.add(B, Xm);
     g.plus(X);
     const int out = last ? 0 : p.xe[i + 1];
-    g.g.e.alpha = pow2(out - p.be[i] - p.xe[i]);
-    g.g.e.beta = p.a[i] * pow2(out - p.xe[i]);
+    g.g.ep.alpha = pow2(out - p.be[i] - p.xe[i]);
+    g.g.ep.beta = p.a[i] * pow2(out - p.xe[i]);
     if (i == 0) {
-      g.g.e.info = w.info;
-      g.g.e.fpow = 1;
+      g.g.ep.info = w.info;
+      g.g.ep.fpow = 1;
     }
     if (last) {
-      g.g.e.y = Y;
-      g.g.e.y_bf16 = p.bf16;
-      g.g.e.y_transposed = p.tall;
+      g.to_caller(p, Y);
     } else {
       g.to(w.X[i + 1]);
     }
@@ -1012,10 +1140,10 @@ cudaError_t backward(const Plan& p, const void* G, const void* dY, void* dG, con
       Product g(p, w.S, p.q, false, true, w.status);
       g.add(H, X);
       g.add(X, H);
-      g.g.e.alpha = pow2(se[i] - p.xe[i]);
+      g.g.ep.alpha = pow2(se[i] - p.xe[i]);
       if (i == 0) {
-        g.g.e.info = f.info;
-        g.g.e.fpow = 1;
+        g.g.ep.info = f.info;
+        g.g.ep.fpow = 1;
       }
       g.to(w.S);
       e = g.launch(log);
@@ -1027,11 +1155,11 @@ cudaError_t backward(const Plan& p, const void* G, const void* dY, void* dG, con
       g.add(A, w.S);
       g.add(w.S, A);
       g.plus(w.S);
-      g.g.e.alpha = p.c[i] * pow2(te - p.ae[i] - se[i]);
-      g.g.e.beta = p.b[i] * pow2(te - se[i]);
+      g.g.ep.alpha = p.c[i] * pow2(te - p.ae[i] - se[i]);
+      g.g.ep.beta = p.b[i] * pow2(te - se[i]);
       if (i == 0) {  // X_0 is f times what is stored
-        g.g.e.info = f.info;
-        g.g.e.fpow = 1;
+        g.g.ep.info = f.info;
+        g.g.ep.fpow = 1;
       }
       g.to(w.T);
       e = g.launch(log);
@@ -1041,42 +1169,55 @@ cudaError_t backward(const Plan& p, const void* G, const void* dY, void* dG, con
     g.add(B, H);
     g.add(w.T, X);
     g.plus(H);
-    g.g.e.alpha = pow2(-p.be[i]);
-    g.g.e.beta = p.a[i];
-    g.g.e.sums = w.step_sums[turn];
-    if (i > 0) {
-      g.g.e.scale_sums = sums;
-      g.g.e.scale_parts = parts;
-      g.g.e.target = target[i - 1];
-      g.g.e.exp_in = w.exp[i + 1];
-      g.g.e.exp_out = w.exp[i];
-      g.to(w.H[turn ^ 1]);
-    } else {
-      g.g.e.of32 = w.h0;
-      g.g.e.olds = p.ldq;
-      g.g.e.dhi = f.X[0].hi;
-      g.g.e.dlo = f.X[0].lo;
-    }
+    g.g.ep.alpha = pow2(-p.be[i]);
+    g.g.ep.beta = p.a[i];
+    g.g.ep.sums = i > 0 ? w.step_sums[turn] : nullptr;
+    g.g.ep.scale_sums = sums;
+    g.g.ep.scale_parts = parts;
+    g.g.ep.target = i > 0 ? target[i - 1] : 12;
+    g.g.ep.exp_in = w.exp[i + 1];
+    g.g.ep.exp_out = w.exp[i];
+    g.to(w.H[turn ^ 1]);
     sums = w.step_sums[turn];
     parts = product_parts(p);
     e = g.launch(log);
   }
   if (e != cudaSuccess) return e;
+  const Terms &H0 = w.H[turn], &X0 = f.X[0];
+  DotArgs d = {};
+  d.h[0] = H0.hi;
+  d.h[1] = H0.lo;
+  d.x[0] = X0.hi;
+  d.x[1] = X0.lo;
+  d.partial = w.sums;
+  d.p = p.p; d.q = p.q; d.ld = p.ldq;
+  term_dots<<<dim3((unsigned)p.square_parts, (unsigned)p.L), kSumThreads, 0, log.stream>>>(d);
+  e = cudaGetLastError();
+  log.mark();
+  if (e != cudaSuccess) return e;
   EndArgs n = {};
   n.g = G;
   n.dg = dG;
-  n.h = w.h0;
-  n.dots = sums;
-  n.parts = parts;
+  n.h[0] = H0.hi;
+  n.h[1] = H0.lo;
+  n.dots = w.sums;
+  n.parts = p.square_parts;
   n.p = p.p; n.q = p.q; n.ld = p.ldq; n.tall = p.tall; n.x_exp = p.xe[0];
   n.info = f.info;
-  n.exp = w.exp[1];
+  n.exp = w.exp[0];
   const dim3 tiles((unsigned)((p.q + kPack - 1) / kPack), (unsigned)((p.p + kPack - 1) / kPack), (unsigned)p.L);
   if (p.bf16) end_gradient<__nv_bfloat16><<<tiles, kSumThreads, 0, log.stream>>>(n);
   else end_gradient<float><<<tiles, kSumThreads, 0, log.stream>>>(n);
   e = cudaGetLastError();
   log.mark();
   return e;
+}
+
+// Makes the device's context current in a thread that is new to the GPU (autograd's
+// are), as making tensor maps needs.
+bool enter() {
+  int dev;
+  return cudaGetDevice(&dev) == cudaSuccess && cudaSetDevice(dev) == cudaSuccess;
 }
 
 bool off(const void* p, size_t n) { return reinterpret_cast<uintptr_t>(p) % n != 0; }
@@ -1102,8 +1243,10 @@ int fbob_orth_forward(const fbob_orth_t* o, const void* g, void* y, void* ws, si
   if (st != FBOB_OK) return st;
   const size_t size = p.bf16 ? 2 : 4;
   if (!g || !y || !ws || off(g, size) || off(y, size) || off(ws, 256)) return FBOB_ERR_INVALID_ARG;
+  if (ws_bytes < carve_forward(p, nullptr).bytes) return FBOB_ERR_WORKSPACE;
+  if (!enter()) return FBOB_ERR_CUDA;
   const Forward w = carve_forward(p, static_cast<char*>(ws));
-  if (ws_bytes < w.bytes) return FBOB_ERR_WORKSPACE;
+  if (!w.ok) return FBOB_ERR_CUDA;
   LaunchLog log{static_cast<cudaStream_t>(stream)};
   begin_call(log);
   const cudaError_t e = forward(p, g, y, w, log);
@@ -1120,9 +1263,12 @@ int fbob_orth_backward(const fbob_orth_t* o, const void* g, const void* dy, void
   if (!p.keep || !g || !dy || !dg || !kept || !ws || off(g, size) || off(dy, size) || off(dg, size) ||
       off(kept, 256) || off(ws, 256))
     return FBOB_ERR_INVALID_ARG;
+  if (kept_bytes < carve_forward(p, nullptr).bytes || ws_bytes < carve_backward(p, nullptr).bytes)
+    return FBOB_ERR_WORKSPACE;
+  if (!enter()) return FBOB_ERR_CUDA;
   const Forward f = carve_forward(p, const_cast<char*>(static_cast<const char*>(kept)));
   const Backward w = carve_backward(p, static_cast<char*>(ws));
-  if (kept_bytes < f.bytes || ws_bytes < w.bytes) return FBOB_ERR_WORKSPACE;
+  if (!f.ok || !w.ok) return FBOB_ERR_CUDA;
   LaunchLog log{static_cast<cudaStream_t>(stream)};
   begin_call(log);
   const cudaError_t e = backward(p, g, dy, dg, f, w, log);
