@@ -80,7 +80,9 @@ constexpr int kThreads = 320;
 constexpr int kMaxSegs = 6;
 // Two groups of four warps finish 64 columns at a time, each through two slots of
 // 128 rows x 64 columns: what is added comes in by TMA, the result is written in its place and
-// leaves by TMA.  Values of two terms take both slots.
+// leaves by TMA.  Values of two terms take both slots; of one term, where the result is
+// symmetric, the second holds the tile transposed.  (Mirrored by stores from registers
+// a tile of 128 x 64 took 4 us, with a box more to store 2.)
 constexpr int kGroups = 2;
 constexpr uint32_t kOffSlots = kStages * kStageBytes;
 constexpr uint32_t kOffMisc = kOffSlots + kGroups * 2 * kTileBytes;
@@ -92,7 +94,7 @@ struct Epilogue {
   int e_terms;                  // of E: 0 without
   const MatInfo* info;          // f of each matrix
   int fpow;
-  // results: o_terms terms by rows (sym: also mirrored, at o), or the caller's tensor y,
+  // results: o_terms terms by rows (sym: also mirrored, two terms at o), or the caller's tensor y,
   // through maps as well where its rows are at 16-byte steps (o_terms 0)
   int o_terms;
   __half* o[2];
@@ -124,6 +126,11 @@ __host__ __device__ constexpr uint32_t idesc_f16(int M, int N, bool b_mn_major) 
          ((uint32_t)(M >> 4) << 24);
 }
 
+// The kernels of a call follow one another closely: each lets the next one start as soon as
+// all its own blocks run, and begins to read and write when the one before is done.
+__device__ __forceinline__ void let_next_start() { asm volatile("griddepcontrol.launch_dependents;" ::: "memory"); }
+__device__ __forceinline__ void after_previous() { asm volatile("griddepcontrol.wait;" ::: "memory"); }
+
 struct TileAt {
   int l, i, j, index;  // matrix, tile row and column, its number within the matrix
 };
@@ -151,25 +158,25 @@ __device__ __forceinline__ void split(float v, __half& hi, __half& lo) {
   lo = __float2half_rn(v - __half2float(hi));
 }
 
-__device__ __forceinline__ uint32_t pack2(__half a, __half b) {
-  return (uint32_t)__half_as_ushort(a) | ((uint32_t)__half_as_ushort(b) << 16);
-}
-
 // 32 columns (half h) of a thread's row in a slot: 16-byte chunks 4 h .. 4 h + 3.
 __device__ __forceinline__ uint4* slot_chunk(uint8_t* slot, int row, int c) {
   return reinterpret_cast<uint4*>(slot + sw128_offset(row, c));
 }
-__device__ __forceinline__ void add_slot(float (&v)[32], uint8_t* slot, int row, int h, float beta) {
+__device__ __forceinline__ f2 halves(uint32_t w) {
+  return __half22float2(*reinterpret_cast<const __half2*>(&w));
+}
+__device__ __forceinline__ uint32_t to_halves(f2 v) {
+  const __half2 h = __floats2half2_rn(v.x, v.y);
+  return *reinterpret_cast<const uint32_t*>(&h);
+}
+__device__ __forceinline__ void add_slot(f2 (&v)[16], uint8_t* slot, int row, int h, float beta) {
+  const f2 b = {beta, beta};
 #pragma unroll
   for (int q = 0; q < 4; ++q) {
     const uint4 x = *slot_chunk(slot, row, 4 * h + q);
     const uint32_t w[4] = {x.x, x.y, x.z, x.w};
 #pragma unroll
-    for (int k = 0; k < 4; ++k) {
-      const float2 t = __half22float2(*reinterpret_cast<const __half2*>(&w[k]));
-      v[8 * q + 2 * k] = fmaf(beta, t.x, v[8 * q + 2 * k]);
-      v[8 * q + 2 * k + 1] = fmaf(beta, t.y, v[8 * q + 2 * k + 1]);
-    }
+    for (int k = 0; k < 4; ++k) v[4 * q + k] = fma2(b, halves(w[k]), v[4 * q + k]);
   }
 }
 __device__ __forceinline__ void put_slot(const uint32_t (&w)[16], uint8_t* slot, int row, int h) {
@@ -177,15 +184,30 @@ __device__ __forceinline__ void put_slot(const uint32_t (&w)[16], uint8_t* slot,
   for (int q = 0; q < 4; ++q)
     *slot_chunk(slot, row, 4 * h + q) = make_uint4(w[4 * q], w[4 * q + 1], w[4 * q + 2], w[4 * q + 3]);
 }
-
-__device__ __forceinline__ void put_floats(const float (&v)[32], uint8_t* slot, int row) {
+__device__ __forceinline__ void put_floats(const f2 (&v)[16], uint8_t* slot, int row) {
 #pragma unroll
   for (int k = 0; k < 8; ++k)
     *reinterpret_cast<float4*>(slot_chunk(slot, row, k)) =
-        make_float4(v[4 * k], v[4 * k + 1], v[4 * k + 2], v[4 * k + 3]);
+        make_float4(v[2 * k].x, v[2 * k].y, v[2 * k + 1].x, v[2 * k + 1].y);
+}
+// The same columns as rows of the transposed tile: two boxes of 64 rows x 64 columns,
+// the tile's rows 0 .. 63 and 64 .. 127.  A warp's lanes write neighbouring elements.
+__device__ __forceinline__ void put_slot_transposed(const uint32_t (&w)[16], uint8_t* slot, int row, int h) {
+  const uint32_t box = smem_u32(slot) + (row >> 6) * (kTileBytes / 2) + (row & 7) * 2;
+  const uint32_t chunk = (row & 63) >> 3;
+#pragma unroll
+  for (int k = 0; k < 16; ++k) {
+    const uint32_t c = 32 * h + 2 * k;
+    asm volatile("st.shared.u16 [%0], %1;" ::"r"(box + sw128_offset(c, chunk)),
+                 "h"((unsigned short)(w[k] & 0xffffu))
+                 : "memory");
+    asm volatile("st.shared.u16 [%0], %1;" ::"r"(box + sw128_offset(c + 1, chunk)),
+                 "h"((unsigned short)(w[k] >> 16))
+                 : "memory");
+  }
 }
 
-// Writes 32 columns of a row to the mirrored place.  Neighbouring lanes hold
+// Writes 32 columns of a row in two terms to the mirrored place.  Neighbouring lanes hold
 // neighbouring rows: they exchange halves, so that each writes two rows of every other
 // column at once.  (An odd matrix's last pair reaches into the padding of its rows.)
 __device__ __forceinline__ void put_mirrored(const uint32_t (&hi)[16], const uint32_t (&lo)[16],
@@ -204,13 +226,13 @@ __device__ __forceinline__ void put_mirrored(const uint32_t (&hi)[16], const uin
     if (pair < rows && c < cols) {
       const size_t at = base + (size_t)c * e.old + pair;
       *reinterpret_cast<uint32_t*>(e.o[0] + at) = h;
-      if (e.o_terms == 2) *reinterpret_cast<uint32_t*>(e.o[1] + at) = l;
+      *reinterpret_cast<uint32_t*>(e.o[1] + at) = l;
     }
   }
 }
 
 // 32 values of a row straight to the caller's tensor, where no map can take them.
-__device__ __forceinline__ void put_caller(const float (&v)[32], const ProductArgs& g, int l, int row, int col) {
+__device__ __forceinline__ void put_caller(const f2 (&v)[16], const ProductArgs& g, int l, int row, int col) {
   const Epilogue& e = g.ep;
   if (row >= g.rows) return;
   const size_t first = (size_t)l * g.rows * g.cols +
@@ -219,8 +241,9 @@ __device__ __forceinline__ void put_caller(const float (&v)[32], const ProductAr
 #pragma unroll
   for (int c = 0; c < 32; ++c)
     if (col + c < g.cols) {
-      if (e.y_bf16) static_cast<__nv_bfloat16*>(e.y)[first + c * step] = __float2bfloat16_rn(v[c]);
-      else static_cast<float*>(e.y)[first + c * step] = v[c];
+      const float x = c & 1 ? v[c / 2].y : v[c / 2].x;
+      if (e.y_bf16) static_cast<__nv_bfloat16*>(e.y)[first + c * step] = __float2bfloat16_rn(x);
+      else static_cast<float*>(e.y)[first + c * step] = x;
     }
 }
 
@@ -242,6 +265,7 @@ template <int CTAS, bool NN>
 __global__ void __launch_bounds__(kThreads, 1) product(const __grid_constant__ ProductArgs g) {
   extern __shared__ __align__(1024) uint8_t smem[];
   const uint32_t sb = smem_u32(smem);
+  let_next_start();
   if (sb & 1023u) {  // 128-byte swizzled tiles need a 1024-byte aligned base
     if (threadIdx.x == 0) report_status(g.status, FBOB_ERR_CUDA);
     return;
@@ -286,6 +310,7 @@ __global__ void __launch_bounds__(kThreads, 1) product(const __grid_constant__ P
   __syncthreads();
   if (CTAS == 2) cluster_sync();  // the other's barriers are there
   tc_fence_after();
+  after_previous();
   const uint32_t tmem = *tmem_slot;
   const int tm = (g.rows + kSide - 1) / kSide, tn = (g.cols + kSide - 1) / kSide;
   const int per = g.sym ? tm * (tm + 1) / 2 : tm * tn;
@@ -392,7 +417,7 @@ __global__ void __launch_bounds__(kThreads, 1) product(const __grid_constant__ P
     uint8_t* const slots = smem + kOffSlots + group * 2 * kTileBytes;
     uint64_t* const e_bar = e_full + 2 * group;
     constexpr int kChunks = kSide / 64 / kGroups;  // of a tile, for each group
-    const bool two = e.e_terms == 2 || e.o_terms == 2 || (e.y_mapped && !e.y_bf16);
+    const bool two = g.sym || e.e_terms == 2 || e.o_terms == 2 || (e.y_mapped && !e.y_bf16);
     const int nslots = two ? 1 : 2;
     const int mine = first < tiles ? ((tiles - 1 - first) / step + 1) * kChunks : 0;
     // the slot of chunk u is free once the result before it has left; then what is
@@ -447,48 +472,56 @@ __global__ void __launch_bounds__(kThreads, 1) product(const __grid_constant__ P
         const int s = u % nslots;
         uint8_t* const slot = slots + s * kTileBytes;
         ok = ok && warp_wait(e_bar + s, (u / nslots) & 1, ab, g.status);
-        float kept[32];
-#pragma unroll
+        const bool mirror = g.sym && at.i != at.j;
+#pragma unroll 1
         for (int h = 0; h < 2; ++h) {
           const int col = col0 + 32 * h;
           uint32_t acc[32];
           tmem_ld32(tmem + lane_off + (n & 1) * kSide + in_tile + 32 * h, acc);
-          float v[32];
+          f2 v[16];
 #pragma unroll
-          for (int k = 0; k < 32; ++k) v[k] = alpha * __uint_as_float(acc[k]);
+          for (int k = 0; k < 16; ++k)
+            v[k] = mul2(f2{alpha, alpha}, f2{__uint_as_float(acc[2 * k]), __uint_as_float(acc[2 * k + 1])});
           if (e.e_terms) add_slot(v, slot, r, h, beta);
           if (e.e_terms == 2) add_slot(v, slot + kTileBytes, r, h, beta);
           if (e.sums) {  // (what lies outside is zero)
 #pragma unroll
-            for (int k = 0; k < 32; ++k) sum = fmaf(v[k], v[k], sum);
+            for (int k = 0; k < 16; ++k) sum = fmaf(v[k].x, v[k].x, fmaf(v[k].y, v[k].y, sum));
           }
           uint32_t w[16];
           if (e.o_terms) {
-            uint32_t lo[16];
 #pragma unroll
-            for (int k = 0; k < 16; ++k) {
-              __half ha, la, hb, lb;
-              split(v[2 * k], ha, la);
-              split(v[2 * k + 1], hb, lb);
-              w[k] = pack2(ha, hb);
-              lo[k] = pack2(la, lb);
-            }
+            for (int k = 0; k < 16; ++k) w[k] = to_halves(v[k]);
             put_slot(w, slot, r, h);
-            if (e.o_terms == 2) put_slot(lo, slot + kTileBytes, r, h);
-            if (g.sym && at.i != at.j)
-              put_mirrored(w, lo, e, (size_t)at.l * g.rows * e.old, row, col, g.rows, g.cols);
+            if (e.o_terms == 2) {
+              uint32_t lo[16];
+#pragma unroll
+              for (int k = 0; k < 16; ++k) lo[k] = to_halves(fma2(f2{-1.f, -1.f}, halves(w[k]), v[k]));
+              put_slot(lo, slot + kTileBytes, r, h);
+              if (mirror)
+                put_mirrored(w, lo, e, (size_t)at.l * g.rows * e.old, row, col, g.rows, g.cols);
+            } else if (mirror) {
+              put_slot_transposed(w, slot + kTileBytes, r, h);
+            }
           } else if (!e.y_mapped) {
             put_caller(v, g, at.l, row, col);
           } else if (e.y_bf16) {
 #pragma unroll
-            for (int k = 0; k < 16; ++k) w[k] = pack_bf16(v[2 * k], v[2 * k + 1]);
+            for (int k = 0; k < 16; ++k) w[k] = pack_bf16(v[k].x, v[k].y);
             put_slot(w, slot, r, h);
-          } else if (h == 0) {  // 32 fp32 columns fill a slot's rows: after the second half is read
+          } else if (h == 0) {  // 32 fp32 columns fill a slot row: kept in both until all is read
 #pragma unroll
-            for (int k = 0; k < 32; ++k) kept[k] = v[k];
+            for (int k = 0; k < 8; ++k)
+              *reinterpret_cast<float4*>(slot_chunk(slot + (k >> 2) * kTileBytes, r, k & 3)) =
+                  make_float4(v[2 * k].x, v[2 * k].y, v[2 * k + 1].x, v[2 * k + 1].y);
           } else {
-            put_floats(kept, slot, r);
+            float4 f[4];
+#pragma unroll
+            for (int k = 0; k < 4; ++k)
+              f[k] = *reinterpret_cast<float4*>(slot_chunk(slot + kTileBytes, r, k));
             put_floats(v, slot + kTileBytes, r);
+#pragma unroll
+            for (int k = 0; k < 4; ++k) *reinterpret_cast<float4*>(slot_chunk(slot, r, 4 + k)) = f[k];
           }
         }
         if (c == kChunks - 1) {
@@ -504,7 +537,13 @@ __global__ void __launch_bounds__(kThreads, 1) product(const __grid_constant__ P
         if (issuer) {
           if ((e.o_terms || e.y_mapped) && row0 < g.rows && col0 < g.cols && !ab->flag) {
             tma_store_3d(&g.o[0], slot, col0, row0, at.l);
-            if (e.o_terms == 2) tma_store_3d(&g.o[1], slot + kTileBytes, col0, row0, at.l);
+            if (e.o_terms == 2) {
+              tma_store_3d(&g.o[1], slot + kTileBytes, col0, row0, at.l);
+            } else if (mirror) {
+              tma_store_3d(&g.o[1], slot + kTileBytes, row0, col0, at.l);
+              if (row0 + 64 < g.rows)
+                tma_store_3d(&g.o[1], slot + kTileBytes + kTileBytes / 2, row0 + 64, col0, at.l);
+            }
             if (!e.o_terms && !e.y_bf16 && col0 + 32 < g.cols)
               tma_store_3d(&g.o[0], slot + kTileBytes, col0 + 32, row0, at.l);
             bulk_commit_group();
@@ -548,6 +587,7 @@ template <typename T>
 __global__ void __launch_bounds__(kSumThreads)
     square_sums(const T* __restrict__ x, float* __restrict__ partial, size_t elems, int* status) {
   __shared__ float sm[kSumThreads / 32];
+  let_next_start();
   if (blockIdx.x == 0 && blockIdx.y == 0 && threadIdx.x == 0) *status = 0;
   x += (size_t)blockIdx.y * elems;
   const size_t per = (elems + gridDim.x - 1) / gridDim.x;
@@ -610,6 +650,8 @@ __global__ void __launch_bounds__(kSumThreads) pack(PackArgs a) {
   __shared__ float sm[kSumThreads / 32];
   __shared__ float tile[kPack][kPack + 1];
   const int l = blockIdx.z;
+  let_next_start();
+  after_previous();
   const float nu2 = parts_sum(a.sums + (size_t)l * a.parts, a.parts, sm);
   const bool writer = blockIdx.x == 0 && blockIdx.y == 0 && threadIdx.x == 0;
   float factor;
@@ -665,6 +707,8 @@ struct DotArgs {
 };
 __global__ void __launch_bounds__(kSumThreads) term_dots(DotArgs a) {
   __shared__ float sm[kSumThreads / 32];
+  let_next_start();
+  after_previous();
   const size_t base = (size_t)blockIdx.y * a.p * a.ld;
   const int chunks = a.ld / 8;
   const long long all = (long long)a.p * chunks, per = (all + gridDim.x - 1) / gridDim.x;
@@ -720,6 +764,7 @@ __global__ void __launch_bounds__(kSumThreads) end_gradient(EndArgs a) {
   __shared__ float sm[kSumThreads / 32];
   __shared__ float tile[kPack][kPack + 1];
   const int l = blockIdx.z;
+  after_previous();
   const MatInfo r = a.info[l];
   const float dot = parts_sum(a.dots + (size_t)l * a.parts, a.parts, sm);
   // <h, G> = dot 2^-(k + x_exp); a zero matrix has no direction to take off
@@ -847,8 +892,7 @@ struct Carver {
     off += align_up(bytes);
     return r;
   }
-  // right: also a right operand of P Q
-  Terms terms(const Plan& p, int cols, int ld, int n, bool right) {
+  Terms terms(const Plan& p, int cols, int ld, int n) {
     Terms t;
     const size_t one = (size_t)p.L * p.p * ld * sizeof(__half);
     t.hi = static_cast<__half*>(take(one));
@@ -858,7 +902,7 @@ struct Carver {
       const __half* at = i ? t.lo : t.hi;
       const auto half = CU_TENSOR_MAP_DATA_TYPE_FLOAT16;
       ok = ok && make_tile_map(&t.tile[i], half, 2, at, p.L, p.p, cols, ld, kTile);
-      ok = ok && (!right || make_tile_map(&t.step[i], half, 2, at, p.L, p.p, cols, ld, kDepth));
+      ok = ok && make_tile_map(&t.step[i], half, 2, at, p.L, p.p, cols, ld, kDepth);
     }
     return t;
   }
@@ -898,14 +942,14 @@ Forward carve_forward(const Plan& p, char* base) {
   for (int i = 0; !p.keep && i < 2; ++i) {
     int t = 1;
     for (int k = i; k < p.steps; k += 2) t = p.xt[k] > t ? p.xt[k] : t;
-    turn[i] = c.terms(p, p.q, p.ldq, t, true);
+    turn[i] = c.terms(p, p.q, p.ldq, t);
   }
   for (int i = 0; i < p.steps; ++i) {
-    w.X[i] = p.keep ? c.terms(p, p.q, p.ldq, p.xt[i], true) : turn[i & 1];
+    w.X[i] = p.keep ? c.terms(p, p.q, p.ldq, p.xt[i]) : turn[i & 1];
     if (p.xt[i] == 1) w.X[i].lo = nullptr;
     if (p.keep || i == 0) {
-      w.A[i] = c.terms(p, p.p, p.ldp, small, false);
-      w.B[i] = c.terms(p, p.p, p.ldp, small, false);
+      w.A[i] = c.terms(p, p.p, p.ldp, small);
+      w.B[i] = c.terms(p, p.p, p.ldp, small);
     } else {
       w.A[i] = w.A[0];
       w.B[i] = w.B[0];
@@ -935,12 +979,34 @@ Backward carve_backward(const Plan& p, char* base) {
   w.first = static_cast<float*>(c.take(sizeof(float) * p.L));
   for (float*& s : w.step_sums) s = static_cast<float*>(c.take(sizeof(float) * p.L * product_parts(p)));
   for (int i = 0; i <= p.steps; ++i) w.exp[i] = static_cast<int*>(c.take(sizeof(int) * p.L));
-  for (Terms& h : w.H) h = c.terms(p, p.q, p.ldq, t, true);
-  w.S = c.terms(p, p.p, p.ldp, t, false);
-  w.T = c.terms(p, p.p, p.ldp, t, false);
+  for (Terms& h : w.H) h = c.terms(p, p.q, p.ldq, t);
+  w.S = c.terms(p, p.p, p.ldp, t);
+  w.T = c.terms(p, p.p, p.ldp, t);
   w.ok = c.ok;
   w.bytes = c.off;
   return w;
+}
+
+// Launches a kernel that may start while the one before it in the stream ends.
+template <typename... P, typename... A>
+cudaError_t launch_next(void (*kernel)(P...), dim3 grid, int threads, size_t smem, int cluster,
+                        LaunchLog& log, A... args) {
+  cudaLaunchConfig_t c = {};
+  c.gridDim = grid;
+  c.blockDim = dim3((unsigned)threads);
+  c.dynamicSmemBytes = smem;
+  c.stream = log.stream;
+  cudaLaunchAttribute attr[2];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  attr[1].id = cudaLaunchAttributeClusterDimension;
+  attr[1].val.clusterDim.x = (unsigned)cluster;
+  attr[1].val.clusterDim.y = attr[1].val.clusterDim.z = 1;
+  c.attrs = attr;
+  c.numAttrs = cluster > 1 ? 2 : 1;
+  const cudaError_t e = cudaLaunchKernelEx(&c, kernel, args...);
+  log.mark();
+  return e;
 }
 
 // Builds and launches one product.
@@ -983,7 +1049,7 @@ struct Product {
   void to(const Terms& O) {
     g.ep.o_terms = O.lo ? 2 : 1;
     g.o[0] = O.tile[0];
-    g.o[1] = O.tile[1];
+    g.o[1] = O.lo ? O.tile[1] : O.step[0];  // one term: mirrored in boxes of 64 rows
     g.ep.o[0] = O.hi;
     g.ep.o[1] = O.lo;
     g.ep.old = O.ld;
@@ -1010,20 +1076,7 @@ struct Product {
                             : (nn ? product<1, true> : product<1, false>);
     cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmem);
     if (e != cudaSuccess) return e;
-    cudaLaunchConfig_t c = {};
-    c.gridDim = dim3((unsigned)grid);
-    c.blockDim = dim3(kThreads);
-    c.dynamicSmemBytes = kSmem;
-    c.stream = log.stream;
-    cudaLaunchAttribute attr[1];
-    attr[0].id = cudaLaunchAttributeClusterDimension;
-    attr[0].val.clusterDim.x = (unsigned)ctas;
-    attr[0].val.clusterDim.y = attr[0].val.clusterDim.z = 1;
-    c.attrs = attr;
-    c.numAttrs = 1;
-    e = cudaLaunchKernelEx(&c, kernel, g);
-    log.mark();
-    return e;
+    return launch_next(kernel, dim3((unsigned)grid), kThreads, kSmem, ctas, log, g);
   }
 };
 
@@ -1044,11 +1097,7 @@ cudaError_t squares_and_pack(const Plan& p, const void* x, float* sums, int* sta
   a.p = p.p; a.q = p.q; a.ld = p.ldq; a.tall = p.tall;
   a.eps = p.eps;
   const dim3 tiles((unsigned)((p.q + kPack - 1) / kPack), (unsigned)((p.p + kPack - 1) / kPack), (unsigned)p.L);
-  if (p.bf16) pack<__nv_bfloat16><<<tiles, kSumThreads, 0, log.stream>>>(a);
-  else pack<float><<<tiles, kSumThreads, 0, log.stream>>>(a);
-  e = cudaGetLastError();
-  log.mark();
-  return e;
+  return launch_next(p.bf16 ? pack<__nv_bfloat16> : pack<float>, tiles, kSumThreads, 0, 1, log, a);
 }
 
 float pow2(int e) { return ldexpf(1.f, e); }
@@ -1191,9 +1240,7 @@ cudaError_t backward(const Plan& p, const void* G, const void* dY, void* dG, con
   d.x[1] = X0.lo;
   d.partial = w.sums;
   d.p = p.p; d.q = p.q; d.ld = p.ldq;
-  term_dots<<<dim3((unsigned)p.square_parts, (unsigned)p.L), kSumThreads, 0, log.stream>>>(d);
-  e = cudaGetLastError();
-  log.mark();
+  e = launch_next(term_dots, dim3((unsigned)p.square_parts, (unsigned)p.L), kSumThreads, 0, 1, log, d);
   if (e != cudaSuccess) return e;
   EndArgs n = {};
   n.g = G;
@@ -1206,11 +1253,8 @@ cudaError_t backward(const Plan& p, const void* G, const void* dY, void* dG, con
   n.info = f.info;
   n.exp = w.exp[0];
   const dim3 tiles((unsigned)((p.q + kPack - 1) / kPack), (unsigned)((p.p + kPack - 1) / kPack), (unsigned)p.L);
-  if (p.bf16) end_gradient<__nv_bfloat16><<<tiles, kSumThreads, 0, log.stream>>>(n);
-  else end_gradient<float><<<tiles, kSumThreads, 0, log.stream>>>(n);
-  e = cudaGetLastError();
-  log.mark();
-  return e;
+  return launch_next(p.bf16 ? end_gradient<__nv_bfloat16> : end_gradient<float>, tiles, kSumThreads, 0, 1,
+                     log, n);
 }
 
 // Makes the device's context current in a thread that is new to the GPU (autograd's
