@@ -8,7 +8,7 @@
 // and at the end dG = s (H_0 - G <H_0, G> s / |G|_F).
 //
 // All of these are products P Q^T or P Q of matrices stored by rows, summed in one
-// accumulator and finished by alpha acc + beta E: one kernel (product) serves them
+// accumulator and finished by alpha acc + beta E: one kernel (orth_chain.cu) runs them
 // all.  A, B, S and T are symmetric: only tiles on and below the diagonal are computed,
 // and written in both places.  S and A S + S A are sums of a product and its transpose: as
 // one accumulation [H | X] [X | H]^T they need half the tiles, too.
@@ -38,542 +38,21 @@
 #include "fbob.h"
 #include "internal.h"
 #include "ops.h"
-#include "sm103.cuh"
+#include "orth.h"
 #include "tc_common.cuh"
 
 namespace fbob {
 namespace {
 
-using namespace tc;
+using namespace orth;
+using tc::encode_fn;
 
 constexpr size_t kAlign = 256;
 size_t align_up(size_t x) { return (x + kAlign - 1) / kAlign * kAlign; }
 
-// ---------------------------------------------------------------------------
-// What is kept of a matrix
-// ---------------------------------------------------------------------------
-struct MatInfo {
-  float norm, s;  // |G|_F and 1 / (norm + eps)
-  float f;        // X_0 = f G 2^k: f in [1, 2)
-  int k;
-};
-
-// A matrix in one or two fp16 terms: rows of ld elements, [count] matrices.  Its maps:
-// tiles of 128 rows and 64 columns (left operands, right ones of P Q^T, what is added,
-// results) and of 64 rows and 64 columns (right operands of P Q).
-struct Terms {
-  __half *hi = nullptr, *lo = nullptr;
-  int rows = 0, cols = 0, ld = 0;
-  CUtensorMap tile[2], step[2];
-};
-
-// ---------------------------------------------------------------------------
-// The product kernel
-// ---------------------------------------------------------------------------
-constexpr int kTile = 128;        // rows, and columns, of a CTA's operand tiles
-constexpr int kDepth = 64;        // contraction elements of a stage (128-byte rows)
-constexpr int kStages = 5;
-constexpr uint32_t kTileBytes = kTile * kDepth * 2;
-constexpr uint32_t kStageBytes = 2 * kTileBytes;
-constexpr int kEpiWarps = 8, kProducerWarp = 8, kMmaWarp = 9;
-constexpr int kThreads = 320;
-constexpr int kMaxSegs = 6;
-// Two groups of four warps finish 64 columns at a time, each through two slots of
-// 128 rows x 64 columns: what is added comes in by TMA, the result is written in its place and
-// leaves by TMA.  Values of two terms take both slots; of one term, where the result is
-// symmetric, the second holds the tile transposed.  (Mirrored by stores from registers
-// a tile of 128 x 64 took 4 us, with a box more to store 2.)
-constexpr int kGroups = 2;
-constexpr uint32_t kOffSlots = kStages * kStageBytes;
-constexpr uint32_t kOffMisc = kOffSlots + kGroups * 2 * kTileBytes;
-constexpr uint32_t kSmem = kOffMisc + 512;
-static_assert(kSmem <= 232448, "shared memory budget");
-
-struct Epilogue {
-  float alpha, beta;            // value = (alpha acc + beta E) f^fpow, times the rescaling
-  int e_terms;                  // of E: 0 without
-  const MatInfo* info;          // f of each matrix
-  int fpow;
-  // results: o_terms terms by rows (sym: also mirrored, two terms at o), or the caller's tensor y,
-  // through maps as well where its rows are at 16-byte steps (o_terms 0)
-  int o_terms;
-  __half* o[2];
-  int old;
-  void* y;
-  int y_bf16, y_transposed, y_mapped;
-  float* sums;                  // [count][parts of a matrix]: squares of the values, or null
-  // rescaling by the norm of the step's input: [count][scale_parts] squares
-  const float* scale_sums;
-  int scale_parts, target;
-  const int* exp_in;
-  int* exp_out;
-};
-
-struct ProductArgs {
-  CUtensorMap a[4], b[4], e[2], o[2];
-  unsigned char seg_a[kMaxSegs], seg_b[kMaxSegs];
-  int nseg;
-  int rows, cols, depth, count;
-  int sym;
-  Epilogue ep;
-  int* status;
-  unsigned long long wait_ns;
-};
-
-// Instruction descriptor: fp16 operands (formats 0), fp32 accumulator.
-__host__ __device__ constexpr uint32_t idesc_f16(int M, int N, bool b_mn_major) {
-  return (1u << 4) | ((b_mn_major ? 1u : 0u) << 16) | ((uint32_t)(N >> 3) << 17) |
-         ((uint32_t)(M >> 4) << 24);
-}
-
-// The kernels of a call follow one another closely: each lets the next one start as soon as
-// all its own blocks run, and begins to read and write when the one before is done.
-__device__ __forceinline__ void let_next_start() { asm volatile("griddepcontrol.launch_dependents;" ::: "memory"); }
-__device__ __forceinline__ void after_previous() { asm volatile("griddepcontrol.wait;" ::: "memory"); }
-
-struct TileAt {
-  int l, i, j, index;  // matrix, tile row and column, its number within the matrix
-};
-__device__ __forceinline__ TileAt tile_at(const ProductArgs& g, int t, int side) {
-  const int tm = (g.rows + side - 1) / side, tn = (g.cols + side - 1) / side;
-  const int per = g.sym ? tm * (tm + 1) / 2 : tm * tn;
-  TileAt r;
-  r.l = t / per;
-  r.index = t - r.l * per;
-  if (g.sym) {
-    int i = (int)((sqrtf(8.f * r.index + 1.f) - 1.f) * 0.5f);
-    while (i * (i + 1) / 2 > r.index) --i;
-    while ((i + 1) * (i + 2) / 2 <= r.index) ++i;
-    r.i = i;
-    r.j = r.index - i * (i + 1) / 2;
-  } else {  // a column of tiles after the other: its operand tile is shared
-    r.j = r.index / tm;
-    r.i = r.index - r.j * tm;
-  }
-  return r;
-}
-
 __device__ __forceinline__ void split(float v, __half& hi, __half& lo) {
   hi = __float2half_rn(v);
   lo = __float2half_rn(v - __half2float(hi));
-}
-
-// 32 columns (half h) of a thread's row in a slot: 16-byte chunks 4 h .. 4 h + 3.
-__device__ __forceinline__ uint4* slot_chunk(uint8_t* slot, int row, int c) {
-  return reinterpret_cast<uint4*>(slot + sw128_offset(row, c));
-}
-__device__ __forceinline__ f2 halves(uint32_t w) {
-  return __half22float2(*reinterpret_cast<const __half2*>(&w));
-}
-__device__ __forceinline__ uint32_t to_halves(f2 v) {
-  const __half2 h = __floats2half2_rn(v.x, v.y);
-  return *reinterpret_cast<const uint32_t*>(&h);
-}
-__device__ __forceinline__ void add_slot(f2 (&v)[16], uint8_t* slot, int row, int h, float beta) {
-  const f2 b = {beta, beta};
-#pragma unroll
-  for (int q = 0; q < 4; ++q) {
-    const uint4 x = *slot_chunk(slot, row, 4 * h + q);
-    const uint32_t w[4] = {x.x, x.y, x.z, x.w};
-#pragma unroll
-    for (int k = 0; k < 4; ++k) v[4 * q + k] = fma2(b, halves(w[k]), v[4 * q + k]);
-  }
-}
-__device__ __forceinline__ void put_slot(const uint32_t (&w)[16], uint8_t* slot, int row, int h) {
-#pragma unroll
-  for (int q = 0; q < 4; ++q)
-    *slot_chunk(slot, row, 4 * h + q) = make_uint4(w[4 * q], w[4 * q + 1], w[4 * q + 2], w[4 * q + 3]);
-}
-__device__ __forceinline__ void put_floats(const f2 (&v)[16], uint8_t* slot, int row) {
-#pragma unroll
-  for (int k = 0; k < 8; ++k)
-    *reinterpret_cast<float4*>(slot_chunk(slot, row, k)) =
-        make_float4(v[2 * k].x, v[2 * k].y, v[2 * k + 1].x, v[2 * k + 1].y);
-}
-// The same columns as rows of the transposed tile: two boxes of 64 rows x 64 columns,
-// the tile's rows 0 .. 63 and 64 .. 127.  A warp's lanes write neighbouring elements.
-__device__ __forceinline__ void put_slot_transposed(const uint32_t (&w)[16], uint8_t* slot, int row, int h) {
-  const uint32_t box = smem_u32(slot) + (row >> 6) * (kTileBytes / 2) + (row & 7) * 2;
-  const uint32_t chunk = (row & 63) >> 3;
-#pragma unroll
-  for (int k = 0; k < 16; ++k) {
-    const uint32_t c = 32 * h + 2 * k;
-    asm volatile("st.shared.u16 [%0], %1;" ::"r"(box + sw128_offset(c, chunk)),
-                 "h"((unsigned short)(w[k] & 0xffffu))
-                 : "memory");
-    asm volatile("st.shared.u16 [%0], %1;" ::"r"(box + sw128_offset(c + 1, chunk)),
-                 "h"((unsigned short)(w[k] >> 16))
-                 : "memory");
-  }
-}
-
-// Writes 32 columns of a row in two terms to the mirrored place.  Neighbouring lanes hold
-// neighbouring rows: they exchange halves, so that each writes two rows of every other
-// column at once.  (An odd matrix's last pair reaches into the padding of its rows.)
-__device__ __forceinline__ void put_mirrored(const uint32_t (&hi)[16], const uint32_t (&lo)[16],
-                                             const Epilogue& e, size_t base, int row, int col, int rows,
-                                             int cols) {
-  const bool odd = row & 1;
-  const int pair = row & ~1;
-#pragma unroll
-  for (int k = 0; k < 16; ++k) {  // columns 2k (low half) and 2k + 1
-    // hi and lo of the column that the partner writes
-    const uint32_t mine = odd ? (hi[k] & 0xffffu) | (lo[k] << 16) : (hi[k] >> 16) | (lo[k] & 0xffff0000u);
-    const uint32_t other = __shfl_xor_sync(0xffffffffu, mine, 1);
-    const int c = col + 2 * k + odd;
-    const uint32_t h = odd ? (other & 0xffffu) | (hi[k] & 0xffff0000u) : (hi[k] & 0xffffu) | (other << 16);
-    const uint32_t l = odd ? (other >> 16) | (lo[k] & 0xffff0000u) : (lo[k] & 0xffffu) | (other & 0xffff0000u);
-    if (pair < rows && c < cols) {
-      const size_t at = base + (size_t)c * e.old + pair;
-      *reinterpret_cast<uint32_t*>(e.o[0] + at) = h;
-      *reinterpret_cast<uint32_t*>(e.o[1] + at) = l;
-    }
-  }
-}
-
-// 32 values of a row straight to the caller's tensor, where no map can take them.
-__device__ __forceinline__ void put_caller(const f2 (&v)[16], const ProductArgs& g, int l, int row, int col) {
-  const Epilogue& e = g.ep;
-  if (row >= g.rows) return;
-  const size_t first = (size_t)l * g.rows * g.cols +
-                       (e.y_transposed ? (size_t)col * g.rows + row : (size_t)row * g.cols + col);
-  const size_t step = e.y_transposed ? g.rows : 1;
-#pragma unroll
-  for (int c = 0; c < 32; ++c)
-    if (col + c < g.cols) {
-      const float x = c & 1 ? v[c / 2].y : v[c / 2].x;
-      if (e.y_bf16) static_cast<__nv_bfloat16*>(e.y)[first + c * step] = __float2bfloat16_rn(x);
-      else static_cast<float*>(e.y)[first + c * step] = x;
-    }
-}
-
-// The exponent that brings a matrix with sum of squares nu2 to a norm in
-// (2^(target - 1), 2^target], or nearly; 0 for zeros and for what is not finite.
-__device__ __forceinline__ int rescaling(float nu2, int target) {
-  if (!(nu2 > 0.f) || nu2 > 3.0e38f) return 0;
-  int e;
-  frexpf(nu2, &e);  // nu2 < 2^e
-  return target - ((e + 1) >> 1);
-}
-
-// acc = sum over segments of P Q^T (Q stored [cols, depth]) or P Q (NN: Q stored
-// [depth, cols]); blocks stay and take tiles in turn.  Warps: 8 finish tiles, one
-// loads, one multiplies; two accumulators, so that a tile is finished while the next
-// is multiplied.  CTAS = 2: a pair of CTAs multiplies a tile of 256 x 256, each loading its
-// 128 rows of P and 128 columns of Q, CTA 0 issuing for both.
-template <int CTAS, bool NN>
-__global__ void __launch_bounds__(kThreads, 1) product(const __grid_constant__ ProductArgs g) {
-  extern __shared__ __align__(1024) uint8_t smem[];
-  const uint32_t sb = smem_u32(smem);
-  let_next_start();
-  if (sb & 1023u) {  // 128-byte swizzled tiles need a 1024-byte aligned base
-    if (threadIdx.x == 0) report_status(g.status, FBOB_ERR_CUDA);
-    return;
-  }
-  uint64_t* full = reinterpret_cast<uint64_t*>(smem + kOffMisc);  // [kStages]
-  uint64_t* empty = full + kStages;                               // [kStages]
-  uint64_t* t_full = empty + kStages;                             // [2]
-  uint64_t* t_empty = t_full + 2;                                 // [2]
-  uint64_t* e_full = t_empty + 2;                                 // [kGroups][2]
-  uint64_t* drain = e_full + 2 * kGroups;
-  uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(smem + kOffMisc + 256);
-  Abort* ab = reinterpret_cast<Abort*>(smem + kOffMisc + 264);
-  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  const uint32_t rank = CTAS == 2 ? cluster_rank() : 0;
-  constexpr int kSide = kTile * CTAS;
-  constexpr uint32_t kCols = 2 * kSide;
-  if (threadIdx.x == 0) {
-    for (int s = 0; s < kStages; ++s) {
-      mbar_init(full + s, 1);
-      mbar_init(empty + s, 1);
-    }
-    for (int b = 0; b < 2; ++b) {
-      mbar_init(t_full + b, 1);
-      mbar_init(t_empty + b, kEpiWarps * CTAS);
-    }
-    for (int i = 0; i < 2 * kGroups; ++i) mbar_init(e_full + i, 1);
-    mbar_init(drain, 1);
-    ab->flag = 0;
-    ab->limit_ns = g.wait_ns;
-    fence_mbar_init();
-  }
-  if (warp == kMmaWarp) {
-    if (CTAS == 2) {
-      tmem_alloc_pair(tmem_slot, kCols);
-      tmem_relinquish_pair();
-    } else {
-      tmem_alloc(tmem_slot, kCols);
-      tmem_relinquish();
-    }
-  }
-  tc_fence_before();
-  __syncthreads();
-  if (CTAS == 2) cluster_sync();  // the other's barriers are there
-  tc_fence_after();
-  after_previous();
-  const uint32_t tmem = *tmem_slot;
-  const int tm = (g.rows + kSide - 1) / kSide, tn = (g.cols + kSide - 1) / kSide;
-  const int per = g.sym ? tm * (tm + 1) / 2 : tm * tn;
-  const int tiles = g.count * per;
-  const int blocks = (g.depth + kDepth - 1) / kDepth;
-  const int first = blockIdx.x / CTAS, step = gridDim.x / CTAS;
-
-  if (warp == kProducerWarp) {
-    if (lane == 0) {
-      int it = 0;
-      bool ok = true;
-      for (int t = first; ok && t < tiles; t += step) {
-        const TileAt at = tile_at(g, t, kSide);
-        const int row = at.i * kSide + rank * kTile, col = at.j * kSide + rank * kTile;
-        for (int sg = 0; ok && sg < g.nseg; ++sg) {
-          const CUtensorMap* ma = &g.a[g.seg_a[sg]];
-          const CUtensorMap* mb = &g.b[g.seg_b[sg]];
-          for (int k = 0; k < blocks; ++k, ++it) {
-            const int s = it % kStages;
-            if (it >= kStages && !wait_bar(empty + s, ((it / kStages) - 1) & 1, ab, g.status)) {
-              ok = false;
-              break;
-            }
-            if (ab->flag) {
-              ok = false;
-              break;
-            }
-            uint8_t *pa = smem + s * kStageBytes, *pb = pa + kTileBytes;
-            if (rank == 0) mbar_arrive_expect_tx(full + s, CTAS * kStageBytes);
-            if (CTAS == 2) {
-              const uint32_t bar = cluster_addr(full + s, 0);
-              tma_load_3d_pair(pa, ma, bar, k * kDepth, row, at.l);
-              if (NN) {
-                tma_load_3d_pair(pb, mb, bar, col, k * kDepth, at.l);
-                tma_load_3d_pair(pb + kTileBytes / 2, mb, bar, col + 64, k * kDepth, at.l);
-              } else {
-                tma_load_3d_pair(pb, mb, bar, k * kDepth, col, at.l);
-              }
-            } else {
-              tma_load_3d(pa, ma, full + s, k * kDepth, row, at.l);
-              if (NN) {
-                tma_load_3d(pb, mb, full + s, col, k * kDepth, at.l);
-                tma_load_3d(pb + kTileBytes / 2, mb, full + s, col + 64, k * kDepth, at.l);
-              } else {
-                tma_load_3d(pb, mb, full + s, k * kDepth, col, at.l);
-              }
-            }
-          }
-        }
-      }
-      // every load issued has landed before the block exits: CTA 0 sees the barriers
-      // that count both CTAs' loads; what an abort leaves uncounted gets a fixed time
-      if (rank == 0)
-        for (int u = max(0, it - kStages); u < it; ++u)
-          mbar_wait_bounded(full + u % kStages, (u / kStages) & 1, g.status, 100000000ull);
-      if (CTAS == 2 && ab->flag) {
-        const uint64_t t0 = global_ns();
-        while (global_ns() - t0 < 10000000ull) __nanosleep(10000);
-      }
-    }
-  } else if (warp == kMmaWarp) {
-    if (rank == 0) {
-      constexpr uint32_t id = idesc_f16(kSide, kSide, NN);
-      int it = 0, n = 0;
-      bool ok = true;
-      for (int t = first; ok && t < tiles; t += step, ++n) {
-        const uint32_t d = tmem + (n & 1) * kSide;
-        if (n >= 2 && !warp_wait(t_empty + (n & 1), ((n >> 1) - 1) & 1, ab, g.status)) break;
-        tc_fence_after();
-        const int total = g.nseg * blocks;
-        for (int k = 0; k < total; ++k, ++it) {
-          const int s = it % kStages;
-          if (!warp_wait(full + s, (it / kStages) & 1, ab, g.status)) {
-            ok = false;
-            break;
-          }
-          tc_fence_after();
-          const uint32_t a_lo = opaque(lo_kmajor(sb + s * kStageBytes));
-          const uint32_t b_at = sb + s * kStageBytes + kTileBytes;
-          const uint32_t b_lo = opaque(NN ? lo_mnmajor(b_at, kTileBytes / 2) : lo_kmajor(b_at));
-#pragma unroll
-          for (int u = 0; u < kDepth / 16; ++u) {
-            const uint32_t al = a_lo + 2 * u, bl = b_lo + (NN ? kstep_off(u) : 2 * u);
-            if (CTAS == 2) mma_ss_pair_w(d, al, bl, id, k + u > 0 ? 1u : 0u);
-            else mma_ss_w(d, al, bl, id, k + u > 0 ? 1u : 0u);
-          }
-          if (CTAS == 2) mma_commit_pair_w(empty + s, 3);
-          else mma_commit_w(empty + s);
-        }
-        if (!ok) break;
-        if (CTAS == 2) mma_commit_pair_w(t_full + (n & 1), 3);
-        else mma_commit_w(t_full + (n & 1));
-      }
-      // every MMA this warp issued has completed before TMEM is released
-      if (CTAS == 2) mma_commit_pair_w(drain, 1);
-      else mma_commit_w(drain);
-      mbar_wait_bounded(drain, 0, g.status, 100000000ull);
-    }
-  } else {
-    const Epilogue& e = g.ep;
-    const uint32_t lane_off = (uint32_t)(32 * (warp & 3)) << 16;
-    const int group = warp >> 2, r = 32 * (warp & 3) + lane;
-    const bool issuer = (threadIdx.x & 127) == 0;
-    uint8_t* const slots = smem + kOffSlots + group * 2 * kTileBytes;
-    uint64_t* const e_bar = e_full + 2 * group;
-    constexpr int kChunks = kSide / 64 / kGroups;  // of a tile, for each group
-    const bool two = g.sym || e.e_terms == 2 || e.o_terms == 2 || (e.y_mapped && !e.y_bf16);
-    const int nslots = two ? 1 : 2;
-    const int mine = first < tiles ? ((tiles - 1 - first) / step + 1) * kChunks : 0;
-    // the slot of chunk u is free once the result before it has left; then what is
-    // added comes in
-    auto prepare = [&](int u) {
-      const int s = u % nslots;
-      if (e.e_terms) {
-        const TileAt at = tile_at(g, first + u / kChunks * step, kSide);
-        const int row = at.i * kSide + rank * kTile;
-        const int col = at.j * kSide + (group + u % kChunks * kGroups) * 64;
-        mbar_arrive_expect_tx(e_bar + s, e.e_terms * kTileBytes);
-        tma_load_3d(slots + s * kTileBytes, &g.e[0], e_bar + s, col, row, at.l);
-        if (e.e_terms == 2) tma_load_3d(slots + kTileBytes, &g.e[1], e_bar + s, col, row, at.l);
-      } else {
-        mbar_arrive(e_bar + s);
-      }
-    };
-    int ahead = 0;  // chunks prepared
-    if (issuer)
-      for (; ahead < nslots && ahead < mine; ++ahead) prepare(ahead);
-    int n = 0, u = 0, scaled = -1, shift = 0;
-    bool ok = true;
-    // after an abort the loops run to their end without waiting, so that a group's warps
-    // keep meeting at its barrier
-    for (int t = first; t < tiles; t += step, ++n) {
-      const TileAt at = tile_at(g, t, kSide);
-      float alpha = e.alpha, beta = e.beta;
-      if (e.fpow) {
-        const float f = e.info[at.l].f, ff = e.fpow == 2 ? f * f : f;
-        alpha *= ff;
-        beta *= ff;
-      }
-      if (e.scale_sums) {
-        if (scaled != at.l) {
-          const float* p = e.scale_sums + (size_t)at.l * e.scale_parts;
-          float nu2 = 0.f;
-          for (int i = lane; i < e.scale_parts; i += 32) nu2 += p[i];
-          shift = rescaling(warp_sum(nu2), e.target);
-          scaled = at.l;
-        }
-        alpha = ldexpf(alpha, shift);
-        beta = ldexpf(beta, shift);
-        if (at.index == 0 && threadIdx.x == 0 && rank == 0) e.exp_out[at.l] = e.exp_in[at.l] + shift;
-      }
-      ok = ok && warp_wait(t_full + (n & 1), (n >> 1) & 1, ab, g.status);
-      tc_fence_after();
-      float sum = 0.f;
-      const int row0 = at.i * kSide + rank * kTile, row = row0 + r;
-#pragma unroll 1
-      for (int c = 0; c < kChunks; ++c, ++u) {
-        const int in_tile = (group + c * kGroups) * 64, col0 = at.j * kSide + in_tile;
-        const int s = u % nslots;
-        uint8_t* const slot = slots + s * kTileBytes;
-        ok = ok && warp_wait(e_bar + s, (u / nslots) & 1, ab, g.status);
-        const bool mirror = g.sym && at.i != at.j;
-#pragma unroll 1
-        for (int h = 0; h < 2; ++h) {
-          const int col = col0 + 32 * h;
-          uint32_t acc[32];
-          tmem_ld32(tmem + lane_off + (n & 1) * kSide + in_tile + 32 * h, acc);
-          f2 v[16];
-#pragma unroll
-          for (int k = 0; k < 16; ++k)
-            v[k] = mul2(f2{alpha, alpha}, f2{__uint_as_float(acc[2 * k]), __uint_as_float(acc[2 * k + 1])});
-          if (e.e_terms) add_slot(v, slot, r, h, beta);
-          if (e.e_terms == 2) add_slot(v, slot + kTileBytes, r, h, beta);
-          if (e.sums) {  // (what lies outside is zero)
-#pragma unroll
-            for (int k = 0; k < 16; ++k) sum = fmaf(v[k].x, v[k].x, fmaf(v[k].y, v[k].y, sum));
-          }
-          uint32_t w[16];
-          if (e.o_terms) {
-#pragma unroll
-            for (int k = 0; k < 16; ++k) w[k] = to_halves(v[k]);
-            put_slot(w, slot, r, h);
-            if (e.o_terms == 2) {
-              uint32_t lo[16];
-#pragma unroll
-              for (int k = 0; k < 16; ++k) lo[k] = to_halves(fma2(f2{-1.f, -1.f}, halves(w[k]), v[k]));
-              put_slot(lo, slot + kTileBytes, r, h);
-              if (mirror)
-                put_mirrored(w, lo, e, (size_t)at.l * g.rows * e.old, row, col, g.rows, g.cols);
-            } else if (mirror) {
-              put_slot_transposed(w, slot + kTileBytes, r, h);
-            }
-          } else if (!e.y_mapped) {
-            put_caller(v, g, at.l, row, col);
-          } else if (e.y_bf16) {
-#pragma unroll
-            for (int k = 0; k < 16; ++k) w[k] = pack_bf16(v[k].x, v[k].y);
-            put_slot(w, slot, r, h);
-          } else if (h == 0) {  // 32 fp32 columns fill a slot row: kept in both until all is read
-#pragma unroll
-            for (int k = 0; k < 8; ++k)
-              *reinterpret_cast<float4*>(slot_chunk(slot + (k >> 2) * kTileBytes, r, k & 3)) =
-                  make_float4(v[2 * k].x, v[2 * k].y, v[2 * k + 1].x, v[2 * k + 1].y);
-          } else {
-            float4 f[4];
-#pragma unroll
-            for (int k = 0; k < 4; ++k)
-              f[k] = *reinterpret_cast<float4*>(slot_chunk(slot + kTileBytes, r, k));
-            put_floats(v, slot + kTileBytes, r);
-#pragma unroll
-            for (int k = 0; k < 4; ++k) *reinterpret_cast<float4*>(slot_chunk(slot, r, 4 + k)) = f[k];
-          }
-        }
-        if (c == kChunks - 1) {
-          tc_fence_before();
-          __syncwarp();
-          if (lane == 0) {
-            if (CTAS == 2) mbar_arrive_cluster(cluster_addr(t_empty + (n & 1), 0));
-            else mbar_arrive(t_empty + (n & 1));
-          }
-        }
-        fence_async_smem();
-        named_sync<128>(1 + group);
-        if (issuer) {
-          if ((e.o_terms || e.y_mapped) && row0 < g.rows && col0 < g.cols && !ab->flag) {
-            tma_store_3d(&g.o[0], slot, col0, row0, at.l);
-            if (e.o_terms == 2) {
-              tma_store_3d(&g.o[1], slot + kTileBytes, col0, row0, at.l);
-            } else if (mirror) {
-              tma_store_3d(&g.o[1], slot + kTileBytes, row0, col0, at.l);
-              if (row0 + 64 < g.rows)
-                tma_store_3d(&g.o[1], slot + kTileBytes + kTileBytes / 2, row0 + 64, col0, at.l);
-            }
-            if (!e.o_terms && !e.y_bf16 && col0 + 32 < g.cols)
-              tma_store_3d(&g.o[0], slot + kTileBytes, col0 + 32, row0, at.l);
-            bulk_commit_group();
-            bulk_wait_read_all();
-          }
-          if (ahead < mine && !ab->flag) prepare(ahead++);
-        }
-      }
-      if (e.sums) {
-        sum = warp_sum(sum);
-        if (lane == 0)
-          e.sums[((size_t)at.l * per + at.index) * (CTAS * kEpiWarps) + rank * kEpiWarps + warp] = sum;
-      }
-    }
-    if (issuer) {
-      bulk_wait_all();
-      // what was loaded ahead has landed (after an abort some was never awaited)
-      for (int k = max(0, ahead - nslots); k < ahead; ++k)
-        mbar_wait_bounded(e_bar + k % nslots, (k / nslots) & 1, g.status, 100000000ull);
-    }
-  }
-  tc_fence_before();
-  __syncthreads();
-  __syncwarp();
-  if (CTAS == 2) cluster_sync();  // neither leaves before the other's last use of it
-  if (warp == kMmaWarp) {
-    tc_fence_after();
-    if (CTAS == 2) tmem_dealloc_pair(tmem, kCols);
-    else tmem_dealloc(tmem, kCols);
-  }
 }
 
 // ---------------------------------------------------------------------------
@@ -582,13 +61,17 @@ __global__ void __launch_bounds__(kThreads, 1) product(const __grid_constant__ P
 constexpr int kSumThreads = 256;
 
 // partial[l][block] = sum of squares of a slice of matrix l; also clears the call's
-// status word, before every kernel that may write it.
+// status word and the chain's counters, before the kernels that write them.
 template <typename T>
 __global__ void __launch_bounds__(kSumThreads)
-    square_sums(const T* __restrict__ x, float* __restrict__ partial, size_t elems, int* status) {
+    square_sums(const T* __restrict__ x, float* __restrict__ partial, size_t elems, int* status,
+                int* counters, size_t n_counters) {
   __shared__ float sm[kSumThreads / 32];
   let_next_start();
   if (blockIdx.x == 0 && blockIdx.y == 0 && threadIdx.x == 0) *status = 0;
+  for (size_t i = ((size_t)blockIdx.y * gridDim.x + blockIdx.x) * kSumThreads + threadIdx.x; i < n_counters;
+       i += (size_t)gridDim.x * gridDim.y * kSumThreads)
+    counters[i] = 0;
   x += (size_t)blockIdx.y * elems;
   const size_t per = (elems + gridDim.x - 1) / gridDim.x;
   const size_t first = blockIdx.x * per, last = min(elems, first + per);
@@ -799,17 +282,20 @@ __global__ void __launch_bounds__(kSumThreads) end_gradient(EndArgs a) {
 // ---------------------------------------------------------------------------
 // Host: scales, workspace, launches
 // ---------------------------------------------------------------------------
-constexpr int kMaxSteps = 16;
-
 struct Plan {
-  int L, m, n, p, q, ldq, ldp, steps, bf16, keep, tall;
+  int L, m, n, p, q, ldq, ldp, steps, bf16, keep, tall, ctas;
   float eps;
   float a[kMaxSteps], b[kMaxSteps], c[kMaxSteps];
   int xe[kMaxSteps], ae[kMaxSteps], be[kMaxSteps];  // exponents of X, A, B as stored
   int xt[kMaxSteps];                                // terms of X
-  double M[kMaxSteps + 1];                          // bound on X's singular values
+  double M[kMaxSteps];                              // bound on X's singular values
   int square_parts;
 };
+
+// CTAs that share a tile.
+int choose_ctas(const Plan& p) {
+  return getenv("ORTH_CTAS") ? atoi(getenv("ORTH_CTAS")) : 2;
+}
 
 int floor_log2(double x) { return (int)floor(log2(x)); }
 int store_exp(double bound) {  // entries up to 2^15
@@ -838,11 +324,11 @@ int make_plan(const fbob_orth_t* o, Plan* out) {
   p.keep = o->keep;
   p.eps = o->eps;
   double M = 1.0;
-  p.M[0] = M;
   for (int i = 0; i < p.steps; ++i) {
     const double a = o->coefficients[3 * i], b = o->coefficients[3 * i + 1], c = o->coefficients[3 * i + 2];
     if (!(fabs(a) < 1e6 && fabs(b) < 1e6 && fabs(c) < 1e6)) return FBOB_ERR_INVALID_ARG;
     p.a[i] = (float)a; p.b[i] = (float)b; p.c[i] = (float)c;
+    p.M[i] = M;
     p.xe[i] = store_exp(M);
     p.ae[i] = store_exp(M * M);
     p.be[i] = store_exp(fabs(b) * M * M + fabs(c) * M * M * M * M);
@@ -853,7 +339,6 @@ int make_plan(const fbob_orth_t* o, Plan* out) {
     }
     M = 1.01 * most;
     if (!(M < 64.0)) return FBOB_ERR_INVALID_ARG;  // singular values that run away
-    p.M[i + 1] = M;
   }
   // terms of X: the growth of a rounding error by the steps that follow
   double growth = 1;
@@ -865,16 +350,20 @@ int make_plan(const fbob_orth_t* o, Plan* out) {
   const long long elems = (long long)p.p * p.q;
   const long long parts = (elems + 8191) / 8192;
   p.square_parts = (int)(parts < 1024 ? parts : 1024);
+  p.ctas = choose_ctas(p);
+  // items of a chain are counted in 32 bits
+  const double tiles = 2.0 * tiles_of(p.p, p.p, true, p.ctas) + (double)tiles_of(p.p, p.q, false, p.ctas);
+  if (tiles * p.L * p.steps > (double)(1 << 30)) return FBOB_ERR_UNSUPPORTED;
   *out = p;
   return FBOB_OK;
 }
 
 // A map of [count][rows][ld] elements, cols of each row; a box: 128 bytes of box_rows rows.
-bool make_tile_map(CUtensorMap* m, CUtensorMapDataType type, int size, const void* ptr, int L, int rows,
-                   int cols, long long ld, int box_rows) {
+bool make_map(CUtensorMap* m, CUtensorMapDataType type, int size, const void* ptr, long long count, int rows,
+              int cols, long long ld, int box_rows) {
   auto fn = encode_fn();
   if (!fn) return false;
-  cuuint64_t dims[3] = {(cuuint64_t)cols, (cuuint64_t)rows, (cuuint64_t)L};
+  cuuint64_t dims[3] = {(cuuint64_t)cols, (cuuint64_t)rows, (cuuint64_t)count};
   cuuint64_t strides[2] = {(cuuint64_t)ld * size, (cuuint64_t)rows * ld * size};
   cuuint32_t box[3] = {(cuuint32_t)(128 / size), (cuuint32_t)box_rows, 1};
   cuuint32_t es[3] = {1, 1, 1};
@@ -883,211 +372,214 @@ bool make_tile_map(CUtensorMap* m, CUtensorMapDataType type, int size, const voi
             CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
+// Slots of L matrices of p rows each, in one fp16 term, the first low_slots in two.
+struct Mats {
+  __half *hi, *lo;
+  int slots, low_slots, cols, ld;
+  size_t slot;              // elements
+  unsigned char tile[2];    // maps in boxes of 128 rows: left operands, right ones of P Q^T, what
+  unsigned char step[2];    // is added, results; and of 64 rows: right operands of P Q, mirrors
+};
+
 struct Carver {
   char* base;
   size_t off;
-  bool ok;
   void* take(size_t bytes) {
     void* r = base ? base + off : nullptr;
     off += align_up(bytes);
     return r;
   }
-  Terms terms(const Plan& p, int cols, int ld, int n) {
-    Terms t;
-    const size_t one = (size_t)p.L * p.p * ld * sizeof(__half);
-    t.hi = static_cast<__half*>(take(one));
-    t.lo = n == 2 ? static_cast<__half*>(take(one)) : nullptr;
-    t.rows = p.p; t.cols = cols; t.ld = ld;
-    for (int i = 0; base && i < n; ++i) {
-      const __half* at = i ? t.lo : t.hi;
-      const auto half = CU_TENSOR_MAP_DATA_TYPE_FLOAT16;
-      ok = ok && make_tile_map(&t.tile[i], half, 2, at, p.L, p.p, cols, ld, kTile);
-      ok = ok && make_tile_map(&t.step[i], half, 2, at, p.L, p.p, cols, ld, kDepth);
-    }
+  Mats mats(const Plan& p, int cols, int ld, int slots, int low_slots) {
+    Mats t = {};
+    t.slot = (size_t)p.L * p.p * ld;
+    t.hi = static_cast<__half*>(take(slots * t.slot * sizeof(__half)));
+    t.lo = low_slots ? static_cast<__half*>(take(low_slots * t.slot * sizeof(__half))) : nullptr;
+    t.slots = slots;
+    t.low_slots = low_slots;
+    t.cols = cols;
+    t.ld = ld;
     return t;
   }
 };
 
-// CTAs that share a tile of a rows x cols product.
-int product_ctas(const Plan& p, int rows, int cols, bool sym) {
-  return getenv("ORTH_CTAS") ? atoi(getenv("ORTH_CTAS")) : 2;
-}
-int product_tiles(int rows, int cols, bool sym, int ctas) {  // of one matrix
-  const int side = kTile * ctas, tm = (rows + side - 1) / side, tn = (cols + side - 1) / side;
-  return sym ? tm * (tm + 1) / 2 : tm * tn;
-}
-int product_parts(const Plan& p) {  // sums of a [p, q] product
-  const int ctas = product_ctas(p, p.p, p.q, false);
-  return product_tiles(p.p, p.q, false, ctas) * ctas * kEpiWarps;
-}
+size_t counters(const Plan& p) { return 1 + (size_t)3 * p.steps * p.L; }  // ticket, done
 
-// Forward: [status][info][square sums], then X, A and B of each step (kept), or of two
-// and one (X in turn).
+// Forward: [status][counters][info][square sums], then X, A and B of every step (keep), or
+// of two and one.
 struct Forward {
-  int* status;
+  int *status, *counters;
   MatInfo* info;
   float* sums;
-  Terms X[kMaxSteps], A[kMaxSteps], B[kMaxSteps];
-  bool ok;
+  Mats X, A, B;
   size_t bytes;
+  int keep;
+  int x(int i) const { return keep ? i : i & 1; }
+  int a(int i) const { return keep ? i : 0; }
 };
 Forward carve_forward(const Plan& p, char* base) {
   Forward w;
-  Carver c{base, 0, true};
+  Carver c{base, 0};
+  w.keep = p.keep;
   w.status = static_cast<int*>(c.take(sizeof(int)));
+  w.counters = static_cast<int*>(c.take(sizeof(int) * counters(p)));
   w.info = static_cast<MatInfo*>(c.take(sizeof(MatInfo) * p.L));
   w.sums = static_cast<float*>(c.take(sizeof(float) * p.L * p.square_parts));
-  const int small = p.bf16 ? 1 : 2;
-  Terms turn[2];  // without keep: room for every step that shares one
-  for (int i = 0; !p.keep && i < 2; ++i) {
-    int t = 1;
-    for (int k = i; k < p.steps; k += 2) t = p.xt[k] > t ? p.xt[k] : t;
-    turn[i] = c.terms(p, p.q, p.ldq, t);
-  }
-  for (int i = 0; i < p.steps; ++i) {
-    w.X[i] = p.keep ? c.terms(p, p.q, p.ldq, p.xt[i]) : turn[i & 1];
-    if (p.xt[i] == 1) w.X[i].lo = nullptr;
-    if (p.keep || i == 0) {
-      w.A[i] = c.terms(p, p.p, p.ldp, small);
-      w.B[i] = c.terms(p, p.p, p.ldp, small);
-    } else {
-      w.A[i] = w.A[0];
-      w.B[i] = w.B[0];
-    }
-  }
-  w.ok = c.ok;
+  const int xs = p.keep ? p.steps : p.steps > 1 ? 2 : 1, as = p.keep ? p.steps : 1;
+  int low = 0;
+  for (int i = 0; i < p.steps; ++i)
+    if (p.xt[i] == 2 && w.x(i) >= low) low = w.x(i) + 1;
+  w.X = c.mats(p, p.q, p.ldq, xs, low);
+  w.A = c.mats(p, p.p, p.ldp, as, p.bf16 ? 0 : as);
+  w.B = c.mats(p, p.p, p.ldp, as, p.bf16 ? 0 : as);
   w.bytes = c.off;
   return w;
 }
 
-// Backward: [status][square sums of dY][exponents: steps + 1][sums of the steps'
-// results: two in turn], H in turn, S, T.
+// Backward: [status][counters][square sums of dY][the same of H as packed][exponents:
+// steps + 1][sums of the steps' results: two in turn], H in turn, S, T.
 struct Backward {
-  int* status;
+  int *status, *counters;
   float *sums, *first, *step_sums[2];
   int* exp[kMaxSteps + 1];
-  Terms H[2], S, T;
-  bool ok;
+  Mats H, S, T;
   size_t bytes;
 };
+int step_parts(const Plan& p) { return parts_of(tiles_of(p.p, p.q, false, p.ctas), p.ctas); }
 Backward carve_backward(const Plan& p, char* base) {
   Backward w;
-  Carver c{base, 0, true};
-  const int t = p.bf16 ? 1 : 2;
+  Carver c{base, 0};
+  const int two = p.bf16 ? 0 : 1;
   w.status = static_cast<int*>(c.take(sizeof(int)));
+  w.counters = static_cast<int*>(c.take(sizeof(int) * counters(p)));
   w.sums = static_cast<float*>(c.take(sizeof(float) * p.L * p.square_parts));
   w.first = static_cast<float*>(c.take(sizeof(float) * p.L));
-  for (float*& s : w.step_sums) s = static_cast<float*>(c.take(sizeof(float) * p.L * product_parts(p)));
+  for (float*& s : w.step_sums) s = static_cast<float*>(c.take(sizeof(float) * p.L * step_parts(p)));
   for (int i = 0; i <= p.steps; ++i) w.exp[i] = static_cast<int*>(c.take(sizeof(int) * p.L));
-  for (Terms& h : w.H) h = c.terms(p, p.q, p.ldq, t);
-  w.S = c.terms(p, p.p, p.ldp, t);
-  w.T = c.terms(p, p.p, p.ldp, t);
-  w.ok = c.ok;
+  w.H = c.mats(p, p.q, p.ldq, 2, 2 * two);
+  w.S = c.mats(p, p.p, p.ldp, 1, two);
+  w.T = c.mats(p, p.p, p.ldp, 1, two);
   w.bytes = c.off;
   return w;
 }
 
-// Launches a kernel that may start while the one before it in the stream ends.
-template <typename... P, typename... A>
-cudaError_t launch_next(void (*kernel)(P...), dim3 grid, int threads, size_t smem, int cluster,
-                        LaunchLog& log, A... args) {
-  cudaLaunchConfig_t c = {};
-  c.gridDim = grid;
-  c.blockDim = dim3((unsigned)threads);
-  c.dynamicSmemBytes = smem;
-  c.stream = log.stream;
-  cudaLaunchAttribute attr[2];
-  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
-  attr[0].val.programmaticStreamSerializationAllowed = 1;
-  attr[1].id = cudaLaunchAttributeClusterDimension;
-  attr[1].val.clusterDim.x = (unsigned)cluster;
-  attr[1].val.clusterDim.y = attr[1].val.clusterDim.z = 1;
-  c.attrs = attr;
-  c.numAttrs = cluster > 1 ? 2 : 1;
-  const cudaError_t e = cudaLaunchKernelEx(&c, kernel, args...);
-  log.mark();
-  return e;
-}
+// A matrix (L of them) as a product takes it: a family's slot, in one or two terms.
+struct Ref {
+  const Mats* m;
+  int slot, terms;
+};
 
-// Builds and launches one product.
-struct Product {
-  ProductArgs g;
-  int na = 0, nb = 0, high_a[2], high_b[2], highs = 0, ctas;
-  bool nn;
-  Product(const Plan& p, const Terms& out, int depth, bool nn_, bool sym, int* status) : nn(nn_) {
-    memset(&g, 0, sizeof g);
-    ctas = product_ctas(p, out.rows, out.cols, sym);
-    g.rows = out.rows;
-    g.cols = out.cols;
-    g.depth = depth;
+// Builds a chain, phase by phase.
+struct Chain {
+  ChainArgs g;
+  const Plan& p;
+  int maps = 0, items = 0;
+  bool ok = true;
+  int highs = 0;
+  Ref high_p[2], high_q[2];
+  Chain(const Plan& plan, int* status, int* counts, const MatInfo* info) : p(plan) {
+    g.phases = 0;
+    g.rows = p.p;
+    g.cols = p.q;
     g.count = p.L;
-    g.sym = sym;
+    g.info = info;
+    g.y = nullptr;
+    g.y_bf16 = p.bf16;
+    g.y_transposed = p.tall;
+    g.y_mapped = 0;
     g.status = status;
+    g.ticket = counts;
+    g.done = counts + 1;
     g.wait_ns = wait_limit_ns();
   }
+  void use(Mats& m) {
+    for (int t = 0; t < 2; ++t) {
+      const int slots = t ? m.low_slots : m.slots;
+      if (!slots) continue;
+      const __half* at = t ? m.lo : m.hi;
+      const auto half = CU_TENSOR_MAP_DATA_TYPE_FLOAT16;
+      m.tile[t] = (unsigned char)maps;
+      ok = ok && make_map(&g.maps[maps++], half, 2, at, (long long)slots * p.L, p.p, m.cols, m.ld, kTile);
+      m.step[t] = (unsigned char)maps;
+      ok = ok && make_map(&g.maps[maps++], half, 2, at, (long long)slots * p.L, p.p, m.cols, m.ld, kDepth);
+    }
+  }
+  Phase& phase() { return g.phase[g.phases]; }
+  void begin(int cols, int depth, bool nn, bool sym) {
+    Phase& f = phase();
+    memset(&f, 0, sizeof f);
+    f.cols = cols;
+    f.depth = depth;
+    f.nn = nn;
+    f.sym = sym;
+    f.first = items;
+    f.tiles = tiles_of(p.p, cols, sym, p.ctas);
+    highs = 0;
+  }
+  void pair(const Ref& P, int tp, const Ref& Q, int tq) {
+    Phase& f = phase();
+    f.seg_a[f.nseg] = P.m->tile[tp];
+    f.at_a[f.nseg] = P.slot * p.L;
+    f.seg_b[f.nseg] = f.nn ? Q.m->step[tq] : Q.m->tile[tq];
+    f.at_b[f.nseg++] = Q.slot * p.L;
+  }
   // acc += P Q^T (or P Q): every pair of terms but the two low ones
-  void add(const Terms& P, const Terms& Q) {
-    const int a0 = na, b0 = nb;
-    g.a[na++] = P.tile[0];
-    if (P.lo) g.a[na++] = P.tile[1];
-    g.b[nb++] = nn ? Q.step[0] : Q.tile[0];
-    if (Q.lo) g.b[nb++] = nn ? Q.step[1] : Q.tile[1];
-    if (Q.lo) pair(a0, b0 + 1);
-    if (P.lo) pair(a0 + 1, b0);
-    high_a[highs] = a0;
-    high_b[highs++] = b0;
+  void add(const Ref& P, const Ref& Q) {
+    if (Q.terms == 2) pair(P, 0, Q, 1);
+    if (P.terms == 2) pair(P, 1, Q, 0);
+    high_p[highs] = P;
+    high_q[highs++] = Q;
   }
-  void pair(int a, int b) {
-    g.seg_a[g.nseg] = (unsigned char)a;
-    g.seg_b[g.nseg++] = (unsigned char)b;
+  void plus(const Ref& E) {
+    Phase& f = phase();
+    f.e_terms = E.terms;
+    f.e_map[0] = E.m->tile[0];
+    f.e_map[1] = E.m->tile[1];
+    f.e_at = E.slot * p.L;
   }
-  void plus(const Terms& E) {
-    g.ep.e_terms = E.lo ? 2 : 1;
-    g.e[0] = E.tile[0];
-    g.e[1] = E.tile[1];
+  void to(const Ref& O) {
+    Phase& f = phase();
+    f.o_terms = O.terms;
+    f.o_map[0] = O.m->tile[0];
+    f.o_map[1] = O.terms == 2 ? O.m->tile[1] : O.m->step[0];
+    f.o_at = O.slot * p.L;
+    f.mirror[0] = O.m->hi;
+    f.mirror[1] = O.m->lo;
+    f.ld = O.m->ld;
   }
-  void to(const Terms& O) {
-    g.ep.o_terms = O.lo ? 2 : 1;
-    g.o[0] = O.tile[0];
-    g.o[1] = O.lo ? O.tile[1] : O.step[0];  // one term: mirrored in boxes of 64 rows
-    g.ep.o[0] = O.hi;
-    g.ep.o[1] = O.lo;
-    g.ep.old = O.ld;
-  }
-  // the caller's tensor, by rows (its map where one can be made) or transposed
-  void to_caller(const Plan& p, void* y) {
+  // the caller's tensor, by rows (through a map where one can be made) or transposed
+  void to_caller(void* y) {
     const int size = p.bf16 ? 2 : 4;
-    g.ep.y = y;
-    g.ep.y_bf16 = p.bf16;
-    g.ep.y_transposed = p.tall;
-    g.ep.y_mapped = !p.tall && (reinterpret_cast<uintptr_t>(y) & 15u) == 0 && p.q * size % 16 == 0 &&
-                    make_tile_map(&g.o[0], p.bf16 ? CU_TENSOR_MAP_DATA_TYPE_BFLOAT16
-                                                  : CU_TENSOR_MAP_DATA_TYPE_FLOAT32,
-                                  size, y, p.L, p.p, p.q, p.q, kTile);
+    g.y = y;
+    g.y_mapped = !p.tall && (reinterpret_cast<uintptr_t>(y) & 15u) == 0 && (long long)p.q * size % 16 == 0 &&
+                 make_map(&g.maps[maps], p.bf16 ? CU_TENSOR_MAP_DATA_TYPE_BFLOAT16
+                                                : CU_TENSOR_MAP_DATA_TYPE_FLOAT32,
+                          size, y, p.L, p.p, p.q, p.q, kTile);
+    phase().o_map[0] = (unsigned char)maps++;
   }
-  cudaError_t launch(LaunchLog& log) {
+  void end() {
     // The products of high terms come last: the tensor cores cut every addition off to the
     // accumulator's 24 bits, which costs nothing while it holds the small ones only.
-    for (int i = 0; i < highs; ++i) pair(high_a[i], high_b[i]);
-    const long long tiles = (long long)g.count * product_tiles(g.rows, g.cols, g.sym, ctas);
-    const long long most = kSms / ctas;
-    const int grid = (int)(tiles < most ? tiles : most) * ctas;
-    auto kernel = ctas == 2 ? (nn ? product<2, true> : product<2, false>)
-                            : (nn ? product<1, true> : product<1, false>);
-    cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmem);
-    if (e != cudaSuccess) return e;
-    return launch_next(kernel, dim3((unsigned)grid), kThreads, kSmem, ctas, log, g);
+    for (int i = 0; i < highs; ++i) pair(high_p[i], 0, high_q[i], 0);
+    items += p.L * phase().tiles;
+    ++g.phases;
+  }
+  cudaError_t launch(LaunchLog& log) {
+    if (!ok) return cudaErrorUnknown;
+    g.items = items;
+    return launch_chain(g, p.ctas, log);
   }
 };
 
-cudaError_t squares_and_pack(const Plan& p, const void* x, float* sums, int* status, PackArgs a,
-                             LaunchLog& log) {
+cudaError_t squares_and_pack(const Plan& p, const void* x, float* sums, int* status, int* counts,
+                             PackArgs a, LaunchLog& log) {
   const size_t elems = (size_t)p.p * p.q;
   const dim3 grid((unsigned)p.square_parts, (unsigned)p.L);
   if (p.bf16)
-    square_sums<<<grid, kSumThreads, 0, log.stream>>>(static_cast<const __nv_bfloat16*>(x), sums, elems, status);
+    square_sums<<<grid, kSumThreads, 0, log.stream>>>(static_cast<const __nv_bfloat16*>(x), sums, elems, status,
+                                                      counts, counters(p));
   else
-    square_sums<<<grid, kSumThreads, 0, log.stream>>>(static_cast<const float*>(x), sums, elems, status);
+    square_sums<<<grid, kSumThreads, 0, log.stream>>>(static_cast<const float*>(x), sums, elems, status, counts,
+                                                      counters(p));
   cudaError_t e = cudaGetLastError();
   log.mark();
   if (e != cudaSuccess) return e;
@@ -1102,62 +594,52 @@ cudaError_t squares_and_pack(const Plan& p, const void* x, float* sums, int* sta
 
 float pow2(int e) { return ldexpf(1.f, e); }
 
-cudaError_t forward(const Plan& p, const void* G, void* Y, const Forward& w, LaunchLog& log) {
+cudaError_t forward(const Plan& p, const void* G, void* Y, Forward& w, LaunchLog& log) {
+  Chain c(p, w.status, w.counters, w.info);
+  c.use(w.X);
+  c.use(w.A);
+  c.use(w.B);
+  const int terms = p.bf16 ? 1 : 2;
+  for (int i = 0; i < p.steps; ++i) {
+    const Ref X{&w.X, w.x(i), p.xt[i]}, Xm{&w.X, w.x(i), terms};  // as it is added, and multiplied
+    const Ref A{&w.A, w.a(i), terms}, B{&w.B, w.a(i), terms};
+    const bool last = i + 1 == p.steps;
+    c.begin(p.p, p.q, false, true);
+    c.add(Xm, Xm);
+    c.phase().alpha = pow2(p.ae[i] - 2 * p.xe[i]);
+    c.phase().fpow = i == 0 ? 2 : 0;
+    c.to(A);
+    c.end();
+    c.begin(p.p, p.p, false, true);
+    c.add(A, A);
+    c.plus(A);
+    c.phase().alpha = p.c[i] * pow2(p.be[i] - 2 * p.ae[i]);
+    c.phase().beta = p.b[i] * pow2(p.be[i] - p.ae[i]);
+    c.to(B);
+    c.end();
+    c.begin(p.q, p.p, true, false);
+    c.add(B, Xm);
+    c.plus(X);
+    const int out = last ? 0 : p.xe[i + 1];
+    c.phase().alpha = pow2(out - p.be[i] - p.xe[i]);
+    c.phase().beta = p.a[i] * pow2(out - p.xe[i]);
+    c.phase().fpow = i == 0 ? 1 : 0;
+    if (last) c.to_caller(Y);
+    else c.to(Ref{&w.X, w.x(i + 1), p.xt[i + 1]});
+    c.end();
+  }
+  if (!c.ok) return cudaErrorUnknown;
   PackArgs a = {};
-  a.hi = w.X[0].hi;
-  a.lo = w.X[0].lo;
+  a.hi = w.X.hi;
+  a.lo = p.xt[0] == 2 ? w.X.lo : nullptr;
   a.target = p.xe[0];
   a.info = w.info;
-  cudaError_t e = squares_and_pack(p, G, w.sums, w.status, a, log);
-  for (int i = 0; e == cudaSuccess && i < p.steps; ++i) {
-    const Terms &X = w.X[i], &A = w.A[i], &B = w.B[i];
-    Terms Xm = X;  // as it is multiplied
-    if (p.bf16) Xm.lo = nullptr;
-    {
-      Product g(p, A, p.q, false, true, w.status);
-      g.add(Xm, Xm);
-      g.g.ep.alpha = pow2(p.ae[i] - 2 * p.xe[i]);
-      if (i == 0) {
-        g.g.ep.info = w.info;
-        g.g.ep.fpow = 2;
-      }
-      g.to(A);
-      e = g.launch(log);
-    }
-    if (e != cudaSuccess) break;
-    {
-      Product g(p, B, p.p, false, true, w.status);
-      g.add(A, A);
-      g.plus(A);
-      g.g.ep.alpha = p.c[i] * pow2(p.be[i] - 2 * p.ae[i]);
-      g.g.ep.beta = p.b[i] * pow2(p.be[i] - p.ae[i]);
-      g.to(B);
-      e = g.launch(log);
-    }
-    if (e != cudaSuccess) break;
-    const bool last = i + 1 == p.steps;
-    Product g(p, X, p.p, true, false, w.status);
-    g.add(B, Xm);
-    g.plus(X);
-    const int out = last ? 0 : p.xe[i + 1];
-    g.g.ep.alpha = pow2(out - p.be[i] - p.xe[i]);
-    g.g.ep.beta = p.a[i] * pow2(out - p.xe[i]);
-    if (i == 0) {
-      g.g.ep.info = w.info;
-      g.g.ep.fpow = 1;
-    }
-    if (last) {
-      g.to_caller(p, Y);
-    } else {
-      g.to(w.X[i + 1]);
-    }
-    e = g.launch(log);
-  }
-  return e;
+  const cudaError_t e = squares_and_pack(p, G, w.sums, w.status, w.counters, a, log);
+  return e == cudaSuccess ? c.launch(log) : e;
 }
 
-cudaError_t backward(const Plan& p, const void* G, const void* dY, void* dG, const Forward& f,
-                     const Backward& w, LaunchLog& log) {
+cudaError_t backward(const Plan& p, const void* G, const void* dY, void* dG, Forward& f, Backward& w,
+                     LaunchLog& log) {
   // H's norm is brought to 2^target: every entry of H, S, T and of the next H stays below
   // 2^15 whatever their directions
   int target[kMaxSteps], se[kMaxSteps];
@@ -1171,73 +653,65 @@ cudaError_t backward(const Plan& p, const void* G, const void* dY, void* dG, con
     target[i] = (int)floor(most) < 12 ? (int)floor(most) : 12;
     se[i] = store_exp(pow2(target[i]) * 2 * M);
   }
-  const int top = p.steps - 1;
+  const int top = p.steps - 1, terms = p.bf16 ? 1 : 2;
+  Chain c(p, w.status, w.counters, f.info);
+  for (Mats* m : {&f.X, &f.A, &f.B, &w.H, &w.S, &w.T}) c.use(*m);
+  const Ref S{&w.S, 0, terms}, T{&w.T, 0, terms};
+  const float* sums = w.first;
+  int parts = 1, turn = 0;
+  for (int i = top; i >= 0; --i, turn ^= 1) {
+    const Ref H{&w.H, turn, terms}, X{&f.X, i, terms}, A{&f.A, i, terms}, B{&f.B, i, terms};
+    const int by_f = i == 0 ? 1 : 0;  // X_0 is f times what is stored
+    c.begin(p.p, p.q, false, true);
+    c.add(H, X);
+    c.add(X, H);
+    c.phase().alpha = pow2(se[i] - p.xe[i]);
+    c.phase().fpow = by_f;
+    c.to(S);
+    c.end();
+    const int te = p.be[i] - p.xe[i];  // T X and B H share an accumulator
+    c.begin(p.p, p.p, false, true);
+    c.add(A, S);
+    c.add(S, A);
+    c.plus(S);
+    c.phase().alpha = p.c[i] * pow2(te - p.ae[i] - se[i]);
+    c.phase().beta = p.b[i] * pow2(te - se[i]);
+    c.phase().fpow = by_f;
+    c.to(T);
+    c.end();
+    c.begin(p.q, p.p, true, false);
+    c.add(B, H);
+    c.add(T, X);
+    c.plus(H);
+    Phase& h = c.phase();
+    h.alpha = pow2(-p.be[i]);
+    h.beta = p.a[i];
+    h.sums = i > 0 ? w.step_sums[turn] : nullptr;
+    h.scale_sums = sums;
+    h.scale_parts = parts;
+    h.target = i > 0 ? target[i - 1] : 12;
+    h.exp_in = w.exp[i + 1];
+    h.exp_out = w.exp[i];
+    c.to(Ref{&w.H, turn ^ 1, terms});
+    c.end();
+    sums = w.step_sums[turn];
+    parts = step_parts(p);
+  }
+  if (!c.ok) return cudaErrorUnknown;
   PackArgs a = {};
-  a.hi = w.H[0].hi;
-  a.lo = w.H[0].lo;
+  a.hi = w.H.hi;
+  a.lo = w.H.lo;
   a.target = target[top];
   a.exp_out = w.exp[p.steps];
   a.sums_out = w.first;
-  cudaError_t e = squares_and_pack(p, dY, w.sums, w.status, a, log);
-  const float* sums = w.first;
-  int parts = 1, turn = 0;
-  for (int i = top; e == cudaSuccess && i >= 0; --i, turn ^= 1) {
-    const Terms &H = w.H[turn], &A = f.A[i], &B = f.B[i];
-    Terms X = f.X[i];
-    if (p.bf16) X.lo = nullptr;
-    {
-      Product g(p, w.S, p.q, false, true, w.status);
-      g.add(H, X);
-      g.add(X, H);
-      g.g.ep.alpha = pow2(se[i] - p.xe[i]);
-      if (i == 0) {
-        g.g.ep.info = f.info;
-        g.g.ep.fpow = 1;
-      }
-      g.to(w.S);
-      e = g.launch(log);
-    }
-    if (e != cudaSuccess) break;
-    const int te = p.be[i] - p.xe[i];  // T X and B H share an accumulator
-    {
-      Product g(p, w.T, p.p, false, true, w.status);
-      g.add(A, w.S);
-      g.add(w.S, A);
-      g.plus(w.S);
-      g.g.ep.alpha = p.c[i] * pow2(te - p.ae[i] - se[i]);
-      g.g.ep.beta = p.b[i] * pow2(te - se[i]);
-      if (i == 0) {  // X_0 is f times what is stored
-        g.g.ep.info = f.info;
-        g.g.ep.fpow = 1;
-      }
-      g.to(w.T);
-      e = g.launch(log);
-    }
-    if (e != cudaSuccess) break;
-    Product g(p, H, p.p, true, false, w.status);
-    g.add(B, H);
-    g.add(w.T, X);
-    g.plus(H);
-    g.g.ep.alpha = pow2(-p.be[i]);
-    g.g.ep.beta = p.a[i];
-    g.g.ep.sums = i > 0 ? w.step_sums[turn] : nullptr;
-    g.g.ep.scale_sums = sums;
-    g.g.ep.scale_parts = parts;
-    g.g.ep.target = i > 0 ? target[i - 1] : 12;
-    g.g.ep.exp_in = w.exp[i + 1];
-    g.g.ep.exp_out = w.exp[i];
-    g.to(w.H[turn ^ 1]);
-    sums = w.step_sums[turn];
-    parts = product_parts(p);
-    e = g.launch(log);
-  }
+  cudaError_t e = squares_and_pack(p, dY, w.sums, w.status, w.counters, a, log);
+  if (e == cudaSuccess) e = c.launch(log);
   if (e != cudaSuccess) return e;
-  const Terms &H0 = w.H[turn], &X0 = f.X[0];
   DotArgs d = {};
-  d.h[0] = H0.hi;
-  d.h[1] = H0.lo;
-  d.x[0] = X0.hi;
-  d.x[1] = X0.lo;
+  d.h[0] = w.H.hi + turn * w.H.slot;
+  d.h[1] = w.H.lo ? w.H.lo + turn * w.H.slot : nullptr;
+  d.x[0] = f.X.hi;
+  d.x[1] = p.xt[0] == 2 ? f.X.lo : nullptr;
   d.partial = w.sums;
   d.p = p.p; d.q = p.q; d.ld = p.ldq;
   e = launch_next(term_dots, dim3((unsigned)p.square_parts, (unsigned)p.L), kSumThreads, 0, 1, log, d);
@@ -1245,8 +719,8 @@ cudaError_t backward(const Plan& p, const void* G, const void* dY, void* dG, con
   EndArgs n = {};
   n.g = G;
   n.dg = dG;
-  n.h[0] = H0.hi;
-  n.h[1] = H0.lo;
+  n.h[0] = d.h[0];
+  n.h[1] = d.h[1];
   n.dots = w.sums;
   n.parts = p.square_parts;
   n.p = p.p; n.q = p.q; n.ld = p.ldq; n.tall = p.tall; n.x_exp = p.xe[0];
@@ -1289,8 +763,7 @@ int fbob_orth_forward(const fbob_orth_t* o, const void* g, void* y, void* ws, si
   if (!g || !y || !ws || off(g, size) || off(y, size) || off(ws, 256)) return FBOB_ERR_INVALID_ARG;
   if (ws_bytes < carve_forward(p, nullptr).bytes) return FBOB_ERR_WORKSPACE;
   if (!enter()) return FBOB_ERR_CUDA;
-  const Forward w = carve_forward(p, static_cast<char*>(ws));
-  if (!w.ok) return FBOB_ERR_CUDA;
+  Forward w = carve_forward(p, static_cast<char*>(ws));
   LaunchLog log{static_cast<cudaStream_t>(stream)};
   begin_call(log);
   const cudaError_t e = forward(p, g, y, w, log);
@@ -1310,9 +783,8 @@ int fbob_orth_backward(const fbob_orth_t* o, const void* g, const void* dy, void
   if (kept_bytes < carve_forward(p, nullptr).bytes || ws_bytes < carve_backward(p, nullptr).bytes)
     return FBOB_ERR_WORKSPACE;
   if (!enter()) return FBOB_ERR_CUDA;
-  const Forward f = carve_forward(p, const_cast<char*>(static_cast<const char*>(kept)));
-  const Backward w = carve_backward(p, static_cast<char*>(ws));
-  if (!f.ok || !w.ok) return FBOB_ERR_CUDA;
+  Forward f = carve_forward(p, const_cast<char*>(static_cast<const char*>(kept)));
+  Backward w = carve_backward(p, static_cast<char*>(ws));
   LaunchLog log{static_cast<cudaStream_t>(stream)};
   begin_call(log);
   const cudaError_t e = backward(p, g, dy, dg, f, w, log);
