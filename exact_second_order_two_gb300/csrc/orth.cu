@@ -60,6 +60,77 @@ __device__ __forceinline__ void split(float v, __half& hi, __half& lo) {
 // ---------------------------------------------------------------------------
 constexpr int kSumThreads = 256;
 
+// 16 aligned bytes of elements.
+__device__ __forceinline__ void load_vector(const __nv_bfloat16* p, float (&v)[8]) {
+  const uint4 x = *reinterpret_cast<const uint4*>(p);
+  const __nv_bfloat162* h = reinterpret_cast<const __nv_bfloat162*>(&x);
+#pragma unroll
+  for (int k = 0; k < 4; ++k) {
+    const float2 t = __bfloat1622float2(h[k]);
+    v[2 * k] = t.x;
+    v[2 * k + 1] = t.y;
+  }
+}
+__device__ __forceinline__ void load_vector(const float* p, float (&v)[4]) {
+  const float4 x = *reinterpret_cast<const float4*>(p);
+  v[0] = x.x; v[1] = x.y; v[2] = x.z; v[3] = x.w;
+}
+// Eight elements of which `valid` exist; `wide`: all do, at 16-byte steps.
+template <typename T>
+__device__ __forceinline__ void load8(const T* p, bool wide, int valid, float (&v)[8]) {
+  constexpr int V = 16 / sizeof(T);
+  if (wide) {
+#pragma unroll
+    for (int j = 0; j < 8; j += V) {
+      float t[V];
+      load_vector(p + j, t);
+#pragma unroll
+      for (int k = 0; k < V; ++k) v[j + k] = t[k];
+    }
+  } else {
+#pragma unroll
+    for (int k = 0; k < 8; ++k) v[k] = k < valid ? to_f32<T>(p[k]) : 0.f;
+  }
+}
+template <typename T>
+__device__ __forceinline__ void store8(T* p, bool wide, int valid, const float (&v)[8]) {
+  if (wide) {
+    alignas(16) T t[8];
+#pragma unroll
+    for (int k = 0; k < 8; ++k) t[k] = from_f32<T>(v[k]);
+#pragma unroll
+    for (int j = 0; j < (int)sizeof(T) / 2; ++j)
+      reinterpret_cast<uint4*>(p)[j] = reinterpret_cast<const uint4*>(t)[j];
+  } else {
+#pragma unroll
+    for (int k = 0; k < 8; ++k)
+      if (k < valid) p[k] = from_f32<T>(v[k]);
+  }
+}
+// Eight elements of a row of terms (rows are padded to eights).
+__device__ __forceinline__ void load_terms(const __half* hi, const __half* lo, float (&v)[8]) {
+#pragma unroll
+  for (int t = 0; t < 2; ++t) {
+    const __half* p = t ? lo : hi;
+    if (!p) continue;
+    const uint4 x = *reinterpret_cast<const uint4*>(p);
+    const __half2* h = reinterpret_cast<const __half2*>(&x);
+#pragma unroll
+    for (int k = 0; k < 4; ++k) {
+      const float2 f = __half22float2(h[k]);
+      v[2 * k] = t ? v[2 * k] + f.x : f.x;
+      v[2 * k + 1] = t ? v[2 * k + 1] + f.y : f.y;
+    }
+  }
+}
+__device__ __forceinline__ void store_terms(__half* hi, __half* lo, const float (&v)[8]) {
+  alignas(16) __half h[8], l[8];
+#pragma unroll
+  for (int k = 0; k < 8; ++k) split(v[k], h[k], l[k]);
+  *reinterpret_cast<uint4*>(hi) = *reinterpret_cast<const uint4*>(h);
+  if (lo) *reinterpret_cast<uint4*>(lo) = *reinterpret_cast<const uint4*>(l);
+}
+
 // partial[l][block] = sum of squares of a slice of matrix l; also clears the call's
 // status word and the chain's counters, before the kernels that write them.
 template <typename T>
@@ -73,20 +144,25 @@ __global__ void __launch_bounds__(kSumThreads)
        i += (size_t)gridDim.x * gridDim.y * kSumThreads)
     counters[i] = 0;
   x += (size_t)blockIdx.y * elems;
-  const size_t per = (elems + gridDim.x - 1) / gridDim.x;
-  const size_t first = blockIdx.x * per, last = min(elems, first + per);
   float s[4] = {0.f, 0.f, 0.f, 0.f};
-  size_t i = first + threadIdx.x;
-  for (; i + 3 * kSumThreads < last; i += 4 * kSumThreads) {
+  constexpr int V = 16 / sizeof(T);
+  if (elems % V == 0 && (reinterpret_cast<uintptr_t>(x) & 15u) == 0) {
+    const size_t chunks = elems / V, per = (chunks + gridDim.x - 1) / gridDim.x;
+    const size_t first = blockIdx.x * per, last = min(chunks, first + per);
+#pragma unroll 4
+    for (size_t i = first + threadIdx.x; i < last; i += kSumThreads) {
+      float v[V];
+      load_vector(x + i * V, v);
 #pragma unroll
-    for (int u = 0; u < 4; ++u) {
-      const float v = to_f32<T>(x[i + u * kSumThreads]);
-      s[u] = fmaf(v, v, s[u]);
+      for (int k = 0; k < V; ++k) s[k & 3] = fmaf(v[k], v[k], s[k & 3]);
     }
-  }
-  for (; i < last; i += kSumThreads) {
-    const float v = to_f32<T>(x[i]);
-    s[0] = fmaf(v, v, s[0]);
+  } else {
+    const size_t per = (elems + gridDim.x - 1) / gridDim.x;
+    const size_t first = blockIdx.x * per, last = min(elems, first + per);
+    for (size_t i = first + threadIdx.x; i < last; i += kSumThreads) {
+      const float v = to_f32<T>(x[i]);
+      s[0] = fmaf(v, v, s[0]);
+    }
   }
   const float w = warp_sum((s[0] + s[1]) + (s[2] + s[3]));
   if ((threadIdx.x & 31) == 0) sm[threadIdx.x >> 5] = w;
@@ -125,18 +201,18 @@ struct PackArgs {
   float* sums_out;
 };
 
-constexpr int kPack = 64;  // rows and columns of a block's tile
+constexpr int kPack = 64;  // rows and columns of a tile of a tall matrix
 
 // x times a power of two, in fp16 terms, the shorter side first.
 template <typename T>
 __global__ void __launch_bounds__(kSumThreads) pack(PackArgs a) {
   __shared__ float sm[kSumThreads / 32];
   __shared__ float tile[kPack][kPack + 1];
-  const int l = blockIdx.z;
+  const int l = blockIdx.y;
   let_next_start();
   after_previous();
   const float nu2 = parts_sum(a.sums + (size_t)l * a.parts, a.parts, sm);
-  const bool writer = blockIdx.x == 0 && blockIdx.y == 0 && threadIdx.x == 0;
+  const bool writer = blockIdx.x == 0 && threadIdx.x == 0;
   float factor;
   if (a.info) {
     MatInfo r;
@@ -163,22 +239,41 @@ __global__ void __launch_bounds__(kSumThreads) pack(PackArgs a) {
   }
   const T* x = static_cast<const T*>(a.x) + (size_t)l * a.p * a.q;
   const size_t base = (size_t)l * a.p * a.ld;
-  const int r0 = blockIdx.y * kPack, c0 = blockIdx.x * kPack;  // of the packed matrix
-  if (a.tall) {
-    for (int i = threadIdx.x; i < kPack * kPack; i += kSumThreads) {
-      const int c = i / kPack, r = i % kPack;  // x is [q][p]
-      if (c0 + c < a.q && r0 + r < a.p) tile[r][c] = to_f32<T>(x[(size_t)(c0 + c) * a.p + r0 + r]);
+  const int chunks = a.ld / 8;
+  if (a.tall) {  // x is [q][p]: tiles through shared memory
+    const int across = (a.q + kPack - 1) / kPack, all = across * ((a.p + kPack - 1) / kPack);
+    for (int t = blockIdx.x; t < all; t += gridDim.x) {
+      const int r0 = t / across * kPack, c0 = t % across * kPack;  // of the packed matrix
+      __syncthreads();
+      for (int i = threadIdx.x; i < kPack * kPack; i += kSumThreads) {
+        const int c = i / kPack, r = i % kPack;
+        tile[r][c] = c0 + c < a.q && r0 + r < a.p ? to_f32<T>(x[(size_t)(c0 + c) * a.p + r0 + r]) * factor : 0.f;
+      }
+      __syncthreads();
+      for (int i = threadIdx.x; i < kPack * kPack / 8; i += kSumThreads) {
+        const int r = i / (kPack / 8), c = i % (kPack / 8) * 8;
+        if (r0 + r >= a.p || c0 + c >= a.q) continue;
+        float v[8];
+#pragma unroll
+        for (int k = 0; k < 8; ++k) v[k] = tile[r][c + k];
+        const size_t at = base + (size_t)(r0 + r) * a.ld + c0 + c;
+        store_terms(a.hi + at, a.lo ? a.lo + at : nullptr, v);
+      }
     }
-    __syncthreads();
+    return;
   }
-  for (int i = threadIdx.x; i < kPack * kPack; i += kSumThreads) {
-    const int r = i / kPack, c = i % kPack;
-    if (r0 + r >= a.p || c0 + c >= a.q) continue;
-    const float v = (a.tall ? tile[r][c] : to_f32<T>(x[(size_t)(r0 + r) * a.q + c0 + c])) * factor;
-    __half hi, lo;
-    split(v, hi, lo);
-    a.hi[base + (size_t)(r0 + r) * a.ld + c0 + c] = hi;
-    if (a.lo) a.lo[base + (size_t)(r0 + r) * a.ld + c0 + c] = lo;
+  const bool wide = a.q % 8 == 0 && (reinterpret_cast<uintptr_t>(x) & 15u) == 0;
+  const long long all = (long long)a.p * chunks;
+#pragma unroll 2
+  for (long long i = (long long)blockIdx.x * kSumThreads + threadIdx.x; i < all;
+       i += (long long)gridDim.x * kSumThreads) {
+    const int r = (int)(i / chunks), c = (int)(i - (long long)r * chunks) * 8;
+    float v[8];
+    load8(x + (size_t)r * a.q + c, wide, a.q - c, v);
+#pragma unroll
+    for (int k = 0; k < 8; ++k) v[k] *= factor;
+    const size_t at = base + (size_t)r * a.ld + c;
+    store_terms(a.hi + at, a.lo ? a.lo + at : nullptr, v);
   }
 }
 
@@ -200,22 +295,9 @@ __global__ void __launch_bounds__(kSumThreads) term_dots(DotArgs a) {
   for (long long i = first + threadIdx.x; i < last; i += kSumThreads) {
     const int row = (int)(i / chunks), c = (int)(i - (long long)row * chunks) * 8;
     const size_t at = base + (size_t)row * a.ld + c;
-    float h[8] = {}, x[8] = {};
-#pragma unroll
-    for (int t = 0; t < 2; ++t) {
-      if (a.h[t]) {
-        const uint4 v = *reinterpret_cast<const uint4*>(a.h[t] + at);
-        const __half* w = reinterpret_cast<const __half*>(&v);
-#pragma unroll
-        for (int k = 0; k < 8; ++k) h[k] += __half2float(w[k]);
-      }
-      if (a.x[t]) {
-        const uint4 v = *reinterpret_cast<const uint4*>(a.x[t] + at);
-        const __half* w = reinterpret_cast<const __half*>(&v);
-#pragma unroll
-        for (int k = 0; k < 8; ++k) x[k] += __half2float(w[k]);
-      }
-    }
+    float h[8], x[8];
+    load_terms(a.h[0] + at, a.h[1] ? a.h[1] + at : nullptr, h);
+    load_terms(a.x[0] + at, a.x[1] ? a.x[1] + at : nullptr, x);
 #pragma unroll
     for (int k = 0; k < 8; ++k)  // (the padding of a row holds anything)
       if (c + k < a.q) s = fmaf(h[k], x[k], s);
@@ -246,7 +328,7 @@ template <typename T>
 __global__ void __launch_bounds__(kSumThreads) end_gradient(EndArgs a) {
   __shared__ float sm[kSumThreads / 32];
   __shared__ float tile[kPack][kPack + 1];
-  const int l = blockIdx.z;
+  const int l = blockIdx.y;
   after_previous();
   const MatInfo r = a.info[l];
   const float dot = parts_sum(a.dots + (size_t)l * a.parts, a.parts, sm);
@@ -255,27 +337,47 @@ __global__ void __launch_bounds__(kSumThreads) end_gradient(EndArgs a) {
   const double scale = ldexp((double)r.s, -a.exp[l]);
   const float by_h = (float)scale, by_g = (float)(scale * along);
   const size_t n = (size_t)l * a.p * a.q;
-  const int r0 = blockIdx.y * kPack, c0 = blockIdx.x * kPack;  // of h
   const size_t base = (size_t)l * a.p * a.ld;
   const T* g = static_cast<const T*>(a.g) + n;
   T* dg = static_cast<T*>(a.dg) + n;
-  auto value = [&](int rr, int c) {
-    const size_t at = base + (size_t)(r0 + rr) * a.ld + c0 + c;
-    return __half2float(a.h[0][at]) + (a.h[1] ? __half2float(a.h[1][at]) : 0.f);
-  };
-  if (a.tall) {
-    for (int i = threadIdx.x; i < kPack * kPack; i += kSumThreads) {
-      const int rr = i / kPack, c = i % kPack;
-      if (r0 + rr < a.p && c0 + c < a.q) tile[rr][c] = value(rr, c);
+  const int chunks = a.ld / 8;
+  if (a.tall) {  // g is [q][p]: tiles of h through shared memory
+    const int across = (a.q + kPack - 1) / kPack, all = across * ((a.p + kPack - 1) / kPack);
+    for (int t = blockIdx.x; t < all; t += gridDim.x) {
+      const int r0 = t / across * kPack, c0 = t % across * kPack;  // of h
+      __syncthreads();
+      for (int i = threadIdx.x; i < kPack * kPack / 8; i += kSumThreads) {
+        const int r = i / (kPack / 8), c = i % (kPack / 8) * 8;
+        if (r0 + r >= a.p || c0 + c >= a.q) continue;
+        const size_t at = base + (size_t)(r0 + r) * a.ld + c0 + c;
+        float v[8];
+        load_terms(a.h[0] + at, a.h[1] ? a.h[1] + at : nullptr, v);
+#pragma unroll
+        for (int k = 0; k < 8; ++k) tile[r][c + k] = v[k];
+      }
+      __syncthreads();
+      for (int i = threadIdx.x; i < kPack * kPack; i += kSumThreads) {
+        const int c = i / kPack, r = i % kPack;
+        if (r0 + r >= a.p || c0 + c >= a.q) continue;
+        const size_t at = (size_t)(c0 + c) * a.p + r0 + r;
+        dg[at] = from_f32<T>(fmaf(-by_g, to_f32<T>(g[at]), by_h * tile[r][c]));
+      }
     }
-    __syncthreads();
+    return;
   }
-  for (int i = threadIdx.x; i < kPack * kPack; i += kSumThreads) {
-    const int rr = a.tall ? i % kPack : i / kPack, c = a.tall ? i / kPack : i % kPack;
-    if (r0 + rr >= a.p || c0 + c >= a.q) continue;
-    const size_t at = a.tall ? (size_t)(c0 + c) * a.p + r0 + rr : (size_t)(r0 + rr) * a.q + c0 + c;
-    const float v = a.tall ? tile[rr][c] : value(rr, c);
-    dg[at] = from_f32<T>(fmaf(-by_g, to_f32<T>(g[at]), by_h * v));
+  const bool wide = a.q % 8 == 0 && ((reinterpret_cast<uintptr_t>(g) | reinterpret_cast<uintptr_t>(dg)) & 15u) == 0;
+  const long long all = (long long)a.p * chunks;
+#pragma unroll 2
+  for (long long i = (long long)blockIdx.x * kSumThreads + threadIdx.x; i < all;
+       i += (long long)gridDim.x * kSumThreads) {
+    const int r = (int)(i / chunks), c = (int)(i - (long long)r * chunks) * 8;
+    const size_t at = base + (size_t)r * a.ld + c, to = (size_t)r * a.q + c;
+    float v[8], x[8];
+    load_terms(a.h[0] + at, a.h[1] ? a.h[1] + at : nullptr, v);
+    load8(g + to, wide, a.q - c, x);
+#pragma unroll
+    for (int k = 0; k < 8; ++k) v[k] = fmaf(-by_g, x[k], by_h * v[k]);
+    store8(dg + to, wide, a.q - c, v);
   }
 }
 
@@ -283,7 +385,7 @@ __global__ void __launch_bounds__(kSumThreads) end_gradient(EndArgs a) {
 // Host: scales, workspace, launches
 // ---------------------------------------------------------------------------
 struct Plan {
-  int L, m, n, p, q, ldq, ldp, steps, bf16, keep, tall, ctas;
+  int L, m, n, p, q, ldq, ldp, steps, bf16, keep, tall;
   float eps;
   float a[kMaxSteps], b[kMaxSteps], c[kMaxSteps];
   int xe[kMaxSteps], ae[kMaxSteps], be[kMaxSteps];  // exponents of X, A, B as stored
@@ -292,9 +394,23 @@ struct Plan {
   int square_parts;
 };
 
-// CTAs that share a tile.
-int choose_ctas(const Plan& p) {
-  return getenv("ORTH_CTAS") ? atoi(getenv("ORTH_CTAS")) : 2;
+// Columns of a product's tiles: 128 where that fills more of the GPU.  A tile costs its
+// multiplications (128 columns 0.8 of what 256 do: half, less well fed), in stages of
+// 64 elements, and as much as 8 stages beside them.
+int choose_wide(const Plan& p, int cols, int depth, bool sym, int segs) {
+  if (getenv("ORTH_WIDE")) return atoi(getenv("ORTH_WIDE"));
+  double best = 0;
+  int wide = 0;
+  for (int w : {256, 128}) {
+    const long long tiles = p.L * tiles_of(p.p, cols, sym, w);
+    const double stages = (double)segs * ((depth + kDepth - 1) / kDepth);
+    const double t = (double)((tiles + kPairs - 1) / kPairs) * (stages * (w == 256 ? 1.0 : 0.8) + 8);
+    if (!wide || t < best) {
+      best = t;
+      wide = w;
+    }
+  }
+  return wide;
 }
 
 int floor_log2(double x) { return (int)floor(log2(x)); }
@@ -350,9 +466,8 @@ int make_plan(const fbob_orth_t* o, Plan* out) {
   const long long elems = (long long)p.p * p.q;
   const long long parts = (elems + 8191) / 8192;
   p.square_parts = (int)(parts < 1024 ? parts : 1024);
-  p.ctas = choose_ctas(p);
   // items of a chain are counted in 32 bits
-  const double tiles = 2.0 * tiles_of(p.p, p.p, true, p.ctas) + (double)tiles_of(p.p, p.q, false, p.ctas);
+  const double tiles = 2.0 * tiles_of(p.p, p.p, true, 128) + (double)tiles_of(p.p, p.q, false, 128);
   if (tiles * p.L * p.steps > (double)(1 << 30)) return FBOB_ERR_UNSUPPORTED;
   *out = p;
   return FBOB_OK;
@@ -444,7 +559,10 @@ struct Backward {
   Mats H, S, T;
   size_t bytes;
 };
-int step_parts(const Plan& p) { return parts_of(tiles_of(p.p, p.q, false, p.ctas), p.ctas); }
+int step_wide(const Plan& p) {  // of B H + T X
+  return choose_wide(p, p.q, p.p, false, p.bf16 ? 2 : 6);
+}
+int step_parts(const Plan& p) { return (int)tiles_of(p.p, p.q, false, step_wide(p)) * 2 * kEpiWarps; }
 Backward carve_backward(const Plan& p, char* base) {
   Backward w;
   Carver c{base, 0};
@@ -474,8 +592,9 @@ struct Chain {
   const Plan& p;
   int maps = 0, items = 0;
   bool ok = true;
-  int highs = 0;
+  int highs = 0, q_terms[kMaxSegs];
   Ref high_p[2], high_q[2];
+  const Mats* q_of[kMaxSegs];
   Chain(const Plan& plan, int* status, int* counts, const MatInfo* info) : p(plan) {
     g.phases = 0;
     g.rows = p.p;
@@ -512,14 +631,14 @@ struct Chain {
     f.nn = nn;
     f.sym = sym;
     f.first = items;
-    f.tiles = tiles_of(p.p, cols, sym, p.ctas);
     highs = 0;
   }
   void pair(const Ref& P, int tp, const Ref& Q, int tq) {
     Phase& f = phase();
     f.seg_a[f.nseg] = P.m->tile[tp];
     f.at_a[f.nseg] = P.slot * p.L;
-    f.seg_b[f.nseg] = f.nn ? Q.m->step[tq] : Q.m->tile[tq];
+    q_terms[f.nseg] = tq;
+    q_of[f.nseg] = Q.m;
     f.at_b[f.nseg++] = Q.slot * p.L;
   }
   // acc += P Q^T (or P Q): every pair of terms but the two low ones
@@ -560,15 +679,30 @@ struct Chain {
     // The products of high terms come last: the tensor cores cut every addition off to the
     // accumulator's 24 bits, which costs nothing while it holds the small ones only.
     for (int i = 0; i < highs; ++i) pair(high_p[i], 0, high_q[i], 0);
-    items += p.L * phase().tiles;
+    Phase& f = phase();
+    f.wide = choose_wide(p, f.cols, f.depth, f.sym, f.nseg);
+    f.tiles = (int)tiles_of(p.p, f.cols, f.sym, f.wide);
+    // a CTA's half of the right operand's tile: 64 or 128 rows of it, or columns 64 at a time
+    for (int i = 0; i < f.nseg; ++i)
+      f.seg_b[i] = (f.nn || f.wide == 128 ? q_of[i]->step : q_of[i]->tile)[q_terms[i]];
+    items += p.L * f.tiles;
     ++g.phases;
   }
   cudaError_t launch(LaunchLog& log) {
     if (!ok) return cudaErrorUnknown;
     g.items = items;
-    return launch_chain(g, p.ctas, log);
+    return launch_chain(g, log);
   }
 };
+
+// Blocks of a pass over every matrix: 2048 elements (a tile of 4096 of a tall one) each,
+// up to eight blocks an SM.
+dim3 passes(const Plan& p) {
+  const long long tiles = (long long)((p.p + kPack - 1) / kPack) * ((p.q + kPack - 1) / kPack);
+  const long long n = p.tall ? tiles : ((long long)p.p * p.ldq + 2047) / 2048;
+  const long long most = (8ll * kSms + p.L - 1) / p.L;
+  return dim3((unsigned)(n < most ? n : most), (unsigned)p.L);
+}
 
 cudaError_t squares_and_pack(const Plan& p, const void* x, float* sums, int* status, int* counts,
                              PackArgs a, LaunchLog& log) {
@@ -588,8 +722,7 @@ cudaError_t squares_and_pack(const Plan& p, const void* x, float* sums, int* sta
   a.parts = p.square_parts;
   a.p = p.p; a.q = p.q; a.ld = p.ldq; a.tall = p.tall;
   a.eps = p.eps;
-  const dim3 tiles((unsigned)((p.q + kPack - 1) / kPack), (unsigned)((p.p + kPack - 1) / kPack), (unsigned)p.L);
-  return launch_next(p.bf16 ? pack<__nv_bfloat16> : pack<float>, tiles, kSumThreads, 0, 1, log, a);
+  return launch_next(p.bf16 ? pack<__nv_bfloat16> : pack<float>, passes(p), kSumThreads, 0, 1, log, a);
 }
 
 float pow2(int e) { return ldexpf(1.f, e); }
@@ -726,8 +859,7 @@ cudaError_t backward(const Plan& p, const void* G, const void* dY, void* dG, For
   n.p = p.p; n.q = p.q; n.ld = p.ldq; n.tall = p.tall; n.x_exp = p.xe[0];
   n.info = f.info;
   n.exp = w.exp[0];
-  const dim3 tiles((unsigned)((p.q + kPack - 1) / kPack), (unsigned)((p.p + kPack - 1) / kPack), (unsigned)p.L);
-  return launch_next(p.bf16 ? end_gradient<__nv_bfloat16> : end_gradient<float>, tiles, kSumThreads, 0, 1,
+  return launch_next(p.bf16 ? end_gradient<__nv_bfloat16> : end_gradient<float>, passes(p), kSumThreads, 0, 1,
                      log, n);
 }
 

@@ -19,7 +19,10 @@ struct MatInfo {
   int k;
 };
 
-constexpr int kTile = 128;      // rows, and columns, of a CTA's operand tiles
+constexpr int kTile = 128;      // rows of a CTA's operand tiles
+constexpr int kHigh = 256;      // rows of a pair's tile of a product
+constexpr int kWide = 256;      // its columns, at most
+constexpr int kPairs = kSms / 2;
 constexpr int kDepth = 64;      // contraction elements of a stage (128-byte rows)
 constexpr int kEpiWarps = 8;    // warps that finish tiles
 constexpr int kGroups = 2;      // in groups of four
@@ -38,6 +41,7 @@ struct Phase {
   int nseg, nn;
   int cols, depth;
   int sym;                      // symmetric: tiles on and below the diagonal
+  int wide;                     // columns of a tile: 128 or 256
   unsigned char e_map[2], o_map[2];
   int e_terms, e_at;            // terms of E: 0 without
   int o_terms, o_at;            // of the result: 0 where it goes to the caller's tensor.  One
@@ -71,13 +75,12 @@ struct ChainArgs {
 
 static_assert(sizeof(ChainArgs) <= 32000, "kernel argument budget");
 
-inline int tiles_of(int rows, int cols, bool sym, int ctas) {  // of one matrix
-  const int side = kTile * ctas, tm = (rows + side - 1) / side, tn = (cols + side - 1) / side;
-  return sym ? tm * (tm + 1) / 2 : tm * tn;
+inline long long tiles_of(int rows, int cols, bool sym, int wide) {  // of one matrix
+  const long long tm = (rows + kHigh - 1) / kHigh, tn = (cols + wide - 1) / wide;
+  return sym ? kHigh / wide * tm * (tm + 1) / 2 : tm * tn;
 }
-inline int parts_of(int tiles, int ctas) { return tiles * ctas * kEpiWarps; }  // of Phase::sums
 
-cudaError_t launch_chain(const ChainArgs& g, int ctas, LaunchLog& log);
+cudaError_t launch_chain(const ChainArgs& g, LaunchLog& log);
 
 // Launches a kernel that may start while the one before it in the stream ends; it
 // waits for that one's results by after_previous().

@@ -13,10 +13,13 @@
 // results out, one takes items and waits for what they read; two accumulators, so that
 // a tile is finished while the next is multiplied, and items taken ahead, so that the next
 // tile's loads follow at once.  (With the waits in the loading and finishing warps a tile
-// of 256 x 256 x 2048 took 15 us, 10.5 of them its MMAs.)  CTAS = 2: a pair of CTAs multiplies a tile of
-// 256 x 256, each loading its 128 rows of P and 128 columns of Q (64 bytes a clock of shared
-// memory and of L2 for each SM; 128 x 128 tiles need twice that, and 128 bytes is what an SM
-// has), CTA 0 issuing for both.
+// of 256 x 256 x 2048 took 15 us, 10.5 of them its MMAs.)
+//
+// A pair of CTAs multiplies a tile of 256 rows and 256 or 128 columns, each loading its
+// 128 rows of P and half of the columns of Q, CTA 0 issuing for both: at 256 columns 64
+// bytes a clock of shared memory and of L2 for each SM.  (Single CTAs with tiles of
+// 128 x 128 need 128, which is what an SM has: 4 x 2048 x 2048 took 1.5 times as long.)
+// 128 columns where 256 leave pairs idle.
 #include <cuda.h>
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
@@ -58,22 +61,26 @@ __host__ __device__ constexpr uint32_t idesc_f16(int M, int N, bool b_mn_major) 
 
 struct TileAt {
   int l, i, j, index;  // matrix, tile row and column, its number within the matrix
+  bool below;          // the diagonal's square: its mirror is no tile
 };
-__device__ __forceinline__ TileAt tile_at(const Phase& p, int rows, int item, int side) {
-  const int tm = (rows + side - 1) / side;
+__device__ __forceinline__ TileAt tile_at(const Phase& p, int rows, int item) {
   const int t = item - p.first;
   TileAt r;
   r.l = t / p.tiles;
   r.index = t - r.l * p.tiles;
-  if (p.sym) {
-    int i = (int)((sqrtf(8.f * r.index + 1.f) - 1.f) * 0.5f);
-    while (i * (i + 1) / 2 > r.index) --i;
-    while ((i + 1) * (i + 2) / 2 <= r.index) ++i;
+  if (p.sym) {  // rows of w, 2 w, 3 w .. tiles, of which the last w hold the diagonal
+    const int w = kHigh / p.wide;
+    int i = (int)((sqrtf(8.f * (r.index / w) + 1.f) - 1.f) * 0.5f);
+    while (w * i * (i + 1) / 2 > r.index) --i;
+    while (w * (i + 1) * (i + 2) / 2 <= r.index) ++i;
     r.i = i;
-    r.j = r.index - i * (i + 1) / 2;
+    r.j = r.index - w * i * (i + 1) / 2;
+    r.below = r.j < w * i;
   } else {  // a column of tiles after the other: its operand tile is shared
+    const int tm = (rows + kHigh - 1) / kHigh;
     r.j = r.index / tm;
     r.i = r.index - r.j * tm;
+    r.below = false;
   }
   return r;
 }
@@ -215,7 +222,6 @@ __device__ __forceinline__ int slots_of(const Phase& p, const ChainArgs& g) {
   return p.sym || p.e_terms == 2 || p.o_terms == 2 || (p.o_terms == 0 && !g.y_bf16) ? 1 : 2;
 }
 
-template <int CTAS>
 __global__ void __launch_bounds__(kThreads, 1) chain(const __grid_constant__ ChainArgs g) {
   extern __shared__ __align__(1024) uint8_t smem[];
   const uint32_t sb = smem_u32(smem);
@@ -239,10 +245,8 @@ __global__ void __launch_bounds__(kThreads, 1) chain(const __grid_constant__ Cha
   Abort* ab = reinterpret_cast<Abort*>(smem + kOffMisc + 264);
   volatile int* ring = reinterpret_cast<volatile int*>(smem + kOffMisc + 288);  // [kRing]: items, -1: none left
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  const uint32_t rank = CTAS == 2 ? cluster_rank() : 0;
-  constexpr int kSide = kTile * CTAS;
-  constexpr uint32_t kCols = 2 * kSide;
-  constexpr int kChunks = kSide / 64 / kGroups;  // of a tile, for each group
+  const uint32_t rank = cluster_rank();
+  constexpr uint32_t kCols = 2 * kWide;
   if (threadIdx.x == 0) {
     for (int s = 0; s < kStages; ++s) {
       mbar_init(full + s, 1);
@@ -250,7 +254,7 @@ __global__ void __launch_bounds__(kThreads, 1) chain(const __grid_constant__ Cha
     }
     for (int b = 0; b < 2; ++b) {
       mbar_init(t_full + b, 1);
-      mbar_init(t_empty + b, kEpiWarps * CTAS);
+      mbar_init(t_empty + b, 2 * kEpiWarps);
     }
     for (int i = 0; i < 2 * kGroups; ++i) {
       mbar_init(e_full + i, 1);
@@ -259,7 +263,7 @@ __global__ void __launch_bounds__(kThreads, 1) chain(const __grid_constant__ Cha
     for (int i = 0; i < kRing; ++i) {
       mbar_init(r_full + i, 1);
       // the multiplying warp, and each CTA's finishing, loading and moving ones
-      mbar_init(r_empty + i, 1 + (kEpiWarps + 2) * CTAS);
+      mbar_init(r_empty + i, 1 + 2 * (kEpiWarps + 2));
     }
     mbar_init(started, 1);
     mbar_init(drain, 1);
@@ -268,17 +272,12 @@ __global__ void __launch_bounds__(kThreads, 1) chain(const __grid_constant__ Cha
     fence_mbar_init();
   }
   if (warp == kMmaWarp) {
-    if (CTAS == 2) {
-      tmem_alloc_pair(tmem_slot, kCols);
-      tmem_relinquish_pair();
-    } else {
-      tmem_alloc(tmem_slot, kCols);
-      tmem_relinquish();
-    }
+    tmem_alloc_pair(tmem_slot, kCols);
+    tmem_relinquish_pair();
   }
   tc_fence_before();
   __syncthreads();
-  if (CTAS == 2) cluster_sync();  // the other's barriers are there
+  cluster_sync();  // the other's barriers are there
   tc_fence_after();
   after_previous();
   const uint32_t tmem = *tmem_slot;
@@ -302,8 +301,7 @@ __global__ void __launch_bounds__(kThreads, 1) chain(const __grid_constant__ Cha
     return true;
   };
   auto item_read = [&](int n) {
-    if (CTAS == 2) mbar_arrive_cluster(cluster_addr(r_empty + n % kRing, 0));
-    else mbar_arrive(r_empty + n % kRing);
+    mbar_arrive_cluster(cluster_addr(r_empty + n % kRing, 0));
   };
   // the phase of an item (items come in order)
   auto phase_of = [&](int ph, int item) {
@@ -323,17 +321,15 @@ __global__ void __launch_bounds__(kThreads, 1) chain(const __grid_constant__ Cha
           ph = phase_of(ph, item);
           const Phase& p = g.phase[ph];
           const int l = (item - p.first) / p.tiles;
-          if (ph > 0 && !wait_count(g.done + (size_t)(ph - 1) * g.count + l, g.phase[ph - 1].tiles * CTAS, ab,
+          if (ph > 0 && !wait_count(g.done + (size_t)(ph - 1) * g.count + l, 2 * g.phase[ph - 1].tiles, ab,
                                     g.status))
             break;
         }
         if (n >= kRing && !wait_bar(r_empty + n % kRing, ((n / kRing) - 1) & 1, ab, g.status)) break;
         ring[n % kRing] = item;
         mbar_arrive(r_full + n % kRing);
-        if (CTAS == 2) {
-          st_cluster(cluster_addr(const_cast<int*>(ring + n % kRing), 1), item);
-          mbar_arrive_cluster(cluster_addr(r_full + n % kRing, 1));
-        }
+        st_cluster(cluster_addr(const_cast<int*>(ring + n % kRing), 1), item);
+        mbar_arrive_cluster(cluster_addr(r_full + n % kRing, 1));
         if (item < 0) break;
       }
     }
@@ -350,8 +346,9 @@ __global__ void __launch_bounds__(kThreads, 1) chain(const __grid_constant__ Cha
         fence_async_all();  // the loads see what the scheduler saw written
         ph = phase_of(ph, item);
         const Phase& p = g.phase[ph];
-        const TileAt at = tile_at(p, g.rows, item, kSide);
-        const int row = at.i * kSide + rank * kTile, col = at.j * kSide + rank * kTile;
+        const TileAt at = tile_at(p, g.rows, item);
+        const int half = p.wide / 2;  // of the tile's columns, this CTA's part of Q
+        const int row = at.i * kHigh + rank * kTile, col = at.j * p.wide + rank * half;
         const int blocks = (p.depth + kDepth - 1) / kDepth;
         const bool nn = p.nn;
         for (int sg = 0; ok && sg < p.nseg; ++sg) {
@@ -369,24 +366,14 @@ __global__ void __launch_bounds__(kThreads, 1) chain(const __grid_constant__ Cha
             }
             if (lane != 0) continue;
             uint8_t *pa = smem + s * kStageBytes, *pb = pa + kTileBytes;
-            if (rank == 0) mbar_arrive_expect_tx(full + s, CTAS * kStageBytes);
-            if (CTAS == 2) {
-              const uint32_t bar = cluster_addr(full + s, 0);
-              tma_load_3d_pair(pa, ma, bar, k * kDepth, row, la);
-              if (nn) {
-                tma_load_3d_pair(pb, mb, bar, col, k * kDepth, lb);
-                tma_load_3d_pair(pb + kTileBytes / 2, mb, bar, col + 64, k * kDepth, lb);
-              } else {
-                tma_load_3d_pair(pb, mb, bar, k * kDepth, col, lb);
-              }
+            if (rank == 0) mbar_arrive_expect_tx(full + s, 2 * (kTileBytes + half * 128));
+            const uint32_t bar = cluster_addr(full + s, 0);
+            tma_load_3d_pair(pa, ma, bar, k * kDepth, row, la);
+            if (nn) {
+              tma_load_3d_pair(pb, mb, bar, col, k * kDepth, lb);
+              if (half > 64) tma_load_3d_pair(pb + kTileBytes / 2, mb, bar, col + 64, k * kDepth, lb);
             } else {
-              tma_load_3d(pa, ma, full + s, k * kDepth, row, la);
-              if (nn) {
-                tma_load_3d(pb, mb, full + s, col, k * kDepth, lb);
-                tma_load_3d(pb + kTileBytes / 2, mb, full + s, col + 64, k * kDepth, lb);
-              } else {
-                tma_load_3d(pb, mb, full + s, k * kDepth, col, lb);
-              }
+              tma_load_3d_pair(pb, mb, bar, k * kDepth, col, lb);
             }
           }
         }
@@ -397,7 +384,7 @@ __global__ void __launch_bounds__(kThreads, 1) chain(const __grid_constant__ Cha
       if (rank == 0 && lane == 0)
         for (int u = max(0, it - kStages); u < it; ++u)
           mbar_wait_bounded(full + u % kStages, (u / kStages) & 1, g.status, 100000000ull);
-      if (CTAS == 2 && ab->flag) sleep_10ms();
+      if (ab->flag) sleep_10ms();
     }
   } else if (warp == kMmaWarp) {
     if (rank == 0) {
@@ -412,8 +399,8 @@ __global__ void __launch_bounds__(kThreads, 1) chain(const __grid_constant__ Cha
         ph = phase_of(ph, item);
         const Phase& p = g.phase[ph];
         const bool nn = p.nn;
-        const uint32_t id = nn ? idesc_f16(kSide, kSide, true) : idesc_f16(kSide, kSide, false);
-        const uint32_t d = tmem + (n & 1) * kSide;
+        const uint32_t id = idesc_f16(kHigh, p.wide, nn);
+        const uint32_t d = tmem + (n & 1) * kWide;
         if (n >= 2 && !warp_wait(t_empty + (n & 1), ((n >> 1) - 1) & 1, ab, g.status)) break;
         tc_fence_after();
         const int total = p.nseg * ((p.depth + kDepth - 1) / kDepth);
@@ -432,19 +419,15 @@ __global__ void __launch_bounds__(kThreads, 1) chain(const __grid_constant__ Cha
 #pragma unroll
           for (int u = 0; u < kDepth / 16; ++u) {
             const uint32_t al = a_lo + 2 * u, bl = b_lo + b_step * u;
-            if (CTAS == 2) mma_ss_pair_w(d, al, bl, id, k + u > 0 ? 1u : 0u);
-            else mma_ss_w(d, al, bl, id, k + u > 0 ? 1u : 0u);
+            mma_ss_pair_w(d, al, bl, id, k + u > 0 ? 1u : 0u);
           }
-          if (CTAS == 2) mma_commit_pair_w(empty + s, 3);
-          else mma_commit_w(empty + s);
+          mma_commit_pair_w(empty + s, 3);
         }
         if (!ok) break;
-        if (CTAS == 2) mma_commit_pair_w(t_full + (n & 1), 3);
-        else mma_commit_w(t_full + (n & 1));
+        mma_commit_pair_w(t_full + (n & 1), 3);
       }
       // every MMA this warp issued has completed before TMEM is released
-      if (CTAS == 2) mma_commit_pair_w(drain, 1);
-      else mma_commit_w(drain);
+      mma_commit_pair_w(drain, 1);
       mbar_wait_bounded(drain, 0, g.status, 100000000ull);
     }
   } else if (warp == kMoverWarp) {
@@ -460,14 +443,14 @@ __global__ void __launch_bounds__(kThreads, 1) chain(const __grid_constant__ Cha
         fence_async_all();
         ph = phase_of(ph, item);
         const Phase& p = g.phase[ph];
-        const TileAt at = tile_at(p, g.rows, item, kSide);
-        const int row0 = at.i * kSide + rank * kTile;
+        const TileAt at = tile_at(p, g.rows, item);
+        const int row0 = at.i * kHigh + rank * kTile;
         const bool to_caller = p.o_terms == 0, mapped = !to_caller || g.y_mapped;
-        const bool mirror = p.sym && at.i != at.j;
-        const int nslots = slots_of(p, g);
+        const bool mirror = p.sym && at.below;
+        const int nslots = slots_of(p, g), chunks = p.wide / (64 * kGroups);
         // what is added to chunk c of a group comes into its slot
         auto prepare = [&](int group, int c) {
-          const int s = 2 * group + c % nslots, col = at.j * kSide + (group + c * kGroups) * 64;
+          const int s = 2 * group + c % nslots, col = at.j * p.wide + (group + c * kGroups) * 64;
           uint8_t* const slot = smem + kOffSlots + s * kTileBytes;
           if (p.e_terms) {
             mbar_arrive_expect_tx(e_full + s, p.e_terms * kTileBytes);
@@ -480,10 +463,10 @@ __global__ void __launch_bounds__(kThreads, 1) chain(const __grid_constant__ Cha
         };
         if (ab->flag) break;
         for (int group = 0; group < kGroups; ++group)
-          for (int c = 0; c < nslots && c < kChunks; ++c) prepare(group, c);
-        for (int c = 0; ok && c < kChunks; ++c)
+          for (int c = 0; c < nslots && c < chunks; ++c) prepare(group, c);
+        for (int c = 0; ok && c < chunks; ++c)
           for (int group = 0; ok && group < kGroups; ++group) {
-            const int s = 2 * group + c % nslots, col0 = at.j * kSide + (group + c * kGroups) * 64;
+            const int s = 2 * group + c % nslots, col0 = at.j * p.wide + (group + c * kGroups) * 64;
             uint8_t* const slot = smem + kOffSlots + s * kTileBytes;
             if (!wait_bar(written + s, (uses >> s) & 1, ab, g.status) || ab->flag) {
               ok = false;
@@ -505,7 +488,7 @@ __global__ void __launch_bounds__(kThreads, 1) chain(const __grid_constant__ Cha
               }
               bulk_commit_group();
             }
-            if (c + nslots < kChunks) {
+            if (c + nslots < chunks) {
               bulk_wait_read_all();
               prepare(group, c + nslots);
             }
@@ -513,7 +496,6 @@ __global__ void __launch_bounds__(kThreads, 1) chain(const __grid_constant__ Cha
         if (!ok) break;
         // the tile is in memory: its stores, and what the finishing warps wrote themselves
         bulk_wait_all();
-        fence_async_all();
         asm volatile("red.release.gpu.global.add.s32 [%0], 1;" ::"l"(g.done + (size_t)ph * g.count + at.l)
                      : "memory");
       }
@@ -533,11 +515,11 @@ __global__ void __launch_bounds__(kThreads, 1) chain(const __grid_constant__ Cha
       if (item < 0) break;
       ph = phase_of(ph, item);
       const Phase& p = g.phase[ph];
-      const TileAt at = tile_at(p, g.rows, item, kSide);
-      const int row0 = at.i * kSide + rank * kTile, row = row0 + r;
+      const TileAt at = tile_at(p, g.rows, item);
+      const int row0 = at.i * kHigh + rank * kTile, row = row0 + r;
       const bool to_caller = p.o_terms == 0, mapped = !to_caller || g.y_mapped;
-      const bool mirror = p.sym && at.i != at.j;
-      const int nslots = slots_of(p, g);
+      const bool mirror = p.sym && at.below;
+      const int nslots = slots_of(p, g), chunks = p.wide / (64 * kGroups);  // chunks for each group
       float alpha = p.alpha, beta = p.beta;
       if (p.fpow) {
         const float f = g.info[at.l].f, ff = p.fpow == 2 ? f * f : f;
@@ -561,8 +543,8 @@ __global__ void __launch_bounds__(kThreads, 1) chain(const __grid_constant__ Cha
       tc_fence_after();
       float sum = 0.f;
 #pragma unroll 1
-      for (int c = 0; c < kChunks; ++c) {
-        const int in_tile = (group + c * kGroups) * 64, col0 = at.j * kSide + in_tile;
+      for (int c = 0; c < chunks; ++c) {
+        const int in_tile = (group + c * kGroups) * 64, col0 = at.j * p.wide + in_tile;
         const int s = 2 * group + c % nslots;
         uint8_t* const slot = smem + kOffSlots + s * kTileBytes;
         if (!warp_wait(e_full + s, (uses >> s) & 1, ab, g.status)) {
@@ -574,7 +556,7 @@ __global__ void __launch_bounds__(kThreads, 1) chain(const __grid_constant__ Cha
         for (int h = 0; h < 2; ++h) {
           const int col = col0 + 32 * h;
           uint32_t acc[32];
-          tmem_ld32(tmem + lane_off + (n & 1) * kSide + in_tile + 32 * h, acc);
+          tmem_ld32(tmem + lane_off + (n & 1) * kWide + in_tile + 32 * h, acc);
           f2 v[16];
 #pragma unroll
           for (int k = 0; k < 16; ++k)
@@ -624,12 +606,12 @@ __global__ void __launch_bounds__(kThreads, 1) chain(const __grid_constant__ Cha
             for (int k = 0; k < 4; ++k) *reinterpret_cast<float4*>(slot_chunk(slot, r, 4 + k)) = f[k];
           }
         }
-        if (c == kChunks - 1) {
+        if (c == chunks - 1) {
           tc_fence_before();
           if (p.sums) {
             sum = warp_sum(sum);
             if (lane == 0) {
-              p.sums[((size_t)at.l * p.tiles + at.index) * (CTAS * kEpiWarps) + rank * kEpiWarps + warp] = sum;
+              p.sums[((size_t)at.l * p.tiles + at.index) * (2 * kEpiWarps) + rank * kEpiWarps + warp] = sum;
               __threadfence();
             }
           }
@@ -638,9 +620,8 @@ __global__ void __launch_bounds__(kThreads, 1) chain(const __grid_constant__ Cha
         __syncwarp();
         if (lane == 0) {
           mbar_arrive(written + s);
-          if (c == kChunks - 1) {
-            if (CTAS == 2) mbar_arrive_cluster(cluster_addr(t_empty + (n & 1), 0));
-            else mbar_arrive(t_empty + (n & 1));
+          if (c == chunks - 1) {
+            mbar_arrive_cluster(cluster_addr(t_empty + (n & 1), 0));
           }
         }
       }
@@ -649,22 +630,20 @@ __global__ void __launch_bounds__(kThreads, 1) chain(const __grid_constant__ Cha
   tc_fence_before();
   __syncthreads();
   __syncwarp();
-  if (CTAS == 2) cluster_sync();  // neither leaves before the other's last use of it
+  cluster_sync();  // neither leaves before the other's last use of it
   if (warp == kMmaWarp) {
     tc_fence_after();
-    if (CTAS == 2) tmem_dealloc_pair(tmem, kCols);
-    else tmem_dealloc(tmem, kCols);
+    tmem_dealloc_pair(tmem, kCols);
   }
 }
 
 }  // namespace
 
-cudaError_t launch_chain(const ChainArgs& g, int ctas, LaunchLog& log) {
-  auto kernel = ctas == 2 ? chain<2> : chain<1>;
-  const cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmem);
+cudaError_t launch_chain(const ChainArgs& g, LaunchLog& log) {
+  const cudaError_t e = cudaFuncSetAttribute(chain, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmem);
   if (e != cudaSuccess) return e;
-  const int most = kSms / ctas, grid = (g.items < most ? g.items : most) * ctas;
-  return launch_next(kernel, dim3((unsigned)grid), kThreads, kSmem, ctas, log, g);
+  const int grid = 2 * (g.items < kPairs ? g.items : kPairs);
+  return launch_next(chain, dim3((unsigned)grid), kThreads, kSmem, 2, log, g);
 }
 
 }  // namespace orth
