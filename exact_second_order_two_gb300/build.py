@@ -23,7 +23,7 @@ LIB_DIR = os.path.join(PKG, "_lib")
 LIB_PATH = os.path.join(LIB_DIR, "libfbob.so")
 
 SOURCES = ["api.cu", "simt.cu", "tc.cu", "tc_attn.cu", "noalloc.cu",
-           "rotary.cu", "qk_norm.cu", "orth.cu", "orth_chain.cu", "diff.cu", "diff_simt.cu", "diff_tc.cu"]
+           "rotary.cu", "qk_norm.cu", "orth.cu", "orth_chain.cu", "orth_small.cu", "diff.cu", "diff_simt.cu", "diff_tc.cu"]
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 NVCC_FLAGS = ARCH + [
     "-O3", "-lineinfo", "-std=c++17", "-Xcompiler", "-fPIC",

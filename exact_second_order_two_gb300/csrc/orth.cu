@@ -216,18 +216,7 @@ __global__ void __launch_bounds__(kSumThreads) pack(PackArgs a) {
   float factor;
   if (a.info) {
     MatInfo r;
-    r.norm = sqrtf(nu2);
-    r.s = 1.f / (r.norm + a.eps);
-    if (r.s > 0.f && r.s < 3.0e38f) {
-      int e;
-      r.f = 2.f * frexpf(r.s, &e);  // s = f 2^(e - 1)
-      r.k = e - 1;
-      factor = ldexpf(1.f, r.k + a.target);
-    } else {  // an infinite or NaN norm, or 0 and eps = 0: zeros and NaN as s G gives them
-      r.f = 1.f;
-      r.k = 0;
-      factor = r.s;
-    }
+    factor = info_of(nu2, a.eps, a.target, r);
     if (writer) a.info[l] = r;
   } else {
     const int e = rescaling(nu2, a.target);
@@ -332,10 +321,8 @@ __global__ void __launch_bounds__(kSumThreads) end_gradient(EndArgs a) {
   after_previous();
   const MatInfo r = a.info[l];
   const float dot = parts_sum(a.dots + (size_t)l * a.parts, a.parts, sm);
-  // <h, G> = dot 2^-(k + x_exp); a zero matrix has no direction to take off
-  const double along = r.norm > 0.f ? ldexp((double)dot, -(r.k + a.x_exp)) * r.s / r.norm : 0.0;
-  const double scale = ldexp((double)r.s, -a.exp[l]);
-  const float by_h = (float)scale, by_g = (float)(scale * along);
+  float by_h, by_g;
+  end_factors(r, dot, a.exp[l], a.x_exp, by_h, by_g);
   const size_t n = (size_t)l * a.p * a.q;
   const size_t base = (size_t)l * a.p * a.ld;
   const T* g = static_cast<const T*>(a.g) + n;
@@ -727,7 +714,69 @@ cudaError_t squares_and_pack(const Plan& p, const void* x, float* sums, int* sta
 
 float pow2(int e) { return ldexpf(1.f, e); }
 
+// H's norm is brought to 2^target: every entry of H, S (stored at 2^se), T and of the next
+// H stays below 2^15 whatever their directions.
+void backward_scales(const Plan& p, int* target, int* se) {
+  for (int i = 0; i < p.steps; ++i) {
+    const double M = p.M[i], a = fabs(p.a[i]), b = fabs(p.b[i]), c = fabs(p.c[i]);
+    const double growth = a + 3 * b * M * M + 5 * c * M * M * M * M;
+    const double t = (b + 2 * c * M * M) * 2 * M;
+    double most = 15 - log2(growth > 1 ? growth : 1);
+    const double by_t = 15 - log2(t > 1e-30 ? t : 1e-30) - (p.be[i] - p.xe[i]);
+    if (by_t < most) most = by_t;
+    target[i] = (int)floor(most) < 12 ? (int)floor(most) : 12;
+    se[i] = store_exp(pow2(target[i]) * 2 * M);
+  }
+}
+
+// A call for small matrices: one launch.
+cudaError_t small(const Plan& p, const void* G, const void* dY, void* out, Forward& f, int* status,
+                  LaunchLog& log) {
+  SmallArgs g = {};
+  g.g = G;
+  g.dy = dY;
+  g.y = out;
+  g.info = f.info;
+  g.status = status;
+  g.wait_ns = wait_limit_ns();
+  g.L = p.L; g.p = p.p; g.q = p.q; g.tall = p.tall; g.steps = p.steps; g.keep = p.keep;
+  g.eps = p.eps;
+  int target[kMaxSteps], se[kMaxSteps];
+  backward_scales(p, target, se);
+  g.x_terms = 1;
+  for (int i = 0; i < p.steps; ++i) {
+    const int te = p.be[i] - p.xe[i], out_exp = i + 1 < p.steps ? p.xe[i + 1] : 0;
+    if (p.xt[i] > g.x_terms) g.x_terms = p.xt[i];
+    g.xt[i] = p.xt[i];
+    g.xe[i] = p.xe[i];
+    g.to_a[i] = pow2(p.ae[i] - 2 * p.xe[i]);
+    g.to_b[i] = p.c[i] * pow2(p.be[i] - 2 * p.ae[i]);
+    g.a_to_b[i] = p.b[i] * pow2(p.be[i] - p.ae[i]);
+    g.to_x[i] = pow2(out_exp - p.be[i] - p.xe[i]);
+    g.x_to_x[i] = p.a[i] * pow2(out_exp - p.xe[i]);
+    g.to_s[i] = pow2(se[i] - p.xe[i]);
+    g.to_t[i] = p.c[i] * pow2(te - p.ae[i] - se[i]);
+    g.s_to_t[i] = p.b[i] * pow2(te - se[i]);
+    g.to_h[i] = pow2(-p.be[i]);
+    g.h_to_h[i] = p.a[i];
+    g.target[i] = i > 0 ? target[i - 1] : 12;
+  }
+  g.target[p.steps] = target[p.steps - 1];
+  const auto half = CU_TENSOR_MAP_DATA_TYPE_FLOAT16;
+  const Mats* from[3] = {&f.X, &f.A, &f.B};
+  CUtensorMap* maps[3] = {g.x_map, g.a_map, g.b_map};
+  for (int k = 0; p.keep && k < 3; ++k)
+    for (int t = 0; t < 2; ++t) {
+      const int slots = t ? from[k]->low_slots : from[k]->slots;
+      if (slots && !make_map(&maps[k][t], half, 2, t ? from[k]->lo : from[k]->hi, (long long)slots * p.L, p.p,
+                             from[k]->cols, from[k]->ld, kTile))
+        return cudaErrorUnknown;
+    }
+  return launch_small(g, p.bf16, dY != nullptr, log);
+}
+
 cudaError_t forward(const Plan& p, const void* G, void* Y, Forward& w, LaunchLog& log) {
+  if (small_fits(p.p, p.q, p.bf16)) return small(p, G, nullptr, Y, w, w.status, log);
   Chain c(p, w.status, w.counters, w.info);
   c.use(w.X);
   c.use(w.A);
@@ -773,19 +822,9 @@ cudaError_t forward(const Plan& p, const void* G, void* Y, Forward& w, LaunchLog
 
 cudaError_t backward(const Plan& p, const void* G, const void* dY, void* dG, Forward& f, Backward& w,
                      LaunchLog& log) {
-  // H's norm is brought to 2^target: every entry of H, S, T and of the next H stays below
-  // 2^15 whatever their directions
+  if (small_fits(p.p, p.q, p.bf16)) return small(p, G, dY, dG, f, w.status, log);
   int target[kMaxSteps], se[kMaxSteps];
-  for (int i = 0; i < p.steps; ++i) {
-    const double M = p.M[i], a = fabs(p.a[i]), b = fabs(p.b[i]), c = fabs(p.c[i]);
-    const double growth = a + 3 * b * M * M + 5 * c * M * M * M * M;
-    const double t = (b + 2 * c * M * M) * 2 * M;
-    double most = 15 - log2(growth > 1 ? growth : 1);
-    const double by_t = 15 - log2(t > 1e-30 ? t : 1e-30) - (p.be[i] - p.xe[i]);
-    if (by_t < most) most = by_t;
-    target[i] = (int)floor(most) < 12 ? (int)floor(most) : 12;
-    se[i] = store_exp(pow2(target[i]) * 2 * M);
-  }
+  backward_scales(p, target, se);
   const int top = p.steps - 1, terms = p.bf16 ? 1 : 2;
   Chain c(p, w.status, w.counters, f.info);
   for (Mats* m : {&f.X, &f.A, &f.B, &w.H, &w.S, &w.T}) c.use(*m);

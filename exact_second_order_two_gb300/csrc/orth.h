@@ -82,6 +82,28 @@ inline long long tiles_of(int rows, int cols, bool sym, int wide) {  // of one m
 
 cudaError_t launch_chain(const ChainArgs& g, LaunchLog& log);
 
+// A small matrix's steps, or their gradient, in one block (orth_small.cu).  Factors of
+// each step: A = to_a acc, B = to_b acc + a_to_b A, X' = to_x acc + x_to_x X; S = to_s acc,
+// T = to_t acc + s_to_t S, H' = to_h acc + h_to_h H, H' brought to 2^target[step] and dY to
+// 2^target[steps].
+struct SmallArgs {
+  CUtensorMap x_map[2], a_map[2], b_map[2];  // kept: [step][matrix]
+  const void *g, *dy;
+  void* y;  // or dG
+  MatInfo* info;
+  int* status;
+  unsigned long long wait_ns;
+  int L, p, q, tall, steps, keep;
+  float eps;
+  int x_terms;                               // most of X in a step
+  int xt[kMaxSteps], xe[kMaxSteps];
+  float to_a[kMaxSteps], to_b[kMaxSteps], a_to_b[kMaxSteps], to_x[kMaxSteps], x_to_x[kMaxSteps];
+  float to_s[kMaxSteps], to_t[kMaxSteps], s_to_t[kMaxSteps], to_h[kMaxSteps], h_to_h[kMaxSteps];
+  int target[kMaxSteps + 1];
+};
+bool small_fits(int p, int q, bool bf16);
+cudaError_t launch_small(const SmallArgs& g, bool bf16, bool backward, LaunchLog& log);
+
 // Launches a kernel that may start while the one before it in the stream ends; it
 // waits for that one's results by after_previous().
 template <typename... P, typename... A>
@@ -120,6 +142,33 @@ __device__ __forceinline__ int rescaling(float nu2, int target) {
   int e;
   frexpf(nu2, &e);  // nu2 < 2^e
   return target - ((e + 1) >> 1);
+}
+
+// A matrix's scales from its sum of squares; returns what G is multiplied by to be X_0's
+// terms, stored at 2^x_exp.
+__device__ __forceinline__ float info_of(float nu2, float eps, int x_exp, MatInfo& r) {
+  r.norm = sqrtf(nu2);
+  r.s = 1.f / (r.norm + eps);
+  if (r.s > 0.f && r.s < 3.0e38f) {
+    int e;
+    r.f = 2.f * frexpf(r.s, &e);  // s = f 2^(e - 1)
+    r.k = e - 1;
+    return ldexpf(1.f, r.k + x_exp);
+  }
+  // an infinite or NaN norm, or 0 and eps = 0: zeros and NaN as s G gives them
+  r.f = 1.f;
+  r.k = 0;
+  return r.s;
+}
+
+// dG = by_h H_0 - by_g G, for H_0 stored at 2^exp and its product with X_0's terms: s (H_0 -
+// G <H_0, G> s / norm).  A zero matrix has no direction to take off.
+__device__ __forceinline__ void end_factors(const MatInfo& r, float dot, int exp, int x_exp, float& by_h,
+                                            float& by_g) {
+  const double along = r.norm > 0.f ? ldexp((double)dot, -(r.k + x_exp)) * r.s / r.norm : 0.0;
+  const double scale = ldexp((double)r.s, -exp);
+  by_h = (float)scale;
+  by_g = (float)(scale * along);
 }
 #endif
 

@@ -75,13 +75,13 @@ def model(G, dY, polynomials, eps=1e-7):
 
 
 def check(got, want, modelled, dtype):
-    """In the Frobenius norm of each matrix: twice the documented roundings' own error, the
-    result's rounding, and what fp32 sums of up to 2048 products of 16 lose (2^-24 each)
-    through 15 products: 2^-16 at worst."""
-    err, own, size = (torch.linalg.matrix_norm(t) for t in (got.double() - want, modelled.double() - want, want))
+    """In the Frobenius norm of the whole stack: twice the documented roundings' own error
+    (the same number of roundings at other places: over 1000 entries and more their norms
+    agree to a tenth), the result's rounding, and what fp32 sums of up to 2048 products of 16
+    lose (2^-24 each) through 15 products: 2^-16 at worst."""
+    err, own, size = ((t.double()).norm() for t in (got.double() - want, modelled.double() - want, want))
     limit = 2 * own + (torch.finfo(dtype).eps / 2 + 2.0 ** -16) * size
-    assert torch.isfinite(got).all() and (err <= limit).all(), \
-        ((err / size).max().item(), (limit / size).max().item())
+    assert torch.isfinite(got).all() and err <= limit, ((err / size).item(), (limit / size).item())
 
 
 def gradient(shape, dtype, seed=0, std=1e-3):
@@ -95,9 +95,10 @@ def gradient(shape, dtype, seed=0, std=1e-3):
     return (std * x).to(dtype), dY.to(dtype)
 
 
-SHAPES = [(1, 1), (1, 37), (37, 1), (3, 2, 5), (16, 64, 64), (65, 63), (2, 3, 30, 100), (128, 128),
+SHAPES = [(1, 1), (40, 1, 37), (40, 37, 1), (300, 2, 5), (16, 64, 64), (65, 63), (2, 3, 30, 100), (128, 128),
           (129, 257), (2, 333, 127), (130, 1000), (1000, 130), (256, 256), (300, 300), (515, 519),
-          (700, 100), (3, 384, 1152), (1024, 640)]
+          (700, 100), (3, 384, 1152), (1024, 640),
+          (128, 256), (129, 90), (200, 3, 17), (128, 200), (256, 64), (5, 129, 128), (257, 128)]
 
 
 class TestValues:
