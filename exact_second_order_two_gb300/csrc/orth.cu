@@ -435,10 +435,20 @@ int make_plan(const fbob_orth_t* o, Plan* out) {
     p.xe[i] = store_exp(M);
     p.ae[i] = store_exp(M * M);
     p.be[i] = store_exp(fabs(b) * M * M + fabs(c) * M * M * M * M);
-    double most = 0;  // of the polynomial up to M, which rounding may pass a little
-    for (int k = 0; k <= 1024; ++k) {
-      const double x = 1.01 * M * k / 1024, y = fabs(x * (a + x * x * (b + x * x * c)));
-      if (y > most) most = y;
+    // the polynomial's most up to M, which rounding may pass a little: at the end, or
+    // where a + 3 b t + 5 c t^2 = 0, t = x^2
+    const double end = 1.01 * M, root = 9 * b * b - 20 * a * c;
+    double at[3] = {end, 0, 0}, most = 0;
+    if (c != 0 && root >= 0) {
+      at[1] = sqrt(fmax(0.0, (-3 * b + sqrt(root)) / (10 * c)));
+      at[2] = sqrt(fmax(0.0, (-3 * b - sqrt(root)) / (10 * c)));
+    } else if (c == 0 && b != 0) {
+      at[1] = sqrt(fmax(0.0, -a / (3 * b)));
+    }
+    for (double x : at) {
+      if (x > end) continue;
+      const double y = fabs(x * (a + x * x * (b + x * x * c)));
+      if (!(y <= most)) most = y;
     }
     M = 1.01 * most;
     if (!(M < 64.0)) return FBOB_ERR_INVALID_ARG;  // singular values that run away

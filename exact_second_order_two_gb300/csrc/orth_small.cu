@@ -27,7 +27,7 @@ namespace fbob {
 namespace orth {
 namespace {
 
-constexpr int kThreads = 256;
+constexpr int kThreads = 512;  // a warp to 32 rows and 32 columns of a square result
 constexpr int kSquare = 2;  // tiles (64 columns) of A, B, S and T
 
 // A matrix in shared memory: `terms` times `tiles` tiles.
@@ -212,7 +212,7 @@ __global__ void __launch_bounds__(kThreads, 1) small_forward(const __grid_consta
   if (l == 0 && threadIdx.x == 0) *g.status = 0;
   begin_block(sh, cols, g);
   const uint32_t acc = sh->tmem;
-  const int row = 32 * ((threadIdx.x >> 5) & 3) + (threadIdx.x & 31), side = threadIdx.x >> 7;
+  const int row = 32 * ((threadIdx.x >> 5) & 3) + (threadIdx.x & 31), unit = threadIdx.x >> 7;
   const T* x = static_cast<const T*>(g.g) + (size_t)l * g.p * g.q;
   MatInfo info;
   const float factor = info_of(squares(x, g.p * g.q, sh->red), g.eps, g.xe[0], info);
@@ -241,24 +241,20 @@ __global__ void __launch_bounds__(kThreads, 1) small_forward(const __grid_consta
     product(X, X, false, tiles, [&] {
       if (g.keep) store_held(&g.x_map[0], g.xt[i] == 2 ? &g.x_map[1] : nullptr, X, i * g.L + l, g.q, g.p);
     });
-    for (int u = 2 * side; u < 2 * side + 2; ++u) {
-      read_acc(acc, u, f * f * g.to_a[i], v);
-      put(v, A, TERMS, row, u);
-    }
+    read_acc(acc, unit, f * f * g.to_a[i], v);
+    put(v, A, TERMS, row, unit);
     product(A, A, false, deep, [&] {
       if (g.keep) store_held(&g.a_map[0], TERMS == 2 ? &g.a_map[1] : nullptr, A, i * g.L + l, g.p, g.p);
     });
-    for (int u = 2 * side; u < 2 * side + 2; ++u) {
-      read_acc(acc, u, g.to_b[i], v);
-      add_slot(v, A.tile(0, u >> 1), row, u & 1, g.a_to_b[i]);
-      if (TERMS == 2) add_slot(v, A.tile(1, u >> 1), row, u & 1, g.a_to_b[i]);
-      put(v, A, TERMS, row, u);
-    }
+    read_acc(acc, unit, g.to_b[i], v);
+    add_slot(v, A.tile(0, unit >> 1), row, unit & 1, g.a_to_b[i]);
+    if (TERMS == 2) add_slot(v, A.tile(1, unit >> 1), row, unit & 1, g.a_to_b[i]);
+    put(v, A, TERMS, row, unit);
     product(A, X, true, deep, [&] {
       if (g.keep) store_held(&g.b_map[0], TERMS == 2 ? &g.b_map[1] : nullptr, A, i * g.L + l, g.p, g.p);
     });
     const bool last = i + 1 == g.steps;
-    for (int u = side; u < 2 * tiles; u += 2) {
+    for (int u = unit; u < 2 * tiles; u += 4) {
       read_acc(acc, u, f * g.to_x[i], v);
       add_slot(v, X.tile(0, u >> 1), row, u & 1, f * g.x_to_x[i]);
       if (g.xt[i] == 2) add_slot(v, X.tile(1, u >> 1), row, u & 1, f * g.x_to_x[i]);
@@ -294,7 +290,7 @@ __global__ void __launch_bounds__(kThreads, 1) small_backward(const __grid_const
   if (l == 0 && threadIdx.x == 0) *g.status = 0;
   begin_block(sh, cols, g);
   const uint32_t acc = sh->tmem;
-  const int row = 32 * ((threadIdx.x >> 5) & 3) + (threadIdx.x & 31), side = threadIdx.x >> 7;
+  const int row = 32 * ((threadIdx.x >> 5) & 3) + (threadIdx.x & 31), unit = threadIdx.x >> 7;
   const int deep = (g.p + 63) / 64;
   const T* dy = static_cast<const T*>(g.dy) + (size_t)l * g.p * g.q;
   const MatInfo info = g.info[l];
@@ -331,10 +327,8 @@ __global__ void __launch_bounds__(kThreads, 1) small_backward(const __grid_const
       multiply_terms<TERMS>(acc, X, H, false, tiles, begun);
     });
     if (threadIdx.x == 0) load(g.a_map, A, kSquare, i);
-    for (int u = 2 * side; u < 2 * side + 2; ++u) {
-      read_acc(acc, u, f * g.to_s[i], v);
-      put(v, S, TERMS, row, u);
-    }
+    read_acc(acc, unit, f * g.to_s[i], v);
+    put(v, S, TERMS, row, unit);
     loaded();
     product([&] {
       begun = false;
@@ -342,12 +336,10 @@ __global__ void __launch_bounds__(kThreads, 1) small_backward(const __grid_const
       multiply_terms<TERMS>(acc, S, A, false, deep, begun);
     });
     if (threadIdx.x == 0) load(g.b_map, A, kSquare, i);
-    for (int u = 2 * side; u < 2 * side + 2; ++u) {  // T in S's place
-      read_acc(acc, u, f * g.to_t[i], v);
-      add_slot(v, S.tile(0, u >> 1), row, u & 1, f * g.s_to_t[i]);
-      if (TERMS == 2) add_slot(v, S.tile(1, u >> 1), row, u & 1, f * g.s_to_t[i]);
-      put(v, S, TERMS, row, u);
-    }
+    read_acc(acc, unit, f * g.to_t[i], v);  // T in S's place
+    add_slot(v, S.tile(0, unit >> 1), row, unit & 1, f * g.s_to_t[i]);
+    if (TERMS == 2) add_slot(v, S.tile(1, unit >> 1), row, unit & 1, f * g.s_to_t[i]);
+    put(v, S, TERMS, row, unit);
     loaded();
     begun = false;
     product([&] { multiply_terms<TERMS>(acc, A, H, true, deep, begun); });
@@ -358,7 +350,7 @@ __global__ void __launch_bounds__(kThreads, 1) small_backward(const __grid_const
     exp += shift;
     const float alpha = ldexpf(g.to_h[i], shift), beta = ldexpf(g.h_to_h[i], shift);
     float sum = 0.f;
-    for (int u = side; u < 2 * tiles; u += 2) {
+    for (int u = unit; u < 2 * tiles; u += 4) {
       read_acc(acc, u, alpha, v);
       add_slot(v, H.tile(0, u >> 1), row, u & 1, beta);
       if (TERMS == 2) add_slot(v, H.tile(1, u >> 1), row, u & 1, beta);

@@ -9,6 +9,7 @@ passes to what the update was computed from.
 """
 from __future__ import annotations
 
+import ctypes
 import functools
 import math
 import operator
@@ -22,9 +23,8 @@ from . import _binding as _b
 QUINTIC = (3.4445, -4.7750, 2.0315)
 
 
-@functools.lru_cache(maxsize=64)
 def _coefficients(steps, polynomials):
-    """The steps' a, b, c as a C array (kept alive by the cache's callers)."""
+    """The steps' a, b, c as a C array."""
     if len(polynomials) == 1:
         polynomials = polynomials * steps
     if len(polynomials) != steps:
@@ -32,31 +32,43 @@ def _coefficients(steps, polynomials):
     flat = [float(x) for abc in polynomials for x in abc]
     if len(flat) != 3 * steps or not all(math.isfinite(x) for x in flat):
         raise ValueError("a polynomial is three finite numbers a, b, c of a x + b x^3 + c x^5")
-    return (_b.ctypes.c_float * len(flat))(*flat)
+    return (ctypes.c_float * len(flat))(*flat)
 
 
-def _problem(g, steps, polynomials, eps, keep):
+@functools.lru_cache(maxsize=256)
+def _problem(shape, dtype, steps, polynomials, eps, keep):
+    """The C description of a call on tensors of ``shape``, and its workspaces' bytes
+    (forward, backward)."""
     coefficients = _coefficients(steps, polynomials)
-    m, n = g.shape[-2:]
-    o = _b.Orth(math.prod(g.shape[:-2]), m, n, _b.DTYPES[g.dtype], steps, int(keep), eps,
-                _b.ctypes.addressof(coefficients))
-    return o, coefficients
-
-
-def _workspace(op, o, device):
-    size = _b.lib().fbob_orth_workspace_size(op, _b.ctypes.byref(o))
-    if size == 0:
-        raise _b.FbobError(2, "fbob_orth_workspace_size")
-    return torch.empty(size, dtype=torch.uint8, device=device)
+    o = _b.Orth(math.prod(shape[:-2]), shape[-2], shape[-1], _b.DTYPES[dtype], steps, int(keep), eps,
+                ctypes.addressof(coefficients))
+    o.held = coefficients  # lives as long as its address is used
+    ref = ctypes.byref(o)
+    sizes = tuple(_b.lib().fbob_orth_workspace_size(op, ref) for op in (_b.OP_FORWARD, _b.OP_BACKWARD))
+    if 0 in sizes:
+        raise _b.FbobError(2, "orthogonalize")
+    return ref, sizes
 
 
 def _forward(g, how, keep):
-    o, coefficients = _problem(g, *how, keep)
-    y = torch.empty(g.shape, dtype=g.dtype, device=g.device)
-    ws = _workspace(_b.OP_FORWARD, o, g.device)
-    _b.call_on(g.device, "fbob_orth_forward", _b.lib().fbob_orth_forward, _b.ctypes.byref(o),
-               g.data_ptr(), y.data_ptr(), ws.data_ptr(), ws.numel())
+    ref, sizes = _problem(g.shape, g.dtype, *how, keep)
+    dev = g.device
+    y = torch.empty(g.shape, dtype=g.dtype, device=dev)
+    ws = torch.empty(sizes[0], dtype=torch.uint8, device=dev)
+    _b.call_on(dev, "fbob_orth_forward", _b.lib().fbob_orth_forward, ref, g.data_ptr(), y.data_ptr(),
+               ws.data_ptr(), sizes[0])
     return y, ws
+
+
+def _backward(g, kept, dy, how):
+    ref, sizes = _problem(g.shape, g.dtype, *how, True)
+    dev = g.device
+    dy = dy.contiguous()
+    dg = torch.empty(g.shape, dtype=g.dtype, device=dev)
+    ws = torch.empty(sizes[1], dtype=torch.uint8, device=dev)
+    _b.call_on(dev, "fbob_orth_backward", _b.lib().fbob_orth_backward, ref, g.data_ptr(), dy.data_ptr(),
+               dg.data_ptr(), kept.data_ptr(), sizes[0], ws.data_ptr(), sizes[1])
+    return dg
 
 
 class _Orthogonalize(torch.autograd.Function):
@@ -68,18 +80,23 @@ class _Orthogonalize(torch.autograd.Function):
         return y
 
     @staticmethod
-    @torch.autograd.function.once_differentiable
     def backward(ctx, dy):
         g, kept = ctx.saved_tensors
-        _b.refuse_dual("orthogonalize's derivative", dy)
-        dy = dy.contiguous()
-        o, coefficients = _problem(g, *ctx.how, True)
-        dg = torch.empty(g.shape, dtype=g.dtype, device=g.device)
-        ws = _workspace(_b.OP_BACKWARD, o, g.device)
-        _b.call_on(g.device, "fbob_orth_backward", _b.lib().fbob_orth_backward, _b.ctypes.byref(o),
-                   g.data_ptr(), dy.data_ptr(), dg.data_ptr(), kept.data_ptr(), kept.numel(),
-                   ws.data_ptr(), ws.numel())
-        return dg, None
+        if torch.is_grad_enabled() or _b.dual(dy):
+            return _OrthogonalizeBackward.apply(g, dy, kept, ctx.how), None
+        return _backward(g, kept, dy, ctx.how), None
+
+
+class _OrthogonalizeBackward(torch.autograd.Function):
+    """(g, dY) -> dG, of which no further derivative is known."""
+
+    @staticmethod
+    def forward(ctx, g, dy, kept, how):
+        return _backward(g, kept, dy, how)
+
+    @staticmethod
+    def backward(ctx, *grads):
+        raise NotImplementedError("orthogonalize has no second derivative")
 
 
 def orthogonalize(g: torch.Tensor, steps: int = 5, coefficients=QUINTIC,
@@ -103,16 +120,16 @@ def orthogonalize(g: torch.Tensor, steps: int = 5, coefficients=QUINTIC,
         raise ValueError("g must be a matrix or a stack of matrices")
     if g.dtype not in _b.DTYPES:
         raise TypeError(f"unsupported dtype {g.dtype}; use bfloat16 or float32")
+    if 0 in g.shape:
+        raise _b.FbobError(1, "orthogonalize: g must not be empty")
     steps = operator.index(steps)
     if not 1 <= steps <= 16:
         raise ValueError(f"steps must be from 1 to 16, got {steps}")
     if not (eps >= 0 and math.isfinite(eps)):
         raise ValueError(f"eps must be at least 0 and finite, got {eps}")
-    if coefficients is not QUINTIC:
-        coefficients = tuple(coefficients)
-    polynomials = coefficients if isinstance(coefficients[0], (tuple, list)) else (coefficients,)
-    how = (steps, tuple(tuple(p) for p in polynomials), float(eps))
-    _coefficients(*how[:2])
+    if not isinstance(coefficients[0], (tuple, list)):
+        coefficients = (coefficients,)
+    how = (steps, tuple(map(tuple, coefficients)), float(eps))
     g = g.contiguous()
     if (torch.is_grad_enabled() and g.requires_grad) or _b.dual(g):
         return _Orthogonalize.apply(g, how)

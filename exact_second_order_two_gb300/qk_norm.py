@@ -10,6 +10,7 @@ which a MAML step takes, are one pass over the rows each, and a small sum.
 """
 from __future__ import annotations
 
+import functools
 import math
 import struct
 
@@ -43,8 +44,8 @@ def _like(x):
     heads of: [B, N, H, d] where its heads lie within its positions."""
     B, H, N, d = x.shape
     if x.stride(2) > x.stride(1):
-        return torch.empty((B, N, H, d), dtype=x.dtype, device=x.device).transpose(1, 2)
-    return torch.empty((B, H, N, d), dtype=x.dtype, device=x.device)
+        return torch.empty_strided(x.shape, (N * H * d, d, H * d, 1), dtype=x.dtype, device=x.device)
+    return torch.empty(x.shape, dtype=x.dtype, device=x.device)
 
 
 def _side(x, w, y, dy=None, a=None, c=None, dw=None, ddy=None):
@@ -62,10 +63,15 @@ def _forward(q, k, wq, wk, inv_freq, positions, problem, dtype):
     return yq, yk
 
 
+@functools.lru_cache(maxsize=64)
+def _workspace_size(problem):
+    return _b.lib().fbob_qk_norm_workspace_size(problem)
+
+
 def _derivative(name, problem, sides, inv_freq, positions, sums, device):
     """A backward call on one or two sides; sums: whether it writes a weight's
     gradient."""
-    n = _b.lib().fbob_qk_norm_workspace_size(problem) if sums else 0
+    n = _workspace_size(problem) if sums else 0
     ws = torch.empty(n, dtype=torch.uint8, device=device) if sums else None
     _b.call_on(device, name, getattr(_b.lib(), name), problem, sides[0],
                sides[1] if len(sides) > 1 else None, _ptr(inv_freq), _ptr(positions), _ptr(ws), n)
@@ -81,7 +87,7 @@ def _backward(xs, ws, dys, inv_freq, positions, problem, wanted):
         dy = _rows(dy)
         out[i] = _like(x)
         if w is not None and wanted[i]:
-            out[2 + i] = torch.empty_like(w)
+            out[2 + i] = torch.empty(w.shape, dtype=w.dtype, device=w.device)
             sums = True
         sides.append(_side(x, w, out[i], dy, dw=out[2 + i]))
     if sides:
@@ -132,7 +138,7 @@ class _QkNormBackward(torch.autograd.Function):
             c = None if c is None else c.contiguous()
             out[i], out[4 + i] = _like(x), torch.empty(dy.shape, dtype=dy.dtype, device=dy.device)
             if w is not None and ctx.needs_input_grad[2 + i]:
-                out[2 + i] = torch.empty_like(w)
+                out[2 + i] = torch.empty(w.shape, dtype=w.dtype, device=w.device)
                 sums = True
             sides.append(_side(x, w, out[i], dy, a, c, out[2 + i], out[4 + i]))
         if sides:

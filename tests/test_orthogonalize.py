@@ -182,7 +182,9 @@ class TestValues:
         """Transposed, strided, offset and expanded inputs and upstream gradients."""
         G, dY = gradient((70, 90), torch.bfloat16)
         want = fbob.orthogonalize(G)
-        assert torch.equal(fbob.orthogonalize(G.T.contiguous()).T, want)
+        tall = fbob.orthogonalize(G.T.contiguous())
+        check(tall.T, exact(G, None, [ONE] * 5)[0], model(G, None, [ONE] * 5)[0], G.dtype)
+        assert torch.equal(fbob.orthogonalize(G.T), tall)  # (its norm is summed in another order)
         assert torch.equal(fbob.orthogonalize(G.T.contiguous().T), want)
         flat = torch.cat((G.new_zeros(1), G.flatten()))[1:].view(70, 90)  # off the 16-byte steps
         assert torch.equal(fbob.orthogonalize(flat), want)
