@@ -20,6 +20,7 @@
 #include <cuda_bf16.h>
 #include <cuda_runtime.h>
 #include <stdint.h>
+#include <type_traits>
 
 #include "common.cuh"
 #include "internal.h"
@@ -197,11 +198,21 @@ __device__ __forceinline__ void from_shared(Row<P, C>& r, const float* v, const 
 
 enum { kForward, kBackward, kSecond };
 
+// A block's sums over rows, from those of its groups of lanes.
+__device__ __forceinline__ void block_partial(const float* red, const NormArgs& a, bool second_side, int block,
+                                              int per_block) {
+  __syncthreads();
+  float* const out = a.partial + ((size_t)(second_side && a.side[0].sums ? a.side[0].blocks : 0) + block) * a.d;
+  for (int i = threadIdx.x; i < a.d; i += kThreads) {
+    float t = 0.f;
+    for (int k = 0; k < per_block; ++k) t += red[k * a.d + i];
+    out[i] = t;
+  }
+}
+
 // Rows whose loads are in flight together.
-template <int OP, typename TI, typename TO, int P, int C>
-constexpr int kRows = C > 1 ? 1 : OP == kForward ? (sizeof(TI) == 2 ? 4 : 2)
-                              : OP == kBackward  ? 2
-                                                 : 1;
+template <int OP, int C>
+constexpr int kRows = C > 1 || OP != kForward ? 1 : 2;
 
 // Shared memory: [half] angles of one position, [d] w, [d] c; then, for the sums
 // at the end, [rows of a block][d].
@@ -210,7 +221,7 @@ __global__ void __launch_bounds__(kThreads) norm_kernel(const __grid_constant__ 
   extern __shared__ unsigned long long turns[];
   float* const sw = reinterpret_cast<float*>(turns + a.half);
   float* const sc = sw + a.d;
-  constexpr int U = kRows<OP, TI, TO, P, C>;
+  constexpr int U = kRows<OP, C>;
   const bool second_side = blockIdx.x >= (unsigned)a.side[0].blocks;
   const Side& s = a.side[second_side];
   const int block = blockIdx.x - (second_side ? a.side[0].blocks : 0);
@@ -345,13 +356,338 @@ __global__ void __launch_bounds__(kThreads) norm_kernel(const __grid_constant__ 
     if (place.one[j]) red[group * a.d + place.e0[j] + i] = acc.u[j][i];
     if (place.two[j]) red[group * a.d + place.e1[j] + i] = acc.v[j][i];
   }
-  __syncthreads();
-  float* const out = a.partial + ((size_t)(second_side && a.side[0].sums ? a.side[0].blocks : 0) + block) * a.d;
-  for (int i = threadIdx.x; i < a.d; i += kThreads) {
-    float t = 0.f;
-    for (int k = 0; k < per_block; ++k) t += red[k * a.d + i];
-    out[i] = t;
+  block_partial(red, a, second_side, block, per_block);
+}
+
+
+// ---------------------------------------------------------------------------
+// Rows in chunks of 16 features, aligned: most heads.  Arithmetic is in pairs of
+// features; weights are read from shared memory where a row needs them, which leaves
+// registers for rows in flight (with everything in registers, one feature at a time, 12
+// warps fitted an SM and 32 heads x 8192 x 128, bf16, took 39 us forward, 53 backward
+// and 121 for the second derivative).
+// ---------------------------------------------------------------------------
+using f2 = float2;
+__device__ __forceinline__ f2 fma2(f2 a, f2 b, f2 c) { return __ffma2_rn(a, b, c); }
+__device__ __forceinline__ f2 mul2(f2 a, f2 b) { return __fmul2_rn(a, b); }
+__device__ __forceinline__ f2 both(float a) { return f2{a, a}; }
+
+struct Half {  // 8 features
+  f2 p[4];
+};
+struct Pair16 {  // the two runs of a chunk
+  Half u, v;
+};
+
+template <typename T>
+struct Raw16;
+template <>
+struct Raw16<__nv_bfloat16> {
+  uint4 a, b;
+  __device__ __forceinline__ void load(const __nv_bfloat16* p, int e0, int e1) {
+    a = *reinterpret_cast<const uint4*>(p + e0);
+    b = *reinterpret_cast<const uint4*>(p + e1);
   }
+  static __device__ __forceinline__ void wide(const uint4& x, Half& h) {
+    const uint32_t w[4] = {x.x, x.y, x.z, x.w};
+#pragma unroll
+    for (int i = 0; i < 4; ++i)
+      h.p[i] = f2{__uint_as_float(w[i] << 16), __uint_as_float(w[i] & 0xffff0000u)};
+  }
+  __device__ __forceinline__ void get(Pair16& r) const {
+    wide(a, r.u);
+    wide(b, r.v);
+  }
+};
+template <>
+struct Raw16<float> {
+  float4 a[2], b[2];
+  __device__ __forceinline__ void load(const float* p, int e0, int e1) {
+#pragma unroll
+    for (int i = 0; i < 2; ++i) {
+      a[i] = reinterpret_cast<const float4*>(p + e0)[i];
+      b[i] = reinterpret_cast<const float4*>(p + e1)[i];
+    }
+  }
+  __device__ __forceinline__ void get(Pair16& r) const {
+#pragma unroll
+    for (int i = 0; i < 2; ++i) {
+      r.u.p[2 * i] = f2{a[i].x, a[i].y};
+      r.u.p[2 * i + 1] = f2{a[i].z, a[i].w};
+      r.v.p[2 * i] = f2{b[i].x, b[i].y};
+      r.v.p[2 * i + 1] = f2{b[i].z, b[i].w};
+    }
+  }
+};
+__device__ __forceinline__ void put8(__nv_bfloat16* p, const Half& h) {
+  __nv_bfloat162 t[4];
+#pragma unroll
+  for (int i = 0; i < 4; ++i) t[i] = __floats2bfloat162_rn(h.p[i].x, h.p[i].y);
+  *reinterpret_cast<uint4*>(p) = *reinterpret_cast<const uint4*>(t);
+}
+__device__ __forceinline__ void put8(float* p, const Half& h) {
+#pragma unroll
+  for (int i = 0; i < 2; ++i)
+    reinterpret_cast<float4*>(p)[i] = make_float4(h.p[2 * i].x, h.p[2 * i].y, h.p[2 * i + 1].x, h.p[2 * i + 1].y);
+}
+__device__ __forceinline__ Half shared8(const float* p) {
+  Half h;
+#pragma unroll
+  for (int i = 0; i < 2; ++i) {
+    const float4 t = reinterpret_cast<const float4*>(p)[i];
+    h.p[2 * i] = f2{t.x, t.y};
+    h.p[2 * i + 1] = f2{t.z, t.w};
+  }
+  return h;
+}
+
+__device__ __forceinline__ float dot16(const Pair16& a, const Pair16& b) {
+  f2 s = mul2(a.u.p[0], b.u.p[0]), t = mul2(a.v.p[0], b.v.p[0]);
+#pragma unroll
+  for (int i = 1; i < 4; ++i) {
+    s = fma2(a.u.p[i], b.u.p[i], s);
+    t = fma2(a.v.p[i], b.v.p[i], t);
+  }
+  return (s.x + t.x) + (s.y + t.y);
+}
+
+// Cosines and sines of a chunk's eight pairs; a chunk that is not turned has 1 and 0.
+struct Turn8 {
+  float cs[8], sn[8];
+  // r turned: half layout pairs u[i] with v[i], interleaved neighbours in a run
+  template <bool INTERLEAVED, bool INVERSE>
+  __device__ __forceinline__ void apply(Pair16& r) const {
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      if (INTERLEAVED) {
+#pragma unroll
+        for (int k = 0; k < 2; ++k) {
+          f2& x = k ? r.v.p[i] : r.u.p[i];
+          const float c = cs[4 * k + i], s = INVERSE ? -sn[4 * k + i] : sn[4 * k + i];
+          x = f2{fmaf(x.x, c, -x.y * s), fmaf(x.x, s, x.y * c)};
+        }
+      } else {
+        const f2 c = {cs[2 * i], cs[2 * i + 1]}, s = {sn[2 * i], sn[2 * i + 1]};
+        const f2 u = r.u.p[i], v = r.v.p[i];
+        const f2 uc = mul2(u, c), vc = mul2(v, c);
+        if (INVERSE) {
+          r.u.p[i] = fma2(v, s, uc);
+          r.v.p[i] = f2{fmaf(-u.x, s.x, vc.x), fmaf(-u.y, s.y, vc.y)};
+        } else {
+          r.u.p[i] = f2{fmaf(-v.x, s.x, uc.x), fmaf(-v.y, s.y, uc.y)};
+          r.v.p[i] = fma2(u, s, vc);
+        }
+      }
+    }
+  }
+};
+
+// Rows whose loads are in flight together, and blocks an SM is to hold.
+template <int OP, typename TI, typename TO>
+constexpr int kFlight = OP == kForward ? (sizeof(TI) == 2 ? 4 : 2) : OP == kBackward ? 2 : 1;
+template <int OP>
+constexpr int kResident = OP == kForward ? 5 : 3;
+
+template <int OP, typename TI, typename TO, bool INTERLEAVED>
+__global__ void __launch_bounds__(kThreads, kResident<OP>) norm_rows(const __grid_constant__ NormArgs a) {
+  extern __shared__ __align__(16) unsigned long long turns[];
+  float* const sw = reinterpret_cast<float*>(turns + ((a.half + 1) & ~1));
+  float* const sc = sw + a.d;
+  constexpr int U = kFlight<OP, TI, TO>;
+  const bool second_side = blockIdx.x >= (unsigned)a.side[0].blocks;
+  const Side& s = a.side[second_side];
+  const int block = blockIdx.x - (second_side ? a.side[0].blocks : 0);
+  const int lane = threadIdx.x & (a.lanes - 1), group = threadIdx.x / a.lanes;
+  const int per_block = kThreads / a.lanes;  // positions of a unit
+  const int rot = a.half / 8;
+  const bool have = lane < a.d / 16, turned = lane < rot;
+  const int e0 = turned ? (INTERLEAVED ? 16 : 8) * lane : 2 * a.half + (lane - rot) * 16;
+  const int e1 = turned && !INTERLEAVED ? e0 + a.half : e0 + 8;
+
+  turns_table<kThreads>(turns, a.inv_freq, a.half);
+  for (int i = threadIdx.x; i < a.d; i += kThreads) {
+    sw[i] = s.w ? vector_at(s.w, a.w_bf16, i) : 1.f;
+    if (OP == kSecond) sc[i] = s.c ? vector_at(s.c, a.w_bf16, i) : 0.f;
+  }
+  __syncthreads();
+  Pair16 acc;
+#pragma unroll
+  for (int i = 0; i < 4; ++i) acc.u.p[i] = acc.v.p[i] = both(0.f);
+
+  const long long items = (long long)a.B * a.N;
+  for (long long unit = block; unit < s.units; unit += s.blocks) {
+    const long long ib = s.groups == 1 ? unit : unit / s.groups;
+    const int h0 = (int)(unit - ib * s.groups) * s.heads, h1 = min(s.H, h0 + s.heads);
+    const long long item = ib * per_block + group;
+    const bool active = item < items && have;  // the other lanes only take part in exchanges
+    const int b = active ? (int)(item / a.N) : 0, n = active ? (int)(item - (long long)b * a.N) : 0;
+    const TI* x = static_cast<const TI*>(s.x) + b * s.xs[0] + n * s.xs[2] + h0 * s.xs[1];
+    const TO* dy = static_cast<const TO*>(s.dy) + b * s.dys[0] + n * s.dys[2] + h0 * s.dys[1];
+    const TI* ca = static_cast<const TI*>(s.a) + b * s.as[0] + n * s.as[2] + h0 * s.as[1];
+    using TY = typename std::conditional<OP == kForward, TO, TI>::type;
+    TY* y = static_cast<TY*>(s.y) + b * s.ys[0] + n * s.ys[2] + h0 * s.ys[1];
+    TO* ddy = static_cast<TO*>(s.ddy) + b * s.ddys[0] + n * s.ddys[2] + h0 * s.ddys[1];
+    Turn8 t8;
+    for (int hb = h0; hb < h1; hb += U) {
+      Raw16<TI> rx[U], ra[U];
+      Raw16<TO> rdy[U];
+#pragma unroll
+      for (int i = 0; i < U; ++i)
+        if (active && hb + i < h1) {
+          rx[i].load(x, e0, e1);
+          x += s.xs[1];
+          if (OP != kForward) {
+            rdy[i].load(dy, e0, e1);
+            dy += s.dys[1];
+          }
+          if (OP == kSecond && s.a) {
+            ra[i].load(ca, e0, e1);
+            ca += s.as[1];
+          }
+        }
+      if (hb == h0) {
+        const long long p = !active ? 0 : a.positions ? a.positions[b * a.pos_sb + n] : a.offset + n;
+#pragma unroll
+        for (int i = 0; i < 8; ++i) {
+          float sn = 0.f, cs = 1.f;
+          if (turned) {
+            sincos_turns((uint32_t)(((unsigned long long)p * turns[8 * lane + i] + 0x80000000ull) >> 32), sn, cs);
+            sn *= a.magnitude;
+            cs *= a.magnitude;
+          }
+          t8.cs[i] = cs;
+          t8.sn[i] = sn;
+        }
+      }
+#pragma unroll
+      for (int k = 0; k < U; ++k) {
+        if (hb + k >= h1) break;  // the same for the whole block
+        Pair16 xv, g;
+        if (active) {
+          rx[k].get(xv);
+          if (OP != kForward) rdy[k].get(g);
+        } else {
+#pragma unroll
+          for (int i = 0; i < 4; ++i) xv.u.p[i] = xv.v.p[i] = g.u.p[i] = g.v.p[i] = both(0.f);
+        }
+        if (OP == kForward) {
+          float sum[1] = {dot16(xv, xv)};
+          row_sums(sum, a.lanes);
+          const f2 r = both(rsqrtf(fmaf(sum[0], a.inv_d, a.eps)));
+          if (!active) continue;
+          const Half wu = shared8(sw + e0), wv = shared8(sw + e1);
+#pragma unroll
+          for (int i = 0; i < 4; ++i) {
+            xv.u.p[i] = mul2(mul2(r, wu.p[i]), xv.u.p[i]);
+            xv.v.p[i] = mul2(mul2(r, wv.p[i]), xv.v.p[i]);
+          }
+          t8.template apply<INTERLEAVED, false>(xv);
+          put8(y + e0, xv.u);
+          put8(y + e1, xv.v);
+          y += s.ys[1];
+        } else if (OP == kBackward) {
+          t8.template apply<INTERLEAVED, true>(g);
+          Pair16 h;
+          if (have) {
+            const Half wu = shared8(sw + e0), wv = shared8(sw + e1);
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+              h.u.p[i] = mul2(wu.p[i], g.u.p[i]);
+              h.v.p[i] = mul2(wv.p[i], g.v.p[i]);
+            }
+          } else {
+            h = g;
+          }
+          float sum[2] = {dot16(xv, xv), dot16(h, xv)};
+          row_sums(sum, a.lanes);
+          if (!active) continue;
+          const float r = rsqrtf(fmaf(sum[0], a.inv_d, a.eps));
+          // dx = r h - (r^3 <h, x> / d) x
+          const f2 r2 = both(r), back = both(-r * (r * r * sum[1] * a.inv_d));
+#pragma unroll
+          for (int i = 0; i < 4; ++i) {
+            acc.u.p[i] = fma2(g.u.p[i], mul2(r2, xv.u.p[i]), acc.u.p[i]);
+            acc.v.p[i] = fma2(g.v.p[i], mul2(r2, xv.v.p[i]), acc.v.p[i]);
+            xv.u.p[i] = fma2(r2, h.u.p[i], mul2(back, xv.u.p[i]));
+            xv.v.p[i] = fma2(r2, h.v.p[i], mul2(back, xv.v.p[i]));
+          }
+          put8(y + e0, xv.u);
+          put8(y + e1, xv.v);
+          y += s.ys[1];
+        } else {
+          Pair16 av;
+          if (active && s.a) {
+            ra[k].get(av);
+          } else {
+#pragma unroll
+            for (int i = 0; i < 4; ++i) av.u.p[i] = av.v.p[i] = both(0.f);
+          }
+          t8.template apply<INTERLEAVED, true>(g);
+          // <x, x>, <h, x>, <a, x>, <h, a>, <c . g, x>
+          float sum[5] = {dot16(xv, xv), 0.f, dot16(av, xv), 0.f, 0.f};
+          if (have) {
+            f2 hx = both(0.f), ha = both(0.f), cx = both(0.f);
+#pragma unroll
+            for (int run = 0; run < 2; ++run) {
+              const Half w = shared8(sw + (run ? e1 : e0)), c = shared8(sc + (run ? e1 : e0));
+              const Half &gr = run ? g.v : g.u, &xr = run ? xv.v : xv.u, &ar = run ? av.v : av.u;
+#pragma unroll
+              for (int i = 0; i < 4; ++i) {
+                const f2 h = mul2(w.p[i], gr.p[i]);
+                hx = fma2(h, xr.p[i], hx);
+                ha = fma2(h, ar.p[i], ha);
+                cx = fma2(mul2(c.p[i], gr.p[i]), xr.p[i], cx);
+              }
+            }
+            sum[1] = hx.x + hx.y;
+            sum[3] = ha.x + ha.y;
+            sum[4] = cx.x + cx.y;
+          }
+          row_sums(sum, a.lanes);
+          if (!active) continue;
+          const float r = rsqrtf(fmaf(sum[0], a.inv_d, a.eps));
+          const float hn = r * sum[1] * a.inv_d, an = r * sum[2] * a.inv_d;  // <h, n> / d, <a, n> / d
+          const float ht = r * (sum[3] - r * sum[1] * an);                   // <h, t>
+          const float un = r * a.inv_d * sum[4] - 2.f * r * an * hn;         // <u, n> / d
+          // gx = r (c . g - r (an h + hn a) - back x),  t = r (a - an r x)
+          const f2 r2 = both(r), by_h = both(-r * an), by_a = both(-r * (r * hn)),
+                   by_x = both(-r * (r * (un + ht * a.inv_d))), at = both(-r * (an * r));
+#pragma unroll
+          for (int run = 0; run < 2; ++run) {
+            const Half w = shared8(sw + (run ? e1 : e0)), c = shared8(sc + (run ? e1 : e0));
+            Half &gr = run ? g.v : g.u, &xr = run ? xv.v : xv.u, &ac = run ? acc.v : acc.u;
+            const Half& ar = run ? av.v : av.u;
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+              const f2 t = fma2(r2, ar.p[i], mul2(at, xr.p[i]));
+              ac.p[i] = fma2(gr.p[i], t, ac.p[i]);
+              const f2 q = mul2(r2, fma2(by_h, w.p[i], c.p[i]));  // what multiplies g in gx
+              const f2 out = fma2(w.p[i], t, mul2(c.p[i], mul2(r2, xr.p[i])));
+              xr.p[i] = fma2(q, gr.p[i], fma2(by_a, ar.p[i], mul2(by_x, xr.p[i])));
+              gr.p[i] = out;
+            }
+          }
+          t8.template apply<INTERLEAVED, false>(g);
+          put8(y + e0, xv.u);
+          put8(y + e1, xv.v);
+          put8(ddy + e0, g.u);
+          put8(ddy + e1, g.v);
+          y += s.ys[1];
+          ddy += s.ddys[1];
+        }
+      }
+    }
+  }
+  if (OP == kForward || !s.sums) return;
+  float* const red = sc + (OP == kSecond ? a.d : 0);  // [per_block][d]
+  if (have) {
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      *reinterpret_cast<f2*>(red + group * a.d + e0 + 2 * i) = acc.u.p[i];
+      *reinterpret_cast<f2*>(red + group * a.d + e1 + 2 * i) = acc.v.p[i];
+    }
+  }
+  block_partial(red, a, second_side, block, per_block);
 }
 
 // dw[i] = sum over the blocks' partial sums: 32 features and 32 parts of the blocks
@@ -378,14 +714,14 @@ __global__ void __launch_bounds__(1024) norm_sums(SumArgs a) {
   }
 }
 
-// Blocks that carry sums: this many per SM in all.
+// Blocks per SM of norm_kernel, and as many or more of norm_rows with sums.
 constexpr int kBlocksPerSm = 6;
 
 // Lanes of a row, heads of a unit and blocks of each tensor.  A unit takes as
 // many heads (up to 16) as leave half a wave of threads, so that few sines are
-// computed; one where the call is small and latency counts.  Without sums a block
-// takes one unit.
-void plan(NormArgs& a, int P, int C, bool stay) {
+// computed; one where the call is small and latency counts.  Blocks stay and take units in
+// turn, so that the table of angles is made, and sums are carried, a few times an SM.
+void plan(NormArgs& a, int P, int C, int per_sm) {
   const int chunks = a.d / (2 * P) + (P == 1 ? (a.d & 1) : 0);
   int lanes = 1;
   while (lanes < 32 && lanes < (chunks + C - 1) / C) lanes *= 2;
@@ -403,22 +739,23 @@ void plan(NormArgs& a, int P, int C, bool stay) {
     }
     if (heads == 1 || units * kThreads >= kSms * 1024ll) break;
   }
-  const long long most = kSms * kBlocksPerSm;
+  // blocks in proportion to the rows of each tensor
+  const long long most = kSms * per_sm, rows = a.side[0].H + a.side[1].H;
   for (Side& s : a.side) {
-    long long n = s.units;
-    if (!stay) n = n < (1ll << 30) ? n : 1ll << 30;
-    else if (units > most) n = s.units * most / units;
-    s.blocks = (int)(n > 0 ? n : s.units > 0 ? 1 : 0);
+    const long long n = units > most ? most * s.H / rows : s.units;
+    s.blocks = (int)(n < s.units ? (n > 0 ? n : 1) : s.units);
   }
 }
 
+// P = 8: norm_rows; else norm_kernel.
 template <int OP, typename TI, typename TO, int P, int C, bool INTERLEAVED>
 cudaError_t launch(NormArgs& a, LaunchLog& log) {
-  plan(a, P, C, OP != kForward && (a.side[0].sums || a.side[1].sums));
-  size_t smem = sizeof(unsigned long long) * a.half + sizeof(float) * a.d * (OP == kSecond ? 2 : 1);
+  plan(a, P, C, P == 8 ? kResident<OP> * (OP == kForward ? 2 : 1) : kBlocksPerSm);
+  size_t smem = sizeof(unsigned long long) * ((a.half + 1) & ~1) + sizeof(float) * a.d * (OP == kSecond ? 2 : 1);
   smem += OP == kForward ? 0 : sizeof(float) * a.d * (kThreads / a.lanes);
-  norm_kernel<OP, TI, TO, P, C, INTERLEAVED>
-      <<<(unsigned)(a.side[0].blocks + a.side[1].blocks), kThreads, smem, log.stream>>>(a);
+  const unsigned grid = (unsigned)(a.side[0].blocks + a.side[1].blocks);
+  if constexpr (P == 8) norm_rows<OP, TI, TO, INTERLEAVED><<<grid, kThreads, smem, log.stream>>>(a);
+  else norm_kernel<OP, TI, TO, P, C, INTERLEAVED><<<grid, kThreads, smem, log.stream>>>(a);
   const cudaError_t e = cudaGetLastError();
   log.mark();
   return e;
