@@ -30,7 +30,6 @@
 #include <cuda_fp16.h>
 #include <cuda_runtime.h>
 #include <math.h>
-#include <stdlib.h>
 #include <string.h>
 #include <stdint.h>
 
@@ -385,7 +384,7 @@ struct Plan {
 // multiplications (128 columns 0.8 of what 256 do: half, less well fed), in stages of
 // 64 elements, and as much as 8 stages beside them.
 int choose_wide(const Plan& p, int cols, int depth, bool sym, int segs) {
-  if (getenv("ORTH_WIDE")) return atoi(getenv("ORTH_WIDE"));
+  if (!p.bf16) return 128;  // two terms: the finishing warps hold sums of 128 columns
   double best = 0;
   int wide = 0;
   for (int w : {256, 128}) {
@@ -673,8 +672,8 @@ struct Chain {
     phase().o_map[0] = (unsigned char)maps++;
   }
   void end() {
-    // The products of high terms come last: the tensor cores cut every addition off to the
-    // accumulator's 24 bits, which costs nothing while it holds the small ones only.
+    // the products of high terms come last: additions are cut off to the accumulator's 24
+    // bits, which costs little while it holds the small ones only
     for (int i = 0; i < highs; ++i) pair(high_p[i], 0, high_q[i], 0);
     Phase& f = phase();
     f.wide = choose_wide(p, f.cols, f.depth, f.sym, f.nseg);
@@ -688,7 +687,7 @@ struct Chain {
   cudaError_t launch(LaunchLog& log) {
     if (!ok) return cudaErrorUnknown;
     g.items = items;
-    return launch_chain(g, log);
+    return launch_chain(g, !p.bf16, log);
   }
 };
 

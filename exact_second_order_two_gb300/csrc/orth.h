@@ -80,7 +80,8 @@ inline long long tiles_of(int rows, int cols, bool sym, int wide) {  // of one m
   return sym ? kHigh / wide * tm * (tm + 1) / 2 : tm * tn;
 }
 
-cudaError_t launch_chain(const ChainArgs& g, LaunchLog& log);
+// split: two-term operands, tiles of 128 columns.
+cudaError_t launch_chain(const ChainArgs& g, bool split, LaunchLog& log);
 
 // A small matrix's steps, or their gradient, in one block (orth_small.cu).  Factors of
 // each step: A = to_a acc, B = to_b acc + a_to_b A, X' = to_x acc + x_to_x X; S = to_s acc,

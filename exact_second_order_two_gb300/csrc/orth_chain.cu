@@ -190,6 +190,13 @@ __device__ __forceinline__ int slots_of(const Phase& p, const ChainArgs& g) {
   return p.sym || p.e_terms == 2 || p.o_terms == 2 || (p.o_terms == 0 && !g.y_bf16) ? 1 : 2;
 }
 
+// SPLIT: two-term operands.  The tensor cores cut each addition off to the accumulator's 24
+// bits, always towards zero, which over a long contraction would be the largest error by
+// far (4 x 128 x 128: 2.5 times that of the same sums in fp32).  So the accumulator
+// takes kSplit stages at a time, and the finishing warps add these sums up, rounded.
+constexpr int kSplit = 4;
+
+template <bool SPLIT>
 __global__ void __launch_bounds__(kThreads, 1) chain(const __grid_constant__ ChainArgs g) {
   extern __shared__ __align__(1024) uint8_t smem[];
   const uint32_t sb = smem_u32(smem);
@@ -356,7 +363,7 @@ __global__ void __launch_bounds__(kThreads, 1) chain(const __grid_constant__ Cha
     }
   } else if (warp == kMmaWarp) {
     if (rank == 0) {
-      int it = 0, ph = 0;
+      int it = 0, nb = 0, ph = 0;  // stages, accumulators taken
       bool ok = true;
       for (int n = 0; ok; ++n) {
         int item = -1;
@@ -368,31 +375,35 @@ __global__ void __launch_bounds__(kThreads, 1) chain(const __grid_constant__ Cha
         const Phase& p = g.phase[ph];
         const bool nn = p.nn;
         const uint32_t id = idesc_f16(kHigh, p.wide, nn);
-        const uint32_t d = tmem + (n & 1) * kWide;
-        if (n >= 2 && !warp_wait(t_empty + (n & 1), ((n >> 1) - 1) & 1, ab, g.status)) break;
-        tc_fence_after();
         const int total = p.nseg * ((p.depth + kDepth - 1) / kDepth);
-        for (int k = 0; k < total; ++k, ++it) {
-          const int s = it % kStages;
-          if (!warp_wait(full + s, (it / kStages) & 1, ab, g.status)) {
+        const int part = SPLIT ? kSplit : total;
+        for (int k0 = 0; ok && k0 < total; k0 += part, ++nb) {
+          const uint32_t d = tmem + (nb & 1) * kWide;
+          if (nb >= 2 && !warp_wait(t_empty + (nb & 1), ((nb >> 1) - 1) & 1, ab, g.status)) {
             ok = false;
             break;
           }
           tc_fence_after();
-          if (k == 0 && lane == 0) mbar_arrive(started);
-          const uint32_t a_lo = opaque(lo_kmajor(sb + s * kStageBytes));
-          const uint32_t b_at = sb + s * kStageBytes + kTileBytes;
-          const uint32_t b_lo = opaque(nn ? lo_mnmajor(b_at, kTileBytes / 2) : lo_kmajor(b_at));
-          const uint32_t b_step = nn ? kstep_off(1) : 2;
+          const int k1 = min(total, k0 + part);
+          for (int k = k0; k < k1; ++k, ++it) {
+            const int s = it % kStages;
+            if (!warp_wait(full + s, (it / kStages) & 1, ab, g.status)) {
+              ok = false;
+              break;
+            }
+            tc_fence_after();
+            if (k == 0 && lane == 0) mbar_arrive(started);
+            const uint32_t a_lo = opaque(lo_kmajor(sb + s * kStageBytes));
+            const uint32_t b_at = sb + s * kStageBytes + kTileBytes;
+            const uint32_t b_lo = opaque(nn ? lo_mnmajor(b_at, kTileBytes / 2) : lo_kmajor(b_at));
+            const uint32_t b_step = nn ? kstep_off(1) : 2;
 #pragma unroll
-          for (int u = 0; u < kDepth / 16; ++u) {
-            const uint32_t al = a_lo + 2 * u, bl = b_lo + b_step * u;
-            mma_ss_pair_w(d, al, bl, id, k + u > 0 ? 1u : 0u);
+            for (int u = 0; u < kDepth / 16; ++u)
+              mma_ss_pair_w(d, a_lo + 2 * u, b_lo + b_step * u, id, k - k0 + u > 0 ? 1u : 0u);
+            mma_commit_pair_w(empty + s, 3);
           }
-          mma_commit_pair_w(empty + s, 3);
+          if (ok) mma_commit_pair_w(t_full + (nb & 1), 3);
         }
-        if (!ok) break;
-        mma_commit_pair_w(t_full + (n & 1), 3);
       }
       // every MMA this warp issued has completed before TMEM is released
       mma_commit_pair_w(drain, 1);
@@ -474,7 +485,7 @@ __global__ void __launch_bounds__(kThreads, 1) chain(const __grid_constant__ Cha
     const uint32_t lane_off = (uint32_t)(32 * (warp & 3)) << 16;
     const int group = warp >> 2, r = 32 * (warp & 3) + lane;
     uint32_t uses = 0;
-    int ph = 0, scaled = -1, scaled_ph = -1, shift = 0;
+    int ph = 0, nb = 0, scaled = -1, scaled_ph = -1, shift = 0;
     bool ok = true;
     for (int n = 0; ok; ++n) {
       int item = -1;
@@ -507,8 +518,36 @@ __global__ void __launch_bounds__(kThreads, 1) chain(const __grid_constant__ Cha
         beta = ldexpf(beta, shift);
         if (at.index == 0 && threadIdx.x == 0 && rank == 0) p.exp_out[at.l] = __ldcg(p.exp_in + at.l) + shift;
       }
-      if (!warp_wait(t_full + (n & 1), (n >> 1) & 1, ab, g.status)) break;
-      tc_fence_after();
+      f2 total[SPLIT ? 32 : 1];  // of the thread's 64 columns
+      if (SPLIT) {
+#pragma unroll
+        for (int k = 0; k < 32; ++k) total[SPLIT ? k : 0] = f2{0.f, 0.f};
+        const int stages = p.nseg * ((p.depth + kDepth - 1) / kDepth);
+        for (int k0 = 0; ok && k0 < stages; k0 += kSplit, ++nb) {
+          if (!warp_wait(t_full + (nb & 1), (nb >> 1) & 1, ab, g.status)) {
+            ok = false;
+            break;
+          }
+          tc_fence_after();
+#pragma unroll
+          for (int h = 0; h < 2; ++h) {
+            uint32_t acc[32];
+            tmem_ld32(tmem + lane_off + (nb & 1) * kWide + group * 64 + 32 * h, acc);
+#pragma unroll
+            for (int k = 0; k < 16; ++k) {
+              f2& t = total[SPLIT ? 16 * h + k : 0];
+              t = add2(t, f2{__uint_as_float(acc[2 * k]), __uint_as_float(acc[2 * k + 1])});
+            }
+          }
+          tc_fence_before();
+          __syncwarp();
+          if (lane == 0) mbar_arrive_cluster(cluster_addr(t_empty + (nb & 1), 0));
+        }
+        if (!ok) break;
+      } else {
+        if (!warp_wait(t_full + (n & 1), (n >> 1) & 1, ab, g.status)) break;
+        tc_fence_after();
+      }
       float sum = 0.f;
 #pragma unroll 1
       for (int c = 0; c < chunks; ++c) {
@@ -520,15 +559,20 @@ __global__ void __launch_bounds__(kThreads, 1) chain(const __grid_constant__ Cha
           break;
         }
         uses ^= 1u << s;
-#pragma unroll 1
+#pragma unroll(SPLIT ? 2 : 1)
         for (int h = 0; h < 2; ++h) {
           const int col = col0 + 32 * h;
-          uint32_t acc[32];
-          tmem_ld32(tmem + lane_off + (n & 1) * kWide + in_tile + 32 * h, acc);
           f2 v[16];
+          if (SPLIT) {
 #pragma unroll
-          for (int k = 0; k < 16; ++k)
-            v[k] = mul2(f2{alpha, alpha}, f2{__uint_as_float(acc[2 * k]), __uint_as_float(acc[2 * k + 1])});
+            for (int k = 0; k < 16; ++k) v[k] = mul2(f2{alpha, alpha}, total[SPLIT ? 16 * h + k : 0]);
+          } else {
+            uint32_t acc[32];
+            tmem_ld32(tmem + lane_off + (n & 1) * kWide + in_tile + 32 * h, acc);
+#pragma unroll
+            for (int k = 0; k < 16; ++k)
+              v[k] = mul2(f2{alpha, alpha}, f2{__uint_as_float(acc[2 * k]), __uint_as_float(acc[2 * k + 1])});
+          }
           if (p.e_terms) add_slot(v, slot, r, h, beta);
           if (p.e_terms == 2) add_slot(v, slot + kTileBytes, r, h, beta);
           if (p.sums) {  // (what lies outside is zero)
@@ -588,9 +632,7 @@ __global__ void __launch_bounds__(kThreads, 1) chain(const __grid_constant__ Cha
         __syncwarp();
         if (lane == 0) {
           mbar_arrive(written + s);
-          if (c == chunks - 1) {
-            mbar_arrive_cluster(cluster_addr(t_empty + (n & 1), 0));
-          }
+          if (!SPLIT && c == chunks - 1) mbar_arrive_cluster(cluster_addr(t_empty + (n & 1), 0));
         }
       }
     }
@@ -607,11 +649,12 @@ __global__ void __launch_bounds__(kThreads, 1) chain(const __grid_constant__ Cha
 
 }  // namespace
 
-cudaError_t launch_chain(const ChainArgs& g, LaunchLog& log) {
-  const cudaError_t e = cudaFuncSetAttribute(chain, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmem);
+cudaError_t launch_chain(const ChainArgs& g, bool split, LaunchLog& log) {
+  auto kernel = split ? chain<true> : chain<false>;
+  const cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmem);
   if (e != cudaSuccess) return e;
   const int grid = 2 * (g.items < kPairs ? g.items : kPairs);
-  return launch_next(chain, dim3((unsigned)grid), kThreads, kSmem, 2, log, g);
+  return launch_next(kernel, dim3((unsigned)grid), kThreads, kSmem, 2, log, g);
 }
 
 }  // namespace orth

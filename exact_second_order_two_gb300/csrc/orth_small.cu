@@ -101,31 +101,35 @@ __device__ __forceinline__ void take_in(const T* x, const Held& h, int terms, fl
   }
 }
 
-// Issued by one thread: acc (+)= P Q^T over `depth` tiles of columns, or P Q over `depth`
-// tiles of Q's rows (64 each).
+// Issued by one thread: acc (+)= P Q^T over tile k of columns, or P Q over tile k of Q's
+// rows (64 each).
 __device__ __forceinline__ void multiply(uint32_t acc, const Held& P, int tp, const Held& Q, int tq, bool nn,
-                                         int depth, bool& begun) {
+                                         int k, bool begun) {
   const uint32_t id = idesc_f16(kTile, nn ? 64 * Q.tiles : kTile, nn);
-  for (int k = 0; k < depth; ++k) {
-    const uint32_t a = lo_kmajor(smem_u32(P.tile(tp, k)));
-    const uint32_t b = nn ? lo_mnmajor(smem_u32(Q.tile(tq, 0)), kTileBytes) + 4 * k * kstep_off(1)
-                          : lo_kmajor(smem_u32(Q.tile(tq, k)));
+  const uint32_t a = lo_kmajor(smem_u32(P.tile(tp, k)));
+  const uint32_t b = nn ? lo_mnmajor(smem_u32(Q.tile(tq, 0)), kTileBytes) + 4 * k * kstep_off(1)
+                        : lo_kmajor(smem_u32(Q.tile(tq, k)));
 #pragma unroll
-    for (int u = 0; u < 4; ++u) {
-      mma_ss(acc, a + 2 * u, b + (nn ? kstep_off(u) : 2 * u), id, begun ? 1u : 0u);
-      begun = true;
-    }
-  }
+  for (int u = 0; u < 4; ++u)
+    mma_ss(acc, a + 2 * u, b + (nn ? kstep_off(u) : 2 * u), id, begun || u > 0 ? 1u : 0u);
 }
-// every pair of terms but the two low ones, the high ones last
+// A product over `depth` tiles: every pair of terms but the two low ones, the high ones
+// last.  With two terms, sums of 64 products of high terms each in an accumulator of their own
+// (of four; at most two tiles, two products), for what the tensor cores cut off their
+// additions; `first` is the product's first accumulator.
 template <int TERMS>
 __device__ __forceinline__ void multiply_terms(uint32_t acc, const Held& P, const Held& Q, bool nn, int depth,
-                                               bool& begun) {
-  if (TERMS == 2) {
-    multiply(acc, P, 0, Q, 1, nn, depth, begun);
-    multiply(acc, P, 1, Q, 0, nn, depth, begun);
+                                               int first) {
+  for (int k = 0; k < depth; ++k) {
+    if (TERMS == 2) {
+      const uint32_t own = acc + 128 * (first + k);
+      multiply(own, P, 0, Q, 1, nn, k, false);
+      multiply(own, P, 1, Q, 0, nn, k, true);
+      multiply(own, P, 0, Q, 0, nn, k, true);
+    } else {
+      multiply(acc, P, 0, Q, 0, nn, k, first + k > 0);
+    }
   }
-  multiply(acc, P, 0, Q, 0, nn, depth, begun);
 }
 
 __device__ __forceinline__ void store_held(const CUtensorMap* hi, const CUtensorMap* lo, const Held& h, int at,
@@ -175,13 +179,20 @@ __device__ __forceinline__ void hand_over() {
   tc_fence_after();
 }
 
-// The thread's 32 columns (32 u on) of the accumulator, times alpha.
-__device__ __forceinline__ void read_acc(uint32_t acc, int u, float alpha, f2 (&v)[16]) {
-  uint32_t w[32];
-  tmem_ld32(acc + ((uint32_t)(32 * ((threadIdx.x >> 5) & 3)) << 16) + 32 * u, w);
+// The thread's 32 columns (32 u on) of the sum of `count` accumulators, times alpha.
+__device__ __forceinline__ void read_acc(uint32_t acc, int count, int u, float alpha, f2 (&v)[16]) {
+  acc += ((uint32_t)(32 * ((threadIdx.x >> 5) & 3)) << 16) + 32 * u;
 #pragma unroll
-  for (int k = 0; k < 16; ++k)
-    v[k] = mul2(f2{alpha, alpha}, f2{__uint_as_float(w[2 * k]), __uint_as_float(w[2 * k + 1])});
+  for (int k = 0; k < 16; ++k) v[k] = f2{0.f, 0.f};
+  for (int i = 0; i < count; ++i) {
+    uint32_t w[32];
+    tmem_ld32(acc + 128 * i, w);
+#pragma unroll
+    for (int k = 0; k < 16; ++k)
+      v[k] = add2(v[k], f2{__uint_as_float(w[2 * k]), __uint_as_float(w[2 * k + 1])});
+  }
+#pragma unroll
+  for (int k = 0; k < 16; ++k) v[k] = mul2(f2{alpha, alpha}, v[k]);
 }
 // in `terms` terms to columns 32 u .. of h
 __device__ __forceinline__ void put(const f2 (&v)[16], const Held& h, int terms, int row, int u) {
@@ -208,7 +219,7 @@ __global__ void __launch_bounds__(kThreads, 1) small_forward(const __grid_consta
   const int tiles = (g.q + 63) / 64, l = blockIdx.x;
   const Held X{smem, tiles}, A{smem + g.x_terms * tiles * kTileBytes, kSquare};  // B in A's place
   Shared* sh = reinterpret_cast<Shared*>(A.at + TERMS * kSquare * kTileBytes);
-  const uint32_t cols = tiles > 2 ? 256 : 128;
+  const uint32_t cols = TERMS == 2 ? 512 : tiles > 2 ? 256 : 128;
   if (l == 0 && threadIdx.x == 0) *g.status = 0;
   begin_block(sh, cols, g);
   const uint32_t acc = sh->tmem;
@@ -219,6 +230,7 @@ __global__ void __launch_bounds__(kThreads, 1) small_forward(const __grid_consta
   if (threadIdx.x == 0 && g.info) g.info[l] = info;
   take_in(x, X, g.xt[0], factor, g.p, g.q, g.tall);
   const int deep = (g.p + 63) / 64;  // tiles of A's columns
+  const int wide_sums = TERMS == 2 ? tiles : 1, deep_sums = TERMS == 2 ? deep : 1;
   int n = 0;                         // products so far
   bool ok = true;
   // one product: what `store` sends off is read before the tiles can be written again
@@ -226,8 +238,7 @@ __global__ void __launch_bounds__(kThreads, 1) small_forward(const __grid_consta
     hand_over();
     if (threadIdx.x == 0 && !sh->ab.flag) {
       store();
-      bool begun = false;
-      multiply_terms<TERMS>(acc, P, Q, nn, depth, begun);
+      multiply_terms<TERMS>(acc, P, Q, nn, depth, 0);
       bulk_wait_read_all();
       mma_commit(&sh->mma);
     }
@@ -241,12 +252,12 @@ __global__ void __launch_bounds__(kThreads, 1) small_forward(const __grid_consta
     product(X, X, false, tiles, [&] {
       if (g.keep) store_held(&g.x_map[0], g.xt[i] == 2 ? &g.x_map[1] : nullptr, X, i * g.L + l, g.q, g.p);
     });
-    read_acc(acc, unit, f * f * g.to_a[i], v);
+    read_acc(acc, wide_sums, unit, f * f * g.to_a[i], v);
     put(v, A, TERMS, row, unit);
     product(A, A, false, deep, [&] {
       if (g.keep) store_held(&g.a_map[0], TERMS == 2 ? &g.a_map[1] : nullptr, A, i * g.L + l, g.p, g.p);
     });
-    read_acc(acc, unit, g.to_b[i], v);
+    read_acc(acc, deep_sums, unit, g.to_b[i], v);
     add_slot(v, A.tile(0, unit >> 1), row, unit & 1, g.a_to_b[i]);
     if (TERMS == 2) add_slot(v, A.tile(1, unit >> 1), row, unit & 1, g.a_to_b[i]);
     put(v, A, TERMS, row, unit);
@@ -255,7 +266,7 @@ __global__ void __launch_bounds__(kThreads, 1) small_forward(const __grid_consta
     });
     const bool last = i + 1 == g.steps;
     for (int u = unit; u < 2 * tiles; u += 4) {
-      read_acc(acc, u, f * g.to_x[i], v);
+      read_acc(acc, deep_sums, u, f * g.to_x[i], v);
       add_slot(v, X.tile(0, u >> 1), row, u & 1, f * g.x_to_x[i]);
       if (g.xt[i] == 2) add_slot(v, X.tile(1, u >> 1), row, u & 1, f * g.x_to_x[i]);
       if (!last) {
@@ -286,12 +297,13 @@ __global__ void __launch_bounds__(kThreads, 1) small_backward(const __grid_const
   // what comes from memory: X, or A or B
   const Held X{S.at + TERMS * kSquare * kTileBytes, tiles}, A{X.at, kSquare};
   Shared* sh = reinterpret_cast<Shared*>(X.at + TERMS * room * kTileBytes);
-  const uint32_t cols = tiles > 2 ? 256 : 128;
+  const uint32_t cols = TERMS == 2 ? 512 : tiles > 2 ? 256 : 128;
   if (l == 0 && threadIdx.x == 0) *g.status = 0;
   begin_block(sh, cols, g);
   const uint32_t acc = sh->tmem;
   const int row = 32 * ((threadIdx.x >> 5) & 3) + (threadIdx.x & 31), unit = threadIdx.x >> 7;
   const int deep = (g.p + 63) / 64;
+  const int wide_sums = TERMS == 2 ? 2 * tiles : 1, deep_sums = TERMS == 2 ? 2 * deep : 1;
   const T* dy = static_cast<const T*>(g.dy) + (size_t)l * g.p * g.q;
   const MatInfo info = g.info[l];
   int n = 0, m = 0;  // products and loads so far
@@ -320,38 +332,35 @@ __global__ void __launch_bounds__(kThreads, 1) small_backward(const __grid_const
   for (int i = g.steps - 1; i >= 0; --i) {
     const float f = i == 0 ? info.f : 1.f;  // X_0 is f times what is stored
     f2 v[16];
-    bool begun = false;
     loaded();
     product([&] {
-      multiply_terms<TERMS>(acc, H, X, false, tiles, begun);
-      multiply_terms<TERMS>(acc, X, H, false, tiles, begun);
+      multiply_terms<TERMS>(acc, H, X, false, tiles, 0);
+      multiply_terms<TERMS>(acc, X, H, false, tiles, tiles);
     });
     if (threadIdx.x == 0) load(g.a_map, A, kSquare, i);
-    read_acc(acc, unit, f * g.to_s[i], v);
+    read_acc(acc, wide_sums, unit, f * g.to_s[i], v);
     put(v, S, TERMS, row, unit);
     loaded();
     product([&] {
-      begun = false;
-      multiply_terms<TERMS>(acc, A, S, false, deep, begun);
-      multiply_terms<TERMS>(acc, S, A, false, deep, begun);
+      multiply_terms<TERMS>(acc, A, S, false, deep, 0);
+      multiply_terms<TERMS>(acc, S, A, false, deep, deep);
     });
     if (threadIdx.x == 0) load(g.b_map, A, kSquare, i);
-    read_acc(acc, unit, f * g.to_t[i], v);  // T in S's place
+    read_acc(acc, deep_sums, unit, f * g.to_t[i], v);  // T in S's place
     add_slot(v, S.tile(0, unit >> 1), row, unit & 1, f * g.s_to_t[i]);
     if (TERMS == 2) add_slot(v, S.tile(1, unit >> 1), row, unit & 1, f * g.s_to_t[i]);
     put(v, S, TERMS, row, unit);
     loaded();
-    begun = false;
-    product([&] { multiply_terms<TERMS>(acc, A, H, true, deep, begun); });
+    product([&] { multiply_terms<TERMS>(acc, A, H, true, deep, 0); });
     if (threadIdx.x == 0) load(g.x_map, X, tiles, i);
     loaded();
-    product([&] { multiply_terms<TERMS>(acc, S, X, true, deep, begun); });
+    product([&] { multiply_terms<TERMS>(acc, S, X, true, deep, deep); });
     const int shift = rescaling(nu2, g.target[i]);
     exp += shift;
     const float alpha = ldexpf(g.to_h[i], shift), beta = ldexpf(g.h_to_h[i], shift);
     float sum = 0.f;
     for (int u = unit; u < 2 * tiles; u += 4) {
-      read_acc(acc, u, alpha, v);
+      read_acc(acc, deep_sums, u, alpha, v);
       add_slot(v, H.tile(0, u >> 1), row, u & 1, beta);
       if (TERMS == 2) add_slot(v, H.tile(1, u >> 1), row, u & 1, beta);
       f2 w[16];
