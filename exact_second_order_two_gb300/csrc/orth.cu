@@ -588,8 +588,7 @@ struct Chain {
   const Plan& p;
   int maps = 0, items = 0;
   bool ok = true;
-  int highs = 0, q_terms[kMaxSegs];
-  Ref high_p[2], high_q[2];
+  int q_terms[kMaxSegs];
   const Mats* q_of[kMaxSegs];
   Chain(const Plan& plan, int* status, int* counts, const MatInfo* info) : p(plan) {
     g.phases = 0;
@@ -627,7 +626,6 @@ struct Chain {
     f.nn = nn;
     f.sym = sym;
     f.first = items;
-    highs = 0;
   }
   void pair(const Ref& P, int tp, const Ref& Q, int tq) {
     Phase& f = phase();
@@ -639,10 +637,11 @@ struct Chain {
   }
   // acc += P Q^T (or P Q): every pair of terms but the two low ones
   void add(const Ref& P, const Ref& Q) {
-    if (Q.terms == 2) pair(P, 0, Q, 1);
-    if (P.terms == 2) pair(P, 1, Q, 0);
-    high_p[highs] = P;
-    high_q[highs++] = Q;
+    if (P.terms == 2) {
+      pair(P, 0, Q, 1);
+      pair(P, 1, Q, 0);
+    }
+    pair(P, 0, Q, 0);
   }
   void plus(const Ref& E) {
     Phase& f = phase();
@@ -672,9 +671,6 @@ struct Chain {
     phase().o_map[0] = (unsigned char)maps++;
   }
   void end() {
-    // the products of high terms come last: additions are cut off to the accumulator's 24
-    // bits, which costs little while it holds the small ones only
-    for (int i = 0; i < highs; ++i) pair(high_p[i], 0, high_q[i], 0);
     Phase& f = phase();
     f.wide = choose_wide(p, f.cols, f.depth, f.sym, f.nseg);
     f.tiles = (int)tiles_of(p.p, f.cols, f.sym, f.wide);

@@ -192,9 +192,11 @@ __device__ __forceinline__ int slots_of(const Phase& p, const ChainArgs& g) {
 
 // SPLIT: two-term operands.  The tensor cores cut each addition off to the accumulator's 24
 // bits, always towards zero, which over a long contraction would be the largest error by
-// far (4 x 128 x 128: 2.5 times that of the same sums in fp32).  So the accumulator
-// takes kSplit stages at a time, and the finishing warps add these sums up, rounded.
-constexpr int kSplit = 4;
+// far (a steep polynomial of a result near 1 enlarges it ten times: 512 x 2048 was 5.6e-6 off
+// with sums of 256 elements, the same in fp32 torch 2.8e-6).  So the accumulator takes 64
+// elements at a time, the products with low terms first, and the finishing warps add
+// these sums up, rounded.
+constexpr int kSplit = 3;  // stages: the pairs of terms of a product
 
 template <bool SPLIT>
 __global__ void __launch_bounds__(kThreads, 1) chain(const __grid_constant__ ChainArgs g) {
@@ -326,11 +328,14 @@ __global__ void __launch_bounds__(kThreads, 1) chain(const __grid_constant__ Cha
         const int row = at.i * kHigh + rank * kTile, col = at.j * p.wide + rank * half;
         const int blocks = (p.depth + kDepth - 1) / kDepth;
         const bool nn = p.nn;
-        for (int sg = 0; ok && sg < p.nseg; ++sg) {
-          const CUtensorMap *ma = &g.maps[p.seg_a[sg]], *mb = &g.maps[p.seg_b[sg]];
-          const int la = p.at_a[sg] + at.l, lb = p.at_b[sg] + at.l;
-          for (int k = 0; k < blocks; ++k, ++it) {
-            const int s = it % kStages;
+        // a segment after the other; SPLIT: every pair of terms of one stretch of the
+        // contraction together
+        const int outer = SPLIT ? blocks : p.nseg, inner = SPLIT ? p.nseg : blocks;
+        for (int o = 0; ok && o < outer; ++o) {
+          const CUtensorMap *ma = &g.maps[p.seg_a[SPLIT ? 0 : o]], *mb = &g.maps[p.seg_b[SPLIT ? 0 : o]];
+          int la = p.at_a[SPLIT ? 0 : o] + at.l, lb = p.at_b[SPLIT ? 0 : o] + at.l;
+          for (int i = 0; i < inner; ++i, ++it) {
+            const int s = it % kStages, k = SPLIT ? o : i;
             if (it >= kStages && !warp_wait(empty + s, ((it / kStages) - 1) & 1, ab, g.status)) {
               ok = false;
               break;
@@ -340,6 +345,12 @@ __global__ void __launch_bounds__(kThreads, 1) chain(const __grid_constant__ Cha
               break;
             }
             if (lane != 0) continue;
+            if (SPLIT) {
+              ma = &g.maps[p.seg_a[i]];
+              mb = &g.maps[p.seg_b[i]];
+              la = p.at_a[i] + at.l;
+              lb = p.at_b[i] + at.l;
+            }
             uint8_t *pa = smem + s * kStageBytes, *pb = pa + kTileBytes;
             if (rank == 0) mbar_arrive_expect_tx(full + s, 2 * (kTileBytes + half * 128));
             const uint32_t bar = cluster_addr(full + s, 0);
