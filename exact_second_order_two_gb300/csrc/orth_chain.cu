@@ -311,7 +311,10 @@ __global__ void __launch_bounds__(kThreads, 1) chain(const __grid_constant__ Cha
       }
     }
   } else if (warp == kProducerWarp) {
-    {  // the whole warp, with operands that are the same in all lanes; one lane issues
+    // The whole warp, with operands that are the same in all lanes; one lane issues.  What this
+    // loop does for a stage bounds the rate: a look at the abort flag in it (which the
+    // waits do when they have to wait) made 4096 x 16384 5% slower.
+    {
       int it = 0, ph = 0;
       bool ok = true;
       for (int n = 0; ok; ++n) {
@@ -337,10 +340,6 @@ __global__ void __launch_bounds__(kThreads, 1) chain(const __grid_constant__ Cha
           for (int i = 0; i < inner; ++i, ++it) {
             const int s = it % kStages, k = SPLIT ? o : i;
             if (it >= kStages && !warp_wait(empty + s, ((it / kStages) - 1) & 1, ab, g.status)) {
-              ok = false;
-              break;
-            }
-            if (__any_sync(0xffffffffu, ab->flag)) {
               ok = false;
               break;
             }
