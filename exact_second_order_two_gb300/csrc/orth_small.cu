@@ -162,6 +162,8 @@ __device__ __forceinline__ void begin_block(Shared* sh, uint32_t cols, const Sma
   tc_fence_after();
 }
 __device__ __forceinline__ void end_block(Shared* sh, uint32_t cols) {
+  if (threadIdx.x == 0 && sh->ab.flag)  // what an abort leaves in flight lands
+    for (const uint64_t t0 = global_ns(); global_ns() - t0 < 10000000ull;) __nanosleep(10000);
   tc_fence_before();
   __syncthreads();
   if (threadIdx.x < 32) {
@@ -398,8 +400,6 @@ __global__ void __launch_bounds__(kThreads, 1) small_backward(const __grid_const
                                                          2 * (c & 7)));
     out[i] = from_f32<T>(fmaf(-by_g, to_f32<T>(x[i]), by_h * h));
   }
-  if (threadIdx.x == 0 && sh->ab.flag)  // what an abort leaves in flight lands
-    for (const uint64_t t0 = global_ns(); global_ns() - t0 < 10000000ull;) __nanosleep(10000);
   end_block(sh, cols);
 }
 

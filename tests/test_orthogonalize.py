@@ -244,6 +244,65 @@ class TestValues:
         assert all(torch.equal(a, b) for a, b in zip(outs[0], want))
         assert all(torch.equal(a, b) for a, b in zip(outs[1], expect))
 
+    def test_calls_at_once_on_two_streams(self):
+        """Chains whose blocks wait for one another's tiles, two of them at a time and
+        each too large for the GPU beside the other."""
+        inputs = [gradient((2, 1100, 1500), d, seed=i) for i, d in enumerate(DT.values())]
+
+        def step(x, dY):
+            leaf = x.clone().requires_grad_()
+            y = fbob.orthogonalize(leaf)
+            return y, torch.autograd.grad(y, leaf, dY)[0]
+
+        want = [step(*i) for i in inputs]
+        streams = [torch.cuda.Stream() for _ in inputs]
+        for s in streams:
+            s.wait_stream(torch.cuda.current_stream())
+        got = []
+        for _ in range(5):
+            for s, i in zip(streams, inputs):
+                with torch.cuda.stream(s):
+                    got.append(step(*i))
+        torch.cuda.synchronize()
+        for k, pair in enumerate(got):
+            assert all(torch.equal(a, b) for a, b in zip(pair, want[k % 2]))
+
+    @pytest.mark.parametrize("shape", [(2, 700, 900), (8, 100, 128)], ids=str)
+    @pytest.mark.parametrize("dtype", ["bf16", "fp32"])
+    def test_waits_that_run_out_end_the_call(self, shape, dtype):
+        """With a limit of 1 ns the first wait that is not over runs out: the call ends, its
+        status word says so, and the next call with the default limit is right.  (A small
+        matrix's waits can be over before the timer moves.)"""
+        G, dY = gradient(shape, DT[dtype])
+        coef = (ctypes.c_float * 15)(*(ONE * 5))
+        o = B.Orth(*shape, B.DTYPES[DT[dtype]], 5, 1, 1e-7, ctypes.addressof(coef))
+        lib, r = B.lib(), ctypes.byref(o)
+        sizes = [lib.fbob_orth_workspace_size(op, r) for op in (0, 1)]
+        kept, ws = (torch.empty(n, dtype=torch.uint8, device="cuda") for n in sizes)
+        y, dG = torch.empty_like(G), torch.empty_like(G)
+        stream = B._stream(G.device)
+        p = lambda t: t.data_ptr()  # noqa: E731
+
+        def forward():
+            assert lib.fbob_orth_forward(r, p(G), p(y), p(kept), sizes[0], stream) == 0
+            return fbob.status(kept)
+
+        def backward():
+            assert lib.fbob_orth_backward(r, p(G), p(dY), p(dG), p(kept), sizes[0], p(ws), sizes[1], stream) == 0
+            return fbob.status(ws)
+
+        assert forward() == 0 and backward() == 0
+        want = y.clone(), dG.clone()
+        for call in (backward, forward):
+            old = fbob.set_wait_limit(1)
+            try:
+                st = call()
+            finally:
+                fbob.set_wait_limit(old)
+            assert st == 5 or (st == 0 and shape[1] <= 128)
+        assert forward() == 0 and backward() == 0
+        assert torch.equal(y, want[0]) and torch.equal(dG, want[1])
+
     def test_nothing_is_written_outside(self):
         """Outputs and workspaces of the C calls between guards, at sizes off every tile."""
         for dtype in DT.values():
