@@ -215,12 +215,13 @@ __global__ void __launch_bounds__(kThreads, 1) chain(const __grid_constant__ Cha
   uint64_t* written = e_full + 2 * kGroups;                       // [kGroups][2]
   uint64_t* r_full = written + 2 * kGroups;                       // [kRing]
   uint64_t* r_empty = r_full + kRing;                             // [kRing]
-  uint64_t* started = r_empty + kRing;
+  uint64_t* go = r_empty + kRing;                                 // [kRing]
+  uint64_t* started = go + kRing;
   uint64_t* drain = started + 1;
-  static_assert((2 * kStages + 4 + 4 * kGroups + 2 * kRing + 2) * 8 <= 256, "barriers end below the rest");
-  uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(smem + kOffMisc + 256);
-  Abort* ab = reinterpret_cast<Abort*>(smem + kOffMisc + 264);
-  volatile int* ring = reinterpret_cast<volatile int*>(smem + kOffMisc + 288);  // [kRing]: items, -1: none left
+  static_assert((2 * kStages + 4 + 4 * kGroups + 3 * kRing + 2) * 8 <= 320, "barriers end below the rest");
+  uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(smem + kOffMisc + 320);
+  Abort* ab = reinterpret_cast<Abort*>(smem + kOffMisc + 328);
+  volatile int* ring = reinterpret_cast<volatile int*>(smem + kOffMisc + 352);  // [kRing]: items, -1: none left
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const uint32_t rank = cluster_rank();
   constexpr uint32_t kCols = 2 * kWide;
@@ -239,6 +240,7 @@ __global__ void __launch_bounds__(kThreads, 1) chain(const __grid_constant__ Cha
     }
     for (int i = 0; i < kRing; ++i) {
       mbar_init(r_full + i, 1);
+      mbar_init(go + i, 1);
       // the multiplying warp, and each CTA's finishing, loading and moving ones
       mbar_init(r_empty + i, 1 + 2 * (kEpiWarps + 2));
     }
@@ -259,9 +261,10 @@ __global__ void __launch_bounds__(kThreads, 1) chain(const __grid_constant__ Cha
   after_previous();
   const uint32_t tmem = *tmem_slot;
 
-  // the n-th item, for one who reads the ring; false after an abort
-  auto next_item = [&](int n, int& item) -> bool {
-    uint64_t* bar = r_full + n % kRing;
+  // waits for the n-th phase of a ring of barriers that the scheduler arrives on; false
+  // after an abort
+  auto await_ring = [&](uint64_t* bars, int n) -> bool {
+    uint64_t* bar = bars + n % kRing;
     const uint32_t parity = (n / kRing) & 1;
     if (!try_wait_cluster(bar, parity)) {
       const uint64_t t0 = global_ns();
@@ -274,6 +277,11 @@ __global__ void __launch_bounds__(kThreads, 1) chain(const __grid_constant__ Cha
         }
       }
     }
+    return true;
+  };
+  // the n-th item, for one who reads the ring
+  auto next_item = [&](int n, int& item) -> bool {
+    if (!await_ring(r_full, n)) return false;
     item = ring[n % kRing];
     return true;
   };
@@ -293,21 +301,23 @@ __global__ void __launch_bounds__(kThreads, 1) chain(const __grid_constant__ Cha
         if (n >= 1 && !wait_bar(started, (n - 1) & 1, ab, g.status)) break;
         int item = atomicAdd(g.ticket, 1);
         if (item >= g.items) item = -1;
-        if (item >= 0) {
-          // what the phase reads of this matrix is written
-          ph = phase_of(ph, item);
-          const Phase& p = g.phase[ph];
-          const int l = (item - p.first) / p.tiles;
-          if (ph > 0 && !wait_count(g.done + (size_t)(ph - 1) * g.count + l, 2 * g.phase[ph - 1].tiles, ab,
-                                    g.status))
-            break;
-        }
+        // The others learn of it at once, and see to what it needs of the arguments (maps, that
+        // are far when first used); they load when what the phase reads of this matrix is
+        // written.
         if (n >= kRing && !wait_bar(r_empty + n % kRing, ((n / kRing) - 1) & 1, ab, g.status)) break;
         ring[n % kRing] = item;
         mbar_arrive(r_full + n % kRing);
         st_cluster(cluster_addr(const_cast<int*>(ring + n % kRing), 1), item);
         mbar_arrive_cluster(cluster_addr(r_full + n % kRing, 1));
         if (item < 0) break;
+        ph = phase_of(ph, item);
+        const Phase& p = g.phase[ph];
+        const int l = (item - p.first) / p.tiles;
+        if (ph > 0 && !wait_count(g.done + (size_t)(ph - 1) * g.count + l, 2 * g.phase[ph - 1].tiles, ab,
+                                  g.status))
+          break;
+        mbar_arrive(go + n % kRing);
+        mbar_arrive_cluster(cluster_addr(go + n % kRing, 1));
       }
     }
   } else if (warp == kProducerWarp) {
@@ -323,7 +333,6 @@ __global__ void __launch_bounds__(kThreads, 1) chain(const __grid_constant__ Cha
         if (lane == 0) item_read(n);
         item = __reduce_max_sync(0xffffffffu, item);
         if (item < 0) break;
-        fence_async_all();  // the loads see what the scheduler saw written
         ph = phase_of(ph, item);
         const Phase& p = g.phase[ph];
         const TileAt at = tile_at(p, g.rows, item);
@@ -331,6 +340,12 @@ __global__ void __launch_bounds__(kThreads, 1) chain(const __grid_constant__ Cha
         const int row = at.i * kHigh + rank * kTile, col = at.j * p.wide + rank * half;
         const int blocks = (p.depth + kDepth - 1) / kDepth;
         const bool nn = p.nn;
+        if (lane < p.nseg) {
+          tma_prefetch_desc(&g.maps[p.seg_a[lane]]);
+          tma_prefetch_desc(&g.maps[p.seg_b[lane]]);
+        }
+        if (!__all_sync(0xffffffffu, await_ring(go, n))) break;
+        fence_async_all();  // the loads see what the scheduler saw written
         // a segment after the other; SPLIT: every pair of terms of one stretch of the
         // contraction together
         const int outer = SPLIT ? blocks : p.nseg, inner = SPLIT ? p.nseg : blocks;
@@ -429,7 +444,6 @@ __global__ void __launch_bounds__(kThreads, 1) chain(const __grid_constant__ Cha
         if (!next_item(n, item)) break;
         item_read(n);
         if (item < 0) break;
-        fence_async_all();
         ph = phase_of(ph, item);
         const Phase& p = g.phase[ph];
         const TileAt at = tile_at(p, g.rows, item);
@@ -450,6 +464,10 @@ __global__ void __launch_bounds__(kThreads, 1) chain(const __grid_constant__ Cha
             mbar_arrive(e_full + s);
           }
         };
+        if (p.e_terms) {
+          if (!await_ring(go, n)) break;
+          fence_async_all();
+        }
         if (ab->flag) break;
         for (int group = 0; group < kGroups; ++group)
           for (int c = 0; c < nslots && c < chunks; ++c) prepare(group, c);
@@ -516,6 +534,7 @@ __global__ void __launch_bounds__(kThreads, 1) chain(const __grid_constant__ Cha
         beta *= ff;
       }
       if (p.scale_sums) {
+        if (!__all_sync(0xffffffffu, await_ring(go, n))) break;
         if (scaled != at.l || scaled_ph != ph) {
           const float* q = p.scale_sums + (size_t)at.l * p.scale_parts;
           float nu2 = 0.f;
