@@ -727,7 +727,8 @@ void backward_scales(const Plan& p, int* target, int* se) {
     const double growth = a + 3 * b * M * M + 5 * c * M * M * M * M;
     const double t = (b + 2 * c * M * M) * 2 * M;
     double most = 15 - log2(growth > 1 ? growth : 1);
-    const double by_t = 15 - log2(t > 1e-30 ? t : 1e-30) - (p.be[i] - p.xe[i]);
+    // (T of the first step is stored times f < 2)
+    const double by_t = (i > 0 ? 15 : 14) - log2(t > 1e-30 ? t : 1e-30) - (p.be[i] - p.xe[i]);
     if (by_t < most) most = by_t;
     target[i] = (int)floor(most) < 12 ? (int)floor(most) : 12;
     se[i] = store_exp(pow2(target[i]) * 2 * M);
