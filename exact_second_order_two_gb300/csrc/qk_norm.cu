@@ -222,6 +222,7 @@ __global__ void __launch_bounds__(kThreads) norm_kernel(const __grid_constant__ 
   float* const sw = reinterpret_cast<float*>(turns + a.half);
   float* const sc = sw + a.d;
   constexpr int U = kRows<OP, C>;
+  if (OP != kForward) asm volatile("griddepcontrol.launch_dependents;" ::: "memory");  // norm_sums
   const bool second_side = blockIdx.x >= (unsigned)a.side[0].blocks;
   const Side& s = a.side[second_side];
   const int block = blockIdx.x - (second_side ? a.side[0].blocks : 0);
@@ -362,10 +363,11 @@ __global__ void __launch_bounds__(kThreads) norm_kernel(const __grid_constant__ 
 
 // ---------------------------------------------------------------------------
 // Rows in chunks of 16 features, aligned: most heads.  Arithmetic is in pairs of
-// features; weights are read from shared memory where a row needs them, which leaves
-// registers for rows in flight (with everything in registers, one feature at a time, 12
-// warps fitted an SM and 32 heads x 8192 x 128, bf16, took 39 us forward, 53 backward
-// and 121 for the second derivative).
+// features; rows come through shared memory, a row ahead of the one that is worked on, and
+// weights are read from there where a row needs them.  32 heads x 8192 x 128, bf16, with the
+// sums over rows: 31 us forward, 50 backward and 75 for the second derivative (4.3 to 4.5
+// TB/s).  With rows loaded into registers 33, 62 and 93; with everything in registers, one
+// feature at a time, 39, 59 and 127.
 // ---------------------------------------------------------------------------
 using f2 = float2;
 __device__ __forceinline__ f2 fma2(f2 a, f2 b, f2 c) { return __ffma2_rn(a, b, c); }
@@ -379,46 +381,50 @@ struct Pair16 {  // the two runs of a chunk
   Half u, v;
 };
 
+// A lane's 16 features of a row, on their way through shared memory: each thread copies
+// its own pieces of 16 bytes, as many rows ahead as the ring holds, and no other reads them.
 template <typename T>
-struct Raw16;
-template <>
-struct Raw16<__nv_bfloat16> {
-  uint4 a, b;
-  __device__ __forceinline__ void load(const __nv_bfloat16* p, int e0, int e1) {
-    a = *reinterpret_cast<const uint4*>(p + e0);
-    b = *reinterpret_cast<const uint4*>(p + e1);
+constexpr int kPieces = 2 * 8 * (int)sizeof(T) / 16;
+
+// A lane's fp32 run is two pieces, half a sector each: through L1, where the second finds
+// what the first brought.
+template <typename T>
+__device__ __forceinline__ void copy16(uint32_t to, const T* from) {
+  if (sizeof(T) == 2) asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(to), "l"(from) : "memory");
+  else asm volatile("cp.async.ca.shared.global [%0], [%1], 16;" ::"r"(to), "l"(from) : "memory");
+}
+template <typename T>
+__device__ __forceinline__ void copy_row(uint32_t to, const T* p, int e0, int e1) {
+#pragma unroll
+  for (int i = 0; i < kPieces<T> / 2; ++i) {
+    copy16(to + i * kThreads * 16, p + e0 + i * 16 / (int)sizeof(T));
+    copy16(to + (i + kPieces<T> / 2) * kThreads * 16, p + e1 + i * 16 / (int)sizeof(T));
   }
-  static __device__ __forceinline__ void wide(const uint4& x, Half& h) {
+}
+template <typename T>
+__device__ __forceinline__ void get_row(Pair16& r, const uint4* from);
+template <>
+__device__ __forceinline__ void get_row<__nv_bfloat16>(Pair16& r, const uint4* from) {
+#pragma unroll
+  for (int k = 0; k < 2; ++k) {
+    const uint4 x = from[k * kThreads];
     const uint32_t w[4] = {x.x, x.y, x.z, x.w};
+    Half& h = k ? r.v : r.u;
 #pragma unroll
     for (int i = 0; i < 4; ++i)
       h.p[i] = f2{__uint_as_float(w[i] << 16), __uint_as_float(w[i] & 0xffff0000u)};
   }
-  __device__ __forceinline__ void get(Pair16& r) const {
-    wide(a, r.u);
-    wide(b, r.v);
-  }
-};
+}
 template <>
-struct Raw16<float> {
-  float4 a[2], b[2];
-  __device__ __forceinline__ void load(const float* p, int e0, int e1) {
+__device__ __forceinline__ void get_row<float>(Pair16& r, const uint4* from) {
 #pragma unroll
-    for (int i = 0; i < 2; ++i) {
-      a[i] = reinterpret_cast<const float4*>(p + e0)[i];
-      b[i] = reinterpret_cast<const float4*>(p + e1)[i];
-    }
+  for (int k = 0; k < 4; ++k) {
+    const float4 x = *reinterpret_cast<const float4*>(from + k * kThreads);
+    Half& h = k < 2 ? r.u : r.v;
+    h.p[2 * (k & 1)] = f2{x.x, x.y};
+    h.p[2 * (k & 1) + 1] = f2{x.z, x.w};
   }
-  __device__ __forceinline__ void get(Pair16& r) const {
-#pragma unroll
-    for (int i = 0; i < 2; ++i) {
-      r.u.p[2 * i] = f2{a[i].x, a[i].y};
-      r.u.p[2 * i + 1] = f2{a[i].z, a[i].w};
-      r.v.p[2 * i] = f2{b[i].x, b[i].y};
-      r.v.p[2 * i + 1] = f2{b[i].z, b[i].w};
-    }
-  }
-};
+}
 __device__ __forceinline__ void put8(__nv_bfloat16* p, const Half& h) {
   __nv_bfloat162 t[4];
 #pragma unroll
@@ -482,18 +488,23 @@ struct Turn8 {
   }
 };
 
-// Rows whose loads are in flight together, and blocks an SM is to hold.
-template <int OP, typename TI, typename TO>
-constexpr int kFlight = OP == kForward ? (sizeof(TI) == 2 ? 4 : 2) : OP == kBackward ? 2 : 1;
+// Blocks an SM is to hold, 16-byte pieces of a thread's row, and rows of its ring (four to
+// sixteen rows were no faster than two: what is in flight at 12 to 24 warps is enough then).
 template <int OP>
-constexpr int kResident = OP == kForward ? 5 : 3;
+constexpr int kResident = OP == kForward ? 6 : OP == kBackward ? 4 : 3;
+template <int OP, typename TI, typename TO>
+constexpr int kRowPieces = kPieces<TI> + (OP == kForward ? 0 : kPieces<TO>) + (OP == kSecond ? kPieces<TI> : 0);
+constexpr int kDeep = 2;
 
 template <int OP, typename TI, typename TO, bool INTERLEAVED>
 __global__ void __launch_bounds__(kThreads, kResident<OP>) norm_rows(const __grid_constant__ NormArgs a) {
   extern __shared__ __align__(16) unsigned long long turns[];
-  float* const sw = reinterpret_cast<float*>(turns + ((a.half + 1) & ~1));
+  constexpr int D = kDeep, R = kRowPieces<OP, TI, TO>;
+  uint4* const ring = reinterpret_cast<uint4*>(turns);  // [D][R][threads]
+  unsigned long long* const table = reinterpret_cast<unsigned long long*>(ring + D * R * kThreads);
+  float* const sw = reinterpret_cast<float*>(table + ((a.half + 1) & ~1));
   float* const sc = sw + a.d;
-  constexpr int U = kFlight<OP, TI, TO>;
+  if (OP != kForward) asm volatile("griddepcontrol.launch_dependents;" ::: "memory");  // norm_sums
   const bool second_side = blockIdx.x >= (unsigned)a.side[0].blocks;
   const Side& s = a.side[second_side];
   const int block = blockIdx.x - (second_side ? a.side[0].blocks : 0);
@@ -503,8 +514,59 @@ __global__ void __launch_bounds__(kThreads, kResident<OP>) norm_rows(const __gri
   const bool have = lane < a.d / 16, turned = lane < rot;
   const int e0 = turned ? (INTERLEAVED ? 16 : 8) * lane : 2 * a.half + (lane - rot) * 16;
   const int e1 = turned && !INTERLEAVED ? e0 + a.half : e0 + 8;
+  const long long items = (long long)a.B * a.N;
+  // a unit's first head, the end of its heads, and this thread's row of it, if any
+  auto unit_at = [&](long long unit, int& h0, int& h1, int& b, int& n) -> bool {
+    const long long ib = s.groups == 1 ? unit : unit / s.groups;
+    h0 = (int)(unit - ib * s.groups) * s.heads;
+    h1 = min(s.H, h0 + s.heads);
+    const long long item = ib * per_block + group;
+    const bool active = item < items && have;  // the other lanes only take part in exchanges
+    b = active ? (int)(item / a.N) : 0;
+    n = active ? (int)(item - (long long)b * a.N) : 0;
+    return active;
+  };
 
-  turns_table<kThreads>(turns, a.inv_freq, a.half);
+  // the next row to copy
+  long long c_unit = block;
+  int c_left = 0, c_slot = 0;
+  bool c_active = false;
+  const TI *cx = nullptr, *cca = nullptr;
+  const TO* cdy = nullptr;
+  const uint32_t ring_at = smem_u32(ring + threadIdx.x);
+  auto enter_unit = [&] {
+    if (c_unit >= s.units) return;
+    int h0, h1, b, n;
+    c_active = unit_at(c_unit, h0, h1, b, n);
+    c_left = h1 - h0;
+    cx = static_cast<const TI*>(s.x) + b * s.xs[0] + n * s.xs[2] + h0 * s.xs[1];
+    if (OP != kForward) cdy = static_cast<const TO*>(s.dy) + b * s.dys[0] + n * s.dys[2] + h0 * s.dys[1];
+    if (OP == kSecond && s.a) cca = static_cast<const TI*>(s.a) + b * s.as[0] + n * s.as[2] + h0 * s.as[1];
+  };
+  auto copy_next = [&] {
+    if (c_unit < s.units) {
+      if (c_active) {
+        const uint32_t to = ring_at + c_slot * (R * kThreads * 16);
+        copy_row(to, cx, e0, e1);
+        if (OP != kForward) copy_row(to + kPieces<TI> * kThreads * 16, cdy, e0, e1);
+        if (OP == kSecond && s.a) copy_row(to + (kPieces<TI> + kPieces<TO>)*kThreads * 16, cca, e0, e1);
+      }
+      cx += s.xs[1];
+      if (OP != kForward) cdy += s.dys[1];
+      if (OP == kSecond && s.a) cca += s.as[1];
+      if (--c_left == 0) {
+        c_unit += s.blocks;
+        enter_unit();
+      }
+    }
+    c_slot = c_slot + 1 == D ? 0 : c_slot + 1;
+    asm volatile("cp.async.commit_group;" ::: "memory");
+  };
+  enter_unit();
+#pragma unroll 1
+  for (int i = 0; i < D; ++i) copy_next();
+
+  turns_table<kThreads>(table, a.inv_freq, a.half);
   for (int i = threadIdx.x; i < a.d; i += kThreads) {
     sw[i] = s.w ? vector_at(s.w, a.w_bf16, i) : 1.f;
     if (OP == kSecond) sc[i] = s.c ? vector_at(s.c, a.w_bf16, i) : 0.f;
@@ -514,62 +576,49 @@ __global__ void __launch_bounds__(kThreads, kResident<OP>) norm_rows(const __gri
 #pragma unroll
   for (int i = 0; i < 4; ++i) acc.u.p[i] = acc.v.p[i] = both(0.f);
 
-  const long long items = (long long)a.B * a.N;
+  int slot = 0;
   for (long long unit = block; unit < s.units; unit += s.blocks) {
-    const long long ib = s.groups == 1 ? unit : unit / s.groups;
-    const int h0 = (int)(unit - ib * s.groups) * s.heads, h1 = min(s.H, h0 + s.heads);
-    const long long item = ib * per_block + group;
-    const bool active = item < items && have;  // the other lanes only take part in exchanges
-    const int b = active ? (int)(item / a.N) : 0, n = active ? (int)(item - (long long)b * a.N) : 0;
-    const TI* x = static_cast<const TI*>(s.x) + b * s.xs[0] + n * s.xs[2] + h0 * s.xs[1];
-    const TO* dy = static_cast<const TO*>(s.dy) + b * s.dys[0] + n * s.dys[2] + h0 * s.dys[1];
-    const TI* ca = static_cast<const TI*>(s.a) + b * s.as[0] + n * s.as[2] + h0 * s.as[1];
+    int h0, h1, b, n;
+    const bool active = unit_at(unit, h0, h1, b, n);
     using TY = typename std::conditional<OP == kForward, TO, TI>::type;
     TY* y = static_cast<TY*>(s.y) + b * s.ys[0] + n * s.ys[2] + h0 * s.ys[1];
     TO* ddy = static_cast<TO*>(s.ddy) + b * s.ddys[0] + n * s.ddys[2] + h0 * s.ddys[1];
     Turn8 t8;
-    for (int hb = h0; hb < h1; hb += U) {
-      Raw16<TI> rx[U], ra[U];
-      Raw16<TO> rdy[U];
+    const long long p = !active ? 0 : a.positions ? a.positions[b * a.pos_sb + n] : a.offset + n;
 #pragma unroll
-      for (int i = 0; i < U; ++i)
-        if (active && hb + i < h1) {
-          rx[i].load(x, e0, e1);
-          x += s.xs[1];
-          if (OP != kForward) {
-            rdy[i].load(dy, e0, e1);
-            dy += s.dys[1];
-          }
-          if (OP == kSecond && s.a) {
-            ra[i].load(ca, e0, e1);
-            ca += s.as[1];
-          }
-        }
-      if (hb == h0) {
-        const long long p = !active ? 0 : a.positions ? a.positions[b * a.pos_sb + n] : a.offset + n;
-#pragma unroll
-        for (int i = 0; i < 8; ++i) {
-          float sn = 0.f, cs = 1.f;
-          if (turned) {
-            sincos_turns((uint32_t)(((unsigned long long)p * turns[8 * lane + i] + 0x80000000ull) >> 32), sn, cs);
-            sn *= a.magnitude;
-            cs *= a.magnitude;
-          }
-          t8.cs[i] = cs;
-          t8.sn[i] = sn;
-        }
+    for (int i = 0; i < 8; ++i) {
+      float sn = 0.f, cs = 1.f;
+      if (turned) {
+        sincos_turns((uint32_t)(((unsigned long long)p * table[8 * lane + i] + 0x80000000ull) >> 32), sn, cs);
+        sn *= a.magnitude;
+        cs *= a.magnitude;
       }
+      t8.cs[i] = cs;
+      t8.sn[i] = sn;
+    }
+#pragma unroll 1
+    for (int head = h0; head < h1; ++head) {
+      asm volatile("cp.async.wait_group %0;" ::"n"(D - 1) : "memory");
+      const uint4* from = ring + (size_t)slot * R * kThreads + threadIdx.x;
+      slot = slot + 1 == D ? 0 : slot + 1;
+      Pair16 xv, g, av;
+      if (active) {
+        get_row<TI>(xv, from);
+        if (OP != kForward) get_row<TO>(g, from + kPieces<TI> * kThreads);
+      } else {
 #pragma unroll
-      for (int k = 0; k < U; ++k) {
-        if (hb + k >= h1) break;  // the same for the whole block
-        Pair16 xv, g;
-        if (active) {
-          rx[k].get(xv);
-          if (OP != kForward) rdy[k].get(g);
+        for (int i = 0; i < 4; ++i) xv.u.p[i] = xv.v.p[i] = g.u.p[i] = g.v.p[i] = both(0.f);
+      }
+      if (OP == kSecond) {
+        if (active && s.a) {
+          get_row<TI>(av, from + (kPieces<TI> + kPieces<TO>)*kThreads);
         } else {
 #pragma unroll
-          for (int i = 0; i < 4; ++i) xv.u.p[i] = xv.v.p[i] = g.u.p[i] = g.v.p[i] = both(0.f);
+          for (int i = 0; i < 4; ++i) av.u.p[i] = av.v.p[i] = both(0.f);
         }
+      }
+      copy_next();  // into the slot that was just read
+      {
         if (OP == kForward) {
           float sum[1] = {dot16(xv, xv)};
           row_sums(sum, a.lanes);
@@ -615,13 +664,6 @@ __global__ void __launch_bounds__(kThreads, kResident<OP>) norm_rows(const __gri
           put8(y + e1, xv.v);
           y += s.ys[1];
         } else {
-          Pair16 av;
-          if (active && s.a) {
-            ra[k].get(av);
-          } else {
-#pragma unroll
-            for (int i = 0; i < 4; ++i) av.u.p[i] = av.v.p[i] = both(0.f);
-          }
           t8.template apply<INTERLEAVED, true>(g);
           // <x, x>, <h, x>, <a, x>, <h, a>, <c . g, x>
           float sum[5] = {dot16(xv, xv), 0.f, dot16(av, xv), 0.f, 0.f};
@@ -679,7 +721,8 @@ __global__ void __launch_bounds__(kThreads, kResident<OP>) norm_rows(const __gri
     }
   }
   if (OP == kForward || !s.sums) return;
-  float* const red = sc + (OP == kSecond ? a.d : 0);  // [per_block][d]
+  __syncthreads();  // every thread is past its last row
+  float* const red = reinterpret_cast<float*>(ring);  // [per_block][d]: 8 KB at most
   if (have) {
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
@@ -701,9 +744,12 @@ struct SumArgs {
 __global__ void __launch_bounds__(1024) norm_sums(SumArgs a) {
   __shared__ float sm[32][33];
   const int t = blockIdx.y, f = blockIdx.x * 32 + (threadIdx.x & 31), part = threadIdx.x >> 5;
+  asm volatile("griddepcontrol.wait;" ::: "memory");  // launched while the rows' kernel ends
   float s = 0.f;
-  if (f < a.d)
+  if (f < a.d) {
+#pragma unroll 8
     for (int b = part; b < a.blocks[t]; b += 32) s += a.partial[((size_t)a.first[t] + b) * a.d + f];
+  }
   sm[part][threadIdx.x & 31] = s;
   __syncthreads();
   s = warp_sum(sm[threadIdx.x & 31][part]);
@@ -750,12 +796,19 @@ void plan(NormArgs& a, int P, int C, int per_sm) {
 // P = 8: norm_rows; else norm_kernel.
 template <int OP, typename TI, typename TO, int P, int C, bool INTERLEAVED>
 cudaError_t launch(NormArgs& a, LaunchLog& log) {
-  plan(a, P, C, P == 8 ? kResident<OP> * (OP == kForward ? 2 : 1) : kBlocksPerSm);
+  plan(a, P, C, P == 8 ? kResident<OP> : kBlocksPerSm);
   size_t smem = sizeof(unsigned long long) * ((a.half + 1) & ~1) + sizeof(float) * a.d * (OP == kSecond ? 2 : 1);
-  smem += OP == kForward ? 0 : sizeof(float) * a.d * (kThreads / a.lanes);
   const unsigned grid = (unsigned)(a.side[0].blocks + a.side[1].blocks);
-  if constexpr (P == 8) norm_rows<OP, TI, TO, INTERLEAVED><<<grid, kThreads, smem, log.stream>>>(a);
-  else norm_kernel<OP, TI, TO, P, C, INTERLEAVED><<<grid, kThreads, smem, log.stream>>>(a);
+  if constexpr (P == 8) {
+    smem += sizeof(uint4) * kThreads * kDeep * kRowPieces<OP, TI, TO>;
+    const cudaError_t e = cudaFuncSetAttribute(norm_rows<OP, TI, TO, INTERLEAVED>,
+                                               cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
+    if (e != cudaSuccess) return e;
+    norm_rows<OP, TI, TO, INTERLEAVED><<<grid, kThreads, smem, log.stream>>>(a);
+  } else {
+    smem += OP == kForward ? 0 : sizeof(float) * a.d * (kThreads / a.lanes);
+    norm_kernel<OP, TI, TO, P, C, INTERLEAVED><<<grid, kThreads, smem, log.stream>>>(a);
+  }
   const cudaError_t e = cudaGetLastError();
   log.mark();
   return e;
@@ -894,8 +947,16 @@ int call(int op, const fbob_qk_norm_t* s, const fbob_norm_side_t* q, const fbob_
     r.partial = a.partial;
     r.d = a.d;
     r.bf16 = a.w_bf16;
-    norm_sums<<<dim3((unsigned)(a.d + 31) / 32, 2), 1024, 0, log.stream>>>(r);
-    e = cudaGetLastError();
+    cudaLaunchConfig_t c = {};
+    c.gridDim = dim3((unsigned)(a.d + 31) / 32, 2);
+    c.blockDim = dim3(1024);
+    c.stream = log.stream;
+    cudaLaunchAttribute early;
+    early.id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    early.val.programmaticStreamSerializationAllowed = 1;
+    c.attrs = &early;
+    c.numAttrs = 1;
+    e = cudaLaunchKernelEx(&c, norm_sums, r);
     log.mark();
   }
   end_call(log);
