@@ -378,13 +378,15 @@ struct Plan {
   int xt[kMaxSteps];                                // terms of X
   double M[kMaxSteps];                              // bound on X's singular values
   int square_parts;
+  // sums of products are added up in parts (orth_chain.cu)
+  bool split() const { return !bf16 || q > 65536; }
 };
 
 // Columns of a product's tiles: 128 where that fills more of the GPU.  A tile costs its
 // multiplications (128 columns 0.8 of what 256 do: half, less well fed), in stages of
 // 64 elements, and as much as 8 stages beside them.
 int choose_wide(const Plan& p, int cols, int depth, bool sym, int segs) {
-  if (!p.bf16) return 128;  // two terms: the finishing warps hold sums of 128 columns
+  if (p.split()) return 128;  // the finishing warps hold sums of 128 columns
   double best = 0;
   int wide = 0;
   for (int w : {256, 128}) {
@@ -683,7 +685,9 @@ struct Chain {
   cudaError_t launch(LaunchLog& log) {
     if (!ok) return cudaErrorUnknown;
     g.items = items;
-    return launch_chain(g, !p.bf16, log);
+    // parts of 64 elements, longer where there would be more than 4096 of them to add
+    g.part = p.bf16 ? 64 : 3 * ((p.q + 64 * 4096 - 1) / (64 * 4096));
+    return launch_chain(g, p.split(), log);
   }
 };
 

@@ -63,6 +63,7 @@ struct ChainArgs {
   CUtensorMap maps[kMaxMaps];
   Phase phase[kMaxPhases];
   int phases, items;
+  int part;                     // split: stages of an accumulator
   int rows, cols, count;        // p, q of the caller's tensor, and matrices
   const MatInfo* info;
   void* y;
@@ -80,7 +81,7 @@ inline long long tiles_of(int rows, int cols, bool sym, int wide) {  // of one m
   return sym ? kHigh / wide * tm * (tm + 1) / 2 : tm * tn;
 }
 
-// split: two-term operands, tiles of 128 columns.
+// split: sums in parts, tiles of 128 columns.
 cudaError_t launch_chain(const ChainArgs& g, bool split, LaunchLog& log);
 
 // A small matrix's steps, or their gradient, in one block (orth_small.cu).  Factors of

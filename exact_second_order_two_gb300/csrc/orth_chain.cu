@@ -190,14 +190,13 @@ __device__ __forceinline__ int slots_of(const Phase& p, const ChainArgs& g) {
   return p.sym || p.e_terms == 2 || p.o_terms == 2 || (p.o_terms == 0 && !g.y_bf16) ? 1 : 2;
 }
 
-// SPLIT: two-term operands.  The tensor cores cut each addition off to the accumulator's 24
-// bits, always towards zero, which over a long contraction would be the largest error by
-// far (a steep polynomial of a result near 1 enlarges it ten times: 512 x 2048 was 5.6e-6 off
-// with sums of 256 elements, the same in fp32 torch 2.8e-6).  So the accumulator takes 64
-// elements at a time, the products with low terms first, and the finishing warps add
-// these sums up, rounded.
-constexpr int kSplit = 3;  // stages: the pairs of terms of a product
-
+// SPLIT.  The tensor cores cut each addition off to the accumulator's 24 bits, always
+// towards zero, which over a long contraction would be the largest error by far (a
+// steep polynomial of a result near 1 enlarges it ten times: 512 x 2048, fp32, was 5.6e-6 off
+// with sums of 256 elements, the same in fp32 torch 2.8e-6).  So the accumulator takes
+// g.part stages at a time, and the finishing warps add these sums up, rounded: for two-term
+// operands 64 elements (more above 2^18), the products with low terms first; for one term
+// 4096, where there are more than 65536 (1 x 2^22 was 3.5% off in one sum).
 template <bool SPLIT>
 __global__ void __launch_bounds__(kThreads, 1) chain(const __grid_constant__ ChainArgs g) {
   extern __shared__ __align__(1024) uint8_t smem[];
@@ -401,7 +400,7 @@ __global__ void __launch_bounds__(kThreads, 1) chain(const __grid_constant__ Cha
         const bool nn = p.nn;
         const uint32_t id = idesc_f16(kHigh, p.wide, nn);
         const int total = p.nseg * ((p.depth + kDepth - 1) / kDepth);
-        const int part = SPLIT ? kSplit : total;
+        const int part = SPLIT ? g.part : total;
         for (int k0 = 0; ok && k0 < total; k0 += part, ++nb) {
           const uint32_t d = tmem + (nb & 1) * kWide;
           if (nb >= 2 && !warp_wait(t_empty + (nb & 1), ((nb >> 1) - 1) & 1, ab, g.status)) {
@@ -552,7 +551,7 @@ __global__ void __launch_bounds__(kThreads, 1) chain(const __grid_constant__ Cha
 #pragma unroll
         for (int k = 0; k < 32; ++k) total[SPLIT ? k : 0] = f2{0.f, 0.f};
         const int stages = p.nseg * ((p.depth + kDepth - 1) / kDepth);
-        for (int k0 = 0; ok && k0 < stages; k0 += kSplit, ++nb) {
+        for (int k0 = 0; ok && k0 < stages; k0 += g.part, ++nb) {
           if (!warp_wait(t_full + (nb & 1), (nb >> 1) & 1, ab, g.status)) {
             ok = false;
             break;

@@ -303,6 +303,46 @@ class TestValues:
         assert forward() == 0 and backward() == 0
         assert torch.equal(y, want[0]) and torch.equal(dG, want[1])
 
+    def test_past_31_bits_of_elements_in_a_stack(self):
+        """The last matrices of 2.2e9 elements are what they are alone."""
+        G = torch.zeros(530, 1024, 4096, dtype=torch.bfloat16, device="cuda")
+        some, dY = gradient((2, 1024, 4096), torch.bfloat16)
+        G[0], G[-1] = some[0], some[1]
+        Y = fbob.orthogonalize(G)
+        for i, k in ((0, 0), (-1, 1)):
+            assert torch.equal(Y[i], fbob.orthogonalize(some[k]))
+        assert (Y[1:-1:50] == 0).all()
+
+    @pytest.mark.parametrize("tall", [False, True])
+    def test_past_32_bits_of_elements_in_a_matrix(self, tall):
+        """A block in the last corner of 4.3e9 elements of zeros: the block's own result,
+        which sums the same products, among zeros."""
+        p, q = 8192, (1 << 19) + 128
+        block, _ = gradient((300, 200), torch.bfloat16)
+        shape = (q, p) if tall else (p, q)
+        G = torch.zeros(shape, dtype=torch.bfloat16, device="cuda")
+        G[-300:, -200:] = block
+        Y = fbob.orthogonalize(G)
+        want, own = exact(block, None, [ONE] * 5)[0], model(block, None, [ONE] * 5)[0]
+        check(Y[-300:, -200:], want, own, torch.bfloat16)
+        Y[-300:, -200:] = 0
+        assert not Y.any()
+
+    def test_many_and_long_matrices(self):
+        """As many matrices, and as long a side, as one launch's grids come to."""
+        for dtype in DT.values():
+            G, _ = gradient((65535, 2, 3), dtype)
+            Y = fbob.orthogonalize(G)
+            check(Y, exact(G, None, [ONE] * 5)[0], model(G, None, [ONE] * 5)[0], dtype)
+            for shape in ((1, 1 << 22), (1 << 22, 2)):
+                G, dY = gradient(shape, dtype)
+                G.requires_grad_()
+                Y = fbob.orthogonalize(G)
+                (dG,) = torch.autograd.grad(Y, G, dY)
+                (X, want), (mY, mG) = exact(G, dY, [ONE] * 5), model(G, dY, [ONE] * 5)
+                check(Y, X, mY, dtype)
+                check(dG, want, mG, dtype)
+
     def test_nothing_is_written_outside(self):
         """Outputs and workspaces of the C calls between guards, at sizes off every tile."""
         for dtype in DT.values():
