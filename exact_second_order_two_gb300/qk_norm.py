@@ -49,6 +49,9 @@ def _like(x):
 
 
 def _side(x, w, y, dy=None, a=None, c=None, dw=None, ddy=None):
+    if dy is None:  # forward
+        return _pack_side(x.shape[1], x.data_ptr(), 0 if w is None else w.data_ptr(), 0, 0, 0, y.data_ptr(),
+                          0, 0, *x.stride()[:3], *_NONE, *_NONE, *y.stride()[:3], *_NONE)
     at = [0 if t is None else t.data_ptr() for t in (x, w, dy, a, c, y, dw, ddy)]
     return _pack_side(x.shape[1], *at, *x.stride()[:3], *_strides(dy), *_strides(a), *y.stride()[:3],
                       *_strides(ddy))
@@ -146,6 +149,15 @@ class _QkNormBackward(torch.autograd.Function):
         return *out, None, None, None, None
 
 
+def _weight(name, w, d, device):
+    """A weight's dtype, checked."""
+    if w.device != device or w.dim() != 1 or w.shape[0] != d:
+        raise ValueError(f"{name} must be [{d}] on {device}")
+    if w.dtype not in _b.DTYPES:
+        raise TypeError(f"unsupported {name} dtype {w.dtype}; use bfloat16 or float32")
+    return w.dtype
+
+
 def qk_norm_rotary(q: torch.Tensor, k: torch.Tensor, q_weight: torch.Tensor | None = None,
                    k_weight: torch.Tensor | None = None, inv_freq: torch.Tensor | None = None,
                    positions=None, *, eps: float = 1e-6, interleaved: bool = False,
@@ -171,25 +183,23 @@ def qk_norm_rotary(q: torch.Tensor, k: torch.Tensor, q_weight: torch.Tensor | No
             raise _b.FbobError(1, f"qk_norm_rotary: {name} must be a CUDA tensor")
         if t.dim() != 4:
             raise ValueError(f"{name} must be [B, heads, N, d]")
-    dtype = q.dtype if dtype is None else dtype
-    if q.dtype not in _b.DTYPES or dtype not in _b.DTYPES:
-        raise TypeError(f"unsupported dtypes {q.dtype}, {dtype}; use bfloat16 or float32")
-    if k.dtype != q.dtype or k.device != q.device:
-        raise ValueError(f"k must match q: {q.dtype} on {q.device}")
-    B, H, N, d = q.shape
+    shape, device, in_dtype = q.shape, q.device, q.dtype
+    if dtype is None:
+        dtype = in_dtype
+    if in_dtype not in _b.DTYPES or dtype not in _b.DTYPES:
+        raise TypeError(f"unsupported dtypes {in_dtype}, {dtype}; use bfloat16 or float32")
+    if k.dtype != in_dtype or k.device != device:
+        raise ValueError(f"k must match q: {in_dtype} on {device}")
+    B, _, N, d = shape
     if k.shape[0] != B or k.shape[2] != N or k.shape[3] != d:
         raise ValueError(f"k must be [{B}, heads, {N}, {d}] to go with q")
-    weight_dtype = None
-    for name, w in (("q_weight", q_weight), ("k_weight", k_weight)):
-        if w is None:
-            continue
-        if w.device != q.device or tuple(w.shape) != (d,):
-            raise ValueError(f"{name} must be [{d}] on {q.device}")
-        if w.dtype not in _b.DTYPES:
-            raise TypeError(f"unsupported {name} dtype {w.dtype}; use bfloat16 or float32")
-        if weight_dtype not in (None, w.dtype):
+    weight_dtype = torch.float32
+    if q_weight is not None:
+        weight_dtype = _weight("q_weight", q_weight, d, device)
+    if k_weight is not None:
+        if _weight("k_weight", k_weight, d, device) != weight_dtype and q_weight is not None:
             raise ValueError("the weights must have one dtype")
-        weight_dtype = w.dtype
+        weight_dtype = k_weight.dtype
     if not (eps >= 0 and math.isfinite(eps)):
         raise ValueError(f"eps must be at least 0 and finite, got {eps}")
     if not math.isfinite(magnitude):
@@ -197,14 +207,16 @@ def qk_norm_rotary(q: torch.Tensor, k: torch.Tensor, q_weight: torch.Tensor | No
     offset, turned = 0, 0
     if inv_freq is not None:
         inv_freq, positions, offset = _angles(inv_freq, positions, q)
-        turned = 2 * inv_freq.numel()
+        turned = 2 * inv_freq.shape[0]
     elif positions is not None:
         raise ValueError("positions need inv_freq")
-    problem = _pack(B, N, d, turned, bool(interleaved), _b.DTYPES[q.dtype], _b.DTYPES[dtype],
-                    _b.DTYPES[weight_dtype or torch.float32], eps, magnitude,
+    problem = _pack(B, N, d, turned, bool(interleaved), _b.DTYPES[in_dtype], _b.DTYPES[dtype],
+                    _b.DTYPES[weight_dtype], eps, magnitude,
                     0 if positions is None else positions.stride(0), offset)
     tensors = (_rows(q), _rows(k), _rows(q_weight), _rows(k_weight))
-    seen = torch.is_grad_enabled() and any(t is not None and t.requires_grad for t in tensors)
+    seen = torch.is_grad_enabled() and (
+        q.requires_grad or k.requires_grad or (q_weight is not None and q_weight.requires_grad)
+        or (k_weight is not None and k_weight.requires_grad))
     if seen or _b.dual(*tensors):
         return _QkNorm.apply(*tensors, inv_freq, positions, problem, dtype)
     return _forward(*tensors, inv_freq, positions, problem, dtype)
