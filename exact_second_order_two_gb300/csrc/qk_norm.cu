@@ -16,7 +16,9 @@
 // cosine serve them all; queries and keys are one launch.  The sums over rows
 // are carried in registers by blocks that stay (a few per SM), added up in the block
 // through shared memory, and over the blocks by a second launch: every sum in a
-// fixed order.
+// fixed order.  norm_rows takes chunks of 16 or 8 features, norm_kernel what is left (odd
+// widths, odd addresses), a feature at a time: 16 heads x 27679 x 37, bf16, 85, 167 and 224 us,
+// a third of the other's rate.
 #include <cuda_bf16.h>
 #include <cuda_runtime.h>
 #include <stdint.h>
@@ -362,10 +364,10 @@ __global__ void __launch_bounds__(kThreads) norm_kernel(const __grid_constant__ 
 
 
 // ---------------------------------------------------------------------------
-// Rows in chunks of 16 features, aligned: most heads.  Arithmetic is in pairs of
+// Rows in chunks of 16 or 8 features, aligned: nearly all heads.  Arithmetic is in pairs of
 // features; rows come through shared memory, a row ahead of the one that is worked on, and
 // weights are read from there where a row needs them.  32 heads x 8192 x 128, bf16, with the
-// sums over rows: 31 us forward, 50 backward and 75 for the second derivative (4.3 to 4.5
+// sums over rows: 33 us forward, 48 backward and 73 for the second derivative (4.0 to 4.6
 // TB/s).  With rows loaded into registers 33, 62 and 93; with everything in registers, one
 // feature at a time, 39, 59 and 127.
 // ---------------------------------------------------------------------------
@@ -374,72 +376,95 @@ __device__ __forceinline__ f2 fma2(f2 a, f2 b, f2 c) { return __ffma2_rn(a, b, c
 __device__ __forceinline__ f2 mul2(f2 a, f2 b) { return __fmul2_rn(a, b); }
 __device__ __forceinline__ f2 both(float a) { return f2{a, a}; }
 
-struct Half {  // 8 features
-  f2 p[4];
+template <int P>
+struct Run {  // P features
+  f2 p[P / 2];
 };
-struct Pair16 {  // the two runs of a chunk
-  Half u, v;
+template <int P>
+struct Runs {  // the two runs of a chunk
+  Run<P> u, v;
 };
-
-// A lane's 16 features of a row, on their way through shared memory: each thread copies
-// its own pieces of 16 bytes, as many rows ahead as the ring holds, and no other reads them.
-template <typename T>
-constexpr int kPieces = 2 * 8 * (int)sizeof(T) / 16;
-
-// A lane's fp32 run is two pieces, half a sector each: through L1, where the second finds
-// what the first brought.
-template <typename T>
-__device__ __forceinline__ void copy16(uint32_t to, const T* from) {
-  if (sizeof(T) == 2) asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(to), "l"(from) : "memory");
-  else asm volatile("cp.async.ca.shared.global [%0], [%1], 16;" ::"r"(to), "l"(from) : "memory");
-}
-template <typename T>
-__device__ __forceinline__ void copy_row(uint32_t to, const T* p, int e0, int e1) {
+template <int P>
+__device__ __forceinline__ void clear(Runs<P>& r) {
 #pragma unroll
-  for (int i = 0; i < kPieces<T> / 2; ++i) {
-    copy16(to + i * kThreads * 16, p + e0 + i * 16 / (int)sizeof(T));
-    copy16(to + (i + kPieces<T> / 2) * kThreads * 16, p + e1 + i * 16 / (int)sizeof(T));
+  for (int i = 0; i < P / 2; ++i) r.u.p[i] = r.v.p[i] = both(0.f);
+}
+
+// A lane's two runs of a row, on their way through shared memory: each thread copies its
+// own pieces, as many rows ahead as the ring holds, and no other reads them.  Pieces are 16
+// bytes, or a whole run of 8.
+template <typename T, int P>
+constexpr int kPiece = P * (int)sizeof(T) < 16 ? P * (int)sizeof(T) : 16;
+template <typename T, int P>
+constexpr int kRowBytes = 2 * P * (int)sizeof(T) * kThreads;  // of a block's threads
+
+template <int BYTES>
+__device__ __forceinline__ void copy_piece(uint32_t to, const void* from, bool whole) {
+  // fp32 runs are pieces of half a sector each, runs of 8 bytes less: through L1, where one
+  // finds what another brought
+  if (BYTES == 16 && whole) asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(to), "l"(from) : "memory");
+  else asm volatile("cp.async.ca.shared.global [%0], [%1], %2;" ::"r"(to), "l"(from), "n"(BYTES) : "memory");
+}
+template <typename T, int P>
+__device__ __forceinline__ void copy_row(uint32_t to, const T* p, int e0, int e1) {
+  constexpr int B = kPiece<T, P>, N = P * (int)sizeof(T) / B;  // pieces of a run
+  to += threadIdx.x * B;
+#pragma unroll
+  for (int i = 0; i < N; ++i) {
+    copy_piece<B>(to + i * kThreads * B, p + e0 + i * B / (int)sizeof(T), N == 1);
+    copy_piece<B>(to + (i + N) * kThreads * B, p + e1 + i * B / (int)sizeof(T), N == 1);
   }
 }
-template <typename T>
-__device__ __forceinline__ void get_row(Pair16& r, const uint4* from);
-template <>
-__device__ __forceinline__ void get_row<__nv_bfloat16>(Pair16& r, const uint4* from) {
+template <int P>
+__device__ __forceinline__ void get_row(Runs<P>& r, const uint8_t* from, const __nv_bfloat16*) {
+  from += threadIdx.x * kPiece<__nv_bfloat16, P>;
 #pragma unroll
   for (int k = 0; k < 2; ++k) {
-    const uint4 x = from[k * kThreads];
-    const uint32_t w[4] = {x.x, x.y, x.z, x.w};
-    Half& h = k ? r.v : r.u;
+    uint32_t w[P / 2];
+    const uint8_t* at = from + k * kThreads * kPiece<__nv_bfloat16, P>;
+    if (P == 8) {
+      const uint4 x = *reinterpret_cast<const uint4*>(at);
+      w[0] = x.x; w[1] = x.y; w[P / 2 - 2] = x.z; w[P / 2 - 1] = x.w;
+    } else {
+      const uint2 x = *reinterpret_cast<const uint2*>(at);
+      w[0] = x.x; w[1] = x.y;
+    }
+    Run<P>& h = k ? r.v : r.u;
 #pragma unroll
-    for (int i = 0; i < 4; ++i)
+    for (int i = 0; i < P / 2; ++i)
       h.p[i] = f2{__uint_as_float(w[i] << 16), __uint_as_float(w[i] & 0xffff0000u)};
   }
 }
-template <>
-__device__ __forceinline__ void get_row<float>(Pair16& r, const uint4* from) {
+template <int P>
+__device__ __forceinline__ void get_row(Runs<P>& r, const uint8_t* from, const float*) {
+  from += threadIdx.x * 16;
 #pragma unroll
-  for (int k = 0; k < 4; ++k) {
-    const float4 x = *reinterpret_cast<const float4*>(from + k * kThreads);
-    Half& h = k < 2 ? r.u : r.v;
-    h.p[2 * (k & 1)] = f2{x.x, x.y};
-    h.p[2 * (k & 1) + 1] = f2{x.z, x.w};
+  for (int k = 0; k < P / 2; ++k) {
+    const float4 x = *reinterpret_cast<const float4*>(from + k * kThreads * 16);
+    Run<P>& h = k < P / 4 ? r.u : r.v;
+    h.p[2 * (k % (P / 4))] = f2{x.x, x.y};
+    h.p[2 * (k % (P / 4)) + 1] = f2{x.z, x.w};
   }
 }
-__device__ __forceinline__ void put8(__nv_bfloat16* p, const Half& h) {
-  __nv_bfloat162 t[4];
+template <int P>
+__device__ __forceinline__ void put_run(__nv_bfloat16* p, const Run<P>& h) {
+  __nv_bfloat162 t[P / 2];
 #pragma unroll
-  for (int i = 0; i < 4; ++i) t[i] = __floats2bfloat162_rn(h.p[i].x, h.p[i].y);
-  *reinterpret_cast<uint4*>(p) = *reinterpret_cast<const uint4*>(t);
+  for (int i = 0; i < P / 2; ++i) t[i] = __floats2bfloat162_rn(h.p[i].x, h.p[i].y);
+  if (P == 8) *reinterpret_cast<uint4*>(p) = *reinterpret_cast<const uint4*>(t);
+  else *reinterpret_cast<uint2*>(p) = *reinterpret_cast<const uint2*>(t);
 }
-__device__ __forceinline__ void put8(float* p, const Half& h) {
+template <int P>
+__device__ __forceinline__ void put_run(float* p, const Run<P>& h) {
 #pragma unroll
-  for (int i = 0; i < 2; ++i)
+  for (int i = 0; i < P / 4; ++i)
     reinterpret_cast<float4*>(p)[i] = make_float4(h.p[2 * i].x, h.p[2 * i].y, h.p[2 * i + 1].x, h.p[2 * i + 1].y);
 }
-__device__ __forceinline__ Half shared8(const float* p) {
-  Half h;
+template <int P>
+__device__ __forceinline__ Run<P> shared_run(const float* p) {
+  Run<P> h;
 #pragma unroll
-  for (int i = 0; i < 2; ++i) {
+  for (int i = 0; i < P / 4; ++i) {
     const float4 t = reinterpret_cast<const float4*>(p)[i];
     h.p[2 * i] = f2{t.x, t.y};
     h.p[2 * i + 1] = f2{t.z, t.w};
@@ -447,29 +472,31 @@ __device__ __forceinline__ Half shared8(const float* p) {
   return h;
 }
 
-__device__ __forceinline__ float dot16(const Pair16& a, const Pair16& b) {
+template <int P>
+__device__ __forceinline__ float dot(const Runs<P>& a, const Runs<P>& b) {
   f2 s = mul2(a.u.p[0], b.u.p[0]), t = mul2(a.v.p[0], b.v.p[0]);
 #pragma unroll
-  for (int i = 1; i < 4; ++i) {
+  for (int i = 1; i < P / 2; ++i) {
     s = fma2(a.u.p[i], b.u.p[i], s);
     t = fma2(a.v.p[i], b.v.p[i], t);
   }
   return (s.x + t.x) + (s.y + t.y);
 }
 
-// Cosines and sines of a chunk's eight pairs; a chunk that is not turned has 1 and 0.
-struct Turn8 {
-  float cs[8], sn[8];
+// Cosines and sines of a chunk's P pairs; a chunk that is not turned has 1 and 0.
+template <int P>
+struct TurnRuns {
+  float cs[P], sn[P];
   // r turned: half layout pairs u[i] with v[i], interleaved neighbours in a run
   template <bool INTERLEAVED, bool INVERSE>
-  __device__ __forceinline__ void apply(Pair16& r) const {
+  __device__ __forceinline__ void apply(Runs<P>& r) const {
 #pragma unroll
-    for (int i = 0; i < 4; ++i) {
+    for (int i = 0; i < P / 2; ++i) {
       if (INTERLEAVED) {
 #pragma unroll
         for (int k = 0; k < 2; ++k) {
           f2& x = k ? r.v.p[i] : r.u.p[i];
-          const float c = cs[4 * k + i], s = INVERSE ? -sn[4 * k + i] : sn[4 * k + i];
+          const float c = cs[P / 2 * k + i], s = INVERSE ? -sn[P / 2 * k + i] : sn[P / 2 * k + i];
           x = f2{fmaf(x.x, c, -x.y * s), fmaf(x.x, s, x.y * c)};
         }
       } else {
@@ -488,20 +515,21 @@ struct Turn8 {
   }
 };
 
-// Blocks an SM is to hold, 16-byte pieces of a thread's row, and rows of its ring (four to
-// sixteen rows were no faster than two: what is in flight at 12 to 24 warps is enough then).
+// Blocks an SM is to hold, bytes of a row of a block's ring, and its rows (four to sixteen
+// were no faster than two: what is in flight at 12 to 24 warps is enough then).
 template <int OP>
 constexpr int kResident = OP == kForward ? 6 : OP == kBackward ? 4 : 3;
-template <int OP, typename TI, typename TO>
-constexpr int kRowPieces = kPieces<TI> + (OP == kForward ? 0 : kPieces<TO>) + (OP == kSecond ? kPieces<TI> : 0);
+template <int OP, typename TI, typename TO, int P>
+constexpr int kRingRow = kRowBytes<TI, P> + (OP == kForward ? 0 : kRowBytes<TO, P>) +
+                         (OP == kSecond ? kRowBytes<TI, P> : 0);
 constexpr int kDeep = 2;
 
-template <int OP, typename TI, typename TO, bool INTERLEAVED>
+template <int OP, typename TI, typename TO, int P, bool INTERLEAVED>
 __global__ void __launch_bounds__(kThreads, kResident<OP>) norm_rows(const __grid_constant__ NormArgs a) {
   extern __shared__ __align__(16) unsigned long long turns[];
-  constexpr int D = kDeep, R = kRowPieces<OP, TI, TO>;
-  uint4* const ring = reinterpret_cast<uint4*>(turns);  // [D][R][threads]
-  unsigned long long* const table = reinterpret_cast<unsigned long long*>(ring + D * R * kThreads);
+  constexpr int D = kDeep, R = kRingRow<OP, TI, TO, P>;
+  uint8_t* const ring = reinterpret_cast<uint8_t*>(turns);  // [D][R]
+  unsigned long long* const table = reinterpret_cast<unsigned long long*>(ring + D * R);
   float* const sw = reinterpret_cast<float*>(table + ((a.half + 1) & ~1));
   float* const sc = sw + a.d;
   if (OP != kForward) asm volatile("griddepcontrol.launch_dependents;" ::: "memory");  // norm_sums
@@ -510,10 +538,10 @@ __global__ void __launch_bounds__(kThreads, kResident<OP>) norm_rows(const __gri
   const int block = blockIdx.x - (second_side ? a.side[0].blocks : 0);
   const int lane = threadIdx.x & (a.lanes - 1), group = threadIdx.x / a.lanes;
   const int per_block = kThreads / a.lanes;  // positions of a unit
-  const int rot = a.half / 8;
-  const bool have = lane < a.d / 16, turned = lane < rot;
-  const int e0 = turned ? (INTERLEAVED ? 16 : 8) * lane : 2 * a.half + (lane - rot) * 16;
-  const int e1 = turned && !INTERLEAVED ? e0 + a.half : e0 + 8;
+  const int rot = a.half / P;
+  const bool have = lane < a.d / (2 * P), turned = lane < rot;
+  const int e0 = turned ? (INTERLEAVED ? 2 * P : P) * lane : 2 * a.half + (lane - rot) * 2 * P;
+  const int e1 = turned && !INTERLEAVED ? e0 + a.half : e0 + P;
   const long long items = (long long)a.B * a.N;
   // a unit's first head, the end of its heads, and this thread's row of it, if any
   auto unit_at = [&](long long unit, int& h0, int& h1, int& b, int& n) -> bool {
@@ -533,7 +561,7 @@ __global__ void __launch_bounds__(kThreads, kResident<OP>) norm_rows(const __gri
   bool c_active = false;
   const TI *cx = nullptr, *cca = nullptr;
   const TO* cdy = nullptr;
-  const uint32_t ring_at = smem_u32(ring + threadIdx.x);
+  const uint32_t ring_at = smem_u32(ring);
   auto enter_unit = [&] {
     if (c_unit >= s.units) return;
     int h0, h1, b, n;
@@ -546,10 +574,10 @@ __global__ void __launch_bounds__(kThreads, kResident<OP>) norm_rows(const __gri
   auto copy_next = [&] {
     if (c_unit < s.units) {
       if (c_active) {
-        const uint32_t to = ring_at + c_slot * (R * kThreads * 16);
-        copy_row(to, cx, e0, e1);
-        if (OP != kForward) copy_row(to + kPieces<TI> * kThreads * 16, cdy, e0, e1);
-        if (OP == kSecond && s.a) copy_row(to + (kPieces<TI> + kPieces<TO>)*kThreads * 16, cca, e0, e1);
+        const uint32_t to = ring_at + c_slot * R;
+        copy_row<TI, P>(to, cx, e0, e1);
+        if (OP != kForward) copy_row<TO, P>(to + kRowBytes<TI, P>, cdy, e0, e1);
+        if (OP == kSecond && s.a) copy_row<TI, P>(to + kRowBytes<TI, P> + kRowBytes<TO, P>, cca, e0, e1);
       }
       cx += s.xs[1];
       if (OP != kForward) cdy += s.dys[1];
@@ -572,9 +600,9 @@ __global__ void __launch_bounds__(kThreads, kResident<OP>) norm_rows(const __gri
     if (OP == kSecond) sc[i] = s.c ? vector_at(s.c, a.w_bf16, i) : 0.f;
   }
   __syncthreads();
-  Pair16 acc;
+  Runs<P> acc;
 #pragma unroll
-  for (int i = 0; i < 4; ++i) acc.u.p[i] = acc.v.p[i] = both(0.f);
+  for (int i = 0; i < P / 2; ++i) acc.u.p[i] = acc.v.p[i] = both(0.f);
 
   int slot = 0;
   for (long long unit = block; unit < s.units; unit += s.blocks) {
@@ -583,13 +611,13 @@ __global__ void __launch_bounds__(kThreads, kResident<OP>) norm_rows(const __gri
     using TY = typename std::conditional<OP == kForward, TO, TI>::type;
     TY* y = static_cast<TY*>(s.y) + b * s.ys[0] + n * s.ys[2] + h0 * s.ys[1];
     TO* ddy = static_cast<TO*>(s.ddy) + b * s.ddys[0] + n * s.ddys[2] + h0 * s.ddys[1];
-    Turn8 t8;
+    TurnRuns<P> t8;
     const long long p = !active ? 0 : a.positions ? a.positions[b * a.pos_sb + n] : a.offset + n;
 #pragma unroll
-    for (int i = 0; i < 8; ++i) {
+    for (int i = 0; i < P; ++i) {
       float sn = 0.f, cs = 1.f;
       if (turned) {
-        sincos_turns((uint32_t)(((unsigned long long)p * table[8 * lane + i] + 0x80000000ull) >> 32), sn, cs);
+        sincos_turns((uint32_t)(((unsigned long long)p * table[P * lane + i] + 0x80000000ull) >> 32), sn, cs);
         sn *= a.magnitude;
         cs *= a.magnitude;
       }
@@ -599,82 +627,82 @@ __global__ void __launch_bounds__(kThreads, kResident<OP>) norm_rows(const __gri
 #pragma unroll 1
     for (int head = h0; head < h1; ++head) {
       asm volatile("cp.async.wait_group %0;" ::"n"(D - 1) : "memory");
-      const uint4* from = ring + (size_t)slot * R * kThreads + threadIdx.x;
+      const uint8_t* from = ring + slot * R;
       slot = slot + 1 == D ? 0 : slot + 1;
-      Pair16 xv, g, av;
+      Runs<P> xv, g, av;
       if (active) {
-        get_row<TI>(xv, from);
-        if (OP != kForward) get_row<TO>(g, from + kPieces<TI> * kThreads);
+        get_row(xv, from, static_cast<const TI*>(nullptr));
+        if (OP != kForward) get_row(g, from + kRowBytes<TI, P>, static_cast<const TO*>(nullptr));
       } else {
 #pragma unroll
-        for (int i = 0; i < 4; ++i) xv.u.p[i] = xv.v.p[i] = g.u.p[i] = g.v.p[i] = both(0.f);
+        for (int i = 0; i < P / 2; ++i) xv.u.p[i] = xv.v.p[i] = g.u.p[i] = g.v.p[i] = both(0.f);
       }
       if (OP == kSecond) {
         if (active && s.a) {
-          get_row<TI>(av, from + (kPieces<TI> + kPieces<TO>)*kThreads);
+          get_row(av, from + kRowBytes<TI, P> + kRowBytes<TO, P>, static_cast<const TI*>(nullptr));
         } else {
 #pragma unroll
-          for (int i = 0; i < 4; ++i) av.u.p[i] = av.v.p[i] = both(0.f);
+          for (int i = 0; i < P / 2; ++i) av.u.p[i] = av.v.p[i] = both(0.f);
         }
       }
       copy_next();  // into the slot that was just read
       {
         if (OP == kForward) {
-          float sum[1] = {dot16(xv, xv)};
+          float sum[1] = {dot(xv, xv)};
           row_sums(sum, a.lanes);
           const f2 r = both(rsqrtf(fmaf(sum[0], a.inv_d, a.eps)));
           if (!active) continue;
-          const Half wu = shared8(sw + e0), wv = shared8(sw + e1);
+          const Run<P> wu = shared_run<P>(sw + e0), wv = shared_run<P>(sw + e1);
 #pragma unroll
-          for (int i = 0; i < 4; ++i) {
+          for (int i = 0; i < P / 2; ++i) {
             xv.u.p[i] = mul2(mul2(r, wu.p[i]), xv.u.p[i]);
             xv.v.p[i] = mul2(mul2(r, wv.p[i]), xv.v.p[i]);
           }
           t8.template apply<INTERLEAVED, false>(xv);
-          put8(y + e0, xv.u);
-          put8(y + e1, xv.v);
+          put_run<P>(y + e0, xv.u);
+          put_run<P>(y + e1, xv.v);
           y += s.ys[1];
         } else if (OP == kBackward) {
           t8.template apply<INTERLEAVED, true>(g);
-          Pair16 h;
+          Runs<P> h;
           if (have) {
-            const Half wu = shared8(sw + e0), wv = shared8(sw + e1);
+            const Run<P> wu = shared_run<P>(sw + e0), wv = shared_run<P>(sw + e1);
 #pragma unroll
-            for (int i = 0; i < 4; ++i) {
+            for (int i = 0; i < P / 2; ++i) {
               h.u.p[i] = mul2(wu.p[i], g.u.p[i]);
               h.v.p[i] = mul2(wv.p[i], g.v.p[i]);
             }
           } else {
             h = g;
           }
-          float sum[2] = {dot16(xv, xv), dot16(h, xv)};
+          float sum[2] = {dot(xv, xv), dot(h, xv)};
           row_sums(sum, a.lanes);
           if (!active) continue;
           const float r = rsqrtf(fmaf(sum[0], a.inv_d, a.eps));
           // dx = r h - (r^3 <h, x> / d) x
           const f2 r2 = both(r), back = both(-r * (r * r * sum[1] * a.inv_d));
 #pragma unroll
-          for (int i = 0; i < 4; ++i) {
+          for (int i = 0; i < P / 2; ++i) {
             acc.u.p[i] = fma2(g.u.p[i], mul2(r2, xv.u.p[i]), acc.u.p[i]);
             acc.v.p[i] = fma2(g.v.p[i], mul2(r2, xv.v.p[i]), acc.v.p[i]);
             xv.u.p[i] = fma2(r2, h.u.p[i], mul2(back, xv.u.p[i]));
             xv.v.p[i] = fma2(r2, h.v.p[i], mul2(back, xv.v.p[i]));
           }
-          put8(y + e0, xv.u);
-          put8(y + e1, xv.v);
+          put_run<P>(y + e0, xv.u);
+          put_run<P>(y + e1, xv.v);
           y += s.ys[1];
         } else {
           t8.template apply<INTERLEAVED, true>(g);
           // <x, x>, <h, x>, <a, x>, <h, a>, <c . g, x>
-          float sum[5] = {dot16(xv, xv), 0.f, dot16(av, xv), 0.f, 0.f};
+          float sum[5] = {dot(xv, xv), 0.f, dot(av, xv), 0.f, 0.f};
           if (have) {
             f2 hx = both(0.f), ha = both(0.f), cx = both(0.f);
 #pragma unroll
             for (int run = 0; run < 2; ++run) {
-              const Half w = shared8(sw + (run ? e1 : e0)), c = shared8(sc + (run ? e1 : e0));
-              const Half &gr = run ? g.v : g.u, &xr = run ? xv.v : xv.u, &ar = run ? av.v : av.u;
+              const Run<P> w = shared_run<P>(sw + (run ? e1 : e0)), c = shared_run<P>(sc + (run ? e1 : e0));
+              const Run<P> &gr = run ? g.v : g.u, &xr = run ? xv.v : xv.u, &ar = run ? av.v : av.u;
 #pragma unroll
-              for (int i = 0; i < 4; ++i) {
+              for (int i = 0; i < P / 2; ++i) {
                 const f2 h = mul2(w.p[i], gr.p[i]);
                 hx = fma2(h, xr.p[i], hx);
                 ha = fma2(h, ar.p[i], ha);
@@ -696,11 +724,11 @@ __global__ void __launch_bounds__(kThreads, kResident<OP>) norm_rows(const __gri
                    by_x = both(-r * (r * (un + ht * a.inv_d))), at = both(-r * (an * r));
 #pragma unroll
           for (int run = 0; run < 2; ++run) {
-            const Half w = shared8(sw + (run ? e1 : e0)), c = shared8(sc + (run ? e1 : e0));
-            Half &gr = run ? g.v : g.u, &xr = run ? xv.v : xv.u, &ac = run ? acc.v : acc.u;
-            const Half& ar = run ? av.v : av.u;
+            const Run<P> w = shared_run<P>(sw + (run ? e1 : e0)), c = shared_run<P>(sc + (run ? e1 : e0));
+            Run<P> &gr = run ? g.v : g.u, &xr = run ? xv.v : xv.u, &ac = run ? acc.v : acc.u;
+            const Run<P>& ar = run ? av.v : av.u;
 #pragma unroll
-            for (int i = 0; i < 4; ++i) {
+            for (int i = 0; i < P / 2; ++i) {
               const f2 t = fma2(r2, ar.p[i], mul2(at, xr.p[i]));
               ac.p[i] = fma2(gr.p[i], t, ac.p[i]);
               const f2 q = mul2(r2, fma2(by_h, w.p[i], c.p[i]));  // what multiplies g in gx
@@ -710,10 +738,10 @@ __global__ void __launch_bounds__(kThreads, kResident<OP>) norm_rows(const __gri
             }
           }
           t8.template apply<INTERLEAVED, false>(g);
-          put8(y + e0, xv.u);
-          put8(y + e1, xv.v);
-          put8(ddy + e0, g.u);
-          put8(ddy + e1, g.v);
+          put_run<P>(y + e0, xv.u);
+          put_run<P>(y + e1, xv.v);
+          put_run<P>(ddy + e0, g.u);
+          put_run<P>(ddy + e1, g.v);
           y += s.ys[1];
           ddy += s.ddys[1];
         }
@@ -725,7 +753,7 @@ __global__ void __launch_bounds__(kThreads, kResident<OP>) norm_rows(const __gri
   float* const red = reinterpret_cast<float*>(ring);  // [per_block][d]: 8 KB at most
   if (have) {
 #pragma unroll
-    for (int i = 0; i < 4; ++i) {
+    for (int i = 0; i < P / 2; ++i) {
       *reinterpret_cast<f2*>(red + group * a.d + e0 + 2 * i) = acc.u.p[i];
       *reinterpret_cast<f2*>(red + group * a.d + e1 + 2 * i) = acc.v.p[i];
     }
@@ -793,18 +821,18 @@ void plan(NormArgs& a, int P, int C, int per_sm) {
   }
 }
 
-// P = 8: norm_rows; else norm_kernel.
+// norm_rows, or norm_kernel where P = 1.
 template <int OP, typename TI, typename TO, int P, int C, bool INTERLEAVED>
 cudaError_t launch(NormArgs& a, LaunchLog& log) {
-  plan(a, P, C, P == 8 ? kResident<OP> : kBlocksPerSm);
+  plan(a, P, C, P > 1 ? kResident<OP> : kBlocksPerSm);
   size_t smem = sizeof(unsigned long long) * ((a.half + 1) & ~1) + sizeof(float) * a.d * (OP == kSecond ? 2 : 1);
   const unsigned grid = (unsigned)(a.side[0].blocks + a.side[1].blocks);
-  if constexpr (P == 8) {
-    smem += sizeof(uint4) * kThreads * kDeep * kRowPieces<OP, TI, TO>;
-    const cudaError_t e = cudaFuncSetAttribute(norm_rows<OP, TI, TO, INTERLEAVED>,
+  if constexpr (P > 1) {
+    smem += kDeep * kRingRow<OP, TI, TO, P>;
+    const cudaError_t e = cudaFuncSetAttribute(norm_rows<OP, TI, TO, P, INTERLEAVED>,
                                                cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
     if (e != cudaSuccess) return e;
-    norm_rows<OP, TI, TO, INTERLEAVED><<<grid, kThreads, smem, log.stream>>>(a);
+    norm_rows<OP, TI, TO, P, INTERLEAVED><<<grid, kThreads, smem, log.stream>>>(a);
   } else {
     smem += OP == kForward ? 0 : sizeof(float) * a.d * (kThreads / a.lanes);
     norm_kernel<OP, TI, TO, P, C, INTERLEAVED><<<grid, kThreads, smem, log.stream>>>(a);
