@@ -294,7 +294,8 @@ __global__ void __launch_bounds__(kThreads) norm_kernel(const __grid_constant__ 
           FBOB_EACH(j, i) sum[1] = fmaf(w.u[j][i] * g.u[j][i], xv.u[j][i],
                                         fmaf(w.v[j][i] * g.v[j][i], xv.v[j][i], sum[1]));
           row_sums(sum, a.lanes);
-          const float r = rsqrtf(fmaf(sum[0], a.inv_d, a.eps));
+          // (0 where there is no row: without eps it would be an infinity times the zeros)
+          const float r = active ? rsqrtf(fmaf(sum[0], a.inv_d, a.eps)) : 0.f;
           const float back = r * r * sum[1] * a.inv_d;  // dx = r (h - back x)
           FBOB_EACH(j, i) {
             acc.u[j][i] = fmaf(g.u[j][i], r * xv.u[j][i], acc.u[j][i]);
@@ -322,7 +323,8 @@ __global__ void __launch_bounds__(kThreads) norm_kernel(const __grid_constant__ 
                           fmaf(c.v[j][i] * g.v[j][i], xv.v[j][i], sum[4]));
           }
           row_sums(sum, a.lanes);
-          const float r = rsqrtf(fmaf(sum[0], a.inv_d, a.eps));
+          // (0 where there is no row: without eps it would be an infinity times the zeros)
+          const float r = active ? rsqrtf(fmaf(sum[0], a.inv_d, a.eps)) : 0.f;
           const float hn = r * sum[1] * a.inv_d, an = r * sum[2] * a.inv_d;  // <h, n> / d, <a, n> / d
           const float ht = r * (sum[3] - r * sum[1] * an);                   // <h, t>
           const float un = r * a.inv_d * sum[4] - 2.f * r * an * hn;         // <u, n> / d

@@ -11,7 +11,6 @@ which a MAML step takes, are one pass over the rows each, and a small sum.
 from __future__ import annotations
 
 import functools
-import math
 import struct
 
 import torch
@@ -24,6 +23,7 @@ from .rotary import _angles
 _pack = struct.Struct("@8i2f2q").pack
 _pack_side = struct.Struct("@i8P15q").pack
 _NONE = (0, 0, 0)
+_FP32_END = 3.4e38  # eps and magnitude are passed in fp32
 
 
 def _strides(t):
@@ -193,6 +193,8 @@ def qk_norm_rotary(q: torch.Tensor, k: torch.Tensor, q_weight: torch.Tensor | No
     B, _, N, d = shape
     if k.shape[0] != B or k.shape[2] != N or k.shape[3] != d:
         raise ValueError(f"k must be [{B}, heads, {N}, {d}] to go with q")
+    if max(*shape, k.shape[1]) >= 1 << 31:
+        raise _b.FbobError(2, "qk_norm_rotary")
     weight_dtype = torch.float32
     if q_weight is not None:
         weight_dtype = _weight("q_weight", q_weight, d, device)
@@ -200,9 +202,9 @@ def qk_norm_rotary(q: torch.Tensor, k: torch.Tensor, q_weight: torch.Tensor | No
         if _weight("k_weight", k_weight, d, device) != weight_dtype and q_weight is not None:
             raise ValueError("the weights must have one dtype")
         weight_dtype = k_weight.dtype
-    if not (eps >= 0 and math.isfinite(eps)):
+    if not 0 <= eps < _FP32_END:
         raise ValueError(f"eps must be at least 0 and finite, got {eps}")
-    if not math.isfinite(magnitude):
+    if not abs(magnitude) < _FP32_END:
         raise ValueError(f"magnitude must be finite, got {magnitude}")
     offset, turned = 0, 0
     if inv_freq is not None:

@@ -266,6 +266,21 @@ class TestValues:
             assert torch.isfinite(t[~bad]).all() and t[bad].isnan().any(-1).all()
         assert dw.isnan().any()
 
+    @pytest.mark.parametrize("d", [37, 64])
+    def test_without_eps_lanes_without_a_row_add_nothing(self, d):
+        """eps = 0, and fewer rows than a block's lanes hold: gradients are those with an
+        eps far below the rows' squares."""
+        g = torch.Generator("cuda").manual_seed(5)
+        leaves = [torch.randn(s, generator=g, device="cuda").requires_grad_()
+                  for s in ((1, 2, 3, d), (1, 1, 3, d), (d,), (d,))]
+        got = []
+        for eps in (0.0, 1e-30):
+            y = fbob.qk_norm_rotary(*leaves, eps=eps)
+            first = torch.autograd.grad(y, leaves, [torch.ones_like(t) for t in y], create_graph=True)
+            got.append([*first, *torch.autograd.grad(first, leaves, [torch.ones_like(t) for t in first])])
+        for a, b in zip(*got):
+            assert torch.isfinite(a).all() and torch.equal(a, b)
+
     def test_past_32_bit_offsets(self):
         """Two batches 2^32 + 64 elements apart."""
         buf = torch.empty((1 << 32) + 64 + 4 * 64 * 3, dtype=torch.bfloat16, device="cuda")
@@ -328,6 +343,17 @@ class TestValues:
                     lambda: fbob.qk_norm_rotary(*(torch.zeros(1, 1, 1, 257, device="cuda"),) * 2)):
             with pytest.raises(fbob.FbobError):
                 bad()
+
+    def test_numbers_past_their_c_types_are_refused(self):
+        (q, k), (wq, wk), f, *_ = make(CASES[2])
+        for how in (dict(eps=1e39), dict(magnitude=1e39), dict(magnitude=-1e39)):
+            with pytest.raises(ValueError):
+                fbob.qk_norm_rotary(q, k, wq, wk, f, **how)
+        one = torch.zeros(1, 1, 1, 1, device="cuda")
+        long, many = one.expand(1, 1, 1 << 31, 1), one.expand(1, 1 << 31, 1, 1)
+        for q, k in ((long, long), (many, one), (one, many), (many.transpose(0, 1),) * 2):
+            with pytest.raises(fbob.FbobError):
+                fbob.qk_norm_rotary(q, k)
 
     def test_third_and_forward_mode_derivatives_are_refused(self):
         (q, k), (wq, wk), f, (dy, _), *_ = make(CASES[2])
