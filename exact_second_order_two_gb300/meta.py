@@ -169,12 +169,12 @@ def mse(a: torch.Tensor, b: torch.Tensor) -> torch.Tensor:
 def orthogonal_updates(grads, orthogonal=orthogonalize):
     """Each matrix [m, n] among ``grads`` orthogonalised, times
     sqrt(max(1, m / n)); vectors and numbers as they are.  Matrices of one shape
-    go through one call."""
+    and dtype go through one call."""
     out, stacks = list(grads), {}
     for i, g in enumerate(grads):
         if g.dim() == 2:
-            stacks.setdefault(g.shape, []).append(i)
-    for (m, n), at in stacks.items():
+            stacks.setdefault((*g.shape, g.dtype, g.device), []).append(i)
+    for (m, n, *_), at in stacks.items():
         scale = max(1.0, m / n) ** 0.5
         for i, u in zip(at, orthogonal(torch.stack([grads[i] for i in at])).unbind(0)):
             out[i] = scale * u

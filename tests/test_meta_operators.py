@@ -95,6 +95,20 @@ def test_updates_of_one_shape_go_through_one_call():
     assert out[3] is grads[3] and out[4] is grads[4]
 
 
+def test_updates_keep_their_dtypes():
+    """Matrices of one shape and different dtypes do not go through one call."""
+    grads = [torch.ones(4, 3, dtype=t) for t in (torch.float32, torch.bfloat16, torch.float32)]
+    calls = []
+
+    def spy(x):
+        calls.append((x.dtype, x.shape[0]))
+        return x
+
+    out = orthogonal_updates(grads, spy)
+    assert [t.dtype for t in out] == [t.dtype for t in grads]
+    assert sorted(calls, key=str) == [(torch.bfloat16, 1), (torch.float32, 2)]
+
+
 def test_refusals():
     layer = AttentionLayer.random(16, 2, "cpu", qk_norm=True)
     assert len(layer.params()) == 6
