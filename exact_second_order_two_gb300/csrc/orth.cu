@@ -723,20 +723,28 @@ cudaError_t squares_and_pack(const Plan& p, const void* x, float* sums, int* sta
 
 float pow2(int e) { return ldexpf(1.f, e); }
 
-// H's norm is brought to 2^target: every entry of H, S (stored at 2^se), T and of the next
-// H stays below 2^15 whatever their directions.
+// Exponents of the gradient.  A step multiplies the norm of H by growth = max |p'| over X's
+// singular values at most (on blocks of singular vectors it is a divided difference of
+// p, which is odd: a mean of p' between them).  H may have a norm of 2^room as step i takes
+// it, so that every entry of H, S (stored at 2^se), T and H' is below 2^15, whatever their
+// directions.  What step i is to scale its H' by comes from the norm of its own H:
+// that is brought to 2^target[i], and H' by growth further; dY to 2^target[steps].
 void backward_scales(const Plan& p, int* target, int* se) {
+  double after = 15;  // the room of what step i makes: the caller's gradient is past all products
   for (int i = 0; i < p.steps; ++i) {
-    const double M = p.M[i], a = fabs(p.a[i]), b = fabs(p.b[i]), c = fabs(p.c[i]);
-    const double growth = a + 3 * b * M * M + 5 * c * M * M * M * M;
-    const double t = (b + 2 * c * M * M) * 2 * M;
-    double most = 15 - log2(growth > 1 ? growth : 1);
+    const double M = p.M[i], a = p.a[i], b = p.b[i], c = p.c[i], end = 1.01 * M * 1.01 * M;
+    double growth = fmax(1.0, fmax(fabs(a), fabs(a + end * (3 * b + end * 5 * c))));
+    const double middle = c != 0 ? -3 * b / (10 * c) : -1;
+    if (middle > 0 && middle < end) growth = fmax(growth, fabs(a + middle * (3 * b + middle * 5 * c)));
+    const double t = (fabs(b) + 2 * fabs(c) * M * M) * 2 * M;
     // (T of the first step is stored times f < 2)
     const double by_t = (i > 0 ? 15 : 14) - log2(t > 1e-30 ? t : 1e-30) - (p.be[i] - p.xe[i]);
-    if (by_t < most) most = by_t;
-    target[i] = (int)floor(most) < 12 ? (int)floor(most) : 12;
-    se[i] = store_exp(pow2(target[i]) * 2 * M);
+    const double room = fmin(12.0, fmin(15 - log2(growth), by_t));
+    target[i] = (int)floor(fmin(12.0, after - log2(growth)));
+    se[i] = store_exp(exp2(room) * 2 * M);
+    after = room;
   }
+  target[p.steps] = (int)floor(after);
 }
 
 // A call for small matrices: one launch.
@@ -751,8 +759,8 @@ cudaError_t small(const Plan& p, const void* G, const void* dY, void* out, Forwa
   g.wait_ns = wait_limit_ns();
   g.L = p.L; g.p = p.p; g.q = p.q; g.tall = p.tall; g.steps = p.steps; g.keep = p.keep;
   g.eps = p.eps;
-  int target[kMaxSteps], se[kMaxSteps];
-  backward_scales(p, target, se);
+  int se[kMaxSteps];
+  backward_scales(p, g.target, se);
   g.x_terms = 1;
   for (int i = 0; i < p.steps; ++i) {
     const int te = p.be[i] - p.xe[i], out_exp = i + 1 < p.steps ? p.xe[i + 1] : 0;
@@ -769,9 +777,7 @@ cudaError_t small(const Plan& p, const void* G, const void* dY, void* out, Forwa
     g.s_to_t[i] = p.b[i] * pow2(te - se[i]);
     g.to_h[i] = pow2(-p.be[i]);
     g.h_to_h[i] = p.a[i];
-    g.target[i] = i > 0 ? target[i - 1] : 12;
   }
-  g.target[p.steps] = target[p.steps - 1];
   const auto half = CU_TENSOR_MAP_DATA_TYPE_FLOAT16;
   const Mats* from[3] = {&f.X, &f.A, &f.B};
   CUtensorMap* maps[3] = {g.x_map, g.a_map, g.b_map};
@@ -833,7 +839,7 @@ cudaError_t forward(const Plan& p, const void* G, void* Y, Forward& w, LaunchLog
 cudaError_t backward(const Plan& p, const void* G, const void* dY, void* dG, Forward& f, Backward& w,
                      LaunchLog& log) {
   if (small_fits(p.p, p.q, p.bf16)) return small(p, G, dY, dG, f, w.status, log);
-  int target[kMaxSteps], se[kMaxSteps];
+  int target[kMaxSteps + 1], se[kMaxSteps];
   backward_scales(p, target, se);
   const int top = p.steps - 1, terms = p.bf16 ? 1 : 2;
   Chain c(p, w.status, w.counters, f.info);
@@ -871,7 +877,7 @@ cudaError_t backward(const Plan& p, const void* G, const void* dY, void* dG, For
     h.sums = i > 0 ? w.step_sums[turn] : nullptr;
     h.scale_sums = sums;
     h.scale_parts = parts;
-    h.target = i > 0 ? target[i - 1] : 12;
+    h.target = target[i];
     h.exp_in = w.exp[i + 1];
     h.exp_out = w.exp[i];
     c.to(Ref{&w.H, turn ^ 1, terms});
@@ -883,7 +889,7 @@ cudaError_t backward(const Plan& p, const void* G, const void* dY, void* dG, For
   PackArgs a = {};
   a.hi = w.H.hi;
   a.lo = w.H.lo;
-  a.target = target[top];
+  a.target = target[p.steps];
   a.exp_out = w.exp[p.steps];
   a.sums_out = w.first;
   cudaError_t e = squares_and_pack(p, dY, w.sums, w.status, w.counters, a, log);

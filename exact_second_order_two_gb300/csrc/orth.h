@@ -86,8 +86,8 @@ cudaError_t launch_chain(const ChainArgs& g, bool split, LaunchLog& log);
 
 // A small matrix's steps, or their gradient, in one block (orth_small.cu).  Factors of
 // each step: A = to_a acc, B = to_b acc + a_to_b A, X' = to_x acc + x_to_x X; S = to_s acc,
-// T = to_t acc + s_to_t S, H' = to_h acc + h_to_h H, H' brought to 2^target[step] and dY to
-// 2^target[steps].
+// T = to_t acc + s_to_t S, H' = to_h acc + h_to_h H, times what brings the norm of H to
+// 2^target[step]; dY is brought to 2^target[steps].
 struct SmallArgs {
   CUtensorMap x_map[2], a_map[2], b_map[2];  // kept: [step][matrix]
   const void *g, *dy;
@@ -155,7 +155,8 @@ __device__ __forceinline__ float info_of(float nu2, float eps, int x_exp, MatInf
     int e;
     r.f = 2.f * frexpf(r.s, &e);  // s = f 2^(e - 1)
     r.k = e - 1;
-    return ldexpf(1.f, r.k + x_exp);
+    // (a finite factor: only zeros, and what is lost beside a norm of 0, have a larger one)
+    return ldexpf(1.f, r.k + x_exp < 127 ? r.k + x_exp : 127);
   }
   // an infinite or NaN norm, or 0 and eps = 0: zeros and NaN as s G gives them
   r.f = 1.f;

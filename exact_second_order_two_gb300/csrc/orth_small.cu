@@ -330,7 +330,7 @@ __global__ void __launch_bounds__(kThreads, 1) small_backward(const __grid_const
   int exp = rescaling(nu2, g.target[g.steps]);
   const float factor = ldexpf(1.f, exp);
   take_in(dy, H, TERMS, factor, g.p, g.q, g.tall);
-  nu2 *= factor * factor;
+  nu2 = nu2 * factor * factor;  // (the factor's own square can be past fp32's range)
   float dots = 0.f;
   for (int i = g.steps - 1; i >= 0; --i) {
     const float f = i == 0 ? info.f : 1.f;  // X_0 is f times what is stored

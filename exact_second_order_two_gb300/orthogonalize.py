@@ -40,7 +40,10 @@ def _problem(shape, dtype, steps, polynomials, eps, keep):
     """The C description of a call on tensors of ``shape``, and its workspaces' bytes
     (forward, backward)."""
     coefficients = _coefficients(steps, polynomials)
-    o = _b.Orth(math.prod(shape[:-2]), shape[-2], shape[-1], _b.DTYPES[dtype], steps, int(keep), eps,
+    sizes = math.prod(shape[:-2]), shape[-2], shape[-1]
+    if max(sizes) >= 1 << 31:  # would wrap in the description
+        raise _b.FbobError(2, "orthogonalize")
+    o = _b.Orth(*sizes, _b.DTYPES[dtype], steps, int(keep), eps,
                 ctypes.addressof(coefficients))
     o.held = coefficients  # lives as long as its address is used
     ref = ctypes.byref(o)
@@ -108,7 +111,8 @@ def orthogonalize(g: torch.Tensor, steps: int = 5, coefficients=QUINTIC,
     g: bf16 or fp32 CUDA tensor, not empty (copied first if not contiguous).
     coefficients: (a, b, c), or one such triple for each step; singular values
     that start in [0, 1] must stay below 64 under them.  steps from 1 to 16.
-    eps >= 0.  The shorter side is taken as the rows of X.
+    eps >= 0.  The shorter side is taken as the rows of X.  Norms, of g and of what comes
+    from above in the backward, are taken by squares in fp32: from 1e-19 to 1e19.
 
     Returns a contiguous tensor of g's shape and dtype.  Differentiable once in g, in
     reverse mode.  bf16: products of fp16 operands with fp32 sums, about as far from

@@ -2,6 +2,7 @@
 bits (torch's autograd), at the sizes, shapes and values where it can go wrong,
 and what the call refuses."""
 import ctypes
+import importlib
 import math
 
 import pytest
@@ -177,6 +178,38 @@ class TestValues:
         G.requires_grad_()
         (dG,) = torch.autograd.grad(fbob.orthogonalize(G), G, torch.zeros_like(dY))
         assert (dG == 0).all()
+
+    @pytest.mark.parametrize("shape", [(60, 80), (150, 300)], ids=str)
+    @pytest.mark.parametrize("dtype", ["bf16", "fp32"])
+    @pytest.mark.parametrize("power", [-62, -57, -50, 40, 55])
+    def test_gradients_of_any_size(self, shape, dtype, power):
+        """The gradient is linear in what comes from above, and a power of two in it only
+        moves exponents: the result's bits are the same, times it."""
+        G, dY = gradient(shape, DT[dtype])
+        G.requires_grad_()
+        Y = fbob.orthogonalize(G)
+        (want,) = torch.autograd.grad(Y, G, dY, retain_graph=True)
+        (got,) = torch.autograd.grad(Y, G, dY * 2.0 ** power)
+        assert torch.equal(got, want * 2.0 ** power)
+
+    @pytest.mark.parametrize("shape", [(60, 80), (150, 300)], ids=str)
+    def test_a_small_gradient_of_one_entry(self, shape):
+        """The same where a step enlarges fifty times what lies in one entry."""
+        G, dY = gradient(shape, torch.float32)
+        G.requires_grad_()
+        dY.zero_()[3, 5] = 1.0
+        Y = fbob.orthogonalize(G, 5, CUBIC + ((50.0, 0.0, 0.0), (1.0, 0.0, 0.0)))
+        (want,) = torch.autograd.grad(Y, G, dY, retain_graph=True)
+        (got,) = torch.autograd.grad(Y, G, dY * 2.0 ** -62)
+        assert torch.isfinite(want).all() and torch.equal(got, want * 2.0 ** -62)
+
+    @pytest.mark.parametrize("shape", [(60, 80), (150, 300)], ids=str)
+    def test_zeros_with_little_or_no_eps(self, shape):
+        """A zero matrix stays zero for any eps above 0; without it, it is 0 / 0."""
+        G = torch.zeros(shape, device="cuda")
+        for eps in (1e-38, 1e-30, 1e-7):
+            assert (fbob.orthogonalize(G, eps=eps) == 0).all()
+        assert fbob.orthogonalize(G, eps=0.0).isnan().all()
 
     def test_views(self):
         """Transposed, strided, offset and expanded inputs and upstream gradients."""
@@ -439,6 +472,15 @@ def test_c_call_refuses_bad_arguments():
     assert lib.fbob_orth_backward(r, good, None, good, good, 1 << 30, good, 1 << 30, None) == 1
     # without a backward two buffers in turn; with one, all steps
     assert lib.fbob_orth_workspace_size(0, r) > lib.fbob_orth_workspace_size(0, ctypes.byref(problem(keep=0)))
+
+
+@pytest.mark.parametrize("shape", [((1 << 32) + 5, 4, 4), (1 << 16, 1 << 16, 4, 4), (4, (1 << 32) + 4),
+                                   ((1 << 32) + 4, 4), (4, 1 << 31)], ids=str)
+def test_sizes_past_32_bits_are_refused(shape):
+    """None is taken for what its lowest 32 bits say."""
+    problem = importlib.import_module("exact_second_order_two_gb300.orthogonalize")._problem
+    with pytest.raises(fbob.FbobError):
+        problem(shape, torch.bfloat16, 5, (ONE,), 1e-7, False)
 
 
 def test_cpu_tensors_are_refused():
