@@ -16,7 +16,9 @@
 // Numbers.  Operands are fp16 with exponents chosen for each matrix, accumulation
 // is fp32.  X has singular values up to M (bounded on the host from the
 // polynomials), so that one power of two for all of X, A and B keeps them inside fp16's
-// range, with 11 bits down to 2^-26 of the bound; H is rescaled every step by the norm
+// range, with 11 bits down to 2^-26 of the bound; a matrix that eps keeps below that bound
+// is stored as many powers of two larger (300 x 400, fp32, of norm 3e-15 beside an eps of
+// 1e-7: 4.9e-2 off without); H is rescaled every step by the norm
 // that it was measured to have.  fp32 tensors are held as the sum of two fp16 (22 bits)
 // and multiplied in three products; bf16 tensors in one.  There, a rounding error of X
 // between its weak directions grows by a every step.  It reaches them through a X alone
@@ -194,6 +196,7 @@ struct PackArgs {
   int p, q, ld, tall;
   float eps;
   int target;
+  Steps steps;
   // forward: the matrices' scales; backward (info null): their exponents and square sums
   MatInfo* info;
   int* exp_out;
@@ -215,8 +218,16 @@ __global__ void __launch_bounds__(kSumThreads) pack(PackArgs a) {
   float factor;
   if (a.info) {
     MatInfo r;
-    factor = info_of(nu2, a.eps, a.target, r);
-    if (writer) a.info[l] = r;
+    factor = info_of(nu2, a.eps, a.target, a.steps, r);
+    if (writer) {
+      float m = fminf(r.norm * r.s, 1.f);  // (1 for NaN: no room)
+      for (int i = 0; i < a.steps.n; ++i) {
+        if (i > 0) r.e[i] = (short)room_below(a.steps.bound[i], m);
+        m = next_bound(a.steps, i, m);
+      }
+      r.e[a.steps.n] = 0;
+      a.info[l] = r;
+    }
   } else {
     const int e = rescaling(nu2, a.target);
     factor = ldexpf(1.f, e);
@@ -377,6 +388,7 @@ struct Plan {
   int xe[kMaxSteps], ae[kMaxSteps], be[kMaxSteps];  // exponents of X, A, B as stored
   int xt[kMaxSteps];                                // terms of X
   double M[kMaxSteps];                              // bound on X's singular values
+  Steps device;                                     // the same for the kernels
   int square_parts;
   // sums of products are added up in parts (orth_chain.cu)
   bool split() const { return !bf16 || q > 65536; }
@@ -427,7 +439,7 @@ int make_plan(const fbob_orth_t* o, Plan* out) {
   p.bf16 = o->dtype == FBOB_BF16;
   p.keep = o->keep;
   p.eps = o->eps;
-  double M = 1.0;
+  double M = 1.0, falls = 1.0;
   for (int i = 0; i < p.steps; ++i) {
     const double a = o->coefficients[3 * i], b = o->coefficients[3 * i + 1], c = o->coefficients[3 * i + 2];
     if (!(fabs(a) < 1e6 && fabs(b) < 1e6 && fabs(c) < 1e6)) return FBOB_ERR_INVALID_ARG;
@@ -453,6 +465,15 @@ int make_plan(const fbob_orth_t* o, Plan* out) {
     }
     M = 1.01 * most;
     if (!(M < 64.0)) return FBOB_ERR_INVALID_ARG;  // singular values that run away
+    // exponents come from bounds: where small singular values, which go with a, fall far
+    // behind those, fp16 has no digits left for them
+    falls *= fmin(1.0, fabs(a));
+    if (!(falls >= 1.0 / 256)) return FBOB_ERR_INVALID_ARG;
+  }
+  p.device.n = p.steps;
+  for (int i = 0; i < p.steps; ++i) {
+    p.device.a[i] = p.a[i]; p.device.b[i] = p.b[i]; p.device.c[i] = p.c[i];
+    p.device.bound[i] = (float)p.M[i];
   }
   // terms of X: the growth of a rounding error by the steps that follow
   double growth = 1;
@@ -627,6 +648,7 @@ struct Chain {
     f.depth = depth;
     f.nn = nn;
     f.sym = sym;
+    f.step = -1;
     f.first = items;
   }
   void pair(const Ref& P, int tp, const Ref& Q, int tq) {
@@ -644,6 +666,15 @@ struct Chain {
       pair(P, 1, Q, 0);
     }
     pair(P, 0, Q, 0);
+  }
+  // exponents of alpha and of beta for a matrix with exponents e[i], e[i + 1]
+  void by_matrix(int i, int alpha0, int alpha1, int beta0, int beta1) {
+    Phase& f = phase();
+    f.step = i;
+    f.e_alpha[0] = (signed char)alpha0;
+    f.e_alpha[1] = (signed char)alpha1;
+    f.e_beta[0] = (signed char)beta0;
+    f.e_beta[1] = (signed char)beta1;
   }
   void plus(const Ref& E) {
     Phase& f = phase();
@@ -718,6 +749,7 @@ cudaError_t squares_and_pack(const Plan& p, const void* x, float* sums, int* sta
   a.parts = p.square_parts;
   a.p = p.p; a.q = p.q; a.ld = p.ldq; a.tall = p.tall;
   a.eps = p.eps;
+  a.steps = p.device;
   return launch_next(p.bf16 ? pack<__nv_bfloat16> : pack<float>, passes(p), kSumThreads, 0, 1, log, a);
 }
 
@@ -757,8 +789,9 @@ cudaError_t small(const Plan& p, const void* G, const void* dY, void* out, Forwa
   g.info = f.info;
   g.status = status;
   g.wait_ns = wait_limit_ns();
-  g.L = p.L; g.p = p.p; g.q = p.q; g.tall = p.tall; g.steps = p.steps; g.keep = p.keep;
+  g.L = p.L; g.p = p.p; g.q = p.q; g.tall = p.tall; g.keep = p.keep;
   g.eps = p.eps;
+  g.steps = p.device;
   int se[kMaxSteps];
   backward_scales(p, g.target, se);
   g.x_terms = 1;
@@ -813,6 +846,7 @@ cudaError_t forward(const Plan& p, const void* G, void* Y, Forward& w, LaunchLog
     c.plus(A);
     c.phase().alpha = p.c[i] * pow2(p.be[i] - 2 * p.ae[i]);
     c.phase().beta = p.b[i] * pow2(p.be[i] - p.ae[i]);
+    c.by_matrix(i, -2, 0, 0, 0);
     c.to(B);
     c.end();
     c.begin(p.q, p.p, true, false);
@@ -822,6 +856,7 @@ cudaError_t forward(const Plan& p, const void* G, void* Y, Forward& w, LaunchLog
     c.phase().alpha = pow2(out - p.be[i] - p.xe[i]);
     c.phase().beta = p.a[i] * pow2(out - p.xe[i]);
     c.phase().fpow = i == 0 ? 1 : 0;
+    c.by_matrix(i, -3, 1, -1, 1);
     if (last) c.to_caller(Y);
     else c.to(Ref{&w.X, w.x(i + 1), p.xt[i + 1]});
     c.end();
@@ -857,7 +892,8 @@ cudaError_t backward(const Plan& p, const void* G, const void* dY, void* dG, For
     c.phase().fpow = by_f;
     c.to(S);
     c.end();
-    const int te = p.be[i] - p.xe[i];  // T X and B H share an accumulator
+    // T X and B H share an accumulator: T is stored 2^e[i] larger, as S and X are
+    const int te = p.be[i] - p.xe[i];
     c.begin(p.p, p.p, false, true);
     c.add(A, S);
     c.add(S, A);
@@ -865,6 +901,7 @@ cudaError_t backward(const Plan& p, const void* G, const void* dY, void* dG, For
     c.phase().alpha = p.c[i] * pow2(te - p.ae[i] - se[i]);
     c.phase().beta = p.b[i] * pow2(te - se[i]);
     c.phase().fpow = by_f;
+    c.by_matrix(i, -2, 0, 0, 0);
     c.to(T);
     c.end();
     c.begin(p.q, p.p, true, false);
@@ -874,6 +911,7 @@ cudaError_t backward(const Plan& p, const void* G, const void* dY, void* dG, For
     Phase& h = c.phase();
     h.alpha = pow2(-p.be[i]);
     h.beta = p.a[i];
+    c.by_matrix(i, -2, 0, 0, 0);
     h.sums = i > 0 ? w.step_sums[turn] : nullptr;
     h.scale_sums = sums;
     h.scale_parts = parts;

@@ -12,13 +12,6 @@
 namespace fbob {
 namespace orth {
 
-// What is known of a matrix from its norm.
-struct MatInfo {
-  float norm, s;  // |G|_F and 1 / (norm + eps)
-  float f;        // X_0 = f G 2^k: f in [1, 2)
-  int k;
-};
-
 constexpr int kTile = 128;      // rows of a CTA's operand tiles
 constexpr int kHigh = 256;      // rows of a pair's tile of a product
 constexpr int kWide = 256;      // its columns, at most
@@ -31,10 +24,28 @@ constexpr int kMaxSteps = 16;
 constexpr int kMaxPhases = 3 * kMaxSteps;
 constexpr int kMaxMaps = 24;
 
+// What is known of a matrix from its norm.
+struct MatInfo {
+  float norm, s;  // |G|_F and 1 / (norm + eps)
+  float f;        // X_0 = f G 2^k: f in [1, 2)
+  int k;
+  // Where eps takes part, X is smaller than the stack's bound: X of step i is stored 2^e[i]
+  // larger than its exponent says, A and B 2^(2 e[i]), S 2^e[i].  The result is not
+  // (e[steps] = 0).
+  short e[kMaxSteps + 1];
+};
+
+// The steps' polynomials, and bounds on the singular values of any matrix's X.
+struct Steps {
+  int n;
+  float a[kMaxSteps], b[kMaxSteps], c[kMaxSteps], bound[kMaxSteps];
+};
+
 // One product for every matrix of the stack:
-//   value = (alpha sum over segments P Q^T (nn: P Q) + beta E) f^fpow 2^shift,
+//   value = (alpha 2^ea sum over segments P Q^T (nn: P Q) + beta 2^eb E) f^fpow 2^shift,
 // the operands, E and the result given by map and by the number of the stack's first
-// matrix in it.
+// matrix in it; ea and eb are the sums of e_alpha and e_beta times the matrix's exponents of
+// this step and the next.
 struct Phase {
   unsigned char seg_a[kMaxSegs], seg_b[kMaxSegs];
   int at_a[kMaxSegs], at_b[kMaxSegs];
@@ -50,6 +61,8 @@ struct Phase {
   int ld;
   float alpha, beta;
   int fpow;
+  int step;                     // < 0: ea = eb = 0
+  signed char e_alpha[2], e_beta[2];
   float* sums;                  // [count][parts of a matrix]: squares of the values, or null
   // shift: brings the norm of the phase's input, whose squares these are, to 2^target
   const float* scale_sums;
@@ -95,8 +108,9 @@ struct SmallArgs {
   MatInfo* info;
   int* status;
   unsigned long long wait_ns;
-  int L, p, q, tall, steps, keep;
+  int L, p, q, tall, keep;
   float eps;
+  Steps steps;
   int x_terms;                               // most of X in a step
   int xt[kMaxSteps], xe[kMaxSteps];
   float to_a[kMaxSteps], to_b[kMaxSteps], a_to_b[kMaxSteps], to_x[kMaxSteps], x_to_x[kMaxSteps];
@@ -146,17 +160,32 @@ __device__ __forceinline__ int rescaling(float nu2, int target) {
   return target - ((e + 1) >> 1);
 }
 
-// A matrix's scales from its sum of squares; returns what G is multiplied by to be X_0's
-// terms, stored at 2^x_exp.
-__device__ __forceinline__ float info_of(float nu2, float eps, int x_exp, MatInfo& r) {
+// Powers of two that are sure to lie between m and the bound (by their exponents: none
+// where m is infinite or NaN).
+__device__ __forceinline__ int room_below(float bound, float m) {
+  const int e = (__float_as_int(bound) >> 23) - (__float_as_int(fmaxf(m, 1e-27f)) >> 23) - 1;
+  return m == m && e > 0 ? e : 0;
+}
+// Singular values behind step i, from those before (1.01 for what is rounded on the way).
+__device__ __forceinline__ float next_bound(const Steps& s, int i, float m) {
+  return 1.01f * m * (fabsf(s.a[i]) + m * m * (fabsf(s.b[i]) + m * m * fabsf(s.c[i])));
+}
+
+// A matrix's scales from its sum of squares, but for those behind X_0; returns what G is
+// multiplied by to be X_0's terms, stored at 2^(x_exp + e[0]).
+__device__ __forceinline__ float info_of(float nu2, float eps, int x_exp, const Steps& steps, MatInfo& r) {
   r.norm = sqrtf(nu2);
   r.s = 1.f / (r.norm + eps);
+  r.e[0] = 0;
   if (r.s > 0.f && r.s < 3.0e38f) {
     int e;
     r.f = 2.f * frexpf(r.s, &e);  // s = f 2^(e - 1)
     r.k = e - 1;
+    r.e[0] = (short)room_below(steps.bound[0], r.norm * r.s);
     // (a finite factor: only zeros, and what is lost beside a norm of 0, have a larger one)
-    return ldexpf(1.f, r.k + x_exp < 127 ? r.k + x_exp : 127);
+    const int most = 127 - r.k - x_exp;
+    if (r.e[0] > most) r.e[0] = (short)(most > 0 ? most : 0);
+    return ldexpf(1.f, most > 0 ? r.k + x_exp + r.e[0] : 127);
   }
   // an infinite or NaN norm, or 0 and eps = 0: zeros and NaN as s G gives them
   r.f = 1.f;
@@ -168,7 +197,7 @@ __device__ __forceinline__ float info_of(float nu2, float eps, int x_exp, MatInf
 // G <H_0, G> s / norm).  A zero matrix has no direction to take off.
 __device__ __forceinline__ void end_factors(const MatInfo& r, float dot, int exp, int x_exp, float& by_h,
                                             float& by_g) {
-  const double along = r.norm > 0.f ? ldexp((double)dot, -(r.k + x_exp)) * r.s / r.norm : 0.0;
+  const double along = r.norm > 0.f ? ldexp((double)dot, -(r.k + x_exp + r.e[0])) * r.s / r.norm : 0.0;
   const double scale = ldexp((double)r.s, -exp);
   by_h = (float)scale;
   by_g = (float)(scale * along);

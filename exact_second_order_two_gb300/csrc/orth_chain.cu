@@ -532,6 +532,12 @@ __global__ void __launch_bounds__(kThreads, 1) chain(const __grid_constant__ Cha
         alpha *= ff;
         beta *= ff;
       }
+      int by_alpha = 0, by_beta = 0;  // powers of two
+      if (p.step >= 0) {
+        const int e0 = g.info[at.l].e[p.step], e1 = g.info[at.l].e[p.step + 1];
+        by_alpha = p.e_alpha[0] * e0 + p.e_alpha[1] * e1;
+        by_beta = p.e_beta[0] * e0 + p.e_beta[1] * e1;
+      }
       if (p.scale_sums) {
         if (!__all_sync(0xffffffffu, await_ring(go, n))) break;
         if (scaled != at.l || scaled_ph != ph) {
@@ -542,9 +548,13 @@ __global__ void __launch_bounds__(kThreads, 1) chain(const __grid_constant__ Cha
           scaled = at.l;
           scaled_ph = ph;
         }
-        alpha = ldexpf(alpha, shift);
-        beta = ldexpf(beta, shift);
+        by_alpha += shift;
+        by_beta += shift;
         if (at.index == 0 && threadIdx.x == 0 && rank == 0) p.exp_out[at.l] = __ldcg(p.exp_in + at.l) + shift;
+      }
+      if (by_alpha | by_beta) {
+        alpha = ldexpf(alpha, by_alpha);
+        beta = ldexpf(beta, by_beta);
       }
       f2 total[SPLIT ? 32 : 1];  // of the thread's 64 columns
       if (SPLIT) {

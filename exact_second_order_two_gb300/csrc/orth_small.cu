@@ -229,8 +229,10 @@ __global__ void __launch_bounds__(kThreads, 1) small_forward(const __grid_consta
   const int row = 32 * ((threadIdx.x >> 5) & 3) + (threadIdx.x & 31), unit = threadIdx.x >> 7;
   const T* x = static_cast<const T*>(g.g) + (size_t)l * g.p * g.q;
   MatInfo info;
-  const float factor = info_of(squares(x, g.p * g.q, sh->red), g.eps, g.xe[0], info);
-  if (threadIdx.x == 0 && g.info) g.info[l] = info;
+  const float factor = info_of(squares(x, g.p * g.q, sh->red), g.eps, g.xe[0], g.steps, info);
+  float bound = fminf(info.norm * info.s, 1.f);  // of X's singular values (1 for NaN: no room)
+  int e = info.e[0];
+  if (threadIdx.x == 32) g.info[l] = info;
   take_in(x, X, g.xt[0], factor, g.p, g.q, g.tall);
   const int deep = (g.p + 63) / 64;  // tiles of A's columns
   const int wide_sums = TERMS == 2 ? tiles : 1, deep_sums = TERMS == 2 ? deep : 1;
@@ -249,8 +251,12 @@ __global__ void __launch_bounds__(kThreads, 1) small_forward(const __grid_consta
     ok = ok && warp_wait(&sh->mma, n++ & 1, &sh->ab, g.status);
     tc_fence_after();
   };
-  for (int i = 0; i < g.steps; ++i) {
+  for (int i = 0; i < g.steps.n; ++i) {
     const float f = i == 0 ? info.f : 1.f;
+    const bool last = i + 1 == g.steps.n;
+    bound = next_bound(g.steps, i, bound);
+    const int e1 = last ? 0 : room_below(g.steps.bound[i + 1], bound);
+    if (threadIdx.x == 32) g.info[l].e[i + 1] = (short)e1;
     f2 v[16];
     product(X, X, false, tiles, [&] {
       if (g.keep) store_held(&g.x_map[0], g.xt[i] == 2 ? &g.x_map[1] : nullptr, X, i * g.L + l, g.q, g.p);
@@ -260,18 +266,19 @@ __global__ void __launch_bounds__(kThreads, 1) small_forward(const __grid_consta
     product(A, A, false, deep, [&] {
       if (g.keep) store_held(&g.a_map[0], TERMS == 2 ? &g.a_map[1] : nullptr, A, i * g.L + l, g.p, g.p);
     });
-    read_acc(acc, deep_sums, unit, g.to_b[i], v);
+    read_acc(acc, deep_sums, unit, ldexpf(g.to_b[i], -2 * e), v);
     add_slot(v, A.tile(0, unit >> 1), row, unit & 1, g.a_to_b[i]);
     if (TERMS == 2) add_slot(v, A.tile(1, unit >> 1), row, unit & 1, g.a_to_b[i]);
     put(v, A, TERMS, row, unit);
     product(A, X, true, deep, [&] {
       if (g.keep) store_held(&g.b_map[0], TERMS == 2 ? &g.b_map[1] : nullptr, A, i * g.L + l, g.p, g.p);
     });
-    const bool last = i + 1 == g.steps;
+    const float to_x = ldexpf(f * g.to_x[i], e1 - 3 * e), x_to_x = ldexpf(f * g.x_to_x[i], e1 - e);
+    e = e1;
     for (int u = unit; u < 2 * tiles; u += 4) {
-      read_acc(acc, deep_sums, u, f * g.to_x[i], v);
-      add_slot(v, X.tile(0, u >> 1), row, u & 1, f * g.x_to_x[i]);
-      if (g.xt[i] == 2) add_slot(v, X.tile(1, u >> 1), row, u & 1, f * g.x_to_x[i]);
+      read_acc(acc, deep_sums, u, to_x, v);
+      add_slot(v, X.tile(0, u >> 1), row, u & 1, x_to_x);
+      if (g.xt[i] == 2) add_slot(v, X.tile(1, u >> 1), row, u & 1, x_to_x);
       if (!last) {
         put(v, X, g.xt[i + 1], row, u);
         continue;
@@ -325,14 +332,15 @@ __global__ void __launch_bounds__(kThreads, 1) small_backward(const __grid_const
     ok = ok && warp_wait(&sh->mma, n++ & 1, &sh->ab, g.status);
     tc_fence_after();
   };
-  if (threadIdx.x == 0) load(g.x_map, X, tiles, g.steps - 1);
+  if (threadIdx.x == 0) load(g.x_map, X, tiles, g.steps.n - 1);
   float nu2 = squares(dy, g.p * g.q, sh->red);
-  int exp = rescaling(nu2, g.target[g.steps]);
+  int exp = rescaling(nu2, g.target[g.steps.n]);
   const float factor = ldexpf(1.f, exp);
   take_in(dy, H, TERMS, factor, g.p, g.q, g.tall);
   nu2 = nu2 * factor * factor;  // (the factor's own square can be past fp32's range)
   float dots = 0.f;
-  for (int i = g.steps - 1; i >= 0; --i) {
+  for (int i = g.steps.n - 1; i >= 0; --i) {
+    const int e = g.info[l].e[i];  // X, S and T are 2^e larger in store, A and B 2^(2 e)
     const float f = i == 0 ? info.f : 1.f;  // X_0 is f times what is stored
     f2 v[16];
     loaded();
@@ -349,7 +357,7 @@ __global__ void __launch_bounds__(kThreads, 1) small_backward(const __grid_const
       multiply_terms<TERMS>(acc, S, A, false, deep, deep);
     });
     if (threadIdx.x == 0) load(g.b_map, A, kSquare, i);
-    read_acc(acc, deep_sums, unit, f * g.to_t[i], v);  // T in S's place
+    read_acc(acc, deep_sums, unit, ldexpf(f * g.to_t[i], -2 * e), v);  // T in S's place
     add_slot(v, S.tile(0, unit >> 1), row, unit & 1, f * g.s_to_t[i]);
     if (TERMS == 2) add_slot(v, S.tile(1, unit >> 1), row, unit & 1, f * g.s_to_t[i]);
     put(v, S, TERMS, row, unit);
@@ -360,7 +368,7 @@ __global__ void __launch_bounds__(kThreads, 1) small_backward(const __grid_const
     product([&] { multiply_terms<TERMS>(acc, S, X, true, deep, deep); });
     const int shift = rescaling(nu2, g.target[i]);
     exp += shift;
-    const float alpha = ldexpf(g.to_h[i], shift), beta = ldexpf(g.h_to_h[i], shift);
+    const float alpha = ldexpf(g.to_h[i], shift - 2 * e), beta = ldexpf(g.h_to_h[i], shift);
     float sum = 0.f;
     for (int u = unit; u < 2 * tiles; u += 4) {
       read_acc(acc, deep_sums, u, alpha, v);

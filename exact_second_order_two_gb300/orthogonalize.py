@@ -110,7 +110,8 @@ def orthogonalize(g: torch.Tensor, steps: int = 5, coefficients=QUINTIC,
 
     g: bf16 or fp32 CUDA tensor, not empty (copied first if not contiguous).
     coefficients: (a, b, c), or one such triple for each step; singular values
-    that start in [0, 1] must stay below 64 under them.  steps from 1 to 16.
+    that start in [0, 1] must stay below 64 under them, and small ones must not fall
+    far: the product of those |a| that are below 1 is at least 1/256.  steps from 1 to 16.
     eps >= 0.  The shorter side is taken as the rows of X.  Norms, of g and of what comes
     from above in the backward, are taken by squares in fp32: from 1e-19 to 1e19.
 

@@ -363,7 +363,9 @@ int fbob_qk_norm_bob(const fbob_qk_norm_t* s, const fbob_norm_side_t* q,
  *   X = G / (|G|_F + eps);   steps times:  A = X X^T, X = a X + (b A + c A^2) X
  * (A = X^T X, from the other side, where m > n).  coefficients: a, b, c of each
  * step, 3 * steps floats in host memory, read during the call.  They must
- * hold singular values that start in [0, 1] below 64; an infinite or NaN
+ * hold singular values that start in [0, 1] below 64, and the product of those
+ * |a| that are below 1 is at least 1/256 (small singular values go with a, and
+ * exponents with the large ones); an infinite or NaN
  * entry spoils its matrix.
  * g, y, dy and dg are dense [L,m,n] of `dtype`, aligned to their elements;
  * workspaces to 256 bytes.  Operands are fp16, one term for bf16 tensors (X in
