@@ -132,11 +132,11 @@ __device__ __forceinline__ void store_terms(__half* hi, __half* lo, const float 
   if (lo) *reinterpret_cast<uint4*>(lo) = *reinterpret_cast<const uint4*>(l);
 }
 
-// partial[l][block] = sum of squares of a slice of matrix l; also clears the call's
+// partial[l][block] = the squares of a slice of matrix l; also clears the call's
 // status word and the chain's counters, before the kernels that write them.
 template <typename T>
 __global__ void __launch_bounds__(kSumThreads)
-    square_sums(const T* __restrict__ x, float* __restrict__ partial, size_t elems, int* status,
+    square_sums(const T* __restrict__ x, Squares* __restrict__ partial, size_t elems, int* status,
                 int* counters, size_t n_counters) {
   __shared__ float sm[kSumThreads / 32];
   let_next_start();
@@ -145,34 +145,36 @@ __global__ void __launch_bounds__(kSumThreads)
        i += (size_t)gridDim.x * gridDim.y * kSumThreads)
     counters[i] = 0;
   x += (size_t)blockIdx.y * elems;
-  float s[4] = {0.f, 0.f, 0.f, 0.f};
-  constexpr int V = 16 / sizeof(T);
-  if (elems % V == 0 && (reinterpret_cast<uintptr_t>(x) & 15u) == 0) {
-    const size_t chunks = elems / V, per = (chunks + gridDim.x - 1) / gridDim.x;
-    const size_t first = blockIdx.x * per, last = min(chunks, first + per);
+  const Squares r = squares_of([&](float scale) {
+    float s[4] = {0.f, 0.f, 0.f, 0.f};
+    constexpr int V = 16 / sizeof(T);
+    if (elems % V == 0 && (reinterpret_cast<uintptr_t>(x) & 15u) == 0) {
+      const size_t chunks = elems / V, per = (chunks + gridDim.x - 1) / gridDim.x;
+      const size_t first = blockIdx.x * per, last = min(chunks, first + per);
 #pragma unroll 4
-    for (size_t i = first + threadIdx.x; i < last; i += kSumThreads) {
-      float v[V];
-      load_vector(x + i * V, v);
+      for (size_t i = first + threadIdx.x; i < last; i += kSumThreads) {
+        float v[V];
+        load_vector(x + i * V, v);
 #pragma unroll
-      for (int k = 0; k < V; ++k) s[k & 3] = fmaf(v[k], v[k], s[k & 3]);
+        for (int k = 0; k < V; ++k) s[k & 3] = fmaf(v[k] * scale, v[k] * scale, s[k & 3]);
+      }
+    } else {
+      const size_t per = (elems + gridDim.x - 1) / gridDim.x;
+      const size_t first = blockIdx.x * per, last = min(elems, first + per);
+      for (size_t i = first + threadIdx.x; i < last; i += kSumThreads) {
+        const float v = to_f32<T>(x[i]) * scale;
+        s[0] = fmaf(v, v, s[0]);
+      }
     }
-  } else {
-    const size_t per = (elems + gridDim.x - 1) / gridDim.x;
-    const size_t first = blockIdx.x * per, last = min(elems, first + per);
-    for (size_t i = first + threadIdx.x; i < last; i += kSumThreads) {
-      const float v = to_f32<T>(x[i]);
-      s[0] = fmaf(v, v, s[0]);
-    }
-  }
-  const float w = warp_sum((s[0] + s[1]) + (s[2] + s[3]));
-  if ((threadIdx.x & 31) == 0) sm[threadIdx.x >> 5] = w;
-  __syncthreads();
-  if (threadIdx.x == 0) {
+    const float w = warp_sum((s[0] + s[1]) + (s[2] + s[3]));
+    __syncthreads();
+    if ((threadIdx.x & 31) == 0) sm[threadIdx.x >> 5] = w;
+    __syncthreads();
     float t = 0.f;
     for (int k = 0; k < kSumThreads / 32; ++k) t += sm[k];
-    partial[(size_t)blockIdx.y * gridDim.x + blockIdx.x] = t;
-  }
+    return t;
+  });
+  if (threadIdx.x == 0) partial[(size_t)blockIdx.y * gridDim.x + blockIdx.x] = r;
 }
 
 // Sum of `parts` values, the same in every thread of the block.
@@ -188,9 +190,37 @@ __device__ __forceinline__ float parts_sum(const float* p, int parts, float* sm)
   return s;
 }
 
+// The same of squares, of which those with the largest exponent count most.
+__device__ __forceinline__ Squares parts_sum(const Squares* p, int parts, float* sm) {
+  int most = -1000, least = 1000;
+  for (int i = threadIdx.x; i < parts; i += kSumThreads) {
+    if (p[i].m == 0.f) continue;
+    most = max(most, p[i].e);
+    least = min(least, p[i].e);
+  }
+  if (__syncthreads_or(most >= least && (most != 0 || least != 0))) {
+    most = __reduce_max_sync(0xffffffffu, most);
+    if ((threadIdx.x & 31) == 0) sm[threadIdx.x >> 5] = (float)most;
+    __syncthreads();
+    for (int k = 0; k < kSumThreads / 32; ++k) most = max(most, (int)sm[k]);
+  } else {
+    most = 0;
+  }
+  float s = 0.f;
+  for (int i = threadIdx.x; i < parts; i += kSumThreads)
+    s += most == p[i].e || p[i].m == 0.f ? p[i].m : ldexpf(p[i].m, p[i].e - most);
+  s = warp_sum(s);
+  __syncthreads();
+  if ((threadIdx.x & 31) == 0) sm[threadIdx.x >> 5] = s;
+  __syncthreads();
+  s = 0.f;
+  for (int k = 0; k < kSumThreads / 32; ++k) s += sm[k];
+  return Squares{s, most};
+}
+
 struct PackArgs {
-  const void* x;       // [count][m][n]
-  const float* sums;   // [count][parts] squares
+  const void* x;        // [count][m][n]
+  const Squares* sums;  // [count][parts]
   int parts;
   __half *hi, *lo;     // [count][p][ld]
   int p, q, ld, tall;
@@ -213,7 +243,7 @@ __global__ void __launch_bounds__(kSumThreads) pack(PackArgs a) {
   const int l = blockIdx.y;
   let_next_start();
   after_previous();
-  const float nu2 = parts_sum(a.sums + (size_t)l * a.parts, a.parts, sm);
+  const Squares nu2 = parts_sum(a.sums + (size_t)l * a.parts, a.parts, sm);
   const bool writer = blockIdx.x == 0 && threadIdx.x == 0;
   float factor;
   if (a.info) {
@@ -233,7 +263,7 @@ __global__ void __launch_bounds__(kSumThreads) pack(PackArgs a) {
     factor = ldexpf(1.f, e);
     if (writer) {
       a.exp_out[l] = e;
-      a.sums_out[l] = nu2 * factor * factor;
+      a.sums_out[l] = ldexpf(nu2.m, nu2.e + 2 * e);
     }
   }
   const T* x = static_cast<const T*>(a.x) + (size_t)l * a.p * a.q;
@@ -322,7 +352,7 @@ struct EndArgs {
   const int* exp;
 };
 
-// dG = s (H_0 - G <H_0, G> s / norm)
+// dG = s (H_0 - G <H_0, G> s / norm), as end_factors has it
 template <typename T>
 __global__ void __launch_bounds__(kSumThreads) end_gradient(EndArgs a) {
   __shared__ float sm[kSumThreads / 32];
@@ -331,8 +361,8 @@ __global__ void __launch_bounds__(kSumThreads) end_gradient(EndArgs a) {
   after_previous();
   const MatInfo r = a.info[l];
   const float dot = parts_sum(a.dots + (size_t)l * a.parts, a.parts, sm);
-  float by_h, by_g;
-  end_factors(r, dot, a.exp[l], a.x_exp, by_h, by_g);
+  float by_h, by_g, up;
+  end_factors(r, dot, a.exp[l], a.x_exp, by_h, by_g, up);
   const size_t n = (size_t)l * a.p * a.q;
   const size_t base = (size_t)l * a.p * a.ld;
   const T* g = static_cast<const T*>(a.g) + n;
@@ -357,7 +387,7 @@ __global__ void __launch_bounds__(kSumThreads) end_gradient(EndArgs a) {
         const int c = i / kPack, r = i % kPack;
         if (r0 + r >= a.p || c0 + c >= a.q) continue;
         const size_t at = (size_t)(c0 + c) * a.p + r0 + r;
-        dg[at] = from_f32<T>(fmaf(-by_g, to_f32<T>(g[at]), by_h * tile[r][c]));
+        dg[at] = from_f32<T>(fmaf(-by_g, to_f32<T>(g[at]) * up, by_h * tile[r][c]));
       }
     }
     return;
@@ -373,7 +403,7 @@ __global__ void __launch_bounds__(kSumThreads) end_gradient(EndArgs a) {
     load_terms(a.h[0] + at, a.h[1] ? a.h[1] + at : nullptr, v);
     load8(g + to, wide, a.q - c, x);
 #pragma unroll
-    for (int k = 0; k < 8; ++k) v[k] = fmaf(-by_g, x[k], by_h * v[k]);
+    for (int k = 0; k < 8; ++k) v[k] = fmaf(-by_g, x[k] * up, by_h * v[k]);
     store8(dg + to, wide, a.q - c, v);
   }
 }
@@ -543,7 +573,7 @@ size_t counters(const Plan& p) { return 1 + (size_t)3 * p.steps * p.L; }  // tic
 struct Forward {
   int *status, *counters;
   MatInfo* info;
-  float* sums;
+  Squares* sums;
   Mats X, A, B;
   size_t bytes;
   int keep;
@@ -557,7 +587,7 @@ Forward carve_forward(const Plan& p, char* base) {
   w.status = static_cast<int*>(c.take(sizeof(int)));
   w.counters = static_cast<int*>(c.take(sizeof(int) * counters(p)));
   w.info = static_cast<MatInfo*>(c.take(sizeof(MatInfo) * p.L));
-  w.sums = static_cast<float*>(c.take(sizeof(float) * p.L * p.square_parts));
+  w.sums = static_cast<Squares*>(c.take(sizeof(Squares) * p.L * p.square_parts));
   const int xs = p.keep ? p.steps : p.steps > 1 ? 2 : 1, as = p.keep ? p.steps : 1;
   int low = 0;
   for (int i = 0; i < p.steps; ++i)
@@ -570,10 +600,11 @@ Forward carve_forward(const Plan& p, char* base) {
 }
 
 // Backward: [status][counters][square sums of dY][the same of H as packed][exponents:
-// steps + 1][sums of the steps' results: two in turn], H in turn, S, T.
+// steps + 1][sums of the steps' results: two in turn][<H, X>], H in turn, S, T.
 struct Backward {
   int *status, *counters;
-  float *sums, *first, *step_sums[2];
+  Squares* sums;
+  float *first, *step_sums[2], *dots;
   int* exp[kMaxSteps + 1];
   Mats H, S, T;
   size_t bytes;
@@ -588,7 +619,8 @@ Backward carve_backward(const Plan& p, char* base) {
   const int two = p.bf16 ? 0 : 1;
   w.status = static_cast<int*>(c.take(sizeof(int)));
   w.counters = static_cast<int*>(c.take(sizeof(int) * counters(p)));
-  w.sums = static_cast<float*>(c.take(sizeof(float) * p.L * p.square_parts));
+  w.sums = static_cast<Squares*>(c.take(sizeof(Squares) * p.L * p.square_parts));
+  w.dots = static_cast<float*>(c.take(sizeof(float) * p.L * p.square_parts));
   w.first = static_cast<float*>(c.take(sizeof(float) * p.L));
   for (float*& s : w.step_sums) s = static_cast<float*>(c.take(sizeof(float) * p.L * step_parts(p)));
   for (int i = 0; i <= p.steps; ++i) w.exp[i] = static_cast<int*>(c.take(sizeof(int) * p.L));
@@ -731,7 +763,7 @@ dim3 passes(const Plan& p) {
   return dim3((unsigned)(n < most ? n : most), (unsigned)p.L);
 }
 
-cudaError_t squares_and_pack(const Plan& p, const void* x, float* sums, int* status, int* counts,
+cudaError_t squares_and_pack(const Plan& p, const void* x, Squares* sums, int* status, int* counts,
                              PackArgs a, LaunchLog& log) {
   const size_t elems = (size_t)p.p * p.q;
   const dim3 grid((unsigned)p.square_parts, (unsigned)p.L);
@@ -938,7 +970,7 @@ cudaError_t backward(const Plan& p, const void* G, const void* dY, void* dG, For
   d.h[1] = w.H.lo ? w.H.lo + turn * w.H.slot : nullptr;
   d.x[0] = f.X.hi;
   d.x[1] = p.xt[0] == 2 ? f.X.lo : nullptr;
-  d.partial = w.sums;
+  d.partial = w.dots;
   d.p = p.p; d.q = p.q; d.ld = p.ldq;
   e = launch_next(term_dots, dim3((unsigned)p.square_parts, (unsigned)p.L), kSumThreads, 0, 1, log, d);
   if (e != cudaSuccess) return e;
@@ -947,7 +979,7 @@ cudaError_t backward(const Plan& p, const void* G, const void* dY, void* dG, For
   n.dg = dG;
   n.h[0] = d.h[0];
   n.h[1] = d.h[1];
-  n.dots = w.sums;
+  n.dots = w.dots;
   n.parts = p.square_parts;
   n.p = p.p; n.q = p.q; n.ld = p.ldq; n.tall = p.tall; n.x_exp = p.xe[0];
   n.info = f.info;

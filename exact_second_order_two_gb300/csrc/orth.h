@@ -151,13 +151,36 @@ __device__ __forceinline__ void let_next_start() {
 }
 __device__ __forceinline__ void after_previous() { asm volatile("griddepcontrol.wait;" ::: "memory"); }
 
-// The exponent that brings a matrix with sum of squares nu2 to a norm in
-// (2^(target - 1), 2^target], or nearly; 0 for zeros and for what is not finite.
-__device__ __forceinline__ int rescaling(float nu2, int target) {
-  if (!(nu2 > 0.f) || nu2 > 3.0e38f) return 0;
+// A sum of squares, m 2^e.  Squares are added as they are (e = 0) where their sum shows
+// that none was lost: the others, of less than 2^-60 or infinite, are taken again of elements
+// times a power of two that keeps any fp32 number's square, and a sum of 2^36 of them, inside
+// fp32.
+struct Squares {
+  float m;
   int e;
-  frexpf(nu2, &e);  // nu2 < 2^e
-  return target - ((e + 1) >> 1);
+};
+constexpr float kScaleSmall = 0x1p80f, kScaleLarge = 0x1p-96f;
+// sum(scale): the squares of elements times the scale; the same in all threads of a block.
+template <typename F>
+__device__ __forceinline__ Squares squares_of(F sum) {
+  Squares r = {sum(1.f), 0};
+  if (r.m < 0x1p-60f) {
+    r = Squares{sum(kScaleSmall), -160};
+  } else if (r.m > 3.4e38f) {
+    r = Squares{sum(kScaleLarge), 192};
+  }
+  return r;
+}
+
+// The exponent that brings a matrix with this sum of squares to a norm in
+// (2^(target - 1), 2^target], or nearly; 0 for zeros and for what is not finite.  (127 at
+// most, for a finite factor.)
+__device__ __forceinline__ int rescaling(Squares nu2, int target) {
+  if (!(nu2.m > 0.f) || nu2.m > 3.0e38f) return 0;
+  int e;
+  frexpf(nu2.m, &e);
+  e += nu2.e;  // nu2 < 2^e
+  return min(127, target - ((e + 1) >> 1));
 }
 
 // Powers of two that are sure to lie between m and the bound (by their exponents: none
@@ -173,8 +196,8 @@ __device__ __forceinline__ float next_bound(const Steps& s, int i, float m) {
 
 // A matrix's scales from its sum of squares, but for those behind X_0; returns what G is
 // multiplied by to be X_0's terms, stored at 2^(x_exp + e[0]).
-__device__ __forceinline__ float info_of(float nu2, float eps, int x_exp, const Steps& steps, MatInfo& r) {
-  r.norm = sqrtf(nu2);
+__device__ __forceinline__ float info_of(Squares nu2, float eps, int x_exp, const Steps& steps, MatInfo& r) {
+  r.norm = ldexpf(sqrtf(nu2.m), nu2.e / 2);
   r.s = 1.f / (r.norm + eps);
   r.e[0] = 0;
   if (r.s > 0.f && r.s < 3.0e38f) {
@@ -193,14 +216,16 @@ __device__ __forceinline__ float info_of(float nu2, float eps, int x_exp, const 
   return r.s;
 }
 
-// dG = by_h H_0 - by_g G, for H_0 stored at 2^exp and its product with X_0's terms: s (H_0 -
-// G <H_0, G> s / norm).  A zero matrix has no direction to take off.
+// dG = by_h H_0 - by_g (up G), for H_0 stored at 2^exp and its product with X_0's terms: s (H_0
+// - G <H_0, G> s / norm).  A zero matrix has no direction to take off.  (up = 2^k brings G to
+// a norm of about 1: s s / norm alone could be past fp32's range.)
 __device__ __forceinline__ void end_factors(const MatInfo& r, float dot, int exp, int x_exp, float& by_h,
-                                            float& by_g) {
+                                            float& by_g, float& up) {
   const double along = r.norm > 0.f ? ldexp((double)dot, -(r.k + x_exp + r.e[0])) * r.s / r.norm : 0.0;
   const double scale = ldexp((double)r.s, -exp);
   by_h = (float)scale;
-  by_g = (float)(scale * along);
+  by_g = (float)ldexp(scale * along, -r.k);
+  up = ldexpf(1.f, r.k);
 }
 #endif
 

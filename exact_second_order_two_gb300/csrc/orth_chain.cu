@@ -544,7 +544,7 @@ __global__ void __launch_bounds__(kThreads, 1) chain(const __grid_constant__ Cha
           const float* q = p.scale_sums + (size_t)at.l * p.scale_parts;
           float nu2 = 0.f;
           for (int i = lane; i < p.scale_parts; i += 32) nu2 += __ldcg(q + i);
-          shift = rescaling(warp_sum(nu2), p.target);
+          shift = rescaling(Squares{warp_sum(nu2), 0}, p.target);
           scaled = at.l;
           scaled_ph = ph;
         }

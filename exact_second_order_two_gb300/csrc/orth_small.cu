@@ -67,14 +67,16 @@ __device__ __forceinline__ const T* element(const T* x, int r, int c, int p, int
 }
 
 template <typename T>
-__device__ __forceinline__ float squares(const T* x, int elems, float* red) {
-  float s = 0.f;
+__device__ __forceinline__ Squares squares(const T* x, int elems, float* red) {
+  return squares_of([&](float scale) {
+    float s = 0.f;
 #pragma unroll 4
-  for (int i = threadIdx.x; i < elems; i += kThreads) {
-    const float v = to_f32<T>(x[i]);
-    s = fmaf(v, v, s);
-  }
-  return block_sum(s, red);
+    for (int i = threadIdx.x; i < elems; i += kThreads) {
+      const float v = to_f32<T>(x[i]) * scale;
+      s = fmaf(v, v, s);
+    }
+    return block_sum(s, red);
+  });
 }
 
 // factor x into tiles of `terms` terms, zeros around it.
@@ -333,11 +335,11 @@ __global__ void __launch_bounds__(kThreads, 1) small_backward(const __grid_const
     tc_fence_after();
   };
   if (threadIdx.x == 0) load(g.x_map, X, tiles, g.steps.n - 1);
-  float nu2 = squares(dy, g.p * g.q, sh->red);
-  int exp = rescaling(nu2, g.target[g.steps.n]);
+  const Squares dy2 = squares(dy, g.p * g.q, sh->red);
+  int exp = rescaling(dy2, g.target[g.steps.n]);
   const float factor = ldexpf(1.f, exp);
   take_in(dy, H, TERMS, factor, g.p, g.q, g.tall);
-  nu2 = nu2 * factor * factor;  // (the factor's own square can be past fp32's range)
+  float nu2 = ldexpf(dy2.m, dy2.e + 2 * exp);
   float dots = 0.f;
   for (int i = g.steps.n - 1; i >= 0; --i) {
     const int e = g.info[l].e[i];  // X, S and T are 2^e larger in store, A and B 2^(2 e)
@@ -366,7 +368,7 @@ __global__ void __launch_bounds__(kThreads, 1) small_backward(const __grid_const
     if (threadIdx.x == 0) load(g.x_map, X, tiles, i);
     loaded();
     product([&] { multiply_terms<TERMS>(acc, S, X, true, deep, deep); });
-    const int shift = rescaling(nu2, g.target[i]);
+    const int shift = rescaling(Squares{nu2, 0}, g.target[i]);
     exp += shift;
     const float alpha = ldexpf(g.to_h[i], shift - 2 * e), beta = ldexpf(g.h_to_h[i], shift);
     float sum = 0.f;
@@ -394,9 +396,8 @@ __global__ void __launch_bounds__(kThreads, 1) small_backward(const __grid_const
     }
   }
   __syncthreads();
-  // dG = s (H_0 - G <H_0, G> s / norm), <h, G> = dots 2^-(k + xe)
-  float by_h, by_g;
-  end_factors(info, dots, exp, g.xe[0], by_h, by_g);
+  float by_h, by_g, up;
+  end_factors(info, dots, exp, g.xe[0], by_h, by_g, up);
   const T* x = static_cast<const T*>(g.g) + (size_t)l * g.p * g.q;
   T* out = static_cast<T*>(g.y) + (size_t)l * g.p * g.q;
   for (int i = threadIdx.x; i < g.p * g.q; i += kThreads) {
@@ -407,7 +408,7 @@ __global__ void __launch_bounds__(kThreads, 1) small_backward(const __grid_const
     for (int t = 0; t < TERMS; ++t)
       h += __half2float(*reinterpret_cast<const __half*>(H.tile(t, c >> 6) + sw128_offset(r, (c & 63) >> 3) +
                                                          2 * (c & 7)));
-    out[i] = from_f32<T>(fmaf(-by_g, to_f32<T>(x[i]), by_h * h));
+    out[i] = from_f32<T>(fmaf(-by_g, to_f32<T>(x[i]) * up, by_h * h));
   }
   end_block(sh, cols);
 }

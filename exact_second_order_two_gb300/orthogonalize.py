@@ -113,7 +113,7 @@ def orthogonalize(g: torch.Tensor, steps: int = 5, coefficients=QUINTIC,
     that start in [0, 1] must stay below 64 under them, and small ones must not fall
     far: the product of those |a| that are below 1 is at least 1/256.  steps from 1 to 16.
     eps >= 0.  The shorter side is taken as the rows of X.  Norms, of g and of what comes
-    from above in the backward, are taken by squares in fp32: from 1e-19 to 1e19.
+    from above in the backward, may be from 1e-34 to 1e38, or 0.
 
     Returns a contiguous tensor of g's shape and dtype.  Differentiable once in g, in
     reverse mode.  bf16: products of fp16 operands with fp32 sums, about as far from

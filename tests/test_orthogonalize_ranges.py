@@ -1,5 +1,6 @@
-"""Orthogonalisation of matrices whose norm is small beside eps, against the
-definition in 64 bits: what eps takes off the norm is no loss of digits."""
+"""Orthogonalisation of matrices whose norm is small beside eps, or whose squares are
+past fp32's range, against the definition in 64 bits and against themselves times
+powers of two."""
 import pytest
 import torch
 
@@ -70,3 +71,66 @@ def test_small_beside_eps_it_is_linear(shape):
     by = 3.4445 ** 5 / 1e-7
     for got, want in ((Y, by * G.double()), (dG, by * dY.double())):
         assert (got.double() - want).norm() <= 2.0 ** -18 * want.norm()
+
+
+def same(got, want, power):
+    """got is want 2^power: the same bits, but for results about the subnormal ones.  There
+    both terms of dG = by_h H - by_g G, or their sum, are rounded to the subnormals' step
+    (2^-126 eps; fp32's for the terms): up to half a step for each of the two roundings here and
+    of the one there.  Above 2^-124 a half of that step is below half of the result's own."""
+    want = want * 2.0 ** power
+    step = 2.0 ** -126 * torch.finfo(got.dtype).eps
+    off = torch.where(want.abs() >= 2.0 ** -124, 0.0, 1.5 * step).double()
+    return bool(torch.isfinite(want).all() and ((got.double() - want.double()).abs() <= off).all())
+
+
+@pytest.mark.parametrize("shape", [(60, 80), (300, 400), (403, 301), (3, 40, 50), (2048, 2048)], ids=str)
+@pytest.mark.parametrize("dtype", ["bf16", "fp32"])
+@pytest.mark.parametrize("power", [-90, -80, -66, 66, 80, 105])
+def test_a_power_of_two_leaves_the_bits(shape, dtype, power):
+    """Without eps the result does not know G's size, and the gradient goes with its
+    reciprocal: bits are the same, for entries whose squares are past fp32's range on both sides."""
+    G, dY = gradient(shape, DT[dtype], std=1.0)
+    Y, dG = both(G, dY, [ONE] * 5, eps=0.0)
+    y, dg = both(G * 2.0 ** power, dY, [ONE] * 5, eps=0.0)
+    assert same(y, Y, 0) and same(dg, dG, -power)
+
+
+@pytest.mark.parametrize("shape", [(60, 80), (300, 400), (403, 301), (2048, 2048)], ids=str)
+@pytest.mark.parametrize("dtype", ["bf16", "fp32"])
+@pytest.mark.parametrize("power", [-90, -80, -66, 66, 80, 105])
+def test_a_power_of_two_in_the_gradient_leaves_the_bits(shape, dtype, power):
+    G, dY = gradient(shape, DT[dtype], std=1.0)
+    want = both(G, dY, [ONE] * 5)[1]
+    assert same(both(G, dY * 2.0 ** power, [ONE] * 5)[1], want, power)
+
+
+def test_one_entry_of_any_size_among_zeros():
+    """x / |x| for the smallest and largest entries, in an edge of one matrix of a stack.  One
+    singular value of 1 takes the polynomial's own values.  X, A and B are rounded once a step
+    (2^-11 for bf16, 2^-22 for fp32), which the step multiplies by at most 8 all three together
+    (|b x| + 2 |c x| and what X gives A, for x <= 1.2), and the slopes behind it, of 1.3 at most, by
+    3: five steps, 120 roundings; the result's own is 2^-8 and 2^-24."""
+    for dtype, tol in ((torch.bfloat16, 120 * 2.0 ** -11 + 2.0 ** -8), (torch.float32, 120 * 2.0 ** -22)):
+        for shape in ((2, 30, 40), (2, 200, 300), (2, 1500, 1600)):
+            for x in (1e-34, 1e-20, 1e18, 1e37):
+                G = torch.zeros(shape, dtype=dtype, device="cuda")
+                G[0, 0, 0] = 1.0
+                G[1, -1, -1] = x
+                Y = fbob.orthogonalize(G, eps=0.0)
+                want = 1.0
+                for _ in range(5):
+                    want = 3.4445 * want - 4.775 * want ** 3 + 2.0315 * want ** 5
+                assert abs(Y[1, -1, -1].item() - want) <= tol * abs(want), (dtype, shape, x)
+                Y[0, 0, 0] = Y[1, -1, -1] = 0
+                assert not Y.any()
+
+
+def test_norms_past_fp32_of_entries_within():
+    """Entries of 1e38 in rows, norms of up to 3e38."""
+    for dtype in DT.values():
+        G = torch.zeros(200, 300, dtype=dtype, device="cuda")
+        G[torch.arange(8), torch.arange(8)] = 1e38
+        Y = fbob.orthogonalize(G)
+        X, own = exact(G.float() * 2.0 ** -100, None, [ONE] * 5, eps=0.0)[0], model(G * 2.0 ** -100, None, [ONE] * 5)[0]
+        check(Y, X, own, dtype)
