@@ -26,7 +26,12 @@
 // so that X is kept in two terms, of which the products take the first and a X
 // both, in steps whose rounding later steps would multiply by more than 16.
 // (256 x 1024 of rank 16 with noise of a hundredth: 1.6e-2 of the norm off with one term,
-// 2.2e-3 with two, 1.7e-3 for the result's own rounding.)
+// 2.2e-3 with two, 1.7e-3 for the result's own rounding.)  In the backward the same growth
+// meets the errors of H, S and T, and S and T are factors only: they have two terms where the
+// steps still to come multiply a rounding by more than 4, and products read H's second
+// term where they do by more than 16.  (1024 x 1024 of rank 16 with noise of 0.3, dY among the
+// strong directions: dG 1.7e-2 off with one term each, 2.4e-3 so, of which 1.7e-3 are its own
+// rounding; 2.4e-3 with second terms everywhere.)
 #include <cuda.h>
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
@@ -417,6 +422,8 @@ struct Plan {
   float a[kMaxSteps], b[kMaxSteps], c[kMaxSteps];
   int xe[kMaxSteps], ae[kMaxSteps], be[kMaxSteps];  // exponents of X, A, B as stored
   int xt[kMaxSteps];                                // terms of X
+  int st[kMaxSteps], ht[kMaxSteps];                 // of S and T, and of the H that a step takes,
+  int hp[kMaxSteps];                                // in its sum and in its products
   double M[kMaxSteps];                              // bound on X's singular values
   Steps device;                                     // the same for the kernels
   int square_parts;
@@ -511,6 +518,15 @@ int make_plan(const fbob_orth_t* o, Plan* out) {
     growth *= fabs(p.a[i]) > 1 ? fabs(p.a[i]) : 1;
     // (a bf16 G is one fp16 term, times a power of two)
     p.xt[i] = !p.bf16 || (growth > 16 && i > 0) ? 2 : 1;
+  }
+  growth = 1;  // by the steps that the backward takes behind step i
+  for (int i = 0; i < p.steps; ++i) {
+    p.st[i] = !p.bf16 || growth > 4 ? 2 : 1;
+    const bool much = growth > 16;
+    growth *= fabs(p.a[i]) > 1 ? fabs(p.a[i]) : 1;
+    // (a bf16 dY is one fp16 term, times a power of two)
+    p.ht[i] = !p.bf16 || (growth > 4 && i + 1 < p.steps) ? 2 : 1;
+    p.hp[i] = !p.bf16 || (p.ht[i] == 2 && much) ? 2 : 1;
   }
   const long long elems = (long long)p.p * p.q;
   const long long parts = (elems + 8191) / 8192;
@@ -609,24 +625,29 @@ struct Backward {
   Mats H, S, T;
   size_t bytes;
 };
-int step_wide(const Plan& p) {  // of B H + T X
-  return choose_wide(p, p.q, p.p, false, p.bf16 ? 2 : 6);
+int step_parts(const Plan& p, int i) {  // of the squares of B H + T X
+  const int segs = p.bf16 ? p.hp[i] + p.st[i] : 6;
+  return (int)tiles_of(p.p, p.q, false, choose_wide(p, p.q, p.p, false, segs)) * 2 * kEpiWarps;
 }
-int step_parts(const Plan& p) { return (int)tiles_of(p.p, p.q, false, step_wide(p)) * 2 * kEpiWarps; }
 Backward carve_backward(const Plan& p, char* base) {
   Backward w;
   Carver c{base, 0};
-  const int two = p.bf16 ? 0 : 1;
+  int h_two = 0, s_two = 0, most = 0;
+  for (int i = 0; i < p.steps; ++i) {
+    if (p.ht[i] == 2) h_two = 1;
+    if (p.st[i] == 2) s_two = 1;
+    if (step_parts(p, i) > most) most = step_parts(p, i);
+  }
   w.status = static_cast<int*>(c.take(sizeof(int)));
   w.counters = static_cast<int*>(c.take(sizeof(int) * counters(p)));
   w.sums = static_cast<Squares*>(c.take(sizeof(Squares) * p.L * p.square_parts));
   w.dots = static_cast<float*>(c.take(sizeof(float) * p.L * p.square_parts));
   w.first = static_cast<float*>(c.take(sizeof(float) * p.L));
-  for (float*& s : w.step_sums) s = static_cast<float*>(c.take(sizeof(float) * p.L * step_parts(p)));
+  for (float*& s : w.step_sums) s = static_cast<float*>(c.take(sizeof(float) * p.L * most));
   for (int i = 0; i <= p.steps; ++i) w.exp[i] = static_cast<int*>(c.take(sizeof(int) * p.L));
-  w.H = c.mats(p, p.q, p.ldq, 2, 2 * two);
-  w.S = c.mats(p, p.p, p.ldp, 1, two);
-  w.T = c.mats(p, p.p, p.ldp, 1, two);
+  w.H = c.mats(p, p.q, p.ldq, 2, 2 * h_two);
+  w.S = c.mats(p, p.p, p.ldp, 1, s_two);
+  w.T = c.mats(p, p.p, p.ldp, 1, s_two);
   w.bytes = c.off;
   return w;
 }
@@ -693,10 +714,8 @@ struct Chain {
   }
   // acc += P Q^T (or P Q): every pair of terms but the two low ones
   void add(const Ref& P, const Ref& Q) {
-    if (P.terms == 2) {
-      pair(P, 0, Q, 1);
-      pair(P, 1, Q, 0);
-    }
+    if (Q.terms == 2) pair(P, 0, Q, 1);
+    if (P.terms == 2) pair(P, 1, Q, 0);
     pair(P, 0, Q, 0);
   }
   // exponents of alpha and of beta for a matrix with exponents e[i], e[i + 1]
@@ -826,11 +845,15 @@ cudaError_t small(const Plan& p, const void* G, const void* dY, void* out, Forwa
   g.steps = p.device;
   int se[kMaxSteps];
   backward_scales(p, g.target, se);
-  g.x_terms = 1;
+  g.x_terms = g.h_terms = 1;
   for (int i = 0; i < p.steps; ++i) {
     const int te = p.be[i] - p.xe[i], out_exp = i + 1 < p.steps ? p.xe[i + 1] : 0;
     if (p.xt[i] > g.x_terms) g.x_terms = p.xt[i];
+    if (p.ht[i] == 2 || p.st[i] == 2) g.h_terms = 2;
     g.xt[i] = p.xt[i];
+    g.two_s |= (unsigned)(p.st[i] == 2) << i;
+    g.two_h |= (unsigned)(p.ht[i] == 2) << i;
+    g.two_hp |= (unsigned)(p.hp[i] == 2) << i;
     g.xe[i] = p.xe[i];
     g.to_a[i] = pow2(p.ae[i] - 2 * p.xe[i]);
     g.to_b[i] = p.c[i] * pow2(p.be[i] - 2 * p.ae[i]);
@@ -911,15 +934,16 @@ cudaError_t backward(const Plan& p, const void* G, const void* dY, void* dG, For
   const int top = p.steps - 1, terms = p.bf16 ? 1 : 2;
   Chain c(p, w.status, w.counters, f.info);
   for (Mats* m : {&f.X, &f.A, &f.B, &w.H, &w.S, &w.T}) c.use(*m);
-  const Ref S{&w.S, 0, terms}, T{&w.T, 0, terms};
   const float* sums = w.first;
   int parts = 1, turn = 0;
   for (int i = top; i >= 0; --i, turn ^= 1) {
-    const Ref H{&w.H, turn, terms}, X{&f.X, i, terms}, A{&f.A, i, terms}, B{&f.B, i, terms};
+    const Ref H{&w.H, turn, p.ht[i]}, Hm{&w.H, turn, p.hp[i]};  // as it is added, and multiplied
+    const Ref X{&f.X, i, terms}, A{&f.A, i, terms}, B{&f.B, i, terms};
+    const Ref S{&w.S, 0, p.st[i]}, T{&w.T, 0, p.st[i]};
     const int by_f = i == 0 ? 1 : 0;  // X_0 is f times what is stored
     c.begin(p.p, p.q, false, true);
-    c.add(H, X);
-    c.add(X, H);
+    c.add(Hm, X);
+    c.add(X, Hm);
     c.phase().alpha = pow2(se[i] - p.xe[i]);
     c.phase().fpow = by_f;
     c.to(S);
@@ -937,7 +961,7 @@ cudaError_t backward(const Plan& p, const void* G, const void* dY, void* dG, For
     c.to(T);
     c.end();
     c.begin(p.q, p.p, true, false);
-    c.add(B, H);
+    c.add(B, Hm);
     c.add(T, X);
     c.plus(H);
     Phase& h = c.phase();
@@ -950,15 +974,15 @@ cudaError_t backward(const Plan& p, const void* G, const void* dY, void* dG, For
     h.target = target[i];
     h.exp_in = w.exp[i + 1];
     h.exp_out = w.exp[i];
-    c.to(Ref{&w.H, turn ^ 1, terms});
+    c.to(Ref{&w.H, turn ^ 1, i > 0 ? p.ht[i - 1] : terms});
     c.end();
     sums = w.step_sums[turn];
-    parts = step_parts(p);
+    parts = step_parts(p, i);
   }
   if (!c.ok) return cudaErrorUnknown;
   PackArgs a = {};
   a.hi = w.H.hi;
-  a.lo = w.H.lo;
+  a.lo = p.bf16 ? nullptr : w.H.lo;
   a.target = target[p.steps];
   a.exp_out = w.exp[p.steps];
   a.sums_out = w.first;
@@ -967,7 +991,7 @@ cudaError_t backward(const Plan& p, const void* G, const void* dY, void* dG, For
   if (e != cudaSuccess) return e;
   DotArgs d = {};
   d.h[0] = w.H.hi + turn * w.H.slot;
-  d.h[1] = w.H.lo ? w.H.lo + turn * w.H.slot : nullptr;
+  d.h[1] = p.bf16 ? nullptr : w.H.lo + turn * w.H.slot;
   d.x[0] = f.X.hi;
   d.x[1] = p.xt[0] == 2 ? f.X.lo : nullptr;
   d.partial = w.dots;

@@ -111,8 +111,11 @@ struct SmallArgs {
   int L, p, q, tall, keep;
   float eps;
   Steps steps;
-  int x_terms;                               // most of X in a step
+  int x_terms, h_terms;                      // most of X, and of H, S and T, in a step
+  int x_tiles;                               // backward: tiles of X (64 columns) held at a time
   int xt[kMaxSteps], xe[kMaxSteps];
+  // a bit for each step: two terms of S and T; of H where it is added; of H in products
+  unsigned two_s, two_h, two_hp;
   float to_a[kMaxSteps], to_b[kMaxSteps], a_to_b[kMaxSteps], to_x[kMaxSteps], x_to_x[kMaxSteps];
   float to_s[kMaxSteps], to_t[kMaxSteps], s_to_t[kMaxSteps], to_h[kMaxSteps], h_to_h[kMaxSteps];
   int target[kMaxSteps + 1];
@@ -182,6 +185,9 @@ __device__ __forceinline__ int rescaling(Squares nu2, int target) {
   e += nu2.e;  // nu2 < 2^e
   return min(127, target - ((e + 1) >> 1));
 }
+
+// x 2^e, nearly always x.
+__device__ __forceinline__ float times_pow2(float x, int e) { return e == 0 ? x : ldexpf(x, e); }
 
 // Powers of two that are sure to lie between m and the bound (by their exponents: none
 // where m is infinite or NaN).

@@ -10,7 +10,8 @@
 // fp32, with its gradient: 168 us, of 357.  Symmetric results are computed whole, which saves the mirroring.
 //
 // With a backward to follow, X, A and B of every step leave for the workspace by TMA.  The
-// backward holds H, S (then T) and, in turn in one place, X, A, B and X again.
+// backward holds H, S (then T) and, in turn in one place, X (in two parts where second terms of
+// H and S leave no room for more), A, B and X again.
 #include <cuda.h>
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
@@ -45,6 +46,7 @@ struct Shared {
   uint32_t tmem;
   Abort ab;
   float red[kThreads / 32];
+  short e[kMaxSteps + 1];
 };
 constexpr uint32_t kMisc = 256;
 static_assert(sizeof(Shared) <= kMisc, "small orthogonalisation: shared memory");
@@ -117,12 +119,13 @@ __device__ __forceinline__ void multiply(uint32_t acc, const Held& P, int tp, co
     mma_ss(acc, a + 2 * u, b + (nn ? kstep_off(u) : 2 * u), id, begun || u > 0 ? 1u : 0u);
 }
 // A product over `depth` tiles: every pair of terms but the two low ones, the high ones
-// last.  With two terms, sums of 64 products of high terms each in an accumulator of their own
+// last.  For fp32, sums of 64 products of high terms each in an accumulator of their own
 // (of four; at most two tiles, two products), for what the tensor cores cut off their
-// additions; `first` is the product's first accumulator.
+// additions; `first` is the product's first accumulator, or not 0 where the one that there is
+// has been begun.  pt, qt: terms of P and Q for bf16.
 template <int TERMS>
-__device__ __forceinline__ void multiply_terms(uint32_t acc, const Held& P, const Held& Q, bool nn, int depth,
-                                               int first) {
+__device__ __forceinline__ void multiply_terms(uint32_t acc, const Held& P, int pt, const Held& Q, int qt, bool nn,
+                                               int depth, int first) {
   for (int k = 0; k < depth; ++k) {
     if (TERMS == 2) {
       const uint32_t own = acc + 128 * (first + k);
@@ -130,7 +133,16 @@ __device__ __forceinline__ void multiply_terms(uint32_t acc, const Held& P, cons
       multiply(own, P, 1, Q, 0, nn, k, true);
       multiply(own, P, 0, Q, 0, nn, k, true);
     } else {
-      multiply(acc, P, 0, Q, 0, nn, k, first + k > 0);
+      bool begun = first + k > 0;
+      if (qt == 2) {
+        multiply(acc, P, 0, Q, 1, nn, k, begun);
+        begun = true;
+      }
+      if (pt == 2) {
+        multiply(acc, P, 1, Q, 0, nn, k, begun);
+        begun = true;
+      }
+      multiply(acc, P, 0, Q, 0, nn, k, begun);
     }
   }
 }
@@ -141,11 +153,12 @@ __device__ __forceinline__ void store_held(const CUtensorMap* hi, const CUtensor
     for (int c = 0; c < h.tiles && 64 * c < cols; ++c) tma_store_3d(t ? lo : hi, h.tile(t, c), 64 * c, 0, at);
   bulk_commit_group();
 }
-__device__ __forceinline__ void load_held(const CUtensorMap* hi, const CUtensorMap* lo, const Held& h, int tiles,
-                                          uint64_t* bar, int at) {
+// tiles first .. first + tiles - 1 of the columns, to h's first
+__device__ __forceinline__ void load_held(const CUtensorMap* hi, const CUtensorMap* lo, const Held& h, int first,
+                                          int tiles, uint64_t* bar, int at) {
   mbar_arrive_expect_tx(bar, (lo ? 2 : 1) * tiles * kTileBytes);
   for (int t = 0; t < (lo ? 2 : 1); ++t)
-    for (int c = 0; c < tiles; ++c) tma_load_3d(h.tile(t, c), t ? lo : hi, bar, 64 * c, 0, at);
+    for (int c = 0; c < tiles; ++c) tma_load_3d(h.tile(t, c), t ? lo : hi, bar, 64 * (first + c), 0, at);
 }
 
 __device__ __forceinline__ void begin_block(Shared* sh, uint32_t cols, const SmallArgs& g) {
@@ -245,7 +258,7 @@ __global__ void __launch_bounds__(kThreads, 1) small_forward(const __grid_consta
     hand_over();
     if (threadIdx.x == 0 && !sh->ab.flag) {
       store();
-      multiply_terms<TERMS>(acc, P, Q, nn, depth, 0);
+      multiply_terms<TERMS>(acc, P, 1, Q, 1, nn, depth, 0);
       bulk_wait_read_all();
       mma_commit(&sh->mma);
     }
@@ -268,14 +281,14 @@ __global__ void __launch_bounds__(kThreads, 1) small_forward(const __grid_consta
     product(A, A, false, deep, [&] {
       if (g.keep) store_held(&g.a_map[0], TERMS == 2 ? &g.a_map[1] : nullptr, A, i * g.L + l, g.p, g.p);
     });
-    read_acc(acc, deep_sums, unit, ldexpf(g.to_b[i], -2 * e), v);
+    read_acc(acc, deep_sums, unit, times_pow2(g.to_b[i], -2 * e), v);
     add_slot(v, A.tile(0, unit >> 1), row, unit & 1, g.a_to_b[i]);
     if (TERMS == 2) add_slot(v, A.tile(1, unit >> 1), row, unit & 1, g.a_to_b[i]);
     put(v, A, TERMS, row, unit);
     product(A, X, true, deep, [&] {
       if (g.keep) store_held(&g.b_map[0], TERMS == 2 ? &g.b_map[1] : nullptr, A, i * g.L + l, g.p, g.p);
     });
-    const float to_x = ldexpf(f * g.to_x[i], e1 - 3 * e), x_to_x = ldexpf(f * g.x_to_x[i], e1 - e);
+    const float to_x = times_pow2(f * g.to_x[i], e1 - 3 * e), x_to_x = times_pow2(f * g.x_to_x[i], e1 - e);
     e = e1;
     for (int u = unit; u < 2 * tiles; u += 4) {
       read_acc(acc, deep_sums, u, to_x, v);
@@ -304,13 +317,14 @@ __global__ void __launch_bounds__(kThreads, 1) small_backward(const __grid_const
     if (threadIdx.x == 0) report_status(g.status, FBOB_ERR_CUDA);
     return;
   }
-  const int tiles = (g.q + 63) / 64, l = blockIdx.x, room = tiles > kSquare ? tiles : kSquare;
-  const Held H{smem, tiles}, S{smem + TERMS * tiles * kTileBytes, kSquare};
-  // what comes from memory: X, or A or B
-  const Held X{S.at + TERMS * kSquare * kTileBytes, tiles}, A{X.at, kSquare};
+  const int tiles = (g.q + 63) / 64, l = blockIdx.x, room = g.x_tiles > kSquare ? g.x_tiles : kSquare;
+  const Held H{smem, tiles}, S{smem + g.h_terms * tiles * kTileBytes, kSquare};
+  // what comes from memory: X, x_tiles of it at a time, or A or B
+  const Held X{S.at + g.h_terms * kSquare * kTileBytes, g.x_tiles}, A{X.at, kSquare};
   Shared* sh = reinterpret_cast<Shared*>(X.at + TERMS * room * kTileBytes);
   const uint32_t cols = TERMS == 2 ? 512 : tiles > 2 ? 256 : 128;
   if (l == 0 && threadIdx.x == 0) *g.status = 0;
+  if (threadIdx.x < g.steps.n) sh->e[threadIdx.x] = g.info[l].e[threadIdx.x];
   begin_block(sh, cols, g);
   const uint32_t acc = sh->tmem;
   const int row = 32 * ((threadIdx.x >> 5) & 3) + (threadIdx.x & 31), unit = threadIdx.x >> 7;
@@ -320,9 +334,10 @@ __global__ void __launch_bounds__(kThreads, 1) small_backward(const __grid_const
   const MatInfo info = g.info[l];
   int n = 0, m = 0;  // products and loads so far
   bool ok = true;
-  auto load = [&](const CUtensorMap* maps, const Held& to, int count, int i) {  // by thread 0
-    if (!sh->ab.flag) load_held(&maps[0], TERMS == 2 ? &maps[1] : nullptr, to, count, &sh->load, i * g.L + l);
+  auto load = [&](const CUtensorMap* maps, const Held& to, int first, int count, int i) {  // by thread 0
+    if (!sh->ab.flag) load_held(&maps[0], TERMS == 2 ? &maps[1] : nullptr, to, first, count, &sh->load, i * g.L + l);
   };
+  auto part = [&](int first) { return min(g.x_tiles, tiles - first); };  // of X from a tile on
   auto loaded = [&] { ok = ok && warp_wait(&sh->load, m++ & 1, &sh->ab, g.status); };
   auto product = [&](auto issue) {
     hand_over();
@@ -334,7 +349,7 @@ __global__ void __launch_bounds__(kThreads, 1) small_backward(const __grid_const
     ok = ok && warp_wait(&sh->mma, n++ & 1, &sh->ab, g.status);
     tc_fence_after();
   };
-  if (threadIdx.x == 0) load(g.x_map, X, tiles, g.steps.n - 1);
+  if (threadIdx.x == 0) load(g.x_map, X, 0, part(0), g.steps.n - 1);
   const Squares dy2 = squares(dy, g.p * g.q, sh->red);
   int exp = rescaling(dy2, g.target[g.steps.n]);
   const float factor = ldexpf(1.f, exp);
@@ -342,62 +357,75 @@ __global__ void __launch_bounds__(kThreads, 1) small_backward(const __grid_const
   float nu2 = ldexpf(dy2.m, dy2.e + 2 * exp);
   float dots = 0.f;
   for (int i = g.steps.n - 1; i >= 0; --i) {
-    const int e = g.info[l].e[i];  // X, S and T are 2^e larger in store, A and B 2^(2 e)
+    const int e = sh->e[i];  // X, S and T are 2^e larger in store, A and B 2^(2 e)
     const float f = i == 0 ? info.f : 1.f;  // X_0 is f times what is stored
+    // terms of S and T, of H, and of H in products
+    const int st = TERMS == 2 ? 2 : 1 + (g.two_s >> i & 1), ht = TERMS == 2 ? 2 : 1 + (g.two_h >> i & 1);
+    const int hp = TERMS == 2 ? 2 : 1 + (g.two_hp >> i & 1);
     f2 v[16];
-    loaded();
-    product([&] {
-      multiply_terms<TERMS>(acc, H, X, false, tiles, 0);
-      multiply_terms<TERMS>(acc, X, H, false, tiles, tiles);
-    });
-    if (threadIdx.x == 0) load(g.a_map, A, kSquare, i);
+    for (int c = 0; c < tiles; c += g.x_tiles) {
+      loaded();
+      product([&] {
+        const Held Hc{H.at + c * kTileBytes, tiles};  // the columns that are here of X
+        multiply_terms<TERMS>(acc, Hc, hp, X, 1, false, part(c), c);
+        multiply_terms<TERMS>(acc, X, 1, Hc, hp, false, part(c), TERMS == 2 ? tiles : 1);
+      });
+      if (threadIdx.x == 0 && c + g.x_tiles < tiles) load(g.x_map, X, c + g.x_tiles, part(c + g.x_tiles), i);
+    }
+    if (threadIdx.x == 0) load(g.a_map, A, 0, kSquare, i);
     read_acc(acc, wide_sums, unit, f * g.to_s[i], v);
-    put(v, S, TERMS, row, unit);
+    put(v, S, st, row, unit);
     loaded();
     product([&] {
-      multiply_terms<TERMS>(acc, A, S, false, deep, 0);
-      multiply_terms<TERMS>(acc, S, A, false, deep, deep);
+      multiply_terms<TERMS>(acc, A, 1, S, st, false, deep, 0);
+      multiply_terms<TERMS>(acc, S, st, A, 1, false, deep, deep);
     });
-    if (threadIdx.x == 0) load(g.b_map, A, kSquare, i);
-    read_acc(acc, deep_sums, unit, ldexpf(f * g.to_t[i], -2 * e), v);  // T in S's place
+    if (threadIdx.x == 0) load(g.b_map, A, 0, kSquare, i);
+    read_acc(acc, deep_sums, unit, times_pow2(f * g.to_t[i], -2 * e), v);  // T in S's place
     add_slot(v, S.tile(0, unit >> 1), row, unit & 1, f * g.s_to_t[i]);
-    if (TERMS == 2) add_slot(v, S.tile(1, unit >> 1), row, unit & 1, f * g.s_to_t[i]);
-    put(v, S, TERMS, row, unit);
+    if (st == 2) add_slot(v, S.tile(1, unit >> 1), row, unit & 1, f * g.s_to_t[i]);
+    put(v, S, st, row, unit);
     loaded();
-    product([&] { multiply_terms<TERMS>(acc, A, H, true, deep, 0); });
-    if (threadIdx.x == 0) load(g.x_map, X, tiles, i);
-    loaded();
-    product([&] { multiply_terms<TERMS>(acc, S, X, true, deep, deep); });
+    product([&] { multiply_terms<TERMS>(acc, A, 1, H, hp, true, deep, 0); });
     const int shift = rescaling(Squares{nu2, 0}, g.target[i]);
     exp += shift;
     const float alpha = ldexpf(g.to_h[i], shift - 2 * e), beta = ldexpf(g.h_to_h[i], shift);
     float sum = 0.f;
-    for (int u = unit; u < 2 * tiles; u += 4) {
-      read_acc(acc, deep_sums, u, alpha, v);
-      add_slot(v, H.tile(0, u >> 1), row, u & 1, beta);
-      if (TERMS == 2) add_slot(v, H.tile(1, u >> 1), row, u & 1, beta);
-      f2 w[16];
+    for (int c = 0; c < tiles; c += g.x_tiles) {
+      if (threadIdx.x == 0) load(g.x_map, X, c, part(c), i);
+      loaded();
+      product([&] {
+        multiply_terms<TERMS>(acc + 64 * c, S, st, Held{X.at, part(c)}, 1, true, deep, deep);
+      });
+      for (int u = 2 * c + unit; u < 2 * (c + part(c)); u += 4) {
+        read_acc(acc, deep_sums, u, alpha, v);
+        add_slot(v, H.tile(0, u >> 1), row, u & 1, beta);
+        if (ht == 2) add_slot(v, H.tile(1, u >> 1), row, u & 1, beta);
+        f2 w[16];
 #pragma unroll
-      for (int k = 0; k < 16; ++k) w[k] = i > 0 ? v[k] : f2{0.f, 0.f};
-      if (i == 0) {  // <H_0, X_0>, which is still there
-        add_slot(w, X.tile(0, u >> 1), row, u & 1, 1.f);
-        if (TERMS == 2) add_slot(w, X.tile(1, u >> 1), row, u & 1, 1.f);
+        for (int k = 0; k < 16; ++k) w[k] = i > 0 ? v[k] : f2{0.f, 0.f};
+        if (i == 0) {  // <H_0, X_0>, which is still there
+          add_slot(w, X.tile(0, (u >> 1) - c), row, u & 1, 1.f);
+          if (TERMS == 2) add_slot(w, X.tile(1, (u >> 1) - c), row, u & 1, 1.f);
+        }
+#pragma unroll
+        for (int k = 0; k < 16; ++k) sum = fmaf(v[k].x, w[k].x, fmaf(v[k].y, w[k].y, sum));
+        put(v, H, TERMS == 2 ? 2 : i > 0 ? 1 + (g.two_h >> (i - 1) & 1) : 1, row, u);
       }
-#pragma unroll
-      for (int k = 0; k < 16; ++k) sum = fmaf(v[k].x, w[k].x, fmaf(v[k].y, w[k].y, sum));
-      put(v, H, TERMS, row, u);
+      if (i == 0) __syncthreads();  // every thread is past its reads of this part of X
     }
-    sum = block_sum(sum, sh->red);  // (every thread is past its reads of X)
+    sum = block_sum(sum, sh->red);
     if (i > 0) {
       nu2 = sum;
-      if (threadIdx.x == 0) load(g.x_map, X, tiles, i - 1);
+      if (threadIdx.x == 0) load(g.x_map, X, 0, part(0), i - 1);
     } else {
       dots = sum;
     }
   }
   __syncthreads();
-  float by_h, by_g, up;
-  end_factors(info, dots, exp, g.xe[0], by_h, by_g, up);
+  if (threadIdx.x == 0) end_factors(info, dots, exp, g.xe[0], sh->red[0], sh->red[1], sh->red[2]);
+  __syncthreads();  // (64-bit arithmetic is slow: once is enough)
+  const float by_h = sh->red[0], by_g = sh->red[1], up = sh->red[2];
   const T* x = static_cast<const T*>(g.g) + (size_t)l * g.p * g.q;
   T* out = static_cast<T*>(g.y) + (size_t)l * g.p * g.q;
   for (int i = threadIdx.x; i < g.p * g.q; i += kThreads) {
@@ -420,7 +448,7 @@ bool small_fits(int p, int q, bool bf16) { return p <= kTile && q <= (bf16 ? 256
 template <typename T>
 cudaError_t launch(const SmallArgs& g, bool backward, LaunchLog& log) {
   const int terms = sizeof(T) == 2 ? 1 : 2, tiles = (g.q + 63) / 64;
-  const int held = backward ? terms * (tiles + kSquare + (tiles > kSquare ? tiles : kSquare))
+  const int held = backward ? g.h_terms * (tiles + kSquare) + terms * (g.x_tiles > kSquare ? g.x_tiles : kSquare)
                             : g.x_terms * tiles + terms * kSquare;
   const int smem = held * (int)kTileBytes + (int)kMisc;
   auto kernel = backward ? small_backward<T> : small_forward<T>;
@@ -431,7 +459,12 @@ cudaError_t launch(const SmallArgs& g, bool backward, LaunchLog& log) {
   log.mark();
   return e;
 }
-cudaError_t launch_small(const SmallArgs& g, bool bf16, bool backward, LaunchLog& log) {
+cudaError_t launch_small(const SmallArgs& args, bool bf16, bool backward, LaunchLog& log) {
+  SmallArgs g = args;
+  // all of X, or, where 14 tiles of shared memory would not hold that, two tiles at a time: 4 of
+  // H, and S, in two terms each
+  const int tiles = (g.q + 63) / 64;
+  g.x_tiles = g.h_terms * (tiles + kSquare) + tiles <= 14 || !bf16 ? tiles : kSquare;
   return bf16 ? launch<__nv_bfloat16>(g, backward, log) : launch<float>(g, backward, log);
 }
 
