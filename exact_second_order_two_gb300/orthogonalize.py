@@ -23,6 +23,23 @@ from . import _binding as _b
 QUINTIC = (3.4445, -4.7750, 2.0315)
 
 
+def _numbers(coefficients):
+    """One triple or several as tuples of Python's floats, which calls can be told apart by:
+    a tensor could be another number the next time."""
+    if type(coefficients) is tuple and all(type(x) is float for x in coefficients):
+        return (coefficients,)
+    if torch.is_tensor(coefficients) or hasattr(coefficients, "tolist"):
+        if torch.is_tensor(coefficients) and (coefficients.requires_grad or _b.dual(coefficients)):
+            raise ValueError("coefficients are not differentiated: pass them detached")
+        coefficients = coefficients.tolist()
+    if not isinstance(coefficients[0], (tuple, list)) and getattr(coefficients[0], "ndim", 0) == 0:
+        coefficients = (coefficients,)
+    for x in (x for abc in coefficients for x in abc):
+        if torch.is_tensor(x) and (x.requires_grad or _b.dual(x)):
+            raise ValueError("coefficients are not differentiated: pass them detached")
+    return tuple(tuple(float(x) for x in abc) for abc in coefficients)
+
+
 def _coefficients(steps, polynomials):
     """The steps' a, b, c as a C array."""
     if len(polynomials) == 1:
@@ -109,7 +126,8 @@ def orthogonalize(g: torch.Tensor, steps: int = 5, coefficients=QUINTIC,
     times X <- a X + b (X X^T) X + c (X X^T)^2 X.
 
     g: bf16 or fp32 CUDA tensor, not empty (copied first if not contiguous).
-    coefficients: (a, b, c), or one such triple for each step; singular values
+    coefficients: (a, b, c), or one such triple for each step, numbers, which are not
+    differentiated (a tensor on the GPU is waited for); singular values
     that start in [0, 1] must stay below 64 under them, and small ones must not fall
     far: the product of those |a| that are below 1 is at least 1/256.  steps from 1 to 16.
     eps >= 0.  The shorter side is taken as the rows of X.  Norms, of g and of what comes
@@ -136,9 +154,7 @@ def orthogonalize(g: torch.Tensor, steps: int = 5, coefficients=QUINTIC,
         raise ValueError(f"steps must be from 1 to 16, got {steps}")
     if not (eps >= 0 and math.isfinite(eps)):
         raise ValueError(f"eps must be at least 0 and finite, got {eps}")
-    if not isinstance(coefficients[0], (tuple, list)):
-        coefficients = (coefficients,)
-    how = (steps, tuple(map(tuple, coefficients)), float(eps))
+    how = (steps, _numbers(coefficients), float(eps))
     g = g.contiguous()
     if (torch.is_grad_enabled() and g.requires_grad) or _b.dual(g):
         return _Orthogonalize.apply(g, how)
