@@ -23,6 +23,10 @@ from . import _binding as _b
 QUINTIC = (3.4445, -4.7750, 2.0315)
 
 
+# limits of a call, as the library has them
+_MOST_MATRICES, _MOST_ROWS, _MOST_COLUMNS, _MOST_ELEMENTS = 65535, 1 << 16, 1 << 22, 1 << 36
+
+
 def _numbers(coefficients):
     """One triple or several as tuples of Python's floats, which calls can be told apart by:
     a tensor could be another number the next time."""
@@ -32,6 +36,8 @@ def _numbers(coefficients):
         if torch.is_tensor(coefficients) and (coefficients.requires_grad or _b.dual(coefficients)):
             raise ValueError("coefficients are not differentiated: pass them detached")
         coefficients = coefficients.tolist()
+    if not isinstance(coefficients, (tuple, list)) or not coefficients:
+        raise ValueError("coefficients are (a, b, c), or one such triple for each step")
     if not isinstance(coefficients[0], (tuple, list)) and getattr(coefficients[0], "ndim", 0) == 0:
         coefficients = (coefficients,)
     for x in (x for abc in coefficients for x in abc):
@@ -47,7 +53,7 @@ def _coefficients(steps, polynomials):
     if len(polynomials) != steps:
         raise ValueError(f"{len(polynomials)} polynomials for {steps} steps")
     flat = [float(x) for abc in polynomials for x in abc]
-    if len(flat) != 3 * steps or not all(math.isfinite(x) for x in flat):
+    if any(len(abc) != 3 for abc in polynomials) or not all(math.isfinite(x) for x in flat):
         raise ValueError("a polynomial is three finite numbers a, b, c of a x + b x^3 + c x^5")
     return (ctypes.c_float * len(flat))(*flat)
 
@@ -58,15 +64,19 @@ def _problem(shape, dtype, steps, polynomials, eps, keep):
     (forward, backward)."""
     coefficients = _coefficients(steps, polynomials)
     sizes = math.prod(shape[:-2]), shape[-2], shape[-1]
-    if max(sizes) >= 1 << 31:  # would wrap in the description
-        raise _b.FbobError(2, "orthogonalize")
+    L, short, long = sizes[0], min(sizes[1:]), max(sizes[1:])
+    if L > _MOST_MATRICES or short > _MOST_ROWS or long > _MOST_COLUMNS or L * short * long > _MOST_ELEMENTS:
+        raise _b.FbobError(2, f"orthogonalize: {L} matrices of {sizes[1]} x {sizes[2]}; at most "
+                              f"{_MOST_MATRICES} of {_MOST_ROWS} by {_MOST_COLUMNS} (either way round), "
+                              f"{_MOST_ELEMENTS} elements in all")
     o = _b.Orth(*sizes, _b.DTYPES[dtype], steps, int(keep), eps,
                 ctypes.addressof(coefficients))
     o.held = coefficients  # lives as long as its address is used
     ref = ctypes.byref(o)
     sizes = tuple(_b.lib().fbob_orth_workspace_size(op, ref) for op in (_b.OP_FORWARD, _b.OP_BACKWARD))
     if 0 in sizes:
-        raise _b.FbobError(2, "orthogonalize")
+        raise _b.FbobError(2, "orthogonalize: more tiles than a call counts, a polynomial under which singular "
+                              "values of [0, 1] reach 64 or small ones fall below 1/256, or eps beyond fp32")
     return ref, sizes
 
 
@@ -125,7 +135,8 @@ def orthogonalize(g: torch.Tensor, steps: int = 5, coefficients=QUINTIC,
     [..., m, n]: X = g / (|g| + eps) with |g| its Frobenius norm, then ``steps``
     times X <- a X + b (X X^T) X + c (X X^T)^2 X.
 
-    g: bf16 or fp32 CUDA tensor, not empty (copied first if not contiguous).
+    g: bf16 or fp32 CUDA tensor, not empty (copied first if not contiguous): up to 65535
+    matrices, the shorter side up to 65536, the longer up to 2^22, 2^36 elements in all.
     coefficients: (a, b, c), or one such triple for each step, numbers, which are not
     differentiated (a tensor on the GPU is waited for); singular values
     that start in [0, 1] must stay below 64 under them, and small ones must not fall

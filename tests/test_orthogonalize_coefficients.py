@@ -64,3 +64,39 @@ def test_a_polynomial_changed_in_place():
             assert torch.equal(fbob.orthogonalize(G, 3, whole), want)
         with pytest.raises(ValueError):
             fbob.orthogonalize(G, 3, whole.requires_grad_())
+
+
+@pytest.mark.parametrize("bad", [(), [], ((),), ((), ()), [[]], None, 1.5, torch.zeros(0), torch.zeros(0, 3), np.zeros((0, 3)),
+                                 (1.0, 2.0), (1.0, 2.0, 3.0, 4.0), ((1.0, 2.0), (1.0, 2.0, 3.0, 4.0)),
+                                 torch.ones(4), torch.ones(2, 4), (1.0, float("nan"), 0.0), "abc", torch.ones(1, 1, 3)],
+                         ids=repr)
+def test_what_is_no_polynomial(bad):
+    """Refused by name, before any tensor is looked at."""
+    module = importlib.import_module("exact_second_order_two_gb300.orthogonalize")
+    with pytest.raises((ValueError, TypeError)):
+        module._coefficients(2, numbers(bad))
+
+
+def test_a_call_with_no_polynomial(monkeypatch):
+    """The public call says what it wants (its tensor stands for one on a GPU)."""
+    class Gpu(torch.Tensor):
+        is_cuda = True
+    g = torch.zeros(3, 4).as_subclass(Gpu)
+    for bad in ((), [], torch.zeros(0)):
+        with pytest.raises(ValueError):
+            fbob.orthogonalize(g, 2, bad)
+
+
+@pytest.mark.parametrize("shape", [(65536, 2, 3), (65537, 65537), (4, (1 << 22) + 1), ((1 << 22) + 1, 4),
+                                   (60000, 2048, 2048)], ids=str)
+def test_limits_are_named(shape):
+    problem = importlib.import_module("exact_second_order_two_gb300.orthogonalize")._problem
+    with pytest.raises(fbob.FbobError, match="at most 65535 of 65536 by 4194304"):
+        problem(shape, torch.bfloat16, 5, (ONE,), 1e-7, False)
+
+
+def test_polynomials_that_are_refused_are_named():
+    problem = importlib.import_module("exact_second_order_two_gb300.orthogonalize")._problem
+    for poly in ((4.0, 0.0, 0.0), (0.1, 0.5, 0.0)):
+        with pytest.raises(fbob.FbobError, match="polynomial"):
+            problem((4, 5), torch.bfloat16, 5, (poly,), 1e-7, False)
