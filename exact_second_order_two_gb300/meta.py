@@ -166,16 +166,21 @@ def mse(a: torch.Tensor, b: torch.Tensor) -> torch.Tensor:
     return ((a - b) ** 2).mean()
 
 
-def orthogonal_updates(grads, orthogonal=orthogonalize):
-    """Each matrix [m, n] among ``grads`` orthogonalised, times
-    sqrt(max(1, m / n)); vectors and numbers as they are.  Matrices of one shape
-    and dtype go through one call."""
+def orthogonal_updates(grads, orthogonal=orthogonalize, inputs_first: bool = False):
+    """Each matrix among ``grads`` orthogonalised, times sqrt(max(1, outputs /
+    inputs)); vectors and numbers as they are.  Matrices of one shape and dtype go
+    through one call.
+
+    Weights are [outputs, inputs], or, with inputs_first, [inputs, outputs] as
+    ``x @ w`` takes them.  An update of singular values 1 turns inputs of root mean square
+    1 into outputs of sqrt(inputs / outputs) at most, so that a layer with
+    more outputs than inputs moves by as much as a square one only with that factor."""
     out, stacks = list(grads), {}
     for i, g in enumerate(grads):
         if g.dim() == 2:
             stacks.setdefault((*g.shape, g.dtype, g.device), []).append(i)
     for (m, n, *_), at in stacks.items():
-        scale = max(1.0, m / n) ** 0.5
+        scale = max(1.0, n / m if inputs_first else m / n) ** 0.5
         for i, u in zip(at, orthogonal(torch.stack([grads[i] for i in at])).unbind(0)):
             out[i] = scale * u
     return out
@@ -205,7 +210,7 @@ def maml_step(layer, support, query, inner_lr: float = 0.1, causal: bool = True,
     loss = mse(layer.forward(params, xs, *how), ys)
     grads = torch.autograd.grad(loss, params, create_graph=True)
     if inner == "orthogonal":
-        grads = orthogonal_updates(grads, orthogonal or orthogonalize)
+        grads = orthogonal_updates(grads, orthogonal or orthogonalize, inputs_first=True)
     adapted = [w - inner_lr * g for w, g in zip(params, grads)]
     outer = mse(layer.forward(adapted, xq, *how), yq)
     meta_grads = torch.autograd.grad(outer, params)
