@@ -689,7 +689,9 @@ template <typename K>
 cudaError_t launch(K kernel, int blocks, int split, size_t floats, const Args& a, LaunchLog& log,
                    int parts = 1) {
   const size_t bytes = floats * sizeof(float);
-  cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)bytes);
+  // (the limit belongs to the kernel, which another thread may be about to launch: it is always
+  // set to the most there is)
+  cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)kMaxShared);
   if (e != cudaSuccess) return e;
   kernel<<<dim3(blocks * a.heads, parts), split * kThreads, bytes, log.stream>>>(a);
   e = cudaGetLastError();

@@ -49,6 +49,8 @@ struct Shared {
   short e[kMaxSteps + 1];
 };
 constexpr uint32_t kMisc = 256;
+constexpr int kMostTiles = 14;  // in shared memory
+static_assert(kMostTiles * kTileBytes + kMisc <= 232448, "small orthogonalisation: shared memory");
 static_assert(sizeof(Shared) <= kMisc, "small orthogonalisation: shared memory");
 
 __device__ __forceinline__ float block_sum(float v, float* red) {
@@ -452,7 +454,10 @@ cudaError_t launch(const SmallArgs& g, bool backward, LaunchLog& log) {
                             : g.x_terms * tiles + terms * kSquare;
   const int smem = held * (int)kTileBytes + (int)kMisc;
   auto kernel = backward ? small_backward<T> : small_forward<T>;
-  cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
+  // (the limit belongs to the kernel, which another thread may be about to launch: it is always
+  // set to the most that a call takes)
+  cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                       kMostTiles * (int)kTileBytes + (int)kMisc);
   if (e != cudaSuccess) return e;
   kernel<<<g.L, kThreads, smem, log.stream>>>(g);
   e = cudaGetLastError();
@@ -461,10 +466,10 @@ cudaError_t launch(const SmallArgs& g, bool backward, LaunchLog& log) {
 }
 cudaError_t launch_small(const SmallArgs& args, bool bf16, bool backward, LaunchLog& log) {
   SmallArgs g = args;
-  // all of X, or, where 14 tiles of shared memory would not hold that, two tiles at a time: 4 of
-  // H, and S, in two terms each
+  // all of X, or, where shared memory would not hold that, two tiles at a time: 4 of H, and S, in
+  // two terms each
   const int tiles = (g.q + 63) / 64;
-  g.x_tiles = g.h_terms * (tiles + kSquare) + tiles <= 14 || !bf16 ? tiles : kSquare;
+  g.x_tiles = g.h_terms * (tiles + kSquare) + tiles <= kMostTiles || !bf16 ? tiles : kSquare;
   return bf16 ? launch<__nv_bfloat16>(g, backward, log) : launch<float>(g, backward, log);
 }
 

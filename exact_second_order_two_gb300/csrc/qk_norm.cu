@@ -830,9 +830,13 @@ cudaError_t launch(NormArgs& a, LaunchLog& log) {
   size_t smem = sizeof(unsigned long long) * ((a.half + 1) & ~1) + sizeof(float) * a.d * (OP == kSecond ? 2 : 1);
   const unsigned grid = (unsigned)(a.side[0].blocks + a.side[1].blocks);
   if constexpr (P > 1) {
-    smem += kDeep * kRingRow<OP, TI, TO, P>;
+    // (the limit belongs to the kernel, which another thread may be about to launch: it is always
+    // set to the most that a call takes, kMaxDim features, all turned)
+    constexpr size_t ring = kDeep * kRingRow<OP, TI, TO, P>;
+    constexpr size_t most = ring + sizeof(unsigned long long) * (kMaxDim / 2) + sizeof(float) * kMaxDim * 2;
+    smem += ring;
     const cudaError_t e = cudaFuncSetAttribute(norm_rows<OP, TI, TO, P, INTERLEAVED>,
-                                               cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
+                                               cudaFuncAttributeMaxDynamicSharedMemorySize, (int)most);
     if (e != cudaSuccess) return e;
     norm_rows<OP, TI, TO, P, INTERLEAVED><<<grid, kThreads, smem, log.stream>>>(a);
   } else {

@@ -421,16 +421,19 @@ size_t col_smem(int d) {
   return sizeof(float) * (4 * kWarps * d + 3 * kTile * (d + 1) + 4 * kTile);
 }
 
+constexpr int kMaxDim = 128;
+// The limit belongs to the kernel, which another thread may be about to launch with another d:
+// it is always set to what the widest heads take.
 template <typename K>
-cudaError_t set_smem(K kernel, size_t bytes) {
+cudaError_t set_smem(K kernel, size_t most) {
   return cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                              (int)bytes);
+                              (int)most);
 }
 
 template <typename T, int MODE>
 cudaError_t launch_row(const Problem& p, const RowArgs& a, LaunchLog& log) {
   const size_t smem = row_smem(p.d);
-  cudaError_t e = set_smem(row_kernel<T, MODE>, smem);
+  cudaError_t e = set_smem(row_kernel<T, MODE>, row_smem(kMaxDim));
   if (e != cudaSuccess) return e;
   dim3 grid((p.N + kWarps - 1) / kWarps, p.BH());
   row_kernel<T, MODE><<<grid, kWarps * 32, smem, log.stream>>>(a);
@@ -442,7 +445,7 @@ cudaError_t launch_row(const Problem& p, const RowArgs& a, LaunchLog& log) {
 template <typename T, int MODE>
 cudaError_t launch_col(const Problem& p, const ColArgs& a, LaunchLog& log) {
   const size_t smem = col_smem(p.d);
-  cudaError_t e = set_smem(col_kernel<T, MODE>, smem);
+  cudaError_t e = set_smem(col_kernel<T, MODE>, col_smem(kMaxDim));
   if (e != cudaSuccess) return e;
   dim3 grid((p.N + kWarps - 1) / kWarps, p.BH());
   col_kernel<T, MODE><<<grid, kWarps * 32, smem, log.stream>>>(a);
