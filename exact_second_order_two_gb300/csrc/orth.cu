@@ -182,6 +182,11 @@ __global__ void __launch_bounds__(kSumThreads)
   if (threadIdx.x == 0) partial[(size_t)blockIdx.y * gridDim.x + blockIdx.x] = r;
 }
 
+__global__ void clear_status(int* status) {
+  let_next_start();
+  *status = 0;
+}
+
 // Sum of `parts` values, the same in every thread of the block.
 __device__ __forceinline__ float parts_sum(const float* p, int parts, float* sm) {
   float s = 0.f;
@@ -830,7 +835,7 @@ void backward_scales(const Plan& p, int* target, int* se) {
   target[p.steps] = (int)floor(after);
 }
 
-// A call for small matrices: one launch.
+// A call for small matrices: one launch, and one that clears the status word.
 cudaError_t small(const Plan& p, const void* G, const void* dY, void* out, Forward& f, int* status,
                   LaunchLog& log) {
   SmallArgs g = {};
@@ -876,7 +881,12 @@ cudaError_t small(const Plan& p, const void* G, const void* dY, void* out, Forwa
                              from[k]->cols, from[k]->ld, kTile))
         return cudaErrorUnknown;
     }
-  return launch_small(g, p.bf16, dY != nullptr, log);
+  // (in the stream's order: no block of the kernel clears it behind another's report.  A memset
+  // would have to be over before the kernel starts: 2 us of 22.)
+  clear_status<<<1, 1, 0, log.stream>>>(status);
+  const cudaError_t e = cudaGetLastError();
+  log.mark();
+  return e == cudaSuccess ? launch_small(g, p.bf16, dY != nullptr, log) : e;
 }
 
 cudaError_t forward(const Plan& p, const void* G, void* Y, Forward& w, LaunchLog& log) {

@@ -176,6 +176,7 @@ __device__ __forceinline__ void begin_block(Shared* sh, uint32_t cols, const Sma
     tmem_relinquish();
   }
   tc_fence_before();
+  after_previous();
   __syncthreads();
   tc_fence_after();
 }
@@ -233,6 +234,7 @@ __global__ void __launch_bounds__(kThreads, 1) small_forward(const __grid_consta
   constexpr int TERMS = sizeof(T) == 2 ? 1 : 2;
   extern __shared__ __align__(1024) uint8_t smem[];
   if (smem_u32(smem) & 1023u) {
+    after_previous();
     if (threadIdx.x == 0) report_status(g.status, FBOB_ERR_CUDA);
     return;
   }
@@ -240,7 +242,6 @@ __global__ void __launch_bounds__(kThreads, 1) small_forward(const __grid_consta
   const Held X{smem, tiles}, A{smem + g.x_terms * tiles * kTileBytes, kSquare};  // B in A's place
   Shared* sh = reinterpret_cast<Shared*>(A.at + TERMS * kSquare * kTileBytes);
   const uint32_t cols = TERMS == 2 ? 512 : tiles > 2 ? 256 : 128;
-  if (l == 0 && threadIdx.x == 0) *g.status = 0;
   begin_block(sh, cols, g);
   const uint32_t acc = sh->tmem;
   const int row = 32 * ((threadIdx.x >> 5) & 3) + (threadIdx.x & 31), unit = threadIdx.x >> 7;
@@ -316,6 +317,7 @@ __global__ void __launch_bounds__(kThreads, 1) small_backward(const __grid_const
   constexpr int TERMS = sizeof(T) == 2 ? 1 : 2;
   extern __shared__ __align__(1024) uint8_t smem[];
   if (smem_u32(smem) & 1023u) {
+    after_previous();
     if (threadIdx.x == 0) report_status(g.status, FBOB_ERR_CUDA);
     return;
   }
@@ -325,9 +327,8 @@ __global__ void __launch_bounds__(kThreads, 1) small_backward(const __grid_const
   const Held X{S.at + g.h_terms * kSquare * kTileBytes, g.x_tiles}, A{X.at, kSquare};
   Shared* sh = reinterpret_cast<Shared*>(X.at + TERMS * room * kTileBytes);
   const uint32_t cols = TERMS == 2 ? 512 : tiles > 2 ? 256 : 128;
-  if (l == 0 && threadIdx.x == 0) *g.status = 0;
-  if (threadIdx.x < g.steps.n) sh->e[threadIdx.x] = g.info[l].e[threadIdx.x];
   begin_block(sh, cols, g);
+  if (threadIdx.x < g.steps.n) sh->e[threadIdx.x] = g.info[l].e[threadIdx.x];
   const uint32_t acc = sh->tmem;
   const int row = 32 * ((threadIdx.x >> 5) & 3) + (threadIdx.x & 31), unit = threadIdx.x >> 7;
   const int deep = (g.p + 63) / 64;
@@ -459,10 +460,7 @@ cudaError_t launch(const SmallArgs& g, bool backward, LaunchLog& log) {
   cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
                                        kMostTiles * (int)kTileBytes + (int)kMisc);
   if (e != cudaSuccess) return e;
-  kernel<<<g.L, kThreads, smem, log.stream>>>(g);
-  e = cudaGetLastError();
-  log.mark();
-  return e;
+  return launch_next(kernel, dim3((unsigned)g.L), kThreads, smem, 1, log, g);
 }
 cudaError_t launch_small(const SmallArgs& args, bool bf16, bool backward, LaunchLog& log) {
   SmallArgs g = args;
