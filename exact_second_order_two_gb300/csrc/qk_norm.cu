@@ -16,9 +16,12 @@
 // cosine serve them all; queries and keys are one launch.  The sums over rows
 // are carried in registers by blocks that stay (a few per SM), added up in the block
 // through shared memory, and over the blocks by a second launch: every sum in a
-// fixed order.  norm_rows takes chunks of 16 or 8 features, norm_kernel what is left (odd
-// widths, odd addresses), a feature at a time: 16 heads x 27679 x 37, bf16, 85, 167 and 224 us,
-// a third of the other's rate.
+// fixed order.  norm_rows takes chunks of 16 or 8 features, where they tile the turned and
+// the other part; norm_kernel what is left, a feature at a time: odd widths, odd addresses, and
+// aligned heads of which as many are turned as no chunk tiles (20 of 40, 12 of 64).  8 + 8
+// heads x 26214 x 40, bf16, forward, backward and second derivative: 44, 81 and 116 us with 20
+// turned, 30, 46 and 75 in chunks with all turned; x 16384 x 64 with 12 turned 36, 56 and 85,
+// with all 21, 31 and 46.
 #include <cuda_bf16.h>
 #include <cuda_runtime.h>
 #include <stdint.h>
@@ -366,7 +369,7 @@ __global__ void __launch_bounds__(kThreads) norm_kernel(const __grid_constant__ 
 
 
 // ---------------------------------------------------------------------------
-// Rows in chunks of 16 or 8 features, aligned: nearly all heads.  Arithmetic is in pairs of
+// Rows in chunks of 16 or 8 features, aligned.  Arithmetic is in pairs of
 // features; rows come through shared memory, a row ahead of the one that is worked on, and
 // weights are read from there where a row needs them.  32 heads x 8192 x 128, bf16, with the
 // sums over rows: 33 us forward, 48 backward and 73 for the second derivative (4.0 to 4.6
