@@ -853,9 +853,13 @@ cudaError_t small(const Plan& p, const void* G, const void* dY, void* out, Forwa
   g.x_terms = g.h_terms = 1;
   for (int i = 0; i < p.steps; ++i) {
     const int te = p.be[i] - p.xe[i], out_exp = i + 1 < p.steps ? p.xe[i + 1] : 0;
-    if (p.xt[i] > g.x_terms) g.x_terms = p.xt[i];
     if (p.ht[i] == 2 || p.st[i] == 2) g.h_terms = 2;
-    g.xt[i] = p.xt[i];
+    double left = 1;  // what small singular values still grow by
+    for (int j = i; j < p.steps; ++j) left *= fabs(p.a[j]) > 1 ? fabs(p.a[j]) : 1;
+    const bool two = !p.bf16 || left <= 64;
+    g.two_b |= (unsigned)two << i;
+    g.xt[i] = !p.bf16 || (two && i > 0) ? 2 : p.xt[i];  // (a bf16 X_0 is one term)
+    if (g.xt[i] == 2) g.x_terms = 2;
     g.two_s |= (unsigned)(p.st[i] == 2) << i;
     g.two_h |= (unsigned)(p.ht[i] == 2) << i;
     g.two_hp |= (unsigned)(p.hp[i] == 2) << i;

@@ -114,8 +114,9 @@ struct SmallArgs {
   int x_terms, h_terms;                      // most of X, and of H, S and T, in a step
   int x_tiles;                               // backward: tiles of X (64 columns) held at a time
   int xt[kMaxSteps], xe[kMaxSteps];
-  // a bit for each step: two terms of S and T; of H where it is added; of H in products
-  unsigned two_s, two_h, two_hp;
+  // a bit for each step: two terms of S and T; of H where it is added; of H in products; of B,
+  // and of X in products
+  unsigned two_s, two_h, two_hp, two_b;
   float to_a[kMaxSteps], to_b[kMaxSteps], a_to_b[kMaxSteps], to_x[kMaxSteps], x_to_x[kMaxSteps];
   float to_s[kMaxSteps], to_t[kMaxSteps], s_to_t[kMaxSteps], to_h[kMaxSteps], h_to_h[kMaxSteps];
   int target[kMaxSteps + 1];

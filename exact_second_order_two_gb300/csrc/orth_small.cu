@@ -9,6 +9,12 @@
 // GPU (orth_chain.cu) each takes 8.  16 x 64 x 64, bf16: 93 us there, 25 here; 4 x 128 x 128,
 // fp32, with its gradient: 168 us, of 357.  Symmetric results are computed whole, which saves the mirroring.
 //
+// bf16: X and B have two terms in products, too, in the steps behind which small singular values
+// grow by 64 at most (before, X is small, and what B adds smaller).  In a large matrix each
+// result is a sum of many roundings, in a small one of few, and MMAs cost little: 16 x 24 to
+// 64 x 96, the result 2.1e-3 to 2.3e-3 off with one term and the gradient 2.7e-3 to 3.9e-3,
+// 1.8e-3 and 2.3e-3 to 2.6e-3 so; 16 x 64 x 64 takes 26.6 us, 22.6 with one.
+//
 // With a backward to follow, X, A and B of every step leave for the workspace by TMA.  The
 // backward holds H, S (then T) and, in turn in one place, X (in two parts where second terms of
 // H and S leave no room for more), A, B and X again.
@@ -240,7 +246,7 @@ __global__ void __launch_bounds__(kThreads, 1) small_forward(const __grid_consta
   }
   const int tiles = (g.q + 63) / 64, l = blockIdx.x;
   const Held X{smem, tiles}, A{smem + g.x_terms * tiles * kTileBytes, kSquare};  // B in A's place
-  Shared* sh = reinterpret_cast<Shared*>(A.at + TERMS * kSquare * kTileBytes);
+  Shared* sh = reinterpret_cast<Shared*>(A.at + 2 * kSquare * kTileBytes);
   const uint32_t cols = TERMS == 2 ? 512 : tiles > 2 ? 256 : 128;
   begin_block(sh, cols, g);
   const uint32_t acc = sh->tmem;
@@ -257,11 +263,11 @@ __global__ void __launch_bounds__(kThreads, 1) small_forward(const __grid_consta
   int n = 0;                         // products so far
   bool ok = true;
   // one product: what `store` sends off is read before the tiles can be written again
-  auto product = [&](const Held& P, const Held& Q, bool nn, int depth, auto store) {
+  auto product = [&](const Held& P, int pt, const Held& Q, int qt, bool nn, int depth, auto store) {
     hand_over();
     if (threadIdx.x == 0 && !sh->ab.flag) {
       store();
-      multiply_terms<TERMS>(acc, P, 1, Q, 1, nn, depth, 0);
+      multiply_terms<TERMS>(acc, P, pt, Q, qt, nn, depth, 0);
       bulk_wait_read_all();
       mma_commit(&sh->mma);
     }
@@ -276,19 +282,21 @@ __global__ void __launch_bounds__(kThreads, 1) small_forward(const __grid_consta
     const int e1 = last ? 0 : room_below(g.steps.bound[i + 1], bound);
     if (threadIdx.x == 32) g.info[l].e[i + 1] = (short)e1;
     f2 v[16];
-    product(X, X, false, tiles, [&] {
-      if (g.keep) store_held(&g.x_map[0], g.xt[i] == 2 ? &g.x_map[1] : nullptr, X, i * g.L + l, g.q, g.p);
+    // terms of B, and of X in products
+    const int bt = TERMS == 2 ? 2 : 1 + (g.two_b >> i & 1), xp = min(bt, g.xt[i]);
+    product(X, xp, X, xp, false, tiles, [&] {
+      if (g.keep) store_held(&g.x_map[0], TERMS == 2 ? &g.x_map[1] : nullptr, X, i * g.L + l, g.q, g.p);
     });
     read_acc(acc, wide_sums, unit, f * f * g.to_a[i], v);
     put(v, A, TERMS, row, unit);
-    product(A, A, false, deep, [&] {
+    product(A, 1, A, 1, false, deep, [&] {
       if (g.keep) store_held(&g.a_map[0], TERMS == 2 ? &g.a_map[1] : nullptr, A, i * g.L + l, g.p, g.p);
     });
     read_acc(acc, deep_sums, unit, times_pow2(g.to_b[i], -2 * e), v);
     add_slot(v, A.tile(0, unit >> 1), row, unit & 1, g.a_to_b[i]);
     if (TERMS == 2) add_slot(v, A.tile(1, unit >> 1), row, unit & 1, g.a_to_b[i]);
-    put(v, A, TERMS, row, unit);
-    product(A, X, true, deep, [&] {
+    put(v, A, bt, row, unit);
+    product(A, bt, X, xp, true, deep, [&] {
       if (g.keep) store_held(&g.b_map[0], TERMS == 2 ? &g.b_map[1] : nullptr, A, i * g.L + l, g.p, g.p);
     });
     const float to_x = times_pow2(f * g.to_x[i], e1 - 3 * e), x_to_x = times_pow2(f * g.x_to_x[i], e1 - e);
@@ -452,7 +460,7 @@ template <typename T>
 cudaError_t launch(const SmallArgs& g, bool backward, LaunchLog& log) {
   const int terms = sizeof(T) == 2 ? 1 : 2, tiles = (g.q + 63) / 64;
   const int held = backward ? g.h_terms * (tiles + kSquare) + terms * (g.x_tiles > kSquare ? g.x_tiles : kSquare)
-                            : g.x_terms * tiles + terms * kSquare;
+                            : g.x_terms * tiles + 2 * kSquare;
   const int smem = held * (int)kTileBytes + (int)kMisc;
   auto kernel = backward ? small_backward<T> : small_forward<T>;
   // (the limit belongs to the kernel, which another thread may be about to launch: it is always

@@ -146,10 +146,10 @@ def orthogonalize(g: torch.Tensor, steps: int = 5, coefficients=QUINTIC,
 
     Returns a contiguous tensor of g's shape and dtype.  Differentiable once in g, in
     reverse mode.  bf16: products of fp16 operands with fp32 sums.  With five steps the
-    result is 1.8e-3 to 2.0e-3 of its norm off and its own rounding 1.7e-3 of that; the
-    gradient 1.7e-3 off for white noise from above, 2.4e-3 to 4.7e-3 for what lies among g's
-    strong directions.  More steps enlarge what the iterates were rounded by: with eight,
-    2.7e-3 to 3.3e-3 and 0.7e-2 to 2.5e-2.  fp32: operands of 22 bits, of the largest
+    result is 1.7e-3 to 1.9e-3 of its norm off and its own rounding 1.7e-3 of that; the
+    gradient 1.8e-3 to 2.6e-3 off for white noise from above, 2.4e-3 to 4.0e-3 for what lies
+    among g's strong directions.  More steps enlarge what the iterates were rounded by: with
+    eight, 2.7e-3 to 2.9e-3 and 0.7e-2 to 1.4e-2.  fp32: operands of 22 bits, of the largest
     entries (of others down to 2^-36 of the bound on singular values).
     """
     if not g.is_cuda:

@@ -4,7 +4,7 @@ import pytest
 import torch
 
 import exact_second_order_two_gb300 as fbob
-from test_orthogonalize import ONE, exact
+from test_orthogonalize import ONE, exact, gradient
 
 pytestmark = [pytest.mark.gpu, pytest.mark.skipif(not torch.cuda.is_available(), reason="needs a GPU")]
 
@@ -63,6 +63,24 @@ def test_every_number_of_steps(shape, steps):
         # 96^(1/2) 2^-12.8 = 0.35 u for 16 steps, enlarged by 4 at most where they have one
         # term, and the result's rounding, an rms of 0.43 u
         assert (out[0] - out[1]).norm() <= 2 * 2.0 ** -8 * out[1].norm()
+
+
+@pytest.mark.parametrize("shape", [(16, 16, 24), (16, 17, 25), (16, 24, 16), (16, 24, 36), (16, 64, 96), (8, 128, 200)],
+                         ids=str)
+@pytest.mark.parametrize("seed", [0, 1, 2])
+def test_small_matrices(shape, seed):
+    """Value and gradient of small stacks for white noise from above, in units of u = 2^-8 (an rms:
+    the results' rounding is 0.43).  What has one term adds 2^-12.8 = 0.036 u each: A in five
+    steps, enlarged by the slope of 3.9 at most, 5^(1/2) 0.036 3.9 = 0.31, which with the
+    rounding is 0.53 for the value, held to 0.55; the first terms of X, A and B that the backward
+    reads, enlarged by 3.4, 15^(1/2) 0.036 3.4 = 0.47: 0.71 for the gradient, held to 0.75."""
+    G, dY = gradient(shape, torch.bfloat16, seed=seed)
+    G.requires_grad_()
+    Y = fbob.orthogonalize(G)
+    (dG,) = torch.autograd.grad(Y, G, dY)
+    for got, want, most in zip((Y.detach(), dG), exact(G, dY, [ONE] * 5), (0.55, 0.75)):
+        err = ((got.double() - want).norm() / want.norm()).item() * 2 ** 8
+        assert err <= most, err
 
 
 def test_against_fp32():
