@@ -156,9 +156,9 @@ __device__ __forceinline__ void let_next_start() {
 __device__ __forceinline__ void after_previous() { asm volatile("griddepcontrol.wait;" ::: "memory"); }
 
 // A sum of squares, m 2^e.  Squares are added as they are (e = 0) where their sum shows
-// that none was lost: the others, of less than 2^-60 or infinite, are taken again of elements
-// times a power of two that keeps any fp32 number's square, and a sum of 2^36 of them, inside
-// fp32.
+// that none was lost, and leaves room for 1024 such sums: the others, of less than 2^-60 or more
+// than 2^100, are taken again of elements times a power of two that keeps any fp32 number's
+// square, and a sum of 2^36 of them, inside fp32.
 struct Squares {
   float m;
   int e;
@@ -170,7 +170,7 @@ __device__ __forceinline__ Squares squares_of(F sum) {
   Squares r = {sum(1.f), 0};
   if (r.m < 0x1p-60f) {
     r = Squares{sum(kScaleSmall), -160};
-  } else if (r.m > 3.4e38f) {
+  } else if (r.m > 0x1p100f) {
     r = Squares{sum(kScaleLarge), 192};
   }
   return r;

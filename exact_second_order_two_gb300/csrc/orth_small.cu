@@ -4,10 +4,10 @@
 // tiles that are left operands, right operands by rows (P Q^T) and by columns (P Q) as
 // they lie; the accumulator is in TMEM.  A product is at most 48 MMAs of 64 clocks, so what
 // counts is the way between them: MMAs done, accumulator read, values rounded and
-// written, MMAs issued: three times a step, 1.2 us each for bf16, 2.3 for fp32 (a warp to 32
-// rows and 32 columns; with half as many warps 3).  As products in memory over the whole
-// GPU (orth_chain.cu) each takes 8.  16 x 64 x 64, bf16: 93 us there, 25 here; 4 x 128 x 128,
-// fp32, with its gradient: 168 us, of 357.  Symmetric results are computed whole, which saves the mirroring.
+// written, MMAs issued: three times a step, 1.2 us each for bf16 in one term, 2.3 for fp32 (a
+// warp to 32 rows and 32 columns; with half as many warps 3).  As products in memory over the
+// whole GPU (orth_chain.cu) each takes 8.  16 x 64 x 64, bf16: 93 us there, 25 here in one
+// term; 4 x 128 x 128, fp32, with its gradient: 168 us, of 357.  Symmetric results are computed whole, which saves the mirroring.
 //
 // bf16: X and B have two terms in products, too, in the steps behind which small singular values
 // grow by 64 at most (before, X is small, and what B adds smaller).  In a large matrix each

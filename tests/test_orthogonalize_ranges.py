@@ -134,3 +134,15 @@ def test_norms_past_fp32_of_entries_within():
         Y = fbob.orthogonalize(G)
         X, own = exact(G.float() * 2.0 ** -100, None, [ONE] * 5, eps=0.0)[0], model(G * 2.0 ** -100, None, [ONE] * 5)[0]
         check(Y, X, own, dtype)
+
+
+@pytest.mark.parametrize("shape", [(60, 80), (300, 400), (1500, 1600)], ids=str)
+@pytest.mark.parametrize("dtype", ["bf16", "fp32"])
+def test_every_power_of_two_about_the_ends_of_squares(shape, dtype):
+    """Norms whose squares, or sums of them in parts, or parts of them, are past fp32's range:
+    every size of G and of dY from 2^40 to 2^70, and from 2^-40 to 2^-70."""
+    G, dY = gradient(shape, DT[dtype], std=1.0)
+    Y, dG = both(G, dY, [ONE] * 5, eps=0.0)
+    for power in (*range(40, 71), *range(-70, -39)):
+        y, dg = both(G * 2.0 ** power, dY * 2.0 ** power, [ONE] * 5, eps=0.0)
+        assert torch.equal(y, Y) and torch.equal(dg, dG), power
