@@ -46,3 +46,34 @@ def test_status(shape, dtype):
                     fbob.set_wait_limit(old)
             if limit:  # the backward reads what a whole forward kept
                 assert forward()[0] == 0 and fbob.status(kept) == 0
+
+
+@pytest.mark.parametrize("shape", [(16, 64, 64), (3, 100, 250), (2, 250, 100)], ids=str)
+@pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float32], ids=["bf16", "fp32"])
+def test_captured_and_replayed(shape, dtype):
+    """Two graphs of a call with its gradient, replayed in turn with inputs that change, beside
+    calls of the same size outside: every result is that of a call by itself."""
+    def step(x, d):
+        y = fbob.orthogonalize(x)
+        return y, torch.autograd.grad(y, x, d)[0]
+
+    some = [gradient(shape, dtype, seed=i) for i in range(4)]
+    want = [[t.detach().clone() for t in step(G.clone().requires_grad_(), dY)] for G, dY in some]
+    leaves = [(torch.zeros_like(G).requires_grad_(), torch.zeros_like(dY)) for G, dY in some[:2]]
+    graphs, outs = [], []
+    for leaf in leaves:
+        graphs.append(torch.cuda.CUDAGraph())
+        with torch.cuda.graph(graphs[-1]):
+            outs.append(step(*leaf))
+    for first in (0, 2, 1):
+        at = [first, (first + 1) % 4]
+        with torch.no_grad():
+            for (x, d), i in zip(leaves, at):
+                x.copy_(some[i][0])
+                d.copy_(some[i][1])
+        for g in graphs:
+            g.replay()
+        alone = step(some[3][0].clone().requires_grad_(), some[3][1])
+        assert all(torch.equal(a, b) for a, b in zip(alone, want[3]))
+        for out, i in zip(outs, at):
+            assert all(torch.equal(a, b) for a, b in zip(out, want[i]))
