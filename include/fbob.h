@@ -368,9 +368,9 @@ int fbob_qk_norm_bob(const fbob_qk_norm_t* s, const fbob_norm_side_t* q,
  * exponents with the large ones); an infinite or NaN
  * entry spoils its matrix.
  * g, y, dy and dg are dense [L,m,n] of `dtype`, aligned to their elements;
- * workspaces to 256 bytes.  Operands are fp16, one term for bf16 tensors (X in
- * two where it is added and later steps would enlarge its rounding), two for
- * fp32; sums are fp32, in a fixed order: equal inputs give equal bits.
+ * workspaces to 256 bytes.  Operands are fp16, one term for bf16 tensors (two
+ * for what is added, or goes on into later steps, where those would enlarge its
+ * rounding, and for X and B of small matrices), two for fp32; sums are fp32, in a fixed order: equal inputs give equal bits.
  * steps <= 16, min(m, n) <= 65536, max(m, n) <= 2^22, L <= 65535,
  * L*m*n <= 2^36. */
 typedef struct {
