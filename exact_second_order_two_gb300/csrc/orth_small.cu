@@ -2,7 +2,7 @@
 //
 // Up to 128 rows (p) and 128 columns (256 for bf16), X, A and B stay in shared memory, as
 // tiles that are left operands, right operands by rows (P Q^T) and by columns (P Q) as
-// they lie; the accumulator is in TMEM.  A product is at most 48 MMAs of 64 clocks, so what
+// they lie; the accumulator is in TMEM.  A product is at most 64 MMAs of 64 clocks, so what
 // counts is the way between them: MMAs done, accumulator read, values rounded and
 // written, MMAs issued: three times a step, 1.2 us each for bf16 in one term, 2.3 for fp32 (a
 // warp to 32 rows and 32 columns; with half as many warps 3).  As products in memory over the
